@@ -450,6 +450,68 @@ rlk_status rlk_logp_fwd_noalloc(const rlk_logp_contract* contract, const void* l
                                 float* lse, float* partials, rlk_stream_t stream);
 
 /*
+ * FP8 projections: E4M3 operands with one FP32 scale for each group of 128.
+ * (The pages have no counterpart: they score BF16 models.  These calls give
+ * a model whose tokens the calls above score its 8-bit projections, and an
+ * 8-bit head whose logits go to rlk_logp_fwd or rlk_grpo_fused_step.)
+ *
+ * rlk_fp8_quantize: a group is 128 consecutive elements of a row
+ * (block_rows 1) or a block of 128 rows x 128 columns (block_rows 128); the
+ * last groups may be shorter.  With amax a group's largest magnitude,
+ *     s = max(amax, 2^-100) / 448,   q = e4m3(x * (1 / s)),
+ * each operation one FP32 rounding, e4m3() to nearest even.  x stands for
+ * q * s.  A group holding a NaN or an infinity stands for NaN throughout.
+ *   x        [rows, x_stride] row-major; x_type RLK_BF16 or RLK_F32.
+ *            x_stride >= cols (elements); any alignment (16-byte rows load
+ *            fastest).
+ *   q        NULL, or [rows, q_stride] E4M3 out (one byte each), 16-byte
+ *            aligned, q_stride >= cols a multiple of 16; bytes past column
+ *            cols of a row are not touched.
+ *   scale    with q: FP32 out, group-major: [ceil(cols / 128), rows], or
+ *            [ceil(cols / 128), ceil(rows / 128)] for blocks.
+ *   qt       NULL, or [cols, qt_stride] E4M3 out: the quantised transpose,
+ *            its groups running along x's rows (qt_stride >= rows, a multiple
+ *            of 16); for blocks, the same values as q's.
+ *   scale_t  with qt: FP32 out, [ceil(rows / 128), cols], or
+ *            [ceil(rows / 128), ceil(cols / 128)] for blocks.
+ * At least one of q and qt; both come from one read of x.  No output may
+ * overlap x or another output.  rows = 0 or cols = 0 does nothing.
+ * Asynchronous on `stream`; needs no workspace.
+ */
+typedef enum { RLK_BF16 = 0, RLK_F32 = 1 } rlk_type;
+
+rlk_status rlk_fp8_quantize(int64_t rows, int64_t cols, const void* x, int32_t x_type, int64_t x_stride,
+                            int32_t block_rows, void* q, int64_t q_stride, float* scale, void* qt, int64_t qt_stride,
+                            float* scale_t, rlk_stream_t stream);
+
+/*
+ * C = A B^T of operands quantised as above:
+ *   C[m, n] = sum_g a_scale[g, m] b_scale[g, n] sum_{k in group g} A[m, k] B[n, k],
+ * g over the ceil(K / 128) groups along K, all sums in FP32, groups in order.
+ *   a        [M, a_stride] E4M3, 16-byte aligned, a_stride >= K a multiple of
+ *            16; a_scale [ceil(K / 128), M] FP32.
+ *   b        [N, b_stride] E4M3, likewise; b_scale [ceil(K / 128), N] FP32
+ *            (b_block_rows 1) or [ceil(K / 128), ceil(N / 128)] (b_block_rows 128).
+ *   c        [M, c_stride] out, c_type RLK_BF16 (rounded once, to nearest
+ *            even) or RLK_F32; c_stride >= N, any alignment of the type.
+ *   accumulate  1: c (RLK_F32 only) receives its old value plus the product.
+ *   workspace   RLK_FP8_WORKSPACE bytes, 16-byte aligned, zeroed by the
+ *            caller before its first use: the status word, which a call only
+ *            ever sets (rlk_logp_workspace_status reads it).  The one
+ *            device-side condition is an expired wait (RLK_ERR_TIMEOUT).
+ * With W [N, K] in blocks and x [M, K] in rows the call is x W^T; the
+ * gradients of it are dY W (B the quantised transpose of W, the same blocks)
+ * and dY^T x (A and B the transposes of dY and x, both in rows).  M = 0 or
+ * N = 0 does nothing; K >= 1.  c must not overlap an input.  The bits depend
+ * on M, N, K and the device's SM count only.  Asynchronous on `stream`.
+ */
+#define RLK_FP8_WORKSPACE 256
+
+rlk_status rlk_fp8_matmul(int64_t M, int64_t N, int64_t K, const void* a, int64_t a_stride, const float* a_scale,
+                          const void* b, int64_t b_stride, const float* b_scale, int32_t b_block_rows, void* c,
+                          int32_t c_type, int64_t c_stride, int32_t accumulate, void* workspace, rlk_stream_t stream);
+
+/*
  * Synchronises `stream` and decodes the status word a previous asynchronous
  * call left in `workspace` (RLK_OK when no device-side error was recorded).
  */

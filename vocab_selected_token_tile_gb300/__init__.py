@@ -22,6 +22,11 @@ RLK_ERR_NONFINITE_LSE = 6
 RLK_ERR_TIMEOUT = 7
 RLK_ERR_CUDA = 8
 
+RLK_BF16 = 0
+RLK_F32 = 1
+
+RLK_FP8_WORKSPACE = 256
+
 MASK_EXPLICIT = 0
 MASK_IGNORE_INDEX = 1
 
@@ -46,6 +51,8 @@ EXPORTED = (
     "rlk_logp_shard_fwd",
     "rlk_logp_fold",
     "rlk_logp_shard_bwd",
+    "rlk_fp8_quantize",
+    "rlk_fp8_matmul",
     "rlk_logp_workspace_status",
     "rlk_selftest_bounded_wait",
     "rlk_status_string",
@@ -138,6 +145,13 @@ def library():
         lib.rlk_logp_fold.restype = i
         lib.rlk_logp_shard_bwd.argtypes = [P, ctypes.c_int32, vp, vp, vp, vp, vp, vp, vp, vp]
         lib.rlk_logp_shard_bwd.restype = i
+        i64 = ctypes.c_int64
+        lib.rlk_fp8_quantize.argtypes = [i64, i64, vp, ctypes.c_int32, i64, ctypes.c_int32, vp, i64, vp, vp, i64, vp,
+                                         vp]
+        lib.rlk_fp8_quantize.restype = i
+        lib.rlk_fp8_matmul.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, ctypes.c_int32, vp, ctypes.c_int32,
+                                       i64, ctypes.c_int32, vp, vp]
+        lib.rlk_fp8_matmul.restype = i
         lib.rlk_logp_workspace_status.argtypes = [vp, vp]
         lib.rlk_logp_workspace_status.restype = i
         lib.rlk_selftest_bounded_wait.argtypes = [ctypes.c_int64, vp, vp]
@@ -258,6 +272,17 @@ def rlk_logp_shard_bwd(contract, shard, logits_shard, targets, active_mask, lse_
                        workspace, stream):
     return library().rlk_logp_shard_bwd(ctypes.byref(contract), shard, logits_shard, targets, active_mask, lse_in,
                                         grad_logp, dlogits_shard, workspace, stream)
+
+
+def rlk_fp8_quantize(rows, cols, x, x_type, x_stride, block_rows, q, q_stride, scale, qt, qt_stride, scale_t, stream):
+    return library().rlk_fp8_quantize(rows, cols, x, x_type, x_stride, block_rows, q, q_stride, scale, qt, qt_stride,
+                                      scale_t, stream)
+
+
+def rlk_fp8_matmul(M, N, K, a, a_stride, a_scale, b, b_stride, b_scale, b_block_rows, c, c_type, c_stride, accumulate,
+                   workspace, stream):
+    return library().rlk_fp8_matmul(M, N, K, a, a_stride, a_scale, b, b_stride, b_scale, b_block_rows, c, c_type,
+                                    c_stride, accumulate, workspace, stream)
 
 
 def rlk_logp_workspace_status(workspace, stream):
@@ -722,3 +747,135 @@ def shard_bwd(contract, shard, logits_shard, targets, mask, lse, grad, dlogits=N
     check(rlk_logp_shard_bwd(contract, shard, _ptr(logits_shard), _ptr(targets), _ptr(mask), _ptr(lse), _ptr(grad),
                              _ptr(dlogits), _ptr(ws), _stream(stream)))
     return dlogits
+
+
+# ------------------------------------------------------------------ FP8 projections
+
+_FP8 = ("float8_e4m3fn", "uint8")  # E4M3 values, or their codes as bytes
+
+
+def _matrix(t, name, kinds):
+    """A 2-D CUDA tensor of one of ``kinds`` with contiguous rows; returns its row stride in elements."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor, not {list(t.shape)} on {t.device}")
+    kind = str(t.dtype)[6:]
+    if kind not in kinds:
+        raise TypeError(f"{name} must be {' or '.join(kinds)}, not {kind}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous: its strides are {list(t.stride())}")
+    stride = t.stride(0) if rows > 1 else max(cols, t.stride(0))
+    if rows > 1 and stride < cols:
+        raise ValueError(f"{name}'s rows overlap: its strides are {list(t.stride())}")
+    return stride
+
+
+def _codes_stride(t, name):
+    """The row stride of an E4M3 operand; a single row may come with any, and takes one of whole 16-byte pieces."""
+    stride = _matrix(t, name, _FP8)
+    return -(-t.shape[1] // 16) * 16 if t.shape[0] <= 1 else stride
+
+
+def _codes(rows, cols, dev):
+    """An E4M3 [rows, cols] tensor whose rows start on 16-byte boundaries."""
+    import torch
+    stride = -(-cols // 16) * 16
+    t = torch.empty((rows, stride), dtype=torch.float8_e4m3fn, device=dev)
+    return (t if stride == cols else t[:, :cols]), stride
+
+
+def _scales(groups, rows, block_rows, dev):
+    import torch
+    return torch.empty((-(-groups // 128), rows if block_rows == 1 else -(-rows // 128)), dtype=torch.float32,
+                       device=dev)
+
+
+def _quantize(x, block_rows, rowwise, transposed, stream):
+    stride = _matrix(x, "x", ("bfloat16", "float32"))
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    (R, C), dev = x.shape, x.device
+    q = scale = qt = scale_t = None
+    ldq = ldt = 0
+    if rowwise:
+        q, ldq = _codes(R, C, dev)
+        scale = _scales(C, R, block_rows, dev)
+    if transposed:
+        qt, ldt = _codes(C, R, dev)
+        scale_t = _scales(R, C, block_rows, dev)
+    check(rlk_fp8_quantize(R, C, _ptr(x), RLK_F32 if x.element_size() == 4 else RLK_BF16, stride, block_rows, _ptr(q),
+                           ldq, _ptr(scale), _ptr(qt), ldt, _ptr(scale_t), _stream(stream)))
+    return q, scale, qt, scale_t
+
+
+def fp8_quantize(x, block_rows=1, transpose=False, stream=None):
+    """(q, scale) of a BF16 or FP32 matrix [R, C]: E4M3 values and one FP32 scale for each 1 x 128 group of a row
+    (block_rows 1) or each 128 x 128 block (128), so that x ~ q * scale.
+
+    ``scale`` is group-major: [ceil(C / 128), R] or [ceil(C / 128), ceil(R / 128)].  With ``transpose`` the result
+    is that of x's transpose [C, R].  q's rows start on 16-byte boundaries (a view where C is not a multiple of 16).
+    """
+    q, scale, qt, scale_t = _quantize(x, block_rows, not transpose, transpose, stream)
+    return (qt, scale_t) if transpose else (q, scale)
+
+
+def fp8_quantize_both(x, block_rows=1, stream=None):
+    """(q, scale, qt, scale_t): fp8_quantize of x and of its transpose from one read of x."""
+    return _quantize(x, block_rows, True, True, stream)
+
+
+_fp8_workspaces = {}
+
+
+def _fp8_workspace(dev, stream):
+    """The status word of a device and stream: zeroed once, only ever set by a call."""
+    import torch
+    ws = _fp8_workspaces.get((dev, stream))
+    if ws is None:
+        ws = _fp8_workspaces[(dev, stream)] = torch.zeros(RLK_FP8_WORKSPACE, dtype=torch.uint8, device=dev)
+    return ws
+
+
+def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=None, accumulate=False, workspace=None,
+               validate=False, stream=None):
+    """a @ b^T [M, N] of E4M3 operands a [M, K] and b [N, K] with the scales fp8_quantize gives them.
+
+    ``a_scale`` is [ceil(K / 128), M]; ``b_scale`` [ceil(K / 128), N] (b_block_rows 1) or [ceil(K / 128),
+    ceil(N / 128)] (128).  The result is BF16 (or FP32 with ``out_dtype`` torch.float32), in ``out`` if given (its rows
+    may be strided); ``accumulate`` adds the product to an FP32 ``out``.  ``validate`` synchronises and raises if a
+    device-side wait expired.
+    """
+    import torch
+    lda, ldb = _codes_stride(a, "a"), _codes_stride(b, "b")
+    (M, K), (N, Kb) = a.shape, b.shape
+    if Kb != K:
+        raise ValueError(f"a is [{M}, {K}] and b [{N}, {Kb}]: their rows must have one length")
+    if b_block_rows not in (1, 128):
+        raise ValueError("b_block_rows must be 1 or 128")
+    groups = -(-K // 128)
+    for name, s, n in (("a_scale", a_scale, M), ("b_scale", b_scale, N if b_block_rows == 1 else -(-N // 128))):
+        if s.dtype != torch.float32 or tuple(s.shape) != (groups, n) or not s.is_contiguous() or not s.is_cuda:
+            raise ValueError(f"{name} must be a contiguous FP32 CUDA tensor [{groups}, {n}], not "
+                             f"{str(s.dtype)[6:]} {list(s.shape)}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out_dtype = out_dtype or torch.bfloat16
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        ldc = N
+    else:
+        ldc = _matrix(out, "out", ("bfloat16", "float32"))
+        if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out is {str(out.dtype)[6:]} {list(out.shape)}; the product is [{M}, {N}]")
+    st = _stream(stream)
+    if workspace is None:
+        workspace = _fp8_workspace(a.device, st)
+    else:
+        _need(workspace, "workspace", RLK_FP8_WORKSPACE, ("uint8",))
+    check(rlk_fp8_matmul(M, N, K, _ptr(a), lda, _ptr(a_scale), _ptr(b), ldb, _ptr(b_scale), b_block_rows, _ptr(out),
+                         RLK_F32 if out.element_size() == 4 else RLK_BF16, ldc, int(accumulate), _ptr(workspace), st))
+    if validate:
+        check(rlk_logp_workspace_status(_ptr(workspace), st))
+    return out

@@ -1,0 +1,780 @@
+// Matrix product of E4M3 operands with an FP32 scale for each group of 128
+// along K (sm_103a):
+//
+//   C[m, n] = sum_g sa[g, m] sb[g, n] sum_{k in group g} a[m, k] b[n, k]
+//
+// A [M, K] has one scale per row and group; B [N, K] one per row and group or
+// one per 128 x 128 block.  The scales are not powers of two, so they cannot
+// ride in the tensor core: each group's partial product is formed by four
+// tcgen05.mma (kind::f8f6f4, K = 32) into a fresh tensor-memory accumulator,
+// and the epilogue warps read it, scale it and add it to the sum they hold in
+// registers (FP32 throughout: a product of two scales, one rounding, then one
+// fused multiply-add per element and group).
+//
+// Two kernels:
+//
+// gemm_kernel, a 128 x 256 tile a CTA, persistent, one CTA per SM.  Bound: the
+// tensor core, 2 M N K operations at the FP8 rate (128 x 256 x 128 takes 512
+// clocks a group); reading the 128 KB accumulator back takes 256 clocks of the
+// tensor-memory port and the scaling 128 (block scales) or 256+ issue slots a
+// scheduler, so the epilogue fits under the MMAs with two accumulators in
+// flight.  Roles: warp 0 issues the TMA loads, warp 1 the MMAs, warp 2 fetches
+// the scales with cp.async (4 bytes each: a row of scales starts at any
+// multiple of 4), warps 4-11 are the epilogue (a warp reads 32 tensor-memory
+// lanes and 128 of the 256 columns: 128 sums a thread, which is why the first
+// warpgroup gives registers away with setmaxnreg).
+//
+// skinny_kernel, for few rows of A: B's rows take the 128 lanes and A's rows
+// the accumulator's columns (16, 32, 64 or 128), so a single token streams the
+// weight once and wastes no more than 15 columns.  Bound: HBM, N K bytes.  Two
+// CTAs per SM keep loads in flight across each other's start and end.  Where N
+// / 128 tiles are fewer than the SMs can hold, a cluster of 2, 4 or 8 CTAs
+// splits K, and adds its partial sums through distributed shared memory in
+// rank order: no workspace, no second launch, the same bits every time.
+//
+// Every wait is bounded; on expiry the CTA records the time-out in the status
+// word, stops issuing, waits (bounded) for its copies and MMAs, frees its
+// tensor memory and returns.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <mutex>
+#include <string>
+
+#include "rlk_internal.h"
+#include "rlk_ptx.cuh"
+
+namespace rlk {
+namespace {
+
+constexpr int kGK = 128;         // K of a group, and of a ring stage: 128 E4M3 = one 128-byte swizzle row
+constexpr int kScaleStages = 8;  // ring of scales, deeper than the operands': its loads are small and unaligned
+constexpr uint64_t kDrainNs8 = 1000000000ull;
+
+// D[tmem] (+)= A[smem] B[smem]^T, E4M3 inputs (format 0 in both fields), FP32 accumulate.
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
+    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// 16 consecutive FP32 columns of a warp's 32 tensor-memory lanes; the values
+// are there only after tmem_wait16 on the same registers.
+__device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])::"memory");
+}
+
+// A 4-byte asynchronous copy, zero where `ok` is false (nothing is read then).
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+// This thread's arrival on `bar` once its earlier copies have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int STAGES>
+struct Bars8 {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t sfull[kScaleStages];
+    uint64_t sempty[kScaleStages];
+    uint64_t drain;
+    uint32_t tmem_addr;
+    int abort_flag;
+};
+
+struct Wait8 {
+    uint32_t* status;
+    uint64_t wait_ns;
+};
+
+__device__ __forceinline__ bool wait8_slow(volatile int* abort_flag, uint32_t bar, uint32_t parity, const Wait8& w) {
+    if (*abort_flag) return false;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > w.wait_ns) {
+            *abort_flag = 1;
+            atomicOr(w.status, kStatusTimeout);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait8(int* abort_flag, uint32_t bar, uint32_t parity, const Wait8& w) {
+    return mbar_try_wait(bar, parity) || wait8_slow(abort_flag, bar, parity, w);
+}
+
+__device__ __forceinline__ void drain8(uint32_t bar, uint32_t parity, const Wait8& w) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (globaltimer_ns() - t0 > kDrainNs8) {
+            atomicOr(w.status, kStatusTimeout);
+            return;
+        }
+    }
+}
+
+template <int STAGES>
+__device__ void init_bars8(Bars8<STAGES>* b, int epilogue_warps) {
+    for (int s = 0; s < STAGES; ++s) {
+        mbar_init(smem_u32(&b->full[s]), 1);
+        mbar_init(smem_u32(&b->empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&b->tfull[i]), 1);
+        mbar_init(smem_u32(&b->tempty[i]), epilogue_warps);
+    }
+    for (int s = 0; s < kScaleStages; ++s) {
+        mbar_init(smem_u32(&b->sfull[s]), 32);
+        mbar_init(smem_u32(&b->sempty[s]), epilogue_warps);
+    }
+    mbar_init(smem_u32(&b->drain), 1);
+    b->abort_flag = 0;
+    fence_mbar_init();
+}
+
+// Position in a ring of n slots: the slot and the parity of its current pass.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+struct Gemm8Params {
+    const float *sa, *sb;
+    void* c;
+    int64_t ldc;
+    int32_t M, N, KB;
+    int32_t MB, NB;     // tiles along M and N
+    int32_t band;       // M tiles per band of the tile order
+    int32_t nsb;        // scales of B per K group: N (rows) or ceil(N / 128) (blocks)
+    int32_t c_f32, accumulate, vec;
+    Wait8 w;
+};
+
+// C elements of one row, columns [col, col + 8): 16-byte stores where the row
+// allows, single elements at the edge.
+__device__ __forceinline__ void store8(const Gemm8Params& p, int64_t row, int col, const float (&v)[8]) {
+    if (col >= p.N) return;
+    if (p.c_f32) {
+        float* c = static_cast<float*>(p.c) + row * p.ldc + col;
+        if (p.vec && col + 8 <= p.N) {
+            float4 lo = make_float4(v[0], v[1], v[2], v[3]), hi = make_float4(v[4], v[5], v[6], v[7]);
+            float4* c4 = reinterpret_cast<float4*>(c);
+            if (p.accumulate) {
+                const float4 x = c4[0], y = c4[1];
+                lo.x += x.x, lo.y += x.y, lo.z += x.z, lo.w += x.w;
+                hi.x += y.x, hi.y += y.y, hi.z += y.z, hi.w += y.w;
+            }
+            c4[0] = lo;
+            c4[1] = hi;
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (col + j < p.N) c[j] = p.accumulate ? c[j] + v[j] : v[j];
+        return;
+    }
+    uint16_t* c = static_cast<uint16_t*>(p.c) + row * p.ldc + col;
+    const uint32_t w[4] = {pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
+                           pack_bf16x2_rn(v[6], v[7])};
+    if (p.vec && col + 8 <= p.N) {
+        *reinterpret_cast<uint4*>(c) = make_uint4(w[0], w[1], w[2], w[3]);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (col + j < p.N) c[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+}
+
+// ----------------------------------------------------------------- 128 x 256 tiles
+
+constexpr int kGM = 128, kGN = 256;
+constexpr int kGStages = 4;
+constexpr uint32_t kGA = kGM * kGK, kGB = kGN * kGK;
+constexpr int kGThreads = 384;
+constexpr int kGScaleFloats = kGM + kGN;
+constexpr size_t kGSmem = 1024 + (size_t)kGStages * (kGA + kGB) + kScaleStages * kGScaleFloats * 4 + 1024;
+static_assert(sizeof(Bars8<kGStages>) <= 1024, "barriers fit their kilobyte");
+
+// Tile t of the persistent order: bands of `band` M tiles, and within a band
+// all M tiles of one N tile before the next, so the tiles in flight share a
+// few N tiles of B and the band's rows of A, which L2 holds.
+__device__ __forceinline__ void tile_of(const Gemm8Params& p, int t, int& mb, int& nb) {
+    const int per = p.band * p.NB, full = p.MB / p.band;
+    const int b = min(t / per, full);
+    const int r = t - b * per;
+    const int width = b < full ? p.band : p.MB - full * p.band;
+    nb = r / width;
+    mb = b * p.band + r % width;
+}
+
+template <bool BROWS>
+__global__ void __launch_bounds__(kGThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ Gemm8Params p) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* sA = smem;
+    unsigned char* sB = smem + kGStages * kGA;
+    float* scales = reinterpret_cast<float*>(sB + kGStages * kGB);
+    auto* bars = reinterpret_cast<Bars8<kGStages>*>(scales + kScaleStages * kGScaleFloats);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tiles = p.MB * p.NB;
+
+    if (threadIdx.x == 0) init_bars8(bars, 8);
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&bars->tmem_addr), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_addr;
+    int* ab = &bars->abort_flag;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------ TMA producer
+            Ring r;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                int mb, nb;
+                tile_of(p, t, mb, nb);
+                for (int kb = 0; kb < p.KB; ++kb) {
+                    if (!(ok = wait8(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
+                    const uint32_t fb = smem_u32(&bars->full[r.slot]);
+                    mbar_arrive_expect_tx(fb, kGA + kGB);
+                    tma_load_2d(smem_u32(sA + r.slot * kGA), &tmA, kb * kGK, mb * kGM, fb);
+                    tma_load_2d(smem_u32(sB + r.slot * kGB), &tmB, kb * kGK, nb * kGN, fb);
+                    ++issued;
+                    r.next(kGStages);
+                }
+            }
+            // every copy lands before the CTA may exit
+            for (int64_t j = issued > kGStages ? issued - kGStages : 0; j < issued; ++j)
+                drain8(smem_u32(&bars->full[j % kGStages]), (uint32_t)((j / kGStages) & 1), p.w);
+        } else if (warp == 1 && lane == 0) {
+            // ------------------------------------------------ MMA issuer
+            Ring r, acc;
+            bool ok = true;
+            const uint32_t idesc = idesc_e4m3_f32(kGM, kGN);
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                for (int kb = 0; kb < p.KB; ++kb) {
+                    if (!(ok = wait8(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
+                    if (!(ok = wait8(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(sA + r.slot * kGA), b0 = smem_u32(sB + r.slot * kGB);
+                    const uint32_t d = tmem + (uint32_t)(acc.slot * kGN);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_e4m3(d, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32), idesc, kk != 0);
+                    umma_commit(smem_u32(&bars->empty[r.slot]));
+                    umma_commit(smem_u32(&bars->tfull[acc.slot]));
+                    r.next(kGStages);
+                    acc.next(2);
+                }
+            }
+            umma_commit(smem_u32(&bars->drain));
+            drain8(smem_u32(&bars->drain), 0u, p.w);
+        } else if (warp == 2) {
+            // ------------------------------------------------ scales
+            Ring r;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                int mb, nb;
+                tile_of(p, t, mb, nb);
+                for (int kb = 0; kb < p.KB; ++kb) {
+                    ok = __all_sync(0xFFFFFFFFu, wait8(ab, smem_u32(&bars->sempty[r.slot]), r.phase ^ 1u, p.w));
+                    if (!ok) break;
+                    const uint32_t dst = smem_u32(scales + r.slot * kGScaleFloats);
+                    const float* a = p.sa + (int64_t)kb * p.M;
+                    const float* b = p.sb + (int64_t)kb * p.nsb;
+#pragma unroll
+                    for (int i = lane; i < kGM; i += 32) {
+                        const int row = mb * kGM + i;
+                        cp_async4(dst + i * 4, a + (row < p.M ? row : 0), row < p.M);
+                    }
+                    if (BROWS) {
+#pragma unroll
+                        for (int i = lane; i < kGN; i += 32) {
+                            const int row = nb * kGN + i;
+                            cp_async4(dst + (kGM + i) * 4, b + (row < p.N ? row : 0), row < p.N);
+                        }
+                    } else if (lane < 2) {
+                        const int blk = nb * (kGN / 128) + lane;
+                        cp_async4(dst + (kGM + lane) * 4, b + (blk < p.nsb ? blk : 0), blk < p.nsb);
+                    }
+                    cp_async_arrive(smem_u32(&bars->sfull[r.slot]));
+                    r.next(kScaleStages);
+                }
+            }
+            cp_async_wait_all();
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ epilogue: scale and sum in registers
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        Ring acc, sc;
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            int mb, nb;
+            tile_of(p, t, mb, nb);
+            float2 sum[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
+            for (int kb = 0; kb < p.KB; ++kb) {
+                ok = wait8(ab, smem_u32(&bars->sfull[sc.slot]), sc.phase, p.w);
+                const float* s = scales + sc.slot * kGScaleFloats;
+                const float sa = s[quarter * 32 + lane];
+                const float sab = BROWS ? 0.f : __fmul_rn(sa, s[kGM + half]);
+                ok = __all_sync(0xFFFFFFFFu, ok && wait8(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t t0 = tmem + lane_base + (uint32_t)(acc.slot * kGN + half * 128);
+                uint32_t v[2][16];
+                tmem_ld16_issue(t0, v[0]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    tmem_wait16(v[c & 1]);
+                    if (c < 7) {
+                        tmem_ld16_issue(t0 + (c + 1) * 16, v[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc.slot]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 d = make_float2(__uint_as_float(v[c & 1][2 * i]),
+                                                     __uint_as_float(v[c & 1][2 * i + 1]));
+                        float2 f = make_float2(sab, sab);
+                        if (BROWS) {
+                            const float2 sb = *reinterpret_cast<const float2*>(s + kGM + half * 128 + c * 16 + 2 * i);
+                            f = fmul2(make_float2(sa, sa), sb);
+                        }
+                        sum[c * 8 + i] = ffma2(d, f, sum[c * 8 + i]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->sempty[sc.slot]));
+                acc.next(2);
+                sc.next(kScaleStages);
+            }
+            if (!ok) break;
+            const int64_t row = (int64_t)mb * kGM + quarter * 32 + lane;
+            if (row < p.M) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    const float v[8] = {sum[4 * q].x,     sum[4 * q].y,     sum[4 * q + 1].x, sum[4 * q + 1].y,
+                                        sum[4 * q + 2].x, sum[4 * q + 2].y, sum[4 * q + 3].x, sum[4 * q + 3].y};
+                    store8(p, row, nb * kGN + half * 128 + q * 8, v);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ----------------------------------------------------------------- few rows of A
+
+constexpr int kSThreads = 256;
+constexpr int kSRows = 128;  // rows of B a tile
+
+template <int NT>
+struct Skinny {
+    // two CTAs per SM; one for 128 rows, whose sums alone are 128 registers a thread
+    static constexpr int kPerSm = NT <= 64 ? 2 : 1;
+    static constexpr int kStages = NT <= 16 ? 5 : NT <= 64 ? 4 : 6;
+    static constexpr uint32_t kW = kSRows * kGK, kX = NT * kGK;
+    static constexpr uint32_t kTmem = 2 * NT < 32 ? 32 : 2 * NT;
+    static constexpr int kScale = NT + kSRows;
+    static constexpr size_t kRing = (size_t)kStages * (kW + kX);
+    static constexpr size_t kReduce = (size_t)NT * kSRows * 4;  // partial sums of a K slice, over the drained ring
+    static constexpr size_t kSmem = 1024 + kRing + kScaleStages * kScale * 4 + 1024;
+    static_assert(kReduce <= kRing, "the partial sums fit the ring");
+};
+
+template <int NT, bool BROWS>
+__global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
+    skinny_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ Gemm8Params p, const int split) {
+    using S = Skinny<NT>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* sW = smem;
+    unsigned char* sX = smem + S::kStages * S::kW;
+    float* scales = reinterpret_cast<float*>(sX + S::kStages * S::kX);
+    auto* bars = reinterpret_cast<Bars8<S::kStages>*>(scales + kScaleStages * S::kScale);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // p.MB blocks of NT rows of A, p.NB tiles of 128 rows of B; the M blocks of one tile run together
+    const int tiles = p.MB * p.NB;
+    const int rank = split > 1 ? (int)cluster_ctarank() : 0;
+    const int first = (int)blockIdx.x / split, step = (int)gridDim.x / split;
+    const int k0 = (int)((int64_t)p.KB * rank / split), k1 = (int)((int64_t)p.KB * (rank + 1) / split);
+
+    if (threadIdx.x == 0) init_bars8(bars, 4);
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&bars->tmem_addr), S::kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_addr;
+    int* ab = &bars->abort_flag;
+    const int quarter = warp & 3, row_in = quarter * 32 + lane;
+    float sum[NT];  // epilogue: this thread's row of B against the NT rows of A
+
+    if (warp == 0) {
+        if (lane == 0) {
+            Ring r;
+            int64_t issued = 0;
+            bool ok = true;
+            for (int t = first; ok && t < tiles; t += step) {
+                const int nb = t / p.MB, mb = t % p.MB;
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!(ok = wait8(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
+                    const uint32_t fb = smem_u32(&bars->full[r.slot]);
+                    mbar_arrive_expect_tx(fb, S::kW + S::kX);
+                    tma_load_2d(smem_u32(sW + r.slot * S::kW), &tmB, kb * kGK, nb * kSRows, fb);
+                    tma_load_2d(smem_u32(sX + r.slot * S::kX), &tmA, kb * kGK, mb * NT, fb);
+                    ++issued;
+                    r.next(S::kStages);
+                }
+            }
+            for (int64_t j = issued > S::kStages ? issued - S::kStages : 0; j < issued; ++j)
+                drain8(smem_u32(&bars->full[j % S::kStages]), (uint32_t)((j / S::kStages) & 1), p.w);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            Ring r, acc;
+            bool ok = true;
+            const uint32_t idesc = idesc_e4m3_f32(kSRows, NT);
+            for (int t = first; ok && t < tiles; t += step) {
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!(ok = wait8(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
+                    if (!(ok = wait8(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                    tc_fence_after();
+                    const uint32_t w0 = smem_u32(sW + r.slot * S::kW), x0 = smem_u32(sX + r.slot * S::kX);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_e4m3(tmem + (uint32_t)(acc.slot * NT), smem_desc_sw128(w0 + kk * 32),
+                                  smem_desc_sw128(x0 + kk * 32), idesc, kk != 0);
+                    umma_commit(smem_u32(&bars->empty[r.slot]));
+                    umma_commit(smem_u32(&bars->tfull[acc.slot]));
+                    r.next(S::kStages);
+                    acc.next(2);
+                }
+            }
+            umma_commit(smem_u32(&bars->drain));
+            drain8(smem_u32(&bars->drain), 0u, p.w);
+        }
+    } else if (warp == 2) {
+        Ring r;
+        bool ok = true;
+        for (int t = first; ok && t < tiles; t += step) {
+            const int nb = t / p.MB, mb = t % p.MB;
+            for (int kb = k0; kb < k1; ++kb) {
+                ok = __all_sync(0xFFFFFFFFu, wait8(ab, smem_u32(&bars->sempty[r.slot]), r.phase ^ 1u, p.w));
+                if (!ok) break;
+                const uint32_t dst = smem_u32(scales + r.slot * S::kScale);
+                const float* a = p.sa + (int64_t)kb * p.M;
+                const float* b = p.sb + (int64_t)kb * p.nsb;
+                for (int i = lane; i < NT; i += 32) {
+                    const int row = mb * NT + i;
+                    cp_async4(dst + i * 4, a + (row < p.M ? row : 0), row < p.M);
+                }
+                if (BROWS) {
+#pragma unroll
+                    for (int i = lane; i < kSRows; i += 32) {
+                        const int row = nb * kSRows + i;
+                        cp_async4(dst + (NT + i) * 4, b + (row < p.N ? row : 0), row < p.N);
+                    }
+                } else if (lane == 0) {
+                    cp_async4(dst + NT * 4, b + nb, true);
+                }
+                cp_async_arrive(smem_u32(&bars->sfull[r.slot]));
+                r.next(kScaleStages);
+            }
+        }
+        cp_async_wait_all();
+    } else if (warp >= 4) {
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        Ring acc, sc;
+        bool ok = true;
+        for (int t = first; ok && t < tiles; t += step) {
+            const int nb = t / p.MB, mb = t % p.MB;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) sum[i] = 0.f;
+            for (int kb = k0; kb < k1; ++kb) {
+                ok = wait8(ab, smem_u32(&bars->sfull[sc.slot]), sc.phase, p.w);
+                const float* s = scales + sc.slot * S::kScale;
+                const float sb = s[NT + (BROWS ? row_in : 0)];
+                ok = __all_sync(0xFFFFFFFFu, ok && wait8(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t t0 = tmem + lane_base + (uint32_t)(acc.slot * NT);
+                uint32_t v[2][16];
+                tmem_ld16_issue(t0, v[0]);
+#pragma unroll
+                for (int c = 0; c < NT / 16; ++c) {
+                    tmem_wait16(v[c & 1]);
+                    if (c < NT / 16 - 1) {
+                        tmem_ld16_issue(t0 + (c + 1) * 16, v[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc.slot]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum[c * 16 + i] = __fmaf_rn(__uint_as_float(v[c & 1][i]), __fmul_rn(s[c * 16 + i], sb),
+                                                    sum[c * 16 + i]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->sempty[sc.slot]));
+                acc.next(2);
+                sc.next(kScaleStages);
+            }
+            if (!ok || split > 1) break;  // a split launch has one tile a cluster, added up below
+            const int col = nb * kSRows + row_in;
+            if (col < p.N) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int64_t at = (int64_t)(mb * NT + i) * p.ldc + col;
+                    if (mb * NT + i >= p.M) break;
+                    if (p.c_f32) {
+                        float* c = static_cast<float*>(p.c) + at;
+                        *c = p.accumulate ? *c + sum[i] : sum[i];
+                    } else {
+                        static_cast<uint16_t*>(p.c)[at] = (uint16_t)pack_bf16x2_rn(sum[i], 0.f);
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    if (split > 1) {
+        // every load has been consumed, so the ring's memory takes the partial sums [NT][128]
+        float* red = reinterpret_cast<float*>(smem);
+        __syncthreads();
+        if (warp >= 4) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) red[i * kSRows + row_in] = sum[i];
+        }
+        cluster_sync_all();
+        const int nb = first / p.MB, mb = first % p.MB;
+        const bool failed = *reinterpret_cast<volatile int*>(ab) != 0;
+        // this CTA adds up rows [lo, hi) of A: 128 consecutive columns of C a row
+        const int lo = NT * rank / split, hi = NT * (rank + 1) / split;
+        for (int e = threadIdx.x; e < (hi - lo) * kSRows && !failed; e += kSThreads) {
+            const int i = lo + e / kSRows, col = nb * kSRows + e % kSRows;
+            if (mb * NT + i >= p.M || col >= p.N) continue;
+            const uint32_t at = smem_u32(red + i * kSRows + e % kSRows);
+            float v = 0.f;
+            for (int r = 0; r < split; ++r) v = __fadd_rn(v, ld_cluster_f32(mapa_shared(at, (uint32_t)r)));
+            const int64_t o = (int64_t)(mb * NT + i) * p.ldc + col;
+            if (p.c_f32) {
+                float* c = static_cast<float*>(p.c) + o;
+                *c = p.accumulate ? *c + v : v;
+            } else {
+                static_cast<uint16_t*>(p.c)[o] = (uint16_t)pack_bf16x2_rn(v, 0.f);
+            }
+        }
+        cluster_sync_all();  // no CTA leaves while another reads its sums
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::kTmem);
+    }
+}
+
+// ----------------------------------------------------------------- host
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_fn8() {
+    static std::mutex mu;
+    static EncodeTiled fn = nullptr;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!fn) {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiled>(ptr);
+    }
+    return fn;
+}
+
+// A byte matrix of `rows` rows of `inner` bytes, `stride` apart, in boxes of
+// 128 bytes x box_rows with the 128-byte swizzle; bytes outside read as zero.
+bool make_map8(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t stride, uint32_t box_rows) {
+    EncodeTiled enc = encode_fn8();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride};
+    const cuuint32_t box[2] = {kGK, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+rlk_status cuda_fail(const char* what, cudaError_t e) {
+    return fail(RLK_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+template <typename K>
+rlk_status allow_smem(K kernel, size_t bytes) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product: shared memory", e);
+}
+
+template <bool BROWS>
+rlk_status launch_gemm(const Gemm8Params& p, const CUtensorMap& a, const CUtensorMap& b, int sms, cudaStream_t st) {
+    const rlk_status s = allow_smem(gemm_kernel<BROWS>, kGSmem);
+    if (s != RLK_OK) return s;
+    const int tiles = p.MB * p.NB;
+    gemm_kernel<BROWS><<<tiles < sms ? tiles : sms, kGThreads, kGSmem, st>>>(a, b, p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product launch", e);
+}
+
+template <int NT, bool BROWS>
+rlk_status launch_skinny(const Gemm8Params& p, const CUtensorMap& a, const CUtensorMap& b, int sms,
+                         cudaStream_t st) {
+    const rlk_status s = allow_smem(skinny_kernel<NT, BROWS>, Skinny<NT>::kSmem);
+    if (s != RLK_OK) return s;
+    const int tiles = p.MB * p.NB, room = Skinny<NT>::kPerSm * sms;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= room && split * 4 <= p.KB) split *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : tiles < room ? tiles : room));
+    cfg.blockDim = dim3(kSThreads);
+    cfg.dynamicSmemBytes = Skinny<NT>::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)split;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, skinny_kernel<NT, BROWS>, a, b, p, split);
+    return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product launch", e);
+}
+
+template <bool BROWS>
+rlk_status launch_skinny_nt(int nt, const Gemm8Params& p, const CUtensorMap& a, const CUtensorMap& b, int sms,
+                            cudaStream_t st) {
+    switch (nt) {
+        case 16: return launch_skinny<16, BROWS>(p, a, b, sms, st);
+        case 32: return launch_skinny<32, BROWS>(p, a, b, sms, st);
+        case 64: return launch_skinny<64, BROWS>(p, a, b, sms, st);
+        default: return launch_skinny<128, BROWS>(p, a, b, sms, st);
+    }
+}
+
+}  // namespace
+
+rlk_status launch_fp8_matmul(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, const float* sa,
+                             const void* b, int64_t ldb, const float* sb, int32_t b_block_rows, void* c, int64_t ldc,
+                             int32_t c_f32, int32_t accumulate, uint32_t* status, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess || sms <= 0) return fail(RLK_ERR_CUDA, "cannot query the device's SM count");
+    const bool rows = b_block_rows == 1;
+    Gemm8Params p{};
+    p.sa = sa;
+    p.sb = sb;
+    p.c = c;
+    p.ldc = ldc;
+    p.M = (int32_t)M;
+    p.N = (int32_t)N;
+    p.KB = (int32_t)((K + kGK - 1) / kGK);
+    p.nsb = (int32_t)(rows ? N : (N + 127) / 128);
+    p.c_f32 = c_f32;
+    p.accumulate = accumulate;
+    p.vec = reinterpret_cast<uintptr_t>(c) % 16 == 0 && (ldc * (c_f32 ? 4 : 2)) % 16 == 0;
+    p.w.status = status;
+    p.w.wait_ns = kDefaultWaitNs;
+    CUtensorMap ta, tb;
+    // Few rows of A: the weight's rows take the lanes.  Up to 128 rows the
+    // 128 x 256 tile would read the weight once as well, but in N / 256 units
+    // that a short N leaves most SMs without.
+    if (M <= 128) {
+        const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+        p.MB = (int32_t)((M + nt - 1) / nt);
+        p.NB = (int32_t)((N + kSRows - 1) / kSRows);
+        if (!make_map8(&ta, a, K, M, lda, (uint32_t)nt) || !make_map8(&tb, b, K, N, ldb, kSRows))
+            return fail(RLK_ERR_CUDA, "cuTensorMapEncodeTiled failed for an operand of the fp8 product");
+        return rows ? launch_skinny_nt<true>(nt, p, ta, tb, sms, stream)
+                    : launch_skinny_nt<false>(nt, p, ta, tb, sms, stream);
+    }
+    p.MB = (int32_t)((M + kGM - 1) / kGM);
+    p.NB = (int32_t)((N + kGN - 1) / kGN);
+    const int64_t band = ((int64_t)32 << 20) / ((int64_t)kGM * K);
+    p.band = (int32_t)(band < 1 ? 1 : band < p.MB ? band : p.MB);
+    if (!make_map8(&ta, a, K, M, lda, kGM) || !make_map8(&tb, b, K, N, ldb, kGN))
+        return fail(RLK_ERR_CUDA, "cuTensorMapEncodeTiled failed for an operand of the fp8 product");
+    return rows ? launch_gemm<true>(p, ta, tb, sms, stream) : launch_gemm<false>(p, ta, tb, sms, stream);
+}
+
+}  // namespace rlk

@@ -793,6 +793,135 @@ RLK_EXPORT rlk_status rlk_logp_fwd_noalloc(const rlk_logp_contract* c, const voi
     return c->validate ? read_status(scratch, st) : RLK_OK;
 }
 
+namespace rlk {
+namespace {
+constexpr int64_t kMaxDim8 = ((int64_t)1 << 31) - 512;
+
+// Bytes from the first element of a [rows, stride] buffer to the end of the
+// last row's `width` elements of `size` bytes.
+int64_t extent(int64_t rows, int64_t stride, int64_t width, int64_t size) {
+    return rows <= 0 ? 0 : ((rows - 1) * stride + width) * size;
+}
+
+struct Span {
+    const void* ptr;
+    int64_t bytes;
+    const char* name;
+};
+
+// The first span (an output) shares no byte with the others; NULL spans are
+// optional arguments left out.
+rlk_status check_disjoint(const Span& out, std::initializer_list<Span> others) {
+    if (!out.ptr) return RLK_OK;
+    const uint64_t a = reinterpret_cast<uintptr_t>(out.ptr);
+    for (const Span& o : others) {
+        const uint64_t b = reinterpret_cast<uintptr_t>(o.ptr);
+        if (o.ptr && a < b + (uint64_t)o.bytes && b < a + (uint64_t)out.bytes)
+            return fail(RLK_ERR_INVALID_ARG, std::string(out.name) + " overlaps " + o.name);
+    }
+    return RLK_OK;
+}
+
+// An E4M3 operand's pointer and row stride (whole 16-byte pieces a row).
+rlk_status check_codes(const char* name, const void* p, int64_t stride, int64_t width) {
+    if (!aligned16(p)) return fail(RLK_ERR_MISALIGNED, std::string(name) + " must be 16-byte aligned");
+    if (stride < width) return fail(RLK_ERR_INVALID_ARG, std::string(name) + "_stride is below its row's length");
+    if (stride % 16 != 0) return fail(RLK_ERR_MISALIGNED, std::string(name) + "_stride must be a multiple of 16");
+    if (stride > ((int64_t)1 << 38)) return fail(RLK_ERR_UNSUPPORTED, std::string(name) + "_stride above 2^38");
+    return RLK_OK;
+}
+
+rlk_status check_natural(const char* name, const void* p, int64_t size) {
+    if (p && reinterpret_cast<uintptr_t>(p) % (uintptr_t)size != 0)
+        return fail(RLK_ERR_MISALIGNED, std::string(name) + " must be aligned to its elements");
+    return RLK_OK;
+}
+}  // namespace
+}  // namespace rlk
+
+RLK_EXPORT rlk_status rlk_fp8_quantize(int64_t rows, int64_t cols, const void* x, int32_t x_type, int64_t x_stride,
+                                       int32_t block_rows, void* q, int64_t q_stride, float* scale, void* qt,
+                                       int64_t qt_stride, float* scale_t, rlk_stream_t stream) {
+    rlk_status s;
+    if (rows < 0 || cols < 0) return fail(RLK_ERR_INVALID_ARG, "rows and cols must be >= 0");
+    if (x_type != RLK_BF16 && x_type != RLK_F32)
+        return fail(RLK_ERR_INVALID_ARG, "x_type must be RLK_BF16 or RLK_F32");
+    if (block_rows != 1 && block_rows != 128) return fail(RLK_ERR_INVALID_ARG, "block_rows must be 1 or 128");
+    if (rows > kMaxDim8 || cols > kMaxDim8) return fail(RLK_ERR_UNSUPPORTED, "rows or cols above 2^31 - 512");
+    if (rows == 0 || cols == 0) return RLK_OK;
+    if (!x) return fail(RLK_ERR_INVALID_ARG, "x is NULL");
+    if (!q && !qt) return fail(RLK_ERR_INVALID_ARG, "q or qt is required");
+    if ((q != nullptr) != (scale != nullptr) || (qt != nullptr) != (scale_t != nullptr))
+        return fail(RLK_ERR_INVALID_ARG, "q comes with scale and qt with scale_t");
+    const int64_t size = x_type == RLK_F32 ? 4 : 2;
+    if (x_stride < cols) return fail(RLK_ERR_INVALID_ARG, "x_stride must be >= cols");
+    if (x_stride > ((int64_t)1 << 38)) return fail(RLK_ERR_UNSUPPORTED, "x_stride above 2^38");
+    if ((s = check_natural("x", x, size)) != RLK_OK) return s;
+    if (q && (s = check_codes("q", q, q_stride, cols)) != RLK_OK) return s;
+    if (qt && (s = check_codes("qt", qt, qt_stride, rows)) != RLK_OK) return s;
+    if ((s = check_natural("scale", scale, 4)) != RLK_OK) return s;
+    if ((s = check_natural("scale_t", scale_t, 4)) != RLK_OK) return s;
+    const int64_t cg = (cols + 127) / 128, rg = (rows + 127) / 128;
+    const Span sx{x, extent(rows, x_stride, cols, size), "x"};
+    const Span sq{q, extent(rows, q_stride, cols, 1), "q"};
+    const Span sqt{qt, extent(cols, qt_stride, rows, 1), "qt"};
+    const Span ss{scale, 4 * cg * (block_rows == 1 ? rows : rg), "scale"};
+    const Span sst{scale_t, 4 * rg * (block_rows == 1 ? cols : cg), "scale_t"};
+    if ((s = check_disjoint(sq, {sx, sqt, ss, sst})) != RLK_OK) return s;
+    if ((s = check_disjoint(sqt, {sx, ss, sst})) != RLK_OK) return s;
+    if ((s = check_disjoint(ss, {sx, sst})) != RLK_OK) return s;
+    if ((s = check_disjoint(sst, {sx})) != RLK_OK) return s;
+    if ((s = select_device(x)) != RLK_OK) return s;
+    if ((s = check_device_ptrs({{q, "q"}, {scale, "scale"}, {qt, "qt"}, {scale_t, "scale_t"}})) != RLK_OK) return s;
+    return launch_fp8_quantize(rows, cols, x, x_type == RLK_F32, x_stride, block_rows, static_cast<uint8_t*>(q),
+                               q_stride, scale, static_cast<uint8_t*>(qt), qt_stride, scale_t,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+RLK_EXPORT rlk_status rlk_fp8_matmul(int64_t M, int64_t N, int64_t K, const void* a, int64_t a_stride,
+                                     const float* a_scale, const void* b, int64_t b_stride, const float* b_scale,
+                                     int32_t b_block_rows, void* c, int32_t c_type, int64_t c_stride,
+                                     int32_t accumulate, void* workspace, rlk_stream_t stream) {
+    rlk_status s;
+    if (M < 0 || N < 0) return fail(RLK_ERR_INVALID_ARG, "M and N must be >= 0");
+    if (K < 1) return fail(RLK_ERR_INVALID_ARG, "K must be >= 1");
+    if (b_block_rows != 1 && b_block_rows != 128) return fail(RLK_ERR_INVALID_ARG, "b_block_rows must be 1 or 128");
+    if (c_type != RLK_BF16 && c_type != RLK_F32)
+        return fail(RLK_ERR_INVALID_ARG, "c_type must be RLK_BF16 or RLK_F32");
+    if (accumulate != 0 && accumulate != 1) return fail(RLK_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+    if (accumulate && c_type != RLK_F32) return fail(RLK_ERR_INVALID_ARG, "accumulate needs an RLK_F32 c");
+    if (M > kMaxDim8 || N > kMaxDim8 || K > kMaxDim8 ||
+        ((M + 127) / 128) * ((N + 127) / 128) > ((int64_t)1 << 30))
+        return fail(RLK_ERR_UNSUPPORTED, "M, N or K above 2^31 - 512, or above 2^30 tiles of 128 x 128");
+    if (M == 0 || N == 0) return RLK_OK;
+    if (!a || !b || !a_scale || !b_scale || !c)
+        return fail(RLK_ERR_INVALID_ARG, "a, a_scale, b, b_scale and c are required");
+    if (!workspace) return fail(RLK_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned16(workspace)) return fail(RLK_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    if ((s = check_codes("a", a, a_stride, K)) != RLK_OK) return s;
+    if ((s = check_codes("b", b, b_stride, K)) != RLK_OK) return s;
+    if ((s = check_natural("a_scale", a_scale, 4)) != RLK_OK) return s;
+    if ((s = check_natural("b_scale", b_scale, 4)) != RLK_OK) return s;
+    const int64_t size = c_type == RLK_F32 ? 4 : 2, groups = (K + 127) / 128;
+    if ((s = check_natural("c", c, size)) != RLK_OK) return s;
+    if (c_stride < N) return fail(RLK_ERR_INVALID_ARG, "c_stride must be >= N");
+    if (c_stride > ((int64_t)1 << 38)) return fail(RLK_ERR_UNSUPPORTED, "c_stride above 2^38");
+    if ((s = check_disjoint({c, extent(M, c_stride, N, size), "c"},
+                            {{a, extent(M, a_stride, K, 1), "a"},
+                             {b, extent(N, b_stride, K, 1), "b"},
+                             {a_scale, 4 * groups * M, "a_scale"},
+                             {b_scale, 4 * groups * (b_block_rows == 1 ? N : (N + 127) / 128), "b_scale"},
+                             {workspace, RLK_FP8_WORKSPACE, "workspace"}})) != RLK_OK)
+        return s;
+    if ((s = select_device(a)) != RLK_OK) return s;
+    if ((s = check_device_ptrs({{a_scale, "a_scale"}, {b, "b"}, {b_scale, "b_scale"}, {c, "c"},
+                                {workspace, "workspace"}})) != RLK_OK)
+        return s;
+    return launch_fp8_matmul(M, N, K, a, a_stride, a_scale, b, b_stride, b_scale, b_block_rows, c, c_stride,
+                             c_type == RLK_F32, accumulate, static_cast<uint32_t*>(workspace),
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
 RLK_EXPORT rlk_status rlk_logp_workspace_status(const void* workspace, rlk_stream_t stream) {
     if (!workspace) return fail(RLK_ERR_INVALID_ARG, "workspace is NULL");
     rlk_status s = select_device(workspace);

@@ -126,6 +126,17 @@ rlk_status launch_grpo_loss(int64_t T, const float* logp, const float* adv, cons
 rlk_status launch_grpo_count(int64_t T, const int64_t* targets, const uint8_t* mask, int64_t ignore_index,
                              uint8_t* mask_out, unsigned long long* n_active, int sm_count, cudaStream_t stream);
 
+// Quantisation to E4M3 with a scale per group of 128 (fp8_quant.cu); q and/or
+// qt (the transpose), each with its scales.
+rlk_status launch_fp8_quantize(int64_t rows, int64_t cols, const void* x, int32_t x_f32, int64_t ldx,
+                               int32_t block_rows, uint8_t* q, int64_t ldq, float* scale, uint8_t* qt, int64_t ldqt,
+                               float* scale_t, cudaStream_t stream);
+
+// C = A B^T of such operands (fp8_gemm.cu); *status is only ever set.
+rlk_status launch_fp8_matmul(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, const float* sa,
+                             const void* b, int64_t ldb, const float* sb, int32_t b_block_rows, void* c, int64_t ldc,
+                             int32_t c_f32, int32_t accumulate, uint32_t* status, cudaStream_t stream);
+
 // Launches the bounded-wait self-test kernel (one warp waiting on an mbarrier
 // that nothing arrives at).
 rlk_status launch_selftest_wait(uint64_t limit_ns, uint32_t* status, cudaStream_t stream);
