@@ -39,9 +39,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <mutex>
 #include <string>
 
+#include "rlk_gemm.cuh"
 #include "rlk_internal.h"
 #include "rlk_ptx.cuh"
 
@@ -642,29 +642,10 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
 
 // ----------------------------------------------------------------- host
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn8() {
-    static std::mutex mu;
-    static EncodeTiled fn = nullptr;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!fn) {
-        void* ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiled>(ptr);
-    }
-    return fn;
-}
-
 // A byte matrix of `rows` rows of `inner` bytes, `stride` apart, in boxes of
 // 128 bytes x box_rows with the 128-byte swizzle; bytes outside read as zero.
 bool make_map8(CUtensorMap* m, const void* base, int64_t inner, int64_t rows, int64_t stride, uint32_t box_rows) {
-    EncodeTiled enc = encode_fn8();
+    EncodeTiled enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)stride};
