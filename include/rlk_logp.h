@@ -450,6 +450,87 @@ rlk_status rlk_logp_fwd_noalloc(const rlk_logp_contract* contract, const void* l
                                 float* lse, float* partials, rlk_stream_t stream);
 
 /*
+ * Softmax cross entropy of logits = hidden @ weight^T over V classes, and its
+ * gradients, without keeping the logits: the loss of a fine-tuning step, with
+ * what such steps ask for beside the selected log-probability.  (The pages
+ * have no counterpart: their step ends in the GRPO loss.)  Per row r, target t:
+ *     y_c = softcap tanh(x_c / softcap) with a softcap, else x_c (FP32 logits);
+ *     lse = log sum_c e^y_c;
+ *     L   = lse - (1 - label_smoothing) y_t - (label_smoothing / V) sum_c y_c
+ *           + z_loss lse^2   on active rows, 0 on inactive ones.
+ * hidden [T, H] and weight [V, H] are BF16, row-major; any T, V and H, rows on
+ * 16-byte boundaries (strides a multiple of 8 elements, 0 -> H).  Every row of
+ * hidden is read, an inactive row's too: its values must be finite, or they
+ * reach dweight as 0 * NaN.
+ */
+typedef enum {
+    RLK_REDUCE_NONE = 0,  /* loss [T] */
+    RLK_REDUCE_SUM = 1,   /* one value */
+    RLK_REDUCE_MEAN = 2   /* one value: the sum over the number of active rows; 0 without any */
+} rlk_reduction;
+
+typedef struct {
+    int64_t T, V, H;
+    int64_t hidden_stride;    /* elements between rows; 0 -> H */
+    int64_t weight_stride;
+    int64_t dhidden_stride;   /* of the gradients; 0 -> H */
+    int64_t dweight_stride;
+    int64_t ignore_index;     /* RLK_MASK_IGNORE_INDEX only */
+    int64_t wait_timeout_ns;  /* bound of every device-side wait; 0 -> 2 s */
+    int64_t piece;            /* vocabulary rows the backward takes at a time; 0 -> as many as keep a
+                                 piece's gradient within 512 MB (2048 at least) */
+    int32_t mask_mode;        /* rlk_mask_mode */
+    int32_t reduction;        /* rlk_reduction */
+    int32_t validate;         /* 0: asynchronous; 1: synchronise and report device status */
+    float label_smoothing;    /* [0, 1] */
+    float z_loss;             /* >= 0 */
+    float softcap;            /* 0: none; > 0 */
+} rlk_linear_ce_contract;     /* 104 bytes, no padding */
+
+/* Host-only validation (touches no device). */
+rlk_status rlk_linear_ce_check(const rlk_linear_ce_contract* contract);
+
+/*
+ * Bytes of device workspace: of the forward (with_grad 0), or of either call
+ * (1): about T V / 32 for the forward's partials (half as much again with
+ * label smoothing); T piece * 2 + T H * 4 for the backward, whatever V is.
+ * 0 for an invalid contract.
+ */
+size_t rlk_linear_ce_workspace_size(const rlk_linear_ce_contract* contract, int32_t with_grad);
+
+/*
+ * Forward.
+ *   targets, active_mask  as for rlk_logp_fwd; active targets in [0, V).
+ *   loss       [T] FP32 out, or one value (reduction).  An active row whose
+ *              target is out of range has a NaN loss.
+ *   lse        [T] FP32 out, every row.
+ *   workspace  rlk_linear_ce_workspace_size bytes, 16-byte aligned, one call's
+ *              at a time.
+ * Device status (validate == 1, or rlk_logp_workspace_status): as for
+ * rlk_logp_fwd.  T = 0: a reduced loss is 0.
+ */
+rlk_status rlk_linear_ce_fwd(const rlk_linear_ce_contract* contract, const void* hidden_bf16, const void* weight_bf16,
+                             const int64_t* targets, const uint8_t* active_mask, float* loss, float* lse,
+                             void* workspace, rlk_stream_t stream);
+
+/*
+ * Backward, from the forward's lse.
+ *   grad_loss  [T] FP32 (RLK_REDUCE_NONE) or one FP32 value: the upstream
+ *              gradient of the loss.
+ *   dhidden    [T, dhidden_stride] BF16 out, or NULL (a frozen trunk);
+ *   dweight    [V, dweight_stride] BF16 out, or NULL (a frozen head); at least
+ *              one of the two.  16-byte aligned, strides a multiple of 8.
+ * Inactive rows have a zero dhidden and add nothing to dweight.  The logits'
+ * gradient is rounded to BF16 between the products, with a summed or averaged
+ * loss's common factor left out of it and applied to the FP32 sums.  The
+ * order of every sum is fixed.  No output may overlap an input.
+ */
+rlk_status rlk_linear_ce_bwd(const rlk_linear_ce_contract* contract, const void* hidden_bf16, const void* weight_bf16,
+                             const int64_t* targets, const uint8_t* active_mask, const float* lse,
+                             const float* grad_loss, void* dhidden_bf16, void* dweight_bf16, void* workspace,
+                             rlk_stream_t stream);
+
+/*
  * FP8 projections: E4M3 operands with one FP32 scale for each group of 128.
  * (The pages have no counterpart: they score BF16 models.  These calls give
  * a model whose tokens the calls above score its 8-bit projections, and an

@@ -48,7 +48,7 @@ def matmul(a, sa, b, sb, b_block_rows):
     return da @ db.T, np.abs(da) @ np.abs(db).T
 
 
-def bound(K, out, terms):
+def bound(K, terms):
     """How far an FP32 sum of the product may be from 64 bits.
 
     A group's sum takes at most 128 additions, its scaling and addition to the total 3 roundings, and the total one
@@ -56,4 +56,4 @@ def bound(K, out, terms):
     where the tensor core truncates).
     """
     n = min(K, GROUP) + 3 + groups(K)
-    return n * 2.0 ** -23 * terms + 1e-37 + (2.0 ** -9 * np.abs(out))
+    return n * 2.0 ** -23 * terms + 1e-37

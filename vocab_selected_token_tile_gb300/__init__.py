@@ -27,6 +27,10 @@ RLK_F32 = 1
 
 RLK_FP8_WORKSPACE = 256
 
+REDUCE_NONE = 0
+REDUCE_SUM = 1
+REDUCE_MEAN = 2
+
 MASK_EXPLICIT = 0
 MASK_IGNORE_INDEX = 1
 
@@ -51,6 +55,10 @@ EXPORTED = (
     "rlk_logp_shard_fwd",
     "rlk_logp_fold",
     "rlk_logp_shard_bwd",
+    "rlk_linear_ce_check",
+    "rlk_linear_ce_workspace_size",
+    "rlk_linear_ce_fwd",
+    "rlk_linear_ce_bwd",
     "rlk_fp8_quantize",
     "rlk_fp8_matmul",
     "rlk_logp_workspace_status",
@@ -84,6 +92,25 @@ class Contract(ctypes.Structure):
         d = {name: getattr(self, name) for name, _ in self._fields_}
         d.update(kw)
         return Contract(**d)
+
+
+class LinearCeContract(ctypes.Structure):
+    """Mirror of ``rlk_linear_ce_contract`` (104 bytes); strides and piece 0 take the header's defaults."""
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "V", "H", "hidden_stride", "weight_stride", "dhidden_stride",
+                                              "dweight_stride", "ignore_index", "wait_timeout_ns", "piece")] + \
+               [(n, ctypes.c_int32) for n in ("mask_mode", "reduction", "validate")] + \
+               [(n, ctypes.c_float) for n in ("label_smoothing", "z_loss", "softcap")]
+
+    def __init__(self, T, V, H, hidden_stride=0, weight_stride=0, dhidden_stride=0, dweight_stride=0,
+                 ignore_index=-100, wait_timeout_ns=0, piece=0, mask_mode=MASK_EXPLICIT, reduction=REDUCE_NONE,
+                 validate=0, label_smoothing=0.0, z_loss=0.0, softcap=0.0):
+        super().__init__(T, V, H, hidden_stride, weight_stride, dhidden_stride, dweight_stride, ignore_index,
+                         wait_timeout_ns, piece, mask_mode, reduction, validate, label_smoothing, z_loss, softcap)
+
+    def replace(self, **kw):
+        d = {name: getattr(self, name) for name, _ in self._fields_}
+        d.update(kw)
+        return LinearCeContract(**d)
 
 
 class RlkError(RuntimeError):
@@ -145,6 +172,15 @@ def library():
         lib.rlk_logp_fold.restype = i
         lib.rlk_logp_shard_bwd.argtypes = [P, ctypes.c_int32, vp, vp, vp, vp, vp, vp, vp, vp]
         lib.rlk_logp_shard_bwd.restype = i
+        C = ctypes.POINTER(LinearCeContract)
+        lib.rlk_linear_ce_check.argtypes = [C]
+        lib.rlk_linear_ce_check.restype = i
+        lib.rlk_linear_ce_workspace_size.argtypes = [C, ctypes.c_int32]
+        lib.rlk_linear_ce_workspace_size.restype = ctypes.c_size_t
+        lib.rlk_linear_ce_fwd.argtypes = [C, vp, vp, vp, vp, vp, vp, vp, vp]
+        lib.rlk_linear_ce_fwd.restype = i
+        lib.rlk_linear_ce_bwd.argtypes = [C, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        lib.rlk_linear_ce_bwd.restype = i
         i64 = ctypes.c_int64
         lib.rlk_fp8_quantize.argtypes = [i64, i64, vp, ctypes.c_int32, i64, ctypes.c_int32, vp, i64, vp, vp, i64, vp,
                                          vp]
@@ -272,6 +308,25 @@ def rlk_logp_shard_bwd(contract, shard, logits_shard, targets, active_mask, lse_
                        workspace, stream):
     return library().rlk_logp_shard_bwd(ctypes.byref(contract), shard, logits_shard, targets, active_mask, lse_in,
                                         grad_logp, dlogits_shard, workspace, stream)
+
+
+def rlk_linear_ce_check(contract):
+    return library().rlk_linear_ce_check(ctypes.byref(contract))
+
+
+def rlk_linear_ce_workspace_size(contract, with_grad):
+    return library().rlk_linear_ce_workspace_size(ctypes.byref(contract), with_grad)
+
+
+def rlk_linear_ce_fwd(contract, hidden, weight, targets, active_mask, loss, lse, workspace, stream):
+    return library().rlk_linear_ce_fwd(ctypes.byref(contract), hidden, weight, targets, active_mask, loss, lse,
+                                       workspace, stream)
+
+
+def rlk_linear_ce_bwd(contract, hidden, weight, targets, active_mask, lse, grad_loss, dhidden, dweight, workspace,
+                      stream):
+    return library().rlk_linear_ce_bwd(ctypes.byref(contract), hidden, weight, targets, active_mask, lse, grad_loss,
+                                       dhidden, dweight, workspace, stream)
 
 
 def rlk_fp8_quantize(rows, cols, x, x_type, x_stride, block_rows, q, q_stride, scale, qt, qt_stride, scale_t, stream):
@@ -879,3 +934,82 @@ def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=Non
     if validate:
         check(rlk_logp_workspace_status(_ptr(workspace), st))
     return out
+
+
+# ------------------------------------------------------------------ cross entropy over a large vocabulary
+
+def _row_stride(t, name, kinds):
+    """A BF16 matrix's row stride; one row takes one of whole 16-byte pieces."""
+    stride = _matrix(t, name, kinds)
+    return -(-t.shape[1] // 8) * 8 if t.shape[0] <= 1 else stride
+
+
+def linear_ce_contract(hidden, weight, mask=None, ignore_index=-100, reduction=REDUCE_NONE, label_smoothing=0.0,
+                       z_loss=0.0, softcap=0.0, piece=0, validate=0, wait_timeout_ns=0):
+    """The contract of linear_ce_fwd and linear_ce_bwd for these operands: hidden [T, H] and weight [V, H], BF16,
+    rows on 16-byte boundaries.  The gradients have rows of whole 16-byte pieces."""
+    hs, wstr = _row_stride(hidden, "hidden", _BF16), _row_stride(weight, "weight", _BF16)
+    (T, H), (V, Hw) = hidden.shape, weight.shape
+    if Hw != H:
+        raise ValueError(f"hidden is [{T}, {H}] and weight [{V}, {Hw}]: their rows must have one length")
+    out = -(-H // 8) * 8
+    c = LinearCeContract(T, V, H, hs, wstr, out, out, ignore_index, wait_timeout_ns, piece,
+                         MASK_EXPLICIT if mask is not None else MASK_IGNORE_INDEX, reduction, validate,
+                         label_smoothing, z_loss, softcap)
+    check(rlk_linear_ce_check(c))
+    return c
+
+
+def _ce_workspace(contract, with_grad, dev, workspace):
+    import torch
+    n = rlk_linear_ce_workspace_size(contract, with_grad)
+    if n == 0:
+        check(rlk_linear_ce_check(contract) or RLK_ERR_UNSUPPORTED)
+    if workspace is None:
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", n, ("uint8",))
+    return workspace
+
+
+def _ce_operands(c, hidden, weight, targets, mask):
+    for name, t, rows, stride in (("hidden", hidden, c.T, c.hidden_stride or c.H),
+                                  ("weight", weight, c.V, c.weight_stride or c.H)):
+        if tuple(t.shape) != (rows, c.H) or _row_stride(t, name, _BF16) != stride and rows > 1:
+            raise ValueError(f"{name} is {list(t.shape)} with strides {list(t.stride())}; the contract's is "
+                             f"[{rows}, {c.H}] with rows {stride} apart")
+    _rowwise(c, targets, mask)
+
+
+def linear_ce_fwd(contract, hidden, weight, targets, mask=None, stream=None, workspace=None):
+    """(loss, lse) of the cross entropy of hidden @ weight^T: loss [T], or one value with a reduction; lse [T]."""
+    import torch
+    _ce_operands(contract, hidden, weight, targets, mask)
+    dev, T = hidden.device, contract.T
+    loss = torch.empty((T,) if contract.reduction == REDUCE_NONE else (), dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    ws = _ce_workspace(contract, 0, dev, workspace)
+    check(rlk_linear_ce_fwd(contract, _ptr(hidden), _ptr(weight), _ptr(targets), _ptr(mask), _ptr(loss), _ptr(lse),
+                            _ptr(ws), _stream(stream)))
+    return loss, lse
+
+
+def linear_ce_bwd(contract, hidden, weight, targets, mask, lse, grad_loss, need_dhidden=True, need_dweight=True,
+                  stream=None, workspace=None):
+    """(dhidden [T, H], dweight [V, H]) in BF16 from the forward's lse and the loss's FP32 gradient ([T], or one value
+    with a reduction); a gradient that is not needed is None and costs nothing."""
+    import torch
+    _ce_operands(contract, hidden, weight, targets, mask)
+    dev, T, V, H = hidden.device, contract.T, contract.V, contract.H
+    _need(lse, "lse", 4 * T, _F32)
+    _need(grad_loss, "grad_loss", 4 * (T if contract.reduction == REDUCE_NONE else 1), _F32)
+
+    def out(rows, stride):
+        t = torch.empty((rows, stride or H), dtype=hidden.dtype, device=dev)
+        return t if t.shape[1] == H else t[:, :H]
+
+    dh = out(T, contract.dhidden_stride) if need_dhidden else None
+    dw = out(V, contract.dweight_stride) if need_dweight else None
+    ws = _ce_workspace(contract, 1, dev, workspace)
+    check(rlk_linear_ce_bwd(contract, _ptr(hidden), _ptr(weight), _ptr(targets), _ptr(mask), _ptr(lse),
+                            _ptr(grad_loss), _ptr(dh), _ptr(dw), _ptr(ws), _stream(stream)))
+    return dh, dw

@@ -1,0 +1,1032 @@
+// Softmax cross entropy of logits = hidden @ weight^T over a large vocabulary,
+// and its gradients, without keeping the logits (sm_103a).
+//
+// Per row r with target t, logits x_c = hidden_r . weight_c, c < V:
+//   y_c   = cap tanh(x_c / cap), or x_c without a cap;
+//   lse   = log sum_c e^y_c;
+//   L     = lse - (1 - eps) y_t - (eps / V) sum_c y_c + z lse^2;
+//   dL/dx_c = ((1 + 2 z lse) p_c - (1 - eps) [c = t] - eps / V) (1 - (y_c / cap)^2),
+//   p_c = e^(y_c - lse).
+// Label smoothing eps, z-loss z and the cap are 0 when unused.
+//
+// Forward: one tcgen05 GEMM over units of (256 vocabulary rows, 128 tokens)
+// whose epilogue turns a row's 256 logits into one (max, sumexp[, sum])
+// partial, then a merge of each row's partials in vocabulary order.  Bound:
+// the tensor core, 2 T V H operations; the epilogue of one accumulator runs
+// under the MMAs of the other.
+//
+// Backward, in pieces of the vocabulary: for each piece the logits are formed
+// again (the price of not keeping them: 2 T V H operations more) and leave
+// the epilogue as BF16 dL/dx [T, P], and one launch then runs both
+//   dHidden[T, H] += dx weight[piece]     (FP32 sums across the pieces)
+//   dWeight[piece] = dx^T hidden.
+// The work space is P T 2 bytes for dx and T H 4 for the sums, whatever V is.
+// P is chosen so that dx stays within kPieceBytes: the sums are read and
+// written once a piece, and with pieces that large that traffic and the ends
+// of the launches are under 2% of a piece's time.
+//
+// What is rounded to BF16 is dx / scale, with scale = the upstream gradient of
+// a summed or averaged loss (the largest row's otherwise): with a common
+// factor folded in, the value of every row's largest entry, about -g, would
+// be rounded in the same direction, a bias of up to 2^-9 in both gradients.
+// The scale multiplies the FP32 sums instead.
+//
+// The roles, waits and unit queue are the lm_head kernels' (rlk_gemm.cuh):
+// warp 0 issues the TMA loads, warp 1 the MMAs, warps 2-5 are the epilogue.
+// Every sum has a fixed order: no split of a K range without an ordered join,
+// no atomics on data.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "rlk_fold.cuh"
+#include "rlk_gemm.cuh"
+#include "rlk_internal.h"
+#include "rlk_ptx.cuh"
+
+namespace rlk {
+namespace {
+
+constexpr int64_t kPieceBytes = (int64_t)512 << 20;  // BF16 dx of one piece
+constexpr int kMinPiece = 2048;                      // vocabulary rows a piece at least
+constexpr int kMaxPieces = 512;
+constexpr size_t kCeTicketBytes = (2 * kMaxPieces + 32) * 8;
+constexpr int kMaxSlices = 32;                       // K slices of dHidden within a piece
+constexpr int64_t kBandBytes = (int64_t)32 << 20;    // hidden of one band of token blocks (as the lm_head's)
+constexpr int kBandH = 8;                            // H blocks per band of the gradient tiles (as the lm_head's)
+constexpr int kFoldSlices = 16;
+
+constexpr size_t kCeSmemCore = ((size_t)kStages * (kStageA + kStageB) + sizeof(Bars) + 1023) / 1024 * 1024;
+constexpr size_t kCeSmem = 1024 + kCeSmemCore;
+constexpr uint32_t kDxStage = 32 * 128;  // per epilogue warp: 32 rows x 64 BF16, one TMA store
+constexpr size_t kCeSmemDx = kCeSmem + 4 * kDxStage;
+
+enum : int { kCeForward = 0, kCeGrad = 1 };
+enum : int32_t { kNoTarget = -1, kInactive = -2 };
+
+struct CeParams {
+    const int64_t* targets;
+    const uint8_t* mask;
+    float2* part;           // [chunks, T] (max, sumexp)         forward
+    float* part_y;          // [chunks, T] sum of y              forward, with smoothing
+    float* yt;              // [T] the target's y                forward
+    const float4* rows;     // [T] (a, b, c, -lse log2 e)        gradient
+    const int32_t* target;  // [T] target, kNoTarget or kInactive  gradient
+    unsigned long long* ticket;
+    WaitCtl w;
+    int64_t T, V, ignore_index;
+    float cap, icap;
+    int32_t KB, mask_mode;
+    int32_t ch0, nch;       // the launch's chunks of 256 vocabulary rows
+    int32_t MB, MBg;        // token blocks, and per band
+};
+
+__device__ __forceinline__ void ce_unit(const CeParams& p, int64_t u, int& ch, int& mb) {
+    const int64_t band = (int64_t)p.nch * p.MBg;
+    const int64_t full = p.MB / p.MBg;
+    const int64_t b = u / band < full ? u / band : full;
+    const int64_t r = u - b * band;
+    const int w = b < full ? p.MBg : p.MB - (int)full * p.MBg;
+    ch = p.ch0 + (int)(r / w);
+    mb = (int)(b * p.MBg + r % w);
+}
+
+// y = cap tanh(x / cap) with r = 2 / (e^(2 |x| / cap) + 1): tanh = sign (1 - r),
+// within a few 2^-24 of 1 absolutely, which the cap scales to a few 10^-6 of a
+// logit; and its slope 1 - tanh^2 = r (2 - r), which keeps its relative
+// precision where tanh saturates.
+__device__ __forceinline__ float ce_cap(float x, float cap, float icap, float& slope) {
+    const float e = ex2_approx(__fmul_rn(__fmul_rn(fabsf(x), icap), 2.f * kLog2e));
+    const float r = __fdividef(2.f, __fadd_rn(e, 1.f));
+    slope = __fmul_rn(r, __fsub_rn(2.f, r));
+    return copysignf(__fmul_rn(cap, __fsub_rn(1.f, r)), x);
+}
+
+// One block of up to 32 logits into the row's running (max, sumexp, sum).
+template <bool SMOOTH>
+__device__ __forceinline__ void ce_online(const float (&y)[32], int nv, float& m_run, float& s_run, float& y_run) {
+    float bm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i < nv) bm = fmax_nan(bm, y[i]);
+    if (bm > m_run || bm != bm) {
+        s_run = __fmul_rn(s_run, ex2_approx(__fmul_rn(__fsub_rn(m_run, bm), kLog2e)));
+        m_run = bm;
+    }
+    if (SMOOTH) {
+        float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < nv) a[i & 3] = __fadd_rn(a[i & 3], y[i]);
+        y_run = __fadd_rn(y_run, __fadd_rn(__fadd_rn(a[0], a[1]), __fadd_rn(a[2], a[3])));
+    }
+    if (m_run == -INFINITY) return;  // nothing finite yet
+    const float nmL = -__fmul_rn(m_run, kLog2e);
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float e = ex2_approx(__fmaf_rn(y[i], kLog2e, nmL));
+        if (i < nv) a[i & 3] = __fadd_rn(a[i & 3], e);
+    }
+    s_run = __fadd_rn(s_run, __fadd_rn(__fadd_rn(a[0], a[1]), __fadd_rn(a[2], a[3])));
+}
+
+template <int MODE, bool CAP, bool SMOOTH>
+__global__ void __launch_bounds__(kThreadsLm, 1)
+    ce_logits_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
+                     const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CeParams p) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* sA = smem;
+    unsigned char* sB = smem + kStages * kStageA;
+    Bars* bars = reinterpret_cast<Bars*>(smem + kStages * (kStageA + kStageB));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t total = (int64_t)p.nch * p.MB;
+
+    if (threadIdx.x == 0) init_bars(bars);
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&bars->tmem_addr), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_addr;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t issued = 0, n = 0;
+            bool aborted = false;
+            const uint64_t keep = l2_policy_evict_last();
+            while (!aborted) {
+                int64_t u = (int64_t)atomicAdd(p.ticket, 1ull);
+                if (u >= total) u = -1;
+                if (!unit_put(bars, n++, u, p.w) || u < 0) break;
+                int ch, mb;
+                ce_unit(p, u, ch, mb);
+                for (int kb = 0; kb < p.KB; ++kb) {
+                    if (!lm_wait(bars, smem_u32(&bars->empty[stage]), phase ^ 1u, p.w)) {
+                        aborted = true;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&bars->full[stage]);
+                    mbar_arrive_expect_tx(fb, kStageA + kStageB);
+                    tma_load_2d_hint(smem_u32(sA + stage * kStageA), &tmH, kb * kBK, mb * kBM, fb, keep);
+                    tma_load_2d(smem_u32(sB + stage * kStageB), &tmW, kb * kBK, ch * kBN, fb);
+                    ++issued;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            drain_copies(bars, issued, p.w);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t tiles = 0, n = 0;
+            bool aborted = false;
+            const uint32_t idesc = idesc_bf16_f32(kBM, kBN);
+            while (!aborted) {
+                int64_t u;
+                if (!unit_get(bars, n, u, p.w)) break;
+                unit_done(bars, n++);
+                if (u < 0) break;
+                const int acc = (int)(tiles & 1);
+                const uint32_t accph = (uint32_t)((tiles >> 1) & 1);
+                ++tiles;
+                if (!lm_wait(bars, smem_u32(&bars->tempty[acc]), accph ^ 1u, p.w)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * kBN);
+                for (int kb = 0; kb < p.KB; ++kb) {
+                    if (!lm_wait(bars, smem_u32(&bars->full[stage]), phase, p.w)) {
+                        aborted = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(sA + stage * kStageA), b0 = smem_u32(sB + stage * kStageB);
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        umma_bf16(d, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32), idesc,
+                                  (kb | kk) != 0);
+                    umma_commit(smem_u32(&bars->empty[stage]));
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!aborted) umma_commit(smem_u32(&bars->tfull[acc]));
+            }
+            umma_commit(smem_u32(&bars->drain));
+            lm_drain_wait(smem_u32(&bars->drain), 0u, p.w);
+        }
+    } else {
+        const int quarter = warp & 3;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        unsigned char* dst = smem + kCeSmemCore + quarter * kDxStage;  // kCeGrad
+        int64_t tiles = 0, n = 0;
+        for (;;) {
+            int64_t u = -1;
+            const bool got = unit_get(bars, n, u, p.w);
+            if (!__all_sync(0xFFFFFFFFu, got)) break;
+            __syncwarp();
+            if (lane == 0) unit_done(bars, n);
+            ++n;
+            if (u < 0) break;
+            int ch, mb;
+            ce_unit(p, u, ch, mb);
+            const int64_t row = (int64_t)mb * kBM + quarter * 32 + lane;
+            const bool valid = row < p.T;
+            int64_t target = kNoTarget;
+            bool active = false;
+            float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (valid && MODE == kCeForward) {
+                target = p.targets[row];
+                active = (p.mask_mode == RLK_MASK_EXPLICIT) ? (p.mask[row] != 0) : (target != p.ignore_index);
+            }
+            if (valid && MODE == kCeGrad) {
+                q = p.rows[row];
+                target = p.target[row];
+                active = target != kInactive;
+            }
+            const int acc = (int)(tiles & 1);
+            const uint32_t accph = (uint32_t)((tiles >> 1) & 1);
+            ++tiles;
+            const bool ok = lm_wait(bars, smem_u32(&bars->tfull[acc]), accph, p.w);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc_fence_after();
+            float m_run = -INFINITY, s_run = 0.f, y_run = 0.f;
+            const int64_t cbase = (int64_t)ch * kBN;
+            const int ncols = (int)(p.V - cbase < kBN ? p.V - cbase : kBN);
+            for (int sub = 0; sub * 32 < ncols; ++sub) {
+                float v[32];
+                tmem_ld32(tmem + lane_base + (uint32_t)(acc * kBN + sub * 32), v);
+                const int nv = min(32, ncols - sub * 32);
+                const int64_t hot = target - (cbase + sub * 32);
+                const bool here = active && hot >= 0 && hot < nv;
+                const uint32_t hot_bit = here ? 1u << (int)hot : 0u;  // an index into v would spill it
+                if (MODE == kCeForward) {
+                    if (CAP) {
+                        float slope;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = ce_cap(v[i], p.cap, p.icap, slope);
+                    }
+                    ce_online<SMOOTH>(v, nv, m_run, s_run, y_run);
+                    if (here) {
+                        float yt = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (hot_bit & (1u << i)) yt = v[i];
+                        p.yt[row] = yt;
+                    }
+                    continue;
+                }
+                // dx = (a p - c - b [c = t]) slope
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    float slope = 1.f;
+                    const float y = CAP ? ce_cap(v[i], p.cap, p.icap, slope) : v[i];
+                    float d = __fmaf_rn(ex2_approx(__fmaf_rn(y, kLog2e, q.w)), q.x, -q.z);
+                    if (hot_bit & (1u << i)) d = __fsub_rn(d, q.y);
+                    if (CAP) d = __fmul_rn(d, slope);
+                    v[i] = active ? d : 0.f;
+                }
+                // 64 columns a store: this block is half of the staged 128-byte rows (16-byte
+                // piece j of row r at j ^ (r mod 8)); the tensor map clips rows and columns outside
+                if ((sub & 1) == 0) {
+                    if (lane == 0) bulk_wait_read_all();  // the previous store has read the block
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<uint4*>(dst + lane * 128 + ((((sub & 1) * 4 + j) ^ (lane & 7)) * 16)) =
+                        make_uint4(pack_bf16x2_rn(v[8 * j], v[8 * j + 1]), pack_bf16x2_rn(v[8 * j + 2], v[8 * j + 3]),
+                                   pack_bf16x2_rn(v[8 * j + 4], v[8 * j + 5]),
+                                   pack_bf16x2_rn(v[8 * j + 6], v[8 * j + 7]));
+                if ((sub & 1) == 1 || (sub + 1) * 32 >= ncols) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&tmD, (ch - p.ch0) * kBN + (sub >> 1) * 64, mb * kBM + quarter * 32,
+                                     smem_u32(dst));
+                        bulk_commit();
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
+            if (MODE == kCeForward && valid) {
+                p.part[(int64_t)ch * p.T + row] = make_float2(m_run, s_run);
+                if (SMOOTH) p.part_y[(int64_t)ch * p.T + row] = y_run;
+            }
+        }
+        if (MODE == kCeGrad && lane == 0) bulk_wait_all();  // the stores complete before the CTA exits
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// (m, s) with (m2, s2): the larger maximum, both sums scaled to it; a maximum
+// of -inf adds nothing, a NaN stays.
+__device__ __forceinline__ void ce_merge(float& m, float& s, float m2, float s2) {
+    if (m2 == -INFINITY) return;
+    const float M = fmax_nan(m, m2);
+    s = __fadd_rn(__fmul_rn(s, m == -INFINITY ? 0.f : ex2_approx(__fmul_rn(__fsub_rn(m, M), kLog2e))),
+                  __fmul_rn(s2, ex2_approx(__fmul_rn(__fsub_rn(m2, M), kLog2e))));
+    m = M;
+}
+
+struct CeFold {
+    const float2* part;
+    const float* part_y;  // NULL without smoothing
+    const float* yt;
+    const int64_t* targets;
+    const uint8_t* mask;
+    float* loss;
+    float* lse;
+    uint32_t* status;
+    int64_t T, V, ignore_index;
+    int32_t chunks, mask_mode;
+    float eps, z;
+};
+
+// Each row's LSE and loss from its partials: 32 rows a CTA, 16 threads a row
+// take runs of chunks in vocabulary order, and their results are merged in
+// order.  The order depends on the number of chunks only.
+__global__ void __launch_bounds__(32 * kFoldSlices) ce_fold_kernel(const CeFold p) {
+    __shared__ float2 sm[kFoldSlices][32];
+    __shared__ float sy[kFoldSlices][32];
+    const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+    float m = -INFINITY, s = 0.f, y = 0.f;
+    if (row < p.T) {
+        const int c0 = (int)((int64_t)p.chunks * sl / kFoldSlices), c1 = (int)((int64_t)p.chunks * (sl + 1) / kFoldSlices);
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) {
+            const float2 q = p.part[(int64_t)c * p.T + row];
+            ce_merge(m, s, q.x, q.y);
+            if (p.part_y) y = __fadd_rn(y, p.part_y[(int64_t)c * p.T + row]);
+        }
+    }
+    sm[sl][lane] = make_float2(m, s);
+    sy[sl][lane] = y;
+    __syncthreads();
+    if (sl != 0 || row >= p.T) return;
+    for (int k = 1; k < kFoldSlices; ++k) {
+        ce_merge(m, s, sm[k][lane].x, sm[k][lane].y);
+        y = __fadd_rn(y, sy[k][lane]);
+    }
+    const float l = m == -INFINITY ? -INFINITY : __fadd_rn(m, logf(s));
+    const int64_t t = p.targets[row];
+    const bool active = (p.mask_mode == RLK_MASK_EXPLICIT) ? (p.mask[row] != 0) : (t != p.ignore_index);
+    p.lse[row] = l;
+    float loss = 0.f;
+    if (active) {
+        if (t < 0 || t >= p.V) {
+            loss = __int_as_float(0x7FC00000);
+            atomicOr(p.status, kStatusTargetRange);
+        } else {
+            loss = __fmaf_rn(-(1.f - p.eps), p.yt[row], l);
+            if (p.eps != 0.f) loss = __fmaf_rn(-p.eps / (float)p.V, y, loss);
+            if (p.z != 0.f) loss = __fmaf_rn(p.z * l, l, loss);
+        }
+        if (!isfinite(l)) atomicOr(p.status, kStatusNonFinite);
+    }
+    p.loss[row] = loss;
+}
+
+// Block-wide sum in a fixed order (1024 threads).
+__device__ double block_sum(double v, double* scratch) {
+    __syncthreads();
+    scratch[threadIdx.x] = v;
+    __syncthreads();
+    for (int o = 512; o; o >>= 1) {
+        if ((int)threadIdx.x < o) scratch[threadIdx.x] += scratch[threadIdx.x + o];
+        __syncthreads();
+    }
+    return scratch[0];
+}
+
+__device__ __forceinline__ bool ce_active(const uint8_t* mask, int mask_mode, int64_t ignore_index, int64_t target,
+                                          int64_t r) {
+    return mask_mode == RLK_MASK_EXPLICIT ? mask[r] != 0 : target != ignore_index;
+}
+
+// The sum, or the mean over the active rows (0 without any), of the rows'
+// losses: one CTA, FP64, a fixed order.
+__global__ void __launch_bounds__(1024) ce_reduce_kernel(const float* loss, const int64_t* targets,
+                                                         const uint8_t* mask, int mask_mode, int64_t ignore_index,
+                                                         int64_t T, int mean, float* out) {
+    __shared__ double scratch[1024];
+    double s = 0., n = 0.;
+    for (int64_t r = threadIdx.x; r < T; r += 1024) {
+        s += (double)loss[r];
+        n += ce_active(mask, mask_mode, ignore_index, targets[r], r) ? 1. : 0.;
+    }
+    s = block_sum(s, scratch);
+    n = block_sum(n, scratch);
+    if (threadIdx.x == 0) *out = (float)(mean ? (n > 0. ? s / n : 0.) : s);
+}
+
+struct CeRows {
+    const int64_t* targets;
+    const uint8_t* mask;
+    const float* lse;
+    const float* grad;  // [T], or one value for a summed or averaged loss
+    float4* rows;
+    int32_t* target;
+    float* scale;
+    uint32_t* status;
+    int64_t T, V, ignore_index;
+    int32_t mask_mode, reduction;
+    float eps, z;
+};
+
+// Per row what its dx needs, and the common factor that is left out of it.
+__global__ void __launch_bounds__(1024) ce_rows_kernel(const CeRows p) {
+    __shared__ double scratch[1024];
+    float top = 0.f;
+    double n = 0.;
+    for (int64_t r = threadIdx.x; r < p.T; r += 1024) {
+        if (!ce_active(p.mask, p.mask_mode, p.ignore_index, p.targets[r], r)) continue;
+        n += 1.;
+        if (p.reduction == RLK_REDUCE_NONE) {
+            const float g = fabsf(p.grad[r]);
+            if (g < INFINITY) top = fmaxf(top, g);  // a non-finite gradient stays its own row's
+        }
+    }
+    float scale;
+    if (p.reduction == RLK_REDUCE_NONE) {
+        __syncthreads();
+        scratch[threadIdx.x] = top;
+        __syncthreads();
+        for (int o = 512; o; o >>= 1) {
+            if ((int)threadIdx.x < o) scratch[threadIdx.x] = fmax(scratch[threadIdx.x], scratch[threadIdx.x + o]);
+            __syncthreads();
+        }
+        scale = (float)scratch[0];
+        if (scale == 0.f) scale = 1.f;
+    } else {
+        n = block_sum(n, scratch);
+        scale = p.grad[0];
+        if (p.reduction == RLK_REDUCE_MEAN) scale = n > 0. ? (float)((double)scale / n) : 0.f;
+    }
+    if (threadIdx.x == 0) *p.scale = scale;
+    for (int64_t r = threadIdx.x; r < p.T; r += 1024) {
+        const int64_t t = p.targets[r];
+        const float l = p.lse[r];
+        int32_t to = kInactive;
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (ce_active(p.mask, p.mask_mode, p.ignore_index, t, r)) {
+            const float g = p.reduction == RLK_REDUCE_NONE ? __fdiv_rn(p.grad[r], scale) : 1.f;
+            q = make_float4(g * (1.f + 2.f * p.z * l), g * (1.f - p.eps), g * p.eps / (float)p.V,
+                            -__fmul_rn(l, kLog2e));
+            to = t >= 0 && t < p.V ? (int32_t)t : kNoTarget;
+            if (to == kNoTarget) atomicOr(p.status, kStatusTargetRange);
+            if (!isfinite(l)) atomicOr(p.status, kStatusNonFinite);
+        }
+        p.rows[r] = q;
+        p.target[r] = to;
+    }
+}
+
+// ----------------------------------------------------------------- the gradients' products
+
+struct CeGrads {
+    uint16_t* dhidden;  // [T, ldh] BF16, or NULL
+    uint16_t* dweight;  // the piece's rows, [cols, ldw] BF16, or NULL
+    float* sums;        // [S, T, Hs] FP32 sums of dHidden across the pieces
+    const float* scale;
+    unsigned long long* ticket;
+    WaitCtl w;
+    int64_t T, ldh, ldw, Hs;
+    int64_t n0, n1;     // tiles of dHidden (S slices of MB0 x NB) and of dWeight (MB1 x NB)
+    int32_t cols;       // vocabulary rows of the piece
+    int32_t H, NB, NBg, MB0, MB1, S, KB0, KB1;
+    int32_t first, last;  // the first and the last piece
+};
+
+struct CeTile {
+    int prob, mb, nb, nblk, slice, k0, k1;
+};
+
+// Tiles of dHidden first (their K range is the longer one), slice by slice;
+// bands of NBg H blocks, M-major within a band.
+__device__ __forceinline__ CeTile ce_tile(const CeGrads& p, int64_t u) {
+    CeTile t;
+    t.prob = u < p.n0 ? 0 : 1;
+    int64_t v = t.prob ? u - p.n0 : u;
+    const int64_t MB = t.prob ? p.MB1 : p.MB0;
+    t.slice = 0;
+    if (!t.prob) {
+        t.slice = (int)(v / (MB * p.NB));
+        v %= MB * p.NB;
+    }
+    const int64_t band = MB * p.NBg, full = p.NB / p.NBg;
+    const int64_t b = v / band < full ? v / band : full;
+    const int64_t r = v - b * band;
+    const int w = b < full ? p.NBg : p.NB - (int)full * p.NBg;
+    t.mb = (int)(r / w);
+    t.nb = (int)(b * p.NBg + r % w);
+    const int left = p.H - t.nb * kBN;
+    t.nblk = left >= kBN ? 4 : (left + 63) / 64;
+    t.k0 = t.prob ? 0 : (int)((int64_t)p.KB0 * t.slice / p.S);
+    t.k1 = t.prob ? p.KB1 : (int)((int64_t)p.KB0 * (t.slice + 1) / p.S);
+    return t;
+}
+
+// Up to 8 BF16 values of an output row; columns past H are not the row's.
+__device__ __forceinline__ void store_bf16x8(uint16_t* row, int col, int H, const float* v) {
+    const uint32_t w[4] = {pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
+                           pack_bf16x2_rn(v[6], v[7])};
+    if (col + 8 <= H) {
+        *reinterpret_cast<uint4*>(row + col) = make_uint4(w[0], w[1], w[2], w[3]);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (col + j < H) row[col + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+}
+
+// tmB*: the MN-major operand's 64-wide blocks in one 3-D box; tmC*: the same
+// matrix in 2-D boxes of one block, for the tile that holds H's ragged end.
+__global__ void __launch_bounds__(kThreadsLm, 1)
+    ce_grads_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
+                    const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmA1,
+                    const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmC1,
+                    const __grid_constant__ CeGrads p) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem =
+        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* sA = smem;
+    unsigned char* sB = smem + kStages * kStageA;
+    Bars* bars = reinterpret_cast<Bars*>(smem + kStages * (kStageA + kStageB));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t total = p.n0 + p.n1;
+
+    if (threadIdx.x == 0) init_bars(bars);
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&bars->tmem_addr), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_addr;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t issued = 0, n = 0;
+            bool aborted = false;
+            while (!aborted) {
+                int64_t u = (int64_t)atomicAdd(p.ticket, 1ull);
+                if (u >= total) u = -1;
+                if (!unit_put(bars, n++, u, p.w) || u < 0) break;
+                const CeTile t = ce_tile(p, u);
+                const int m0 = t.mb * kBM, h0 = t.nb * kBN;
+                const bool ragged = p.H - h0 < t.nblk * 64;
+                const void* tb = t.prob ? (ragged ? &tmC1 : &tmB1) : (ragged ? &tmC0 : &tmB0);
+                for (int kb = t.k0; kb < t.k1; ++kb) {
+                    if (!lm_wait(bars, smem_u32(&bars->empty[stage]), phase ^ 1u, p.w)) {
+                        aborted = true;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&bars->full[stage]);
+                    const uint32_t a = smem_u32(sA + stage * kStageA), b = smem_u32(sB + stage * kStageB);
+                    mbar_arrive_expect_tx(fb, kStageA + (ragged ? (uint32_t)t.nblk : 4u) * kMnBlock);
+                    if (t.prob == 0) {
+                        tma_load_2d(a, &tmA0, kb * kBK, m0, fb);
+                    } else {
+                        tma_load_2d(a, &tmA1, m0, kb * kBK, fb);
+                        tma_load_2d(a + kMnBlock, &tmA1, m0 + 64, kb * kBK, fb);
+                    }
+                    if (ragged) {
+                        for (int j = 0; j < t.nblk; ++j) tma_load_2d(b + j * kMnBlock, tb, h0 + j * 64, kb * kBK, fb);
+                    } else {
+                        tma_load_3d(b, tb, 0, kb * kBK, h0 / 64, fb);
+                    }
+                    ++issued;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            drain_copies(bars, issued, p.w);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int64_t tiles = 0, n = 0;
+            bool aborted = false;
+            while (!aborted) {
+                int64_t u;
+                if (!unit_get(bars, n, u, p.w)) break;
+                unit_done(bars, n++);
+                if (u < 0) break;
+                const CeTile t = ce_tile(p, u);
+                const int acc = (int)(tiles & 1);
+                const uint32_t accph = (uint32_t)((tiles >> 1) & 1);
+                ++tiles;
+                if (!lm_wait(bars, smem_u32(&bars->tempty[acc]), accph ^ 1u, p.w)) break;
+                tc_fence_after();
+                const uint32_t idesc = idesc_bf16_f32_major(kBM, (uint32_t)(64 * t.nblk), t.prob == 1, true);
+                const uint32_t d = tmem + (uint32_t)(acc * kBN);
+                for (int kb = t.k0; kb < t.k1; ++kb) {
+                    if (!lm_wait(bars, smem_u32(&bars->full[stage]), phase, p.w)) {
+                        aborted = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(sA + stage * kStageA), b0 = smem_u32(sB + stage * kStageB);
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk) {
+                        const uint64_t ad = t.prob == 0 ? smem_desc_sw128(a0 + kk * 32)
+                                                        : smem_desc_sw128_mn(a0 + kk * 2048, kMnBlock, 1024);
+                        umma_bf16(d, ad, smem_desc_sw128_mn(b0 + kk * 2048, kMnBlock, 1024), idesc,
+                                  kb != t.k0 || kk != 0);
+                    }
+                    umma_commit(smem_u32(&bars->empty[stage]));
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!aborted) umma_commit(smem_u32(&bars->tfull[acc]));
+            }
+            umma_commit(smem_u32(&bars->drain));
+            lm_drain_wait(smem_u32(&bars->drain), 0u, p.w);
+        }
+    } else {
+        const int quarter = warp & 3;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const float scale = *p.scale;
+        int64_t tiles = 0, n = 0;
+        for (;;) {
+            int64_t u = -1;
+            const bool got = unit_get(bars, n, u, p.w);
+            if (!__all_sync(0xFFFFFFFFu, got)) break;
+            __syncwarp();
+            if (lane == 0) unit_done(bars, n);
+            ++n;
+            if (u < 0) break;
+            const CeTile t = ce_tile(p, u);
+            const int acc = (int)(tiles & 1);
+            const uint32_t accph = (uint32_t)((tiles >> 1) & 1);
+            ++tiles;
+            const bool ok = lm_wait(bars, smem_u32(&bars->tfull[acc]), accph, p.w);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            tc_fence_after();
+            const int64_t row = (int64_t)t.mb * kBM + quarter * 32 + lane;
+            const bool valid = row < (t.prob == 0 ? p.T : (int64_t)p.cols);
+            // dHidden leaves as BF16 from the only slice of the last piece, else into the sums
+            const bool out = t.prob == 1 || (p.S == 1 && p.last);
+            for (int sub = 0; sub < 2 * t.nblk; ++sub) {
+                float v[32];
+                tmem_ld32(tmem + lane_base + (uint32_t)(acc * kBN + sub * 32), v);
+                if (!valid) continue;
+                if (t.k0 == t.k1) {  // a slice without K blocks (a short last piece): no MMA wrote the accumulator
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                }
+                const int col0 = t.nb * kBN + sub * 32;
+                if (t.prob == 0 && !(out && p.first)) {
+                    float4* s4 = reinterpret_cast<float4*>(p.sums + ((int64_t)t.slice * p.T + row) * p.Hs + col0);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        if (!p.first) {
+                            const float4 o = s4[q];
+                            v[4 * q] = __fadd_rn(o.x, v[4 * q]), v[4 * q + 1] = __fadd_rn(o.y, v[4 * q + 1]);
+                            v[4 * q + 2] = __fadd_rn(o.z, v[4 * q + 2]), v[4 * q + 3] = __fadd_rn(o.w, v[4 * q + 3]);
+                        }
+                        if (!out) s4[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                    }
+                }
+                if (out) {
+                    uint16_t* o = t.prob == 0 ? p.dhidden + row * p.ldh : p.dweight + row * p.ldw;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(v[i], scale);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) store_bf16x8(o, col0 + 8 * q, p.H, v + 8 * q);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// dHidden from the S slices' sums, added in order.
+__global__ void __launch_bounds__(256) ce_join_kernel(const float* sums, const float* scale, int S, int64_t T,
+                                                      int64_t Hs, int H, uint16_t* dhidden, int64_t ldh) {
+    const int groups = (H + 7) / 8;
+    const int64_t n = T * groups;
+    const float sc = *scale;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / groups;
+        const int col = (int)(i % groups) * 8;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < S; ++s) {
+            const float4* q = reinterpret_cast<const float4*>(sums + ((int64_t)s * T + row) * Hs + col);
+            const float4 a = q[0], b = q[1];
+            const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], sc);
+        store_bf16x8(dhidden + row * ldh, col, H, v);
+    }
+}
+
+// ----------------------------------------------------------------- host
+
+size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// How the backward cuts the vocabulary and dHidden's K range.
+struct CePlan {
+    int64_t P, pieces, S, Hs;
+    int MB, NB;
+};
+
+CePlan plan_of(const rlk_linear_ce_contract& c) {
+    CePlan q{};
+    q.MB = (int)ceil_div(c.T, kBM);
+    q.NB = (int)ceil_div(c.H, kBN);
+    q.Hs = ceil_div(c.H, 64) * 64;
+    const int64_t whole = ceil_div(c.V, kBN) * kBN;
+    int64_t P = c.piece > 0 ? ceil_div(c.piece, kBN) * kBN : kPieceBytes / (2 * c.T) / kBN * kBN;
+    const int64_t least = ceil_div(ceil_div(c.V, kMaxPieces), kBN) * kBN;
+    if (c.piece <= 0 && P < kMinPiece) P = kMinPiece;
+    if (P < least) P = least;
+    if (P > whole) P = whole;
+    q.pieces = ceil_div(c.V, P);
+    if (c.piece <= 0) P = ceil_div(ceil_div(c.V, q.pieces), kBN) * kBN;  // pieces of one size
+    q.pieces = ceil_div(c.V, P);
+    q.P = P;
+    // dHidden has MB NB tiles with a K range of P: where they are fewer than two a CTA (152 SMs)
+    // the range is cut so that they are, in slices of at least 8 K blocks, with sums of their own.
+    const int64_t tiles = (int64_t)q.MB * q.NB;
+    int64_t S = ceil_div(304, tiles);
+    if (S > P / (8 * kBK)) S = P / (8 * kBK);
+    if (S > kMaxSlices) S = kMaxSlices;
+    q.S = S < 1 ? 1 : S;
+    return q;
+}
+
+struct CeLayout {
+    size_t tickets, loss, yt, part, part_y, fwd_end;
+    size_t rows, target, scale, dx, sums, bwd_end;
+};
+
+CeLayout layout_of(const rlk_linear_ce_contract& c) {
+    CeLayout l{};
+    const size_t T = (size_t)c.T, chunks = (size_t)ceil_div(c.V, kBN);
+    l.tickets = kWorkspaceBytes;
+    size_t at = kWorkspaceBytes + up256(kCeTicketBytes);
+    l.loss = at;
+    l.yt = l.loss + up256(4 * T);
+    l.part = l.yt + up256(4 * T);
+    l.part_y = l.part + up256(8 * T * chunks);
+    l.fwd_end = l.part_y + (c.label_smoothing != 0.f ? up256(4 * T * chunks) : 0);
+    const CePlan q = plan_of(c);
+    l.rows = at;
+    l.target = l.rows + up256(16 * T);
+    l.scale = l.target + up256(4 * T);
+    l.dx = l.scale + 256;
+    l.sums = l.dx + up256(2 * T * (size_t)q.P);
+    l.bwd_end = l.sums + (q.pieces > 1 || q.S > 1 ? up256(4 * (size_t)q.S * T * (size_t)q.Hs) : 0);
+    return l;
+}
+
+rlk_status ce_cuda(const char* what) {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? RLK_OK : fail(RLK_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+rlk_status ce_sms(int* sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || *sms <= 0)
+        return fail(RLK_ERR_CUDA, "cannot query the device's SM count");
+    return RLK_OK;
+}
+
+template <int MODE, bool CAP, bool SMOOTH>
+rlk_status launch_logits(const CUtensorMap& h, const CUtensorMap& w, const CUtensorMap& d, const CeParams& p, int sms,
+                         cudaStream_t st) {
+    const size_t bytes = MODE == kCeGrad ? kCeSmemDx : kCeSmem;
+    if (cudaFuncSetAttribute(ce_logits_kernel<MODE, CAP, SMOOTH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)bytes) != cudaSuccess)
+        return ce_cuda("linear cross entropy: shared memory");
+    const int64_t units = (int64_t)p.nch * p.MB;
+    ce_logits_kernel<MODE, CAP, SMOOTH>
+        <<<(unsigned)(units < sms ? units : sms), kThreadsLm, bytes, st>>>(h, w, d, p);
+    return ce_cuda("linear cross entropy launch");
+}
+
+CeParams ce_params(const rlk_linear_ce_contract& c, const int64_t* targets, const uint8_t* mask, uint32_t* status) {
+    CeParams p{};
+    p.targets = targets;
+    p.mask = mask;
+    p.w.status = status;
+    p.w.wait_ns = c.wait_timeout_ns > 0 ? (uint64_t)c.wait_timeout_ns : kDefaultWaitNs;
+    p.T = c.T;
+    p.V = c.V;
+    p.ignore_index = c.ignore_index;
+    p.cap = c.softcap;
+    p.icap = c.softcap > 0.f ? 1.f / c.softcap : 0.f;
+    p.KB = (int32_t)ceil_div(c.H, kBK);
+    p.mask_mode = c.mask_mode;
+    p.MB = (int32_t)ceil_div(c.T, kBM);
+    const int64_t band = kBandBytes / ((int64_t)kBM * c.H * 2);
+    p.MBg = (int32_t)(band < 1 ? 1 : band < p.MB ? band : p.MB);
+    return p;
+}
+
+const char kMapFailed[] = "cuTensorMapEncodeTiled failed for an operand of the linear cross entropy";
+
+}  // namespace
+
+size_t linear_ce_workspace(const rlk_linear_ce_contract& c, bool grad) {
+    const CeLayout l = layout_of(c);
+    return grad ? (l.bwd_end > l.fwd_end ? l.bwd_end : l.fwd_end) : l.fwd_end;
+}
+
+rlk_status launch_linear_ce_fwd(const rlk_linear_ce_contract& c, const void* hidden, const void* weight,
+                                const int64_t* targets, const uint8_t* mask, float* loss, float* lse, void* workspace,
+                                cudaStream_t st) {
+    int sms = 0;
+    rlk_status s = ce_sms(&sms);
+    if (s != RLK_OK) return s;
+    const CeLayout l = layout_of(c);
+    char* ws = static_cast<char*>(workspace);
+    uint32_t* status = static_cast<uint32_t*>(workspace);
+    if (cudaMemsetAsync(ws, 0, kWorkspaceBytes + 256, st) != cudaSuccess) return ce_cuda("clearing the work space");
+    CeParams p = ce_params(c, targets, mask, status);
+    p.ticket = reinterpret_cast<unsigned long long*>(ws + l.tickets);
+    p.part = reinterpret_cast<float2*>(ws + l.part);
+    p.part_y = reinterpret_cast<float*>(ws + l.part_y);
+    p.yt = reinterpret_cast<float*>(ws + l.yt);
+    p.ch0 = 0;
+    p.nch = (int32_t)ceil_div(c.V, kBN);
+    CUtensorMap tmH, tmW;
+    if (!make_map(&tmH, hidden, c.H, c.T, c.hidden_stride, kBK, kBM) ||
+        !make_map(&tmW, weight, c.H, c.V, c.weight_stride, kBK, kBN))
+        return fail(RLK_ERR_CUDA, kMapFailed);
+    const bool cap = c.softcap > 0.f, smooth = c.label_smoothing != 0.f;
+    s = cap ? (smooth ? launch_logits<kCeForward, true, true>(tmH, tmW, tmH, p, sms, st)
+                      : launch_logits<kCeForward, true, false>(tmH, tmW, tmH, p, sms, st))
+            : (smooth ? launch_logits<kCeForward, false, true>(tmH, tmW, tmH, p, sms, st)
+                      : launch_logits<kCeForward, false, false>(tmH, tmW, tmH, p, sms, st));
+    if (s != RLK_OK) return s;
+    CeFold f{};
+    f.part = p.part;
+    f.part_y = smooth ? p.part_y : nullptr;
+    f.yt = p.yt;
+    f.targets = targets;
+    f.mask = mask;
+    f.loss = c.reduction == RLK_REDUCE_NONE ? loss : reinterpret_cast<float*>(ws + l.loss);
+    f.lse = lse;
+    f.status = status;
+    f.T = c.T;
+    f.V = c.V;
+    f.ignore_index = c.ignore_index;
+    f.chunks = p.nch;
+    f.mask_mode = c.mask_mode;
+    f.eps = c.label_smoothing;
+    f.z = c.z_loss;
+    ce_fold_kernel<<<(unsigned)ceil_div(c.T, 32), 32 * kFoldSlices, 0, st>>>(f);
+    if (c.reduction != RLK_REDUCE_NONE)
+        ce_reduce_kernel<<<1, 1024, 0, st>>>(f.loss, targets, mask, c.mask_mode, c.ignore_index, c.T,
+                                             c.reduction == RLK_REDUCE_MEAN, loss);
+    return ce_cuda("linear cross entropy: merge");
+}
+
+rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hidden, const void* weight,
+                                const int64_t* targets, const uint8_t* mask, const float* lse, const float* grad,
+                                void* dhidden, void* dweight, void* workspace, cudaStream_t st) {
+    int sms = 0;
+    rlk_status s = ce_sms(&sms);
+    if (s != RLK_OK) return s;
+    const CeLayout l = layout_of(c);
+    const CePlan q = plan_of(c);
+    char* ws = static_cast<char*>(workspace);
+    uint32_t* status = static_cast<uint32_t*>(workspace);
+    if (cudaMemsetAsync(ws, 0, kWorkspaceBytes + kCeTicketBytes, st) != cudaSuccess)
+        return ce_cuda("clearing the work space");
+    CeRows r{};
+    r.targets = targets;
+    r.mask = mask;
+    r.lse = lse;
+    r.grad = grad;
+    r.rows = reinterpret_cast<float4*>(ws + l.rows);
+    r.target = reinterpret_cast<int32_t*>(ws + l.target);
+    r.scale = reinterpret_cast<float*>(ws + l.scale);
+    r.status = status;
+    r.T = c.T;
+    r.V = c.V;
+    r.ignore_index = c.ignore_index;
+    r.mask_mode = c.mask_mode;
+    r.reduction = c.reduction;
+    r.eps = c.label_smoothing;
+    r.z = c.z_loss;
+    ce_rows_kernel<<<1, 1024, 0, st>>>(r);
+    if ((s = ce_cuda("linear cross entropy: rows")) != RLK_OK) return s;
+
+    const uint32_t smem = (uint32_t)kCeSmem;
+    if (cudaFuncSetAttribute(ce_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return ce_cuda("linear cross entropy: shared memory");
+    CeParams p = ce_params(c, targets, mask, status);
+    p.rows = r.rows;
+    p.target = r.target;
+    CeGrads g{};
+    g.dhidden = static_cast<uint16_t*>(dhidden);
+    g.sums = reinterpret_cast<float*>(ws + l.sums);
+    g.scale = r.scale;
+    g.w = p.w;
+    g.T = c.T;
+    g.ldh = c.dhidden_stride;
+    g.ldw = c.dweight_stride;
+    g.Hs = q.Hs;
+    g.H = (int32_t)c.H;
+    g.NB = q.NB;
+    g.NBg = q.NB < kBandH ? q.NB : kBandH;
+    g.MB0 = q.MB;
+    g.S = (int32_t)q.S;
+    g.KB1 = (int32_t)ceil_div(c.T, kBK);
+    uint16_t* dx = reinterpret_cast<uint16_t*>(ws + l.dx);
+    unsigned long long* tickets = reinterpret_cast<unsigned long long*>(ws + l.tickets);
+    CUtensorMap tmH, tmB1, tmC1;
+    const bool wide = c.H >= 64;
+    if (!make_map(&tmH, hidden, c.H, c.T, c.hidden_stride, kBK, kBM) ||
+        !make_map(&tmC1, hidden, c.H, c.T, c.hidden_stride, 64, kBK) ||
+        (wide && !make_map_mn3(&tmB1, hidden, c.H / 64 * 64, c.T, c.hidden_stride, kBK, 4)))
+        return fail(RLK_ERR_CUDA, kMapFailed);
+    if (!wide) tmB1 = tmC1;
+    for (int64_t i = 0; i < q.pieces; ++i) {
+        const int64_t c0 = i * q.P, cols = c.V - c0 < q.P ? c.V - c0 : q.P;
+        const uint16_t* w0 = static_cast<const uint16_t*>(weight) + c0 * c.weight_stride;
+        CUtensorMap tmW, tmD, tmA0, tmA1, tmB0, tmC0;
+        if (!make_map(&tmW, weight, c.H, c.V, c.weight_stride, kBK, kBN) ||
+            !make_map(&tmD, dx, cols, c.T, q.P, 64, 32) || !make_map(&tmA0, dx, cols, c.T, q.P, kBK, kBM) ||
+            !make_map(&tmA1, dx, cols, c.T, q.P, 64, kBK) ||
+            !make_map(&tmC0, w0, c.H, cols, c.weight_stride, 64, kBK) ||
+            (wide && !make_map_mn3(&tmB0, w0, c.H / 64 * 64, cols, c.weight_stride, kBK, 4)))
+            return fail(RLK_ERR_CUDA, kMapFailed);
+        if (!wide) tmB0 = tmC0;
+        p.ticket = tickets + 2 * i;
+        p.ch0 = (int32_t)(c0 / kBN);
+        p.nch = (int32_t)ceil_div(cols, kBN);
+        s = c.softcap > 0.f ? launch_logits<kCeGrad, true, false>(tmH, tmW, tmD, p, sms, st)
+                            : launch_logits<kCeGrad, false, false>(tmH, tmW, tmD, p, sms, st);
+        if (s != RLK_OK) return s;
+        g.ticket = tickets + 2 * i + 1;
+        g.dweight = dweight ? static_cast<uint16_t*>(dweight) + c0 * c.dweight_stride : nullptr;
+        g.cols = (int32_t)cols;
+        g.KB0 = (int32_t)ceil_div(cols, kBK);
+        g.MB1 = (int32_t)ceil_div(cols, kBM);
+        g.n0 = dhidden ? q.S * q.MB * (int64_t)q.NB : 0;
+        g.n1 = dweight ? (int64_t)g.MB1 * q.NB : 0;
+        g.first = i == 0;
+        g.last = i == q.pieces - 1;
+        const int64_t tiles = g.n0 + g.n1;
+        ce_grads_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kThreadsLm, smem, st>>>(tmA0, tmB0, tmC0, tmA1, tmB1,
+                                                                                         tmC1, g);
+        if ((s = ce_cuda("linear cross entropy: gradients")) != RLK_OK) return s;
+    }
+    if (dhidden && q.S > 1) {
+        const int64_t blocks = ceil_div(c.T * ceil_div(c.H, 8), 256);
+        ce_join_kernel<<<(unsigned)(blocks < 8 * sms ? blocks : 8 * sms), 256, 0, st>>>(
+            g.sums, g.scale, g.S, c.T, q.Hs, g.H, g.dhidden, g.ldh);
+        return ce_cuda("linear cross entropy: join");
+    }
+    return RLK_OK;
+}
+
+}  // namespace rlk

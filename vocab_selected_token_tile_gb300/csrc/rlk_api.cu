@@ -922,6 +922,144 @@ RLK_EXPORT rlk_status rlk_fp8_matmul(int64_t M, int64_t N, int64_t K, const void
                              reinterpret_cast<cudaStream_t>(stream));
 }
 
+namespace rlk {
+namespace {
+rlk_status check_ce(const rlk_linear_ce_contract* c) {
+    if (!c) return fail(RLK_ERR_INVALID_ARG, "contract is NULL");
+    if (c->T < 0) return fail(RLK_ERR_INVALID_ARG, "T must be >= 0");
+    if (c->V < 1 || c->H < 1) return fail(RLK_ERR_INVALID_ARG, "V and H must be >= 1");
+    if (c->T > ((int64_t)1 << 31) - 512 || c->V > ((int64_t)1 << 31) - 512)
+        return fail(RLK_ERR_UNSUPPORTED, "T or V above 2^31 - 512");
+    if (c->H > ((int64_t)1 << 20)) return fail(RLK_ERR_UNSUPPORTED, "hidden size H above 2^20");
+    const struct {
+        int64_t stride;
+        const char* name;
+    } strides[] = {{c->hidden_stride, "hidden_stride"},
+                   {c->weight_stride, "weight_stride"},
+                   {c->dhidden_stride, "dhidden_stride"},
+                   {c->dweight_stride, "dweight_stride"}};
+    for (const auto& s : strides) {
+        const int64_t v = s.stride ? s.stride : c->H;
+        if (v < c->H) return fail(RLK_ERR_INVALID_ARG, std::string(s.name) + " must be >= H");
+        if (v % 8 != 0)
+            return fail(RLK_ERR_MISALIGNED, std::string(s.name) + " must be a multiple of 8 elements (16-byte rows)");
+        if (v > ((int64_t)1 << 36)) return fail(RLK_ERR_UNSUPPORTED, std::string(s.name) + " above 2^36");
+    }
+    if (c->mask_mode != RLK_MASK_EXPLICIT && c->mask_mode != RLK_MASK_IGNORE_INDEX)
+        return fail(RLK_ERR_INVALID_ARG, "mask_mode must be RLK_MASK_EXPLICIT or RLK_MASK_IGNORE_INDEX");
+    if (c->reduction != RLK_REDUCE_NONE && c->reduction != RLK_REDUCE_SUM && c->reduction != RLK_REDUCE_MEAN)
+        return fail(RLK_ERR_INVALID_ARG, "reduction must be RLK_REDUCE_NONE, _SUM or _MEAN");
+    if (c->validate != 0 && c->validate != 1) return fail(RLK_ERR_INVALID_ARG, "validate must be 0 or 1");
+    if (c->wait_timeout_ns < 0) return fail(RLK_ERR_INVALID_ARG, "wait_timeout_ns must be >= 0");
+    if (c->piece < 0) return fail(RLK_ERR_INVALID_ARG, "piece must be >= 0");
+    if (!(c->label_smoothing >= 0.f && c->label_smoothing <= 1.f))
+        return fail(RLK_ERR_INVALID_ARG, "label_smoothing must be in [0, 1]");
+    if (!(c->z_loss >= 0.f) || !isfinite(c->z_loss))
+        return fail(RLK_ERR_INVALID_ARG, "z_loss must be finite and >= 0");
+    if (!(c->softcap >= 0.f) || !isfinite(c->softcap) || (c->softcap > 0.f && c->softcap < 1e-6f))
+        return fail(RLK_ERR_INVALID_ARG, "softcap must be 0 or a finite value of at least 1e-6");
+    return RLK_OK;
+}
+
+rlk_linear_ce_contract with_strides(const rlk_linear_ce_contract& c) {
+    rlk_linear_ce_contract f = c;
+    if (!f.hidden_stride) f.hidden_stride = f.H;
+    if (!f.weight_stride) f.weight_stride = f.H;
+    if (!f.dhidden_stride) f.dhidden_stride = f.H;
+    if (!f.dweight_stride) f.dweight_stride = f.H;
+    return f;
+}
+
+rlk_status check_ce_inputs(const rlk_linear_ce_contract& c, const void* hidden, const void* weight,
+                           const int64_t* targets, const uint8_t* mask, const void* workspace) {
+    if (!hidden || !weight) return fail(RLK_ERR_INVALID_ARG, "hidden and weight are required");
+    if (!aligned16(hidden) || !aligned16(weight))
+        return fail(RLK_ERR_MISALIGNED, "hidden and weight must be 16-byte aligned");
+    if (!targets) return fail(RLK_ERR_INVALID_ARG, "targets is NULL");
+    if (c.mask_mode == RLK_MASK_EXPLICIT && !mask)
+        return fail(RLK_ERR_INVALID_ARG, "explicit mask mode needs active_mask");
+    if (c.mask_mode == RLK_MASK_IGNORE_INDEX && mask)
+        return fail(RLK_ERR_INVALID_ARG, "ignore_index mode takes no active_mask (pass NULL)");
+    if (!workspace) return fail(RLK_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned16(workspace)) return fail(RLK_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    return RLK_OK;
+}
+}  // namespace
+}  // namespace rlk
+
+RLK_EXPORT rlk_status rlk_linear_ce_check(const rlk_linear_ce_contract* contract) { return check_ce(contract); }
+
+RLK_EXPORT size_t rlk_linear_ce_workspace_size(const rlk_linear_ce_contract* contract, int32_t with_grad) {
+    if (check_ce(contract) != RLK_OK) return 0;
+    return contract->T == 0 ? kWorkspaceBytes : linear_ce_workspace(with_strides(*contract), with_grad != 0);
+}
+
+RLK_EXPORT rlk_status rlk_linear_ce_fwd(const rlk_linear_ce_contract* contract, const void* hidden_bf16,
+                                        const void* weight_bf16, const int64_t* targets, const uint8_t* active_mask,
+                                        float* loss, float* lse, void* workspace, rlk_stream_t stream) {
+    rlk_status s = check_ce(contract);
+    if (s != RLK_OK) return s;
+    const rlk_linear_ce_contract c = with_strides(*contract);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (c.T == 0) {
+        if (c.reduction == RLK_REDUCE_NONE) return RLK_OK;
+        if (!loss) return fail(RLK_ERR_INVALID_ARG, "loss output is required");
+        if ((s = select_device(loss)) != RLK_OK) return s;
+        return cudaMemsetAsync(loss, 0, sizeof(float), st) == cudaSuccess
+                   ? RLK_OK
+                   : fail(RLK_ERR_CUDA, "clearing the loss of no rows");
+    }
+    if ((s = check_ce_inputs(c, hidden_bf16, weight_bf16, targets, active_mask, workspace)) != RLK_OK) return s;
+    if (!loss || !lse) return fail(RLK_ERR_INVALID_ARG, "loss and lse outputs are required");
+    if ((s = select_device(hidden_bf16)) != RLK_OK) return s;
+    if ((s = check_device_ptrs({{weight_bf16, "weight"}, {targets, "targets"}, {active_mask, "active_mask"},
+                                {loss, "loss"}, {lse, "lse"}, {workspace, "workspace"}})) != RLK_OK)
+        return s;
+    if ((s = launch_linear_ce_fwd(c, hidden_bf16, weight_bf16, targets, active_mask, loss, lse, workspace, st)) !=
+        RLK_OK)
+        return s;
+    return c.validate ? read_status(workspace, st) : RLK_OK;
+}
+
+RLK_EXPORT rlk_status rlk_linear_ce_bwd(const rlk_linear_ce_contract* contract, const void* hidden_bf16,
+                                        const void* weight_bf16, const int64_t* targets, const uint8_t* active_mask,
+                                        const float* lse, const float* grad_loss, void* dhidden_bf16,
+                                        void* dweight_bf16, void* workspace, rlk_stream_t stream) {
+    rlk_status s = check_ce(contract);
+    if (s != RLK_OK) return s;
+    const rlk_linear_ce_contract c = with_strides(*contract);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!dhidden_bf16 && !dweight_bf16) return fail(RLK_ERR_INVALID_ARG, "dhidden or dweight is required");
+    if (!aligned16(dhidden_bf16) || !aligned16(dweight_bf16))
+        return fail(RLK_ERR_MISALIGNED, "dhidden and dweight must be 16-byte aligned");
+    if (c.T == 0) {  // no rows: a zero dweight
+        if (!dweight_bf16) return RLK_OK;
+        if ((s = select_device(dweight_bf16)) != RLK_OK) return s;
+        return cudaMemset2DAsync(dweight_bf16, (size_t)c.dweight_stride * 2, 0, (size_t)c.H * 2, (size_t)c.V, st) ==
+                       cudaSuccess
+                   ? RLK_OK
+                   : fail(RLK_ERR_CUDA, "clearing the gradient of no rows");
+    }
+    if ((s = check_ce_inputs(c, hidden_bf16, weight_bf16, targets, active_mask, workspace)) != RLK_OK) return s;
+    if (!lse || !grad_loss) return fail(RLK_ERR_INVALID_ARG, "lse and grad_loss are required");
+    const Span in_h{hidden_bf16, extent(c.T, c.hidden_stride, c.H, 2), "hidden"};
+    const Span in_w{weight_bf16, extent(c.V, c.weight_stride, c.H, 2), "weight"};
+    const Span out_w{dweight_bf16, extent(c.V, c.dweight_stride, c.H, 2), "dweight"};
+    if ((s = check_disjoint({dhidden_bf16, extent(c.T, c.dhidden_stride, c.H, 2), "dhidden"},
+                            {in_h, in_w, out_w})) != RLK_OK)
+        return s;
+    if ((s = check_disjoint(out_w, {in_h, in_w})) != RLK_OK) return s;
+    if ((s = select_device(hidden_bf16)) != RLK_OK) return s;
+    if ((s = check_device_ptrs({{weight_bf16, "weight"}, {targets, "targets"}, {active_mask, "active_mask"},
+                                {lse, "lse"}, {grad_loss, "grad_loss"}, {dhidden_bf16, "dhidden"},
+                                {dweight_bf16, "dweight"}, {workspace, "workspace"}})) != RLK_OK)
+        return s;
+    if ((s = launch_linear_ce_bwd(c, hidden_bf16, weight_bf16, targets, active_mask, lse, grad_loss, dhidden_bf16,
+                                  dweight_bf16, workspace, st)) != RLK_OK)
+        return s;
+    return c.validate ? read_status(workspace, st) : RLK_OK;
+}
+
 RLK_EXPORT rlk_status rlk_logp_workspace_status(const void* workspace, rlk_stream_t stream) {
     if (!workspace) return fail(RLK_ERR_INVALID_ARG, "workspace is NULL");
     rlk_status s = select_device(workspace);

@@ -126,6 +126,16 @@ rlk_status launch_grpo_loss(int64_t T, const float* logp, const float* adv, cons
 rlk_status launch_grpo_count(int64_t T, const int64_t* targets, const uint8_t* mask, int64_t ignore_index,
                              uint8_t* mask_out, unsigned long long* n_active, int sm_count, cudaStream_t stream);
 
+// Cross entropy of hidden @ weight^T (linear_ce.cu), for a checked contract
+// whose strides are filled in.
+size_t linear_ce_workspace(const rlk_linear_ce_contract& c, bool grad);
+rlk_status launch_linear_ce_fwd(const rlk_linear_ce_contract& c, const void* hidden, const void* weight,
+                                const int64_t* targets, const uint8_t* mask, float* loss, float* lse, void* workspace,
+                                cudaStream_t stream);
+rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hidden, const void* weight,
+                                const int64_t* targets, const uint8_t* mask, const float* lse, const float* grad,
+                                void* dhidden, void* dweight, void* workspace, cudaStream_t stream);
+
 // Quantisation to E4M3 with a scale per group of 128 (fp8_quant.cu); q and/or
 // qt (the transpose), each with its scales.
 rlk_status launch_fp8_quantize(int64_t rows, int64_t cols, const void* x, int32_t x_f32, int64_t ldx,
