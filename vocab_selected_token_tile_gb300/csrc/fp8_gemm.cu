@@ -62,6 +62,16 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
+// The same by a pair of CTAs (M = 256: 128 rows of each).
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
     return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
@@ -84,6 +94,26 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
                    "+r"(r[15])::"memory");
 }
 
+// The same for 32 columns.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
 // A 4-byte asynchronous copy, zero where `ok` is false (nothing is read then).
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
@@ -100,12 +130,12 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
-template <int STAGES>
+template <int STAGES, int ACC>
 struct Bars8 {
     uint64_t full[STAGES];
     uint64_t empty[STAGES];
-    uint64_t tfull[2];
-    uint64_t tempty[2];
+    uint64_t tfull[ACC];
+    uint64_t tempty[ACC];
     uint64_t sfull[kScaleStages];
     uint64_t sempty[kScaleStages];
     uint64_t drain;
@@ -118,22 +148,21 @@ struct Wait8 {
     uint64_t wait_ns;
 };
 
-__device__ __forceinline__ bool wait8_slow(volatile int* abort_flag, uint32_t bar, uint32_t parity, const Wait8& w) {
-    if (*abort_flag) return false;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
+// Bounded wait for a phase of a barrier (the clock is read on every 1024th poll).
+__device__ __forceinline__ bool wait8(int* abort_flag, uint32_t bar, uint32_t parity, const Wait8& w) {
+    uint64_t t0 = 0;
+    for (uint32_t polls = 0;; ++polls) {
         if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > w.wait_ns) {
-            *abort_flag = 1;
+        if ((polls & 1023u) != 1023u) continue;
+        if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > w.wait_ns) {
+            *reinterpret_cast<volatile int*>(abort_flag) = 1;
             atomicOr(w.status, kStatusTimeout);
             return false;
         }
     }
-}
-
-__device__ __forceinline__ bool wait8(int* abort_flag, uint32_t bar, uint32_t parity, const Wait8& w) {
-    return mbar_try_wait(bar, parity) || wait8_slow(abort_flag, bar, parity, w);
 }
 
 __device__ __forceinline__ void drain8(uint32_t bar, uint32_t parity, const Wait8& w) {
@@ -146,15 +175,15 @@ __device__ __forceinline__ void drain8(uint32_t bar, uint32_t parity, const Wait
     }
 }
 
-template <int STAGES>
-__device__ void init_bars8(Bars8<STAGES>* b, int epilogue_warps) {
+template <int STAGES, int ACC>
+__device__ void init_bars8(Bars8<STAGES, ACC>* b, int epilogue_warps, int tempty_arrivals) {
     for (int s = 0; s < STAGES; ++s) {
         mbar_init(smem_u32(&b->full[s]), 1);
         mbar_init(smem_u32(&b->empty[s]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < ACC; ++i) {
         mbar_init(smem_u32(&b->tfull[i]), 1);
-        mbar_init(smem_u32(&b->tempty[i]), epilogue_warps);
+        mbar_init(smem_u32(&b->tempty[i]), tempty_arrivals);
     }
     for (int s = 0; s < kScaleStages; ++s) {
         mbar_init(smem_u32(&b->sfull[s]), 32);
@@ -189,50 +218,76 @@ struct Gemm8Params {
     Wait8 w;
 };
 
-// C elements of one row, columns [col, col + 8): 16-byte stores where the row
-// allows, single elements at the edge.
-__device__ __forceinline__ void store8(const Gemm8Params& p, int64_t row, int col, const float (&v)[8]) {
+// A warp's 32 rows x 64 bytes of C (16 FP32 or 32 BF16 columns; a lane holds
+// its row's) through shared memory, so that a row's 64 bytes leave in one
+// piece: 16 bytes a lane straight from the registers, 32 rows an instruction,
+// took 10,700 clocks a 128 x 256 tile, a third of the product's time at K =
+// 4096.  16-byte piece j of row r is kept at j ^ (r / 2 mod 4), which spreads
+// both directions over the banks.
+template <bool F32>
+__device__ __forceinline__ void store_chunk(const Gemm8Params& p, unsigned char* out, int lane, int64_t row0, int col0,
+                                            const float2* v) {
+    constexpr int kPer = F32 ? 4 : 8;  // elements of 16 bytes
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint4 w;
+        if (F32)
+            w = make_uint4(__float_as_uint(v[2 * j].x), __float_as_uint(v[2 * j].y), __float_as_uint(v[2 * j + 1].x),
+                           __float_as_uint(v[2 * j + 1].y));
+        else
+            w = make_uint4(pack_bf16x2_rn(v[4 * j].x, v[4 * j].y), pack_bf16x2_rn(v[4 * j + 1].x, v[4 * j + 1].y),
+                           pack_bf16x2_rn(v[4 * j + 2].x, v[4 * j + 2].y),
+                           pack_bf16x2_rn(v[4 * j + 3].x, v[4 * j + 3].y));
+        *reinterpret_cast<uint4*>(out + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) = w;
+    }
+    __syncwarp();
+    const int j = lane & 3, col = col0 + j * kPer;
     if (col >= p.N) return;
-    if (p.c_f32) {
-        float* c = static_cast<float*>(p.c) + row * p.ldc + col;
-        if (p.vec && col + 8 <= p.N) {
-            float4 lo = make_float4(v[0], v[1], v[2], v[3]), hi = make_float4(v[4], v[5], v[6], v[7]);
-            float4* c4 = reinterpret_cast<float4*>(c);
-            if (p.accumulate) {
-                const float4 x = c4[0], y = c4[1];
-                lo.x += x.x, lo.y += x.y, lo.z += x.z, lo.w += x.w;
-                hi.x += y.x, hi.y += y.y, hi.z += y.z, hi.w += y.w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        if (row0 + r >= p.M) break;
+        uint4 w = *reinterpret_cast<const uint4*>(out + r * 64 + ((j ^ ((r >> 1) & 3)) * 16));
+        if (F32) {
+            float* c = static_cast<float*>(p.c) + (row0 + r) * p.ldc + col;
+            float x[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
+            if (p.vec && col + 4 <= p.N) {
+                float4* c4 = reinterpret_cast<float4*>(c);
+                if (p.accumulate) {
+                    const float4 o = *c4;
+                    x[0] += o.x, x[1] += o.y, x[2] += o.z, x[3] += o.w;
+                }
+                *c4 = make_float4(x[0], x[1], x[2], x[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < p.N) c[e] = p.accumulate ? c[e] + x[e] : x[e];
             }
-            c4[0] = lo;
-            c4[1] = hi;
-            return;
+        } else {
+            uint16_t* c = static_cast<uint16_t*>(p.c) + (row0 + r) * p.ldc + col;
+            if (p.vec && col + 8 <= p.N) {
+                *reinterpret_cast<uint4*>(c) = w;
+            } else {
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (col + e < p.N) c[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+            }
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (col + j < p.N) c[j] = p.accumulate ? c[j] + v[j] : v[j];
-        return;
     }
-    uint16_t* c = static_cast<uint16_t*>(p.c) + row * p.ldc + col;
-    const uint32_t w[4] = {pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
-                           pack_bf16x2_rn(v[6], v[7])};
-    if (p.vec && col + 8 <= p.N) {
-        *reinterpret_cast<uint4*>(c) = make_uint4(w[0], w[1], w[2], w[3]);
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (col + j < p.N) c[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
 }
 
-// ----------------------------------------------------------------- 128 x 256 tiles
+// ----------------------------------------------------------------- 256 x 256 tiles of a CTA pair
 
-constexpr int kGM = 128, kGN = 256;
-constexpr int kGStages = 4;
-constexpr uint32_t kGA = kGM * kGK, kGB = kGN * kGK;
+constexpr int kGM = 128, kGN = 256;  // a CTA's rows of a tile, and the tile's columns
+constexpr int kGStages = 6;
+constexpr uint32_t kGA = kGM * kGK, kGB = kGN / 2 * kGK;  // a CTA loads its rows of A and half of B's
 constexpr int kGThreads = 384;
-constexpr int kGScaleFloats = kGM + kGN;
-constexpr size_t kGSmem = 1024 + (size_t)kGStages * (kGA + kGB) + kScaleStages * kGScaleFloats * 4 + 1024;
-static_assert(sizeof(Bars8<kGStages>) <= 1024, "barriers fit their kilobyte");
+constexpr uint32_t kGOut = 32 * 64;  // an epilogue warp's output stage: 32 rows x 64 bytes
+constexpr size_t kGSmem =
+    1024 + (size_t)kGStages * (kGA + kGB) + kScaleStages * kGN * 4 + 8 * kGOut + 1024;
+static_assert(sizeof(Bars8<kGStages, 2>) <= 1024, "barriers fit their kilobyte");
 
 // Tile t of the persistent order: bands of `band` M tiles, and within a band
 // all M tiles of one N tile before the next, so the tiles in flight share a
@@ -247,103 +302,108 @@ __device__ __forceinline__ void tile_of(const Gemm8Params& p, int t, int& mb, in
 }
 
 template <bool BROWS>
-__global__ void __launch_bounds__(kGThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ Gemm8Params p) {
     extern __shared__ unsigned char smem_raw[];
+    // The same offset in both CTAs (their dynamic shared memory starts alike): descriptors name one offset.
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* sA = smem;
     unsigned char* sB = smem + kGStages * kGA;
-    float* scales = reinterpret_cast<float*>(sB + kGStages * kGB);
-    auto* bars = reinterpret_cast<Bars8<kGStages>*>(scales + kScaleStages * kGScaleFloats);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tiles = p.MB * p.NB;
+    unsigned char* sOut = sB + kGStages * kGB;
+    float* scales = reinterpret_cast<float*>(sOut + 8 * kGOut);
+    auto* bars = reinterpret_cast<Bars8<kGStages, 2>*>(scales + kScaleStages * kGN);
+    const int warp = warp_index(), lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
+    const int tiles = p.MB * p.NB, first = (int)blockIdx.x / 2, step = (int)gridDim.x / 2;
 
-    if (threadIdx.x == 0) init_bars8(bars, 8);
+    if (threadIdx.x == 0) init_bars8(bars, 8, 16);
     if (warp == 1) {
-        tmem_alloc(smem_u32(&bars->tmem_addr), 512);
-        tmem_relinquish();
+        tmem_alloc_pair(smem_u32(&bars->tmem_addr), 512);
+        tmem_relinquish_pair();
     }
     tc_fence_before();
-    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers are initialised and their tensor memory allocated
     tc_fence_after();
     const uint32_t tmem = bars->tmem_addr;
     int* ab = &bars->abort_flag;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 0 && lane == 0) {
-            // ------------------------------------------------ TMA producer
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0) {
+            // ------------------------------------------------ TMA producer: counted on the even CTA's barriers
+            const bool one = elect_one();
+            const uint32_t full0 = mapa_shared(smem_u32(&bars->full[0]), 0);
             Ring r;
-            int64_t issued = 0;
+            int issued = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            for (int t = first; ok && t < tiles; t += step) {
                 int mb, nb;
                 tile_of(p, t, mb, nb);
+                const int a_row = (2 * mb + rank) * kGM, b_row = nb * kGN + rank * (kGN / 2);
                 for (int kb = 0; kb < p.KB; ++kb) {
                     if (!(ok = wait8(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
-                    const uint32_t fb = smem_u32(&bars->full[r.slot]);
-                    mbar_arrive_expect_tx(fb, kGA + kGB);
-                    tma_load_2d(smem_u32(sA + r.slot * kGA), &tmA, kb * kGK, mb * kGM, fb);
-                    tma_load_2d(smem_u32(sB + r.slot * kGB), &tmB, kb * kGK, nb * kGN, fb);
-                    ++issued;
+                    if (one) {
+                        const uint32_t fb = full0 + r.slot * 8;
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars->full[r.slot]), 2 * (kGA + kGB));
+                        tma_load_2d_pair(smem_u32(sA + r.slot * kGA), &tmA, kb * kGK, a_row, fb);
+                        tma_load_2d_pair(smem_u32(sB + r.slot * kGB), &tmB, kb * kGK, b_row, fb);
+                    }
+                    issued = min(issued + 1, kGStages);
                     r.next(kGStages);
                 }
             }
-            // every copy lands before the CTA may exit
-            for (int64_t j = issued > kGStages ? issued - kGStages : 0; j < issued; ++j)
-                drain8(smem_u32(&bars->full[j % kGStages]), (uint32_t)((j / kGStages) & 1), p.w);
-        } else if (warp == 1 && lane == 0) {
-            // ------------------------------------------------ MMA issuer
+            // every copy lands before the CTA may exit: the even CTA's barriers count both CTAs' copies, and the
+            // odd one leaves only after the even one
+            for (int j = 0; j < issued && rank == 0; ++j) {
+                r.slot = r.slot == 0 ? kGStages - 1 : r.slot - 1;
+                if (r.slot == kGStages - 1) r.phase ^= 1u;
+                drain8(smem_u32(&bars->full[r.slot]), r.phase, p.w);
+            }
+        } else if (warp == 1 && rank == 0) {
+            // ------------------------------------------------ MMA issuer of the pair
+            const bool one = elect_one();
+            const uint64_t da = smem_desc_sw128(smem_u32(sA)), db = smem_desc_sw128(smem_u32(sB));
+            const uint32_t idesc = idesc_e4m3_f32(2 * kGM, kGN);
             Ring r, acc;
             bool ok = true;
-            const uint32_t idesc = idesc_e4m3_f32(kGM, kGN);
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            for (int t = first; ok && t < tiles; t += step) {
                 for (int kb = 0; kb < p.KB; ++kb) {
                     if (!(ok = wait8(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
                     if (!(ok = wait8(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(sA + r.slot * kGA), b0 = smem_u32(sB + r.slot * kGB);
-                    const uint32_t d = tmem + (uint32_t)(acc.slot * kGN);
+                    if (one) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_e4m3(d, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32), idesc, kk != 0);
-                    umma_commit(smem_u32(&bars->empty[r.slot]));
-                    umma_commit(smem_u32(&bars->tfull[acc.slot]));
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_e4m3_pair(tmem + (uint32_t)(acc.slot * kGN), da + ((r.slot * kGA + kk * 32) >> 4),
+                                           db + ((r.slot * kGB + kk * 32) >> 4), idesc, kk != 0);
+                        umma_commit_pair(smem_u32(&bars->tfull[acc.slot]));
+                        umma_commit_pair(smem_u32(&bars->empty[r.slot]));
+                    }
+                    __syncwarp();
                     r.next(kGStages);
                     acc.next(2);
                 }
             }
-            umma_commit(smem_u32(&bars->drain));
+            if (one) umma_commit_pair(smem_u32(&bars->drain));
             drain8(smem_u32(&bars->drain), 0u, p.w);
-        } else if (warp == 2) {
-            // ------------------------------------------------ scales
+        } else if (warp == 2 && BROWS) {
+            // ------------------------------------------------ B's row scales, for all epilogue warps
             Ring r;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            for (int t = first; ok && t < tiles; t += step) {
                 int mb, nb;
                 tile_of(p, t, mb, nb);
                 for (int kb = 0; kb < p.KB; ++kb) {
                     ok = __all_sync(0xFFFFFFFFu, wait8(ab, smem_u32(&bars->sempty[r.slot]), r.phase ^ 1u, p.w));
                     if (!ok) break;
-                    const uint32_t dst = smem_u32(scales + r.slot * kGScaleFloats);
-                    const float* a = p.sa + (int64_t)kb * p.M;
+                    const uint32_t dst = smem_u32(scales + r.slot * kGN);
                     const float* b = p.sb + (int64_t)kb * p.nsb;
 #pragma unroll
-                    for (int i = lane; i < kGM; i += 32) {
-                        const int row = mb * kGM + i;
-                        cp_async4(dst + i * 4, a + (row < p.M ? row : 0), row < p.M);
-                    }
-                    if (BROWS) {
-#pragma unroll
-                        for (int i = lane; i < kGN; i += 32) {
-                            const int row = nb * kGN + i;
-                            cp_async4(dst + (kGM + i) * 4, b + (row < p.N ? row : 0), row < p.N);
-                        }
-                    } else if (lane < 2) {
-                        const int blk = nb * (kGN / 128) + lane;
-                        cp_async4(dst + (kGM + lane) * 4, b + (blk < p.nsb ? blk : 0), blk < p.nsb);
+                    for (int i = lane; i < kGN; i += 32) {
+                        const int row = nb * kGN + i;
+                        cp_async4(dst + i * 4, b + (row < p.N ? row : 0), row < p.N);
                     }
                     cp_async_arrive(smem_u32(&bars->sfull[r.slot]));
                     r.next(kScaleStages);
@@ -354,72 +414,105 @@ __global__ void __launch_bounds__(kGThreads, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------ epilogue: scale and sum in registers
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int quarter = warp & 3, part = (warp - 4) >> 2;  // 32 rows, and 128 of the tile's columns
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        unsigned char* out = sOut + (warp - 4) * kGOut;
+        const uint32_t done = mapa_shared(smem_u32(&bars->tempty[0]), 0);
         Ring acc, sc;
-        bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            int mb, nb;
+        bool ok = first < tiles, ready = false;
+        // This row's scale (and, for block scales, the block's) of two K groups, and of the two after them under way;
+        // the first ones of a tile are loaded before the previous tile's result is stored.  A register that a load
+        // still owes is touched, and so waited for, two groups later only.
+        int mb = 0, nb = 0;
+        const float *pa = nullptr, *pb = nullptr;
+        float sa[4], sb[4];
+        auto load_scales = [&](int i, int kb) {
+            const bool in = kb < p.KB;
+            sa[i] = in ? __ldg(pa) : 0.f;
+            sb[i] = !BROWS && in ? __ldg(pb) : 0.f;
+            pa += p.M;
+            pb += p.nsb;
+        };
+        auto first_scales = [&](int t) {
             tile_of(p, t, mb, nb);
+            pa = p.sa + min((2 * mb + rank) * kGM + quarter * 32 + lane, p.M - 1);
+            pb = p.sb + min(nb * 2 + part, p.nsb - 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) load_scales(2 + i, i);
+        };
+        if (ok) first_scales(first);
+        for (int t = first; ok && t < tiles; t += step) {
             float2 sum[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
-            for (int kb = 0; kb < p.KB; ++kb) {
-                ok = wait8(ab, smem_u32(&bars->sfull[sc.slot]), sc.phase, p.w);
-                const float* s = scales + sc.slot * kGScaleFloats;
-                const float sa = s[quarter * 32 + lane];
-                const float sab = BROWS ? 0.f : __fmul_rn(sa, s[kGM + half]);
-                ok = __all_sync(0xFFFFFFFFu, ok && wait8(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w));
-                if (!ok) break;
+            // One K group: false when a wait expired.
+            auto group = [&](float a, float ab2) {
+                bool sready = true;
+                if (BROWS) sready = mbar_try_wait(smem_u32(&bars->sfull[sc.slot]), sc.phase);
+                if (!ready) ok = wait8(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w);
+                if (!sready) ok = ok && wait8(ab, smem_u32(&bars->sfull[sc.slot]), sc.phase, p.w);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) return;
                 tc_fence_after();
-                const uint32_t t0 = tmem + lane_base + (uint32_t)(acc.slot * kGN + half * 128);
-                uint32_t v[2][16];
-                tmem_ld16_issue(t0, v[0]);
+                // 32 columns at a time, the next 32 under way while these are summed
+                const uint32_t t0 = tmem + lane_base + (uint32_t)(acc.slot * kGN + part * 128);
+                uint32_t v[2][32];
+                tmem_ld32_issue(t0, v[0]);
+                const float* s = scales + sc.slot * kGN + part * 128;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tmem_wait16(v[c & 1]);
-                    if (c < 7) {
-                        tmem_ld16_issue(t0 + (c + 1) * 16, v[(c + 1) & 1]);
+                for (int c = 0; c < 4; ++c) {
+                    tmem_wait32(v[c & 1]);
+                    if (c < 3) {
+                        tmem_ld32_issue(t0 + (c + 1) * 32, v[(c + 1) & 1]);
                     } else {
+                        // the accumulator is free again; ask for the next one before this one's last sums
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc.slot]));
+                        if (lane == 0) mbar_arrive_remote(done + acc.slot * 8);
+                        acc.next(2);
+                        ready = mbar_try_wait(smem_u32(&bars->tfull[acc.slot]), acc.phase);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 16; ++i) {
                         const float2 d = make_float2(__uint_as_float(v[c & 1][2 * i]),
                                                      __uint_as_float(v[c & 1][2 * i + 1]));
-                        float2 f = make_float2(sab, sab);
-                        if (BROWS) {
-                            const float2 sb = *reinterpret_cast<const float2*>(s + kGM + half * 128 + c * 16 + 2 * i);
-                            f = fmul2(make_float2(sa, sa), sb);
-                        }
-                        sum[c * 8 + i] = ffma2(d, f, sum[c * 8 + i]);
+                        float2 f = make_float2(ab2, ab2);
+                        if (BROWS) f = fmul2(make_float2(a, a), *reinterpret_cast<const float2*>(s + c * 32 + 2 * i));
+                        sum[c * 16 + i] = ffma2(d, f, sum[c * 16 + i]);
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->sempty[sc.slot]));
-                acc.next(2);
-                sc.next(kScaleStages);
+                if (BROWS) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars->sempty[sc.slot]));
+                    sc.next(kScaleStages);
+                }
+            };
+            for (int kb = 0; ok && kb < p.KB; kb += 2) {
+                sa[0] = sa[2], sa[1] = sa[3], sb[0] = sb[2], sb[1] = sb[3];
+                load_scales(2, kb + 2);
+                load_scales(3, kb + 3);
+                group(sa[0], __fmul_rn(sa[0], sb[0]));
+                if (ok && kb + 1 < p.KB) group(sa[1], __fmul_rn(sa[1], sb[1]));
             }
             if (!ok) break;
-            const int64_t row = (int64_t)mb * kGM + quarter * 32 + lane;
-            if (row < p.M) {
+            const int64_t row0 = (int64_t)(2 * mb + rank) * kGM + quarter * 32;
+            const int col0 = nb * kGN + part * 128;
+            if (t + step < tiles) first_scales(t + step);
+            if (p.c_f32) {
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const float v[8] = {sum[4 * q].x,     sum[4 * q].y,     sum[4 * q + 1].x, sum[4 * q + 1].y,
-                                        sum[4 * q + 2].x, sum[4 * q + 2].y, sum[4 * q + 3].x, sum[4 * q + 3].y};
-                    store8(p, row, nb * kGN + half * 128 + q * 8, v);
-                }
+                for (int q = 0; q < 8; ++q) store_chunk<true>(p, out, lane, row0, col0 + q * 16, sum + q * 8);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) store_chunk<false>(p, out, lane, row0, col0 + q * 32, sum + q * 16);
             }
         }
     }
     tc_fence_before();
-    __syncthreads();
+    cluster_sync_all();  // the pair's MMAs and copies are done, in both CTAs' memory
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 
@@ -453,7 +546,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     unsigned char* sW = smem;
     unsigned char* sX = smem + S::kStages * S::kW;
     float* scales = reinterpret_cast<float*>(sX + S::kStages * S::kX);
-    auto* bars = reinterpret_cast<Bars8<S::kStages>*>(scales + kScaleStages * S::kScale);
+    auto* bars = reinterpret_cast<Bars8<S::kStages, 2>*>(scales + kScaleStages * S::kScale);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // p.MB blocks of NT rows of A, p.NB tiles of 128 rows of B; the M blocks of one tile run together
     const int tiles = p.MB * p.NB;
@@ -461,7 +554,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     const int first = (int)blockIdx.x / split, step = (int)gridDim.x / split;
     const int k0 = (int)((int64_t)p.KB * rank / split), k1 = (int)((int64_t)p.KB * (rank + 1) / split);
 
-    if (threadIdx.x == 0) init_bars8(bars, 4);
+    if (threadIdx.x == 0) init_bars8(bars, 4, 4);
     if (warp == 1) {
         tmem_alloc(smem_u32(&bars->tmem_addr), S::kTmem);
         tmem_relinquish();
@@ -671,8 +764,8 @@ template <bool BROWS>
 rlk_status launch_gemm(const Gemm8Params& p, const CUtensorMap& a, const CUtensorMap& b, int sms, cudaStream_t st) {
     const rlk_status s = allow_smem(gemm_kernel<BROWS>, kGSmem);
     if (s != RLK_OK) return s;
-    const int tiles = p.MB * p.NB;
-    gemm_kernel<BROWS><<<tiles < sms ? tiles : sms, kGThreads, kGSmem, st>>>(a, b, p);
+    const int tiles = p.MB * p.NB, pairs = sms / 2;
+    gemm_kernel<BROWS><<<2 * (tiles < pairs ? tiles : pairs), kGThreads, kGSmem, st>>>(a, b, p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product launch", e);
 }
@@ -749,11 +842,11 @@ rlk_status launch_fp8_matmul(int64_t M, int64_t N, int64_t K, const void* a, int
         return rows ? launch_skinny_nt<true>(nt, p, ta, tb, sms, stream)
                     : launch_skinny_nt<false>(nt, p, ta, tb, sms, stream);
     }
-    p.MB = (int32_t)((M + kGM - 1) / kGM);
+    p.MB = (int32_t)((M + 2 * kGM - 1) / (2 * kGM));
     p.NB = (int32_t)((N + kGN - 1) / kGN);
-    const int64_t band = ((int64_t)32 << 20) / ((int64_t)kGM * K);
+    const int64_t band = ((int64_t)32 << 20) / ((int64_t)2 * kGM * K);
     p.band = (int32_t)(band < 1 ? 1 : band < p.MB ? band : p.MB);
-    if (!make_map8(&ta, a, K, M, lda, kGM) || !make_map8(&tb, b, K, N, ldb, kGN))
+    if (!make_map8(&ta, a, K, M, lda, kGM) || !make_map8(&tb, b, K, N, ldb, kGN / 2))
         return fail(RLK_ERR_CUDA, "cuTensorMapEncodeTiled failed for an operand of the fp8 product");
     return rows ? launch_gemm<true>(p, ta, tb, sms, stream) : launch_gemm<false>(p, ta, tb, sms, stream);
 }

@@ -117,7 +117,7 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int64_t c0, int64_t C,
 }
 
 template <bool F32, bool BLOCKS, bool TRANS>
-__global__ void __launch_bounds__(kQThreads) quantize_kernel(const __grid_constant__ QuantParams p) {
+__global__ void __launch_bounds__(kQThreads, F32 ? 2 : 4) quantize_kernel(const __grid_constant__ QuantParams p) {
     __shared__ float colmax[TRANS && !BLOCKS ? 16 : 1][kQT];
     __shared__ float warpmax[8];
     __shared__ uint2 tile_t[TRANS ? kQT * 16 : 1];  // [column][8-row piece ^ (column / 8)]

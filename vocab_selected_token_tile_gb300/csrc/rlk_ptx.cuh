@@ -79,6 +79,17 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
     return t;
 }
 
+// This thread's warp index as a value the compiler knows to be uniform, and
+// one thread of a converged warp.  A role that a whole warp runs, with its
+// asynchronous instructions under elect_one(), keeps addresses and descriptors
+// in uniform registers; run by a single lane, each has to be moved there first.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
+}
+
 // ----------------------------------------------------------------- bulk copy
 
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
@@ -257,6 +268,52 @@ __device__ __forceinline__ void st_async_f32(uint32_t addr, float a, uint32_t re
 // All threads of all CTAs of the cluster; release/acquire at cluster scope.
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Arrive on an mbarrier of any CTA of the cluster (address from mapa).  For
+// handing tensor memory back, which the tcgen05 fences order: it orders no
+// generic memory between the CTAs.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// ----------------------------------------------------------------- CTA pairs (cta_group::2)
+//
+// Two CTAs of a cluster of two work one MMA: each holds half of A's rows and
+// half of B's, and half of the accumulator's rows in its own tensor memory.
+// One warp of each CTA allocates and frees (the two calls pair up); the even
+// CTA's thread issues the MMAs, whose descriptors name the same offsets in
+// both CTAs' shared memory.
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// Arrive (once) on the barrier at `bar`'s offset in both CTAs of the pair when
+// every tcgen05 operation this thread issued so far has completed.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// tma_load_2d whose completion may be counted on a barrier of either CTA of
+// the pair (`bar`: a cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int32_t c0, int32_t c1,
+                                                 uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
 }
 
 // ----------------------------------------------------------------- arithmetic
