@@ -492,7 +492,7 @@ rlk_status rlk_linear_ce_check(const rlk_linear_ce_contract* contract);
 
 /*
  * Bytes of device workspace: of the forward (with_grad 0), or of either call
- * (1): about T V / 32 for the forward's partials (half as much again with
+ * (1): about T V / 16 for the forward's partials (half as much again with
  * label smoothing); T piece * 2 + T H * 4 for the backward, whatever V is.
  * 0 for an invalid contract.
  */

@@ -31,8 +31,8 @@
 // be rounded in the same direction, a bias of up to 2^-9 in both gradients.
 // The scale multiplies the FP32 sums instead.
 //
-// The roles, waits and unit queue are the lm_head kernels' (rlk_gemm.cuh):
-// warp 0 issues the TMA loads, warp 1 the MMAs, warps 2-5 are the epilogue.
+// Stages, barriers and waits are the lm_head kernels' (rlk_gemm.cuh): warp 0
+// issues the TMA loads, warp 1 the MMAs, warps 2-9 are the epilogue.
 // Every sum has a fixed order: no split of a K range without an ordered join,
 // no atomics on data.
 #include <cuda.h>
@@ -57,32 +57,124 @@ constexpr size_t kCeTicketBytes = (2 * kMaxPieces + 32) * 8;
 constexpr int kMaxSlices = 32;                       // K slices of dHidden within a piece
 constexpr int64_t kBandBytes = (int64_t)32 << 20;    // hidden of one band of token blocks (as the lm_head's)
 constexpr int kBandH = 8;                            // H blocks per band of the gradient tiles (as the lm_head's)
-constexpr int kFoldSlices = 16;
+constexpr int kFoldRows = 8, kFoldSlices = 64;       // of one CTA of the merge
+
+// Ten warps: TMA, MMA and eight of the epilogue, each with 32 rows and half of an accumulator's 256 columns.
+constexpr int kCeThreads = 320, kCeEpilogue = 8;
 
 constexpr size_t kCeSmemCore = ((size_t)kStages * (kStageA + kStageB) + sizeof(Bars) + 1023) / 1024 * 1024;
 constexpr size_t kCeSmem = 1024 + kCeSmemCore;
-constexpr uint32_t kDxStage = 32 * 128;  // per epilogue warp: 32 rows x 64 BF16, one TMA store
-constexpr size_t kCeSmemDx = kCeSmem + 4 * kDxStage;
+constexpr uint32_t kCeOut = 32 * 64;  // per epilogue warp: 32 rows x 64 bytes on their way out
+constexpr size_t kCeSmemOut = kCeSmem + kCeEpilogue * kCeOut;
 
 enum : int { kCeForward = 0, kCeGrad = 1 };
-enum : int32_t { kNoTarget = -1, kInactive = -2 };
 
 struct CeParams {
     const int64_t* targets;
     const uint8_t* mask;
-    float2* part;           // [chunks, T] (max, sumexp)         forward
-    float* part_y;          // [chunks, T] sum of y              forward, with smoothing
-    float* yt;              // [T] the target's y                forward
-    const float4* rows;     // [T] (a, b, c, -lse log2 e)        gradient
-    const int32_t* target;  // [T] target, kNoTarget or kInactive  gradient
+    float2* part;        // [2 chunks, T] (max, sumexp) of 128 columns  forward
+    float* part_y;       // [2 chunks, T] sum of y                      forward, with smoothing
+    float* yt;           // [T] the target's y                          forward
+    const float* lse;    // [T]                                         gradient
+    const float* grad;   // [T], NULL for a summed or averaged loss     gradient
+    const float* scale;  // the common factor left out of dx            gradient
     unsigned long long* ticket;
     WaitCtl w;
     int64_t T, V, ignore_index;
-    float cap, icap;
+    float cap, icap, eps, z;
     int32_t KB, mask_mode;
     int32_t ch0, nch;       // the launch's chunks of 256 vocabulary rows
     int32_t MB, MBg;        // token blocks, and per band
 };
+
+// The unit queue, by whole warps.  The next ticket is asked for before the
+// present unit's loads are issued, so its latency is not the unit's.
+__device__ __forceinline__ unsigned long long ce_ticket(unsigned long long* ticket, int lane) {
+    return lane == 0 ? atomicAdd(ticket, 1ull) : 0ull;
+}
+__device__ __forceinline__ int64_t ce_unit_of(unsigned long long ticket, int64_t total) {
+    const int64_t u = (int64_t)__shfl_sync(0xFFFFFFFFu, ticket, 0);
+    return u < total ? u : -1;
+}
+__device__ __forceinline__ bool ce_put(Bars* bars, int& n, int64_t u, int lane, const WaitCtl& w) {
+    const int s = n % kUq;
+    const uint32_t par = (uint32_t)((n / kUq) & 1);
+    ++n;
+    if (!__all_sync(0xFFFFFFFFu, lm_wait(bars, smem_u32(&bars->uempty[s]), par ^ 1u, w))) return false;
+    if (lane == 0) {
+        *reinterpret_cast<volatile int64_t*>(&bars->unit[s]) = u;
+        mbar_arrive(smem_u32(&bars->ufull[s]));
+    }
+    __syncwarp();
+    return true;
+}
+__device__ __forceinline__ bool ce_get(Bars* bars, int& n, int64_t& u, int lane, const WaitCtl& w) {
+    const int s = n % kUq;
+    if (!__all_sync(0xFFFFFFFFu, lm_wait(bars, smem_u32(&bars->ufull[s]), (uint32_t)((n / kUq) & 1), w))) return false;
+    u = *reinterpret_cast<volatile int64_t*>(&bars->unit[s]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->uempty[s]));
+    ++n;
+    return u >= 0;
+}
+
+// A stage or accumulator ring's position.
+struct CeRing {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// The producer's last copies land before the CTA may exit (r: its position).
+__device__ void ce_drain(Bars* bars, CeRing r, int issued, const WaitCtl& w) {
+    for (int j = 0; j < issued; ++j) {
+        r.slot = r.slot == 0 ? kStages - 1 : r.slot - 1;
+        if (r.slot == kStages - 1) r.phase ^= 1u;
+        lm_drain_wait(smem_u32(&bars->full[r.slot]), r.phase, w);
+    }
+}
+
+// 32 BF16 columns of a warp's 32 rows (a lane's row in v) through shared
+// memory, so that a row's 64 bytes leave in one piece; 16 bytes a lane straight
+// from the registers, 32 rows an instruction, took 10,700 clocks a 128 x 256
+// tile.  16-byte piece j of row r is kept at j ^ (r / 2 mod 4).  Rows of
+// `rows` and columns of `cols` at most; every row starts on a 16-byte boundary.
+__device__ __forceinline__ void ce_store(unsigned char* out, int lane, const float (&v)[32], uint16_t* dst, int64_t ld,
+                                         int rows, int cols) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(out + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) =
+            make_uint4(pack_bf16x2_rn(v[8 * j], v[8 * j + 1]), pack_bf16x2_rn(v[8 * j + 2], v[8 * j + 3]),
+                       pack_bf16x2_rn(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2_rn(v[8 * j + 6], v[8 * j + 7]));
+    __syncwarp();
+    const int j = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        if (r >= rows || j * 8 >= cols) continue;
+        const uint4 w = *reinterpret_cast<const uint4*>(out + r * 64 + ((j ^ ((r >> 1) & 3)) * 16));
+        uint16_t* d = dst + r * ld + j * 8;
+        if (j * 8 + 8 <= cols) {
+            *reinterpret_cast<uint4*>(d) = w;
+        } else {
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (j * 8 + e < cols) d[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+}
+
+__device__ __forceinline__ bool ce_active(const uint8_t* mask, int mask_mode, int64_t ignore_index, int64_t target,
+                                          int64_t r) {
+    return mask_mode == RLK_MASK_EXPLICIT ? mask[r] != 0 : target != ignore_index;
+}
 
 __device__ __forceinline__ void ce_unit(const CeParams& p, int64_t u, int& ch, int& mb) {
     const int64_t band = (int64_t)p.nch * p.MBg;
@@ -135,19 +227,19 @@ __device__ __forceinline__ void ce_online(const float (&y)[32], int nv, float& m
 }
 
 template <int MODE, bool CAP, bool SMOOTH>
-__global__ void __launch_bounds__(kThreadsLm, 1)
+__global__ void __launch_bounds__(kCeThreads, 1)
     ce_logits_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
-                     const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CeParams p) {
+                     uint16_t* dx, const int64_t ldx, const __grid_constant__ CeParams p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* sA = smem;
     unsigned char* sB = smem + kStages * kStageA;
     Bars* bars = reinterpret_cast<Bars*>(smem + kStages * (kStageA + kStageB));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int64_t total = (int64_t)p.nch * p.MB;
 
-    if (threadIdx.x == 0) init_bars(bars);
+    if (threadIdx.x == 0) init_bars(bars, kCeEpilogue);
     if (warp == 1) {
         tmem_alloc(smem_u32(&bars->tmem_addr), kTmemCols);
         tmem_relinquish();
@@ -158,117 +250,103 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
     const uint32_t tmem = bars->tmem_addr;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int64_t issued = 0, n = 0;
-            bool aborted = false;
-            const uint64_t keep = l2_policy_evict_last();
-            while (!aborted) {
-                int64_t u = (int64_t)atomicAdd(p.ticket, 1ull);
-                if (u >= total) u = -1;
-                if (!unit_put(bars, n++, u, p.w) || u < 0) break;
-                int ch, mb;
-                ce_unit(p, u, ch, mb);
-                for (int kb = 0; kb < p.KB; ++kb) {
-                    if (!lm_wait(bars, smem_u32(&bars->empty[stage]), phase ^ 1u, p.w)) {
-                        aborted = true;
-                        break;
-                    }
-                    const uint32_t fb = smem_u32(&bars->full[stage]);
-                    mbar_arrive_expect_tx(fb, kStageA + kStageB);
-                    tma_load_2d_hint(smem_u32(sA + stage * kStageA), &tmH, kb * kBK, mb * kBM, fb, keep);
-                    tma_load_2d(smem_u32(sB + stage * kStageB), &tmW, kb * kBK, ch * kBN, fb);
-                    ++issued;
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            }
-            drain_copies(bars, issued, p.w);
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int64_t tiles = 0, n = 0;
-            bool aborted = false;
-            const uint32_t idesc = idesc_bf16_f32(kBM, kBN);
-            while (!aborted) {
-                int64_t u;
-                if (!unit_get(bars, n, u, p.w)) break;
-                unit_done(bars, n++);
-                if (u < 0) break;
-                const int acc = (int)(tiles & 1);
-                const uint32_t accph = (uint32_t)((tiles >> 1) & 1);
-                ++tiles;
-                if (!lm_wait(bars, smem_u32(&bars->tempty[acc]), accph ^ 1u, p.w)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * kBN);
-                for (int kb = 0; kb < p.KB; ++kb) {
-                    if (!lm_wait(bars, smem_u32(&bars->full[stage]), phase, p.w)) {
-                        aborted = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t a0 = smem_u32(sA + stage * kStageA), b0 = smem_u32(sB + stage * kStageB);
-#pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk)
-                        umma_bf16(d, smem_desc_sw128(a0 + kk * 32), smem_desc_sw128(b0 + kk * 32), idesc,
-                                  (kb | kk) != 0);
-                    umma_commit(smem_u32(&bars->empty[stage]));
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-                if (!aborted) umma_commit(smem_u32(&bars->tfull[acc]));
-            }
-            umma_commit(smem_u32(&bars->drain));
-            lm_drain_wait(smem_u32(&bars->drain), 0u, p.w);
-        }
-    } else {
-        const int quarter = warp & 3;
-        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        unsigned char* dst = smem + kCeSmemCore + quarter * kDxStage;  // kCeGrad
-        int64_t tiles = 0, n = 0;
-        for (;;) {
-            int64_t u = -1;
-            const bool got = unit_get(bars, n, u, p.w);
-            if (!__all_sync(0xFFFFFFFFu, got)) break;
-            __syncwarp();
-            if (lane == 0) unit_done(bars, n);
-            ++n;
-            if (u < 0) break;
+        const bool one = elect_one();
+        const uint64_t keep = l2_policy_evict_last();
+        CeRing r;
+        int issued = 0, n = 0;
+        bool ok = true;
+        int64_t u = ce_unit_of(ce_ticket(p.ticket, lane), total);
+        while (ok) {
+            if (!ce_put(bars, n, u, lane, p.w) || u < 0) break;
+            const unsigned long long ticket = ce_ticket(p.ticket, lane);
             int ch, mb;
             ce_unit(p, u, ch, mb);
-            const int64_t row = (int64_t)mb * kBM + quarter * 32 + lane;
+            for (int kb = 0; kb < p.KB; ++kb) {
+                if (!(ok = lm_wait(bars, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
+                if (one) {
+                    const uint32_t fb = smem_u32(&bars->full[r.slot]);
+                    mbar_arrive_expect_tx(fb, kStageA + kStageB);
+                    tma_load_2d_hint(smem_u32(sA + r.slot * kStageA), &tmH, kb * kBK, mb * kBM, fb, keep);
+                    tma_load_2d(smem_u32(sB + r.slot * kStageB), &tmW, kb * kBK, ch * kBN, fb);
+                }
+                issued = min(issued + 1, kStages);
+                r.next(kStages);
+            }
+            u = ce_unit_of(ticket, total);
+        }
+        ce_drain(bars, r, issued, p.w);
+    } else if (warp == 1) {
+        const bool one = elect_one();
+        const uint64_t da = smem_desc_sw128(smem_u32(sA)), db = smem_desc_sw128(smem_u32(sB));
+        const uint32_t idesc = idesc_bf16_f32(kBM, kBN);
+        CeRing r, acc;
+        int n = 0;
+        bool ok = true;
+        int64_t u;
+        while (ok && ce_get(bars, n, u, lane, p.w)) {
+            if (!(ok = lm_wait(bars, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + (uint32_t)(acc.slot * kBN);
+            for (int kb = 0; kb < p.KB; ++kb) {
+                if (!(ok = lm_wait(bars, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                tc_fence_after();
+                if (one) {
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        umma_bf16(d, da + ((r.slot * kStageA + kk * 32) >> 4), db + ((r.slot * kStageB + kk * 32) >> 4),
+                                  idesc, (kb | kk) != 0);
+                    umma_commit(smem_u32(&bars->empty[r.slot]));
+                    if (kb == p.KB - 1) umma_commit(smem_u32(&bars->tfull[acc.slot]));
+                }
+                __syncwarp();
+                r.next(kStages);
+            }
+            acc.next(2);
+        }
+        if (one) umma_commit(smem_u32(&bars->drain));
+        __syncwarp();
+        lm_drain_wait(smem_u32(&bars->drain), 0u, p.w);
+    } else {
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        unsigned char* out = smem + kCeSmemCore + (warp - 2) * kCeOut;  // kCeGrad
+        const float scale = MODE == kCeGrad ? *p.scale : 1.f;
+        CeRing acc;
+        int n = 0;
+        int64_t u;
+        while (ce_get(bars, n, u, lane, p.w)) {
+            int ch, mb;
+            ce_unit(p, u, ch, mb);
+            const int64_t row0 = (int64_t)mb * kBM + quarter * 32, row = row0 + lane;
             const bool valid = row < p.T;
-            int64_t target = kNoTarget;
+            int64_t target = -1;
             bool active = false;
-            float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (valid && MODE == kCeForward) {
+            float qa = 0.f, qb = 0.f, qc = 0.f, nlL = 0.f;
+            if (valid) {
                 target = p.targets[row];
-                active = (p.mask_mode == RLK_MASK_EXPLICIT) ? (p.mask[row] != 0) : (target != p.ignore_index);
+                active = ce_active(p.mask, p.mask_mode, p.ignore_index, target, row);
+                if (MODE == kCeGrad && active) {
+                    // dx / scale = (qa p - qc - qb [c = t]) slope
+                    const float l = p.lse[row];
+                    const float g = p.grad ? __fdiv_rn(p.grad[row], scale) : 1.f;
+                    qa = g * (1.f + 2.f * p.z * l);
+                    qb = g * (1.f - p.eps);
+                    qc = g * p.eps / (float)p.V;
+                    nlL = -__fmul_rn(l, kLog2e);
+                    if (ch == 0 && half == 0) {  // the device conditions of a row, once
+                        if (target < 0 || target >= p.V) atomicOr(p.w.status, kStatusTargetRange);
+                        if (!isfinite(l)) atomicOr(p.w.status, kStatusNonFinite);
+                    }
+                }
             }
-            if (valid && MODE == kCeGrad) {
-                q = p.rows[row];
-                target = p.target[row];
-                active = target != kInactive;
-            }
-            const int acc = (int)(tiles & 1);
-            const uint32_t accph = (uint32_t)((tiles >> 1) & 1);
-            ++tiles;
-            const bool ok = lm_wait(bars, smem_u32(&bars->tfull[acc]), accph, p.w);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (!__all_sync(0xFFFFFFFFu, lm_wait(bars, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w))) break;
             tc_fence_after();
             float m_run = -INFINITY, s_run = 0.f, y_run = 0.f;
-            const int64_t cbase = (int64_t)ch * kBN;
-            const int ncols = (int)(p.V - cbase < kBN ? p.V - cbase : kBN);
+            const int64_t cbase = (int64_t)ch * kBN + half * 128;
+            const int ncols = (int)max((int64_t)0, min((int64_t)128, p.V - cbase));
             for (int sub = 0; sub * 32 < ncols; ++sub) {
                 float v[32];
-                tmem_ld32(tmem + lane_base + (uint32_t)(acc * kBN + sub * 32), v);
+                tmem_ld32(tmem + lane_base + (uint32_t)(acc.slot * kBN + half * 128 + sub * 32), v);
                 const int nv = min(32, ncols - sub * 32);
                 const int64_t hot = target - (cbase + sub * 32);
                 const bool here = active && hot >= 0 && hot < nv;
@@ -289,48 +367,27 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
                     }
                     continue;
                 }
-                // dx = (a p - c - b [c = t]) slope
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     float slope = 1.f;
                     const float y = CAP ? ce_cap(v[i], p.cap, p.icap, slope) : v[i];
-                    float d = __fmaf_rn(ex2_approx(__fmaf_rn(y, kLog2e, q.w)), q.x, -q.z);
-                    if (hot_bit & (1u << i)) d = __fsub_rn(d, q.y);
+                    float d = __fmaf_rn(ex2_approx(__fmaf_rn(y, kLog2e, nlL)), qa, -qc);
+                    if (hot_bit & (1u << i)) d = __fsub_rn(d, qb);
                     if (CAP) d = __fmul_rn(d, slope);
                     v[i] = active ? d : 0.f;
                 }
-                // 64 columns a store: this block is half of the staged 128-byte rows (16-byte
-                // piece j of row r at j ^ (r mod 8)); the tensor map clips rows and columns outside
-                if ((sub & 1) == 0) {
-                    if (lane == 0) bulk_wait_read_all();  // the previous store has read the block
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<uint4*>(dst + lane * 128 + ((((sub & 1) * 4 + j) ^ (lane & 7)) * 16)) =
-                        make_uint4(pack_bf16x2_rn(v[8 * j], v[8 * j + 1]), pack_bf16x2_rn(v[8 * j + 2], v[8 * j + 3]),
-                                   pack_bf16x2_rn(v[8 * j + 4], v[8 * j + 5]),
-                                   pack_bf16x2_rn(v[8 * j + 6], v[8 * j + 7]));
-                if ((sub & 1) == 1 || (sub + 1) * 32 >= ncols) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tma_store_2d(&tmD, (ch - p.ch0) * kBN + (sub >> 1) * 64, mb * kBM + quarter * 32,
-                                     smem_u32(dst));
-                        bulk_commit();
-                    }
-                }
+                ce_store(out, lane, v, dx + row0 * ldx + (cbase - (int64_t)p.ch0 * kBN) + sub * 32, ldx,
+                         (int)min((int64_t)32, p.T - row0), nv);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
+            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc.slot]));
+            acc.next(2);
             if (MODE == kCeForward && valid) {
-                p.part[(int64_t)ch * p.T + row] = make_float2(m_run, s_run);
-                if (SMOOTH) p.part_y[(int64_t)ch * p.T + row] = y_run;
+                p.part[(int64_t)(2 * ch + half) * p.T + row] = make_float2(m_run, s_run);
+                if (SMOOTH) p.part_y[(int64_t)(2 * ch + half) * p.T + row] = y_run;
             }
         }
-        if (MODE == kCeGrad && lane == 0) bulk_wait_all();  // the stores complete before the CTA exits
-        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -360,22 +417,22 @@ struct CeFold {
     float* lse;
     uint32_t* status;
     int64_t T, V, ignore_index;
-    int32_t chunks, mask_mode;
+    int32_t parts, mask_mode;
     float eps, z;
 };
 
-// Each row's LSE and loss from its partials: 32 rows a CTA, 16 threads a row
-// take runs of chunks in vocabulary order, and their results are merged in
-// order.  The order depends on the number of chunks only.
-__global__ void __launch_bounds__(32 * kFoldSlices) ce_fold_kernel(const CeFold p) {
-    __shared__ float2 sm[kFoldSlices][32];
-    __shared__ float sy[kFoldSlices][32];
-    const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
-    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+// Each row's LSE and loss from its partials: 8 rows a CTA, 64 threads a row
+// take runs of partials in vocabulary order, and the runs are merged pairwise,
+// neighbours first.  The order depends on the number of partials only.
+__global__ void __launch_bounds__(kFoldRows* kFoldSlices) ce_fold_kernel(const CeFold p) {
+    __shared__ float2 sm[kFoldSlices][kFoldRows];
+    __shared__ float sy[kFoldSlices][kFoldRows];
+    const int lane = threadIdx.x % kFoldRows, sl = threadIdx.x / kFoldRows;
+    const int64_t row = (int64_t)blockIdx.x * kFoldRows + lane;
     float m = -INFINITY, s = 0.f, y = 0.f;
     if (row < p.T) {
-        const int c0 = (int)((int64_t)p.chunks * sl / kFoldSlices), c1 = (int)((int64_t)p.chunks * (sl + 1) / kFoldSlices);
-#pragma unroll 8
+        const int c0 = (int)((int64_t)p.parts * sl / kFoldSlices), c1 = (int)((int64_t)p.parts * (sl + 1) / kFoldSlices);
+#pragma unroll 4
         for (int c = c0; c < c1; ++c) {
             const float2 q = p.part[(int64_t)c * p.T + row];
             ce_merge(m, s, q.x, q.y);
@@ -384,18 +441,21 @@ __global__ void __launch_bounds__(32 * kFoldSlices) ce_fold_kernel(const CeFold 
     }
     sm[sl][lane] = make_float2(m, s);
     sy[sl][lane] = y;
-    __syncthreads();
-    if (sl != 0 || row >= p.T) return;
-    for (int k = 1; k < kFoldSlices; ++k) {
-        ce_merge(m, s, sm[k][lane].x, sm[k][lane].y);
-        y = __fadd_rn(y, sy[k][lane]);
+    for (int step = 1; step < kFoldSlices; step *= 2) {
+        __syncthreads();
+        if (sl % (2 * step) == 0) {
+            ce_merge(m, s, sm[sl + step][lane].x, sm[sl + step][lane].y);
+            y = __fadd_rn(y, sy[sl + step][lane]);
+            sm[sl][lane] = make_float2(m, s);
+            sy[sl][lane] = y;
+        }
     }
+    if (sl != 0 || row >= p.T) return;
     const float l = m == -INFINITY ? -INFINITY : __fadd_rn(m, logf(s));
     const int64_t t = p.targets[row];
-    const bool active = (p.mask_mode == RLK_MASK_EXPLICIT) ? (p.mask[row] != 0) : (t != p.ignore_index);
     p.lse[row] = l;
     float loss = 0.f;
-    if (active) {
+    if (ce_active(p.mask, p.mask_mode, p.ignore_index, t, row)) {
         if (t < 0 || t >= p.V) {
             loss = __int_as_float(0x7FC00000);
             atomicOr(p.status, kStatusTargetRange);
@@ -409,21 +469,16 @@ __global__ void __launch_bounds__(32 * kFoldSlices) ce_fold_kernel(const CeFold 
     p.loss[row] = loss;
 }
 
-// Block-wide sum in a fixed order (1024 threads).
-__device__ double block_sum(double v, double* scratch) {
+// Sum over a CTA of 1024 threads in a fixed order; the result is warp 0's.
+template <typename F>
+__device__ F block_sum(F v, F* scratch) {
+    for (int o = 16; o; o >>= 1) v += __shfl_down_sync(0xFFFFFFFFu, v, o);
     __syncthreads();
-    scratch[threadIdx.x] = v;
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
-    for (int o = 512; o; o >>= 1) {
-        if ((int)threadIdx.x < o) scratch[threadIdx.x] += scratch[threadIdx.x + o];
-        __syncthreads();
-    }
-    return scratch[0];
-}
-
-__device__ __forceinline__ bool ce_active(const uint8_t* mask, int mask_mode, int64_t ignore_index, int64_t target,
-                                          int64_t r) {
-    return mask_mode == RLK_MASK_EXPLICIT ? mask[r] != 0 : target != ignore_index;
+    v = scratch[threadIdx.x & 31];
+    for (int o = 16; o; o >>= 1) v += __shfl_down_sync(0xFFFFFFFFu, v, o);
+    return v;
 }
 
 // The sum, or the mean over the active rows (0 without any), of the rows'
@@ -431,77 +486,51 @@ __device__ __forceinline__ bool ce_active(const uint8_t* mask, int mask_mode, in
 __global__ void __launch_bounds__(1024) ce_reduce_kernel(const float* loss, const int64_t* targets,
                                                          const uint8_t* mask, int mask_mode, int64_t ignore_index,
                                                          int64_t T, int mean, float* out) {
-    __shared__ double scratch[1024];
-    double s = 0., n = 0.;
+    __shared__ double sums[32];
+    __shared__ long long counts[32];
+    double s = 0.;
+    long long n = 0;
     for (int64_t r = threadIdx.x; r < T; r += 1024) {
         s += (double)loss[r];
-        n += ce_active(mask, mask_mode, ignore_index, targets[r], r) ? 1. : 0.;
+        n += ce_active(mask, mask_mode, ignore_index, mask_mode == RLK_MASK_EXPLICIT ? 0 : targets[r], r);
     }
-    s = block_sum(s, scratch);
-    n = block_sum(n, scratch);
-    if (threadIdx.x == 0) *out = (float)(mean ? (n > 0. ? s / n : 0.) : s);
+    s = block_sum(s, sums);
+    n = block_sum(n, counts);
+    if (threadIdx.x == 0) *out = (float)(mean ? (n > 0 ? s / (double)n : 0.) : s);
 }
 
-struct CeRows {
-    const int64_t* targets;
-    const uint8_t* mask;
-    const float* lse;
-    const float* grad;  // [T], or one value for a summed or averaged loss
-    float4* rows;
-    int32_t* target;
-    float* scale;
-    uint32_t* status;
-    int64_t T, V, ignore_index;
-    int32_t mask_mode, reduction;
-    float eps, z;
-};
-
-// Per row what its dx needs, and the common factor that is left out of it.
-__global__ void __launch_bounds__(1024) ce_rows_kernel(const CeRows p) {
-    __shared__ double scratch[1024];
+// The factor that is left out of every row's dx: the gradient of a summed
+// loss, that of an averaged one over the active rows, or the largest finite
+// magnitude of the rows' gradients (a non-finite one stays its own row's).
+__global__ void __launch_bounds__(1024) ce_scale_kernel(const float* grad, const int64_t* targets,
+                                                        const uint8_t* mask, int mask_mode, int64_t ignore_index,
+                                                        int64_t T, int reduction, float* scale) {
+    __shared__ long long counts[32];
+    __shared__ float tops[32];
+    long long n = 0;
     float top = 0.f;
-    double n = 0.;
-    for (int64_t r = threadIdx.x; r < p.T; r += 1024) {
-        if (!ce_active(p.mask, p.mask_mode, p.ignore_index, p.targets[r], r)) continue;
-        n += 1.;
-        if (p.reduction == RLK_REDUCE_NONE) {
-            const float g = fabsf(p.grad[r]);
-            if (g < INFINITY) top = fmaxf(top, g);  // a non-finite gradient stays its own row's
+    if (reduction != RLK_REDUCE_SUM) {
+        for (int64_t r = threadIdx.x; r < T; r += 1024) {
+            if (!ce_active(mask, mask_mode, ignore_index, mask_mode == RLK_MASK_EXPLICIT ? 0 : targets[r], r)) continue;
+            ++n;
+            if (reduction == RLK_REDUCE_NONE) {
+                const float g = fabsf(grad[r]);
+                if (g < INFINITY) top = fmaxf(top, g);
+            }
         }
     }
-    float scale;
-    if (p.reduction == RLK_REDUCE_NONE) {
+    if (reduction == RLK_REDUCE_NONE) {
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
         __syncthreads();
-        scratch[threadIdx.x] = top;
-        __syncthreads();
-        for (int o = 512; o; o >>= 1) {
-            if ((int)threadIdx.x < o) scratch[threadIdx.x] = fmax(scratch[threadIdx.x], scratch[threadIdx.x + o]);
-            __syncthreads();
-        }
-        scale = (float)scratch[0];
-        if (scale == 0.f) scale = 1.f;
-    } else {
-        n = block_sum(n, scratch);
-        scale = p.grad[0];
-        if (p.reduction == RLK_REDUCE_MEAN) scale = n > 0. ? (float)((double)scale / n) : 0.f;
+        top = tops[threadIdx.x & 31];
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        if (threadIdx.x == 0) *scale = top == 0.f ? 1.f : top;
+        return;
     }
-    if (threadIdx.x == 0) *p.scale = scale;
-    for (int64_t r = threadIdx.x; r < p.T; r += 1024) {
-        const int64_t t = p.targets[r];
-        const float l = p.lse[r];
-        int32_t to = kInactive;
-        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ce_active(p.mask, p.mask_mode, p.ignore_index, t, r)) {
-            const float g = p.reduction == RLK_REDUCE_NONE ? __fdiv_rn(p.grad[r], scale) : 1.f;
-            q = make_float4(g * (1.f + 2.f * p.z * l), g * (1.f - p.eps), g * p.eps / (float)p.V,
-                            -__fmul_rn(l, kLog2e));
-            to = t >= 0 && t < p.V ? (int32_t)t : kNoTarget;
-            if (to == kNoTarget) atomicOr(p.status, kStatusTargetRange);
-            if (!isfinite(l)) atomicOr(p.status, kStatusNonFinite);
-        }
-        p.rows[r] = q;
-        p.target[r] = to;
-    }
+    n = block_sum(n, counts);
+    if (threadIdx.x == 0)
+        *scale = reduction == RLK_REDUCE_SUM ? grad[0] : n > 0 ? (float)((double)grad[0] / (double)n) : 0.f;
 }
 
 // ----------------------------------------------------------------- the gradients' products
@@ -549,22 +578,9 @@ __device__ __forceinline__ CeTile ce_tile(const CeGrads& p, int64_t u) {
     return t;
 }
 
-// Up to 8 BF16 values of an output row; columns past H are not the row's.
-__device__ __forceinline__ void store_bf16x8(uint16_t* row, int col, int H, const float* v) {
-    const uint32_t w[4] = {pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
-                           pack_bf16x2_rn(v[6], v[7])};
-    if (col + 8 <= H) {
-        *reinterpret_cast<uint4*>(row + col) = make_uint4(w[0], w[1], w[2], w[3]);
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (col + j < H) row[col + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-}
-
 // tmB*: the MN-major operand's 64-wide blocks in one 3-D box; tmC*: the same
 // matrix in 2-D boxes of one block, for the tile that holds H's ragged end.
-__global__ void __launch_bounds__(kThreadsLm, 1)
+__global__ void __launch_bounds__(kCeThreads, 1)
     ce_grads_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
                     const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmA1,
                     const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmC1,
@@ -575,10 +591,10 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
     unsigned char* sA = smem;
     unsigned char* sB = smem + kStages * kStageA;
     Bars* bars = reinterpret_cast<Bars*>(smem + kStages * (kStageA + kStageB));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int64_t total = p.n0 + p.n1;
 
-    if (threadIdx.x == 0) init_bars(bars);
+    if (threadIdx.x == 0) init_bars(bars, kCeEpilogue);
     if (warp == 1) {
         tmem_alloc(smem_u32(&bars->tmem_addr), kTmemCols);
         tmem_relinquish();
@@ -589,26 +605,22 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
     const uint32_t tmem = bars->tmem_addr;
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int64_t issued = 0, n = 0;
-            bool aborted = false;
-            while (!aborted) {
-                int64_t u = (int64_t)atomicAdd(p.ticket, 1ull);
-                if (u >= total) u = -1;
-                if (!unit_put(bars, n++, u, p.w) || u < 0) break;
-                const CeTile t = ce_tile(p, u);
-                const int m0 = t.mb * kBM, h0 = t.nb * kBN;
-                const bool ragged = p.H - h0 < t.nblk * 64;
-                const void* tb = t.prob ? (ragged ? &tmC1 : &tmB1) : (ragged ? &tmC0 : &tmB0);
-                for (int kb = t.k0; kb < t.k1; ++kb) {
-                    if (!lm_wait(bars, smem_u32(&bars->empty[stage]), phase ^ 1u, p.w)) {
-                        aborted = true;
-                        break;
-                    }
-                    const uint32_t fb = smem_u32(&bars->full[stage]);
-                    const uint32_t a = smem_u32(sA + stage * kStageA), b = smem_u32(sB + stage * kStageB);
+        const bool one = elect_one();
+        CeRing r;
+        int issued = 0, n = 0;
+        bool ok = true;
+        int64_t u = ce_unit_of(ce_ticket(p.ticket, lane), total);
+        while (ok) {
+            if (!ce_put(bars, n, u, lane, p.w) || u < 0) break;
+            const unsigned long long ticket = ce_ticket(p.ticket, lane);
+            const CeTile t = ce_tile(p, u);
+            const int m0 = t.mb * kBM, h0 = t.nb * kBN;
+            const bool ragged = p.H - h0 < t.nblk * 64;
+            for (int kb = t.k0; kb < t.k1; ++kb) {
+                if (!(ok = lm_wait(bars, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
+                if (one) {
+                    const uint32_t fb = smem_u32(&bars->full[r.slot]);
+                    const uint32_t a = smem_u32(sA + r.slot * kStageA), b = smem_u32(sB + r.slot * kStageB);
                     mbar_arrive_expect_tx(fb, kStageA + (ragged ? (uint32_t)t.nblk : 4u) * kMnBlock);
                     if (t.prob == 0) {
                         tma_load_2d(a, &tmA0, kb * kBK, m0, fb);
@@ -617,97 +629,81 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
                         tma_load_2d(a + kMnBlock, &tmA1, m0 + 64, kb * kBK, fb);
                     }
                     if (ragged) {
-                        for (int j = 0; j < t.nblk; ++j) tma_load_2d(b + j * kMnBlock, tb, h0 + j * 64, kb * kBK, fb);
+                        for (int j = 0; j < t.nblk; ++j)
+                            tma_load_2d(b + j * kMnBlock, t.prob ? &tmC1 : &tmC0, h0 + j * 64, kb * kBK, fb);
                     } else {
-                        tma_load_3d(b, tb, 0, kb * kBK, h0 / 64, fb);
-                    }
-                    ++issued;
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
+                        tma_load_3d(b, t.prob ? &tmB1 : &tmB0, 0, kb * kBK, h0 / 64, fb);
                     }
                 }
+                issued = min(issued + 1, kStages);
+                r.next(kStages);
             }
-            drain_copies(bars, issued, p.w);
+            u = ce_unit_of(ticket, total);
         }
+        ce_drain(bars, r, issued, p.w);
     } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            int64_t tiles = 0, n = 0;
-            bool aborted = false;
-            while (!aborted) {
-                int64_t u;
-                if (!unit_get(bars, n, u, p.w)) break;
-                unit_done(bars, n++);
-                if (u < 0) break;
-                const CeTile t = ce_tile(p, u);
-                const int acc = (int)(tiles & 1);
-                const uint32_t accph = (uint32_t)((tiles >> 1) & 1);
-                ++tiles;
-                if (!lm_wait(bars, smem_u32(&bars->tempty[acc]), accph ^ 1u, p.w)) break;
-                tc_fence_after();
-                const uint32_t idesc = idesc_bf16_f32_major(kBM, (uint32_t)(64 * t.nblk), t.prob == 1, true);
-                const uint32_t d = tmem + (uint32_t)(acc * kBN);
-                for (int kb = t.k0; kb < t.k1; ++kb) {
-                    if (!lm_wait(bars, smem_u32(&bars->full[stage]), phase, p.w)) {
-                        aborted = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t a0 = smem_u32(sA + stage * kStageA), b0 = smem_u32(sB + stage * kStageB);
-#pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk) {
-                        const uint64_t ad = t.prob == 0 ? smem_desc_sw128(a0 + kk * 32)
-                                                        : smem_desc_sw128_mn(a0 + kk * 2048, kMnBlock, 1024);
-                        umma_bf16(d, ad, smem_desc_sw128_mn(b0 + kk * 2048, kMnBlock, 1024), idesc,
-                                  kb != t.k0 || kk != 0);
-                    }
-                    umma_commit(smem_u32(&bars->empty[stage]));
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-                if (!aborted) umma_commit(smem_u32(&bars->tfull[acc]));
-            }
-            umma_commit(smem_u32(&bars->drain));
-            lm_drain_wait(smem_u32(&bars->drain), 0u, p.w);
-        }
-    } else {
-        const int quarter = warp & 3;
-        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        const float scale = *p.scale;
-        int64_t tiles = 0, n = 0;
-        for (;;) {
-            int64_t u = -1;
-            const bool got = unit_get(bars, n, u, p.w);
-            if (!__all_sync(0xFFFFFFFFu, got)) break;
-            __syncwarp();
-            if (lane == 0) unit_done(bars, n);
-            ++n;
-            if (u < 0) break;
+        const bool one = elect_one();
+        const uint64_t dk = smem_desc_sw128(smem_u32(sA)), dm = smem_desc_sw128_mn(smem_u32(sA), kMnBlock, 1024);
+        const uint64_t db = smem_desc_sw128_mn(smem_u32(sB), kMnBlock, 1024);
+        CeRing r, acc;
+        int n = 0;
+        bool ok = true;
+        int64_t u;
+        while (ok && ce_get(bars, n, u, lane, p.w)) {
             const CeTile t = ce_tile(p, u);
-            const int acc = (int)(tiles & 1);
-            const uint32_t accph = (uint32_t)((tiles >> 1) & 1);
-            ++tiles;
-            const bool ok = lm_wait(bars, smem_u32(&bars->tfull[acc]), accph, p.w);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (!(ok = lm_wait(bars, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
             tc_fence_after();
-            const int64_t row = (int64_t)t.mb * kBM + quarter * 32 + lane;
-            const bool valid = row < (t.prob == 0 ? p.T : (int64_t)p.cols);
+            const uint32_t idesc = idesc_bf16_f32_major(kBM, (uint32_t)(64 * t.nblk), t.prob == 1, true);
+            const uint32_t d = tmem + (uint32_t)(acc.slot * kBN);
+            // K-major A advances 16 elements (32 B) within its swizzle rows; an MN-major operand two 8-row K
+            // groups (2 x 1024 B)
+            const uint64_t da = t.prob == 0 ? dk : dm;
+            const int astep = t.prob == 0 ? 32 : 2048;
+            for (int kb = t.k0; kb < t.k1; ++kb) {
+                if (!(ok = lm_wait(bars, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                tc_fence_after();
+                if (one) {
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        umma_bf16(d, da + ((r.slot * kStageA + kk * astep) >> 4),
+                                  db + ((r.slot * kStageB + kk * 2048) >> 4), idesc, kb != t.k0 || kk != 0);
+                    umma_commit(smem_u32(&bars->empty[r.slot]));
+                }
+                __syncwarp();
+                r.next(kStages);
+            }
+            if (ok && one) umma_commit(smem_u32(&bars->tfull[acc.slot]));
+            __syncwarp();
+            acc.next(2);
+        }
+        if (one) umma_commit(smem_u32(&bars->drain));
+        __syncwarp();
+        lm_drain_wait(smem_u32(&bars->drain), 0u, p.w);
+    } else {
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        unsigned char* stage = smem + kCeSmemCore + (warp - 2) * kCeOut;
+        const float scale = *p.scale;
+        CeRing acc;
+        int n = 0;
+        int64_t u;
+        while (ce_get(bars, n, u, lane, p.w)) {
+            const CeTile t = ce_tile(p, u);
+            if (!__all_sync(0xFFFFFFFFu, lm_wait(bars, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w))) break;
+            tc_fence_after();
+            const int64_t row0 = (int64_t)t.mb * kBM + quarter * 32, row = row0 + lane;
+            const int64_t nrows = t.prob == 0 ? p.T : (int64_t)p.cols;
             // dHidden leaves as BF16 from the only slice of the last piece, else into the sums
             const bool out = t.prob == 1 || (p.S == 1 && p.last);
-            for (int sub = 0; sub < 2 * t.nblk; ++sub) {
+            for (int sub = half * 4; sub < min(half * 4 + 4, 2 * t.nblk); ++sub) {
                 float v[32];
-                tmem_ld32(tmem + lane_base + (uint32_t)(acc * kBN + sub * 32), v);
-                if (!valid) continue;
+                tmem_ld32(tmem + lane_base + (uint32_t)(acc.slot * kBN + sub * 32), v);
                 if (t.k0 == t.k1) {  // a slice without K blocks (a short last piece): no MMA wrote the accumulator
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
                 }
                 const int col0 = t.nb * kBN + sub * 32;
-                if (t.prob == 0 && !(out && p.first)) {
+                if (t.prob == 0 && !(out && p.first) && row < nrows) {
                     float4* s4 = reinterpret_cast<float4*>(p.sums + ((int64_t)t.slice * p.T + row) * p.Hs + col0);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
@@ -720,16 +716,17 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
                     }
                 }
                 if (out) {
-                    uint16_t* o = t.prob == 0 ? p.dhidden + row * p.ldh : p.dweight + row * p.ldw;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(v[i], scale);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) store_bf16x8(o, col0 + 8 * q, p.H, v + 8 * q);
+                    const int64_t ld = t.prob == 0 ? p.ldh : p.ldw;
+                    ce_store(stage, lane, v, (t.prob == 0 ? p.dhidden : p.dweight) + row0 * ld + col0, ld,
+                             (int)max((int64_t)0, min((int64_t)32, nrows - row0)), p.H - col0);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc]));
+            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc.slot]));
+            acc.next(2);
         }
     }
     tc_fence_before();
@@ -738,6 +735,19 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+// Up to 8 BF16 values of an output row; columns past H are not the row's.
+__device__ __forceinline__ void store_bf16x8(uint16_t* row, int col, int H, const float* v) {
+    const uint32_t w[4] = {pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
+                           pack_bf16x2_rn(v[6], v[7])};
+    if (col + 8 <= H) {
+        *reinterpret_cast<uint4*>(row + col) = make_uint4(w[0], w[1], w[2], w[3]);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (col + j < H) row[col + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
 }
 
 // dHidden from the S slices' sums, added in order.
@@ -801,23 +811,21 @@ CePlan plan_of(const rlk_linear_ce_contract& c) {
 
 struct CeLayout {
     size_t tickets, loss, yt, part, part_y, fwd_end;
-    size_t rows, target, scale, dx, sums, bwd_end;
+    size_t scale, dx, sums, bwd_end;
 };
 
 CeLayout layout_of(const rlk_linear_ce_contract& c) {
     CeLayout l{};
-    const size_t T = (size_t)c.T, chunks = (size_t)ceil_div(c.V, kBN);
+    const size_t T = (size_t)c.T, parts = 2 * (size_t)ceil_div(c.V, kBN);
     l.tickets = kWorkspaceBytes;
     size_t at = kWorkspaceBytes + up256(kCeTicketBytes);
     l.loss = at;
     l.yt = l.loss + up256(4 * T);
     l.part = l.yt + up256(4 * T);
-    l.part_y = l.part + up256(8 * T * chunks);
-    l.fwd_end = l.part_y + (c.label_smoothing != 0.f ? up256(4 * T * chunks) : 0);
+    l.part_y = l.part + up256(8 * T * parts);
+    l.fwd_end = l.part_y + (c.label_smoothing != 0.f ? up256(4 * T * parts) : 0);
     const CePlan q = plan_of(c);
-    l.rows = at;
-    l.target = l.rows + up256(16 * T);
-    l.scale = l.target + up256(4 * T);
+    l.scale = at;
     l.dx = l.scale + 256;
     l.sums = l.dx + up256(2 * T * (size_t)q.P);
     l.bwd_end = l.sums + (q.pieces > 1 || q.S > 1 ? up256(4 * (size_t)q.S * T * (size_t)q.Hs) : 0);
@@ -838,15 +846,15 @@ rlk_status ce_sms(int* sms) {
 }
 
 template <int MODE, bool CAP, bool SMOOTH>
-rlk_status launch_logits(const CUtensorMap& h, const CUtensorMap& w, const CUtensorMap& d, const CeParams& p, int sms,
-                         cudaStream_t st) {
-    const size_t bytes = MODE == kCeGrad ? kCeSmemDx : kCeSmem;
+rlk_status launch_logits(const CUtensorMap& h, const CUtensorMap& w, uint16_t* dx, int64_t ldx, const CeParams& p,
+                         int sms, cudaStream_t st) {
+    const size_t bytes = MODE == kCeGrad ? kCeSmemOut : kCeSmem;
     if (cudaFuncSetAttribute(ce_logits_kernel<MODE, CAP, SMOOTH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)bytes) != cudaSuccess)
         return ce_cuda("linear cross entropy: shared memory");
     const int64_t units = (int64_t)p.nch * p.MB;
     ce_logits_kernel<MODE, CAP, SMOOTH>
-        <<<(unsigned)(units < sms ? units : sms), kThreadsLm, bytes, st>>>(h, w, d, p);
+        <<<(unsigned)(units < sms ? units : sms), kCeThreads, bytes, st>>>(h, w, dx, ldx, p);
     return ce_cuda("linear cross entropy launch");
 }
 
@@ -861,6 +869,8 @@ CeParams ce_params(const rlk_linear_ce_contract& c, const int64_t* targets, cons
     p.ignore_index = c.ignore_index;
     p.cap = c.softcap;
     p.icap = c.softcap > 0.f ? 1.f / c.softcap : 0.f;
+    p.eps = c.label_smoothing;
+    p.z = c.z_loss;
     p.KB = (int32_t)ceil_div(c.H, kBK);
     p.mask_mode = c.mask_mode;
     p.MB = (int32_t)ceil_div(c.T, kBM);
@@ -900,10 +910,10 @@ rlk_status launch_linear_ce_fwd(const rlk_linear_ce_contract& c, const void* hid
         !make_map(&tmW, weight, c.H, c.V, c.weight_stride, kBK, kBN))
         return fail(RLK_ERR_CUDA, kMapFailed);
     const bool cap = c.softcap > 0.f, smooth = c.label_smoothing != 0.f;
-    s = cap ? (smooth ? launch_logits<kCeForward, true, true>(tmH, tmW, tmH, p, sms, st)
-                      : launch_logits<kCeForward, true, false>(tmH, tmW, tmH, p, sms, st))
-            : (smooth ? launch_logits<kCeForward, false, true>(tmH, tmW, tmH, p, sms, st)
-                      : launch_logits<kCeForward, false, false>(tmH, tmW, tmH, p, sms, st));
+    s = cap ? (smooth ? launch_logits<kCeForward, true, true>(tmH, tmW, nullptr, 0, p, sms, st)
+                      : launch_logits<kCeForward, true, false>(tmH, tmW, nullptr, 0, p, sms, st))
+            : (smooth ? launch_logits<kCeForward, false, true>(tmH, tmW, nullptr, 0, p, sms, st)
+                      : launch_logits<kCeForward, false, false>(tmH, tmW, nullptr, 0, p, sms, st));
     if (s != RLK_OK) return s;
     CeFold f{};
     f.part = p.part;
@@ -917,11 +927,11 @@ rlk_status launch_linear_ce_fwd(const rlk_linear_ce_contract& c, const void* hid
     f.T = c.T;
     f.V = c.V;
     f.ignore_index = c.ignore_index;
-    f.chunks = p.nch;
+    f.parts = 2 * p.nch;
     f.mask_mode = c.mask_mode;
     f.eps = c.label_smoothing;
     f.z = c.z_loss;
-    ce_fold_kernel<<<(unsigned)ceil_div(c.T, 32), 32 * kFoldSlices, 0, st>>>(f);
+    ce_fold_kernel<<<(unsigned)ceil_div(c.T, kFoldRows), kFoldRows * kFoldSlices, 0, st>>>(f);
     if (c.reduction != RLK_REDUCE_NONE)
         ce_reduce_kernel<<<1, 1024, 0, st>>>(f.loss, targets, mask, c.mask_mode, c.ignore_index, c.T,
                                              c.reduction == RLK_REDUCE_MEAN, loss);
@@ -940,35 +950,21 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     uint32_t* status = static_cast<uint32_t*>(workspace);
     if (cudaMemsetAsync(ws, 0, kWorkspaceBytes + kCeTicketBytes, st) != cudaSuccess)
         return ce_cuda("clearing the work space");
-    CeRows r{};
-    r.targets = targets;
-    r.mask = mask;
-    r.lse = lse;
-    r.grad = grad;
-    r.rows = reinterpret_cast<float4*>(ws + l.rows);
-    r.target = reinterpret_cast<int32_t*>(ws + l.target);
-    r.scale = reinterpret_cast<float*>(ws + l.scale);
-    r.status = status;
-    r.T = c.T;
-    r.V = c.V;
-    r.ignore_index = c.ignore_index;
-    r.mask_mode = c.mask_mode;
-    r.reduction = c.reduction;
-    r.eps = c.label_smoothing;
-    r.z = c.z_loss;
-    ce_rows_kernel<<<1, 1024, 0, st>>>(r);
-    if ((s = ce_cuda("linear cross entropy: rows")) != RLK_OK) return s;
+    float* scale = reinterpret_cast<float*>(ws + l.scale);
+    ce_scale_kernel<<<1, 1024, 0, st>>>(grad, targets, mask, c.mask_mode, c.ignore_index, c.T, c.reduction, scale);
+    if ((s = ce_cuda("linear cross entropy: scale")) != RLK_OK) return s;
 
-    const uint32_t smem = (uint32_t)kCeSmem;
+    const uint32_t smem = (uint32_t)kCeSmemOut;
     if (cudaFuncSetAttribute(ce_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return ce_cuda("linear cross entropy: shared memory");
     CeParams p = ce_params(c, targets, mask, status);
-    p.rows = r.rows;
-    p.target = r.target;
+    p.lse = lse;
+    p.grad = c.reduction == RLK_REDUCE_NONE ? grad : nullptr;
+    p.scale = scale;
     CeGrads g{};
     g.dhidden = static_cast<uint16_t*>(dhidden);
     g.sums = reinterpret_cast<float*>(ws + l.sums);
-    g.scale = r.scale;
+    g.scale = scale;
     g.w = p.w;
     g.T = c.T;
     g.ldh = c.dhidden_stride;
@@ -992,9 +988,9 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     for (int64_t i = 0; i < q.pieces; ++i) {
         const int64_t c0 = i * q.P, cols = c.V - c0 < q.P ? c.V - c0 : q.P;
         const uint16_t* w0 = static_cast<const uint16_t*>(weight) + c0 * c.weight_stride;
-        CUtensorMap tmW, tmD, tmA0, tmA1, tmB0, tmC0;
+        CUtensorMap tmW, tmA0, tmA1, tmB0, tmC0;
         if (!make_map(&tmW, weight, c.H, c.V, c.weight_stride, kBK, kBN) ||
-            !make_map(&tmD, dx, cols, c.T, q.P, 64, 32) || !make_map(&tmA0, dx, cols, c.T, q.P, kBK, kBM) ||
+            !make_map(&tmA0, dx, cols, c.T, q.P, kBK, kBM) ||
             !make_map(&tmA1, dx, cols, c.T, q.P, 64, kBK) ||
             !make_map(&tmC0, w0, c.H, cols, c.weight_stride, 64, kBK) ||
             (wide && !make_map_mn3(&tmB0, w0, c.H / 64 * 64, cols, c.weight_stride, kBK, 4)))
@@ -1003,8 +999,8 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
         p.ticket = tickets + 2 * i;
         p.ch0 = (int32_t)(c0 / kBN);
         p.nch = (int32_t)ceil_div(cols, kBN);
-        s = c.softcap > 0.f ? launch_logits<kCeGrad, true, false>(tmH, tmW, tmD, p, sms, st)
-                            : launch_logits<kCeGrad, false, false>(tmH, tmW, tmD, p, sms, st);
+        s = c.softcap > 0.f ? launch_logits<kCeGrad, true, false>(tmH, tmW, dx, q.P, p, sms, st)
+                            : launch_logits<kCeGrad, false, false>(tmH, tmW, dx, q.P, p, sms, st);
         if (s != RLK_OK) return s;
         g.ticket = tickets + 2 * i + 1;
         g.dweight = dweight ? static_cast<uint16_t*>(dweight) + c0 * c.dweight_stride : nullptr;
@@ -1016,7 +1012,7 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
         g.first = i == 0;
         g.last = i == q.pieces - 1;
         const int64_t tiles = g.n0 + g.n1;
-        ce_grads_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kThreadsLm, smem, st>>>(tmA0, tmB0, tmC0, tmA1, tmB1,
+        ce_grads_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kCeThreads, smem, st>>>(tmA0, tmB0, tmC0, tmA1, tmB1,
                                                                                          tmC1, g);
         if ((s = ce_cuda("linear cross entropy: gradients")) != RLK_OK) return s;
     }

@@ -49,7 +49,7 @@ struct Bars {
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t ufull[kUq];   // unit queue entry written (the producer's arrival)
-    uint64_t uempty[kUq];  // entry read by the MMA thread and the four epilogue warps
+    uint64_t uempty[kUq];  // entry read by the MMA thread and the epilogue warps
     uint64_t drain;
     int64_t unit[kUq];
     uint32_t tmem_addr;
@@ -61,15 +61,18 @@ struct WaitCtl {
     uint64_t wait_ns;
 };
 
+// Bounded wait for a phase; false when it expired or another role gave up.
+// The clock is read on every 256th poll only.
 __device__ bool lm_wait(Bars* bars, uint32_t bar, uint32_t parity, const WaitCtl& w) {
-    if (mbar_try_wait(bar, parity)) return true;
     volatile int* ab = &bars->abort_flag;
-    if (*ab) return false;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
+    uint64_t t0 = 0;
+    for (uint32_t polls = 0;; ++polls) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*ab) return false;
-        if (globaltimer_ns() - t0 > w.wait_ns) {
+        if ((polls & 255u) != 255u) continue;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > w.wait_ns) {
             *ab = 1;
             atomicOr(w.status, kStatusTimeout);
             return false;
@@ -106,18 +109,18 @@ __device__ bool unit_get(Bars* bars, int64_t n, int64_t& u, const WaitCtl& w) {
 
 __device__ __forceinline__ void unit_done(Bars* bars, int64_t n) { mbar_arrive(smem_u32(&bars->uempty[n % kUq])); }
 
-__device__ void init_bars(Bars* bars) {
+__device__ void init_bars(Bars* bars, int epilogue_warps = 4) {
     for (int s = 0; s < kStages; ++s) {
         mbar_init(smem_u32(&bars->full[s]), 1);
         mbar_init(smem_u32(&bars->empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
         mbar_init(smem_u32(&bars->tfull[b]), 1);
-        mbar_init(smem_u32(&bars->tempty[b]), 4);
+        mbar_init(smem_u32(&bars->tempty[b]), epilogue_warps);
     }
     for (int s = 0; s < kUq; ++s) {
         mbar_init(smem_u32(&bars->ufull[s]), 1);
-        mbar_init(smem_u32(&bars->uempty[s]), 5);
+        mbar_init(smem_u32(&bars->uempty[s]), epilogue_warps + 1);
     }
     mbar_init(smem_u32(&bars->drain), 1);
     bars->abort_flag = 0;
