@@ -43,6 +43,7 @@
 
 #include "rlk_gemm.cuh"
 #include "rlk_internal.h"
+#include "rlk_pair.cuh"
 #include "rlk_ptx.cuh"
 
 namespace rlk {
@@ -50,7 +51,6 @@ namespace {
 
 constexpr int kGK = 128;         // K of a group, and of a ring stage: 128 E4M3 = one 128-byte swizzle row
 constexpr int kScaleStages = 8;  // ring of scales, deeper than the operands': its loads are small and unaligned
-constexpr uint64_t kDrainNs8 = 1000000000ull;
 
 // D[tmem] (+)= A[smem] B[smem]^T, E4M3 inputs (format 0 in both fields), FP32 accumulate.
 __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -130,80 +130,51 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
-template <int STAGES, int ACC>
+// A ring of scales: its barriers.
+struct ScaleBars {
+    uint64_t full[kScaleStages];
+    uint64_t empty[kScaleStages];
+};
+
+__device__ void init_scales(ScaleBars* b, int epilogue_warps) {
+    for (int s = 0; s < kScaleStages; ++s) {
+        mbar_init(smem_u32(&b->full[s]), 32);
+        mbar_init(smem_u32(&b->empty[s]), epilogue_warps);
+    }
+}
+
+// The barriers of a CTA on its own (skinny_kernel).
+template <int STAGES>
 struct Bars8 {
     uint64_t full[STAGES];
     uint64_t empty[STAGES];
-    uint64_t tfull[ACC];
-    uint64_t tempty[ACC];
-    uint64_t sfull[kScaleStages];
-    uint64_t sempty[kScaleStages];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    ScaleBars sc;
     uint64_t drain;
     uint32_t tmem_addr;
     int abort_flag;
 };
 
-struct Wait8 {
-    uint32_t* status;
-    uint64_t wait_ns;
-};
-
-// Bounded wait for a phase of a barrier (the clock is read on every 1024th poll).
-__device__ __forceinline__ bool wait8(int* abort_flag, uint32_t bar, uint32_t parity, const Wait8& w) {
-    uint64_t t0 = 0;
-    for (uint32_t polls = 0;; ++polls) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((polls & 1023u) != 1023u) continue;
-        if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
-        const uint64_t now = globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > w.wait_ns) {
-            *reinterpret_cast<volatile int*>(abort_flag) = 1;
-            atomicOr(w.status, kStatusTimeout);
-            return false;
-        }
-    }
-}
-
-__device__ __forceinline__ void drain8(uint32_t bar, uint32_t parity, const Wait8& w) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer_ns() - t0 > kDrainNs8) {
-            atomicOr(w.status, kStatusTimeout);
-            return;
-        }
-    }
-}
-
-template <int STAGES, int ACC>
-__device__ void init_bars8(Bars8<STAGES, ACC>* b, int epilogue_warps, int tempty_arrivals) {
+template <int STAGES>
+__device__ void init_bars8(Bars8<STAGES>* b, int epilogue_warps) {
     for (int s = 0; s < STAGES; ++s) {
         mbar_init(smem_u32(&b->full[s]), 1);
         mbar_init(smem_u32(&b->empty[s]), 1);
     }
-    for (int i = 0; i < ACC; ++i) {
+    for (int i = 0; i < 2; ++i) {
         mbar_init(smem_u32(&b->tfull[i]), 1);
-        mbar_init(smem_u32(&b->tempty[i]), tempty_arrivals);
+        mbar_init(smem_u32(&b->tempty[i]), epilogue_warps);
     }
-    for (int s = 0; s < kScaleStages; ++s) {
-        mbar_init(smem_u32(&b->sfull[s]), 32);
-        mbar_init(smem_u32(&b->sempty[s]), epilogue_warps);
-    }
+    init_scales(&b->sc, epilogue_warps);
     mbar_init(smem_u32(&b->drain), 1);
     b->abort_flag = 0;
     fence_mbar_init();
 }
 
-// Position in a ring of n slots: the slot and the parity of its current pass.
-struct Ring {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next(int n) {
-        if (++slot == n) {
-            slot = 0;
-            phase ^= 1u;
-        }
-    }
+struct GemmBars {
+    PairBars<6> pair;
+    ScaleBars sc;
 };
 
 struct Gemm8Params {
@@ -215,7 +186,7 @@ struct Gemm8Params {
     int32_t band;       // M tiles per band of the tile order
     int32_t nsb;        // scales of B per K group: N (rows) or ceil(N / 128) (blocks)
     int32_t c_f32, accumulate, vec;
-    Wait8 w;
+    PipeWait w;
 };
 
 // A warp's 32 rows x 64 bytes of C (16 FP32 or 32 BF16 columns; a lane holds
@@ -287,7 +258,7 @@ constexpr int kGThreads = 384;
 constexpr uint32_t kGOut = 32 * 64;  // an epilogue warp's output stage: 32 rows x 64 bytes
 constexpr size_t kGSmem =
     1024 + (size_t)kGStages * (kGA + kGB) + kScaleStages * kGN * 4 + 8 * kGOut + 1024;
-static_assert(sizeof(Bars8<kGStages, 2>) <= 1024, "barriers fit their kilobyte");
+static_assert(sizeof(GemmBars) <= 1024, "barriers fit their kilobyte");
 
 // Tile t of the persistent order: bands of `band` M tiles, and within a band
 // all M tiles of one N tile before the next, so the tiles in flight share a
@@ -313,20 +284,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     unsigned char* sB = smem + kGStages * kGA;
     unsigned char* sOut = sB + kGStages * kGB;
     float* scales = reinterpret_cast<float*>(sOut + 8 * kGOut);
-    auto* bars = reinterpret_cast<Bars8<kGStages, 2>*>(scales + kScaleStages * kGN);
+    auto* all = reinterpret_cast<GemmBars*>(scales + kScaleStages * kGN);
+    PairBars<kGStages>* bars = &all->pair;
+    ScaleBars* sbars = &all->sc;
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
     const int tiles = p.MB * p.NB, first = (int)blockIdx.x / 2, step = (int)gridDim.x / 2;
 
-    if (threadIdx.x == 0) init_bars8(bars, 8, 16);
-    if (warp == 1) {
-        tmem_alloc_pair(smem_u32(&bars->tmem_addr), 512);
-        tmem_relinquish_pair();
-    }
-    tc_fence_before();
-    cluster_sync_all();  // both CTAs' barriers are initialised and their tensor memory allocated
-    tc_fence_after();
-    const uint32_t tmem = bars->tmem_addr;
+    if (threadIdx.x == 0) init_scales(sbars, 8);
+    const uint32_t tmem = pair_begin(bars, warp, 8);
     int* ab = &bars->abort_flag;
 
     if (warp < 4) {
@@ -343,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 tile_of(p, t, mb, nb);
                 const int a_row = (2 * mb + rank) * kGM, b_row = nb * kGN + rank * (kGN / 2);
                 for (int kb = 0; kb < p.KB; ++kb) {
-                    if (!(ok = wait8(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
+                    if (!(ok = pipe_wait(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                     if (one) {
                         const uint32_t fb = full0 + r.slot * 8;
                         if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars->full[r.slot]), 2 * (kGA + kGB));
@@ -354,13 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                     r.next(kGStages);
                 }
             }
-            // every copy lands before the CTA may exit: the even CTA's barriers count both CTAs' copies, and the
-            // odd one leaves only after the even one
-            for (int j = 0; j < issued && rank == 0; ++j) {
-                r.slot = r.slot == 0 ? kGStages - 1 : r.slot - 1;
-                if (r.slot == kGStages - 1) r.phase ^= 1u;
-                drain8(smem_u32(&bars->full[r.slot]), r.phase, p.w);
-            }
+            pair_drain_copies(bars, r, issued, rank, p.w);
         } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------ MMA issuer of the pair
             const bool one = elect_one();
@@ -370,8 +330,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
                 for (int kb = 0; kb < p.KB; ++kb) {
-                    if (!(ok = wait8(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
-                    if (!(ok = wait8(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                    if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
+                    if (!(ok = pipe_wait(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
                     tc_fence_after();
                     if (one) {
 #pragma unroll
@@ -386,8 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                     acc.next(2);
                 }
             }
-            if (one) umma_commit_pair(smem_u32(&bars->drain));
-            drain8(smem_u32(&bars->drain), 0u, p.w);
+            pair_drain_mmas(bars, one, p.w);
         } else if (warp == 2 && BROWS) {
             // ------------------------------------------------ B's row scales, for all epilogue warps
             Ring r;
@@ -396,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 int mb, nb;
                 tile_of(p, t, mb, nb);
                 for (int kb = 0; kb < p.KB; ++kb) {
-                    ok = __all_sync(0xFFFFFFFFu, wait8(ab, smem_u32(&bars->sempty[r.slot]), r.phase ^ 1u, p.w));
+                    ok = __all_sync(0xFFFFFFFFu, pipe_wait(ab, smem_u32(&sbars->empty[r.slot]), r.phase ^ 1u, p.w));
                     if (!ok) break;
                     const uint32_t dst = smem_u32(scales + r.slot * kGN);
                     const float* b = p.sb + (int64_t)kb * p.nsb;
@@ -405,7 +364,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                         const int row = nb * kGN + i;
                         cp_async4(dst + i * 4, b + (row < p.N ? row : 0), row < p.N);
                     }
-                    cp_async_arrive(smem_u32(&bars->sfull[r.slot]));
+                    cp_async_arrive(smem_u32(&sbars->full[r.slot]));
                     r.next(kScaleStages);
                 }
             }
@@ -449,9 +408,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             // One K group: false when a wait expired.
             auto group = [&](float a, float ab2) {
                 bool sready = true;
-                if (BROWS) sready = mbar_try_wait(smem_u32(&bars->sfull[sc.slot]), sc.phase);
-                if (!ready) ok = wait8(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w);
-                if (!sready) ok = ok && wait8(ab, smem_u32(&bars->sfull[sc.slot]), sc.phase, p.w);
+                if (BROWS) sready = mbar_try_wait(smem_u32(&sbars->full[sc.slot]), sc.phase);
+                if (!ready) ok = pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w);
+                if (!sready) ok = ok && pipe_wait(ab, smem_u32(&sbars->full[sc.slot]), sc.phase, p.w);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) return;
                 tc_fence_after();
@@ -484,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 }
                 if (BROWS) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bars->sempty[sc.slot]));
+                    if (lane == 0) mbar_arrive(smem_u32(&sbars->empty[sc.slot]));
                     sc.next(kScaleStages);
                 }
             };
@@ -508,12 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             }
         }
     }
-    tc_fence_before();
-    cluster_sync_all();  // the pair's MMAs and copies are done, in both CTAs' memory
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc_pair(tmem, 512);
-    }
+    pair_end(tmem, warp);
 }
 
 // ----------------------------------------------------------------- few rows of A
@@ -546,7 +500,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     unsigned char* sW = smem;
     unsigned char* sX = smem + S::kStages * S::kW;
     float* scales = reinterpret_cast<float*>(sX + S::kStages * S::kX);
-    auto* bars = reinterpret_cast<Bars8<S::kStages, 2>*>(scales + kScaleStages * S::kScale);
+    auto* bars = reinterpret_cast<Bars8<S::kStages>*>(scales + kScaleStages * S::kScale);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // p.MB blocks of NT rows of A, p.NB tiles of 128 rows of B; the M blocks of one tile run together
     const int tiles = p.MB * p.NB;
@@ -554,7 +508,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     const int first = (int)blockIdx.x / split, step = (int)gridDim.x / split;
     const int k0 = (int)((int64_t)p.KB * rank / split), k1 = (int)((int64_t)p.KB * (rank + 1) / split);
 
-    if (threadIdx.x == 0) init_bars8(bars, 4, 4);
+    if (threadIdx.x == 0) init_bars8(bars, 4);
     if (warp == 1) {
         tmem_alloc(smem_u32(&bars->tmem_addr), S::kTmem);
         tmem_relinquish();
@@ -575,7 +529,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
             for (int t = first; ok && t < tiles; t += step) {
                 const int nb = t / p.MB, mb = t % p.MB;
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!(ok = wait8(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
+                    if (!(ok = pipe_wait(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                     const uint32_t fb = smem_u32(&bars->full[r.slot]);
                     mbar_arrive_expect_tx(fb, S::kW + S::kX);
                     tma_load_2d(smem_u32(sW + r.slot * S::kW), &tmB, kb * kGK, nb * kSRows, fb);
@@ -585,7 +539,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
                 }
             }
             for (int64_t j = issued > S::kStages ? issued - S::kStages : 0; j < issued; ++j)
-                drain8(smem_u32(&bars->full[j % S::kStages]), (uint32_t)((j / S::kStages) & 1), p.w);
+                pipe_drain(smem_u32(&bars->full[j % S::kStages]), (uint32_t)((j / S::kStages) & 1), p.w);
         }
     } else if (warp == 1) {
         if (lane == 0) {
@@ -594,8 +548,8 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
             const uint32_t idesc = idesc_e4m3_f32(kSRows, NT);
             for (int t = first; ok && t < tiles; t += step) {
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!(ok = wait8(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
-                    if (!(ok = wait8(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                    if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
+                    if (!(ok = pipe_wait(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
                     tc_fence_after();
                     const uint32_t w0 = smem_u32(sW + r.slot * S::kW), x0 = smem_u32(sX + r.slot * S::kX);
 #pragma unroll
@@ -609,7 +563,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
                 }
             }
             umma_commit(smem_u32(&bars->drain));
-            drain8(smem_u32(&bars->drain), 0u, p.w);
+            pipe_drain(smem_u32(&bars->drain), 0u, p.w);
         }
     } else if (warp == 2) {
         Ring r;
@@ -617,7 +571,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
         for (int t = first; ok && t < tiles; t += step) {
             const int nb = t / p.MB, mb = t % p.MB;
             for (int kb = k0; kb < k1; ++kb) {
-                ok = __all_sync(0xFFFFFFFFu, wait8(ab, smem_u32(&bars->sempty[r.slot]), r.phase ^ 1u, p.w));
+                ok = __all_sync(0xFFFFFFFFu, pipe_wait(ab, smem_u32(&bars->sc.empty[r.slot]), r.phase ^ 1u, p.w));
                 if (!ok) break;
                 const uint32_t dst = smem_u32(scales + r.slot * S::kScale);
                 const float* a = p.sa + (int64_t)kb * p.M;
@@ -635,7 +589,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
                 } else if (lane == 0) {
                     cp_async4(dst + NT * 4, b + nb, true);
                 }
-                cp_async_arrive(smem_u32(&bars->sfull[r.slot]));
+                cp_async_arrive(smem_u32(&bars->sc.full[r.slot]));
                 r.next(kScaleStages);
             }
         }
@@ -649,10 +603,10 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
 #pragma unroll
             for (int i = 0; i < NT; ++i) sum[i] = 0.f;
             for (int kb = k0; kb < k1; ++kb) {
-                ok = wait8(ab, smem_u32(&bars->sfull[sc.slot]), sc.phase, p.w);
+                ok = pipe_wait(ab, smem_u32(&bars->sc.full[sc.slot]), sc.phase, p.w);
                 const float* s = scales + sc.slot * S::kScale;
                 const float sb = s[NT + (BROWS ? row_in : 0)];
-                ok = __all_sync(0xFFFFFFFFu, ok && wait8(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w));
+                ok = __all_sync(0xFFFFFFFFu, ok && pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t t0 = tmem + lane_base + (uint32_t)(acc.slot * NT);
@@ -674,7 +628,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
                                                     sum[c * 16 + i]);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->sempty[sc.slot]));
+                if (lane == 0) mbar_arrive(smem_u32(&bars->sc.empty[sc.slot]));
                 acc.next(2);
                 sc.next(kScaleStages);
             }

@@ -9,8 +9,8 @@
 //   p_c = e^(y_c - lse).
 // Label smoothing eps, z-loss z and the cap are 0 when unused.
 //
-// Forward: one tcgen05 GEMM over units of (256 vocabulary rows, 128 tokens)
-// whose epilogue turns a row's 256 logits into one (max, sumexp[, sum])
+// Forward: one tcgen05 GEMM over units of (256 vocabulary rows, 256 tokens)
+// whose epilogue turns 128 of a row's logits into one (max, sumexp[, sum])
 // partial, then a merge of each row's partials in vocabulary order.  Bound:
 // the tensor core, 2 T V H operations; the epilogue of one accumulator runs
 // under the MMAs of the other.
@@ -31,8 +31,10 @@
 // be rounded in the same direction, a bias of up to 2^-9 in both gradients.
 // The scale multiplies the FP32 sums instead.
 //
-// Stages, barriers and waits are the lm_head kernels' (rlk_gemm.cuh): warp 0
-// issues the TMA loads, warp 1 the MMAs, warps 2-9 are the epilogue.
+// Both GEMM kernels run as CTA pairs (rlk_pair.cuh) on 256 x 256 tiles: warp 0
+// issues the TMA loads, warp 1 of the even CTA the MMAs, warps 2-9 are the
+// epilogue.  The tiles are dealt out before the launch, so every role of both
+// CTAs knows its sequence and no ticket travels between them.
 // Every sum has a fixed order: no split of a K range without an ordered join,
 // no atomics on data.
 #include <cuda.h>
@@ -45,6 +47,7 @@
 #include "rlk_fold.cuh"
 #include "rlk_gemm.cuh"
 #include "rlk_internal.h"
+#include "rlk_pair.cuh"
 #include "rlk_ptx.cuh"
 
 namespace rlk {
@@ -53,7 +56,6 @@ namespace {
 constexpr int64_t kPieceBytes = (int64_t)512 << 20;  // BF16 dx of one piece
 constexpr int kMinPiece = 2048;                      // vocabulary rows a piece at least
 constexpr int kMaxPieces = 512;
-constexpr size_t kCeTicketBytes = (2 * kMaxPieces + 32) * 8;
 constexpr int kMaxSlices = 32;                       // K slices of dHidden within a piece
 constexpr int64_t kBandBytes = (int64_t)32 << 20;    // hidden of one band of token blocks (as the lm_head's)
 constexpr int kBandH = 8;                            // H blocks per band of the gradient tiles (as the lm_head's)
@@ -62,10 +64,11 @@ constexpr int kFoldRows = 8, kFoldSlices = 64;       // of one CTA of the merge
 // Ten warps: TMA, MMA and eight of the epilogue, each with 32 rows and half of an accumulator's 256 columns.
 constexpr int kCeThreads = 320, kCeEpilogue = 8;
 
-constexpr size_t kCeSmemCore = ((size_t)kStages * (kStageA + kStageB) + sizeof(Bars) + 1023) / 1024 * 1024;
-constexpr size_t kCeSmem = 1024 + kCeSmemCore;
-constexpr uint32_t kCeOut = 32 * 64;  // per epilogue warp: 32 rows x 64 bytes on their way out
-constexpr size_t kCeSmemOut = kCeSmem + kCeEpilogue * kCeOut;
+constexpr int kCeStages = 6;
+constexpr uint32_t kCeA = 128 * 128, kCeB = 128 * 128;  // bytes of a stage: a CTA's 128 rows of A, half of B's 256; K = 64
+constexpr uint32_t kCeOut = 32 * 64;                    // per epilogue warp: 32 rows x 64 bytes on their way out
+constexpr size_t kCeSmem = 1024 + (size_t)kCeStages * (kCeA + kCeB) + kCeEpilogue * kCeOut + 1024;
+static_assert(sizeof(PairBars<kCeStages>) <= 1024, "barriers fit their kilobyte");
 
 enum : int { kCeForward = 0, kCeGrad = 1 };
 
@@ -78,66 +81,14 @@ struct CeParams {
     const float* lse;    // [T]                                         gradient
     const float* grad;   // [T], NULL for a summed or averaged loss     gradient
     const float* scale;  // the common factor left out of dx            gradient
-    unsigned long long* ticket;
-    WaitCtl w;
+    PipeWait w;
     int64_t T, V, ignore_index;
     float cap, icap, eps, z;
     int32_t KB, mask_mode;
-    int32_t ch0, nch;       // the launch's chunks of 256 vocabulary rows
-    int32_t MB, MBg;        // token blocks, and per band
+    int32_t ch0, nch;  // the launch's chunks of 256 vocabulary rows
+    int32_t MB, MBg;   // blocks of 256 tokens, and per band
+    int32_t box_rows;  // rows of hidden a load brings (128, or fewer where T is below it)
 };
-
-// The unit queue, by whole warps.  The next ticket is asked for before the
-// present unit's loads are issued, so its latency is not the unit's.
-__device__ __forceinline__ unsigned long long ce_ticket(unsigned long long* ticket, int lane) {
-    return lane == 0 ? atomicAdd(ticket, 1ull) : 0ull;
-}
-__device__ __forceinline__ int64_t ce_unit_of(unsigned long long ticket, int64_t total) {
-    const int64_t u = (int64_t)__shfl_sync(0xFFFFFFFFu, ticket, 0);
-    return u < total ? u : -1;
-}
-__device__ __forceinline__ bool ce_put(Bars* bars, int& n, int64_t u, int lane, const WaitCtl& w) {
-    const int s = n % kUq;
-    const uint32_t par = (uint32_t)((n / kUq) & 1);
-    ++n;
-    if (!__all_sync(0xFFFFFFFFu, lm_wait(bars, smem_u32(&bars->uempty[s]), par ^ 1u, w))) return false;
-    if (lane == 0) {
-        *reinterpret_cast<volatile int64_t*>(&bars->unit[s]) = u;
-        mbar_arrive(smem_u32(&bars->ufull[s]));
-    }
-    __syncwarp();
-    return true;
-}
-__device__ __forceinline__ bool ce_get(Bars* bars, int& n, int64_t& u, int lane, const WaitCtl& w) {
-    const int s = n % kUq;
-    if (!__all_sync(0xFFFFFFFFu, lm_wait(bars, smem_u32(&bars->ufull[s]), (uint32_t)((n / kUq) & 1), w))) return false;
-    u = *reinterpret_cast<volatile int64_t*>(&bars->unit[s]);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&bars->uempty[s]));
-    ++n;
-    return u >= 0;
-}
-
-// A stage or accumulator ring's position.
-struct CeRing {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next(int n) {
-        if (++slot == n) {
-            slot = 0;
-            phase ^= 1u;
-        }
-    }
-};
-
-// The producer's last copies land before the CTA may exit (r: its position).
-__device__ void ce_drain(Bars* bars, CeRing r, int issued, const WaitCtl& w) {
-    for (int j = 0; j < issued; ++j) {
-        r.slot = r.slot == 0 ? kStages - 1 : r.slot - 1;
-        if (r.slot == kStages - 1) r.phase ^= 1u;
-        lm_drain_wait(smem_u32(&bars->full[r.slot]), r.phase, w);
-    }
-}
 
 // 32 BF16 columns of a warp's 32 rows (a lane's row in v) through shared
 // memory, so that a row's 64 bytes leave in one piece; 16 bytes a lane straight
@@ -176,12 +127,14 @@ __device__ __forceinline__ bool ce_active(const uint8_t* mask, int mask_mode, in
     return mask_mode == RLK_MASK_EXPLICIT ? mask[r] != 0 : target != ignore_index;
 }
 
-__device__ __forceinline__ void ce_unit(const CeParams& p, int64_t u, int& ch, int& mb) {
-    const int64_t band = (int64_t)p.nch * p.MBg;
-    const int64_t full = p.MB / p.MBg;
-    const int64_t b = u / band < full ? u / band : full;
-    const int64_t r = u - b * band;
-    const int w = b < full ? p.MBg : p.MB - (int)full * p.MBg;
+// Unit u is (chunk ch of 256 vocabulary rows, block mb of 256 tokens): bands of
+// MBg token blocks, chunk-major within a band, so that the units in flight
+// share a few chunks of weight and one band of hidden, which L2 holds.
+__device__ __forceinline__ void ce_unit(const CeParams& p, uint32_t u, int& ch, int& mb) {
+    const uint32_t band = (uint32_t)p.nch * p.MBg, full = (uint32_t)p.MB / p.MBg;
+    const uint32_t b = min(u / band, full);
+    const uint32_t r = u - b * band;
+    const uint32_t w = b < full ? p.MBg : p.MB - full * p.MBg;
     ch = p.ch0 + (int)(r / w);
     mb = (int)(b * p.MBg + r % w);
 }
@@ -226,98 +179,98 @@ __device__ __forceinline__ void ce_online(const float (&y)[32], int nv, float& m
     s_run = __fadd_rn(s_run, __fadd_rn(__fadd_rn(a[0], a[1]), __fadd_rn(a[2], a[3])));
 }
 
+// The pieces of shared memory of a pair's GEMM: six stages of A and B, the
+// epilogue's output stages, the barriers; at the same offsets in both CTAs.
+struct CeSmem {
+    unsigned char *a, *b, *out;
+    PairBars<kCeStages>* bars;
+};
+__device__ __forceinline__ CeSmem ce_smem(unsigned char* raw) {
+    CeSmem m;
+    m.a = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    m.b = m.a + kCeStages * kCeA;
+    m.out = m.b + kCeStages * kCeB;
+    m.bars = reinterpret_cast<PairBars<kCeStages>*>(m.out + kCeEpilogue * kCeOut);
+    return m;
+}
+
 template <int MODE, bool CAP, bool SMOOTH>
-__global__ void __launch_bounds__(kCeThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
     ce_logits_kernel(const __grid_constant__ CUtensorMap tmH, const __grid_constant__ CUtensorMap tmW,
                      uint16_t* dx, const int64_t ldx, const __grid_constant__ CeParams p) {
     extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem =
-        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char* sA = smem;
-    unsigned char* sB = smem + kStages * kStageA;
-    Bars* bars = reinterpret_cast<Bars*>(smem + kStages * (kStageA + kStageB));
+    const CeSmem m = ce_smem(smem_raw);
+    PairBars<kCeStages>* bars = m.bars;
     const int warp = warp_index(), lane = threadIdx.x & 31;
-    const int64_t total = (int64_t)p.nch * p.MB;
-
-    if (threadIdx.x == 0) init_bars(bars, kCeEpilogue);
-    if (warp == 1) {
-        tmem_alloc(smem_u32(&bars->tmem_addr), kTmemCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = bars->tmem_addr;
+    const int rank = (int)cluster_ctarank();
+    const uint32_t total = (uint32_t)p.nch * p.MB, first = blockIdx.x / 2, step = gridDim.x / 2;
+    const uint32_t tmem = pair_begin(bars, warp, kCeEpilogue);
+    int* ab = &bars->abort_flag;
 
     if (warp == 0) {
         const bool one = elect_one();
+        const uint32_t full0 = mapa_shared(smem_u32(&bars->full[0]), 0);
         const uint64_t keep = l2_policy_evict_last();
-        CeRing r;
-        int issued = 0, n = 0;
+        Ring r;
+        int issued = 0;
         bool ok = true;
-        int64_t u = ce_unit_of(ce_ticket(p.ticket, lane), total);
-        while (ok) {
-            if (!ce_put(bars, n, u, lane, p.w) || u < 0) break;
-            const unsigned long long ticket = ce_ticket(p.ticket, lane);
+        for (uint32_t u = first; ok && u < total; u += step) {
             int ch, mb;
             ce_unit(p, u, ch, mb);
+            // a CTA without a row of its own loads no hidden: its rows of the accumulator are not used
+            const int row = (2 * mb + rank) * 128;
+            const bool mine = row < p.T;
+            const uint32_t bytes = 2 * kCeB + (uint32_t)p.box_rows * 128 * ((2 * mb + 1) * (int64_t)128 < p.T ? 2 : 1);
             for (int kb = 0; kb < p.KB; ++kb) {
-                if (!(ok = lm_wait(bars, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
+                if (!(ok = pipe_wait(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                 if (one) {
-                    const uint32_t fb = smem_u32(&bars->full[r.slot]);
-                    mbar_arrive_expect_tx(fb, kStageA + kStageB);
-                    tma_load_2d_hint(smem_u32(sA + r.slot * kStageA), &tmH, kb * kBK, mb * kBM, fb, keep);
-                    tma_load_2d(smem_u32(sB + r.slot * kStageB), &tmW, kb * kBK, ch * kBN, fb);
+                    const uint32_t fb = full0 + r.slot * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars->full[r.slot]), bytes);
+                    if (mine) tma_load_2d_pair_hint(smem_u32(m.a + r.slot * kCeA), &tmH, kb * kBK, row, fb, keep);
+                    tma_load_2d_pair(smem_u32(m.b + r.slot * kCeB), &tmW, kb * kBK, ch * kBN + rank * 128, fb);
                 }
-                issued = min(issued + 1, kStages);
-                r.next(kStages);
+                issued = min(issued + 1, kCeStages);
+                r.next(kCeStages);
             }
-            u = ce_unit_of(ticket, total);
         }
-        ce_drain(bars, r, issued, p.w);
-    } else if (warp == 1) {
+        pair_drain_copies(bars, r, issued, rank, p.w);
+    } else if (warp == 1 && rank == 0) {
         const bool one = elect_one();
-        const uint64_t da = smem_desc_sw128(smem_u32(sA)), db = smem_desc_sw128(smem_u32(sB));
-        const uint32_t idesc = idesc_bf16_f32(kBM, kBN);
-        CeRing r, acc;
-        int n = 0;
+        const uint64_t da = smem_desc_sw128(smem_u32(m.a)), db = smem_desc_sw128(smem_u32(m.b));
+        const uint32_t idesc = idesc_bf16_f32(256, kBN);
+        Ring r, acc;
         bool ok = true;
-        int64_t u;
-        while (ok && ce_get(bars, n, u, lane, p.w)) {
-            if (!(ok = lm_wait(bars, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
-            tc_fence_after();
+        for (uint32_t u = first; ok && u < total; u += step) {
+            if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
             const uint32_t d = tmem + (uint32_t)(acc.slot * kBN);
             for (int kb = 0; kb < p.KB; ++kb) {
-                if (!(ok = lm_wait(bars, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                if (!(ok = pipe_wait(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
                 tc_fence_after();
                 if (one) {
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
-                        umma_bf16(d, da + ((r.slot * kStageA + kk * 32) >> 4), db + ((r.slot * kStageB + kk * 32) >> 4),
-                                  idesc, (kb | kk) != 0);
-                    umma_commit(smem_u32(&bars->empty[r.slot]));
-                    if (kb == p.KB - 1) umma_commit(smem_u32(&bars->tfull[acc.slot]));
+                        umma_bf16_pair(d, da + ((r.slot * kCeA + kk * 32) >> 4), db + ((r.slot * kCeB + kk * 32) >> 4),
+                                       idesc, (kb | kk) != 0);
+                    if (kb == p.KB - 1) umma_commit_pair(smem_u32(&bars->tfull[acc.slot]));
+                    umma_commit_pair(smem_u32(&bars->empty[r.slot]));
                 }
                 __syncwarp();
-                r.next(kStages);
+                r.next(kCeStages);
             }
             acc.next(2);
         }
-        if (one) umma_commit(smem_u32(&bars->drain));
-        __syncwarp();
-        lm_drain_wait(smem_u32(&bars->drain), 0u, p.w);
-    } else {
+        pair_drain_mmas(bars, one, p.w);
+    } else if (warp >= 2) {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        unsigned char* out = smem + kCeSmemCore + (warp - 2) * kCeOut;  // kCeGrad
+        unsigned char* out = m.out + (warp - 2) * kCeOut;  // kCeGrad
+        const uint32_t done = mapa_shared(smem_u32(&bars->tempty[0]), 0);
         const float scale = MODE == kCeGrad ? *p.scale : 1.f;
-        CeRing acc;
-        int n = 0;
-        int64_t u;
-        while (ce_get(bars, n, u, lane, p.w)) {
+        Ring acc;
+        for (uint32_t u = first; u < total; u += step) {
             int ch, mb;
             ce_unit(p, u, ch, mb);
-            const int64_t row0 = (int64_t)mb * kBM + quarter * 32, row = row0 + lane;
+            const int64_t row0 = (int64_t)(2 * mb + rank) * 128 + quarter * 32, row = row0 + lane;
             const bool valid = row < p.T;
             int64_t target = -1;
             bool active = false;
@@ -339,7 +292,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     }
                 }
             }
-            if (!__all_sync(0xFFFFFFFFu, lm_wait(bars, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w))) break;
+            if (!__all_sync(0xFFFFFFFFu, pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w))) break;
             tc_fence_after();
             float m_run = -INFINITY, s_run = 0.f, y_run = 0.f;
             const int64_t cbase = (int64_t)ch * kBN + half * 128;
@@ -381,7 +334,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc.slot]));
+            if (lane == 0) mbar_arrive_remote(done + acc.slot * 8);
             acc.next(2);
             if (MODE == kCeForward && valid) {
                 p.part[(int64_t)(2 * ch + half) * p.T + row] = make_float2(m_run, s_run);
@@ -389,12 +342,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             }
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
-    }
+    pair_end(tmem, warp);
 }
 
 // (m, s) with (m2, s2): the larger maximum, both sums scaled to it; a maximum
@@ -540,162 +488,167 @@ struct CeGrads {
     uint16_t* dweight;  // the piece's rows, [cols, ldw] BF16, or NULL
     float* sums;        // [S, T, Hs] FP32 sums of dHidden across the pieces
     const float* scale;
-    unsigned long long* ticket;
-    WaitCtl w;
+    PipeWait w;
     int64_t T, ldh, ldw, Hs;
-    int64_t n0, n1;     // tiles of dHidden (S slices of MB0 x NB) and of dWeight (MB1 x NB)
+    int32_t n0, n1;     // tiles of dHidden (S slices of MB0 x NB) and of dWeight (MB1 x NB)
+    int32_t head;       // the tiles with the longer K range: 0 dHidden's, 1 dWeight's
+    int32_t deal;       // of the others, how many make up for a long tile less (ce_walk)
     int32_t cols;       // vocabulary rows of the piece
     int32_t H, NB, NBg, MB0, MB1, S, KB0, KB1;
     int32_t first, last;  // the first and the last piece
 };
 
+// A pair's i-th tile: 0 .. n0 - 1 dHidden's, then dWeight's; -1 past its last.
+// The longer tiles are dealt round; the pairs that the last round leaves out
+// get the first `deal` of the shorter ones among themselves, and the rest are
+// dealt round again.  A deal that both CTAs' roles know from the start.
+__device__ __forceinline__ int ce_walk(const CeGrads& p, int i, int pair, int pairs) {
+    const int nl = p.head ? p.n1 : p.n0, ns = p.head ? p.n0 : p.n1, left = nl % pairs;
+    const int mine = nl / pairs + (pair < left);
+    int v, is_long = 0;
+    if (i < mine) {
+        v = pair + i * pairs;
+        is_long = 1;
+    } else {
+        i -= mine;
+        const int k = pairs - left, at = pair - left;  // `deal` is 0 without a last round
+        const int extra = at >= 0 && at < p.deal ? (p.deal - at + k - 1) / k : 0;
+        v = i < extra ? at + i * k : p.deal + pair + (i - extra) * pairs;
+        if (v >= ns) return -1;
+    }
+    return (is_long != 0) == (p.head == 0) ? v : p.n0 + v;
+}
+
 struct CeTile {
-    int prob, mb, nb, nblk, slice, k0, k1;
+    int prob, mb, nb, wide, slice, k0, k1;  // wide: 64-column blocks of a CTA (2, or 1 in a narrow last tile)
 };
 
-// Tiles of dHidden first (their K range is the longer one), slice by slice;
-// bands of NBg H blocks, M-major within a band.
-__device__ __forceinline__ CeTile ce_tile(const CeGrads& p, int64_t u) {
+// dHidden slice by slice; bands of NBg H blocks, M-major within a band.
+__device__ __forceinline__ CeTile ce_tile(const CeGrads& p, int u) {
     CeTile t;
     t.prob = u < p.n0 ? 0 : 1;
-    int64_t v = t.prob ? u - p.n0 : u;
-    const int64_t MB = t.prob ? p.MB1 : p.MB0;
+    uint32_t v = t.prob ? u - p.n0 : u;
+    const uint32_t MB = t.prob ? p.MB1 : p.MB0;
     t.slice = 0;
     if (!t.prob) {
         t.slice = (int)(v / (MB * p.NB));
         v %= MB * p.NB;
     }
-    const int64_t band = MB * p.NBg, full = p.NB / p.NBg;
-    const int64_t b = v / band < full ? v / band : full;
-    const int64_t r = v - b * band;
-    const int w = b < full ? p.NBg : p.NB - (int)full * p.NBg;
+    const uint32_t band = MB * p.NBg, full = (uint32_t)p.NB / p.NBg;
+    const uint32_t b = min(v / band, full);
+    const uint32_t r = v - b * band;
+    const uint32_t w = b < full ? p.NBg : p.NB - full * p.NBg;
     t.mb = (int)(r / w);
     t.nb = (int)(b * p.NBg + r % w);
-    const int left = p.H - t.nb * kBN;
-    t.nblk = left >= kBN ? 4 : (left + 63) / 64;
+    t.wide = p.H - t.nb * kBN > 128 ? 2 : 1;
     t.k0 = t.prob ? 0 : (int)((int64_t)p.KB0 * t.slice / p.S);
     t.k1 = t.prob ? p.KB1 : (int)((int64_t)p.KB0 * (t.slice + 1) / p.S);
     return t;
 }
 
-// tmB*: the MN-major operand's 64-wide blocks in one 3-D box; tmC*: the same
-// matrix in 2-D boxes of one block, for the tile that holds H's ragged end.
-__global__ void __launch_bounds__(kCeThreads, 1)
+// tmB*: the MN-major operand's 64-wide blocks, two in one 3-D box; tmC*: the
+// same matrix in 2-D boxes of one block, for a tile that holds H's ragged end
+// or is narrow.
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
     ce_grads_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
                     const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmA1,
                     const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmC1,
                     const __grid_constant__ CeGrads p) {
     extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem =
-        reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char* sA = smem;
-    unsigned char* sB = smem + kStages * kStageA;
-    Bars* bars = reinterpret_cast<Bars*>(smem + kStages * (kStageA + kStageB));
+    const CeSmem m = ce_smem(smem_raw);
+    PairBars<kCeStages>* bars = m.bars;
     const int warp = warp_index(), lane = threadIdx.x & 31;
-    const int64_t total = p.n0 + p.n1;
-
-    if (threadIdx.x == 0) init_bars(bars, kCeEpilogue);
-    if (warp == 1) {
-        tmem_alloc(smem_u32(&bars->tmem_addr), kTmemCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = bars->tmem_addr;
+    const int rank = (int)cluster_ctarank();
+    const int pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
+    const uint32_t tmem = pair_begin(bars, warp, kCeEpilogue);
+    int* ab = &bars->abort_flag;
 
     if (warp == 0) {
         const bool one = elect_one();
-        CeRing r;
-        int issued = 0, n = 0;
+        const uint32_t full0 = mapa_shared(smem_u32(&bars->full[0]), 0);
+        Ring r;
+        int issued = 0;
         bool ok = true;
-        int64_t u = ce_unit_of(ce_ticket(p.ticket, lane), total);
-        while (ok) {
-            if (!ce_put(bars, n, u, lane, p.w) || u < 0) break;
-            const unsigned long long ticket = ce_ticket(p.ticket, lane);
+        for (int i = 0, u; ok && (u = ce_walk(p, i, pair, pairs)) >= 0; ++i) {
             const CeTile t = ce_tile(p, u);
-            const int m0 = t.mb * kBM, h0 = t.nb * kBN;
-            const bool ragged = p.H - h0 < t.nblk * 64;
+            const int m0 = (2 * t.mb + rank) * 128, h0 = t.nb * kBN + rank * t.wide * 64;
+            const bool box3 = t.wide == 2 && (p.H % 64 == 0 || p.H - t.nb * kBN >= kBN);
             for (int kb = t.k0; kb < t.k1; ++kb) {
-                if (!(ok = lm_wait(bars, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
+                if (!(ok = pipe_wait(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                 if (one) {
-                    const uint32_t fb = smem_u32(&bars->full[r.slot]);
-                    const uint32_t a = smem_u32(sA + r.slot * kStageA), b = smem_u32(sB + r.slot * kStageB);
-                    mbar_arrive_expect_tx(fb, kStageA + (ragged ? (uint32_t)t.nblk : 4u) * kMnBlock);
+                    const uint32_t fb = full0 + r.slot * 8;
+                    const uint32_t a = smem_u32(m.a + r.slot * kCeA), b = smem_u32(m.b + r.slot * kCeB);
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(smem_u32(&bars->full[r.slot]), 2 * (kCeA + (uint32_t)t.wide * kMnBlock));
                     if (t.prob == 0) {
-                        tma_load_2d(a, &tmA0, kb * kBK, m0, fb);
+                        tma_load_2d_pair(a, &tmA0, kb * kBK, m0, fb);
                     } else {
-                        tma_load_2d(a, &tmA1, m0, kb * kBK, fb);
-                        tma_load_2d(a + kMnBlock, &tmA1, m0 + 64, kb * kBK, fb);
+                        tma_load_2d_pair(a, &tmA1, m0, kb * kBK, fb);
+                        tma_load_2d_pair(a + kMnBlock, &tmA1, m0 + 64, kb * kBK, fb);
                     }
-                    if (ragged) {
-                        for (int j = 0; j < t.nblk; ++j)
-                            tma_load_2d(b + j * kMnBlock, t.prob ? &tmC1 : &tmC0, h0 + j * 64, kb * kBK, fb);
+                    if (box3) {
+                        tma_load_3d_pair(b, t.prob ? &tmB1 : &tmB0, 0, kb * kBK, h0 / 64, fb);
                     } else {
-                        tma_load_3d(b, t.prob ? &tmB1 : &tmB0, 0, kb * kBK, h0 / 64, fb);
+                        for (int j = 0; j < t.wide; ++j)
+                            tma_load_2d_pair(b + j * kMnBlock, t.prob ? &tmC1 : &tmC0, h0 + j * 64, kb * kBK, fb);
                     }
                 }
-                issued = min(issued + 1, kStages);
-                r.next(kStages);
+                issued = min(issued + 1, kCeStages);
+                r.next(kCeStages);
             }
-            u = ce_unit_of(ticket, total);
         }
-        ce_drain(bars, r, issued, p.w);
-    } else if (warp == 1) {
+        pair_drain_copies(bars, r, issued, rank, p.w);
+    } else if (warp == 1 && rank == 0) {
         const bool one = elect_one();
-        const uint64_t dk = smem_desc_sw128(smem_u32(sA)), dm = smem_desc_sw128_mn(smem_u32(sA), kMnBlock, 1024);
-        const uint64_t db = smem_desc_sw128_mn(smem_u32(sB), kMnBlock, 1024);
-        CeRing r, acc;
-        int n = 0;
+        const uint64_t dk = smem_desc_sw128(smem_u32(m.a)), dm = smem_desc_sw128_mn(smem_u32(m.a), kMnBlock, 1024);
+        const uint64_t db = smem_desc_sw128_mn(smem_u32(m.b), kMnBlock, 1024);
+        Ring r, acc;
         bool ok = true;
-        int64_t u;
-        while (ok && ce_get(bars, n, u, lane, p.w)) {
+        for (int i = 0, u; ok && (u = ce_walk(p, i, pair, pairs)) >= 0; ++i) {
             const CeTile t = ce_tile(p, u);
-            if (!(ok = lm_wait(bars, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
+            if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
             tc_fence_after();
-            const uint32_t idesc = idesc_bf16_f32_major(kBM, (uint32_t)(64 * t.nblk), t.prob == 1, true);
+            const uint32_t idesc = idesc_bf16_f32_major(256, (uint32_t)(128 * t.wide), t.prob == 1, true);
             const uint32_t d = tmem + (uint32_t)(acc.slot * kBN);
             // K-major A advances 16 elements (32 B) within its swizzle rows; an MN-major operand two 8-row K
             // groups (2 x 1024 B)
             const uint64_t da = t.prob == 0 ? dk : dm;
             const int astep = t.prob == 0 ? 32 : 2048;
             for (int kb = t.k0; kb < t.k1; ++kb) {
-                if (!(ok = lm_wait(bars, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                if (!(ok = pipe_wait(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
                 tc_fence_after();
                 if (one) {
 #pragma unroll
                     for (int kk = 0; kk < kBK / 16; ++kk)
-                        umma_bf16(d, da + ((r.slot * kStageA + kk * astep) >> 4),
-                                  db + ((r.slot * kStageB + kk * 2048) >> 4), idesc, kb != t.k0 || kk != 0);
-                    umma_commit(smem_u32(&bars->empty[r.slot]));
+                        umma_bf16_pair(d, da + ((r.slot * kCeA + kk * astep) >> 4),
+                                       db + ((r.slot * kCeB + kk * 2048) >> 4), idesc, kb != t.k0 || kk != 0);
+                    umma_commit_pair(smem_u32(&bars->empty[r.slot]));
                 }
                 __syncwarp();
-                r.next(kStages);
+                r.next(kCeStages);
             }
-            if (ok && one) umma_commit(smem_u32(&bars->tfull[acc.slot]));
+            if (ok && one) umma_commit_pair(smem_u32(&bars->tfull[acc.slot]));
             __syncwarp();
             acc.next(2);
         }
-        if (one) umma_commit(smem_u32(&bars->drain));
-        __syncwarp();
-        lm_drain_wait(smem_u32(&bars->drain), 0u, p.w);
-    } else {
+        pair_drain_mmas(bars, one, p.w);
+    } else if (warp >= 2) {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        unsigned char* stage = smem + kCeSmemCore + (warp - 2) * kCeOut;
+        unsigned char* stage = m.out + (warp - 2) * kCeOut;
+        const uint32_t done = mapa_shared(smem_u32(&bars->tempty[0]), 0);
         const float scale = *p.scale;
-        CeRing acc;
-        int n = 0;
-        int64_t u;
-        while (ce_get(bars, n, u, lane, p.w)) {
+        Ring acc;
+        for (int i = 0, u; (u = ce_walk(p, i, pair, pairs)) >= 0; ++i) {
             const CeTile t = ce_tile(p, u);
-            if (!__all_sync(0xFFFFFFFFu, lm_wait(bars, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w))) break;
+            if (!__all_sync(0xFFFFFFFFu, pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w))) break;
             tc_fence_after();
-            const int64_t row0 = (int64_t)t.mb * kBM + quarter * 32, row = row0 + lane;
+            const int64_t row0 = (int64_t)(2 * t.mb + rank) * 128 + quarter * 32, row = row0 + lane;
             const int64_t nrows = t.prob == 0 ? p.T : (int64_t)p.cols;
             // dHidden leaves as BF16 from the only slice of the last piece, else into the sums
             const bool out = t.prob == 1 || (p.S == 1 && p.last);
-            for (int sub = half * 4; sub < min(half * 4 + 4, 2 * t.nblk); ++sub) {
+            for (int sub = half * 2 * t.wide; sub < (half + 1) * 2 * t.wide; ++sub) {
+                if (t.nb * kBN + sub * 32 >= p.H) break;
                 float v[32];
                 tmem_ld32(tmem + lane_base + (uint32_t)(acc.slot * kBN + sub * 32), v);
                 if (t.k0 == t.k1) {  // a slice without K blocks (a short last piece): no MMA wrote the accumulator
@@ -725,16 +678,11 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc.slot]));
+            if (lane == 0) mbar_arrive_remote(done + acc.slot * 8);
             acc.next(2);
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
-    }
+    pair_end(tmem, warp);
 }
 
 // Up to 8 BF16 values of an output row; columns past H are not the row's.
@@ -786,7 +734,7 @@ struct CePlan {
 
 CePlan plan_of(const rlk_linear_ce_contract& c) {
     CePlan q{};
-    q.MB = (int)ceil_div(c.T, kBM);
+    q.MB = (int)ceil_div(c.T, 256);
     q.NB = (int)ceil_div(c.H, kBN);
     q.Hs = ceil_div(c.H, 64) * 64;
     const int64_t whole = ceil_div(c.V, kBN) * kBN;
@@ -799,10 +747,10 @@ CePlan plan_of(const rlk_linear_ce_contract& c) {
     if (c.piece <= 0) P = ceil_div(ceil_div(c.V, q.pieces), kBN) * kBN;  // pieces of one size
     q.pieces = ceil_div(c.V, P);
     q.P = P;
-    // dHidden has MB NB tiles with a K range of P: where they are fewer than two a CTA (152 SMs)
-    // the range is cut so that they are, in slices of at least 8 K blocks, with sums of their own.
+    // dHidden has MB NB tiles with a K range of P: where they are fewer than two a pair of CTAs (76
+    // pairs) the range is cut so that they are, in slices of at least 8 K blocks, with sums of their own.
     const int64_t tiles = (int64_t)q.MB * q.NB;
-    int64_t S = ceil_div(304, tiles);
+    int64_t S = ceil_div(152, tiles);
     if (S > P / (8 * kBK)) S = P / (8 * kBK);
     if (S > kMaxSlices) S = kMaxSlices;
     q.S = S < 1 ? 1 : S;
@@ -810,15 +758,14 @@ CePlan plan_of(const rlk_linear_ce_contract& c) {
 }
 
 struct CeLayout {
-    size_t tickets, loss, yt, part, part_y, fwd_end;
+    size_t loss, yt, part, part_y, fwd_end;
     size_t scale, dx, sums, bwd_end;
 };
 
 CeLayout layout_of(const rlk_linear_ce_contract& c) {
     CeLayout l{};
     const size_t T = (size_t)c.T, parts = 2 * (size_t)ceil_div(c.V, kBN);
-    l.tickets = kWorkspaceBytes;
-    size_t at = kWorkspaceBytes + up256(kCeTicketBytes);
+    const size_t at = kWorkspaceBytes;
     l.loss = at;
     l.yt = l.loss + up256(4 * T);
     l.part = l.yt + up256(4 * T);
@@ -848,13 +795,12 @@ rlk_status ce_sms(int* sms) {
 template <int MODE, bool CAP, bool SMOOTH>
 rlk_status launch_logits(const CUtensorMap& h, const CUtensorMap& w, uint16_t* dx, int64_t ldx, const CeParams& p,
                          int sms, cudaStream_t st) {
-    const size_t bytes = MODE == kCeGrad ? kCeSmemOut : kCeSmem;
     if (cudaFuncSetAttribute(ce_logits_kernel<MODE, CAP, SMOOTH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)bytes) != cudaSuccess)
+                             (int)kCeSmem) != cudaSuccess)
         return ce_cuda("linear cross entropy: shared memory");
-    const int64_t units = (int64_t)p.nch * p.MB;
+    const int64_t units = (int64_t)p.nch * p.MB, pairs = sms / 2;
     ce_logits_kernel<MODE, CAP, SMOOTH>
-        <<<(unsigned)(units < sms ? units : sms), kCeThreads, bytes, st>>>(h, w, dx, ldx, p);
+        <<<(unsigned)(2 * (units < pairs ? units : pairs)), kCeThreads, kCeSmem, st>>>(h, w, dx, ldx, p);
     return ce_cuda("linear cross entropy launch");
 }
 
@@ -873,8 +819,9 @@ CeParams ce_params(const rlk_linear_ce_contract& c, const int64_t* targets, cons
     p.z = c.z_loss;
     p.KB = (int32_t)ceil_div(c.H, kBK);
     p.mask_mode = c.mask_mode;
-    p.MB = (int32_t)ceil_div(c.T, kBM);
-    const int64_t band = kBandBytes / ((int64_t)kBM * c.H * 2);
+    p.MB = (int32_t)ceil_div(c.T, 256);
+    p.box_rows = (int32_t)(c.T < 128 ? ceil_div(c.T, 8) * 8 : 128);
+    const int64_t band = kBandBytes / ((int64_t)256 * c.H * 2);
     p.MBg = (int32_t)(band < 1 ? 1 : band < p.MB ? band : p.MB);
     return p;
 }
@@ -897,17 +844,16 @@ rlk_status launch_linear_ce_fwd(const rlk_linear_ce_contract& c, const void* hid
     const CeLayout l = layout_of(c);
     char* ws = static_cast<char*>(workspace);
     uint32_t* status = static_cast<uint32_t*>(workspace);
-    if (cudaMemsetAsync(ws, 0, kWorkspaceBytes + 256, st) != cudaSuccess) return ce_cuda("clearing the work space");
+    if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return ce_cuda("clearing the status word");
     CeParams p = ce_params(c, targets, mask, status);
-    p.ticket = reinterpret_cast<unsigned long long*>(ws + l.tickets);
     p.part = reinterpret_cast<float2*>(ws + l.part);
     p.part_y = reinterpret_cast<float*>(ws + l.part_y);
     p.yt = reinterpret_cast<float*>(ws + l.yt);
     p.ch0 = 0;
     p.nch = (int32_t)ceil_div(c.V, kBN);
     CUtensorMap tmH, tmW;
-    if (!make_map(&tmH, hidden, c.H, c.T, c.hidden_stride, kBK, kBM) ||
-        !make_map(&tmW, weight, c.H, c.V, c.weight_stride, kBK, kBN))
+    if (!make_map(&tmH, hidden, c.H, c.T, c.hidden_stride, kBK, (uint32_t)p.box_rows) ||
+        !make_map(&tmW, weight, c.H, c.V, c.weight_stride, kBK, 128))
         return fail(RLK_ERR_CUDA, kMapFailed);
     const bool cap = c.softcap > 0.f, smooth = c.label_smoothing != 0.f;
     s = cap ? (smooth ? launch_logits<kCeForward, true, true>(tmH, tmW, nullptr, 0, p, sms, st)
@@ -948,13 +894,12 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     const CePlan q = plan_of(c);
     char* ws = static_cast<char*>(workspace);
     uint32_t* status = static_cast<uint32_t*>(workspace);
-    if (cudaMemsetAsync(ws, 0, kWorkspaceBytes + kCeTicketBytes, st) != cudaSuccess)
-        return ce_cuda("clearing the work space");
+    if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return ce_cuda("clearing the status word");
     float* scale = reinterpret_cast<float*>(ws + l.scale);
     ce_scale_kernel<<<1, 1024, 0, st>>>(grad, targets, mask, c.mask_mode, c.ignore_index, c.T, c.reduction, scale);
     if ((s = ce_cuda("linear cross entropy: scale")) != RLK_OK) return s;
 
-    const uint32_t smem = (uint32_t)kCeSmemOut;
+    const uint32_t smem = (uint32_t)kCeSmem;
     if (cudaFuncSetAttribute(ce_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return ce_cuda("linear cross entropy: shared memory");
     CeParams p = ce_params(c, targets, mask, status);
@@ -977,43 +922,44 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     g.S = (int32_t)q.S;
     g.KB1 = (int32_t)ceil_div(c.T, kBK);
     uint16_t* dx = reinterpret_cast<uint16_t*>(ws + l.dx);
-    unsigned long long* tickets = reinterpret_cast<unsigned long long*>(ws + l.tickets);
     CUtensorMap tmH, tmB1, tmC1;
     const bool wide = c.H >= 64;
-    if (!make_map(&tmH, hidden, c.H, c.T, c.hidden_stride, kBK, kBM) ||
+    if (!make_map(&tmH, hidden, c.H, c.T, c.hidden_stride, kBK, (uint32_t)p.box_rows) ||
         !make_map(&tmC1, hidden, c.H, c.T, c.hidden_stride, 64, kBK) ||
-        (wide && !make_map_mn3(&tmB1, hidden, c.H / 64 * 64, c.T, c.hidden_stride, kBK, 4)))
+        (wide && !make_map_mn3(&tmB1, hidden, c.H / 64 * 64, c.T, c.hidden_stride, kBK, 2)))
         return fail(RLK_ERR_CUDA, kMapFailed);
     if (!wide) tmB1 = tmC1;
     for (int64_t i = 0; i < q.pieces; ++i) {
         const int64_t c0 = i * q.P, cols = c.V - c0 < q.P ? c.V - c0 : q.P;
         const uint16_t* w0 = static_cast<const uint16_t*>(weight) + c0 * c.weight_stride;
         CUtensorMap tmW, tmA0, tmA1, tmB0, tmC0;
-        if (!make_map(&tmW, weight, c.H, c.V, c.weight_stride, kBK, kBN) ||
-            !make_map(&tmA0, dx, cols, c.T, q.P, kBK, kBM) ||
+        if (!make_map(&tmW, weight, c.H, c.V, c.weight_stride, kBK, 128) ||
+            !make_map(&tmA0, dx, cols, c.T, q.P, kBK, 128) ||
             !make_map(&tmA1, dx, cols, c.T, q.P, 64, kBK) ||
             !make_map(&tmC0, w0, c.H, cols, c.weight_stride, 64, kBK) ||
-            (wide && !make_map_mn3(&tmB0, w0, c.H / 64 * 64, cols, c.weight_stride, kBK, 4)))
+            (wide && !make_map_mn3(&tmB0, w0, c.H / 64 * 64, cols, c.weight_stride, kBK, 2)))
             return fail(RLK_ERR_CUDA, kMapFailed);
         if (!wide) tmB0 = tmC0;
-        p.ticket = tickets + 2 * i;
         p.ch0 = (int32_t)(c0 / kBN);
         p.nch = (int32_t)ceil_div(cols, kBN);
         s = c.softcap > 0.f ? launch_logits<kCeGrad, true, false>(tmH, tmW, dx, q.P, p, sms, st)
                             : launch_logits<kCeGrad, false, false>(tmH, tmW, dx, q.P, p, sms, st);
         if (s != RLK_OK) return s;
-        g.ticket = tickets + 2 * i + 1;
         g.dweight = dweight ? static_cast<uint16_t*>(dweight) + c0 * c.dweight_stride : nullptr;
         g.cols = (int32_t)cols;
         g.KB0 = (int32_t)ceil_div(cols, kBK);
-        g.MB1 = (int32_t)ceil_div(cols, kBM);
-        g.n0 = dhidden ? q.S * q.MB * (int64_t)q.NB : 0;
-        g.n1 = dweight ? (int64_t)g.MB1 * q.NB : 0;
+        g.MB1 = (int32_t)ceil_div(cols, 256);
+        g.n0 = dhidden ? (int32_t)(q.S * q.MB * q.NB) : 0;
+        g.n1 = dweight ? g.MB1 * q.NB : 0;
         g.first = i == 0;
         g.last = i == q.pieces - 1;
-        const int64_t tiles = g.n0 + g.n1;
-        ce_grads_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kCeThreads, smem, st>>>(tmA0, tmB0, tmC0, tmA1, tmB1,
-                                                                                         tmC1, g);
+        const int tiles = g.n0 + g.n1, pairs = tiles < sms / 2 ? tiles : sms / 2;
+        const int k0 = (int)ceil_div(g.KB0, q.S), k1 = g.KB1;
+        g.head = k0 >= k1 ? 0 : 1;
+        const int nl = g.head ? g.n1 : g.n0, ns = g.head ? g.n0 : g.n1, left = nl % pairs;
+        const int64_t make_up = left ? (int64_t)(pairs - left) * ((g.head ? k1 : k0) / (g.head ? k0 : k1)) : 0;
+        g.deal = (int32_t)(make_up < ns ? make_up : ns);
+        ce_grads_kernel<<<2 * pairs, kCeThreads, smem, st>>>(tmA0, tmB0, tmC0, tmA1, tmB1, tmC1, g);
         if ((s = ce_cuda("linear cross entropy: gradients")) != RLK_OK) return s;
     }
     if (dhidden && q.S > 1) {

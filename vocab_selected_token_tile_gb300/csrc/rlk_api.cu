@@ -931,6 +931,9 @@ rlk_status check_ce(const rlk_linear_ce_contract* c) {
     if (c->T > ((int64_t)1 << 31) - 512 || c->V > ((int64_t)1 << 31) - 512)
         return fail(RLK_ERR_UNSUPPORTED, "T or V above 2^31 - 512");
     if (c->H > ((int64_t)1 << 20)) return fail(RLK_ERR_UNSUPPORTED, "hidden size H above 2^20");
+    const int64_t tb = (c->T + 255) / 256, vb = (c->V + 255) / 256, hb = (c->H + 255) / 256, most = (int64_t)1 << 30;
+    if (tb * vb > most || tb * hb > most || vb * hb > most)
+        return fail(RLK_ERR_UNSUPPORTED, "above 2^30 tiles of 256 x 256 of the logits or of a gradient");
     const struct {
         int64_t stride;
         const char* name;
