@@ -806,60 +806,76 @@ def shard_bwd(contract, shard, logits_shard, targets, mask, lse, grad, dlogits=N
 
 # ------------------------------------------------------------------ FP8 projections
 
-_FP8 = ("float8_e4m3fn", "uint8")  # E4M3 values, or their codes as bytes
+_torch = None
 
 
-def _matrix(t, name, kinds):
-    """A 2-D CUDA tensor of one of ``kinds`` with contiguous rows; returns its row stride in elements."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor, not {list(t.shape)} on {t.device}")
-    kind = str(t.dtype)[6:]
-    if kind not in kinds:
-        raise TypeError(f"{name} must be {' or '.join(kinds)}, not {kind}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+def _t():
+    """torch, imported at the first call that marshals tensors."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _raw_stream(t, stream):
+    """The stream's handle: the given one's, or the current one's of the tensor's device."""
+    return stream.cuda_stream if stream is not None else _t()._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _matrix(t, name, dtypes):
+    """A 2-D CUDA tensor of one of ``dtypes`` with contiguous rows: (rows, columns, row stride in elements)."""
+    shape = t.shape
+    if len(shape) != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor, not {list(shape)} on {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d)[6:] for d in dtypes)}, not {str(t.dtype)[6:]}")
+    rows, cols = shape
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name}'s rows must be contiguous: its strides are {list(t.stride())}")
-    stride = t.stride(0) if rows > 1 else max(cols, t.stride(0))
-    if rows > 1 and stride < cols:
+    if rows <= 1:
+        return rows, cols, max(cols, stride)
+    if stride < cols:
         raise ValueError(f"{name}'s rows overlap: its strides are {list(t.stride())}")
-    return stride
+    return rows, cols, stride
 
 
-def _codes_stride(t, name):
-    """The row stride of an E4M3 operand; a single row may come with any, and takes one of whole 16-byte pieces."""
-    stride = _matrix(t, name, _FP8)
-    return -(-t.shape[1] // 16) * 16 if t.shape[0] <= 1 else stride
+def _padded(stride, rows, cols, piece):
+    """A row stride; that of a single row, which may come with any, in whole 16-byte pieces."""
+    return -(-cols // piece) * piece if rows <= 1 else stride
 
 
-def _codes(rows, cols, dev):
-    """An E4M3 [rows, cols] tensor whose rows start on 16-byte boundaries."""
-    import torch
+def _codes(x, rows, cols):
+    """An E4M3 [rows, cols] tensor whose rows start on 16-byte boundaries, and its row stride."""
     stride = -(-cols // 16) * 16
-    t = torch.empty((rows, stride), dtype=torch.float8_e4m3fn, device=dev)
+    t = _new(x, rows, stride, _t().float8_e4m3fn)
     return (t if stride == cols else t[:, :cols]), stride
 
 
-def _scales(groups, rows, block_rows, dev):
-    import torch
-    return torch.empty((-(-groups // 128), rows if block_rows == 1 else -(-rows // 128)), dtype=torch.float32,
-                       device=dev)
+def _new(x, rows, cols, dtype):
+    """A contiguous [rows, cols] tensor on x's device (empty_strided takes half the host time of new_empty)."""
+    return _t().empty_strided((rows, cols), (cols, 1), dtype=dtype, device=x.device)
 
 
 def _quantize(x, block_rows, rowwise, transposed, stream):
-    stride = _matrix(x, "x", ("bfloat16", "float32"))
+    torch = _t()
+    R, C, stride = _matrix(x, "x", (torch.bfloat16, torch.float32))
     if block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128")
-    (R, C), dev = x.shape, x.device
     q = scale = qt = scale_t = None
     ldq = ldt = 0
+    gr, gc = -(-R // 128), -(-C // 128)
     if rowwise:
-        q, ldq = _codes(R, C, dev)
-        scale = _scales(C, R, block_rows, dev)
+        q, ldq = _codes(x, R, C)
+        scale = _new(x, gc, R if block_rows == 1 else gr, torch.float32)
     if transposed:
-        qt, ldt = _codes(C, R, dev)
-        scale_t = _scales(R, C, block_rows, dev)
-    check(rlk_fp8_quantize(R, C, _ptr(x), RLK_F32 if x.element_size() == 4 else RLK_BF16, stride, block_rows, _ptr(q),
-                           ldq, _ptr(scale), _ptr(qt), ldt, _ptr(scale_t), _stream(stream)))
+        qt, ldt = _codes(x, C, R)
+        scale_t = _new(x, gr, C if block_rows == 1 else gc, torch.float32)
+    st = rlk_fp8_quantize(R, C, x.data_ptr(), RLK_F32 if x.dtype is torch.float32 else RLK_BF16, stride, block_rows,
+                          _ptr(q), ldq, _ptr(scale), _ptr(qt), ldt, _ptr(scale_t), _raw_stream(x, stream))
+    if st:
+        check(st)
     return q, scale, qt, scale_t
 
 
@@ -882,13 +898,20 @@ def fp8_quantize_both(x, block_rows=1, stream=None):
 _fp8_workspaces = {}
 
 
-def _fp8_workspace(dev, stream):
+def _fp8_workspace(t, stream):
     """The status word of a device and stream: zeroed once, only ever set by a call."""
-    import torch
-    ws = _fp8_workspaces.get((dev, stream))
+    key = (t.device.index, stream)
+    ws = _fp8_workspaces.get(key)
     if ws is None:
-        ws = _fp8_workspaces[(dev, stream)] = torch.zeros(RLK_FP8_WORKSPACE, dtype=torch.uint8, device=dev)
+        ws = _fp8_workspaces[key] = t.new_zeros(RLK_FP8_WORKSPACE, dtype=_t().uint8)
     return ws
+
+
+def _scale_operand(s, name, groups, n):
+    if s.dtype is not _t().float32 or s.shape != (groups, n) or not s.is_contiguous() or not s.is_cuda:
+        raise ValueError(f"{name} must be a contiguous FP32 CUDA tensor [{groups}, {n}], not "
+                         f"{str(s.dtype)[6:]} {list(s.shape)}")
+    return s.data_ptr()
 
 
 def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=None, accumulate=False, workspace=None,
@@ -900,96 +923,115 @@ def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=Non
     may be strided); ``accumulate`` adds the product to an FP32 ``out``.  ``validate`` synchronises and raises if a
     device-side wait expired.
     """
-    import torch
-    lda, ldb = _codes_stride(a, "a"), _codes_stride(b, "b")
-    (M, K), (N, Kb) = a.shape, b.shape
+    torch = _t()
+    codes = (torch.float8_e4m3fn, torch.uint8)  # E4M3 values, or their codes as bytes
+    M, K, lda = _matrix(a, "a", codes)
+    N, Kb, ldb = _matrix(b, "b", codes)
     if Kb != K:
         raise ValueError(f"a is [{M}, {K}] and b [{N}, {Kb}]: their rows must have one length")
     if b_block_rows not in (1, 128):
         raise ValueError("b_block_rows must be 1 or 128")
     groups = -(-K // 128)
-    for name, s, n in (("a_scale", a_scale, M), ("b_scale", b_scale, N if b_block_rows == 1 else -(-N // 128))):
-        if s.dtype != torch.float32 or tuple(s.shape) != (groups, n) or not s.is_contiguous() or not s.is_cuda:
-            raise ValueError(f"{name} must be a contiguous FP32 CUDA tensor [{groups}, {n}], not "
-                             f"{str(s.dtype)[6:]} {list(s.shape)}")
+    pa = _scale_operand(a_scale, "a_scale", groups, M)
+    pb = _scale_operand(b_scale, "b_scale", groups, N if b_block_rows == 1 else -(-N // 128))
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         out_dtype = out_dtype or torch.bfloat16
-        if out_dtype not in (torch.bfloat16, torch.float32):
+        if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
             raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        out = _new(a, M, N, out_dtype)
         ldc = N
     else:
-        ldc = _matrix(out, "out", ("bfloat16", "float32"))
-        if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
+        rows, cols, ldc = _matrix(out, "out", (torch.bfloat16, torch.float32))
+        if (rows, cols) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError(f"out is {str(out.dtype)[6:]} {list(out.shape)}; the product is [{M}, {N}]")
-    st = _stream(stream)
+    st = _raw_stream(a, stream)
     if workspace is None:
-        workspace = _fp8_workspace(a.device, st)
+        workspace = _fp8_workspace(a, st)
     else:
         _need(workspace, "workspace", RLK_FP8_WORKSPACE, ("uint8",))
-    check(rlk_fp8_matmul(M, N, K, _ptr(a), lda, _ptr(a_scale), _ptr(b), ldb, _ptr(b_scale), b_block_rows, _ptr(out),
-                         RLK_F32 if out.element_size() == 4 else RLK_BF16, ldc, int(accumulate), _ptr(workspace), st))
+    status = rlk_fp8_matmul(M, N, K, a.data_ptr(), _padded(lda, M, K, 16), pa, b.data_ptr(), _padded(ldb, N, K, 16),
+                            pb, b_block_rows, out.data_ptr(), RLK_F32 if out.dtype is torch.float32 else RLK_BF16, ldc,
+                            int(accumulate), workspace.data_ptr(), st)
+    if status:
+        check(status)
     if validate:
-        check(rlk_logp_workspace_status(_ptr(workspace), st))
+        check(rlk_logp_workspace_status(workspace.data_ptr(), st))
     return out
 
 
 # ------------------------------------------------------------------ cross entropy over a large vocabulary
 
-def _row_stride(t, name, kinds):
-    """A BF16 matrix's row stride; one row takes one of whole 16-byte pieces."""
-    stride = _matrix(t, name, kinds)
-    return -(-t.shape[1] // 8) * 8 if t.shape[0] <= 1 else stride
+def _head_operand(t, name):
+    """A BF16 (or its int16 bits) matrix's (rows, columns, row stride)."""
+    torch = _t()
+    rows, cols, stride = _matrix(t, name, (torch.bfloat16, torch.int16, torch.uint16))
+    return rows, cols, _padded(stride, rows, cols, 8)
 
 
 def linear_ce_contract(hidden, weight, mask=None, ignore_index=-100, reduction=REDUCE_NONE, label_smoothing=0.0,
                        z_loss=0.0, softcap=0.0, piece=0, validate=0, wait_timeout_ns=0):
     """The contract of linear_ce_fwd and linear_ce_bwd for these operands: hidden [T, H] and weight [V, H], BF16,
     rows on 16-byte boundaries.  The gradients have rows of whole 16-byte pieces."""
-    hs, wstr = _row_stride(hidden, "hidden", _BF16), _row_stride(weight, "weight", _BF16)
-    (T, H), (V, Hw) = hidden.shape, weight.shape
+    T, H, hs = _head_operand(hidden, "hidden")
+    V, Hw, wstr = _head_operand(weight, "weight")
     if Hw != H:
         raise ValueError(f"hidden is [{T}, {H}] and weight [{V}, {Hw}]: their rows must have one length")
     out = -(-H // 8) * 8
     c = LinearCeContract(T, V, H, hs, wstr, out, out, ignore_index, wait_timeout_ns, piece,
                          MASK_EXPLICIT if mask is not None else MASK_IGNORE_INDEX, reduction, validate,
                          label_smoothing, z_loss, softcap)
-    check(rlk_linear_ce_check(c))
+    status = rlk_linear_ce_check(c)
+    if status:
+        check(status)
     return c
 
 
-def _ce_workspace(contract, with_grad, dev, workspace):
-    import torch
+def _ce_workspace(contract, with_grad, like, workspace):
     n = rlk_linear_ce_workspace_size(contract, with_grad)
     if n == 0:
         check(rlk_linear_ce_check(contract) or RLK_ERR_UNSUPPORTED)
     if workspace is None:
-        return torch.empty(n, dtype=torch.uint8, device=dev)
+        return _t().empty_strided((n,), (1,), dtype=_t().uint8, device=like.device)
     _need(workspace, "workspace", n, ("uint8",))
     return workspace
+
+
+def _vector(t, name, n, dtypes):
+    """A contiguous CUDA tensor of n elements (or more) of one of ``dtypes``; its pointer."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d)[6:] for d in dtypes)}, not {str(t.dtype)[6:]}")
+    if not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} elements, not {list(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def _ce_operands(c, hidden, weight, targets, mask):
     for name, t, rows, stride in (("hidden", hidden, c.T, c.hidden_stride or c.H),
                                   ("weight", weight, c.V, c.weight_stride or c.H)):
-        if tuple(t.shape) != (rows, c.H) or _row_stride(t, name, _BF16) != stride and rows > 1:
+        r, cols, s = _head_operand(t, name)
+        if r != rows or cols != c.H or (s != stride and rows > 1):
             raise ValueError(f"{name} is {list(t.shape)} with strides {list(t.stride())}; the contract's is "
                              f"[{rows}, {c.H}] with rows {stride} apart")
-    _rowwise(c, targets, mask)
+    torch = _t()
+    return (hidden.data_ptr(), weight.data_ptr(), _vector(targets, "targets", c.T, (torch.int64,)),
+            None if mask is None else _vector(mask, "mask", c.T, (torch.uint8, torch.bool)))
 
 
 def linear_ce_fwd(contract, hidden, weight, targets, mask=None, stream=None, workspace=None):
     """(loss, lse) of the cross entropy of hidden @ weight^T: loss [T], or one value with a reduction; lse [T]."""
-    import torch
-    _ce_operands(contract, hidden, weight, targets, mask)
-    dev, T = hidden.device, contract.T
-    loss = torch.empty((T,) if contract.reduction == REDUCE_NONE else (), dtype=torch.float32, device=dev)
-    lse = torch.empty(T, dtype=torch.float32, device=dev)
-    ws = _ce_workspace(contract, 0, dev, workspace)
-    check(rlk_linear_ce_fwd(contract, _ptr(hidden), _ptr(weight), _ptr(targets), _ptr(mask), _ptr(loss), _ptr(lse),
-                            _ptr(ws), _stream(stream)))
+    operands = _ce_operands(contract, hidden, weight, targets, mask)
+    f32 = _t().float32
+    new = _t().empty_strided
+    loss = new((contract.T,), (1,), dtype=f32, device=hidden.device) if contract.reduction == REDUCE_NONE else \
+        new((), (), dtype=f32, device=hidden.device)
+    lse = new((contract.T,), (1,), dtype=f32, device=hidden.device)
+    ws = _ce_workspace(contract, 0, hidden, workspace)
+    status = rlk_linear_ce_fwd(contract, *operands, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                               _raw_stream(hidden, stream))
+    if status:
+        check(status)
     return loss, lse
 
 
@@ -997,19 +1039,20 @@ def linear_ce_bwd(contract, hidden, weight, targets, mask, lse, grad_loss, need_
                   stream=None, workspace=None):
     """(dhidden [T, H], dweight [V, H]) in BF16 from the forward's lse and the loss's FP32 gradient ([T], or one value
     with a reduction); a gradient that is not needed is None and costs nothing."""
-    import torch
-    _ce_operands(contract, hidden, weight, targets, mask)
-    dev, T, V, H = hidden.device, contract.T, contract.V, contract.H
-    _need(lse, "lse", 4 * T, _F32)
-    _need(grad_loss, "grad_loss", 4 * (T if contract.reduction == REDUCE_NONE else 1), _F32)
+    operands = _ce_operands(contract, hidden, weight, targets, mask)
+    T, V, H, f32 = contract.T, contract.V, contract.H, (_t().float32,)
+    pl = _vector(lse, "lse", T, f32)
+    pg = _vector(grad_loss, "grad_loss", T if contract.reduction == REDUCE_NONE else 1, f32)
 
     def out(rows, stride):
-        t = torch.empty((rows, stride or H), dtype=hidden.dtype, device=dev)
+        t = _new(hidden, rows, stride or H, hidden.dtype)
         return t if t.shape[1] == H else t[:, :H]
 
     dh = out(T, contract.dhidden_stride) if need_dhidden else None
     dw = out(V, contract.dweight_stride) if need_dweight else None
-    ws = _ce_workspace(contract, 1, dev, workspace)
-    check(rlk_linear_ce_bwd(contract, _ptr(hidden), _ptr(weight), _ptr(targets), _ptr(mask), _ptr(lse),
-                            _ptr(grad_loss), _ptr(dh), _ptr(dw), _ptr(ws), _stream(stream)))
+    ws = _ce_workspace(contract, 1, hidden, workspace)
+    status = rlk_linear_ce_bwd(contract, *operands, pl, pg, _ptr(dh), _ptr(dw), ws.data_ptr(),
+                               _raw_stream(hidden, stream))
+    if status:
+        check(status)
     return dh, dw

