@@ -172,11 +172,6 @@ __device__ void init_bars8(Bars8<STAGES>* b, int epilogue_warps) {
     fence_mbar_init();
 }
 
-struct GemmBars {
-    PairBars<6> pair;
-    ScaleBars sc;
-};
-
 struct Gemm8Params {
     const float *sa, *sb;
     void* c;
@@ -189,19 +184,31 @@ struct Gemm8Params {
     PipeWait w;
 };
 
-// A warp's 32 rows x 64 bytes of C (16 FP32 or 32 BF16 columns; a lane holds
-// its row's) through shared memory, so that a row's 64 bytes leave in one
+// 8 BF16 columns of a row on the 16-byte grid, of which `cols` are C's.
+__device__ __forceinline__ void store_piece(uint16_t* c, uint4 w, int cols) {
+    if (cols >= 8) {
+        *reinterpret_cast<uint4*>(c) = w;
+        return;
+    }
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < cols) c[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+}
+
+// A warp's 32 rows x 128 bytes of C (32 FP32 or 64 BF16 columns; a lane holds
+// its row's) through shared memory, so that a row's 128 bytes leave in one
 // piece: 16 bytes a lane straight from the registers, 32 rows an instruction,
 // took 10,700 clocks a 128 x 256 tile, a third of the product's time at K =
-// 4096.  16-byte piece j of row r is kept at j ^ (r / 2 mod 4), which spreads
-// both directions over the banks.
+// 4096.  16-byte piece j of row r is kept at j ^ (r mod 8), which spreads both
+// directions over the banks.
 template <bool F32>
 __device__ __forceinline__ void store_chunk(const Gemm8Params& p, unsigned char* out, int lane, int64_t row0, int col0,
                                             const float2* v) {
     constexpr int kPer = F32 ? 4 : 8;  // elements of 16 bytes
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
         uint4 w;
         if (F32)
             w = make_uint4(__float_as_uint(v[2 * j].x), __float_as_uint(v[2 * j].y), __float_as_uint(v[2 * j + 1].x),
@@ -210,20 +217,26 @@ __device__ __forceinline__ void store_chunk(const Gemm8Params& p, unsigned char*
             w = make_uint4(pack_bf16x2_rn(v[4 * j].x, v[4 * j].y), pack_bf16x2_rn(v[4 * j + 1].x, v[4 * j + 1].y),
                            pack_bf16x2_rn(v[4 * j + 2].x, v[4 * j + 2].y),
                            pack_bf16x2_rn(v[4 * j + 3].x, v[4 * j + 3].y));
-        *reinterpret_cast<uint4*>(out + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) = w;
+        *reinterpret_cast<uint4*>(out + lane * 128 + ((j ^ (lane & 7)) * 16)) = w;
     }
     __syncwarp();
-    const int j = lane & 3, col = col0 + j * kPer;
-    if (col >= p.N) return;
+    const int rows = (int)min((int64_t)32, p.M - row0), cols = min(8 * kPer, p.N - col0);
+    if (p.vec) {
+        const int j = lane & 7, left = cols - j * kPer;
+        if (left <= 0) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + (lane >> 2);
-        if (row0 + r >= p.M) break;
-        uint4 w = *reinterpret_cast<const uint4*>(out + r * 64 + ((j ^ ((r >> 1) & 3)) * 16));
-        if (F32) {
-            float* c = static_cast<float*>(p.c) + (row0 + r) * p.ldc + col;
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            if (r >= rows) break;
+            const uint4 w = *reinterpret_cast<const uint4*>(out + r * 128 + ((j ^ (r & 7)) * 16));
+            const int64_t at = (row0 + r) * p.ldc + col0 + j * kPer;
+            if (!F32) {
+                store_piece(static_cast<uint16_t*>(p.c) + at, w, left);
+                continue;
+            }
+            float* c = static_cast<float*>(p.c) + at;
             float x[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
-            if (p.vec && col + 4 <= p.N) {
+            if (left >= 4) {
                 float4* c4 = reinterpret_cast<float4*>(c);
                 if (p.accumulate) {
                     const float4 o = *c4;
@@ -233,32 +246,52 @@ __device__ __forceinline__ void store_chunk(const Gemm8Params& p, unsigned char*
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (col + e < p.N) c[e] = p.accumulate ? c[e] + x[e] : x[e];
-            }
-        } else {
-            uint16_t* c = static_cast<uint16_t*>(p.c) + (row0 + r) * p.ldc + col;
-            if (p.vec && col + 8 <= p.N) {
-                *reinterpret_cast<uint4*>(c) = w;
-            } else {
-                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (col + e < p.N) c[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+                    if (e < left) c[e] = p.accumulate ? c[e] + x[e] : x[e];
             }
         }
+        return;
+    }
+    // rows off the 16-byte grid: 4 bytes a lane, a row an instruction
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+        const uint32_t w =
+            *reinterpret_cast<const uint32_t*>(out + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
+        const int64_t at = (row0 + r) * p.ldc + col0;
+        if (F32) {
+            float* c = static_cast<float*>(p.c) + at + lane;
+            if (lane < cols) *c = p.accumulate ? *c + __uint_as_float(w) : __uint_as_float(w);
+            continue;
+        }
+        // a BF16 row that starts between words: the words are shifted by one column, and its first column goes alone
+        uint16_t* c = static_cast<uint16_t*>(p.c) + at;
+        const int odd = (int)((reinterpret_cast<uintptr_t>(c) >> 1) & 1);
+        const uint32_t up = __shfl_down_sync(0xFFFFFFFFu, w, 1);
+        const uint32_t x = odd ? __funnelshift_r(w, up, 16) : w;
+        const int e = 2 * lane + odd;
+        if (e + 1 < min(cols, 64))
+            *reinterpret_cast<uint32_t*>(c + e) = x;
+        else if (e < cols)
+            c[e] = (uint16_t)x;
+        if (odd && lane == 0 && cols > 0) c[0] = (uint16_t)w;
     }
 }
 
 // ----------------------------------------------------------------- 256 x 256 tiles of a CTA pair
 
 constexpr int kGM = 128, kGN = 256;  // a CTA's rows of a tile, and the tile's columns
-constexpr int kGStages = 6;
+constexpr int kGStages = 5;
 constexpr uint32_t kGA = kGM * kGK, kGB = kGN / 2 * kGK;  // a CTA loads its rows of A and half of B's
 constexpr int kGThreads = 384;
-constexpr uint32_t kGOut = 32 * 64;  // an epilogue warp's output stage: 32 rows x 64 bytes
-constexpr size_t kGSmem =
-    1024 + (size_t)kGStages * (kGA + kGB) + kScaleStages * kGN * 4 + 8 * kGOut + 1024;
+constexpr uint32_t kGOut = 32 * 128;  // an epilogue warp's output stage: 32 rows x 128 bytes
+constexpr int kRowScales = 8;         // K groups whose scales an epilogue thread holds or has under way
+constexpr size_t kGSmem = 1024 + (size_t)kGStages * (kGA + kGB) + 8 * kGOut + kRowScales * 256 * sizeof(float2) +
+                          kScaleStages * kGN * 4 + 1024;
+struct GemmBars {
+    PairBars<kGStages> pair;
+    ScaleBars sc;
+};
 static_assert(sizeof(GemmBars) <= 1024, "barriers fit their kilobyte");
+static_assert(kGSmem <= 232448, "shared memory of a CTA");
 
 // Tile t of the persistent order: bands of `band` M tiles, and within a band
 // all M tiles of one N tile before the next, so the tiles in flight share a
@@ -283,7 +316,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     unsigned char* sA = smem;
     unsigned char* sB = smem + kGStages * kGA;
     unsigned char* sOut = sB + kGStages * kGB;
-    float* scales = reinterpret_cast<float*>(sOut + 8 * kGOut);
+    float2* sRow = reinterpret_cast<float2*>(sOut + 8 * kGOut);  // [kRowScales][epilogue thread]
+    float* scales = reinterpret_cast<float*>(sRow + kRowScales * 256);
     auto* all = reinterpret_cast<GemmBars*>(scales + kScaleStages * kGN);
     PairBars<kGStages>* bars = &all->pair;
     ScaleBars* sbars = &all->sc;
@@ -296,7 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     int* ab = &bars->abort_flag;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {
             // ------------------------------------------------ TMA producer: counted on the even CTA's barriers
             const bool one = elect_one();
@@ -373,51 +407,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------ epilogue: scale and sum in registers
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int quarter = warp & 3, part = (warp - 4) >> 2;  // 32 rows, and 128 of the tile's columns
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         unsigned char* out = sOut + (warp - 4) * kGOut;
         const uint32_t done = mapa_shared(smem_u32(&bars->tempty[0]), 0);
         Ring acc, sc;
         bool ok = first < tiles, ready = false;
-        // This row's scale (and, for block scales, the block's) of two K groups, and of the two after them under way;
-        // the first ones of a tile are loaded before the previous tile's result is stored.  A register that a load
-        // still owes is touched, and so waited for, two groups later only.
+        // This row's scale and (for block scales) the block's, copied into shared memory kRowScales - 1 K groups
+        // ahead, the first ones of a tile before the previous one's result is stored.  Each thread reads only what it
+        // copied, so its own wait_group is all the synchronisation; held in registers the loads were waited for early.
         int mb = 0, nb = 0;
         const float *pa = nullptr, *pb = nullptr;
-        float sa[4], sb[4];
-        auto load_scales = [&](int i, int kb) {
-            const bool in = kb < p.KB;
-            sa[i] = in ? __ldg(pa) : 0.f;
-            sb[i] = !BROWS && in ? __ldg(pb) : 0.f;
-            pa += p.M;
-            pb += p.nsb;
+        float2* mine = sRow + (warp - 4) * 32 + lane;
+        auto copy_scales = [&](int kb) {
+            if (kb < p.KB) {
+                const uint32_t dst = smem_u32(mine + (kb % kRowScales) * 256);
+                cp_async4(dst, pa, true);
+                if (!BROWS) cp_async4(dst + 4, pb, true);
+                pa += p.M;
+                pb += p.nsb;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
         auto first_scales = [&](int t) {
             tile_of(p, t, mb, nb);
             pa = p.sa + min((2 * mb + rank) * kGM + quarter * 32 + lane, p.M - 1);
             pb = p.sb + min(nb * 2 + part, p.nsb - 1);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) load_scales(2 + i, i);
+            for (int i = 0; i < kRowScales - 1; ++i) copy_scales(i);
         };
         if (ok) first_scales(first);
         for (int t = first; ok && t < tiles; t += step) {
             float2 sum[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
-            // One K group: false when a wait expired.
-            auto group = [&](float a, float ab2) {
+            for (int kb = 0; kb < p.KB; ++kb) {
                 bool sready = true;
                 if (BROWS) sready = mbar_try_wait(smem_u32(&sbars->full[sc.slot]), sc.phase);
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRowScales - 2) : "memory");
+                const float2 fs = mine[(kb % kRowScales) * 256];
+                copy_scales(kb + kRowScales - 1);
                 if (!ready) ok = pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w);
                 if (!sready) ok = ok && pipe_wait(ab, smem_u32(&sbars->full[sc.slot]), sc.phase, p.w);
                 ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) return;
+                if (!ok) break;
                 tc_fence_after();
                 // 32 columns at a time, the next 32 under way while these are summed
                 const uint32_t t0 = tmem + lane_base + (uint32_t)(acc.slot * kGN + part * 128);
                 uint32_t v[2][32];
                 tmem_ld32_issue(t0, v[0]);
+                const float f1 = BROWS ? fs.x : __fmul_rn(fs.x, fs.y);
                 const float* s = scales + sc.slot * kGN + part * 128;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -436,8 +476,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                     for (int i = 0; i < 16; ++i) {
                         const float2 d = make_float2(__uint_as_float(v[c & 1][2 * i]),
                                                      __uint_as_float(v[c & 1][2 * i + 1]));
-                        float2 f = make_float2(ab2, ab2);
-                        if (BROWS) f = fmul2(make_float2(a, a), *reinterpret_cast<const float2*>(s + c * 32 + 2 * i));
+                        float2 f = make_float2(f1, f1);
+                        if (BROWS) f = fmul2(f, *reinterpret_cast<const float2*>(s + c * 32 + 2 * i));
                         sum[c * 16 + i] = ffma2(d, f, sum[c * 16 + i]);
                     }
                 }
@@ -446,13 +486,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                     if (lane == 0) mbar_arrive(smem_u32(&sbars->empty[sc.slot]));
                     sc.next(kScaleStages);
                 }
-            };
-            for (int kb = 0; ok && kb < p.KB; kb += 2) {
-                sa[0] = sa[2], sa[1] = sa[3], sb[0] = sb[2], sb[1] = sb[3];
-                load_scales(2, kb + 2);
-                load_scales(3, kb + 3);
-                group(sa[0], __fmul_rn(sa[0], sb[0]));
-                if (ok && kb + 1 < p.KB) group(sa[1], __fmul_rn(sa[1], sb[1]));
             }
             if (!ok) break;
             const int64_t row0 = (int64_t)(2 * mb + rank) * kGM + quarter * 32;
@@ -460,13 +493,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             if (t + step < tiles) first_scales(t + step);
             if (p.c_f32) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) store_chunk<true>(p, out, lane, row0, col0 + q * 16, sum + q * 8);
+                for (int q = 0; q < 4; ++q) store_chunk<true>(p, out, lane, row0, col0 + q * 32, sum + q * 16);
             } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) store_chunk<false>(p, out, lane, row0, col0 + q * 32, sum + q * 16);
+                for (int q = 0; q < 2; ++q) store_chunk<false>(p, out, lane, row0, col0 + q * 64, sum + q * 32);
             }
         }
     }
+    cp_async_wait_all();  // an epilogue thread that gave up may have scales under way
     pair_end(tmem, warp);
 }
 
