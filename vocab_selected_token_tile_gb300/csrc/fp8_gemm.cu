@@ -221,6 +221,7 @@ __device__ __forceinline__ void store_chunk(const Gemm8Params& p, unsigned char*
     }
     __syncwarp();
     const int rows = (int)min((int64_t)32, p.M - row0), cols = min(8 * kPer, p.N - col0);
+    if (cols <= 0) return;
     if (p.vec) {
         const int j = lane & 7, left = cols - j * kPer;
         if (left <= 0) return;
@@ -252,27 +253,53 @@ __device__ __forceinline__ void store_chunk(const Gemm8Params& p, unsigned char*
         return;
     }
     // rows off the 16-byte grid: 4 bytes a lane, a row an instruction
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-        const uint32_t w =
-            *reinterpret_cast<const uint32_t*>(out + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
-        const int64_t at = (row0 + r) * p.ldc + col0;
-        if (F32) {
-            float* c = static_cast<float*>(p.c) + at + lane;
-            if (lane < cols) *c = p.accumulate ? *c + __uint_as_float(w) : __uint_as_float(w);
-            continue;
+    auto word = [&](int r, int l) {
+        return *reinterpret_cast<const uint32_t*>(out + r * 128 + (((l >> 2) ^ (r & 7)) * 16) + (l & 3) * 4);
+    };
+    if (F32) {
+        float* c = static_cast<float*>(p.c) + row0 * p.ldc + col0 + lane;
+        if (lane >= cols) return;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r, c += p.ldc)
+            *c = p.accumulate ? *c + __uint_as_float(word(r, lane)) : __uint_as_float(word(r, lane));
+        return;
+    }
+    uint16_t* c0 = static_cast<uint16_t*>(p.c) + row0 * p.ldc + col0;
+    if (cols < 64 || rows < 32) {
+        for (int r = 0; r < rows; ++r)
+            for (int e = lane; e < cols; e += 32)
+                c0[r * p.ldc + e] = (uint16_t)(word(r, e >> 1) >> (16 * (e & 1)));
+        return;
+    }
+    // The even rows, then the odd ones: all of a kind start on a word, or between words, where their words are
+    // shifted by one column, and the first and the last column go alone.
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+        const unsigned char *at[4], *up[4];  // of rows kind + 2 k, and every eighth row after
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = kind + 2 * k, l = (lane + 1) & 31;
+            at[k] = out + r * 128 + (((lane >> 2) ^ r) * 16) + (lane & 3) * 4;
+            up[k] = out + r * 128 + (((l >> 2) ^ r) * 16) + (l & 3) * 4;
         }
-        // a BF16 row that starts between words: the words are shifted by one column, and its first column goes alone
-        uint16_t* c = static_cast<uint16_t*>(p.c) + at;
-        const int odd = (int)((reinterpret_cast<uintptr_t>(c) >> 1) & 1);
-        const uint32_t up = __shfl_down_sync(0xFFFFFFFFu, w, 1);
-        const uint32_t x = odd ? __funnelshift_r(w, up, 16) : w;
-        const int e = 2 * lane + odd;
-        if (e + 1 < min(cols, 64))
-            *reinterpret_cast<uint32_t*>(c + e) = x;
-        else if (e < cols)
-            c[e] = (uint16_t)x;
-        if (odd && lane == 0 && cols > 0) c[0] = (uint16_t)w;
+        uint16_t* c = c0 + kind * p.ldc;
+        if ((reinterpret_cast<uintptr_t>(c) & 2) == 0) {
+            uint32_t* d = reinterpret_cast<uint32_t*>(c) + lane;
+#pragma unroll
+            for (int i = 0; i < 16; ++i, d += p.ldc)
+                *d = *reinterpret_cast<const uint32_t*>(at[i & 3] + (i >> 2) * 1024);
+        } else {
+            uint16_t* d = c + 2 * lane + 1;
+            uint16_t* alone = c + (lane == 0 ? 0 : 63);
+#pragma unroll
+            for (int i = 0; i < 16; ++i, d += 2 * p.ldc, alone += 2 * p.ldc) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(at[i & 3] + (i >> 2) * 1024);
+                const uint32_t x =
+                    __funnelshift_r(w, *reinterpret_cast<const uint32_t*>(up[i & 3] + (i >> 2) * 1024), 16);
+                if (lane < 31) *reinterpret_cast<uint32_t*>(d) = x;
+                if (lane == 0 || lane == 31) *alone = (uint16_t)(lane == 0 ? w : w >> 16);
+            }
+        }
     }
 }
 
@@ -283,15 +310,21 @@ constexpr int kGStages = 5;
 constexpr uint32_t kGA = kGM * kGK, kGB = kGN / 2 * kGK;  // a CTA loads its rows of A and half of B's
 constexpr int kGThreads = 384;
 constexpr uint32_t kGOut = 32 * 128;  // an epilogue warp's output stage: 32 rows x 128 bytes
-constexpr int kRowScales = 8;         // K groups whose scales an epilogue thread holds or has under way
-constexpr size_t kGSmem = 1024 + (size_t)kGStages * (kGA + kGB) + 8 * kGOut + kRowScales * 256 * sizeof(float2) +
-                          kScaleStages * kGN * 4 + 1024;
+// The scales of kGroups K groups at a time, in two slots that warp 2 fills: A's 128 rows', then B's (256 rows', or
+// the tile's two blocks').  By the group, their barriers' latencies were in every group's path; copied by each
+// epilogue thread for itself they cost 26 us of 335.
+constexpr int kGroups = 8, kGSlots = 2;
+template <bool BROWS>
+constexpr int kGScales = kGM + (BROWS ? kGN : 4);
+template <bool BROWS>
+constexpr size_t kGSmem = 1024 + (size_t)kGStages * (kGA + kGB) + 8 * kGOut +
+                          (size_t)kGSlots * kGroups * kGScales<BROWS> * 4 + 1024;
 struct GemmBars {
     PairBars<kGStages> pair;
-    ScaleBars sc;
+    uint64_t sfull[kGSlots], sempty[kGSlots];
 };
 static_assert(sizeof(GemmBars) <= 1024, "barriers fit their kilobyte");
-static_assert(kGSmem <= 232448, "shared memory of a CTA");
+static_assert(kGSmem<true> <= 232448, "shared memory of a CTA");
 
 // Tile t of the persistent order: bands of `band` M tiles, and within a band
 // all M tiles of one N tile before the next, so the tiles in flight share a
@@ -316,16 +349,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     unsigned char* sA = smem;
     unsigned char* sB = smem + kGStages * kGA;
     unsigned char* sOut = sB + kGStages * kGB;
-    float2* sRow = reinterpret_cast<float2*>(sOut + 8 * kGOut);  // [kRowScales][epilogue thread]
-    float* scales = reinterpret_cast<float*>(sRow + kRowScales * 256);
-    auto* all = reinterpret_cast<GemmBars*>(scales + kScaleStages * kGN);
+    float* scales = reinterpret_cast<float*>(sOut + 8 * kGOut);
+    auto* all = reinterpret_cast<GemmBars*>(scales + kGSlots * kGroups * kGScales<BROWS>);
     PairBars<kGStages>* bars = &all->pair;
-    ScaleBars* sbars = &all->sc;
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
     const int tiles = p.MB * p.NB, first = (int)blockIdx.x / 2, step = (int)gridDim.x / 2;
 
-    if (threadIdx.x == 0) init_scales(sbars, 8);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kGSlots; ++i) {
+            mbar_init(smem_u32(&all->sfull[i]), 32);
+            mbar_init(smem_u32(&all->sempty[i]), 8);
+        }
+    }
     const uint32_t tmem = pair_begin(bars, warp, 8);
     int* ab = &bars->abort_flag;
 
@@ -381,25 +417,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 }
             }
             pair_drain_mmas(bars, one, p.w);
-        } else if (warp == 2 && BROWS) {
-            // ------------------------------------------------ B's row scales, for all epilogue warps
+        } else if (warp == 2) {
+            // ------------------------------------------------ scales
             Ring r;
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
                 int mb, nb;
                 tile_of(p, t, mb, nb);
-                for (int kb = 0; kb < p.KB; ++kb) {
-                    ok = __all_sync(0xFFFFFFFFu, pipe_wait(ab, smem_u32(&sbars->empty[r.slot]), r.phase ^ 1u, p.w));
+                const int row = (2 * mb + rank) * kGM + lane, col = nb * kGN + lane;
+                for (int k0 = 0; k0 < p.KB; k0 += kGroups) {
+                    ok = __all_sync(0xFFFFFFFFu, pipe_wait(ab, smem_u32(&all->sempty[r.slot]), r.phase ^ 1u, p.w));
                     if (!ok) break;
-                    const uint32_t dst = smem_u32(scales + r.slot * kGN);
-                    const float* b = p.sb + (int64_t)kb * p.nsb;
+                    uint32_t dst = smem_u32(scales + r.slot * kGroups * kGScales<BROWS>) + lane * 4;
+                    const float *a = p.sa + (int64_t)k0 * p.M, *b = p.sb + (int64_t)k0 * p.nsb;
+                    for (int kb = k0; kb < min(k0 + kGroups, p.KB); ++kb) {
 #pragma unroll
-                    for (int i = lane; i < kGN; i += 32) {
-                        const int row = nb * kGN + i;
-                        cp_async4(dst + i * 4, b + (row < p.N ? row : 0), row < p.N);
+                        for (int i = 0; i < kGM; i += 32) cp_async4(dst + i * 4, a + (row + i < p.M ? row + i : 0), row + i < p.M);
+                        if (BROWS) {
+#pragma unroll
+                            for (int i = 0; i < kGN; i += 32)
+                                cp_async4(dst + (kGM + i) * 4, b + (col + i < p.N ? col + i : 0), col + i < p.N);
+                        } else if (lane < 2) {
+                            const int blk = nb * 2 + lane;
+                            cp_async4(dst + kGM * 4, b + (blk < p.nsb ? blk : 0), blk < p.nsb);
+                        }
+                        dst += kGScales<BROWS> * 4;
+                        a += p.M;
+                        b += p.nsb;
                     }
-                    cp_async_arrive(smem_u32(&sbars->full[r.slot]));
-                    r.next(kScaleStages);
+                    cp_async_arrive(smem_u32(&all->sfull[r.slot]));
+                    r.next(kGSlots);
                 }
             }
             cp_async_wait_all();
@@ -414,42 +461,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         const uint32_t done = mapa_shared(smem_u32(&bars->tempty[0]), 0);
         Ring acc, sc;
         bool ok = first < tiles, ready = false;
-        // This row's scale and (for block scales) the block's, copied into shared memory kRowScales - 1 K groups
-        // ahead, the first ones of a tile before the previous one's result is stored.  Each thread reads only what it
-        // copied, so its own wait_group is all the synchronisation; held in registers the loads were waited for early.
-        int mb = 0, nb = 0;
-        const float *pa = nullptr, *pb = nullptr;
-        float2* mine = sRow + (warp - 4) * 32 + lane;
-        auto copy_scales = [&](int kb) {
-            if (kb < p.KB) {
-                const uint32_t dst = smem_u32(mine + (kb % kRowScales) * 256);
-                cp_async4(dst, pa, true);
-                if (!BROWS) cp_async4(dst + 4, pb, true);
-                pa += p.M;
-                pb += p.nsb;
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        auto first_scales = [&](int t) {
-            tile_of(p, t, mb, nb);
-            pa = p.sa + min((2 * mb + rank) * kGM + quarter * 32 + lane, p.M - 1);
-            pb = p.sb + min(nb * 2 + part, p.nsb - 1);
-#pragma unroll
-            for (int i = 0; i < kRowScales - 1; ++i) copy_scales(i);
-        };
-        if (ok) first_scales(first);
         for (int t = first; ok && t < tiles; t += step) {
             float2 sum[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
+            const float* s = nullptr;
             for (int kb = 0; kb < p.KB; ++kb) {
-                bool sready = true;
-                if (BROWS) sready = mbar_try_wait(smem_u32(&sbars->full[sc.slot]), sc.phase);
-                asm volatile("cp.async.wait_group %0;" ::"n"(kRowScales - 2) : "memory");
-                const float2 fs = mine[(kb % kRowScales) * 256];
-                copy_scales(kb + kRowScales - 1);
-                if (!ready) ok = pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w);
-                if (!sready) ok = ok && pipe_wait(ab, smem_u32(&sbars->full[sc.slot]), sc.phase, p.w);
+                if (kb % kGroups == 0) {
+                    ok = pipe_wait(ab, smem_u32(&all->sfull[sc.slot]), sc.phase, p.w);
+                    s = scales + sc.slot * kGroups * kGScales<BROWS>;
+                }
+                const float f0 = s[quarter * 32 + lane];
+                const float f1 = BROWS ? f0 : __fmul_rn(f0, s[kGM + part]);
+                if (!ready) ok = ok && pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -457,8 +481,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 const uint32_t t0 = tmem + lane_base + (uint32_t)(acc.slot * kGN + part * 128);
                 uint32_t v[2][32];
                 tmem_ld32_issue(t0, v[0]);
-                const float f1 = BROWS ? fs.x : __fmul_rn(fs.x, fs.y);
-                const float* s = scales + sc.slot * kGN + part * 128;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     tmem_wait32(v[c & 1]);
@@ -477,20 +499,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                         const float2 d = make_float2(__uint_as_float(v[c & 1][2 * i]),
                                                      __uint_as_float(v[c & 1][2 * i + 1]));
                         float2 f = make_float2(f1, f1);
-                        if (BROWS) f = fmul2(f, *reinterpret_cast<const float2*>(s + c * 32 + 2 * i));
+                        if (BROWS)
+                            f = fmul2(f, *reinterpret_cast<const float2*>(s + kGM + part * 128 + c * 32 + 2 * i));
                         sum[c * 16 + i] = ffma2(d, f, sum[c * 16 + i]);
                     }
                 }
-                if (BROWS) {
+                s += kGScales<BROWS>;
+                if (kb % kGroups == kGroups - 1 || kb == p.KB - 1) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sbars->empty[sc.slot]));
-                    sc.next(kScaleStages);
+                    if (lane == 0) mbar_arrive(smem_u32(&all->sempty[sc.slot]));
+                    sc.next(kGSlots);
                 }
             }
             if (!ok) break;
+            int mb, nb;
+            tile_of(p, t, mb, nb);
             const int64_t row0 = (int64_t)(2 * mb + rank) * kGM + quarter * 32;
             const int col0 = nb * kGN + part * 128;
-            if (t + step < tiles) first_scales(t + step);
             if (p.c_f32) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) store_chunk<true>(p, out, lane, row0, col0 + q * 32, sum + q * 16);
@@ -500,7 +525,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             }
         }
     }
-    cp_async_wait_all();  // an epilogue thread that gave up may have scales under way
     pair_end(tmem, warp);
 }
 
@@ -750,10 +774,10 @@ rlk_status allow_smem(K kernel, size_t bytes) {
 
 template <bool BROWS>
 rlk_status launch_gemm(const Gemm8Params& p, const CUtensorMap& a, const CUtensorMap& b, int sms, cudaStream_t st) {
-    const rlk_status s = allow_smem(gemm_kernel<BROWS>, kGSmem);
+    const rlk_status s = allow_smem(gemm_kernel<BROWS>, kGSmem<BROWS>);
     if (s != RLK_OK) return s;
     const int tiles = p.MB * p.NB, pairs = sms / 2;
-    gemm_kernel<BROWS><<<2 * (tiles < pairs ? tiles : pairs), kGThreads, kGSmem, st>>>(a, b, p);
+    gemm_kernel<BROWS><<<2 * (tiles < pairs ? tiles : pairs), kGThreads, kGSmem<BROWS>, st>>>(a, b, p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product launch", e);
 }
