@@ -94,8 +94,9 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
                    "+r"(r[15])::"memory");
 }
 
-// The same for 32 columns.
-__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
+// 32 columns of a warp's 32 lanes, a lane's row a thread; the values are there
+// only after tmem_wait32.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
         "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -106,7 +107,25 @@ __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait32(uint32_t* r) {
+// The same as fragments: with t the thread's lane, v[16 h
+// + 4 j + 2 i + e] is row 16 h + 8 i + t / 4, column 8 j + 2 (t mod 4) + e.  A
+// thread then needs 4 rows' scales and 8 columns' for its 32 values, where a
+// row a thread would need all 32 columns' (and shared memory returns 128 bytes
+// of registers a clock); the load itself is the slower one of the two.
+__device__ __forceinline__ void tmem_ld_frag_issue(uint32_t taddr, uint32_t (&v)[32]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t* r = v + 16 * h;
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+            "%14, %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr + ((uint32_t)(16 * h) << 16))
+            : "memory");
+    }
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
@@ -114,6 +133,7 @@ __device__ __forceinline__ void tmem_wait32(uint32_t* r) {
                    "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
                    "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
+
 // A 4-byte asynchronous copy, zero where `ok` is false (nothing is read then).
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
@@ -196,28 +216,48 @@ __device__ __forceinline__ void store_piece(uint16_t* c, uint4 w, int cols) {
         if (e < cols) c[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
 }
 
-// A warp's 32 rows x 128 bytes of C (32 FP32 or 64 BF16 columns; a lane holds
-// its row's) through shared memory, so that a row's 128 bytes leave in one
-// piece: 16 bytes a lane straight from the registers, 32 rows an instruction,
-// took 10,700 clocks a 128 x 256 tile, a third of the product's time at K =
-// 4096.  16-byte piece j of row r is kept at j ^ (r mod 8), which spreads both
-// directions over the banks.
-template <bool F32>
+// A warp's 32 rows x 128 bytes of C (32 FP32 or 64 BF16 columns) through shared
+// memory, so that a row's 128 bytes leave in one piece: 16 bytes a lane
+// straight from the registers, 32 rows an instruction, took 10,700 clocks a 128
+// x 256 tile, a third of the product's time at K = 4096.  16-byte piece j of
+// row r is kept at j ^ turn(r), which spreads both directions over the banks.
+// v: the lane's row (pairs of columns), or with FRAG, of each 32 columns, 4 rows
+// (t / 4 and 8, 16, 24 after) x 4 pairs (2 (t mod 4) and 8, 16, 24 after).
+template <bool F32, bool FRAG>
 __device__ __forceinline__ void store_chunk(const Gemm8Params& p, unsigned char* out, int lane, int64_t row0, int col0,
                                             const float2* v) {
     constexpr int kPer = F32 ? 4 : 8;  // elements of 16 bytes
+    auto turn = [](int r) { return F32 && FRAG ? 2 * (r & 3) : r & 7; };
     __syncwarp();
+    if (FRAG) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        uint4 w;
-        if (F32)
-            w = make_uint4(__float_as_uint(v[2 * j].x), __float_as_uint(v[2 * j].y), __float_as_uint(v[2 * j + 1].x),
-                           __float_as_uint(v[2 * j + 1].y));
-        else
-            w = make_uint4(pack_bf16x2_rn(v[4 * j].x, v[4 * j].y), pack_bf16x2_rn(v[4 * j + 1].x, v[4 * j + 1].y),
-                           pack_bf16x2_rn(v[4 * j + 2].x, v[4 * j + 2].y),
-                           pack_bf16x2_rn(v[4 * j + 3].x, v[4 * j + 3].y));
-        *reinterpret_cast<uint4*>(out + lane * 128 + ((j ^ (lane & 7)) * 16)) = w;
+        for (int q = 0; q < (F32 ? 1 : 2); ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = v[q * 16 + i * 4 + j];
+                    const int r = i * 8 + (lane >> 2);
+                    if (F32)
+                        *reinterpret_cast<float2*>(out + r * 128 + (((2 * j + ((lane & 3) >> 1)) ^ turn(r)) * 16) +
+                                                   (lane & 1) * 8) = x;
+                    else
+                        *reinterpret_cast<uint32_t*>(out + r * 128 + (((q * 4 + j) ^ turn(r)) * 16) +
+                                                     (lane & 3) * 4) = pack_bf16x2_rn(x.x, x.y);
+                }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint4 w;
+            if (F32)
+                w = make_uint4(__float_as_uint(v[2 * j].x), __float_as_uint(v[2 * j].y),
+                               __float_as_uint(v[2 * j + 1].x), __float_as_uint(v[2 * j + 1].y));
+            else
+                w = make_uint4(pack_bf16x2_rn(v[4 * j].x, v[4 * j].y), pack_bf16x2_rn(v[4 * j + 1].x, v[4 * j + 1].y),
+                               pack_bf16x2_rn(v[4 * j + 2].x, v[4 * j + 2].y),
+                               pack_bf16x2_rn(v[4 * j + 3].x, v[4 * j + 3].y));
+            *reinterpret_cast<uint4*>(out + lane * 128 + ((j ^ turn(lane)) * 16)) = w;
+        }
     }
     __syncwarp();
     const int rows = (int)min((int64_t)32, p.M - row0), cols = min(8 * kPer, p.N - col0);
@@ -229,7 +269,7 @@ __device__ __forceinline__ void store_chunk(const Gemm8Params& p, unsigned char*
         for (int i = 0; i < 8; ++i) {
             const int r = i * 4 + (lane >> 3);
             if (r >= rows) break;
-            const uint4 w = *reinterpret_cast<const uint4*>(out + r * 128 + ((j ^ (r & 7)) * 16));
+            const uint4 w = *reinterpret_cast<const uint4*>(out + r * 128 + ((j ^ turn(r)) * 16));
             const int64_t at = (row0 + r) * p.ldc + col0 + j * kPer;
             if (!F32) {
                 store_piece(static_cast<uint16_t*>(p.c) + at, w, left);
@@ -254,7 +294,7 @@ __device__ __forceinline__ void store_chunk(const Gemm8Params& p, unsigned char*
     }
     // rows off the 16-byte grid: 4 bytes a lane, a row an instruction
     auto word = [&](int r, int l) {
-        return *reinterpret_cast<const uint32_t*>(out + r * 128 + (((l >> 2) ^ (r & 7)) * 16) + (l & 3) * 4);
+        return *reinterpret_cast<const uint32_t*>(out + r * 128 + (((l >> 2) ^ turn(r)) * 16) + (l & 3) * 4);
     };
     if (F32) {
         float* c = static_cast<float*>(p.c) + row0 * p.ldc + col0 + lane;
@@ -471,8 +511,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                     ok = pipe_wait(ab, smem_u32(&all->sfull[sc.slot]), sc.phase, p.w);
                     s = scales + sc.slot * kGroups * kGScales<BROWS>;
                 }
-                const float f0 = s[quarter * 32 + lane];
-                const float f1 = BROWS ? f0 : __fmul_rn(f0, s[kGM + part]);
+                // of this thread's row, times the block's; or of its fragments' four rows
+                float f[4];
+                if (BROWS) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) f[i] = s[quarter * 32 + i * 8 + (lane >> 2)];
+                } else {
+                    f[0] = __fmul_rn(s[quarter * 32 + lane], s[kGM + part]);
+                }
                 if (!ready) ok = ok && pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
@@ -480,12 +526,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 // 32 columns at a time, the next 32 under way while these are summed
                 const uint32_t t0 = tmem + lane_base + (uint32_t)(acc.slot * kGN + part * 128);
                 uint32_t v[2][32];
-                tmem_ld32_issue(t0, v[0]);
+                BROWS ? tmem_ld_frag_issue(t0, v[0]) : tmem_ld32_issue(t0, v[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     tmem_wait32(v[c & 1]);
                     if (c < 3) {
-                        tmem_ld32_issue(t0 + (c + 1) * 32, v[(c + 1) & 1]);
+                        BROWS ? tmem_ld_frag_issue(t0 + (c + 1) * 32, v[(c + 1) & 1])
+                              : tmem_ld32_issue(t0 + (c + 1) * 32, v[(c + 1) & 1]);
                     } else {
                         // the accumulator is free again; ask for the next one before this one's last sums
                         tc_fence_before();
@@ -494,14 +541,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                         acc.next(2);
                         ready = mbar_try_wait(smem_u32(&bars->tfull[acc.slot]), acc.phase);
                     }
+                    if (BROWS) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 d = make_float2(__uint_as_float(v[c & 1][2 * i]),
-                                                     __uint_as_float(v[c & 1][2 * i + 1]));
-                        float2 f = make_float2(f1, f1);
-                        if (BROWS)
-                            f = fmul2(f, *reinterpret_cast<const float2*>(s + kGM + part * 128 + c * 32 + 2 * i));
-                        sum[c * 16 + i] = ffma2(d, f, sum[c * 16 + i]);
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 sb =
+                                *reinterpret_cast<const float2*>(s + kGM + part * 128 + c * 32 + j * 8 + 2 * (lane & 3));
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int at = (i >> 1) * 16 + j * 4 + (i & 1) * 2;
+                                sum[c * 16 + i * 4 + j] = ffma2(make_float2(__uint_as_float(v[c & 1][at]),
+                                                                            __uint_as_float(v[c & 1][at + 1])),
+                                                                fmul2(make_float2(f[i], f[i]), sb),
+                                                                sum[c * 16 + i * 4 + j]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            sum[c * 16 + i] = ffma2(make_float2(__uint_as_float(v[c & 1][2 * i]),
+                                                                __uint_as_float(v[c & 1][2 * i + 1])),
+                                                    make_float2(f[0], f[0]), sum[c * 16 + i]);
                     }
                 }
                 s += kGScales<BROWS>;
@@ -518,10 +577,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             const int col0 = nb * kGN + part * 128;
             if (p.c_f32) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) store_chunk<true>(p, out, lane, row0, col0 + q * 32, sum + q * 16);
+                for (int q = 0; q < 4; ++q) store_chunk<true, BROWS>(p, out, lane, row0, col0 + q * 32, sum + q * 16);
             } else {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) store_chunk<false>(p, out, lane, row0, col0 + q * 64, sum + q * 32);
+                for (int q = 0; q < 2; ++q) store_chunk<false, BROWS>(p, out, lane, row0, col0 + q * 64, sum + q * 32);
             }
         }
     }
