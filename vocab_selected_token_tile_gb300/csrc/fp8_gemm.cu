@@ -25,7 +25,7 @@
 // warpgroup gives registers away with setmaxnreg).
 //
 // skinny_kernel, for few rows of A: B's rows take the 128 lanes and A's rows
-// the accumulator's columns (16, 32, 64 or 128), so a single token streams the
+// the accumulator's columns (16, 32 or 64), so a single token streams the
 // weight once and wastes no more than 15 columns.  Bound: HBM, N K bytes.  Two
 // CTAs per SM keep loads in flight across each other's start and end.  Where N
 // / 128 tiles are fewer than the SMs can hold, a cluster of 2, 4 or 8 CTAs
@@ -39,6 +39,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
 #include <string>
 
 #include "rlk_gemm.cuh"
@@ -144,6 +145,14 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -366,6 +375,10 @@ struct GemmBars {
 static_assert(sizeof(GemmBars) <= 1024, "barriers fit their kilobyte");
 static_assert(kGSmem<true> <= 232448, "shared memory of a CTA");
 
+constexpr int kGSplit = 4;  // pairs that share a tile at most: a cluster of eight CTAs
+constexpr int kRedPitch = kGN + 4;
+static_assert((size_t)kGM * kRedPitch * 4 <= (size_t)kGStages * (kGA + kGB), "the partial sums fit the ring");
+
 // Tile t of the persistent order: bands of `band` M tiles, and within a band
 // all M tiles of one N tile before the next, so the tiles in flight share a
 // few N tiles of B and the band's rows of A, which L2 holds.
@@ -378,10 +391,12 @@ __device__ __forceinline__ void tile_of(const Gemm8Params& p, int t, int& mb, in
     mb = b * p.band + r % width;
 }
 
+// split: pairs of a cluster that share a tile, each with a part of the K groups
+// (1: the pair's tiles are its own, one after the other).
 template <bool BROWS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
+__global__ void __launch_bounds__(kGThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const __grid_constant__ Gemm8Params p) {
+                const __grid_constant__ Gemm8Params p, const int split) {
     extern __shared__ unsigned char smem_raw[];
     // The same offset in both CTAs (their dynamic shared memory starts alike): descriptors name one offset.
     unsigned char* smem =
@@ -393,8 +408,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
     auto* all = reinterpret_cast<GemmBars*>(scales + kGSlots * kGroups * kGScales<BROWS>);
     PairBars<kGStages>* bars = &all->pair;
     const int warp = warp_index(), lane = threadIdx.x & 31;
-    const int rank = (int)cluster_ctarank();
-    const int tiles = p.MB * p.NB, first = (int)blockIdx.x / 2, step = (int)gridDim.x / 2;
+    const int place = (int)cluster_ctarank(), rank = place & 1, leader = place & ~1;
+    const uint16_t both = (uint16_t)(3 << leader);
+    const int tiles = p.MB * p.NB, first = (int)blockIdx.x / (2 * split), step = (int)gridDim.x / (2 * split);
+    const int k0 = (int)((int64_t)p.KB * (leader / 2) / split), k1 = (int)((int64_t)p.KB * (leader / 2 + 1) / split);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kGSlots; ++i) {
@@ -410,7 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         if (warp == 0) {
             // ------------------------------------------------ TMA producer: counted on the even CTA's barriers
             const bool one = elect_one();
-            const uint32_t full0 = mapa_shared(smem_u32(&bars->full[0]), 0);
+            const uint32_t full0 = mapa_shared(smem_u32(&bars->full[0]), (uint32_t)leader);
             Ring r;
             int issued = 0;
             bool ok = true;
@@ -418,12 +435,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 int mb, nb;
                 tile_of(p, t, mb, nb);
                 const int a_row = (2 * mb + rank) * kGM, b_row = nb * kGN + rank * (kGN / 2);
-                for (int kb = 0; kb < p.KB; ++kb) {
+                // a CTA without a row of its own loads none: its rows of the accumulator are not used
+                const bool mine = a_row < p.M;
+                const uint32_t bytes = 2 * kGB + ((2 * mb + 1) * kGM < p.M ? 2 : 1) * kGA;
+                for (int kb = k0; kb < k1; ++kb) {
                     if (!(ok = pipe_wait(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                     if (one) {
                         const uint32_t fb = full0 + r.slot * 8;
-                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars->full[r.slot]), 2 * (kGA + kGB));
-                        tma_load_2d_pair(smem_u32(sA + r.slot * kGA), &tmA, kb * kGK, a_row, fb);
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars->full[r.slot]), bytes);
+                        if (mine) tma_load_2d_pair(smem_u32(sA + r.slot * kGA), &tmA, kb * kGK, a_row, fb);
                         tma_load_2d_pair(smem_u32(sB + r.slot * kGB), &tmB, kb * kGK, b_row, fb);
                     }
                     issued = min(issued + 1, kGStages);
@@ -439,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             Ring r, acc;
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
-                for (int kb = 0; kb < p.KB; ++kb) {
+                for (int kb = k0; kb < k1; ++kb) {
                     if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
                     if (!(ok = pipe_wait(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
                     tc_fence_after();
@@ -448,15 +468,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                         for (int kk = 0; kk < 4; ++kk)
                             umma_e4m3_pair(tmem + (uint32_t)(acc.slot * kGN), da + ((r.slot * kGA + kk * 32) >> 4),
                                            db + ((r.slot * kGB + kk * 32) >> 4), idesc, kk != 0);
-                        umma_commit_pair(smem_u32(&bars->tfull[acc.slot]));
-                        umma_commit_pair(smem_u32(&bars->empty[r.slot]));
+                        umma_commit_pair(smem_u32(&bars->tfull[acc.slot]), both);
+                        umma_commit_pair(smem_u32(&bars->empty[r.slot]), both);
                     }
                     __syncwarp();
                     r.next(kGStages);
                     acc.next(2);
                 }
             }
-            pair_drain_mmas(bars, one, p.w);
+            pair_drain_mmas(bars, one, p.w, both);
         } else if (warp == 2) {
             // ------------------------------------------------ scales
             Ring r;
@@ -465,12 +485,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                 int mb, nb;
                 tile_of(p, t, mb, nb);
                 const int row = (2 * mb + rank) * kGM + lane, col = nb * kGN + lane;
-                for (int k0 = 0; k0 < p.KB; k0 += kGroups) {
+                for (int kg = k0; kg < k1; kg += kGroups) {
                     ok = __all_sync(0xFFFFFFFFu, pipe_wait(ab, smem_u32(&all->sempty[r.slot]), r.phase ^ 1u, p.w));
                     if (!ok) break;
                     uint32_t dst = smem_u32(scales + r.slot * kGroups * kGScales<BROWS>) + lane * 4;
-                    const float *a = p.sa + (int64_t)k0 * p.M, *b = p.sb + (int64_t)k0 * p.nsb;
-                    for (int kb = k0; kb < min(k0 + kGroups, p.KB); ++kb) {
+                    const float *a = p.sa + (int64_t)kg * p.M, *b = p.sb + (int64_t)kg * p.nsb;
+                    for (int kb = kg; kb < min(kg + kGroups, k1); ++kb) {
 #pragma unroll
                         for (int i = 0; i < kGM; i += 32) cp_async4(dst + i * 4, a + (row + i < p.M ? row + i : 0), row + i < p.M);
                         if (BROWS) {
@@ -498,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
         const int quarter = warp & 3, part = (warp - 4) >> 2;  // 32 rows, and 128 of the tile's columns
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         unsigned char* out = sOut + (warp - 4) * kGOut;
-        const uint32_t done = mapa_shared(smem_u32(&bars->tempty[0]), 0);
+        const uint32_t done = mapa_shared(smem_u32(&bars->tempty[0]), (uint32_t)leader);
         Ring acc, sc;
         bool ok = first < tiles, ready = false;
         for (int t = first; ok && t < tiles; t += step) {
@@ -506,8 +526,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
 #pragma unroll
             for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
             const float* s = nullptr;
-            for (int kb = 0; kb < p.KB; ++kb) {
-                if (kb % kGroups == 0) {
+            for (int kb = k0; kb < k1; ++kb) {
+                if ((kb - k0) % kGroups == 0) {
                     ok = pipe_wait(ab, smem_u32(&all->sfull[sc.slot]), sc.phase, p.w);
                     s = scales + sc.slot * kGroups * kGScales<BROWS>;
                 }
@@ -539,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive_remote(done + acc.slot * 8);
                         acc.next(2);
-                        ready = mbar_try_wait(smem_u32(&bars->tfull[acc.slot]), acc.phase);
+                        ready = mbar_test_wait(smem_u32(&bars->tfull[acc.slot]), acc.phase);  // must not suspend
                     }
                     if (BROWS) {
 #pragma unroll
@@ -564,13 +584,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
                     }
                 }
                 s += kGScales<BROWS>;
-                if (kb % kGroups == kGroups - 1 || kb == p.KB - 1) {
+                if ((kb - k0) % kGroups == kGroups - 1 || kb == k1 - 1) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&all->sempty[sc.slot]));
                     sc.next(kGSlots);
                 }
             }
             if (!ok) break;
+            if (split > 1) {
+                // every load has been consumed, so the ring's memory takes the partial sums [128][256], a row's
+                // pitch 260 for the banks
+                float* red = reinterpret_cast<float*>(sA) + (quarter * 32) * kRedPitch + part * 128;
+                if (BROWS) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                *reinterpret_cast<float2*>(red + (i * 8 + (lane >> 2)) * kRedPitch + c * 32 + j * 8 +
+                                                           2 * (lane & 3)) = sum[c * 16 + i * 4 + j];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        *reinterpret_cast<float4*>(red + lane * kRedPitch + 4 * i) =
+                            make_float4(sum[2 * i].x, sum[2 * i].y, sum[2 * i + 1].x, sum[2 * i + 1].y);
+                }
+                break;
+            }
             int mb, nb;
             tile_of(p, t, mb, nb);
             const int64_t row0 = (int64_t)(2 * mb + rank) * kGM + quarter * 32;
@@ -584,6 +625,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGThreads, 1)
             }
         }
     }
+    if (split > 1) {
+        // This CTA adds up its share of the rows, the pairs' sums in order.
+        cluster_sync_all();
+        const bool failed = *reinterpret_cast<volatile int*>(ab) != 0;
+        int mb, nb;
+        tile_of(p, first, mb, nb);
+        const int lo = kGM * (leader / 2) / split, hi = kGM * (leader / 2 + 1) / split;
+#pragma unroll 2
+        for (int e = threadIdx.x; e < (hi - lo) * (kGN / 4) && !failed; e += kGThreads) {
+            const int r = lo + e / (kGN / 4), c = e % (kGN / 4) * 4;
+            const int64_t row = (int64_t)(2 * mb + rank) * kGM + r;
+            const int col = nb * kGN + c;
+            if (row >= p.M || col >= p.N) continue;
+            const uint32_t at = smem_u32(reinterpret_cast<float*>(sA) + r * kRedPitch + c);
+            float4 v[kGSplit];  // all under way before the first is added
+#pragma unroll
+            for (int s = 0; s < kGSplit; ++s)
+                v[s] = s < split ? ld_cluster_f32x4(mapa_shared(at, (uint32_t)(2 * s + rank)))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            float x[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int s = 1; s < kGSplit; ++s) {
+                x[0] = __fadd_rn(x[0], v[s].x), x[1] = __fadd_rn(x[1], v[s].y);
+                x[2] = __fadd_rn(x[2], v[s].z), x[3] = __fadd_rn(x[3], v[s].w);
+            }
+            if (p.c_f32) {
+                float* d = static_cast<float*>(p.c) + row * p.ldc + col;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (col + i < p.N) d[i] = p.accumulate ? d[i] + x[i] : x[i];
+            } else {
+                uint16_t* d = static_cast<uint16_t*>(p.c) + row * p.ldc + col;
+                const uint2 w = make_uint2(pack_bf16x2_rn(x[0], x[1]), pack_bf16x2_rn(x[2], x[3]));
+                if (p.vec && col + 4 <= p.N) {
+                    *reinterpret_cast<uint2*>(d) = w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (col + i < p.N) d[i] = (uint16_t)((i < 2 ? w.x : w.y) >> (16 * (i & 1)));
+                }
+            }
+        }
+    }
     pair_end(tmem, warp);
 }
 
@@ -594,9 +678,8 @@ constexpr int kSRows = 128;  // rows of B a tile
 
 template <int NT>
 struct Skinny {
-    // two CTAs per SM; one for 128 rows, whose sums alone are 128 registers a thread
-    static constexpr int kPerSm = NT <= 64 ? 2 : 1;
-    static constexpr int kStages = NT <= 16 ? 5 : NT <= 64 ? 4 : 6;
+    static constexpr int kPerSm = 2;
+    static constexpr int kStages = NT <= 16 ? 5 : 4;
     static constexpr uint32_t kW = kSRows * kGK, kX = NT * kGK;
     static constexpr uint32_t kTmem = 2 * NT < 32 ? 32 : 2 * NT;
     static constexpr int kScale = NT + kSRows;
@@ -831,38 +914,78 @@ rlk_status allow_smem(K kernel, size_t bytes) {
     return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product: shared memory", e);
 }
 
+template <typename... Args>
+rlk_status launch_clusters(void (*kernel)(Args...), int blocks, int threads, size_t smem, int cluster,
+                           cudaStream_t st, Args... args) {
+    const rlk_status s = allow_smem(kernel, smem);
+    if (s != RLK_OK) return s;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product launch", e);
+}
+
+// Clusters of `cluster` CTAs that the device runs at once (asked once a kernel, size and device).
+template <auto KERNEL>
+int clusters_at_once(int threads, size_t smem, int cluster) {
+    static std::mutex mu;
+    static int known[64][9] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || cluster < 1 || cluster > 8) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    int& n = known[dev][cluster];
+    if (n == 0) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)cluster);
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)cluster;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if (allow_smem(KERNEL, smem) != RLK_OK || cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+            return 0;
+        }
+    }
+    return n;
+}
+
 template <bool BROWS>
 rlk_status launch_gemm(const Gemm8Params& p, const CUtensorMap& a, const CUtensorMap& b, int sms, cudaStream_t st) {
-    const rlk_status s = allow_smem(gemm_kernel<BROWS>, kGSmem<BROWS>);
-    if (s != RLK_OK) return s;
+    // Tiles that would leave half of the pairs idle are split along K, over two or four pairs of a cluster of eight
+    // CTAs at most, while each keeps four groups and all clusters run at once: the CTAs of a cluster share a GPC, and
+    // a second round of clusters costs more than the split gains (16 tiles over four pairs each 30 us, over two 19).
     const int tiles = p.MB * p.NB, pairs = sms / 2;
-    gemm_kernel<BROWS><<<2 * (tiles < pairs ? tiles : pairs), kGThreads, kGSmem<BROWS>, st>>>(a, b, p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product launch", e);
+    int split = kGSplit;
+    while (split > 1 && (p.KB < split * 4 || tiles > clusters_at_once<gemm_kernel<BROWS>>(kGThreads, kGSmem<BROWS>, 2 * split)))
+        split /= 2;
+    return launch_clusters(gemm_kernel<BROWS>, 2 * (split > 1 ? tiles * split : tiles < pairs ? tiles : pairs),
+                           kGThreads, kGSmem<BROWS>, 2 * split, st, a, b, p, split);
 }
 
 template <int NT, bool BROWS>
 rlk_status launch_skinny(const Gemm8Params& p, const CUtensorMap& a, const CUtensorMap& b, int sms,
                          cudaStream_t st) {
-    const rlk_status s = allow_smem(skinny_kernel<NT, BROWS>, Skinny<NT>::kSmem);
-    if (s != RLK_OK) return s;
     const int tiles = p.MB * p.NB, room = Skinny<NT>::kPerSm * sms;
     int split = 1;
     while (split < 8 && tiles * split * 2 <= room && split * 4 <= p.KB) split *= 2;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : tiles < room ? tiles : room));
-    cfg.blockDim = dim3(kSThreads);
-    cfg.dynamicSmemBytes = Skinny<NT>::kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)split;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, skinny_kernel<NT, BROWS>, a, b, p, split);
-    return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product launch", e);
+    return launch_clusters(skinny_kernel<NT, BROWS>, split > 1 ? tiles * split : tiles < room ? tiles : room,
+                           kSThreads, Skinny<NT>::kSmem, split, st, a, b, p, split);
 }
 
 template <bool BROWS>
@@ -871,8 +994,7 @@ rlk_status launch_skinny_nt(int nt, const Gemm8Params& p, const CUtensorMap& a, 
     switch (nt) {
         case 16: return launch_skinny<16, BROWS>(p, a, b, sms, st);
         case 32: return launch_skinny<32, BROWS>(p, a, b, sms, st);
-        case 64: return launch_skinny<64, BROWS>(p, a, b, sms, st);
-        default: return launch_skinny<128, BROWS>(p, a, b, sms, st);
+        default: return launch_skinny<64, BROWS>(p, a, b, sms, st);
     }
 }
 
@@ -901,11 +1023,10 @@ rlk_status launch_fp8_matmul(int64_t M, int64_t N, int64_t K, const void* a, int
     p.w.status = status;
     p.w.wait_ns = kDefaultWaitNs;
     CUtensorMap ta, tb;
-    // Few rows of A: the weight's rows take the lanes.  Up to 128 rows the
-    // 128 x 256 tile would read the weight once as well, but in N / 256 units
-    // that a short N leaves most SMs without.
-    if (M <= 128) {
-        const int nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    // Few rows of A: the weight's rows take the lanes.  (With 65 to 128 rows a tile of 128 x 128 has more scales to
+    // read and sums to keep than its share of the weight's bytes takes: 27.5 us at 128 x 16384 x 4096, the pair 24.7.)
+    if (M <= 64) {
+        const int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
         p.MB = (int32_t)((M + nt - 1) / nt);
         p.NB = (int32_t)((N + kSRows - 1) / kSRows);
         if (!make_map8(&ta, a, K, M, lda, (uint32_t)nt) || !make_map8(&tb, b, K, N, ldb, kSRows))

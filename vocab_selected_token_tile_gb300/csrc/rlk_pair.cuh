@@ -109,14 +109,15 @@ __device__ __forceinline__ uint32_t pair_begin(PairBars<STAGES>* bars, int warp,
         tmem_relinquish_pair();
     }
     tc_fence_before();
-    cluster_sync_all();  // both CTAs' barriers are initialised and their tensor memory allocated
+    __syncthreads();         // this CTA's tensor memory address
+    cluster_sync_relaxed();  // both CTAs' barriers (fence_mbar_init released them)
     tc_fence_after();
     return bars->tmem_addr;
 }
 
 __device__ __forceinline__ void pair_end(uint32_t tmem, int warp) {
     tc_fence_before();
-    cluster_sync_all();  // the pair's MMAs and copies are done, in both CTAs' memory
+    cluster_sync_relaxed();  // the pair's MMAs and copies are done, in both CTAs' memory
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
@@ -136,8 +137,9 @@ __device__ void pair_drain_copies(PairBars<STAGES>* bars, Ring r, int issued, in
 
 // The MMA issuer's: every MMA issued so far completes.
 template <int STAGES>
-__device__ __forceinline__ void pair_drain_mmas(PairBars<STAGES>* bars, bool one, const PipeWait& w) {
-    if (one) umma_commit_pair(smem_u32(&bars->drain));
+__device__ __forceinline__ void pair_drain_mmas(PairBars<STAGES>* bars, bool one, const PipeWait& w,
+                                                uint16_t mask = 3) {
+    if (one) umma_commit_pair(smem_u32(&bars->drain), mask);
     __syncwarp();
     pipe_drain(smem_u32(&bars->drain), 0u, w);
 }

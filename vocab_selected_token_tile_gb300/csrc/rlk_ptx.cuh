@@ -277,6 +277,12 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// All threads of all CTAs of the cluster, without ordering memory between
+// them: a release would wait for every global store before it.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+
 // ----------------------------------------------------------------- CTA pairs (cta_group::2)
 //
 // Two CTAs of a cluster of two work one MMA: each holds half of A's rows and
@@ -296,12 +302,13 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Arrive (once) on the barrier at `bar`'s offset in both CTAs of the pair when
-// every tcgen05 operation this thread issued so far has completed.
-__device__ __forceinline__ void umma_commit_pair(uint32_t bar) {
+// Arrive (once) on the barrier at `bar`'s offset in both CTAs of the pair (the
+// cluster ranks of `mask`) when every tcgen05 operation this thread issued so
+// far has completed.
+__device__ __forceinline__ void umma_commit_pair(uint32_t bar, uint16_t mask = 3) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"(mask)
         : "memory");
 }
 
