@@ -159,7 +159,10 @@ def linear_cross_entropy(hidden, weight, targets, mask=None, ignore_index=-100, 
         raise ValueError("reduction must be none, sum or mean")
     c = linear_ce_contract(hidden, weight, mask, ignore_index, kinds[reduction], label_smoothing, z_loss, softcap,
                            piece)
-    loss, lse = LinearCrossEntropy.apply(hidden, weight, targets, mask, c)
+    if torch.is_grad_enabled() and (hidden.requires_grad or weight.requires_grad):
+        loss, lse = LinearCrossEntropy.apply(hidden, weight, targets, mask, c)
+    else:
+        loss, lse = linear_ce_fwd(c, hidden, weight, targets, mask)
     return (loss, lse) if return_lse else loss
 
 
@@ -203,4 +206,9 @@ def fp8_linear(x, weight):
     saved for the backward are the E4M3 transposes, one byte an element.
     """
     lead = x.shape[:-1]
-    return Fp8Linear.apply(x.reshape(-1, x.shape[-1]), weight).reshape(*lead, weight.shape[0])
+    rows = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad):
+        y = Fp8Linear.apply(rows, weight)
+    else:
+        y = fp8_matmul(*fp8_quantize(rows), *fp8_quantize(weight, block_rows=128))
+    return y if x.dim() == 2 else y.reshape(*lead, weight.shape[0])

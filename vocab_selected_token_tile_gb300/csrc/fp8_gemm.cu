@@ -907,17 +907,14 @@ rlk_status cuda_fail(const char* what, cudaError_t e) {
     return fail(RLK_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
-template <typename K>
-rlk_status allow_smem(K kernel, size_t bytes) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product: shared memory", e);
+template <auto KERNEL>
+rlk_status allow_smem(size_t bytes) {
+    return allow_dynamic_smem<KERNEL>(bytes) ? RLK_OK : cuda_fail("fp8 product: shared memory", cudaGetLastError());
 }
 
-template <typename... Args>
-rlk_status launch_clusters(void (*kernel)(Args...), int blocks, int threads, size_t smem, int cluster,
-                           cudaStream_t st, Args... args) {
-    const rlk_status s = allow_smem(kernel, smem);
+template <auto KERNEL, typename... Args>
+rlk_status launch_clusters(int blocks, int threads, size_t smem, int cluster, cudaStream_t st, Args... args) {
+    const rlk_status s = allow_smem<KERNEL>(smem);
     if (s != RLK_OK) return s;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)blocks);
@@ -931,7 +928,7 @@ rlk_status launch_clusters(void (*kernel)(Args...), int blocks, int threads, siz
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, KERNEL, args...);
     return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product launch", e);
 }
 
@@ -956,7 +953,7 @@ int clusters_at_once(int threads, size_t smem, int cluster) {
         at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        if (allow_smem(KERNEL, smem) != RLK_OK || cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess) {
+        if (allow_smem<KERNEL>(smem) != RLK_OK || cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess) {
             cudaGetLastError();
             n = 0;
             return 0;
@@ -974,7 +971,7 @@ rlk_status launch_gemm(const Gemm8Params& p, const CUtensorMap& a, const CUtenso
     int split = kGSplit;
     while (split > 1 && (p.KB < split * 4 || tiles > clusters_at_once<gemm_kernel<BROWS>>(kGThreads, kGSmem<BROWS>, 2 * split)))
         split /= 2;
-    return launch_clusters(gemm_kernel<BROWS>, 2 * (split > 1 ? tiles * split : tiles < pairs ? tiles : pairs),
+    return launch_clusters<gemm_kernel<BROWS>>(2 * (split > 1 ? tiles * split : tiles < pairs ? tiles : pairs),
                            kGThreads, kGSmem<BROWS>, 2 * split, st, a, b, p, split);
 }
 
@@ -984,7 +981,7 @@ rlk_status launch_skinny(const Gemm8Params& p, const CUtensorMap& a, const CUten
     const int tiles = p.MB * p.NB, room = Skinny<NT>::kPerSm * sms;
     int split = 1;
     while (split < 8 && tiles * split * 2 <= room && split * 4 <= p.KB) split *= 2;
-    return launch_clusters(skinny_kernel<NT, BROWS>, split > 1 ? tiles * split : tiles < room ? tiles : room,
+    return launch_clusters<skinny_kernel<NT, BROWS>>(split > 1 ? tiles * split : tiles < room ? tiles : room,
                            kSThreads, Skinny<NT>::kSmem, split, st, a, b, p, split);
 }
 

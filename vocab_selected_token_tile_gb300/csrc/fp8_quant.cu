@@ -24,8 +24,16 @@
 // transposed codes pass through 16 KB of shared memory in 8-byte pieces (8
 // rows of one column), XOR-swizzled by the column's block of 8 so that the 16
 // lanes of a half warp hit 16 different 8-byte bank pairs.
+//
+// What it spends: with the loads under way most of the time the issue slots
+// decide (a tile's share of HBM is about 3,000 clocks).  So the maxima of BF16
+// are taken two at a time (a BF16 maximum is exact), a row's scale is formed by
+// one lane of its sixteen, a column's by one thread of the CTA, and an element
+// is widened once for both directions.
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <string>
 
 #include "rlk_internal.h"
 #include "rlk_ptx.cuh"
@@ -57,11 +65,6 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
     uint16_t v;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
     return v;
-}
-
-__device__ __forceinline__ uint2 pack_e4m3x8(const float (&v)[8]) {
-    return make_uint2(pack_e4m3x2(v[0], v[1]) | (pack_e4m3x2(v[2], v[3]) << 16),
-                      pack_e4m3x2(v[4], v[5]) | (pack_e4m3x2(v[6], v[7]) << 16));
 }
 
 // The thread's 8 x 8 block, kept as it was read (BF16 pairs, or FP32).
@@ -116,90 +119,164 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int64_t c0, int64_t C,
         if (c0 + j < C) row[c0 + j] = (uint8_t)((j < 4 ? v.x >> (8 * j) : v.y >> (8 * (j - 4))) & 0xFFu);
 }
 
+// Bits of |x| of two BF16; their elementwise maximum, and the larger of the two.
+__device__ __forceinline__ uint32_t abs2(uint32_t w) { return w & 0x7FFF7FFFu; }
+__device__ __forceinline__ float max_of(uint32_t w) { return fmax_nan(bf16lo_to_f32(w), bf16hi_to_f32(w)); }
+
 template <bool F32, bool BLOCKS, bool TRANS>
-__global__ void __launch_bounds__(kQThreads, F32 ? 2 : 4) quantize_kernel(const __grid_constant__ QuantParams p) {
-    __shared__ float colmax[TRANS && !BLOCKS ? 16 : 1][kQT];
-    __shared__ float warpmax[8];
-    __shared__ uint2 tile_t[TRANS ? kQT * 16 : 1];  // [column][8-row piece ^ (column / 8)]
+struct TileShared {
+    uint4 colmax[TRANS && !BLOCKS ? 16 : 1][F32 ? 32 : 16];  // [8 rows][8 columns' maxima, as read]
+    float4 colr[TRANS && !BLOCKS ? kQT / 4 : 1];             // a column's 1 / s
+    float warpmax[8];
+    uint2 tile_t[TRANS ? kQT * 16 : 1];                      // [column][8-row piece ^ (column / 8)]
+};
+
+template <bool F32, bool BLOCKS, bool TRANS>
+__device__ __forceinline__ void quantize_tile(const QuantParams& p, const Block<F32>& b, int64_t ct, int64_t rt,
+                                              TileShared<F32, BLOCKS, TRANS>& sh) {
     const int t = threadIdx.x, cx = t & 15, ry = t >> 4;
-    const int64_t ct = blockIdx.x, rt = blockIdx.y + (int64_t)blockIdx.z * 65535;
     const int64_t r0 = rt * kQT + ry * 8, c0 = ct * kQT + cx * 8;
-    if (rt * kQT >= p.R) return;
+    constexpr int W = F32 ? 8 : 4;  // words of a row's 8 elements
 
-    Block<F32> b;
+    // the columns' maxima over this thread's 8 rows, word by word
+    uint32_t cm[W];
+    if (BLOCKS || TRANS) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) load_row(b, i, p, r0 + i, c0);
-
-    float bs = 0.f, br = 0.f;  // the block's scale and reciprocal (BLOCKS)
-    if (BLOCKS) {
-        float m = 0.f;
+        for (int k = 0; k < W; ++k) {
+            cm[k] = F32 ? b.w[0][k] & 0x7FFFFFFFu : abs2(b.w[0][k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmax_nan(m, fabsf(b.at(i, j)));
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if ((t & 31) == 0) warpmax[t >> 5] = m;
-        __syncthreads();
-        m = warpmax[0];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) m = fmax_nan(m, warpmax[w]);
-        scale_of(m, bs, br);
-        if (t == 0) {
-            const int64_t RB = (p.R + kQT - 1) / kQT, CB = (p.C + kQT - 1) / kQT;
-            if (p.q) p.scale[ct * RB + rt] = bs;
-            if (TRANS) p.scale_t[rt * CB + ct] = bs;
+            for (int i = 1; i < 8; ++i)
+                cm[k] = F32 ? __float_as_uint(fmax_nan(__uint_as_float(cm[k]), fabsf(__uint_as_float(b.w[i][k]))))
+                            : bf16x2_max_nan(cm[k], abs2(b.w[i][k]));
         }
     }
-    if (p.q) {
+    float rr[8], cc[8];  // 1 / s of the thread's rows and columns
+    if (BLOCKS) {
+        float m;
+        if (F32) {
+            m = __uint_as_float(cm[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float r = br;
-            if (!BLOCKS) {
-                float m = 0.f, s;
+            for (int k = 1; k < W; ++k) m = fmax_nan(m, __uint_as_float(cm[k]));
+        } else {
+            m = max_of(bf16x2_max_nan(bf16x2_max_nan(cm[0], cm[1]), bf16x2_max_nan(cm[2], cm[W - 1])));
+        }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m = fmax_nan(m, fabsf(b.at(i, j)));
+        for (int o = 16; o; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        if ((t & 31) == 0) sh.warpmax[t >> 5] = m;
+        __syncthreads();
+        m = sh.warpmax[0];
 #pragma unroll
-                for (int o = 8; o; o >>= 1) m = fmax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        for (int w = 1; w < 8; ++w) m = fmax_nan(m, sh.warpmax[w]);
+        float s, r;
+        scale_of(m, s, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rr[i] = cc[i] = r;
+        if (t == 0) {
+            const int64_t RB = (p.R + kQT - 1) / kQT, CB = (p.C + kQT - 1) / kQT;
+            if (p.q) p.scale[ct * RB + rt] = s;
+            if (TRANS) p.scale_t[rt * CB + ct] = s;
+        }
+    } else {
+        if (TRANS) {
+            sh.colmax[ry][(F32 ? 2 : 1) * cx] = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+            if (F32) sh.colmax[ry][2 * cx + 1] = make_uint4(cm[W - 4], cm[W - 3], cm[W - 2], cm[W - 1]);
+        }
+        if (p.q) {
+            // the rows' maxima over the 16 threads of a row: lane l of the sixteen forms the scale of row l mod 8
+            float m;
+            if (F32) {
+                m = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float v = fabsf(__uint_as_float(b.w[i][0]));
+#pragma unroll
+                    for (int k = 1; k < W; ++k) v = fmax_nan(v, fabsf(__uint_as_float(b.w[i][k])));
+#pragma unroll
+                    for (int o = 8; o; o >>= 1) v = fmax_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+                    if ((cx & 7) == i) m = v;
+                }
+            } else {
+                uint32_t pm = 0;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    uint32_t v[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t* w = b.w[i + h];
+                        v[h] = bf16x2_max_nan(bf16x2_max_nan(abs2(w[0]), abs2(w[1])),
+                                              bf16x2_max_nan(abs2(w[2]), abs2(w[W - 1])));
+                    }
+                    // (row i, row i + 1): the lower halves' with the upper halves' maxima
+                    uint32_t m2 = bf16x2_max_nan(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[0], v[1], 0x7632));
+#pragma unroll
+                    for (int o = 8; o; o >>= 1) m2 = bf16x2_max_nan(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, o));
+                    if ((cx & 6) == i) pm = m2;
+                }
+                m = (cx & 1) ? bf16hi_to_f32(pm) : bf16lo_to_f32(pm);
+            }
+            float s, r;
+            scale_of(m, s, r);
+            if (cx < 8 && r0 + cx < p.R) p.scale[ct * p.R + r0 + cx] = s;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) rr[i] = __shfl_sync(0xFFFFFFFFu, r, i, 16);
+        }
+        if (TRANS) {
+            __syncthreads();
+            if (t < kQT) {
+                const uint32_t* cw = reinterpret_cast<const uint32_t*>(sh.colmax);
+                float m = 0.f, s, r;
+                if (F32) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) m = fmax_nan(m, __uint_as_float(cw[k * 128 + t]));
+                } else {
+                    uint32_t v = cw[t >> 1];
+#pragma unroll
+                    for (int k = 1; k < 16; ++k) v = bf16x2_max_nan(v, cw[k * 64 + (t >> 1)]);
+                    m = (t & 1) ? bf16hi_to_f32(v) : bf16lo_to_f32(v);
+                }
                 scale_of(m, s, r);
-                if (cx == 0 && r0 + i < p.R) p.scale[ct * p.R + r0 + i] = s;
+                if (ct * kQT + t < p.C) p.scale_t[rt * p.C + ct * kQT + t] = s;
+                reinterpret_cast<float*>(sh.colr)[t] = r;
             }
-            if (r0 + i < p.R) {
-                float v[8];
+            __syncthreads();
+            const float4 lo = sh.colr[2 * cx], hi = sh.colr[2 * cx + 1];
+            cc[0] = lo.x, cc[1] = lo.y, cc[2] = lo.z, cc[3] = lo.w;
+            cc[4] = hi.x, cc[5] = hi.y, cc[6] = hi.z, cc[7] = hi.w;
+        }
+    }
+    // the codes, two rows at a time: along the rows for q, along the columns for qt
+    uint32_t tc[8][2] = {};  // [column][rows 0-3, 4-7]
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(b.at(i, j), r);
-                store_codes(p.q + (r0 + i) * p.ldq, c0, p.C, pack_e4m3x8(v));
+    for (int i = 0; i < 8; i += 2) {
+        uint32_t code[2][2] = {};  // [row][columns 0-3, 4-7]
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float2 v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                v[h] = make_float2(b.at(i + h, 2 * k), b.at(i + h, 2 * k + 1));
+                if (p.q || BLOCKS) {
+                    const float2 y = fmul2(v[h], make_float2(rr[i + h], rr[i + h]));
+                    if (BLOCKS) v[h] = y;
+                    code[h][k >> 1] |= pack_e4m3x2(y.x, y.y) << (16 * (k & 1));
+                }
+                if (TRANS && !BLOCKS) v[h] = fmul2(v[h], make_float2(cc[2 * k], cc[2 * k + 1]));
             }
+            if (TRANS) {
+                tc[2 * k][i >> 2] |= pack_e4m3x2(v[0].x, v[1].x) << (8 * (i & 2));
+                tc[2 * k + 1][i >> 2] |= pack_e4m3x2(v[0].y, v[1].y) << (8 * (i & 2));
+            }
+        }
+        if (p.q) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (r0 + i + h < p.R)
+                    store_codes(p.q + (r0 + i + h) * p.ldq, c0, p.C, make_uint2(code[h][0], code[h][1]));
         }
     }
     if (TRANS) {
-        if (!BLOCKS) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float m = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m = fmax_nan(m, fabsf(b.at(i, j)));
-                colmax[ry][cx * 8 + j] = m;
-            }
-            __syncthreads();
-            if (t < kQT) {
-                float m = colmax[0][t], s, r;
-#pragma unroll
-                for (int k = 1; k < 16; ++k) m = fmax_nan(m, colmax[k][t]);
-                scale_of(m, s, r);
-                if (ct * kQT + t < p.C) p.scale_t[rt * p.C + ct * kQT + t] = s;
-                colmax[0][t] = r;  // only this thread reads column t's entries
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float r = BLOCKS ? br : colmax[0][cx * 8 + j];
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(b.at(i, j), r);
-            tile_t[(cx * 8 + j) * 16 + (ry ^ cx)] = pack_e4m3x8(v);
-        }
+        for (int j = 0; j < 8; ++j) sh.tile_t[(cx * 8 + j) * 16 + (ry ^ cx)] = make_uint2(tc[j][0], tc[j][1]);
         __syncthreads();
         // 128 columns x 16 pieces of 8 rows, 16 consecutive threads to a column
 #pragma unroll
@@ -207,20 +284,41 @@ __global__ void __launch_bounds__(kQThreads, F32 ? 2 : 4) quantize_kernel(const 
             const int col = k * 16 + ry, piece = cx;
             if (ct * kQT + col < p.C && rt * kQT + piece * 8 < p.R)
                 store_codes(p.qt + (ct * kQT + col) * p.ldqt, rt * kQT + piece * 8, p.R,
-                            tile_t[col * 16 + (piece ^ (col >> 3))]);
+                            sh.tile_t[col * 16 + (piece ^ (col >> 3))]);
         }
     }
 }
 
+template <bool F32, bool BLOCKS, bool TRANS>
+__global__ void __launch_bounds__(kQThreads, F32 ? 3 : 4) quantize_kernel(const __grid_constant__ QuantParams p) {
+    __shared__ TileShared<F32, BLOCKS, TRANS> sh;
+    const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
+    const int64_t ct = blockIdx.x, rt = blockIdx.y + (int64_t)blockIdx.z * 65535;
+    if (rt * kQT >= p.R) return;
+    Block<F32> b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load_row(b, i, p, rt * kQT + ry * 8 + i, ct * kQT + cx * 8);
+    quantize_tile<F32, BLOCKS, TRANS>(p, b, ct, rt, sh);
+}
+
+rlk_status quant_cuda(const char* what) {
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? RLK_OK : fail(RLK_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+template <bool F32, bool BLOCKS, bool TRANS>
+rlk_status launch_as(const QuantParams& p, cudaStream_t st) {
+    const int64_t ct = (p.C + kQT - 1) / kQT, rt = (p.R + kQT - 1) / kQT;
+    const dim3 grid((unsigned)ct, (unsigned)(rt < 65535 ? rt : 65535), (unsigned)((rt + 65534) / 65535));
+    quantize_kernel<F32, BLOCKS, TRANS><<<grid, kQThreads, 0, st>>>(p);
+    return quant_cuda("fp8 quantize launch");
+}
+
 template <bool F32>
-void launch_typed(const QuantParams& p, bool blocks, dim3 grid, cudaStream_t st) {
+rlk_status launch_typed(const QuantParams& p, bool blocks, cudaStream_t st) {
     const bool trans = p.qt != nullptr;
-    if (blocks)
-        trans ? quantize_kernel<F32, true, true><<<grid, kQThreads, 0, st>>>(p)
-              : quantize_kernel<F32, true, false><<<grid, kQThreads, 0, st>>>(p);
-    else
-        trans ? quantize_kernel<F32, false, true><<<grid, kQThreads, 0, st>>>(p)
-              : quantize_kernel<F32, false, false><<<grid, kQThreads, 0, st>>>(p);
+    if (blocks) return trans ? launch_as<F32, true, true>(p, st) : launch_as<F32, true, false>(p, st);
+    return trans ? launch_as<F32, false, true>(p, st) : launch_as<F32, false, false>(p, st);
 }
 
 }  // namespace
@@ -240,15 +338,7 @@ rlk_status launch_fp8_quantize(int64_t rows, int64_t cols, const void* x, int32_
     p.scale = scale;
     p.scale_t = scale_t;
     p.vec = (reinterpret_cast<uintptr_t>(x) % 16 == 0) && (ldx * (x_f32 ? 4 : 2)) % 16 == 0;
-    const int64_t ct = (cols + kQT - 1) / kQT, rt = (rows + kQT - 1) / kQT;
-    const dim3 grid((unsigned)ct, (unsigned)(rt < 65535 ? rt : 65535), (unsigned)((rt + 65534) / 65535));
-    if (x_f32)
-        launch_typed<true>(p, block_rows == kQT, grid, stream);
-    else
-        launch_typed<false>(p, block_rows == kQT, grid, stream);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(RLK_ERR_CUDA, std::string("fp8 quantize launch: ") + cudaGetErrorString(e));
-    return RLK_OK;
+    return x_f32 ? launch_typed<true>(p, block_rows == kQT, stream) : launch_typed<false>(p, block_rows == kQT, stream);
 }
 
 }  // namespace rlk

@@ -795,8 +795,7 @@ rlk_status ce_sms(int* sms) {
 template <int MODE, bool CAP, bool SMOOTH>
 rlk_status launch_logits(const CUtensorMap& h, const CUtensorMap& w, uint16_t* dx, int64_t ldx, const CeParams& p,
                          int sms, cudaStream_t st) {
-    if (cudaFuncSetAttribute(ce_logits_kernel<MODE, CAP, SMOOTH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)kCeSmem) != cudaSuccess)
+    if (!allow_dynamic_smem<ce_logits_kernel<MODE, CAP, SMOOTH>>(kCeSmem))
         return ce_cuda("linear cross entropy: shared memory");
     const int64_t units = (int64_t)p.nch * p.MB, pairs = sms / 2;
     ce_logits_kernel<MODE, CAP, SMOOTH>
@@ -899,8 +898,7 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     ce_scale_kernel<<<1, 1024, 0, st>>>(grad, targets, mask, c.mask_mode, c.ignore_index, c.T, c.reduction, scale);
     if ((s = ce_cuda("linear cross entropy: scale")) != RLK_OK) return s;
 
-    const uint32_t smem = (uint32_t)kCeSmem;
-    if (cudaFuncSetAttribute(ce_grads_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    if (!allow_dynamic_smem<ce_grads_kernel>(kCeSmem))
         return ce_cuda("linear cross entropy: shared memory");
     CeParams p = ce_params(c, targets, mask, status);
     p.lse = lse;
@@ -959,7 +957,7 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
         const int nl = g.head ? g.n1 : g.n0, ns = g.head ? g.n0 : g.n1, left = nl % pairs;
         const int64_t make_up = left ? (int64_t)(pairs - left) * ((g.head ? k1 : k0) / (g.head ? k0 : k1)) : 0;
         g.deal = (int32_t)(make_up < ns ? make_up : ns);
-        ce_grads_kernel<<<2 * pairs, kCeThreads, smem, st>>>(tmA0, tmB0, tmC0, tmA1, tmB1, tmC1, g);
+        ce_grads_kernel<<<2 * pairs, kCeThreads, kCeSmem, st>>>(tmA0, tmB0, tmC0, tmA1, tmB1, tmC1, g);
         if ((s = ce_cuda("linear cross entropy: gradients")) != RLK_OK) return s;
     }
     if (dhidden && q.S > 1) {

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 
 #include "rlk_logp.h"
@@ -57,6 +58,20 @@ struct StreamArgs {
     const unsigned long long* n_active;
     float* grad_out;
 };
+
+// Allows a kernel its dynamic shared memory, once a kernel and device (the
+// call costs about as much host time as a launch's arguments).
+template <auto KERNEL>
+bool allow_dynamic_smem(size_t bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return true;
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+        return false;
+    if (dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    return true;
+}
 
 // Records a failure reason for rlk_last_error_message() and returns `s`.
 rlk_status fail(rlk_status s, const std::string& why);
