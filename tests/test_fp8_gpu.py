@@ -141,11 +141,31 @@ def test_product_matches_64_bits(built, M, N, K, block):
     assert torch.equal(again, f32)
 
 
-@pytest.mark.parametrize("M", [3, 200])
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("M,N,K", [
+    (2100, 2501, 130),    # more tiles than pairs of CTAs, odd rows of C
+    (700, 20002, 300), (256, 20480, 128),
+    (65, 300, 9000), (257, 511, 4001),  # K split over a cluster, many granules of scales
+    (3, 40000, 700), (40, 40001, 260)])  # more tiles than the persistent CTAs of few rows
+def test_product_of_many_tiles(built, M, N, K, block):
+    qa, sa, qb, sb = operands(M, N, K, block, seed=N)
+    a = qa.double() * sa.double().t().repeat_interleave(128, dim=1)[:, :K]
+    b = qb.double() * sb.double().t().repeat_interleave(128, dim=1)[:, :K].repeat_interleave(block, dim=0)[:N]
+    want, terms = a @ b.t(), a.abs() @ b.abs().t()
+    f32 = rlk.fp8_matmul(qa, sa, qb, sb, b_block_rows=block, out_dtype=torch.float32, validate=True)
+    assert ((f32.double() - want).abs() <= ref.bound(K, terms)).all()
+    assert torch.equal(rlk.fp8_matmul(qa, sa, qb, sb, b_block_rows=block), f32.to(torch.bfloat16))
+    base = torch.randn((M, N), device="cuda")
+    out = base.clone()
+    rlk.fp8_matmul(qa, sa, qb, sb, b_block_rows=block, out=out, accumulate=True)
+    assert torch.equal(out, base + f32)
+
+
+@pytest.mark.parametrize("M,K", [(3, 300), (200, 300), (130, 3000)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("offset,stride", [(0, 264), (1, 263), (4, 300)])
-def test_product_into_strided_rows(built, M, dtype, offset, stride):
-    N, K = 259, 300
+def test_product_into_strided_rows(built, M, K, dtype, offset, stride):
+    N = 259
     qa, sa, qb, sb = operands(M, N, K, 128)
     plain = rlk.fp8_matmul(qa, sa, qb, sb, out_dtype=dtype)
     buf = torch.full((M * stride + 16,), 7.0, dtype=dtype, device="cuda")

@@ -284,6 +284,33 @@ def test_large_vocabulary_against_a_blocked_64_bit_form(built):
         assert float((got.double() - want).norm() / want.norm()) < 4e-3
 
 
+@pytest.mark.parametrize("T,V,H,piece", [
+    (300, 700, 2500, 0),      # bands of H blocks, the last one narrow
+    (7100, 600, 2500, 0),     # two bands of token blocks
+    (520, 3000, 136, 512),    # more tiles of dweight than of dhidden, then the reverse
+    (5000, 300, 72, 256)])
+def test_tile_orders_against_64_bits_on_the_gpu(built, T, V, H, piece):
+    h, w, t, on = case(T, V, H, seed=T + V)
+    targets, mask = torch.from_numpy(t).cuda(), torch.from_numpy(on.astype(np.uint8)).cuda()
+    c = rlk.linear_ce_contract(h, w, mask, reduction=rlk.REDUCE_SUM, piece=piece, validate=1)
+    loss, lse = rlk.linear_ce_fwd(c, h, w, targets, mask)
+    dh, dw = rlk.linear_ce_bwd(c, h, w, targets, mask, lse, torch.ones((), device="cuda"))
+    h64, w64, m = h.double(), w.double(), torch.from_numpy(on).cuda()
+    y = h64 @ w64.t()
+    want = torch.logsumexp(y, dim=1)
+    b = torch.from_numpy(ref.lse_bound(host(h), host(w), y.cpu().numpy())).cuda()
+    assert ((lse.double() - want).abs() <= b).all()
+    d = torch.exp(y - want[:, None])
+    d[torch.arange(T, device="cuda")[m], targets[m]] -= 1
+    d[~m] = 0
+    p = torch.exp(y - want[:, None]) * m[:, None]
+    # dx: rounded to BF16, the probabilities off by the logits' and lse's errors; sums of V or T terms in FP32
+    err = 2.0 ** -8 * d.abs() + p * (2 * b[:, None] + 2.0 ** -19 * (1 + want.abs()[:, None])) + 2.0 ** -21 * d.abs()
+    for got, exact, e, terms, n in ((dh, d @ w64, err @ w64.abs(), d.abs() @ w64.abs(), V + 600),
+                                    (dw, d.t() @ h64, err.t() @ h64.abs(), d.abs().t() @ h64.abs(), T + 16)):
+        assert ((got.double() - exact).abs() <= e + n * 2.0 ** -23 * terms + 2.0 ** -8 * exact.abs() + 1e-30).all()
+
+
 def test_fp8_linear_gradients(built):
     # the product's own error is tested elsewhere: here the formulas, through exactly quantised operands
     rng = np.random.default_rng(1)
