@@ -242,6 +242,19 @@ def test_product_on_another_stream_and_in_a_graph(built):
     assert torch.equal(out, rlk.fp8_matmul(*rlk.fp8_quantize(x), qb, sb))
 
 
+def test_stream_argument(built):
+    # the calls enqueue on the given stream, whatever the current one is, and their results may be freed at once
+    x, w = as_input(rand((5, 512), 1), "bf16"), as_input(rand((300, 512), 2), "bf16")
+    want = rlk.fp8_matmul(*rlk.fp8_quantize(x), *rlk.fp8_quantize(w, block_rows=128))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = rlk.fp8_matmul(*rlk.fp8_quantize(x, stream=side), *rlk.fp8_quantize(w, block_rows=128, stream=side),
+                         stream=side)
+    junk = [torch.full((300, 512), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(4)]  # noqa: F841
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_binding_refuses_what_the_call_cannot_read(built):
     qa, sa, qb, sb = operands(4, 130, 200, 128)
     with pytest.raises(ValueError):

@@ -823,6 +823,15 @@ def _raw_stream(t, stream):
     return stream.cuda_stream if stream is not None else _t()._C._cuda_getCurrentRawStream(t.device.index)
 
 
+def _used_on(stream, *tensors):
+    """Tells the allocator that a stream other than the current one uses these new tensors, so that their memory is
+    not handed out again before that stream's work is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _matrix(t, name, dtypes):
     """A 2-D CUDA tensor of one of ``dtypes`` with contiguous rows: (rows, columns, row stride in elements)."""
     shape = t.shape
@@ -876,6 +885,7 @@ def _quantize(x, block_rows, rowwise, transposed, stream):
                           _ptr(q), ldq, _ptr(scale), _ptr(qt), ldt, _ptr(scale_t), _raw_stream(x, stream))
     if st:
         check(st)
+    _used_on(stream, q, scale, qt, scale_t)
     return q, scale, qt, scale_t
 
 
@@ -903,7 +913,13 @@ def _fp8_workspace(t, stream):
     key = (t.device.index, stream)
     ws = _fp8_workspaces.get(key)
     if ws is None:
-        ws = _fp8_workspaces[key] = t.new_zeros(RLK_FP8_WORKSPACE, dtype=_t().uint8)
+        torch = _t()
+        ws = torch.zeros(RLK_FP8_WORKSPACE, dtype=torch.uint8, device=t.device)
+        if torch.cuda.is_current_stream_capturing():
+            return ws  # the graph's memory, not to be kept beyond it
+        if stream != torch._C._cuda_getCurrentRawStream(t.device.index):
+            torch.cuda.current_stream(t.device).synchronize()  # zeroed before the other stream's first call
+        _fp8_workspaces[key] = ws
     return ws
 
 
@@ -941,6 +957,7 @@ def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=Non
         if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
             raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
         out = _new(a, M, N, out_dtype)
+        _used_on(stream, out)
         ldc = N
     else:
         rows, cols, ldc = _matrix(out, "out", (torch.bfloat16, torch.float32))
@@ -1028,6 +1045,7 @@ def linear_ce_fwd(contract, hidden, weight, targets, mask=None, stream=None, wor
         new((), (), dtype=f32, device=hidden.device)
     lse = new((contract.T,), (1,), dtype=f32, device=hidden.device)
     ws = _ce_workspace(contract, 0, hidden, workspace)
+    _used_on(stream, loss, lse, ws)
     status = rlk_linear_ce_fwd(contract, *operands, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
                                _raw_stream(hidden, stream))
     if status:
@@ -1051,6 +1069,7 @@ def linear_ce_bwd(contract, hidden, weight, targets, mask, lse, grad_loss, need_
     dh = out(T, contract.dhidden_stride) if need_dhidden else None
     dw = out(V, contract.dweight_stride) if need_dweight else None
     ws = _ce_workspace(contract, 1, hidden, workspace)
+    _used_on(stream, dh, dw, ws)
     status = rlk_linear_ce_bwd(contract, *operands, pl, pg, _ptr(dh), _ptr(dw), ws.data_ptr(),
                                _raw_stream(hidden, stream))
     if status:

@@ -18,6 +18,7 @@ and ``rlk_linear_ce_bwd``; ``Fp8Linear`` (``fp8_linear``) quantises with
 ``rlk_fp8_matmul``.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (MASK_EXPLICIT, MASK_IGNORE_INDEX, REDUCE_MEAN, REDUCE_NONE, REDUCE_SUM, Contract, fp8_matmul,
                fp8_quantize, fp8_quantize_both, linear_ce_bwd, linear_ce_contract, linear_ce_fwd, logp_bwd,
@@ -134,6 +135,7 @@ class LinearCrossEntropy(torch.autograd.Function):
         return loss, lse
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_loss, grad_lse):
         if grad_loss is None:
             return None, None, None, None, None
@@ -182,6 +184,7 @@ class Fp8Linear(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         xtq, xts, wtq, wts = ctx.saved_tensors
         need_x, need_w = ctx.needs_input_grad
