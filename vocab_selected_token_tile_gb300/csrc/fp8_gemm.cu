@@ -460,8 +460,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
+                    // the operands first: theirs are ready early, so only the accumulator's wait is in its way
                     if (!(ok = pipe_wait(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                    if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
                     tc_fence_after();
                     if (one) {
 #pragma unroll
@@ -748,8 +749,8 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
             const uint32_t idesc = idesc_e4m3_f32(kSRows, NT);
             for (int t = first; ok && t < tiles; t += step) {
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
                     if (!(ok = pipe_wait(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                    if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
                     tc_fence_after();
                     const uint32_t w0 = smem_u32(sW + r.slot * S::kW), x0 = smem_u32(sX + r.slot * S::kX);
 #pragma unroll

@@ -206,6 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
     const uint32_t total = (uint32_t)p.nch * p.MB, first = blockIdx.x / 2, step = gridDim.x / 2;
     const uint32_t tmem = pair_begin(bars, warp, kCeEpilogue);
     int* ab = &bars->abort_flag;
+    if (MODE == kCeForward) grid_launch_dependents();  // the merge
 
     if (warp == 0) {
         const bool one = elect_one();
@@ -372,15 +373,17 @@ struct CeFold {
 // Each row's LSE and loss from its partials: 8 rows a CTA, 64 threads a row
 // take runs of partials in vocabulary order, and the runs are merged pairwise,
 // neighbours first.  The order depends on the number of partials only.
-__global__ void __launch_bounds__(kFoldRows* kFoldSlices) ce_fold_kernel(const CeFold p) {
+__global__ void __launch_bounds__(kFoldRows* kFoldSlices) ce_fold_kernel(CeFold p) {
     __shared__ float2 sm[kFoldSlices][kFoldRows];
     __shared__ float sy[kFoldSlices][kFoldRows];
     const int lane = threadIdx.x % kFoldRows, sl = threadIdx.x / kFoldRows;
     const int64_t row = (int64_t)blockIdx.x * kFoldRows + lane;
+    grid_launch_dependents();
+    grid_wait_prior();
     float m = -INFINITY, s = 0.f, y = 0.f;
     if (row < p.T) {
         const int c0 = (int)((int64_t)p.parts * sl / kFoldSlices), c1 = (int)((int64_t)p.parts * (sl + 1) / kFoldSlices);
-#pragma unroll 4
+#pragma unroll 8
         for (int c = c0; c < c1; ++c) {
             const float2 q = p.part[(int64_t)c * p.T + row];
             ce_merge(m, s, q.x, q.y);
@@ -436,6 +439,7 @@ __global__ void __launch_bounds__(1024) ce_reduce_kernel(const float* loss, cons
                                                          int64_t T, int mean, float* out) {
     __shared__ double sums[32];
     __shared__ long long counts[32];
+    grid_wait_prior();
     double s = 0.;
     long long n = 0;
     for (int64_t r = threadIdx.x; r < T; r += 1024) {
@@ -792,6 +796,22 @@ rlk_status ce_sms(int* sms) {
     return RLK_OK;
 }
 
+// A launch that the kernel before it in the stream may overlap with its setting
+// up (the kernel waits with grid_wait_prior).
+template <typename... Args>
+void launch_behind(void (*kernel)(Args...), int64_t blocks, int threads, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, args...);  // an error stays for ce_cuda
+}
+
 template <int MODE, bool CAP, bool SMOOTH>
 rlk_status launch_logits(const CUtensorMap& h, const CUtensorMap& w, uint16_t* dx, int64_t ldx, const CeParams& p,
                          int sms, cudaStream_t st) {
@@ -876,10 +896,11 @@ rlk_status launch_linear_ce_fwd(const rlk_linear_ce_contract& c, const void* hid
     f.mask_mode = c.mask_mode;
     f.eps = c.label_smoothing;
     f.z = c.z_loss;
-    ce_fold_kernel<<<(unsigned)ceil_div(c.T, kFoldRows), kFoldRows * kFoldSlices, 0, st>>>(f);
+    launch_behind<CeFold>(ce_fold_kernel, ceil_div(c.T, kFoldRows), kFoldRows * kFoldSlices, st, f);
     if (c.reduction != RLK_REDUCE_NONE)
-        ce_reduce_kernel<<<1, 1024, 0, st>>>(f.loss, targets, mask, c.mask_mode, c.ignore_index, c.T,
-                                             c.reduction == RLK_REDUCE_MEAN, loss);
+        launch_behind<const float*, const int64_t*, const uint8_t*, int, int64_t, int64_t, int, float*>(
+            ce_reduce_kernel, 1, 1024, st, f.loss, targets, mask, c.mask_mode, c.ignore_index, c.T,
+            c.reduction == RLK_REDUCE_MEAN, loss);
     return ce_cuda("linear cross entropy: merge");
 }
 

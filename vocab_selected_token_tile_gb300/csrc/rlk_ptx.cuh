@@ -90,6 +90,11 @@ __device__ __forceinline__ bool elect_one() {
     return one != 0;
 }
 
+// Programmatic dependent launch: the next kernel of the stream may be set up
+// from here on; a kernel set up early waits for everything before it.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ----------------------------------------------------------------- bulk copy
 
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
