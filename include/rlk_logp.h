@@ -459,9 +459,9 @@ rlk_status rlk_logp_fwd_noalloc(const rlk_logp_contract* contract, const void* l
  *     L   = lse - (1 - label_smoothing) y_t - (label_smoothing / V) sum_c y_c
  *           + z_loss lse^2   on active rows, 0 on inactive ones.
  * hidden [T, H] and weight [V, H] are BF16, row-major; any T, V and H, rows on
- * 16-byte boundaries (strides a multiple of 8 elements, 0 -> H).  Every row of
- * hidden is read, an inactive row's too: its values must be finite, or they
- * reach dweight as 0 * NaN.
+ * 16-byte boundaries (strides a multiple of 8 elements, 0 -> H).  An inactive
+ * row's hidden reaches its own lse only, whatever it holds, and costs the
+ * backward nothing.
  */
 typedef enum {
     RLK_REDUCE_NONE = 0,  /* loss [T] */
@@ -493,7 +493,7 @@ rlk_status rlk_linear_ce_check(const rlk_linear_ce_contract* contract);
 /*
  * Bytes of device workspace: of the forward (with_grad 0), or of either call
  * (1): about T V / 16 for the forward's partials (half as much again with
- * label smoothing); T piece * 2 + T H * 4 for the backward, whatever V is.
+ * label smoothing); T piece * 2 + T H * 6 for the backward, whatever V is.
  * 0 for an invalid contract.
  */
 size_t rlk_linear_ce_workspace_size(const rlk_linear_ce_contract* contract, int32_t with_grad);

@@ -148,6 +148,26 @@ def test_inactive_rows_do_not_touch_the_others(built):
     assert torch.equal(part, loss[keep]) and torch.equal(part_lse, lse[keep])
 
 
+@pytest.mark.parametrize("T", [30, 300, 900])
+def test_masked_rows_may_hold_anything(built, T):
+    # NaN and infinities in an inactive row's hidden reach nothing but that row's lse
+    h, w, t, on = case(T, 700, 100, seed=T, inactive=0.6)
+    targets, mask = torch.from_numpy(t).cuda(), torch.from_numpy(on.astype(np.uint8)).cuda()
+    c = rlk.linear_ce_contract(h, w, mask, reduction=rlk.REDUCE_MEAN, validate=1)
+    loss, lse = rlk.linear_ce_fwd(c, h, w, targets, mask)
+    one = torch.ones((), device="cuda")
+    want = rlk.linear_ce_bwd(c, h, w, targets, mask, lse, one)
+    dirty = torch.empty_strided(h.shape, h.stride(), dtype=h.dtype, device=h.device).copy_(h)
+    off = torch.from_numpy(np.flatnonzero(~on)).cuda()
+    dirty[off[::2]] = float("nan")
+    dirty[off[1::2]] = float("inf")
+    c = rlk.linear_ce_contract(dirty, w, mask, reduction=rlk.REDUCE_MEAN, validate=1)
+    loss2, lse2 = rlk.linear_ce_fwd(c, dirty, w, targets, mask)
+    got = rlk.linear_ce_bwd(c, dirty, w, targets, mask, lse2, one)
+    assert torch.equal(loss2, loss) and torch.equal(lse2[mask.bool()], lse[mask.bool()])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.isfinite(got[1]).all()
+
+
 def test_only_the_gradient_that_is_asked_for(built):
     c, h, w, targets, mask, loss, lse, grad, dh, dw = run(100, 700, 128, "mean")
     a, b = rlk.linear_ce_bwd(c, h, w, targets, mask, lse, grad, need_dweight=False)

@@ -20,7 +20,12 @@
 // the epilogue as BF16 dL/dx [T, P], and one launch then runs both
 //   dHidden[T, H] += dx weight[piece]     (FP32 sums across the pieces)
 //   dWeight[piece] = dx^T hidden.
-// The work space is P T 2 bytes for dx and T H 4 for the sums, whatever V is.
+// The work space is P T 2 bytes for dx, T H 4 for the sums and T H 2 for the
+// rows below, whatever V is.  Only the active rows take part: their hidden is
+// first copied together (a step's prompts and padding are often half of its
+// rows, and a row of rubbish under a mask must not meet a zero), into rows on
+// 128-byte lines, which a TMA load takes in half the time of others (1000 x
+// 50257 x 1000, rows of 2000 bytes, none masked: backward 253 -> 234 us).
 // P is chosen so that dx stays within kPieceBytes: the sums are read and
 // written once a piece, and with pieces that large that traffic and the ends
 // of the launches are under 2% of a piece's time.
@@ -28,12 +33,12 @@
 // What is rounded to BF16 is dx / scale, with scale = the upstream gradient of
 // a summed or averaged loss (the largest row's otherwise): with a common
 // factor folded in, the value of every row's largest entry, about -g, would
-// be rounded in the same direction, a bias of up to 2^-9 in both gradients.
+// be rounded in the same direction, a bias of up to 2^-8 in both gradients.
 // The scale multiplies the FP32 sums instead.
 //
 // Both GEMM kernels run as CTA pairs (rlk_pair.cuh) on 256 x 256 tiles: warp 0
 // issues the TMA loads, warp 1 of the even CTA the MMAs, warps 2-9 are the
-// epilogue.  The tiles are dealt out before the launch, so every role of both
+// epilogue.  The tiles are dealt out from the sizes alone, so every role of both
 // CTAs knows its sequence and no ticket travels between them.
 // Every sum has a fixed order: no split of a K range without an ordered join,
 // no atomics on data.
@@ -81,6 +86,8 @@ struct CeParams {
     const float* lse;    // [T]                                         gradient
     const float* grad;   // [T], NULL for a summed or averaged loss     gradient
     const float* scale;  // the common factor left out of dx            gradient
+    const int32_t* count;  // the number of active rows                 gradient
+    const int32_t* index;  // [count] their places in the batch         gradient
     PipeWait w;
     int64_t T, V, ignore_index;
     float cap, icap, eps, z;
@@ -94,9 +101,10 @@ struct CeParams {
 // memory, so that a row's 64 bytes leave in one piece; 16 bytes a lane straight
 // from the registers, 32 rows an instruction, took 10,700 clocks a 128 x 256
 // tile.  16-byte piece j of row r is kept at j ^ (r / 2 mod 4).  Rows of
-// `rows` and columns of `cols` at most; every row starts on a 16-byte boundary.
+// `rows` and columns of `cols` at most; every row starts on a 16-byte boundary;
+// row r of them is index[r] of dst, if index is given.
 __device__ __forceinline__ void ce_store(unsigned char* out, int lane, const float (&v)[32], uint16_t* dst, int64_t ld,
-                                         int rows, int cols) {
+                                         int rows, int cols, const int32_t* index = nullptr) {
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -110,7 +118,7 @@ __device__ __forceinline__ void ce_store(unsigned char* out, int lane, const flo
         const int r = i * 8 + (lane >> 2);
         if (r >= rows || j * 8 >= cols) continue;
         const uint4 w = *reinterpret_cast<const uint4*>(out + r * 64 + ((j ^ ((r >> 1) & 3)) * 16));
-        uint16_t* d = dst + r * ld + j * 8;
+        uint16_t* d = dst + (index ? (int64_t)index[r] : (int64_t)r) * ld + j * 8;
         if (j * 8 + 8 <= cols) {
             *reinterpret_cast<uint4*>(d) = w;
         } else {
@@ -130,11 +138,11 @@ __device__ __forceinline__ bool ce_active(const uint8_t* mask, int mask_mode, in
 // Unit u is (chunk ch of 256 vocabulary rows, block mb of 256 tokens): bands of
 // MBg token blocks, chunk-major within a band, so that the units in flight
 // share a few chunks of weight and one band of hidden, which L2 holds.
-__device__ __forceinline__ void ce_unit(const CeParams& p, uint32_t u, int& ch, int& mb) {
-    const uint32_t band = (uint32_t)p.nch * p.MBg, full = (uint32_t)p.MB / p.MBg;
+__device__ __forceinline__ void ce_unit(const CeParams& p, int MB, uint32_t u, int& ch, int& mb) {
+    const uint32_t band = (uint32_t)p.nch * p.MBg, full = (uint32_t)MB / p.MBg;
     const uint32_t b = min(u / band, full);
     const uint32_t r = u - b * band;
-    const uint32_t w = b < full ? p.MBg : p.MB - full * p.MBg;
+    const uint32_t w = b < full ? p.MBg : MB - full * p.MBg;
     ch = p.ch0 + (int)(r / w);
     mb = (int)(b * p.MBg + r % w);
 }
@@ -203,7 +211,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
     PairBars<kCeStages>* bars = m.bars;
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
-    const uint32_t total = (uint32_t)p.nch * p.MB, first = blockIdx.x / 2, step = gridDim.x / 2;
+    // the rows that take part: all of them, or the active ones, copied together
+    const int64_t T = MODE == kCeGrad ? (int64_t)*p.count : p.T;
+    const int MB = (int)((T + 255) / 256);
+    const uint32_t total = (uint32_t)p.nch * MB, first = blockIdx.x / 2, step = gridDim.x / 2;
     const uint32_t tmem = pair_begin(bars, warp, kCeEpilogue);
     int* ab = &bars->abort_flag;
     if (MODE == kCeForward) grid_launch_dependents();  // the merge
@@ -217,11 +228,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
         bool ok = true;
         for (uint32_t u = first; ok && u < total; u += step) {
             int ch, mb;
-            ce_unit(p, u, ch, mb);
+            ce_unit(p, MB, u, ch, mb);
             // a CTA without a row of its own loads no hidden: its rows of the accumulator are not used
             const int row = (2 * mb + rank) * 128;
-            const bool mine = row < p.T;
-            const uint32_t bytes = 2 * kCeB + (uint32_t)p.box_rows * 128 * ((2 * mb + 1) * (int64_t)128 < p.T ? 2 : 1);
+            const bool mine = row < T;
+            const uint32_t bytes = 2 * kCeB + (uint32_t)p.box_rows * 128 * ((2 * mb + 1) * (int64_t)128 < T ? 2 : 1);
             for (int kb = 0; kb < p.KB; ++kb) {
                 if (!(ok = pipe_wait(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                 if (one) {
@@ -270,27 +281,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
         Ring acc;
         for (uint32_t u = first; u < total; u += step) {
             int ch, mb;
-            ce_unit(p, u, ch, mb);
+            ce_unit(p, MB, u, ch, mb);
             const int64_t row0 = (int64_t)(2 * mb + rank) * 128 + quarter * 32, row = row0 + lane;
-            const bool valid = row < p.T;
+            const bool valid = row < T;
             int64_t target = -1;
             bool active = false;
             float qa = 0.f, qb = 0.f, qc = 0.f, nlL = 0.f;
-            if (valid) {
+            if (valid && MODE == kCeForward) {
                 target = p.targets[row];
                 active = ce_active(p.mask, p.mask_mode, p.ignore_index, target, row);
-                if (MODE == kCeGrad && active) {
-                    // dx / scale = (qa p - qc - qb [c = t]) slope
-                    const float l = p.lse[row];
-                    const float g = p.grad ? __fdiv_rn(p.grad[row], scale) : 1.f;
-                    qa = g * (1.f + 2.f * p.z * l);
-                    qb = g * (1.f - p.eps);
-                    qc = g * p.eps / (float)p.V;
-                    nlL = -__fmul_rn(l, kLog2e);
-                    if (ch == 0 && half == 0) {  // the device conditions of a row, once
-                        if (target < 0 || target >= p.V) atomicOr(p.w.status, kStatusTargetRange);
-                        if (!isfinite(l)) atomicOr(p.w.status, kStatusNonFinite);
-                    }
+            }
+            if (valid && MODE == kCeGrad) {
+                // dx / scale = (qa p - qc - qb [c = t]) slope
+                const int64_t at = p.index[row];
+                const float l = p.lse[at];
+                const float g = p.grad ? __fdiv_rn(p.grad[at], scale) : 1.f;
+                target = p.targets[at];
+                active = true;
+                qa = g * (1.f + 2.f * p.z * l);
+                qb = g * (1.f - p.eps);
+                qc = g * p.eps / (float)p.V;
+                nlL = -__fmul_rn(l, kLog2e);
+                if (ch == 0 && half == 0) {  // the device conditions of a row, once
+                    if (target < 0 || target >= p.V) atomicOr(p.w.status, kStatusTargetRange);
+                    if (!isfinite(l)) atomicOr(p.w.status, kStatusNonFinite);
                 }
             }
             if (!__all_sync(0xFFFFFFFFu, pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w))) break;
@@ -330,6 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
                     if (CAP) d = __fmul_rn(d, slope);
                     v[i] = active ? d : 0.f;
                 }
+                // rows past the active ones are zero: dWeight's K range ends on a whole block of 64
                 ce_store(out, lane, v, dx + row0 * ldx + (cbase - (int64_t)p.ch0 * kBN) + sub * 32, ldx,
                          (int)min((int64_t)32, p.T - row0), nv);
             }
@@ -451,38 +466,104 @@ __global__ void __launch_bounds__(1024) ce_reduce_kernel(const float* loss, cons
     if (threadIdx.x == 0) *out = (float)(mean ? (n > 0 ? s / (double)n : 0.) : s);
 }
 
-// The factor that is left out of every row's dx: the gradient of a summed
-// loss, that of an averaged one over the active rows, or the largest finite
-// magnitude of the rows' gradients (a non-finite one stays its own row's).
-__global__ void __launch_bounds__(1024) ce_scale_kernel(const float* grad, const int64_t* targets,
-                                                        const uint8_t* mask, int mask_mode, int64_t ignore_index,
-                                                        int64_t T, int reduction, float* scale) {
-    __shared__ long long counts[32];
+struct CeRows {
+    const float* grad;
+    const int64_t* targets;
+    const uint8_t* mask;
+    float* scale;
+    int32_t* count;
+    int32_t* index;  // [T] the active rows, in order
+    int32_t* place;  // [T] a row's place among them, -1 for an inactive one
+    int64_t T, ignore_index;
+    int32_t mask_mode, reduction;
+};
+
+// The active rows in order, and the factor that is left out of every row's dx:
+// the gradient of a summed loss, that of an averaged one over the active rows,
+// or the largest finite magnitude of the rows' gradients (a non-finite one
+// stays its own row's).  One CTA.
+__global__ void __launch_bounds__(1024) ce_rows_kernel(const CeRows p) {
+    __shared__ int counts[32];
     __shared__ float tops[32];
-    long long n = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int n = 0;
     float top = 0.f;
-    if (reduction != RLK_REDUCE_SUM) {
-        for (int64_t r = threadIdx.x; r < T; r += 1024) {
-            if (!ce_active(mask, mask_mode, ignore_index, mask_mode == RLK_MASK_EXPLICIT ? 0 : targets[r], r)) continue;
-            ++n;
-            if (reduction == RLK_REDUCE_NONE) {
-                const float g = fabsf(grad[r]);
+    for (int64_t r0 = 0; r0 < p.T; r0 += 1024) {
+        const int64_t r = r0 + threadIdx.x;
+        const bool on = r < p.T && ce_active(p.mask, p.mask_mode, p.ignore_index,
+                                             p.mask_mode == RLK_MASK_EXPLICIT ? 0 : p.targets[r], r);
+        const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, on);
+        if (lane == 0) counts[warp] = __popc(ballot);
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int w = 0; w < 32; ++w) {
+            before += w < warp ? counts[w] : 0;
+            all += counts[w];
+        }
+        const int at = n + before + __popc(ballot & ((1u << lane) - 1u));
+        if (r < p.T) p.place[r] = on ? at : -1;
+        if (on) {
+            p.index[at] = (int32_t)r;
+            if (p.reduction == RLK_REDUCE_NONE) {
+                const float g = fabsf(p.grad[r]);
                 if (g < INFINITY) top = fmaxf(top, g);
             }
         }
-    }
-    if (reduction == RLK_REDUCE_NONE) {
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+        n += all;
         __syncthreads();
-        top = tops[threadIdx.x & 31];
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        if (threadIdx.x == 0) *scale = top == 0.f ? 1.f : top;
-        return;
     }
-    n = block_sum(n, counts);
-    if (threadIdx.x == 0)
-        *scale = reduction == RLK_REDUCE_SUM ? grad[0] : n > 0 ? (float)((double)grad[0] / (double)n) : 0.f;
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    *p.count = n;
+    if (p.reduction == RLK_REDUCE_NONE) {
+        for (int w = 1; w < 32; ++w) top = fmaxf(top, tops[w]);
+        *p.scale = top == 0.f ? 1.f : top;
+    } else {
+        *p.scale = p.reduction == RLK_REDUCE_SUM ? p.grad[0] : n > 0 ? (float)((double)p.grad[0] / (double)n) : 0.f;
+    }
+}
+
+// The active rows' hidden together, [.., Hs] with zeros past H and in the rows
+// up to the next whole tile; and zeros into the inactive rows of dHidden.  A
+// warp a row.
+__global__ void __launch_bounds__(256) ce_gather_kernel(const uint16_t* hidden, int64_t ld, int H, int64_t T,
+                                                        const int32_t* count, const int32_t* place, uint16_t* rows,
+                                                        int64_t Hs, uint16_t* dhidden, int64_t ldh) {
+    const int lane = threadIdx.x & 31;
+    const int64_t n = *count, whole = (n + 255) / 256 * 256;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < T + (whole - n); r += (int64_t)gridDim.x * 8) {
+        const int64_t to = r < T ? place[r] : n + (r - T);
+        if (to < 0) {
+            if (dhidden)
+                for (int c = lane * 8; c < H; c += 256) {
+                    uint16_t* d = dhidden + r * ldh + c;
+                    if (c + 8 <= H)
+                        *reinterpret_cast<uint4*>(d) = make_uint4(0u, 0u, 0u, 0u);
+                    else
+                        for (int j = 0; c + j < H; ++j) d[j] = 0;
+                }
+            continue;
+        }
+#pragma unroll 4
+        for (int c = lane * 8; c < Hs; c += 256) {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (r < T && c < H) {
+                const uint16_t* x = hidden + r * ld + c;
+                if (c + 8 <= H) {
+                    v = *reinterpret_cast<const uint4*>(x);
+                } else {
+                    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (c + j < H) w[j >> 1] |= (uint32_t)x[j] << (16 * (j & 1));
+                    v = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            *reinterpret_cast<uint4*>(rows + to * Hs + c) = v;
+        }
+    }
 }
 
 // ----------------------------------------------------------------- the gradients' products
@@ -493,20 +574,41 @@ struct CeGrads {
     float* sums;        // [S, T, Hs] FP32 sums of dHidden across the pieces
     const float* scale;
     PipeWait w;
+    const int32_t *count, *index;  // the active rows
     int64_t T, ldh, ldw, Hs;
-    int32_t n0, n1;     // tiles of dHidden (S slices of MB0 x NB) and of dWeight (MB1 x NB)
-    int32_t head;       // the tiles with the longer K range: 0 dHidden's, 1 dWeight's
-    int32_t deal;       // of the others, how many make up for a long tile less (ce_walk)
-    int32_t cols;       // vocabulary rows of the piece
-    int32_t H, NB, NBg, MB0, MB1, S, KB0, KB1;
+    int32_t cols;         // vocabulary rows of the piece
+    int32_t H, NB, NBg, MB1, S, KB0;
     int32_t first, last;  // the first and the last piece
 };
+
+// What follows from the number of active rows.
+struct CeDeal {
+    int n;        // active rows
+    int MB0, KB1;
+    int n0, n1;   // tiles of dHidden (S slices of MB0 x NB) and of dWeight (MB1 x NB)
+    int head;     // the tiles with the longer K range: 0 dHidden's, 1 dWeight's
+    int deal;     // of the others, how many make up for a long tile less (ce_walk)
+};
+__device__ __forceinline__ CeDeal ce_deal(const CeGrads& p, int pairs) {
+    CeDeal d;
+    d.n = *p.count;
+    d.MB0 = (d.n + 255) / 256;
+    d.KB1 = (d.n + kBK - 1) / kBK;
+    d.n0 = p.dhidden ? p.S * d.MB0 * p.NB : 0;
+    d.n1 = p.dweight ? p.MB1 * p.NB : 0;
+    const int k0 = (p.KB0 + p.S - 1) / p.S, k1 = max(d.KB1, 1);
+    d.head = k0 >= k1 ? 0 : 1;
+    const int nl = d.head ? d.n1 : d.n0, ns = d.head ? d.n0 : d.n1, left = nl % pairs;
+    const int64_t make_up = left ? (int64_t)(pairs - left) * ((d.head ? k1 : k0) / (d.head ? k0 : k1)) : 0;
+    d.deal = (int)min(make_up, (int64_t)ns);
+    return d;
+}
 
 // A pair's i-th tile: 0 .. n0 - 1 dHidden's, then dWeight's; -1 past its last.
 // The longer tiles are dealt round; the pairs that the last round leaves out
 // get the first `deal` of the shorter ones among themselves, and the rest are
 // dealt round again.  A deal that both CTAs' roles know from the start.
-__device__ __forceinline__ int ce_walk(const CeGrads& p, int i, int pair, int pairs) {
+__device__ __forceinline__ int ce_walk(const CeDeal& p, int i, int pair, int pairs) {
     const int nl = p.head ? p.n1 : p.n0, ns = p.head ? p.n0 : p.n1, left = nl % pairs;
     const int mine = nl / pairs + (pair < left);
     int v, is_long = 0;
@@ -528,11 +630,11 @@ struct CeTile {
 };
 
 // dHidden slice by slice; bands of NBg H blocks, M-major within a band.
-__device__ __forceinline__ CeTile ce_tile(const CeGrads& p, int u) {
+__device__ __forceinline__ CeTile ce_tile(const CeGrads& p, const CeDeal& d, int u) {
     CeTile t;
-    t.prob = u < p.n0 ? 0 : 1;
-    uint32_t v = t.prob ? u - p.n0 : u;
-    const uint32_t MB = t.prob ? p.MB1 : p.MB0;
+    t.prob = u < d.n0 ? 0 : 1;
+    uint32_t v = t.prob ? u - d.n0 : u;
+    const uint32_t MB = t.prob ? p.MB1 : d.MB0;
     t.slice = 0;
     if (!t.prob) {
         t.slice = (int)(v / (MB * p.NB));
@@ -546,7 +648,7 @@ __device__ __forceinline__ CeTile ce_tile(const CeGrads& p, int u) {
     t.nb = (int)(b * p.NBg + r % w);
     t.wide = p.H - t.nb * kBN > 128 ? 2 : 1;
     t.k0 = t.prob ? 0 : (int)((int64_t)p.KB0 * t.slice / p.S);
-    t.k1 = t.prob ? p.KB1 : (int)((int64_t)p.KB0 * (t.slice + 1) / p.S);
+    t.k1 = t.prob ? d.KB1 : (int)((int64_t)p.KB0 * (t.slice + 1) / p.S);
     return t;
 }
 
@@ -564,6 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
     const int pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
+    const CeDeal deal = ce_deal(p, pairs);
     const uint32_t tmem = pair_begin(bars, warp, kCeEpilogue);
     int* ab = &bars->abort_flag;
 
@@ -573,10 +676,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
         Ring r;
         int issued = 0;
         bool ok = true;
-        for (int i = 0, u; ok && (u = ce_walk(p, i, pair, pairs)) >= 0; ++i) {
-            const CeTile t = ce_tile(p, u);
+        for (int i = 0, u; ok && (u = ce_walk(deal, i, pair, pairs)) >= 0; ++i) {
+            const CeTile t = ce_tile(p, deal, u);
             const int m0 = (2 * t.mb + rank) * 128, h0 = t.nb * kBN + rank * t.wide * 64;
-            const bool box3 = t.wide == 2 && (p.H % 64 == 0 || p.H - t.nb * kBN >= kBN);
+            // (the active rows' hidden is padded with zeros to whole blocks)
+            const bool box3 = t.wide == 2 && (t.prob == 1 || p.H % 64 == 0 || p.H - t.nb * kBN >= kBN);
             for (int kb = t.k0; kb < t.k1; ++kb) {
                 if (!(ok = pipe_wait(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                 if (one) {
@@ -608,8 +712,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
         const uint64_t db = smem_desc_sw128_mn(smem_u32(m.b), kMnBlock, 1024);
         Ring r, acc;
         bool ok = true;
-        for (int i = 0, u; ok && (u = ce_walk(p, i, pair, pairs)) >= 0; ++i) {
-            const CeTile t = ce_tile(p, u);
+        for (int i = 0, u; ok && (u = ce_walk(deal, i, pair, pairs)) >= 0; ++i) {
+            const CeTile t = ce_tile(p, deal, u);
             if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
             tc_fence_after();
             const uint32_t idesc = idesc_bf16_f32_major(256, (uint32_t)(128 * t.wide), t.prob == 1, true);
@@ -643,12 +747,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
         const uint32_t done = mapa_shared(smem_u32(&bars->tempty[0]), 0);
         const float scale = *p.scale;
         Ring acc;
-        for (int i = 0, u; (u = ce_walk(p, i, pair, pairs)) >= 0; ++i) {
-            const CeTile t = ce_tile(p, u);
+        for (int i = 0, u; (u = ce_walk(deal, i, pair, pairs)) >= 0; ++i) {
+            const CeTile t = ce_tile(p, deal, u);
             if (!__all_sync(0xFFFFFFFFu, pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w))) break;
             tc_fence_after();
             const int64_t row0 = (int64_t)(2 * t.mb + rank) * 128 + quarter * 32, row = row0 + lane;
-            const int64_t nrows = t.prob == 0 ? p.T : (int64_t)p.cols;
+            const int64_t nrows = t.prob == 0 ? deal.n : p.cols;
             // dHidden leaves as BF16 from the only slice of the last piece, else into the sums
             const bool out = t.prob == 1 || (p.S == 1 && p.last);
             for (int sub = half * 2 * t.wide; sub < (half + 1) * 2 * t.wide; ++sub) {
@@ -676,8 +780,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(v[i], scale);
                     const int64_t ld = t.prob == 0 ? p.ldh : p.ldw;
-                    ce_store(stage, lane, v, (t.prob == 0 ? p.dhidden : p.dweight) + row0 * ld + col0, ld,
-                             (int)max((int64_t)0, min((int64_t)32, nrows - row0)), p.H - col0);
+                    ce_store(stage, lane, v, t.prob == 0 ? p.dhidden + col0 : p.dweight + row0 * ld + col0, ld,
+                             (int)max((int64_t)0, min((int64_t)32, nrows - row0)), p.H - col0,
+                             t.prob == 0 ? p.index + row0 : nullptr);
                 }
             }
             tc_fence_before();
@@ -704,9 +809,10 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* row, int col, int H, cons
 
 // dHidden from the S slices' sums, added in order.
 __global__ void __launch_bounds__(256) ce_join_kernel(const float* sums, const float* scale, int S, int64_t T,
-                                                      int64_t Hs, int H, uint16_t* dhidden, int64_t ldh) {
+                                                      int64_t Hs, int H, const int32_t* count, const int32_t* index,
+                                                      uint16_t* dhidden, int64_t ldh) {
     const int groups = (H + 7) / 8;
-    const int64_t n = T * groups;
+    const int64_t n = (int64_t)*count * groups;
     const float sc = *scale;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / groups;
@@ -721,7 +827,7 @@ __global__ void __launch_bounds__(256) ce_join_kernel(const float* sums, const f
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], sc);
-        store_bf16x8(dhidden + row * ldh, col, H, v);
+        store_bf16x8(dhidden + index[row] * ldh, col, H, v);
     }
 }
 
@@ -763,7 +869,7 @@ CePlan plan_of(const rlk_linear_ce_contract& c) {
 
 struct CeLayout {
     size_t loss, yt, part, part_y, fwd_end;
-    size_t scale, dx, sums, bwd_end;
+    size_t scale, count, index, place, rows, dx, sums, bwd_end;
 };
 
 CeLayout layout_of(const rlk_linear_ce_contract& c) {
@@ -777,7 +883,11 @@ CeLayout layout_of(const rlk_linear_ce_contract& c) {
     l.fwd_end = l.part_y + (c.label_smoothing != 0.f ? up256(4 * T * parts) : 0);
     const CePlan q = plan_of(c);
     l.scale = at;
-    l.dx = l.scale + 256;
+    l.count = l.scale + 16;
+    l.index = l.scale + 256;
+    l.place = l.index + up256(4 * T);
+    l.rows = l.place + up256(4 * T);
+    l.dx = l.rows + up256(2 * (size_t)q.MB * 256 * (size_t)q.Hs);
     l.sums = l.dx + up256(2 * T * (size_t)q.P);
     l.bwd_end = l.sums + (q.pieces > 1 || q.S > 1 ? up256(4 * (size_t)q.S * T * (size_t)q.Hs) : 0);
     return l;
@@ -916,8 +1026,25 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     uint32_t* status = static_cast<uint32_t*>(workspace);
     if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return ce_cuda("clearing the status word");
     float* scale = reinterpret_cast<float*>(ws + l.scale);
-    ce_scale_kernel<<<1, 1024, 0, st>>>(grad, targets, mask, c.mask_mode, c.ignore_index, c.T, c.reduction, scale);
-    if ((s = ce_cuda("linear cross entropy: scale")) != RLK_OK) return s;
+    uint16_t* rows = reinterpret_cast<uint16_t*>(ws + l.rows);
+    CeRows r{};
+    r.grad = grad;
+    r.targets = targets;
+    r.mask = mask;
+    r.scale = scale;
+    r.count = reinterpret_cast<int32_t*>(ws + l.count);
+    r.index = reinterpret_cast<int32_t*>(ws + l.index);
+    r.place = reinterpret_cast<int32_t*>(ws + l.place);
+    r.T = c.T;
+    r.ignore_index = c.ignore_index;
+    r.mask_mode = c.mask_mode;
+    r.reduction = c.reduction;
+    ce_rows_kernel<<<1, 1024, 0, st>>>(r);
+    const int64_t gather = ceil_div(c.T + 255, 8);
+    ce_gather_kernel<<<(unsigned)(gather < 8 * sms ? gather : 8 * sms), 256, 0, st>>>(
+        static_cast<const uint16_t*>(hidden), c.hidden_stride, (int)c.H, c.T, r.count, r.place, rows, q.Hs,
+        static_cast<uint16_t*>(dhidden), c.dhidden_stride);
+    if ((s = ce_cuda("linear cross entropy: rows")) != RLK_OK) return s;
 
     if (!allow_dynamic_smem<ce_grads_kernel>(kCeSmem))
         return ce_cuda("linear cross entropy: shared memory");
@@ -925,6 +1052,8 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     p.lse = lse;
     p.grad = c.reduction == RLK_REDUCE_NONE ? grad : nullptr;
     p.scale = scale;
+    p.count = r.count;
+    p.index = r.index;
     CeGrads g{};
     g.dhidden = static_cast<uint16_t*>(dhidden);
     g.sums = reinterpret_cast<float*>(ws + l.sums);
@@ -937,17 +1066,16 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     g.H = (int32_t)c.H;
     g.NB = q.NB;
     g.NBg = q.NB < kBandH ? q.NB : kBandH;
-    g.MB0 = q.MB;
     g.S = (int32_t)q.S;
-    g.KB1 = (int32_t)ceil_div(c.T, kBK);
+    g.count = r.count;
+    g.index = r.index;
     uint16_t* dx = reinterpret_cast<uint16_t*>(ws + l.dx);
     CUtensorMap tmH, tmB1, tmC1;
     const bool wide = c.H >= 64;
-    if (!make_map(&tmH, hidden, c.H, c.T, c.hidden_stride, kBK, (uint32_t)p.box_rows) ||
-        !make_map(&tmC1, hidden, c.H, c.T, c.hidden_stride, 64, kBK) ||
-        (wide && !make_map_mn3(&tmB1, hidden, c.H / 64 * 64, c.T, c.hidden_stride, kBK, 2)))
+    const int64_t whole = (int64_t)q.MB * 256;
+    if (!make_map(&tmH, rows, q.Hs, whole, q.Hs, kBK, (uint32_t)p.box_rows) ||
+        !make_map(&tmC1, rows, q.Hs, whole, q.Hs, 64, kBK) || !make_map_mn3(&tmB1, rows, q.Hs, whole, q.Hs, kBK, 2))
         return fail(RLK_ERR_CUDA, kMapFailed);
-    if (!wide) tmB1 = tmC1;
     for (int64_t i = 0; i < q.pieces; ++i) {
         const int64_t c0 = i * q.P, cols = c.V - c0 < q.P ? c.V - c0 : q.P;
         const uint16_t* w0 = static_cast<const uint16_t*>(weight) + c0 * c.weight_stride;
@@ -968,23 +1096,17 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
         g.cols = (int32_t)cols;
         g.KB0 = (int32_t)ceil_div(cols, kBK);
         g.MB1 = (int32_t)ceil_div(cols, 256);
-        g.n0 = dhidden ? (int32_t)(q.S * q.MB * q.NB) : 0;
-        g.n1 = dweight ? g.MB1 * q.NB : 0;
         g.first = i == 0;
         g.last = i == q.pieces - 1;
-        const int tiles = g.n0 + g.n1, pairs = tiles < sms / 2 ? tiles : sms / 2;
-        const int k0 = (int)ceil_div(g.KB0, q.S), k1 = g.KB1;
-        g.head = k0 >= k1 ? 0 : 1;
-        const int nl = g.head ? g.n1 : g.n0, ns = g.head ? g.n0 : g.n1, left = nl % pairs;
-        const int64_t make_up = left ? (int64_t)(pairs - left) * ((g.head ? k1 : k0) / (g.head ? k0 : k1)) : 0;
-        g.deal = (int32_t)(make_up < ns ? make_up : ns);
+        const int64_t tiles = (dhidden ? q.S * q.MB * q.NB : 0) + (dweight ? (int64_t)g.MB1 * q.NB : 0);
+        const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
         ce_grads_kernel<<<2 * pairs, kCeThreads, kCeSmem, st>>>(tmA0, tmB0, tmC0, tmA1, tmB1, tmC1, g);
         if ((s = ce_cuda("linear cross entropy: gradients")) != RLK_OK) return s;
     }
     if (dhidden && q.S > 1) {
         const int64_t blocks = ceil_div(c.T * ceil_div(c.H, 8), 256);
         ce_join_kernel<<<(unsigned)(blocks < 8 * sms ? blocks : 8 * sms), 256, 0, st>>>(
-            g.sums, g.scale, g.S, c.T, q.Hs, g.H, g.dhidden, g.ldh);
+            g.sums, g.scale, g.S, c.T, q.Hs, g.H, g.count, g.index, g.dhidden, g.ldh);
         return ce_cuda("linear cross entropy: join");
     }
     return RLK_OK;
