@@ -161,6 +161,34 @@ def test_product_of_many_tiles(built, M, N, K, block):
     assert torch.equal(out, base + f32)
 
 
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("M,N,K", [(2309, 2100, 4100), (2560, 4090, 2816), (2100, 2820, 9000)])
+def test_product_whose_last_tiles_are_split(built, M, N, K, block):
+    # 90, 160 and 108 tiles of 256 x 256, K long enough for a second launch that overlaps the first's end: what
+    # follows in the stream, on the same C, must follow both
+    qa, sa, qb, sb = operands(M, N, K, block, seed=K)
+    a = qa.double() * sa.double().t().repeat_interleave(128, dim=1)[:, :K]
+    b = qb.double() * sb.double().t().repeat_interleave(128, dim=1)[:, :K].repeat_interleave(block, dim=0)[:N]
+    f32 = rlk.fp8_matmul(qa, sa, qb, sb, b_block_rows=block, out_dtype=torch.float32, validate=True)
+    assert ((f32.double() - a @ b.t()).abs() <= ref.bound(K, a.abs() @ b.abs().t())).all()
+    ws = torch.zeros(rlk.RLK_FP8_WORKSPACE, dtype=torch.uint8, device="cuda")
+    out, want = torch.zeros((M, N), device="cuda"), torch.zeros((M, N), device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            rlk.fp8_matmul(qa, sa, qb, sb, b_block_rows=block, out=out, accumulate=True, workspace=ws)
+            out.mul_(0.5)
+    graph.replay()
+    for _ in range(4):
+        want.add_(f32).mul_(0.5)
+    assert torch.equal(out, want)
+    for _ in range(4):
+        rlk.fp8_matmul(qa, sa, qb, sb, b_block_rows=block, out=out, accumulate=True, workspace=ws)
+        want.add_(f32)
+    assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("M,K", [(3, 300), (200, 300), (130, 3000)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("offset,stride", [(0, 264), (1, 263), (4, 300)])

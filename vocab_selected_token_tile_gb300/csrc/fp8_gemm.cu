@@ -376,6 +376,7 @@ static_assert(sizeof(GemmBars) <= 1024, "barriers fit their kilobyte");
 static_assert(kGSmem<true> <= 232448, "shared memory of a CTA");
 
 constexpr int kGSplit = 4;  // pairs that share a tile at most: a cluster of eight CTAs
+constexpr int kTailSaves = 16;  // K groups that a launch of the last tiles has to save a pair
 constexpr int kRedPitch = kGN + 4;
 static_assert((size_t)kGM * kRedPitch * 4 <= (size_t)kGStages * (kGA + kGB), "the partial sums fit the ring");
 
@@ -391,12 +392,15 @@ __device__ __forceinline__ void tile_of(const Gemm8Params& p, int t, int& mb, in
     mb = b * p.band + r % width;
 }
 
-// split: pairs of a cluster that share a tile, each with a part of the K groups
-// (1: the pair's tiles are its own, one after the other).
+// Tiles tile0 .. tiles - 1.  split: pairs of a cluster that share a tile, each
+// with a part of the K groups (1: the pair's tiles are its own, one after the
+// other).  A launch with tile0 > 0 runs behind the one with the tiles before,
+// whose inputs are its own and whose outputs are not: it may start as that
+// one's pairs end.
 template <bool BROWS>
 __global__ void __launch_bounds__(kGThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const __grid_constant__ Gemm8Params p, const int split) {
+                const __grid_constant__ Gemm8Params p, const int tile0, const int tiles, const int split) {
     extern __shared__ unsigned char smem_raw[];
     // The same offset in both CTAs (their dynamic shared memory starts alike): descriptors name one offset.
     unsigned char* smem =
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int place = (int)cluster_ctarank(), rank = place & 1, leader = place & ~1;
     const uint16_t both = (uint16_t)(3 << leader);
-    const int tiles = p.MB * p.NB, first = (int)blockIdx.x / (2 * split), step = (int)gridDim.x / (2 * split);
+    const int first = tile0 + (int)blockIdx.x / (2 * split), step = (int)gridDim.x / (2 * split);
     const int k0 = (int)((int64_t)p.KB * (leader / 2) / split), k1 = (int)((int64_t)p.KB * (leader / 2 + 1) / split);
 
     if (threadIdx.x == 0) {
@@ -421,6 +425,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
     }
     const uint32_t tmem = pair_begin(bars, warp, 8);
     int* ab = &bars->abort_flag;
+    grid_launch_dependents();  // the launch of the last tiles
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -669,6 +674,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             }
         }
     }
+    if (tile0 > 0) grid_wait_prior();  // what follows in the stream follows both launches
     pair_end(tmem, warp);
 }
 
@@ -913,8 +919,10 @@ rlk_status allow_smem(size_t bytes) {
     return allow_dynamic_smem<KERNEL>(bytes) ? RLK_OK : cuda_fail("fp8 product: shared memory", cudaGetLastError());
 }
 
+// behind: may start while the kernel before it in the stream ends.
 template <auto KERNEL, typename... Args>
-rlk_status launch_clusters(int blocks, int threads, size_t smem, int cluster, cudaStream_t st, Args... args) {
+rlk_status launch_clusters(int blocks, int threads, size_t smem, int cluster, bool behind, cudaStream_t st,
+                           Args... args) {
     const rlk_status s = allow_smem<KERNEL>(smem);
     if (s != RLK_OK) return s;
     cudaLaunchConfig_t cfg{};
@@ -922,13 +930,15 @@ rlk_status launch_clusters(int blocks, int threads, size_t smem, int cluster, cu
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)cluster;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = behind ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, KERNEL, args...);
     return e == cudaSuccess ? RLK_OK : cuda_fail("fp8 product launch", e);
 }
@@ -968,12 +978,25 @@ rlk_status launch_gemm(const Gemm8Params& p, const CUtensorMap& a, const CUtenso
     // Tiles that would leave half of the pairs idle are split along K, over two or four pairs of a cluster of eight
     // CTAs at most, while each keeps four groups and all clusters run at once: the CTAs of a cluster share a GPC, and
     // a second round of clusters costs more than the split gains (16 tiles over four pairs each 30 us, over two 19).
-    const int tiles = p.MB * p.NB, pairs = sms / 2;
-    int split = kGSplit;
-    while (split > 1 && (p.KB < split * 4 || tiles > clusters_at_once<gemm_kernel<BROWS>>(kGThreads, kGSmem<BROWS>, 2 * split)))
-        split /= 2;
-    return launch_clusters<gemm_kernel<BROWS>>(2 * (split > 1 ? tiles * split : tiles < pairs ? tiles : pairs),
-                           kGThreads, kGSmem<BROWS>, 2 * split, st, a, b, p, split);
+    // The tiles of a last, partial round of the pairs are such tiles too, in a launch of their own; its start and
+    // the sums' joining cost about as much as 12 K groups, so it has to save 16 (4096 x 4096 x 8192, scales by the
+    // row, FP32: 172 us in one launch, 157 in two; 2560 x 4096 of BF16: 31 and 32 at K = 2048, 48.8 and 45.3 at 4096).
+    constexpr auto kernel = gemm_kernel<BROWS>;
+    constexpr size_t smem = kGSmem<BROWS>;
+    const int tiles = p.MB * p.NB, pairs = sms / 2, whole = tiles / pairs * pairs, rest = tiles - whole;
+    int split = rest > 0 ? kGSplit : 1;
+    while (split > 1 && (p.KB < split * 4 || rest > clusters_at_once<kernel>(kGThreads, smem, 2 * split))) split /= 2;
+    if (whole > 0 && p.KB * (split - 1) < kTailSaves * split) split = 1;
+    if (split == 1)
+        return launch_clusters<kernel>(2 * (tiles < pairs ? tiles : pairs), kGThreads, smem, 2, false, st, a, b, p, 0,
+                                       tiles, 1);
+    if (whole > 0) {
+        const rlk_status s =
+            launch_clusters<kernel>(2 * pairs, kGThreads, smem, 2, false, st, a, b, p, 0, whole, 1);
+        if (s != RLK_OK) return s;
+    }
+    return launch_clusters<kernel>(2 * rest * split, kGThreads, smem, 2 * split, whole > 0, st, a, b, p, whole, tiles,
+                                   split);
 }
 
 template <int NT, bool BROWS>
@@ -983,7 +1006,7 @@ rlk_status launch_skinny(const Gemm8Params& p, const CUtensorMap& a, const CUten
     int split = 1;
     while (split < 8 && tiles * split * 2 <= room && split * 4 <= p.KB) split *= 2;
     return launch_clusters<skinny_kernel<NT, BROWS>>(split > 1 ? tiles * split : tiles < room ? tiles : room,
-                           kSThreads, Skinny<NT>::kSmem, split, st, a, b, p, split);
+                           kSThreads, Skinny<NT>::kSmem, split, false, st, a, b, p, split);
 }
 
 template <bool BROWS>
