@@ -584,7 +584,8 @@ rlk_status rlk_fp8_quantize(int64_t rows, int64_t cols, const void* x, int32_t x
  * gradients of it are dY W (B the quantised transpose of W, the same blocks)
  * and dY^T x (A and B the transposes of dY and x, both in rows).  M = 0 or
  * N = 0 does nothing; K >= 1.  c must not overlap an input.  The bits depend
- * on M, N, K and the device's SM count only.  Asynchronous on `stream`.
+ * on M, N, K, b_block_rows and the device (its SMs, and how many clusters of
+ * CTAs they hold at once) only.  Asynchronous on `stream`.
  */
 #define RLK_FP8_WORKSPACE 256
 

@@ -13,20 +13,27 @@
 //
 // Two kernels:
 //
-// gemm_kernel, a 128 x 256 tile a CTA, persistent, one CTA per SM.  Bound: the
-// tensor core, 2 M N K operations at the FP8 rate (128 x 256 x 128 takes 512
-// clocks a group); reading the 128 KB accumulator back takes 256 clocks of the
-// tensor-memory port and the scaling 128 (block scales) or 256+ issue slots a
-// scheduler, so the epilogue fits under the MMAs with two accumulators in
-// flight.  Roles: warp 0 issues the TMA loads, warp 1 the MMAs, warp 2 fetches
-// the scales with cp.async (4 bytes each: a row of scales starts at any
+// gemm_kernel, 256 x 256 tiles by pairs of CTAs (rlk_pair.cuh), persistent, one
+// CTA per SM.  A pair halves what a CTA's MMAs read of B from shared memory (a
+// first kernel, single CTAs with 128 x 256 tiles, took 452 us at 8192 x 12288 x
+// 4096; this one 312).  Floor: the tensor core, 2 M N K operations.  A group's four MMAs take 512 clocks;
+// the epilogue of a group, which reads back 128 KB of accumulator a CTA (256
+// clocks of the tensor-memory port) and scales and adds it (128 issue slots of
+// packed pairs a scheduler, twice that with B's scales by the row), takes about
+// 900 clocks with block scales and 1,250 with row scales, from one accumulator's
+// completion to the next: it is what bounds both.  8192 x 8192 x 8192: 390 us
+// (2.8 PFLOP/s, tensor pipe 55% busy) and 548 us (2.0 PFLOP/s, 38%).  Roles:
+// warp 0 issues the TMA loads, warp 1 of the even CTA the pair's MMAs, warp 2
+// fetches the scales with cp.async (4 bytes each: a row of scales starts at any
 // multiple of 4), warps 4-11 are the epilogue (a warp reads 32 tensor-memory
 // lanes and 128 of the 256 columns: 128 sums a thread, which is why the first
-// warpgroup gives registers away with setmaxnreg).
+// warpgroup gives registers away with setmaxnreg).  Sixteen epilogue warps of
+// 64 sums each were slower (400 us at 8192 x 12288 x 4096).
 //
 // skinny_kernel, for few rows of A: B's rows take the 128 lanes and A's rows
 // the accumulator's columns (16, 32 or 64), so a single token streams the
-// weight once and wastes no more than 15 columns.  Bound: HBM, N K bytes.  Two
+// weight once and wastes no more than 15 columns.  Bound: HBM, N K bytes (37 x
+// 151936 x 4096: 100 us, 6.3 TB/s; 1 x 4096 x 4096: 7.2 us).  Two
 // CTAs per SM keep loads in flight across each other's start and end.  Where N
 // / 128 tiles are fewer than the SMs can hold, a cluster of 2, 4 or 8 CTAs
 // splits K, and adds its partial sums through distributed shared memory in
