@@ -493,8 +493,9 @@ rlk_status rlk_linear_ce_check(const rlk_linear_ce_contract* contract);
 /*
  * Bytes of device workspace: of the forward (with_grad 0), or of either call
  * (1): about T V / 16 for the forward's partials (half as much again with
- * label smoothing); T piece * 2 + T H * 6 for the backward, whatever V is.
- * 0 for an invalid contract.
+ * label smoothing), and T H * 2 where hidden's rows lie between 128-byte lines;
+ * T piece * 2 + T H * 6 for the backward, whatever V is.  0 for an invalid
+ * contract.
  */
 size_t rlk_linear_ce_workspace_size(const rlk_linear_ce_contract* contract, int32_t with_grad);
 

@@ -168,6 +168,27 @@ def test_masked_rows_may_hold_anything(built, T):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.isfinite(got[1]).all()
 
 
+def test_rows_between_lines_give_the_same(built):
+    # large enough for the forward to copy hidden onto 128-byte lines: the bits of rows that lie there already
+    T, V, H = 701, 40003, 1000
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    wide = torch.randn((T, 1024), generator=gen, device="cuda").to(torch.bfloat16)
+    w = (torch.randn((V, H), generator=gen, device="cuda") * 0.03).to(torch.bfloat16)
+    targets = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    targets[::9] = -100
+    out = []
+    for h in (wide[:, :H], wide[:, :H].contiguous()):
+        c = rlk.linear_ce_contract(h, w, reduction=rlk.REDUCE_NONE, label_smoothing=0.1, softcap=20.0, validate=1)
+        out.append(rlk.linear_ce_fwd(c, h, w, targets))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    # FP32 sums of H exact products: H 2^-24 of their magnitudes' sum at the worst, the cap's slope is at most 1
+    a = wide[:, :H].double()
+    x = a @ w.double().t()
+    lse = torch.logsumexp(20.0 * torch.tanh(x / 20.0), dim=1)
+    lim = H * 2.0 ** -24 * (a.abs() @ w.double().abs().t()).amax(dim=1) + 2.0 ** -18 * (lse.abs() + 20.0)
+    assert ((out[1][1].double() - lse).abs() <= lim).all()
+
+
 def test_only_the_gradient_that_is_asked_for(built):
     c, h, w, targets, mask, loss, lse, grad, dh, dw = run(100, 700, 128, "mean")
     a, b = rlk.linear_ce_bwd(c, h, w, targets, mask, lse, grad, need_dweight=False)

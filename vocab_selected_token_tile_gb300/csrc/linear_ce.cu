@@ -14,8 +14,10 @@
 // partial, then a merge of each row's partials in vocabulary order.  Bound:
 // the tensor core, 2 T V H operations; the epilogue of one accumulator runs
 // under the MMAs of the other (4096 x 151936 x 4096: 2.37-2.54 ms, 2.0-2.15
-// PFLOP/s as the clock allows, the tensor pipe 96.5% busy).  Few tokens: the
-// weight's bytes (16 x 151936 x 1024: 65 us, 4.8 TB/s).
+// PFLOP/s as the clock allows, the tensor pipe 96.5% busy).  Hidden whose rows
+// lie between 128-byte lines is copied onto them first, as in the backward
+// below (1000 x 50257 x 1000: 95 -> 76 us).  Few tokens: the weight's bytes (16
+// x 151936 x 1024: 65 us, 4.8 TB/s).
 //
 // Backward, in pieces of the vocabulary: for each piece the logits are formed
 // again (the price of not keeping them: 2 T V H operations more) and leave
@@ -529,15 +531,15 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const CeRows p) {
 }
 
 // The active rows' hidden together, [.., Hs] with zeros past H and in the rows
-// up to the next whole tile; and zeros into the inactive rows of dHidden.  A
-// warp a row.
+// up to the next whole tile; and zeros into the inactive rows of dHidden.  Or,
+// without a count, every row's.  A warp a row.
 __global__ void __launch_bounds__(256) ce_gather_kernel(const uint16_t* hidden, int64_t ld, int H, int64_t T,
                                                         const int32_t* count, const int32_t* place, uint16_t* rows,
                                                         int64_t Hs, uint16_t* dhidden, int64_t ldh) {
     const int lane = threadIdx.x & 31;
-    const int64_t n = *count, whole = (n + 255) / 256 * 256;
+    const int64_t n = count ? *count : T, whole = count ? (n + 255) / 256 * 256 : T;
     for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < T + (whole - n); r += (int64_t)gridDim.x * 8) {
-        const int64_t to = r < T ? place[r] : n + (r - T);
+        const int64_t to = r >= T ? n + (r - T) : count ? place[r] : r;
         if (to < 0) {
             if (dhidden)
                 for (int c = lane * 8; c < H; c += 256) {
@@ -871,9 +873,16 @@ CePlan plan_of(const rlk_linear_ce_contract& c) {
 }
 
 struct CeLayout {
-    size_t loss, yt, part, part_y, fwd_end;
+    size_t loss, yt, part, part_y, all, fwd_end;
     size_t scale, count, index, place, rows, dx, sums, bwd_end;
 };
+
+// Whether the forward first copies hidden onto 128-byte lines, as the backward does: where its rows' stride puts them
+// between lines, and the product is large enough to repay the copy's launch and 4 T H bytes (50257 x 1000: 500 tokens
+// take 62 us without and 55 with it, 1000 take 95 and 76, 4000 take 273 and 225; 250 have 6 us to gain and 4 to pay).
+bool ce_copies(const rlk_linear_ce_contract& c) {
+    return c.hidden_stride % 64 != 0 && c.T > 1 && (double)c.T * (double)c.V * (double)c.H >= 25e9;
+}
 
 CeLayout layout_of(const rlk_linear_ce_contract& c) {
     CeLayout l{};
@@ -883,8 +892,9 @@ CeLayout layout_of(const rlk_linear_ce_contract& c) {
     l.yt = l.loss + up256(4 * T);
     l.part = l.yt + up256(4 * T);
     l.part_y = l.part + up256(8 * T * parts);
-    l.fwd_end = l.part_y + (c.label_smoothing != 0.f ? up256(4 * T * parts) : 0);
+    l.all = l.part_y + (c.label_smoothing != 0.f ? up256(4 * T * parts) : 0);
     const CePlan q = plan_of(c);
+    l.fwd_end = l.all + (ce_copies(c) ? up256(2 * T * (size_t)q.Hs) : 0);
     l.scale = at;
     l.count = l.scale + 16;
     l.index = l.scale + 256;
@@ -958,6 +968,14 @@ CeParams ce_params(const rlk_linear_ce_contract& c, const int64_t* targets, cons
     return p;
 }
 
+void launch_gather(const rlk_linear_ce_contract& c, const void* hidden, const int32_t* count, const int32_t* place,
+                   uint16_t* rows, int64_t Hs, void* dhidden, int sms, cudaStream_t st) {
+    const int64_t blocks = ceil_div(c.T + 255, 8);
+    ce_gather_kernel<<<(unsigned)(blocks < 8 * sms ? blocks : 8 * sms), 256, 0, st>>>(
+        static_cast<const uint16_t*>(hidden), c.hidden_stride, (int)c.H, c.T, count, place, rows, Hs,
+        static_cast<uint16_t*>(dhidden), c.dhidden_stride);
+}
+
 const char kMapFailed[] = "cuTensorMapEncodeTiled failed for an operand of the linear cross entropy";
 
 }  // namespace
@@ -983,8 +1001,15 @@ rlk_status launch_linear_ce_fwd(const rlk_linear_ce_contract& c, const void* hid
     p.yt = reinterpret_cast<float*>(ws + l.yt);
     p.ch0 = 0;
     p.nch = (int32_t)ceil_div(c.V, kBN);
+    int64_t width = c.H, stride = c.hidden_stride;
+    if (ce_copies(c)) {
+        uint16_t* all = reinterpret_cast<uint16_t*>(ws + l.all);
+        width = stride = plan_of(c).Hs;
+        launch_gather(c, hidden, nullptr, nullptr, all, width, nullptr, sms, st);
+        hidden = all;
+    }
     CUtensorMap tmH, tmW;
-    if (!make_map(&tmH, hidden, c.H, c.T, c.hidden_stride, kBK, (uint32_t)p.box_rows) ||
+    if (!make_map(&tmH, hidden, width, c.T, stride, kBK, (uint32_t)p.box_rows) ||
         !make_map(&tmW, weight, c.H, c.V, c.weight_stride, kBK, 128))
         return fail(RLK_ERR_CUDA, kMapFailed);
     const bool cap = c.softcap > 0.f, smooth = c.label_smoothing != 0.f;
@@ -1043,10 +1068,7 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     r.mask_mode = c.mask_mode;
     r.reduction = c.reduction;
     ce_rows_kernel<<<1, 1024, 0, st>>>(r);
-    const int64_t gather = ceil_div(c.T + 255, 8);
-    ce_gather_kernel<<<(unsigned)(gather < 8 * sms ? gather : 8 * sms), 256, 0, st>>>(
-        static_cast<const uint16_t*>(hidden), c.hidden_stride, (int)c.H, c.T, r.count, r.place, rows, q.Hs,
-        static_cast<uint16_t*>(dhidden), c.dhidden_stride);
+    launch_gather(c, hidden, r.count, r.place, rows, q.Hs, dhidden, sms, st);
     if ((s = ce_cuda("linear cross entropy: rows")) != RLK_OK) return s;
 
     if (!allow_dynamic_smem<ce_grads_kernel>(kCeSmem))
