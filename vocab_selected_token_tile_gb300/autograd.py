@@ -140,7 +140,8 @@ class LinearCrossEntropy(torch.autograd.Function):
         if grad_loss is None:
             return None, None, None, None, None
         hidden, weight, targets, mask, lse = ctx.saved_tensors
-        g = grad_loss.to(torch.float32).contiguous()
+        g = grad_loss if grad_loss.dtype is torch.float32 and grad_loss.is_contiguous() else \
+            grad_loss.to(torch.float32).contiguous()
         dh, dw = linear_ce_bwd(ctx.contract, hidden, weight, targets, mask, lse, g, ctx.needs_input_grad[0],
                                ctx.needs_input_grad[1])
         return dh, dw, None, None, None

@@ -479,6 +479,7 @@ struct CeRows {
     int32_t* count;
     int32_t* index;  // [T] the active rows, in order
     int32_t* place;  // [T] a row's place among them, -1 for an inactive one
+    uint32_t* status;
     int64_t T, ignore_index;
     int32_t mask_mode, reduction;
 };
@@ -488,33 +489,41 @@ struct CeRows {
 // or the largest finite magnitude of the rows' gradients (a non-finite one
 // stays its own row's).  One CTA.
 __global__ void __launch_bounds__(1024) ce_rows_kernel(const CeRows p) {
-    __shared__ int counts[32];
+    constexpr int kRuns = 4;  // 1024 rows each, loaded together
+    __shared__ int counts[kRuns][32];
     __shared__ float tops[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) *p.status = 0;  // of this call; what sets it runs later
     int n = 0;
     float top = 0.f;
-    for (int64_t r0 = 0; r0 < p.T; r0 += 1024) {
-        const int64_t r = r0 + threadIdx.x;
-        const bool on = r < p.T && ce_active(p.mask, p.mask_mode, p.ignore_index,
-                                             p.mask_mode == RLK_MASK_EXPLICIT ? 0 : p.targets[r], r);
-        const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, on);
-        if (lane == 0) counts[warp] = __popc(ballot);
+    for (int64_t r0 = 0; r0 < p.T; r0 += kRuns * 1024) {
+        uint32_t on[kRuns];  // of the warp's 32 rows
+#pragma unroll
+        for (int j = 0; j < kRuns; ++j) {
+            const int64_t r = r0 + j * 1024 + threadIdx.x;
+            on[j] = __ballot_sync(0xFFFFFFFFu, r < p.T && ce_active(p.mask, p.mask_mode, p.ignore_index,
+                                                                    p.mask_mode == RLK_MASK_EXPLICIT ? 0 : p.targets[r],
+                                                                    r));
+            if (lane == 0) counts[j][warp] = __popc(on[j]);
+        }
         __syncthreads();
-        int before = 0, all = 0;
-        for (int w = 0; w < 32; ++w) {
-            before += w < warp ? counts[w] : 0;
-            all += counts[w];
-        }
-        const int at = n + before + __popc(ballot & ((1u << lane) - 1u));
-        if (r < p.T) p.place[r] = on ? at : -1;
-        if (on) {
-            p.index[at] = (int32_t)r;
-            if (p.reduction == RLK_REDUCE_NONE) {
-                const float g = fabsf(p.grad[r]);
-                if (g < INFINITY) top = fmaxf(top, g);
+#pragma unroll
+        for (int j = 0; j < kRuns; ++j) {
+            const int64_t r = r0 + j * 1024 + threadIdx.x;
+            const int c = counts[j][lane];
+            const int before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? c : 0);
+            const bool mine = on[j] >> lane & 1u;
+            const int at = n + before + __popc(on[j] & ((1u << lane) - 1u));
+            if (r < p.T) p.place[r] = mine ? at : -1;
+            if (mine) {
+                p.index[at] = (int32_t)r;
+                if (p.reduction == RLK_REDUCE_NONE) {
+                    const float g = fabsf(p.grad[r]);
+                    if (g < INFINITY) top = fmaxf(top, g);
+                }
             }
+            n += __reduce_add_sync(0xFFFFFFFFu, c);
         }
-        n += all;
         __syncthreads();
     }
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
@@ -1052,7 +1061,6 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     const CePlan q = plan_of(c);
     char* ws = static_cast<char*>(workspace);
     uint32_t* status = static_cast<uint32_t*>(workspace);
-    if (cudaMemsetAsync(ws, 0, sizeof(uint32_t), st) != cudaSuccess) return ce_cuda("clearing the status word");
     float* scale = reinterpret_cast<float*>(ws + l.scale);
     uint16_t* rows = reinterpret_cast<uint16_t*>(ws + l.rows);
     CeRows r{};
@@ -1063,6 +1071,7 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     r.count = reinterpret_cast<int32_t*>(ws + l.count);
     r.index = reinterpret_cast<int32_t*>(ws + l.index);
     r.place = reinterpret_cast<int32_t*>(ws + l.place);
+    r.status = status;
     r.T = c.T;
     r.ignore_index = c.ignore_index;
     r.mask_mode = c.mask_mode;
