@@ -189,6 +189,32 @@ def test_rows_between_lines_give_the_same(built):
     assert ((out[1][1].double() - lse).abs() <= lim).all()
 
 
+def test_weight_past_2_to_31_elements(built):
+    T, V, H = 40, 560000, 4000  # 2.24e9 elements
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    h = torch.randn((T, H), generator=gen, device="cuda").to(torch.bfloat16)
+    w = torch.empty((V, H), dtype=torch.bfloat16, device="cuda").normal_(0.0, 0.02, generator=gen)
+    rows = torch.tensor([0, 3, 280000, 536871, V - 1], device="cuda")
+    some = torch.arange(T, device="cuda") % len(rows)
+    c = rlk.linear_ce_contract(h, w, reduction=rlk.REDUCE_SUM, validate=1)
+    loss, lse = rlk.linear_ce_fwd(c, h, w, rows[some])
+    parts = [torch.logsumexp(h.double() @ w[v:v + 40000].double().t(), dim=1) for v in range(0, V, 40000)]
+    want = torch.logsumexp(torch.stack(parts), dim=0)
+    # FP32 sums of H products: H 2^-24 of their magnitudes' sum at the worst, and that is under 5 H 0.02
+    lim = H * 2.0 ** -24 * 5 * H * 0.02 + 2.0 ** -18 * (want.abs() + 20.0)
+    assert ((lse.double() - want).abs() <= lim).all()
+    one = torch.ones((), device="cuda")
+    dh, dw = rlk.linear_ce_bwd(c, h, w, rows[some], None, lse, one)
+    # a row of dweight depends on its own row of weight and on lse: the same bits from those rows alone
+    few = w[rows].contiguous()
+    c2 = rlk.linear_ce_contract(h, few, reduction=rlk.REDUCE_SUM, validate=1)
+    _, dw2 = rlk.linear_ce_bwd(c2, h, few, some, None, lse, one)
+    assert torch.equal(dw[rows], dw2)
+    assert torch.isfinite(dh).all()
+
+
 def test_only_the_gradient_that_is_asked_for(built):
     c, h, w, targets, mask, loss, lse, grad, dh, dw = run(100, 700, 128, "mean")
     a, b = rlk.linear_ce_bwd(c, h, w, targets, mask, lse, grad, need_dweight=False)

@@ -20,7 +20,7 @@
 // the epilogue of a group, which reads back 128 KB of accumulator a CTA (256
 // clocks of the tensor-memory port) and scales and adds it (128 issue slots of
 // packed pairs a scheduler, twice that with B's scales by the row), takes about
-// 900 clocks with block scales and 1,250 with row scales, from one accumulator's
+// 850-900 clocks with block scales and 1,200-1,250 with row scales, from one accumulator's
 // completion to the next: it is what bounds both.  8192 x 8192 x 8192: 390 us
 // (2.8 PFLOP/s, tensor pipe 55% busy) and 548 us (2.0 PFLOP/s, 38%).  Roles:
 // warp 0 issues the TMA loads, warp 1 of the even CTA the pair's MMAs, warp 2

@@ -324,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
                 const int64_t hot = target - (cbase + sub * 32);
                 const bool here = active && hot >= 0 && hot < nv;
                 const uint32_t hot_bit = here ? 1u << (int)hot : 0u;  // an index into v would spill it
-                if (MODE == kCeForward) {
+                if constexpr (MODE == kCeForward) {
                     if (CAP) {
                         float slope;
 #pragma unroll
@@ -338,20 +338,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
                             if (hot_bit & (1u << i)) yt = v[i];
                         p.yt[row] = yt;
                     }
-                    continue;
-                }
+                } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float slope = 1.f;
-                    const float y = CAP ? ce_cap(v[i], p.cap, p.icap, slope) : v[i];
-                    float d = __fmaf_rn(ex2_approx(__fmaf_rn(y, kLog2e, nlL)), qa, -qc);
-                    if (hot_bit & (1u << i)) d = __fsub_rn(d, qb);
-                    if (CAP) d = __fmul_rn(d, slope);
-                    v[i] = active ? d : 0.f;
+                    for (int i = 0; i < 32; ++i) {
+                        float slope = 1.f;
+                        const float y = CAP ? ce_cap(v[i], p.cap, p.icap, slope) : v[i];
+                        float d = __fmaf_rn(ex2_approx(__fmaf_rn(y, kLog2e, nlL)), qa, -qc);
+                        if (hot_bit & (1u << i)) d = __fsub_rn(d, qb);
+                        if (CAP) d = __fmul_rn(d, slope);
+                        v[i] = active ? d : 0.f;
+                    }
+                    // rows past the active ones are zero: dWeight's K range ends on a whole block of 64
+                    ce_store(out, lane, v, dx + row0 * ldx + (cbase - (int64_t)p.ch0 * kBN) + sub * 32, ldx,
+                             (int)min((int64_t)32, p.T - row0), nv);
                 }
-                // rows past the active ones are zero: dWeight's K range ends on a whole block of 64
-                ce_store(out, lane, v, dx + row0 * ldx + (cbase - (int64_t)p.ch0 * kBN) + sub * 32, ldx,
-                         (int)min((int64_t)32, p.T - row0), nv);
             }
             tc_fence_before();
             __syncwarp();
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(const uint16_t* hidden, 
                 }
             continue;
         }
-#pragma unroll 4
+#pragma unroll 2
         for (int c = lane * 8; c < Hs; c += 256) {
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (r < T && c < H) {
