@@ -16,15 +16,16 @@
 // gemm_kernel, 256 x 256 tiles by pairs of CTAs (rlk_pair.cuh), persistent, one
 // CTA per SM.  A pair halves what a CTA's MMAs read of B from shared memory (a
 // first kernel, single CTAs with 128 x 256 tiles, took 452 us at 8192 x 12288 x
-// 4096; this one 312).  Floor: the tensor core, 2 M N K operations.  A group's four MMAs take 512 clocks;
-// the epilogue of a group, which reads back 128 KB of accumulator a CTA (256
-// clocks of the tensor-memory port) and scales and adds it (128 issue slots of
-// packed pairs a scheduler, twice that with B's scales by the row), takes about
-// 850-900 clocks with block scales and 1,200-1,250 with row scales, from one accumulator's
-// completion to the next: it is what bounds both.  8192 x 8192 x 8192: 390 us
-// (2.8 PFLOP/s, tensor pipe 55% busy) and 548 us (2.0 PFLOP/s, 38%).  Roles:
-// warp 0 issues the TMA loads, warp 1 of the even CTA the pair's MMAs, warp 2
-// fetches the scales with cp.async (4 bytes each: a row of scales starts at any
+// 4096; this one 312).  Floor: the tensor core, 2 M N K operations.  A group's
+// four MMAs take 512 clocks; from one accumulator's completion to the next it
+// is 850-900 with block scales and 1,200-1,250 with row scales.  The epilogue
+// of a group reads back 128 KB of accumulator a CTA (256 clocks of the
+// tensor-memory port), scales and adds it (128 packed operations a scheduler,
+// twice that and 32 KB of shared memory with row scales), and hands it back,
+// and tensor memory holds two accumulators.  8192 x 8192 x 8192: 390 us (2.8
+// PFLOP/s, tensor pipe 55% busy) and 548 us (2.0 PFLOP/s, 38%).  Roles: warp 0
+// issues the TMA loads, warp 1 of the even CTA the pair's MMAs, warp 2 fetches
+// the scales with cp.async (4 bytes each: a row of scales starts at any
 // multiple of 4), warps 4-11 are the epilogue (a warp reads 32 tensor-memory
 // lanes and 128 of the 256 columns: 128 sums a thread, which is why the first
 // warpgroup gives registers away with setmaxnreg).  Sixteen epilogue warps of
@@ -505,7 +506,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
                     const float *a = p.sa + (int64_t)kg * p.M, *b = p.sb + (int64_t)kg * p.nsb;
                     for (int kb = kg; kb < min(kg + kGroups, k1); ++kb) {
 #pragma unroll
-                        for (int i = 0; i < kGM; i += 32) cp_async4(dst + i * 4, a + (row + i < p.M ? row + i : 0), row + i < p.M);
+                        for (int i = 0; i < kGM; i += 32)
+                            cp_async4(dst + i * 4, a + (row + i < p.M ? row + i : 0), row + i < p.M);
                         if (BROWS) {
 #pragma unroll
                             for (int i = 0; i < kGN; i += 32)
