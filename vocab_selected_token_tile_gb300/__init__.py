@@ -862,13 +862,13 @@ def _codes(x, rows, cols):
     (8000 x 3517: written in 22.6 us against 23.4; as a weight of 37 tokens read in 40.5 us against 41.8).
     """
     stride = -(-cols // 128) * 128 if cols % 16 and cols >= 2048 else -(-cols // 16) * 16
-    t = _new(x, rows, stride, _t().float8_e4m3fn)
-    return (t if stride == cols else t[:, :cols]), stride
+    return _new(x, rows, cols, _t().float8_e4m3fn, stride), stride
 
 
-def _new(x, rows, cols, dtype):
-    """A contiguous [rows, cols] tensor on x's device (empty_strided takes half the host time of new_empty)."""
-    return _t().empty_strided((rows, cols), (cols, 1), dtype=dtype, device=x.device)
+def _new(x, rows, cols, dtype, stride=None):
+    """A [rows, cols] tensor on x's device, contiguous or with rows `stride` apart (empty_strided takes half the host
+    time of new_empty, and a slice of a wider tensor several times that)."""
+    return _t().empty_strided((rows, cols), (cols if stride is None else stride, 1), dtype=dtype, device=x.device)
 
 
 def _quantize(x, block_rows, rowwise, transposed, stream):
@@ -1066,12 +1066,8 @@ def linear_ce_bwd(contract, hidden, weight, targets, mask, lse, grad_loss, need_
     pl = _vector(lse, "lse", T, f32)
     pg = _vector(grad_loss, "grad_loss", T if contract.reduction == REDUCE_NONE else 1, f32)
 
-    def out(rows, stride):
-        t = _new(hidden, rows, stride or H, hidden.dtype)
-        return t if t.shape[1] == H else t[:, :H]
-
-    dh = out(T, contract.dhidden_stride) if need_dhidden else None
-    dw = out(V, contract.dweight_stride) if need_dweight else None
+    dh = _new(hidden, T, H, hidden.dtype, contract.dhidden_stride or H) if need_dhidden else None
+    dw = _new(hidden, V, H, hidden.dtype, contract.dweight_stride or H) if need_dweight else None
     ws = _ce_workspace(contract, 1, hidden, workspace)
     _used_on(stream, dh, dw, ws)
     status = rlk_linear_ce_bwd(contract, *operands, pl, pg, _ptr(dh), _ptr(dw), ws.data_ptr(),
