@@ -523,7 +523,8 @@ rlk_status rlk_linear_ce_fwd(const rlk_linear_ce_contract* contract, const void*
  *              one of the two.  16-byte aligned, strides a multiple of 8.
  * Inactive rows have a zero dhidden and add nothing to dweight.  The logits'
  * gradient is rounded to BF16 between the products, with a summed or averaged
- * loss's common factor left out of it and applied to the FP32 sums.  The
+ * loss's common factor (and 1 - label_smoothing, if that is not 0) left out of
+ * it and applied to the FP32 sums.  The
  * order of every sum is fixed.  No output may overlap an input.
  */
 rlk_status rlk_linear_ce_bwd(const rlk_linear_ce_contract* contract, const void* hidden_bf16, const void* weight_bf16,

@@ -35,11 +35,12 @@
 // written once a piece, and with pieces that large that traffic and the ends
 // of the launches are under 2% of a piece's time.
 //
-// What is rounded to BF16 is dx / scale, with scale = the upstream gradient of
-// a summed or averaged loss (the largest row's otherwise): with a common
-// factor folded in, the value of every row's largest entry, about -g, would
-// be rounded in the same direction, a bias of up to 2^-8 in both gradients.
-// The scale multiplies the FP32 sums instead.
+// What is rounded to BF16 is dx / scale, with scale = (1 - eps) times the
+// upstream gradient of a summed or averaged loss (the largest row's otherwise):
+// with that common factor folded in, the value of every row's largest entry,
+// about -(1 - eps) g, would be rounded in the same direction, a bias of up to
+// 2^-8 in both gradients (eps = 0.1 alone: -0.9 becomes -0.8984, 0.17% off in
+// every row of dWeight).  The scale multiplies the FP32 sums instead.
 //
 // Both GEMM kernels run as CTA pairs (rlk_pair.cuh) on 256 x 256 tiles: warp 0
 // issues the TMA loads, warp 1 of the even CTA the MMAs, warps 2-9 are the
@@ -96,6 +97,7 @@ struct CeParams {
     PipeWait w;
     int64_t T, V, ignore_index;
     float cap, icap, eps, z;
+    float unit;          // 1 / (1 - eps): a row's own factor in dx under a summed or averaged loss  gradient
     int32_t KB, mask_mode;
     int32_t ch0, nch;  // the launch's chunks of 256 vocabulary rows
     int32_t MB, MBg;   // blocks of 256 tokens, and per band
@@ -300,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
                 // dx / scale = (qa p - qc - qb [c = t]) slope
                 const int64_t at = p.index[row];
                 const float l = p.lse[at];
-                const float g = p.grad ? __fdiv_rn(p.grad[at], scale) : 1.f;
+                const float g = p.grad ? __fdiv_rn(p.grad[at], scale) : p.unit;
                 target = p.targets[at];
                 active = true;
                 qa = g * (1.f + 2.f * p.z * l);
@@ -482,12 +484,13 @@ struct CeRows {
     uint32_t* status;
     int64_t T, ignore_index;
     int32_t mask_mode, reduction;
+    float keep;  // 1 - eps, the target's share of the loss
 };
 
 // The active rows in order, and the factor that is left out of every row's dx:
 // the gradient of a summed loss, that of an averaged one over the active rows,
 // or the largest finite magnitude of the rows' gradients (a non-finite one
-// stays its own row's).  One CTA.
+// stays its own row's), each times 1 - eps.  One CTA.
 __global__ void __launch_bounds__(1024) ce_rows_kernel(const CeRows p) {
     constexpr int kRuns = 4;  // 1024 rows each, loaded together
     __shared__ int counts[kRuns][32];
@@ -533,9 +536,11 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(const CeRows p) {
     *p.count = n;
     if (p.reduction == RLK_REDUCE_NONE) {
         for (int w = 1; w < 32; ++w) top = fmaxf(top, tops[w]);
-        *p.scale = top == 0.f ? 1.f : top;
+        const float s = __fmul_rn(top, p.keep);  // 0 where the product underflows
+        *p.scale = s != 0.f ? s : top != 0.f ? top : 1.f;
     } else {
-        *p.scale = p.reduction == RLK_REDUCE_SUM ? p.grad[0] : n > 0 ? (float)((double)p.grad[0] / (double)n) : 0.f;
+        const float g = p.reduction == RLK_REDUCE_SUM ? p.grad[0] : n > 0 ? (float)((double)p.grad[0] / (double)n) : 0.f;
+        *p.scale = __fmul_rn(g, p.keep);
     }
 }
 
@@ -915,6 +920,9 @@ CeLayout layout_of(const rlk_linear_ce_contract& c) {
     return l;
 }
 
+// The target's share of the loss, which dx leaves out; all of the loss is the uniform distribution's at eps = 1.
+float ce_keep(const rlk_linear_ce_contract& c) { return c.label_smoothing < 1.f ? 1.f - c.label_smoothing : 1.f; }
+
 rlk_status ce_cuda(const char* what) {
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? RLK_OK : fail(RLK_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
@@ -968,6 +976,7 @@ CeParams ce_params(const rlk_linear_ce_contract& c, const int64_t* targets, cons
     p.icap = c.softcap > 0.f ? 1.f / c.softcap : 0.f;
     p.eps = c.label_smoothing;
     p.z = c.z_loss;
+    p.unit = 1.f / ce_keep(c);
     p.KB = (int32_t)ceil_div(c.H, kBK);
     p.mask_mode = c.mask_mode;
     p.MB = (int32_t)ceil_div(c.T, 256);
@@ -1076,6 +1085,7 @@ rlk_status launch_linear_ce_bwd(const rlk_linear_ce_contract& c, const void* hid
     r.ignore_index = c.ignore_index;
     r.mask_mode = c.mask_mode;
     r.reduction = c.reduction;
+    r.keep = ce_keep(c);
     ce_rows_kernel<<<1, 1024, 0, st>>>(r);
     launch_gather(c, hidden, r.count, r.place, rows, q.Hs, dhidden, sms, st);
     if ((s = ce_cuda("linear cross entropy: rows")) != RLK_OK) return s;
