@@ -154,15 +154,16 @@ __device__ __forceinline__ void ce_unit(const CeParams& p, int MB, uint32_t u, i
     mb = (int)(b * p.MBg + r % w);
 }
 
-// y = cap tanh(x / cap) with r = 2 / (e^(2 |x| / cap) + 1): tanh = sign (1 - r),
-// within a few 2^-24 of 1 absolutely, which the cap scales to a few 10^-6 of a
-// logit; and its slope 1 - tanh^2 = r (2 - r), which keeps its relative
-// precision where tanh saturates.
+// y = cap tanh(x / cap), to a few 2^-24 of y whatever the cap: from u = |x| / cap = 1/2 on as cap (1 - r) with
+// r = 2 / (e^(2 u) + 1), below it (where that difference loses y's digits, 10^-7 cap of them) as |x| (1 + u^2 q(u^2)),
+// q interpolating (tanh(u) / u - 1) / u^2 in u^2 at the four Chebyshev nodes of [0, 1/4]: 2^-24 off at most.  And its
+// slope 1 - tanh^2 = r (2 - r), which keeps its relative precision where tanh saturates.
 __device__ __forceinline__ float ce_cap(float x, float cap, float icap, float& slope) {
-    const float e = ex2_approx(__fmul_rn(__fmul_rn(fabsf(x), icap), 2.f * kLog2e));
-    const float r = __fdividef(2.f, __fadd_rn(e, 1.f));
+    const float a = fabsf(x), u = __fmul_rn(a, icap), w = __fmul_rn(u, u);
+    const float r = __fdividef(2.f, __fadd_rn(ex2_approx(__fmul_rn(u, 2.f * kLog2e)), 1.f));
+    const float q = __fmaf_rn(__fmaf_rn(__fmaf_rn(0.017988745f, w, -0.05338711f), w, 0.13330476f), w, -0.3333331f);
     slope = __fmul_rn(r, __fsub_rn(2.f, r));
-    return copysignf(__fmul_rn(cap, __fsub_rn(1.f, r)), x);
+    return copysignf(u < 0.5f ? __fmaf_rn(__fmul_rn(q, w), a, a) : __fmul_rn(cap, __fsub_rn(1.f, r)), x);
 }
 
 // One block of up to 32 logits into the row's running (max, sumexp, sum).
