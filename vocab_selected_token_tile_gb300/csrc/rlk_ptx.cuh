@@ -366,6 +366,13 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// 1 / x on the special-function unit (within 1 ulp; subnormal results flushed to 0).
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Packed FP32 pair arithmetic (PTX fma/add/mul .rn.f32x2, sm_100+): one
 // instruction for both lanes of the pair, each rounded exactly as the scalar
 // operation would be.  The pair travels as one 64-bit register pair.
