@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             const bool one = elect_one();
             const uint32_t full0 = mapa_shared(smem_u32(&bars->full[0]), (uint32_t)leader);
             Ring r;
-            int issued = 0;
+            uint64_t issued = 0;
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
                 int mb, nb;
@@ -451,20 +451,19 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 const int a_row = (2 * mb + rank) * kGM, b_row = nb * kGN + rank * (kGN / 2);
                 // a CTA without a row of its own loads none: its rows of the accumulator are not used
                 const bool mine = a_row < p.M;
-                const uint32_t bytes = 2 * kGB + ((2 * mb + 1) * kGM < p.M ? 2 : 1) * kGA;
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!(ok = pipe_wait(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
+                    if (!(ok = pipe_wait_warp(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                     if (one) {
                         const uint32_t fb = full0 + r.slot * 8;
-                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars->full[r.slot]), bytes);
+                        pair_arm(fb, smem_u32(&bars->full[r.slot]), rank, kGB + (mine ? kGA : 0));
                         if (mine) tma_load_2d_pair(smem_u32(sA + r.slot * kGA), &tmA, kb * kGK, a_row, fb);
                         tma_load_2d_pair(smem_u32(sB + r.slot * kGB), &tmB, kb * kGK, b_row, fb);
                     }
-                    issued = min(issued + 1, kGStages);
+                    ++issued;
                     r.next(kGStages);
                 }
             }
-            pair_drain_copies(bars, r, issued, rank, p.w);
+            pair_end_copies(bars, r, one, issued, ok, p.w);
         } else if (warp == 1 && rank == 0) {
             // ------------------------------------------------ MMA issuer of the pair
             const bool one = elect_one();
@@ -475,8 +474,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
             for (int t = first; ok && t < tiles; t += step) {
                 for (int kb = k0; kb < k1; ++kb) {
                     // the operands first: theirs are ready early, so only the accumulator's wait is in its way
-                    if (!(ok = pipe_wait(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
-                    if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
+                    if (!(ok = pipe_wait_warp(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                    if (!(ok = pipe_wait_warp(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
                     tc_fence_after();
                     if (one) {
 #pragma unroll
@@ -491,7 +490,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                     acc.next(2);
                 }
             }
-            pair_drain_mmas(bars, one, p.w, both);
+            pair_end_mmas(bars, acc, one, ok, p.w, both);
         } else if (warp == 2) {
             // ------------------------------------------------ scales
             Ring r;
@@ -501,7 +500,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 tile_of(p, t, mb, nb);
                 const int row = (2 * mb + rank) * kGM + lane, col = nb * kGN + lane;
                 for (int kg = k0; kg < k1; kg += kGroups) {
-                    ok = __all_sync(0xFFFFFFFFu, pipe_wait(ab, smem_u32(&all->sempty[r.slot]), r.phase ^ 1u, p.w));
+                    ok = pipe_wait_warp(ab, smem_u32(&all->sempty[r.slot]), r.phase ^ 1u, p.w);
                     if (!ok) break;
                     uint32_t dst = smem_u32(scales + r.slot * kGroups * kGScales<BROWS>) + lane * 4;
                     const float *a = p.sa + (int64_t)kg * p.M, *b = p.sb + (int64_t)kg * p.nsb;
@@ -685,7 +684,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
         }
     }
     if (tile0 > 0) grid_wait_prior();  // what follows in the stream follows both launches
-    pair_end(tmem, warp);
+    pair_end(bars, tmem, warp, p.w);
 }
 
 // ----------------------------------------------------------------- few rows of A

@@ -239,7 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
         const uint32_t full0 = mapa_shared(smem_u32(&bars->full[0]), 0);
         const uint64_t keep = l2_policy_evict_last();
         Ring r;
-        int issued = 0;
+        uint64_t issued = 0;
         bool ok = true;
         for (uint32_t u = first; ok && u < total; u += step) {
             int ch, mb;
@@ -247,20 +247,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
             // a CTA without a row of its own loads no hidden: its rows of the accumulator are not used
             const int row = (2 * mb + rank) * 128;
             const bool mine = row < T;
-            const uint32_t bytes = 2 * kCeB + (uint32_t)p.box_rows * 128 * ((2 * mb + 1) * (int64_t)128 < T ? 2 : 1);
+            const uint32_t bytes = kCeB + (mine ? (uint32_t)p.box_rows * 128 : 0);
             for (int kb = 0; kb < p.KB; ++kb) {
-                if (!(ok = pipe_wait(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
+                if (!(ok = pipe_wait_warp(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                 if (one) {
                     const uint32_t fb = full0 + r.slot * 8;
-                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&bars->full[r.slot]), bytes);
+                    pair_arm(fb, smem_u32(&bars->full[r.slot]), rank, bytes);
                     if (mine) tma_load_2d_pair_hint(smem_u32(m.a + r.slot * kCeA), &tmH, kb * kBK, row, fb, keep);
                     tma_load_2d_pair(smem_u32(m.b + r.slot * kCeB), &tmW, kb * kBK, ch * kBN + rank * 128, fb);
                 }
-                issued = min(issued + 1, kCeStages);
+                ++issued;
                 r.next(kCeStages);
             }
         }
-        pair_drain_copies(bars, r, issued, rank, p.w);
+        pair_end_copies(bars, r, one, issued, ok, p.w);
     } else if (warp == 1 && rank == 0) {
         const bool one = elect_one();
         const uint64_t da = smem_desc_sw128(smem_u32(m.a)), db = smem_desc_sw128(smem_u32(m.b));
@@ -268,10 +268,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
         Ring r, acc;
         bool ok = true;
         for (uint32_t u = first; ok && u < total; u += step) {
-            if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
+            if (!(ok = pipe_wait_warp(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
             const uint32_t d = tmem + (uint32_t)(acc.slot * kBN);
             for (int kb = 0; kb < p.KB; ++kb) {
-                if (!(ok = pipe_wait(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                if (!(ok = pipe_wait_warp(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
                 tc_fence_after();
                 if (one) {
 #pragma unroll
@@ -286,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
             }
             acc.next(2);
         }
-        pair_drain_mmas(bars, one, p.w);
+        pair_end_mmas(bars, acc, one, ok, p.w);
     } else if (warp >= 2) {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -379,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
             }
         }
     }
-    pair_end(tmem, warp);
+    pair_end(bars, tmem, warp, p.w);
 }
 
 // (m, s) with (m2, s2): the larger maximum, both sums scaled to it; a maximum
@@ -707,7 +707,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
         const bool one = elect_one();
         const uint32_t full0 = mapa_shared(smem_u32(&bars->full[0]), 0);
         Ring r;
-        int issued = 0;
+        uint64_t issued = 0;
         bool ok = true;
         for (int i = 0, u; ok && (u = ce_walk(deal, i, pair, pairs)) >= 0; ++i) {
             const CeTile t = ce_tile(p, deal, u);
@@ -715,12 +715,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
             // (the active rows' hidden is padded with zeros to whole blocks)
             const bool box3 = t.wide == 2 && (t.prob == 1 || p.H % 64 == 0 || p.H - t.nb * kBN >= kBN);
             for (int kb = t.k0; kb < t.k1; ++kb) {
-                if (!(ok = pipe_wait(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
+                if (!(ok = pipe_wait_warp(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                 if (one) {
                     const uint32_t fb = full0 + r.slot * 8;
                     const uint32_t a = smem_u32(m.a + r.slot * kCeA), b = smem_u32(m.b + r.slot * kCeB);
-                    if (rank == 0)
-                        mbar_arrive_expect_tx(smem_u32(&bars->full[r.slot]), 2 * (kCeA + (uint32_t)t.wide * kMnBlock));
+                    pair_arm(fb, smem_u32(&bars->full[r.slot]), rank, kCeA + (uint32_t)t.wide * kMnBlock);
                     if (t.prob == 0) {
                         tma_load_2d_pair(a, &tmA0, kb * kBK, m0, fb);
                     } else {
@@ -734,11 +733,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
                             tma_load_2d_pair(b + j * kMnBlock, t.prob ? &tmC1 : &tmC0, h0 + j * 64, kb * kBK, fb);
                     }
                 }
-                issued = min(issued + 1, kCeStages);
+                ++issued;
                 r.next(kCeStages);
             }
         }
-        pair_drain_copies(bars, r, issued, rank, p.w);
+        pair_end_copies(bars, r, one, issued, ok, p.w);
     } else if (warp == 1 && rank == 0) {
         const bool one = elect_one();
         const uint64_t dk = smem_desc_sw128(smem_u32(m.a)), dm = smem_desc_sw128_mn(smem_u32(m.a), kMnBlock, 1024);
@@ -747,7 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
         bool ok = true;
         for (int i = 0, u; ok && (u = ce_walk(deal, i, pair, pairs)) >= 0; ++i) {
             const CeTile t = ce_tile(p, deal, u);
-            if (!(ok = pipe_wait(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
+            if (!(ok = pipe_wait_warp(ab, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, p.w))) break;
             tc_fence_after();
             const uint32_t idesc = idesc_bf16_f32_major(256, (uint32_t)(128 * t.wide), t.prob == 1, true);
             const uint32_t d = tmem + (uint32_t)(acc.slot * kBN);
@@ -756,7 +755,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
             const uint64_t da = t.prob == 0 ? dk : dm;
             const int astep = t.prob == 0 ? 32 : 2048;
             for (int kb = t.k0; kb < t.k1; ++kb) {
-                if (!(ok = pipe_wait(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
+                if (!(ok = pipe_wait_warp(ab, smem_u32(&bars->full[r.slot]), r.phase, p.w))) break;
                 tc_fence_after();
                 if (one) {
 #pragma unroll
@@ -772,7 +771,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
             __syncwarp();
             acc.next(2);
         }
-        pair_drain_mmas(bars, one, p.w);
+        pair_end_mmas(bars, acc, one, ok, p.w);
     } else if (warp >= 2) {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -824,7 +823,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kCeThreads, 1)
             acc.next(2);
         }
     }
-    pair_end(tmem, warp);
+    pair_end(bars, tmem, warp, p.w);
 }
 
 // Up to 8 BF16 values of an output row; columns past H are not the row's.
