@@ -7,6 +7,7 @@ marshal torch tensors (allocate outputs, pass ``data_ptr()`` and the current
 stream).  Every step of the computation runs in the CUDA library: if it is
 missing or fails to load, these functions raise -- there is no fallback.
 """
+import contextlib
 import ctypes
 import os
 
@@ -807,6 +808,7 @@ def shard_bwd(contract, shard, logits_shard, targets, mask, lse, grad, dlogits=N
 # ------------------------------------------------------------------ FP8 projections
 
 _torch = None
+_HERE = contextlib.nullcontext()
 
 
 def _t():
@@ -823,13 +825,19 @@ def _raw_stream(t, stream):
     return stream.cuda_stream if stream is not None else _t()._C._cuda_getCurrentRawStream(t.device.index)
 
 
-def _used_on(stream, *tensors):
-    """Tells the allocator that a stream other than the current one uses these new tensors, so that their memory is
-    not handed out again before that stream's work is done."""
+def _allocating(stream):
+    """Within it, new tensors come from the memory of the given stream (None: the current one): the current stream's
+    may still be in use by work that is queued there."""
+    return _HERE if stream is None else _t().cuda.stream(stream)
+
+
+def _used_here(stream, *tensors):
+    """Tells the allocator that the current stream, too, uses these tensors of the given stream's memory, so that it is
+    not handed out again before the work queued here by then is done."""
     if stream is not None:
         for t in tensors:
             if t is not None:
-                t.record_stream(stream)
+                t.record_stream(_t().cuda.current_stream(t.device))
 
 
 def _matrix(t, name, dtypes):
@@ -879,17 +887,18 @@ def _quantize(x, block_rows, rowwise, transposed, stream):
     q = scale = qt = scale_t = None
     ldq = ldt = 0
     gr, gc = -(-R // 128), -(-C // 128)
-    if rowwise:
-        q, ldq = _codes(x, R, C)
-        scale = _new(x, gc, R if block_rows == 1 else gr, torch.float32)
-    if transposed:
-        qt, ldt = _codes(x, C, R)
-        scale_t = _new(x, gr, C if block_rows == 1 else gc, torch.float32)
+    with _allocating(stream):
+        if rowwise:
+            q, ldq = _codes(x, R, C)
+            scale = _new(x, gc, R if block_rows == 1 else gr, torch.float32)
+        if transposed:
+            qt, ldt = _codes(x, C, R)
+            scale_t = _new(x, gr, C if block_rows == 1 else gc, torch.float32)
     st = rlk_fp8_quantize(R, C, x.data_ptr(), RLK_F32 if x.dtype is torch.float32 else RLK_BF16, stride, block_rows,
                           _ptr(q), ldq, _ptr(scale), _ptr(qt), ldt, _ptr(scale_t), _raw_stream(x, stream))
     if st:
         check(st)
-    _used_on(stream, q, scale, qt, scale_t)
+    _used_here(stream, q, scale, qt, scale_t)
     return q, scale, qt, scale_t
 
 
@@ -912,17 +921,16 @@ def fp8_quantize_both(x, block_rows=1, stream=None):
 _fp8_workspaces = {}
 
 
-def _fp8_workspace(t, stream):
-    """The status word of a device and stream: zeroed once, only ever set by a call."""
-    key = (t.device.index, stream)
+def _fp8_workspace(t, raw, stream):
+    """The status word of a device and stream (``raw``: its handle): zeroed there once, only ever set by a call."""
+    key = (t.device.index, raw)
     ws = _fp8_workspaces.get(key)
     if ws is None:
         torch = _t()
-        ws = torch.zeros(RLK_FP8_WORKSPACE, dtype=torch.uint8, device=t.device)
-        if torch.cuda.is_current_stream_capturing():
-            return ws  # the graph's memory, not to be kept beyond it
-        if stream != torch._C._cuda_getCurrentRawStream(t.device.index):
-            torch.cuda.current_stream(t.device).synchronize()  # zeroed before the other stream's first call
+        with _allocating(stream):
+            ws = torch.zeros(RLK_FP8_WORKSPACE, dtype=torch.uint8, device=t.device)
+            if torch.cuda.is_current_stream_capturing():
+                return ws  # the graph's memory, not to be kept beyond it
         _fp8_workspaces[key] = ws
     return ws
 
@@ -960,8 +968,9 @@ def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=Non
         out_dtype = out_dtype or torch.bfloat16
         if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
             raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
-        out = _new(a, M, N, out_dtype)
-        _used_on(stream, out)
+        with _allocating(stream):
+            out = _new(a, M, N, out_dtype)
+        _used_here(stream, out)
         ldc = N
     else:
         rows, cols, ldc = _matrix(out, "out", (torch.bfloat16, torch.float32))
@@ -969,7 +978,7 @@ def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=Non
             raise ValueError(f"out is {str(out.dtype)[6:]} {list(out.shape)}; the product is [{M}, {N}]")
     st = _raw_stream(a, stream)
     if workspace is None:
-        workspace = _fp8_workspace(a, st)
+        workspace = _fp8_workspace(a, st, stream)
     else:
         _need(workspace, "workspace", RLK_FP8_WORKSPACE, ("uint8",))
     status = rlk_fp8_matmul(M, N, K, a.data_ptr(), _padded(lda, M, K, 16), pa, b.data_ptr(), _padded(ldb, N, K, 16),
@@ -1045,11 +1054,12 @@ def linear_ce_fwd(contract, hidden, weight, targets, mask=None, stream=None, wor
     operands = _ce_operands(contract, hidden, weight, targets, mask)
     f32 = _t().float32
     new = _t().empty_strided
-    loss = new((contract.T,), (1,), dtype=f32, device=hidden.device) if contract.reduction == REDUCE_NONE else \
-        new((), (), dtype=f32, device=hidden.device)
-    lse = new((contract.T,), (1,), dtype=f32, device=hidden.device)
-    ws = _ce_workspace(contract, 0, hidden, workspace)
-    _used_on(stream, loss, lse, ws)
+    with _allocating(stream):
+        loss = new((contract.T,), (1,), dtype=f32, device=hidden.device) if contract.reduction == REDUCE_NONE else \
+            new((), (), dtype=f32, device=hidden.device)
+        lse = new((contract.T,), (1,), dtype=f32, device=hidden.device)
+        ws = _ce_workspace(contract, 0, hidden, workspace)
+    _used_here(stream, loss, lse)
     status = rlk_linear_ce_fwd(contract, *operands, loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
                                _raw_stream(hidden, stream))
     if status:
@@ -1066,10 +1076,11 @@ def linear_ce_bwd(contract, hidden, weight, targets, mask, lse, grad_loss, need_
     pl = _vector(lse, "lse", T, f32)
     pg = _vector(grad_loss, "grad_loss", T if contract.reduction == REDUCE_NONE else 1, f32)
 
-    dh = _new(hidden, T, H, hidden.dtype, contract.dhidden_stride or H) if need_dhidden else None
-    dw = _new(hidden, V, H, hidden.dtype, contract.dweight_stride or H) if need_dweight else None
-    ws = _ce_workspace(contract, 1, hidden, workspace)
-    _used_on(stream, dh, dw, ws)
+    with _allocating(stream):
+        dh = _new(hidden, T, H, hidden.dtype, contract.dhidden_stride or H) if need_dhidden else None
+        dw = _new(hidden, V, H, hidden.dtype, contract.dweight_stride or H) if need_dweight else None
+        ws = _ce_workspace(contract, 1, hidden, workspace)
+    _used_here(stream, dh, dw)
     status = rlk_linear_ce_bwd(contract, *operands, pl, pg, _ptr(dh), _ptr(dw), ws.data_ptr(),
                                _raw_stream(hidden, stream))
     if status:
