@@ -948,8 +948,8 @@ def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=Non
 
     ``a_scale`` is [ceil(K / 128), M]; ``b_scale`` [ceil(K / 128), N] (b_block_rows 1) or [ceil(K / 128),
     ceil(N / 128)] (128).  The result is BF16 (or FP32 with ``out_dtype`` torch.float32), in ``out`` if given (its rows
-    may be strided); ``accumulate`` adds the product to an FP32 ``out``.  ``validate`` synchronises and raises if a
-    device-side wait expired.
+    may be strided); ``accumulate`` adds the product to an FP32 ``out``.  K = 0 is an empty sum: zeros, or ``out`` as it
+    was.  ``validate`` synchronises and raises if a device-side wait expired.
     """
     torch = _t()
     codes = (torch.float8_e4m3fn, torch.uint8)  # E4M3 values, or their codes as bytes
@@ -976,6 +976,13 @@ def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=Non
         rows, cols, ldc = _matrix(out, "out", (torch.bfloat16, torch.float32))
         if (rows, cols) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError(f"out is {str(out.dtype)[6:]} {list(out.shape)}; the product is [{M}, {N}]")
+    if K == 0:
+        if accumulate and out.dtype is not torch.float32:
+            raise TypeError("accumulate needs an FP32 out")
+        if not accumulate:
+            with _allocating(stream):
+                out.zero_()
+        return out
     st = _raw_stream(a, stream)
     if workspace is None:
         workspace = _fp8_workspace(a, st, stream)
