@@ -520,7 +520,8 @@ rlk_status rlk_linear_ce_fwd(const rlk_linear_ce_contract* contract, const void*
  *              gradient of the loss.
  *   dhidden    [T, dhidden_stride] BF16 out, or NULL (a frozen trunk);
  *   dweight    [V, dweight_stride] BF16 out, or NULL (a frozen head); at least
- *              one of the two.  16-byte aligned, strides a multiple of 8.
+ *              one of the two unless T = 0.  16-byte aligned, strides a
+ *              multiple of 8.
  * Inactive rows have a zero dhidden and add nothing to dweight.  The logits'
  * gradient is rounded to BF16 between the products, with a summed or averaged
  * loss's common factor (and 1 - label_smoothing, if that is not 0) left out of

@@ -1,9 +1,9 @@
-"""Layers of a batch without rows (an expert that received no token), on the GPU."""
+"""Layers and losses of a batch without rows (an expert that received no token), on the GPU."""
 import pytest
 import torch
 
 import vocab_selected_token_tile_gb300 as rlk
-from vocab_selected_token_tile_gb300.autograd import fp8_linear
+from vocab_selected_token_tile_gb300.autograd import fp8_linear, linear_cross_entropy
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,18 @@ def test_product_over_no_elements(built, dtype):
     assert (buf[:, :70] == 0).all() and (buf[:, 70:] == 5).all()
     total = torch.full((40, 70), 2.0, device="cuda")
     assert rlk.fp8_matmul(q, s, b, sb, b_block_rows=1, out=total, accumulate=True) is total and (total == 2).all()
+
+
+@pytest.mark.parametrize("reduction", ["none", "sum", "mean"])
+@pytest.mark.parametrize("need_h,need_w", [(True, True), (True, False), (False, True)])
+def test_cross_entropy_of_no_rows(built, reduction, need_h, need_w):
+    h = torch.empty((0, 96), dtype=torch.bfloat16, device="cuda", requires_grad=need_h)
+    w = torch.randn((50, 96), device="cuda").to(torch.bfloat16).requires_grad_(need_w)
+    t = torch.empty(0, dtype=torch.int64, device="cuda")
+    loss = linear_cross_entropy(h, w, t, None, reduction=reduction)
+    assert loss.shape == ((0,) if reduction == "none" else ()) and (loss == 0).all()
+    loss.sum().backward()
+    if need_h:
+        assert h.grad.shape == (0, 96)
+    if need_w:
+        assert (w.grad == 0).all()

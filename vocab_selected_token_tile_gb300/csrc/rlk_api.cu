@@ -1057,7 +1057,9 @@ RLK_EXPORT rlk_status rlk_linear_ce_bwd(const rlk_linear_ce_contract* contract, 
     if (s != RLK_OK) return s;
     const rlk_linear_ce_contract c = with_strides(*contract);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (!dhidden_bf16 && !dweight_bf16) return fail(RLK_ERR_INVALID_ARG, "dhidden or dweight is required");
+    // (the dhidden of no rows has no address)
+    if (!dhidden_bf16 && !dweight_bf16 && c.T > 0)
+        return fail(RLK_ERR_INVALID_ARG, "dhidden or dweight is required");
     if (!aligned16(dhidden_bf16) || !aligned16(dweight_bf16))
         return fail(RLK_ERR_MISALIGNED, "dhidden and dweight must be 16-byte aligned");
     if (c.T == 0) {  // no rows: a zero dweight
