@@ -18,6 +18,7 @@ and ``rlk_linear_ce_bwd``; ``Fp8Linear`` (``fp8_linear``) quantises with
 ``rlk_fp8_matmul``.
 """
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import (MASK_EXPLICIT, MASK_IGNORE_INDEX, REDUCE_MEAN, REDUCE_NONE, REDUCE_SUM, Contract, fp8_matmul,
@@ -122,6 +123,13 @@ def lmhead_logprob(hidden, weight, targets, mask=None, v_real=None, num_tiles=64
     return FusedLmHeadLogprob.apply(hidden, weight, targets, mask, c, keep_logits)
 
 
+def _differentiated(*tensors):
+    """Whether a derivative may be asked for through these tensors: a gradient, or the tangent of a dual tensor, which
+    the functions here refuse, as they have no forward-mode rule."""
+    return torch.is_grad_enabled() and any(t.requires_grad for t in tensors) or \
+        any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 class LinearCrossEntropy(torch.autograd.Function):
     """(loss, lse) of the cross entropy of hidden @ weight^T; the backward forms the logits again, a piece of the
     vocabulary at a time."""
@@ -162,7 +170,7 @@ def linear_cross_entropy(hidden, weight, targets, mask=None, ignore_index=-100, 
         raise ValueError("reduction must be none, sum or mean")
     c = linear_ce_contract(hidden, weight, mask, ignore_index, kinds[reduction], label_smoothing, z_loss, softcap,
                            piece)
-    if torch.is_grad_enabled() and (hidden.requires_grad or weight.requires_grad):
+    if _differentiated(hidden, weight):
         loss, lse = LinearCrossEntropy.apply(hidden, weight, targets, mask, c)
     else:
         loss, lse = linear_ce_fwd(c, hidden, weight, targets, mask)
@@ -211,7 +219,7 @@ def fp8_linear(x, weight):
     """
     lead = x.shape[:-1]
     rows = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
-    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad):
+    if _differentiated(x, weight):
         y = Fp8Linear.apply(rows, weight)
     else:
         y = fp8_matmul(*fp8_quantize(rows), *fp8_quantize(weight, block_rows=128))
