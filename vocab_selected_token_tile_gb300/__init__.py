@@ -922,7 +922,8 @@ _fp8_workspaces = {}
 
 
 def _fp8_workspace(t, raw, stream):
-    """The status word of a device and stream (``raw``: its handle): zeroed there once, only ever set by a call."""
+    """The status word of a device and stream (``raw``: its handle): zeroed there once, only ever set by a call, and
+    cleared where fp8_matmul has reported it."""
     key = (t.device.index, raw)
     ws = _fp8_workspaces.get(key)
     if ws is None:
@@ -949,7 +950,8 @@ def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=Non
     ``a_scale`` is [ceil(K / 128), M]; ``b_scale`` [ceil(K / 128), N] (b_block_rows 1) or [ceil(K / 128),
     ceil(N / 128)] (128).  The result is BF16 (or FP32 with ``out_dtype`` torch.float32), in ``out`` if given (its rows
     may be strided); ``accumulate`` adds the product to an FP32 ``out``.  K = 0 is an empty sum: zeros, or ``out`` as it
-    was.  ``validate`` synchronises and raises if a device-side wait expired.
+    was.  ``validate`` synchronises and raises if a device-side wait expired, in this call or in one before it
+    on this stream that was not validated, and clears the record (in a ``workspace`` of the caller's it stays).
     """
     torch = _t()
     codes = (torch.float8_e4m3fn, torch.uint8)  # E4M3 values, or their codes as bytes
@@ -984,17 +986,22 @@ def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=Non
                 out.zero_()
         return out
     st = _raw_stream(a, stream)
-    if workspace is None:
-        workspace = _fp8_workspace(a, st, stream)
-    else:
+    given = workspace is not None
+    if given:
         _need(workspace, "workspace", RLK_FP8_WORKSPACE, ("uint8",))
+    else:
+        workspace = _fp8_workspace(a, st, stream)
     status = rlk_fp8_matmul(M, N, K, a.data_ptr(), _padded(lda, M, K, 16), pa, b.data_ptr(), _padded(ldb, N, K, 16),
                             pb, b_block_rows, out.data_ptr(), RLK_F32 if out.dtype is torch.float32 else RLK_BF16, ldc,
                             int(accumulate), workspace.data_ptr(), st)
     if status:
         check(status)
     if validate:
-        check(rlk_logp_workspace_status(workspace.data_ptr(), st))
+        status = rlk_logp_workspace_status(workspace.data_ptr(), st)
+        if status and not given:
+            with _allocating(stream):
+                workspace.zero_()  # reported once, not with every later call
+        check(status)
     return out
 
 
