@@ -507,6 +507,7 @@ size_t rlk_linear_ce_workspace_size(const rlk_linear_ce_contract* contract, int3
  *   lse        [T] FP32 out, every row.
  *   workspace  rlk_linear_ce_workspace_size bytes, 16-byte aligned, one call's
  *              at a time.
+ * No output (the workspace is one) may overlap an input or another output.
  * Device status (validate == 1, or rlk_logp_workspace_status): as for
  * rlk_logp_fwd.  T = 0: a reduced loss is 0.
  */
@@ -526,7 +527,8 @@ rlk_status rlk_linear_ce_fwd(const rlk_linear_ce_contract* contract, const void*
  * gradient is rounded to BF16 between the products, with a summed or averaged
  * loss's common factor (and 1 - label_smoothing, if that is not 0) left out of
  * it and applied to the FP32 sums.  The
- * order of every sum is fixed.  No output may overlap an input.
+ * order of every sum is fixed.  No output (the workspace is one) may overlap
+ * an input or another output.
  */
 rlk_status rlk_linear_ce_bwd(const rlk_linear_ce_contract* contract, const void* hidden_bf16, const void* weight_bf16,
                              const int64_t* targets, const uint8_t* active_mask, const float* lse,

@@ -847,6 +847,19 @@ rlk_status check_disjoint(const Span& out, std::initializer_list<Span> others) {
     return RLK_OK;
 }
 
+// No output shares a byte with an input or with another output.
+rlk_status check_outputs(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        const rlk_status s = check_disjoint(*o, ins);
+        if (s != RLK_OK) return s;
+        for (const Span* p = o + 1; p != outs.end(); ++p) {
+            const rlk_status t = check_disjoint(*o, {*p});
+            if (t != RLK_OK) return t;
+        }
+    }
+    return RLK_OK;
+}
+
 // An E4M3 operand's pointer and row stride (whole 16-byte pieces a row).
 rlk_status check_codes(const char* name, const void* p, int64_t stride, int64_t width) {
     if (!aligned16(p)) return fail(RLK_ERR_MISALIGNED, std::string(name) + " must be 16-byte aligned");
@@ -1039,6 +1052,14 @@ RLK_EXPORT rlk_status rlk_linear_ce_fwd(const rlk_linear_ce_contract* contract, 
     }
     if ((s = check_ce_inputs(c, hidden_bf16, weight_bf16, targets, active_mask, workspace)) != RLK_OK) return s;
     if (!loss || !lse) return fail(RLK_ERR_INVALID_ARG, "loss and lse outputs are required");
+    if ((s = check_outputs({{loss, c.reduction == RLK_REDUCE_NONE ? 4 * c.T : 4, "loss"},
+                            {lse, 4 * c.T, "lse"},
+                            {workspace, (int64_t)linear_ce_workspace(c, false), "workspace"}},
+                           {{hidden_bf16, extent(c.T, c.hidden_stride, c.H, 2), "hidden"},
+                            {weight_bf16, extent(c.V, c.weight_stride, c.H, 2), "weight"},
+                            {targets, 8 * c.T, "targets"},
+                            {active_mask, c.T, "active_mask"}})) != RLK_OK)
+        return s;
     if ((s = select_device(hidden_bf16)) != RLK_OK) return s;
     if ((s = check_device_ptrs({{weight_bf16, "weight"}, {targets, "targets"}, {active_mask, "active_mask"},
                                 {loss, "loss"}, {lse, "lse"}, {workspace, "workspace"}})) != RLK_OK)
@@ -1072,13 +1093,16 @@ RLK_EXPORT rlk_status rlk_linear_ce_bwd(const rlk_linear_ce_contract* contract, 
     }
     if ((s = check_ce_inputs(c, hidden_bf16, weight_bf16, targets, active_mask, workspace)) != RLK_OK) return s;
     if (!lse || !grad_loss) return fail(RLK_ERR_INVALID_ARG, "lse and grad_loss are required");
-    const Span in_h{hidden_bf16, extent(c.T, c.hidden_stride, c.H, 2), "hidden"};
-    const Span in_w{weight_bf16, extent(c.V, c.weight_stride, c.H, 2), "weight"};
-    const Span out_w{dweight_bf16, extent(c.V, c.dweight_stride, c.H, 2), "dweight"};
-    if ((s = check_disjoint({dhidden_bf16, extent(c.T, c.dhidden_stride, c.H, 2), "dhidden"},
-                            {in_h, in_w, out_w})) != RLK_OK)
+    if ((s = check_outputs({{dhidden_bf16, extent(c.T, c.dhidden_stride, c.H, 2), "dhidden"},
+                            {dweight_bf16, extent(c.V, c.dweight_stride, c.H, 2), "dweight"},
+                            {workspace, (int64_t)linear_ce_workspace(c, true), "workspace"}},
+                           {{hidden_bf16, extent(c.T, c.hidden_stride, c.H, 2), "hidden"},
+                            {weight_bf16, extent(c.V, c.weight_stride, c.H, 2), "weight"},
+                            {targets, 8 * c.T, "targets"},
+                            {active_mask, c.T, "active_mask"},
+                            {lse, 4 * c.T, "lse"},
+                            {grad_loss, c.reduction == RLK_REDUCE_NONE ? 4 * c.T : 4, "grad_loss"}})) != RLK_OK)
         return s;
-    if ((s = check_disjoint(out_w, {in_h, in_w})) != RLK_OK) return s;
     if ((s = select_device(hidden_bf16)) != RLK_OK) return s;
     if ((s = check_device_ptrs({{weight_bf16, "weight"}, {targets, "targets"}, {active_mask, "active_mask"},
                                 {lse, "lse"}, {grad_loss, "grad_loss"}, {dhidden_bf16, "dhidden"},
