@@ -214,7 +214,7 @@ struct Gemm8Params {
     void* c;
     int64_t ldc;
     int32_t M, N, KB;
-    int32_t MB, NB;     // tiles along M and N
+    int32_t MB, NB;     // tiles along M (of pairs) and N
     int32_t band;       // M tiles per band of the tile order
     int32_t nsb;        // scales of B per K group: N (rows) or ceil(N / 128) (blocks)
     int32_t c_f32, accumulate, vec;
@@ -718,8 +718,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     float* scales = reinterpret_cast<float*>(sX + S::kStages * S::kX);
     auto* bars = reinterpret_cast<Bars8<S::kStages>*>(scales + kScaleStages * S::kScale);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // p.MB blocks of NT rows of A, p.NB tiles of 128 rows of B; the M blocks of one tile run together
-    const int tiles = p.MB * p.NB;
+    const int tiles = p.NB;  // of 128 rows of B; all of A's rows are one block
     const int rank = split > 1 ? (int)cluster_ctarank() : 0;
     const int first = (int)blockIdx.x / split, step = (int)gridDim.x / split;
     const int k0 = (int)((int64_t)p.KB * rank / split), k1 = (int)((int64_t)p.KB * (rank + 1) / split);
@@ -743,13 +742,12 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
             int64_t issued = 0;
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
-                const int nb = t / p.MB, mb = t % p.MB;
                 for (int kb = k0; kb < k1; ++kb) {
                     if (!(ok = pipe_wait(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                     const uint32_t fb = smem_u32(&bars->full[r.slot]);
                     mbar_arrive_expect_tx(fb, S::kW + S::kX);
-                    tma_load_2d(smem_u32(sW + r.slot * S::kW), &tmB, kb * kGK, nb * kSRows, fb);
-                    tma_load_2d(smem_u32(sX + r.slot * S::kX), &tmA, kb * kGK, mb * NT, fb);
+                    tma_load_2d(smem_u32(sW + r.slot * S::kW), &tmB, kb * kGK, t * kSRows, fb);
+                    tma_load_2d(smem_u32(sX + r.slot * S::kX), &tmA, kb * kGK, 0, fb);
                     ++issued;
                     r.next(S::kStages);
                 }
@@ -785,25 +783,21 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
         Ring r;
         bool ok = true;
         for (int t = first; ok && t < tiles; t += step) {
-            const int nb = t / p.MB, mb = t % p.MB;
             for (int kb = k0; kb < k1; ++kb) {
                 ok = __all_sync(0xFFFFFFFFu, pipe_wait(ab, smem_u32(&bars->sc.empty[r.slot]), r.phase ^ 1u, p.w));
                 if (!ok) break;
                 const uint32_t dst = smem_u32(scales + r.slot * S::kScale);
                 const float* a = p.sa + (int64_t)kb * p.M;
                 const float* b = p.sb + (int64_t)kb * p.nsb;
-                for (int i = lane; i < NT; i += 32) {
-                    const int row = mb * NT + i;
-                    cp_async4(dst + i * 4, a + (row < p.M ? row : 0), row < p.M);
-                }
+                for (int i = lane; i < NT; i += 32) cp_async4(dst + i * 4, a + (i < p.M ? i : 0), i < p.M);
                 if (BROWS) {
 #pragma unroll
                     for (int i = lane; i < kSRows; i += 32) {
-                        const int row = nb * kSRows + i;
+                        const int row = t * kSRows + i;
                         cp_async4(dst + (NT + i) * 4, b + (row < p.N ? row : 0), row < p.N);
                     }
                 } else if (lane == 0) {
-                    cp_async4(dst + NT * 4, b + nb, true);
+                    cp_async4(dst + NT * 4, b + t, true);
                 }
                 cp_async_arrive(smem_u32(&bars->sc.full[r.slot]));
                 r.next(kScaleStages);
@@ -815,7 +809,6 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
         Ring acc, sc;
         bool ok = true;
         for (int t = first; ok && t < tiles; t += step) {
-            const int nb = t / p.MB, mb = t % p.MB;
 #pragma unroll
             for (int i = 0; i < NT; ++i) sum[i] = 0.f;
             for (int kb = k0; kb < k1; ++kb) {
@@ -849,12 +842,12 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
                 sc.next(kScaleStages);
             }
             if (!ok || split > 1) break;  // a split launch has one tile a cluster, added up below
-            const int col = nb * kSRows + row_in;
+            const int col = t * kSRows + row_in;
             if (col < p.N) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    const int64_t at = (int64_t)(mb * NT + i) * p.ldc + col;
-                    if (mb * NT + i >= p.M) break;
+                    const int64_t at = (int64_t)i * p.ldc + col;
+                    if (i >= p.M) break;
                     if (p.c_f32) {
                         float* c = static_cast<float*>(p.c) + at;
                         *c = p.accumulate ? *c + sum[i] : sum[i];
@@ -875,17 +868,16 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
             for (int i = 0; i < NT; ++i) red[i * kSRows + row_in] = sum[i];
         }
         cluster_sync_all();
-        const int nb = first / p.MB, mb = first % p.MB;
         const bool failed = *reinterpret_cast<volatile int*>(ab) != 0;
         // this CTA adds up rows [lo, hi) of A: 128 consecutive columns of C a row
         const int lo = NT * rank / split, hi = NT * (rank + 1) / split;
         for (int e = threadIdx.x; e < (hi - lo) * kSRows && !failed; e += kSThreads) {
-            const int i = lo + e / kSRows, col = nb * kSRows + e % kSRows;
-            if (mb * NT + i >= p.M || col >= p.N) continue;
+            const int i = lo + e / kSRows, col = first * kSRows + e % kSRows;
+            if (i >= p.M || col >= p.N) continue;
             const uint32_t at = smem_u32(red + i * kSRows + e % kSRows);
             float v = 0.f;
             for (int r = 0; r < split; ++r) v = __fadd_rn(v, ld_cluster_f32(mapa_shared(at, (uint32_t)r)));
-            const int64_t o = (int64_t)(mb * NT + i) * p.ldc + col;
+            const int64_t o = (int64_t)i * p.ldc + col;
             if (p.c_f32) {
                 float* c = static_cast<float*>(p.c) + o;
                 *c = p.accumulate ? *c + v : v;
@@ -1011,7 +1003,7 @@ rlk_status launch_gemm(const Gemm8Params& p, const CUtensorMap& a, const CUtenso
 template <int NT, bool BROWS>
 rlk_status launch_skinny(const Gemm8Params& p, const CUtensorMap& a, const CUtensorMap& b, int sms,
                          cudaStream_t st) {
-    const int tiles = p.MB * p.NB, room = Skinny<NT>::kPerSm * sms;
+    const int tiles = p.NB, room = Skinny<NT>::kPerSm * sms;
     int split = 1;
     while (split < 8 && tiles * split * 2 <= room && split * 4 <= p.KB) split *= 2;
     return launch_clusters<skinny_kernel<NT, BROWS>>(split > 1 ? tiles * split : tiles < room ? tiles : room,
@@ -1057,7 +1049,6 @@ rlk_status launch_fp8_matmul(int64_t M, int64_t N, int64_t K, const void* a, int
     // read and sums to keep than its share of the weight's bytes takes: 27.5 us at 128 x 16384 x 4096, the pair 24.7.)
     if (M <= 64) {
         const int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-        p.MB = (int32_t)((M + nt - 1) / nt);
         p.NB = (int32_t)((N + kSRows - 1) / kSRows);
         if (!make_map8(&ta, a, K, M, lda, (uint32_t)nt) || !make_map8(&tb, b, K, N, ldb, kSRows))
             return fail(RLK_ERR_CUDA, "cuTensorMapEncodeTiled failed for an operand of the fp8 product");

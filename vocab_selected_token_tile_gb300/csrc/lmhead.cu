@@ -63,6 +63,29 @@
 namespace rlk {
 namespace {
 
+// TMA tile store from shared memory (bulk group); the writing threads fence
+// the async proxy first.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int32_t c0, int32_t c1, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(tmap), "r"(c0),
+                 "r"(c1), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// The source of every committed store has been read (the buffer may be rewritten).
+__device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// Every committed store has completed.
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async_smem() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+constexpr int kBM = 128;  // token rows per unit (TMEM lanes)
+constexpr int kStages = 4;
+constexpr int kUq = 4;  // depth of the unit queue from the producer to the other roles
+constexpr int kThreadsLm = 192;
+constexpr uint32_t kTmemCols = 512;  // two accumulators of kBN columns
+constexpr uint32_t kStageA = kBM * kBK * 2;
+constexpr uint32_t kStageB = kBN * kBK * 2;
 constexpr int kMaxGroups = 8;
 // Unit order of the logits GEMMs: a unit is one 256-row weight chunk of one token block; units
 // come in bands of token blocks whose hidden spans at most kBandHiddenBytes, chunk-major within a
@@ -88,6 +111,19 @@ constexpr size_t kTicketBytes = 256;
 // and the FP32 logits written to a [T, V_padded] buffer; kEpiGrad: dlogits.
 enum : int { kEpiPartials = 0, kEpiGrad = 1, kEpiPartialsStore = 2 };
 
+struct Bars {
+    uint64_t full[kStages];
+    uint64_t empty[kStages];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t ufull[kUq];   // unit queue entry written (the producer's arrival)
+    uint64_t uempty[kUq];  // entry read by the MMA thread and the four epilogue warps
+    uint64_t drain;
+    int64_t unit[kUq];
+    uint32_t tmem_addr;
+    int abort_flag;
+};
+
 // Shared memory of the logits GEMMs past the 1024-byte alignment slack: the
 // operand stages, then the barriers (then, for kEpiPartialsStore, the staging
 // blocks of the logits store).
@@ -95,6 +131,50 @@ constexpr size_t kGemmSmemCore = ((size_t)kStages * (kStageA + kStageB) + sizeof
 // Per epilogue warp: 32 rows x 32 FP32 columns with the 128-byte swizzle (the
 // TMA store's source), or 32 rows at pitch 33 (the 16-column remainder).
 constexpr int kStoreStage = 1280;  // floats (5 KB, a multiple of 1024 bytes)
+
+// The producer publishes the CTA's n-th unit (-1: no more units).
+__device__ bool unit_put(Bars* bars, int64_t n, int64_t u, const PipeWait& w) {
+    const int s = (int)(n % kUq);
+    const uint32_t par = (uint32_t)((n / kUq) & 1);
+    if (!pipe_wait(&bars->abort_flag, smem_u32(&bars->uempty[s]), par ^ 1u, w)) return false;
+    *reinterpret_cast<volatile int64_t*>(&bars->unit[s]) = u;
+    mbar_arrive(smem_u32(&bars->ufull[s]));  // release: the entry is visible to whoever acquires the phase
+    return true;
+}
+
+__device__ bool unit_get(Bars* bars, int64_t n, int64_t& u, const PipeWait& w) {
+    const int s = (int)(n % kUq);
+    if (!pipe_wait(&bars->abort_flag, smem_u32(&bars->ufull[s]), (uint32_t)((n / kUq) & 1), w)) return false;
+    u = *reinterpret_cast<volatile int64_t*>(&bars->unit[s]);
+    return true;
+}
+
+__device__ __forceinline__ void unit_done(Bars* bars, int64_t n) { mbar_arrive(smem_u32(&bars->uempty[n % kUq])); }
+
+__device__ void init_bars(Bars* bars) {
+    for (int s = 0; s < kStages; ++s) {
+        mbar_init(smem_u32(&bars->full[s]), 1);
+        mbar_init(smem_u32(&bars->empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_u32(&bars->tfull[b]), 1);
+        mbar_init(smem_u32(&bars->tempty[b]), 4);
+    }
+    for (int s = 0; s < kUq; ++s) {
+        mbar_init(smem_u32(&bars->ufull[s]), 1);
+        mbar_init(smem_u32(&bars->uempty[s]), 5);
+    }
+    mbar_init(smem_u32(&bars->drain), 1);
+    bars->abort_flag = 0;
+    fence_mbar_init();
+}
+
+// The producer's final step: every copy it issued lands before the CTA may exit.
+__device__ void drain_copies(Bars* bars, int64_t issued, const PipeWait& w) {
+    const int64_t first = issued > kStages ? issued - kStages : 0;
+    for (int64_t j = first; j < issued; ++j)
+        pipe_drain(smem_u32(&bars->full[j % kStages]), (uint32_t)((j / kStages) & 1), w);
+}
 
 // ----------------------------------------------------------------- logits GEMM (forward partials / dlogits)
 
@@ -108,7 +188,7 @@ struct LmParams {
     const float* grad;    // [T] upstream g of logp   (kEpiGrad)
     uint16_t* dlogits;    // [T, Vp] BF16 out         (kEpiGrad)
     unsigned long long* tickets;  // one per virtual-TP group, 0 at launch
-    WaitCtl w;
+    PipeWait w;
     int64_t T, Vr, Vp, ignore_index;
     int32_t K, NT, W, vtp, nchunk, rem, mask_mode;
     int32_t MB;   // token blocks
@@ -253,7 +333,7 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
                 const int nrows = last_rem ? p.rem : kBN;
                 const int n0 = tile * p.W + ch * kBN;
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!lm_wait(bars, smem_u32(&bars->empty[stage]), phase ^ 1u, p.w)) {
+                    if (!pipe_wait(&bars->abort_flag, smem_u32(&bars->empty[stage]), phase ^ 1u, p.w)) {
                         aborted = true;
                         break;
                     }
@@ -290,13 +370,13 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
                 const int acc = (int)(chunk & 1);
                 const uint32_t accph = (uint32_t)((chunk >> 1) & 1);
                 ++chunk;
-                if (!lm_wait(bars, smem_u32(&bars->tempty[acc]), accph ^ 1u, p.w)) break;
+                if (!pipe_wait(&bars->abort_flag, smem_u32(&bars->tempty[acc]), accph ^ 1u, p.w)) break;
                 tc_fence_after();
                 const bool last_rem = (ch == p.nchunk - 1) && p.rem;
                 const uint32_t idesc = idesc_bf16_f32(kBM, last_rem ? (uint32_t)p.rem : (uint32_t)kBN);
                 const uint32_t d = tmem + (uint32_t)(acc * kBN);
                 for (int kb = 0; kb < KB; ++kb) {
-                    if (!lm_wait(bars, smem_u32(&bars->full[stage]), phase, p.w)) {
+                    if (!pipe_wait(&bars->abort_flag, smem_u32(&bars->full[stage]), phase, p.w)) {
                         aborted = true;
                         break;
                     }
@@ -317,7 +397,7 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
             }
             // Every issued MMA completes before tensor memory is freed.
             umma_commit(smem_u32(&bars->drain));
-            lm_drain_wait(smem_u32(&bars->drain), 0u, p.w);
+            pipe_drain(smem_u32(&bars->drain), 0u, p.w);
         }
     } else {
         // ------------------------------------------------ epilogue (warps 2..5)
@@ -363,7 +443,7 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
             const int acc = (int)(chunk & 1);
             const uint32_t accph = (uint32_t)((chunk >> 1) & 1);
             ++chunk;
-            const bool ok = lm_wait(bars, smem_u32(&bars->tfull[acc]), accph, p.w);
+            const bool ok = pipe_wait(&bars->abort_flag, smem_u32(&bars->tfull[acc]), accph, p.w);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after();
             const int ncols = ((ch == p.nchunk - 1) && p.rem) ? p.rem : kBN;
@@ -561,7 +641,7 @@ struct GradParams {
     uint16_t* dw_bf16;  // [V_padded, H] BF16, or NULL
     float* dw_f32;      // [V_padded, H] FP32, or NULL
     unsigned long long* ticket;
-    WaitCtl w;
+    PipeWait w;
     int64_t T, Vr, Vp, n0, n1;
     int32_t H, NB, KB0, KB1;  // n-blocks of H; K blocks of problem 0 (V_real) and problem 1 (T)
     int32_t NBg;              // H blocks per band of the tile order (grad_tile)
@@ -635,7 +715,7 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
                 const int m0 = (int)(t.mb * kBM);
                 const int h0 = t.nb * kBN;
                 for (int kb = 0; kb < t.KB; ++kb) {
-                    if (!lm_wait(bars, smem_u32(&bars->empty[stage]), phase ^ 1u, p.w)) {
+                    if (!pipe_wait(&bars->abort_flag, smem_u32(&bars->empty[stage]), phase ^ 1u, p.w)) {
                         aborted = true;
                         break;
                     }
@@ -680,12 +760,12 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
                 const int acc = (int)(tiles & 1);
                 const uint32_t accph = (uint32_t)((tiles >> 1) & 1);
                 ++tiles;
-                if (!lm_wait(bars, smem_u32(&bars->tempty[acc]), accph ^ 1u, p.w)) break;
+                if (!pipe_wait(&bars->abort_flag, smem_u32(&bars->tempty[acc]), accph ^ 1u, p.w)) break;
                 tc_fence_after();
                 const uint32_t idesc = idesc_bf16_f32_major(kBM, (uint32_t)(64 * t.nbox), t.prob == 1, true);
                 const uint32_t d = tmem + (uint32_t)(acc * kBN);
                 for (int kb = 0; kb < t.KB; ++kb) {
-                    if (!lm_wait(bars, smem_u32(&bars->full[stage]), phase, p.w)) {
+                    if (!pipe_wait(&bars->abort_flag, smem_u32(&bars->full[stage]), phase, p.w)) {
                         aborted = true;
                         break;
                     }
@@ -710,7 +790,7 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
                 if (!aborted) umma_commit(smem_u32(&bars->tfull[acc]));
             }
             umma_commit(smem_u32(&bars->drain));
-            lm_drain_wait(smem_u32(&bars->drain), 0u, p.w);
+            pipe_drain(smem_u32(&bars->drain), 0u, p.w);
         }
     } else {
         // ------------------------------------------------ epilogue (warps 2..5): TMEM -> BF16 / FP32 rows
@@ -730,7 +810,7 @@ __global__ void __launch_bounds__(kThreadsLm, 1)
             const int acc = (int)(tiles & 1);
             const uint32_t accph = (uint32_t)((tiles >> 1) & 1);
             ++tiles;
-            const bool ok = lm_wait(bars, smem_u32(&bars->tfull[acc]), accph, p.w);
+            const bool ok = pipe_wait(&bars->abort_flag, smem_u32(&bars->tfull[acc]), accph, p.w);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             tc_fence_after();
             const int64_t row = t.mb * kBM + r_in;

@@ -1,6 +1,5 @@
 // What the kernels of CTA pairs share (fp8_gemm.cu, linear_ce.cu): ring
-// positions, bounded waits, and the barriers of a pair's pipeline from its
-// start to its end.
+// positions and the barriers of a pair's pipeline from its start to its end.
 //
 // Two CTAs work one 256 x 256 tile: each loads its 128 rows of A and half of
 // B's 256, the even CTA's warp 1 issues the MMAs of both, and each CTA reads
@@ -24,13 +23,12 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "rlk_gemm.cuh"
 #include "rlk_internal.h"
 #include "rlk_ptx.cuh"
 
 namespace rlk {
 namespace {
-
-constexpr uint64_t kPipeDrainNs = 1000000000ull;
 
 // Position in a ring of n slots: the slot and the parity of its current pass.
 struct Ring {
@@ -50,31 +48,7 @@ struct Ring {
     }
 };
 
-struct PipeWait {
-    uint32_t* status;
-    uint64_t wait_ns;
-};
-
-// Bounded wait for a phase of a barrier: false, with the time-out recorded and
-// *abort_flag set, when it expired, or when another role has given up.  The
-// clock and the flag are read on every 256th poll.
-__device__ __forceinline__ bool pipe_wait(int* abort_flag, uint32_t bar, uint32_t parity, const PipeWait& w) {
-    uint64_t t0 = 0;
-    for (uint32_t polls = 0;; ++polls) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((polls & 255u) != 255u) continue;
-        if (*reinterpret_cast<volatile int*>(abort_flag)) return false;
-        const uint64_t now = globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > w.wait_ns) {
-            *reinterpret_cast<volatile int*>(abort_flag) = 1;
-            atomicOr(w.status, kStatusTimeout);
-            return false;
-        }
-    }
-}
-
-// The same by a whole warp, for all of its lanes alike: one may see the phase
+// pipe_wait by a whole warp, for all of its lanes alike: one may see the phase
 // complete after another has given it up, and lanes that leave a role's loop
 // alone would leave the others waiting for them.  The vote costs the FP8
 // product 0.6% (8192 x 12288 x 4096: 319.5 -> 321.5 us).  Voting after the step
@@ -82,17 +56,6 @@ __device__ __forceinline__ bool pipe_wait(int* abort_flag, uint32_t bar, uint32_
 // cross entropy's issuer 10-40% longer.
 __device__ __forceinline__ bool pipe_wait_warp(int* abort_flag, uint32_t bar, uint32_t parity, const PipeWait& w) {
     return __all_sync(0xFFFFFFFFu, pipe_wait(abort_flag, bar, parity, w));
-}
-
-// The wait for a role's own last copies or MMAs, which nothing may cut short.
-__device__ __forceinline__ void pipe_drain(uint32_t bar, uint32_t parity, const PipeWait& w) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer_ns() - t0 > kPipeDrainNs) {
-            atomicOr(w.status, kStatusTimeout);
-            return;
-        }
-    }
 }
 
 template <int STAGES>
