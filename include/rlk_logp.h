@@ -484,7 +484,7 @@ typedef struct {
     int32_t validate;         /* 0: asynchronous; 1: synchronise and report device status */
     float label_smoothing;    /* [0, 1] */
     float z_loss;             /* >= 0 */
-    float softcap;            /* 0: none; > 0 */
+    float softcap;            /* 0: none; else at least 1e-6 */
 } rlk_linear_ce_contract;     /* 104 bytes, no padding */
 
 /* Host-only validation (touches no device). */
@@ -494,8 +494,10 @@ rlk_status rlk_linear_ce_check(const rlk_linear_ce_contract* contract);
  * Bytes of device workspace: of the forward (with_grad 0), or of either call
  * (1): about T V / 16 for the forward's partials (half as much again with
  * label smoothing), and T H * 2 where hidden's rows lie between 128-byte lines;
- * T piece * 2 + T H * 6 for the backward, whatever V is.  0 for an invalid
- * contract.
+ * T piece * 2 + T H * (4 S + 2) for the backward, whatever V is: S = 1 where
+ * dhidden has 152 tiles of 256 x 256 or more, else as many slices of the
+ * vocabulary as make it so many (32 at most), each with sums of its own.  0 for
+ * an invalid contract.
  */
 size_t rlk_linear_ce_workspace_size(const rlk_linear_ce_contract* contract, int32_t with_grad);
 

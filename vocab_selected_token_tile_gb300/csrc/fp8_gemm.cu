@@ -16,14 +16,15 @@
 // gemm_kernel, 256 x 256 tiles by pairs of CTAs (rlk_pair.cuh), persistent, one
 // CTA per SM.  A pair halves what a CTA's MMAs read of B from shared memory (a
 // first kernel, single CTAs with 128 x 256 tiles, took 452 us at 8192 x 12288 x
-// 4096; this one 312).  Floor: the tensor core, 2 M N K operations.  A group's
-// four MMAs take 512 clocks; from one accumulator's completion to the next it
-// is 850-900 with block scales and 1,200-1,250 with row scales.  The epilogue
-// of a group reads back 128 KB of accumulator a CTA (256 clocks of the
+// 4096; this one 320 by itself, 338 call after call).  Floor: the tensor core,
+// 2 M N K operations.  A group's four MMAs take 512 clocks; from one
+// accumulator's completion to the next it is 850-900 with block scales and
+// 1,200-1,250 with row scales.  The epilogue of a group reads back 128 KB of accumulator a CTA (256 clocks of the
 // tensor-memory port), scales and adds it (128 packed operations a scheduler,
 // twice that and 32 KB of shared memory with row scales), and hands it back,
 // and tensor memory holds two accumulators.  8192 x 8192 x 8192: 390 us (2.8
-// PFLOP/s, tensor pipe 55% busy) and 548 us (2.0 PFLOP/s, 38%).  Roles: warp 0
+// PFLOP/s, tensor pipe 55% busy) and 548 us (2.0 PFLOP/s, 38%), 435 and 567 in
+// a long loop of them under the power cap.  Roles: warp 0
 // issues the TMA loads, warp 1 of the even CTA the pair's MMAs, warp 2 fetches
 // the scales with cp.async (4 bytes each: a row of scales starts at any
 // multiple of 4), warps 4-11 are the epilogue (a warp reads 32 tensor-memory
@@ -41,8 +42,8 @@
 // rank order: no workspace, no second launch, the same bits every time.
 //
 // Every wait is bounded; on expiry the CTA records the time-out in the status
-// word, stops issuing, waits (bounded) for its copies and MMAs, frees its
-// tensor memory and returns.
+// word, stops issuing, waits (bounded) for the copies and MMAs under way (a
+// pair for those of both of its CTAs), frees its tensor memory and returns.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

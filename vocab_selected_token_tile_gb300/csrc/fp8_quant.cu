@@ -25,13 +25,16 @@
 // rows of one column), XOR-swizzled by the column's block of 8 so that the 16
 // lanes of a half warp hit 16 different 8-byte bank pairs.
 //
-// What it spends: with the loads under way most of the time the issue slots
-// decide (a tile's share of HBM is about 3,000 clocks).  So the maxima of BF16
-// are taken two at a time (a BF16 maximum is exact), a row's scale is formed by
-// one lane of its sixteen, a column's by one thread of the CTA, and an element
-// is widened once for both directions.  8192 x 4096 of BF16: both directions
-// 28.5 us (4.8 TB/s; the issue slots are 66% busy), rows 17.3 (5.9 TB/s); FP32,
-// 151936 x 4096 in blocks: 443 us (7.0 TB/s: HBM).
+// What it spends: a tile is one chain of loads, maxima, barriers, conversions
+// and stores, and the other CTAs of the SM (three, of BF16) are all that covers
+// it; neither issue slots nor HBM are full (66% and 36%, BF16, both
+// directions).  So instructions count: the maxima of BF16 are taken two at a
+// time (a BF16 maximum is exact), a row's scale is formed by one lane of its
+// sixteen, a column's by one thread of the CTA, and an element is widened once
+// for both directions.  8192 x 4096 of BF16: both directions 28.5 us (4.8
+// TB/s), rows 17.3 (5.9 TB/s); FP32, 151936 x 4096 in blocks: 443 us (7.0 TB/s:
+// HBM).  Rows off the 16-byte grid are read by the element (8000 x 3517: BF16
+// 27.3 us, FP32 33.8; 8000 x 3520: 16.1 and 22.5).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -14,17 +14,18 @@
 // partial, then a merge of each row's partials in vocabulary order.  Bound:
 // the tensor core, 2 T V H operations; the epilogue of one accumulator runs
 // under the MMAs of the other (4096 x 151936 x 4096: 2.37-2.54 ms, 2.0-2.15
-// PFLOP/s as the clock allows, the tensor pipe 96.5% busy).  Hidden whose rows
-// lie between 128-byte lines is copied onto them first, as in the backward
-// below (1000 x 50257 x 1000: 95 -> 76 us).  Few tokens: the weight's bytes (16
-// x 151936 x 1024: 65 us, 4.8 TB/s).
+// PFLOP/s as the clock allows, the tensor pipe 96.5% busy; 2.8 ms in a long
+// loop under the power cap).  Hidden whose rows lie between 128-byte lines is
+// copied onto them first, as in the backward below (1000 x 50257 x 1000: 95 ->
+// 76 us).  Few tokens: the weight's bytes (16 x 151936 x 1024: 61-66 us, of
+// which the GEMM is 50, 6.2 TB/s).
 //
 // Backward, in pieces of the vocabulary: for each piece the logits are formed
 // again (the price of not keeping them: 2 T V H operations more) and leave
 // the epilogue as BF16 dL/dx [T, P], and one launch then runs both
 //   dHidden[T, H] += dx weight[piece]     (FP32 sums across the pieces)
 //   dWeight[piece] = dx^T hidden
-// (8.6-8.7 ms at 4096 x 151936 x 4096, 1.75 PFLOP/s, the tensor pipe 97% busy).
+// (8.6-9.0 ms at 4096 x 151936 x 4096, 1.7-1.75 PFLOP/s, the tensor pipe 97% busy).
 // The work space is P T 2 bytes for dx, T H 4 for the sums and T H 2 for the
 // rows below, whatever V is.  Only the active rows take part: their hidden is
 // first copied together (a step's prompts and padding are often half of its
