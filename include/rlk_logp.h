@@ -601,6 +601,130 @@ rlk_status rlk_fp8_matmul(int64_t M, int64_t N, int64_t K, const void* a, int64_
                           int32_t c_type, int64_t c_stride, int32_t accumulate, void* workspace, rlk_stream_t stream);
 
 /*
+ * The product with an epilogue: a layer of a feed-forward block in one call.
+ *   z = A B^T + bias;   y = act(z), or (gated) act(z_gate) * z_up;   c = y + residual,
+ * everything in FP32 and rounded once, where it is stored.  Gated: B holds N
+ * rows of the gate, then N of the other half (b [2 N, K], bias and z likewise).
+ *   silu z / (1 + e^-z); gelu z Phi(z); gelu_tanh its form with tanh.
+ */
+typedef enum {
+    RLK_ACT_NONE = 0,
+    RLK_ACT_RELU = 1,
+    RLK_ACT_SILU = 2,
+    RLK_ACT_GELU = 3,
+    RLK_ACT_GELU_TANH = 4
+} rlk_activation;
+
+typedef struct {
+    const void* bias;         /* NULL, or [N] ([2 N] gated) per group */
+    const void* residual;     /* NULL, or [M, residual_stride] */
+    void* z;                  /* NULL, or [M, z_stride] BF16 out: z, which the backward needs */
+    int64_t residual_stride;  /* >= N */
+    int64_t z_stride;         /* >= N (2 N gated) */
+    int32_t bias_type;        /* rlk_type */
+    int32_t residual_type;
+    int32_t activation;       /* rlk_activation */
+    int32_t gated;            /* 0, 1: N a multiple of 64 */
+} rlk_fp8_epilogue;           /* 56 bytes, no padding */
+
+/*
+ * C = epilogue(A B^T), operands as rlk_fp8_matmul's with B in blocks:
+ *   b [N (2 N gated), b_stride], b_scale [ceil(K / 128), ceil(N (2 N) / 128)].
+ * residual may be c itself (same type and stride: in place); no other output
+ * may overlap an input or another output.  epilogue NULL: none.  K >= 1.
+ * Workspace, bits and stream as for rlk_fp8_matmul.
+ */
+rlk_status rlk_fp8_matmul_act(int64_t M, int64_t N, int64_t K, const void* a, int64_t a_stride, const float* a_scale,
+                              const void* b, int64_t b_stride, const float* b_scale, const rlk_fp8_epilogue* epilogue,
+                              void* c, int32_t c_type, int64_t c_stride, void* workspace, rlk_stream_t stream);
+
+/*
+ * The same for rows that belong to groups (a mixture's experts), each with a B
+ * and a bias of its own.
+ *   ends  [groups] int32 on the device: the row behind group e's last; group e
+ *         is rows [ends[e - 1], ends[e]), the first from row 0.  Whatever it
+ *         holds, it is taken as its running maximum, held within [0, M], so no
+ *         row is read or written outside [0, M) or by two groups.
+ *   b     [groups, b_group_stride] of [N (2 N), b_stride] each, group strides a
+ *         multiple of 16; b_scale [groups, ceil(K / 128), ceil(N (2 N) / 128)];
+ *         the bias [groups, N (2 N)].
+ * groups is 1 to 1024.  No residual.  Rows of c (and of z) behind the last
+ * group stay as they were; with zero_rest those of c are set to zero.  A group
+ * without rows costs nothing: its B is not read.
+ */
+rlk_status rlk_fp8_grouped_matmul(int64_t groups, int64_t M, int64_t N, int64_t K, const int32_t* ends, const void* a,
+                                  int64_t a_stride, const float* a_scale, const void* b, int64_t b_stride,
+                                  int64_t b_group_stride, const float* b_scale, const rlk_fp8_epilogue* epilogue,
+                                  void* c, int32_t c_type, int64_t c_stride, int32_t zero_rest, void* workspace,
+                                  rlk_stream_t stream);
+
+/*
+ * Quantisation of rows that belong to groups: rlk_fp8_quantize with
+ * block_rows 1, where the transpose's groups of 128 start anew with each group
+ * of rows, each padded with zeros to whole 128s:
+ *   group e's rows take the columns [128 p_e, 128 p_{e+1}) of qt, p_0 = 0 and
+ *   p_{e+1} = p_e + ceil(rows of e / 128).
+ *   q, scale   NULL, or as rlk_fp8_quantize's; rows behind the last group are
+ *              not written.
+ *   qt, scale_t  NULL, or [cols, qt_stride] and [tiles, cols] with qt_stride >=
+ *              128 tiles, tiles = rows / 128 + min(groups, rows), the most that
+ *              any ends can ask for; what is behind the last group's columns is
+ *              not written.
+ */
+rlk_status rlk_fp8_quantize_grouped(int64_t groups, int64_t rows, int64_t cols, const int32_t* ends, const void* x,
+                                    int32_t x_type, int64_t x_stride, void* q, int64_t q_stride, float* scale,
+                                    void* qt, int64_t qt_stride, float* scale_t, rlk_stream_t stream);
+
+/*
+ * Quantisation of several matrices of one size (experts' weights), each as
+ * rlk_fp8_quantize with block_rows 128: x, q and qt with strides between the
+ * matrices (q's and qt's a multiple of 16), scale [count, ceil(cols / 128),
+ * ceil(rows / 128)] and scale_t [count, ceil(rows / 128), ceil(cols / 128)].
+ */
+rlk_status rlk_fp8_quantize_batch(int64_t count, int64_t rows, int64_t cols, const void* x, int32_t x_type,
+                                  int64_t x_stride, int64_t x_batch_stride, void* q, int64_t q_stride,
+                                  int64_t q_batch_stride, float* scale, void* qt, int64_t qt_stride,
+                                  int64_t qt_batch_stride, float* scale_t, rlk_stream_t stream);
+
+/*
+ * The groups' weight gradients from operands of rlk_fp8_quantize_grouped:
+ *   C_e = A_e B_e^T,  A_e [M, its columns of a], B_e [N, its columns of b]:
+ * dW_e = dY_e^T X_e with a the qt of dY and b that of X.
+ *   rows     of the matrices before their transposition, which ends refers to;
+ *   a        [M, a_stride], a_scale [tiles, M]; b [N, b_stride], b_scale [tiles, N].
+ *   c        [groups, c_group_stride] of [M, c_stride]; a group without rows has
+ *            a zero C (accumulate: keeps it).
+ */
+rlk_status rlk_fp8_grouped_dweight(int64_t groups, int64_t rows, int64_t M, int64_t N, const int32_t* ends,
+                                   const void* a, int64_t a_stride, const float* a_scale, const void* b,
+                                   int64_t b_stride, const float* b_scale, void* c, int32_t c_type, int64_t c_stride,
+                                   int64_t c_group_stride, int32_t accumulate, void* workspace, rlk_stream_t stream);
+
+/*
+ * The backward of the epilogue, with the quantisation of its result: from the
+ * kept z (BF16) and dy = d loss / d y, in FP32,
+ *   dz = dy act'(z);  gated: dz_gate = dy z_up act'(z_gate), dz_up = dy act(z_gate);
+ *   dbias = the sum of dz over the rows (of each group);
+ * and the codes of dz [rows, cols (2 cols gated)] along its rows and of its
+ * transpose, from one pass; dz itself is not stored.
+ *   groups   0: the rows are one matrix, and q, scale, qt, scale_t as
+ *            rlk_fp8_quantize's with block_rows 1; 1 to 1024: as
+ *            rlk_fp8_quantize_grouped's, with ends.
+ *   z        [rows, z_stride] BF16; may be NULL without an activation or gate.
+ *   dbias    NULL, or [groups or 1, cols (2 cols)] out in dbias_type, zero for a
+ *            group without rows; it needs a workspace of
+ *            rlk_fp8_act_grad_workspace_size bytes, 16-byte aligned, of one
+ *            call at a time.
+ * No output (the workspace is one) may overlap an input or another output.
+ */
+size_t rlk_fp8_act_grad_workspace_size(int64_t groups, int64_t rows, int64_t cols, int32_t gated);
+
+rlk_status rlk_fp8_act_grad(int64_t groups, int64_t rows, int64_t cols, const int32_t* ends, const void* dy,
+                            int32_t dy_type, int64_t dy_stride, const void* z, int64_t z_stride, int32_t activation,
+                            int32_t gated, void* q, int64_t q_stride, float* scale, void* qt, int64_t qt_stride,
+                            float* scale_t, void* dbias, int32_t dbias_type, void* workspace, rlk_stream_t stream);
+
+/*
  * Synchronises `stream` and decodes the status word a previous asynchronous
  * call left in `workspace` (RLK_OK when no device-side error was recorded).
  */

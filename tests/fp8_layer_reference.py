@@ -1,0 +1,90 @@
+"""The layers of 8-bit feed-forward blocks from their definitions, in plain numpy with 64 bits (test infrastructure only).
+
+z = A B^T + bias; y = act(z), or act(gate) * other, + residual; dz from dy and z.
+"""
+import math
+
+import numpy as np
+
+import fp8_reference as ref
+
+ACTS = ("none", "relu", "silu", "gelu", "gelu_tanh")
+_erf = np.vectorize(math.erf, otypes=[np.float64])
+_C = math.sqrt(2.0 / math.pi)
+
+
+def _sigmoid(z):
+    e = np.exp(-np.abs(z))
+    return np.where(z >= 0, 1.0 / (1.0 + e), e / (1.0 + e))
+
+
+def act(z, kind):
+    if kind == "relu":
+        return np.maximum(z, 0.0)
+    if kind == "silu":
+        return z * _sigmoid(z)
+    if kind == "gelu":
+        return 0.5 * z * (1.0 + _erf(z / math.sqrt(2.0)))
+    if kind == "gelu_tanh":
+        return 0.5 * z * (1.0 + np.tanh(_C * (z + 0.044715 * z ** 3)))
+    return z
+
+
+def slope(z, kind):
+    if kind == "relu":
+        return (z > 0).astype(np.float64)
+    if kind == "silu":
+        s = _sigmoid(z)
+        return s * (1.0 + z * (1.0 - s))
+    if kind == "gelu":
+        return 0.5 * (1.0 + _erf(z / math.sqrt(2.0))) + z * np.exp(-0.5 * z * z) / math.sqrt(2.0 * math.pi)
+    if kind == "gelu_tanh":
+        t = np.tanh(_C * (z + 0.044715 * z ** 3))
+        return 0.5 * (1.0 + t) + 0.5 * z * (1.0 - t * t) * _C * (1.0 + 3 * 0.044715 * z * z)
+    return np.ones_like(z)
+
+
+def forward(z, kind, gated):
+    n = z.shape[1] // 2
+    return act(z[:, :n], kind) * z[:, n:] if gated else act(z, kind)
+
+
+def backward(z, dy, kind, gated):
+    n = dy.shape[1]
+    if gated:
+        return np.concatenate((dy * z[:, n:] * slope(z[:, :n], kind), dy * act(z[:, :n], kind)), axis=1)
+    return dy * slope(z, kind)
+
+
+def act_error(z, kind):
+    """How far the FP32 evaluation of act may be from 64 bits: e^x and 1 / x are within 2^-21 together, a product and a
+    sum round 2^-24 each; gelu's distribution is within 1.5e-7 / 2 of Phi, and 2^-21 of itself."""
+    if kind in ("none", "relu"):
+        return np.zeros_like(z)
+    inner = np.abs(z) * (2.0 ** -22 if kind == "silu" else 2.0 ** -19)  # the exponent's rounding, times x s(1 - s) <= x / 4
+    return 2.0 ** -19 * np.abs(act(z, kind)) + 2e-7 * np.abs(z) + np.minimum(inner, 1.0) * 2.0 ** -2 * np.abs(z) * (np.abs(z) < 30) \
+        + 1e-37
+
+
+def layer(a, sa, b, sb, bias, kind, gated, residual):
+    """(z, y, how far FP32 may be from z and from y) of float64 values a [M, K], b [rows, K] (blocks)."""
+    z, terms = ref.matmul(a, sa, b, sb, 128)
+    K = a.shape[1]
+    dz = ref.bound(K, terms)
+    if bias is not None:
+        z = z + bias
+        dz = dz + 2.0 ** -24 * np.abs(z)
+    n = z.shape[1] // 2 if gated else z.shape[1]
+    g, dg = z[:, :n], dz[:, :n]
+    y = act(g, kind)
+    # the slopes are at most 1.13 in magnitude
+    err = 1.13 * dg + act_error(g, kind)
+    if gated:
+        u, du = z[:, n:], dz[:, n:]
+        err = err * (np.abs(u) + du) + np.abs(y) * du
+        y = y * u
+        err = err + 2.0 ** -24 * np.abs(y)
+    if residual is not None:
+        y = y + residual
+        err = err + 2.0 ** -24 * np.abs(y)
+    return z, y, dz, err

@@ -28,6 +28,8 @@ RLK_F32 = 1
 
 RLK_FP8_WORKSPACE = 256
 
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
 REDUCE_NONE = 0
 REDUCE_SUM = 1
 REDUCE_MEAN = 2
@@ -62,6 +64,13 @@ EXPORTED = (
     "rlk_linear_ce_bwd",
     "rlk_fp8_quantize",
     "rlk_fp8_matmul",
+    "rlk_fp8_matmul_act",
+    "rlk_fp8_grouped_matmul",
+    "rlk_fp8_quantize_grouped",
+    "rlk_fp8_quantize_batch",
+    "rlk_fp8_grouped_dweight",
+    "rlk_fp8_act_grad_workspace_size",
+    "rlk_fp8_act_grad",
     "rlk_logp_workspace_status",
     "rlk_selftest_bounded_wait",
     "rlk_status_string",
@@ -112,6 +121,13 @@ class LinearCeContract(ctypes.Structure):
         d = {name: getattr(self, name) for name, _ in self._fields_}
         d.update(kw)
         return LinearCeContract(**d)
+
+
+class Fp8Epilogue(ctypes.Structure):
+    """Mirror of ``rlk_fp8_epilogue`` (56 bytes)."""
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("z", ctypes.c_void_p),
+                ("residual_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64), ("bias_type", ctypes.c_int32),
+                ("residual_type", ctypes.c_int32), ("activation", ctypes.c_int32), ("gated", ctypes.c_int32)]
 
 
 class RlkError(RuntimeError):
@@ -182,13 +198,28 @@ def library():
         lib.rlk_linear_ce_fwd.restype = i
         lib.rlk_linear_ce_bwd.argtypes = [C, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
         lib.rlk_linear_ce_bwd.restype = i
-        i64 = ctypes.c_int64
+        i64, i32 = ctypes.c_int64, ctypes.c_int32
         lib.rlk_fp8_quantize.argtypes = [i64, i64, vp, ctypes.c_int32, i64, ctypes.c_int32, vp, i64, vp, vp, i64, vp,
                                          vp]
         lib.rlk_fp8_quantize.restype = i
         lib.rlk_fp8_matmul.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, ctypes.c_int32, vp, ctypes.c_int32,
                                        i64, ctypes.c_int32, vp, vp]
         lib.rlk_fp8_matmul.restype = i
+        E = ctypes.POINTER(Fp8Epilogue)
+        lib.rlk_fp8_matmul_act.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, vp, E, vp, i32, i64, vp, vp]
+        lib.rlk_fp8_grouped_matmul.argtypes = [i64, i64, i64, i64, vp, vp, i64, vp, vp, i64, i64, vp, E, vp, i32, i64,
+                                               i32, vp, vp]
+        lib.rlk_fp8_quantize_grouped.argtypes = [i64, i64, i64, vp, vp, i32, i64, vp, i64, vp, vp, i64, vp, vp]
+        lib.rlk_fp8_quantize_batch.argtypes = [i64, i64, i64, vp, i32, i64, i64, vp, i64, i64, vp, vp, i64, i64, vp, vp]
+        lib.rlk_fp8_grouped_dweight.argtypes = [i64, i64, i64, i64, vp, vp, i64, vp, vp, i64, vp, vp, i32, i64, i64,
+                                                i32, vp, vp]
+        lib.rlk_fp8_act_grad_workspace_size.argtypes = [i64, i64, i64, i32]
+        lib.rlk_fp8_act_grad_workspace_size.restype = ctypes.c_size_t
+        lib.rlk_fp8_act_grad.argtypes = [i64, i64, i64, vp, vp, i32, i64, vp, i64, i32, i32, vp, i64, vp, vp, i64, vp,
+                                         vp, i32, vp, vp]
+        for name in ("matmul_act", "grouped_matmul", "quantize_grouped", "quantize_batch", "grouped_dweight",
+                     "act_grad"):
+            getattr(lib, "rlk_fp8_" + name).restype = i
         lib.rlk_logp_workspace_status.argtypes = [vp, vp]
         lib.rlk_logp_workspace_status.restype = i
         lib.rlk_selftest_bounded_wait.argtypes = [ctypes.c_int64, vp, vp]
@@ -339,6 +370,48 @@ def rlk_fp8_matmul(M, N, K, a, a_stride, a_scale, b, b_stride, b_scale, b_block_
                    workspace, stream):
     return library().rlk_fp8_matmul(M, N, K, a, a_stride, a_scale, b, b_stride, b_scale, b_block_rows, c, c_type,
                                     c_stride, accumulate, workspace, stream)
+
+
+def rlk_fp8_matmul_act(M, N, K, a, a_stride, a_scale, b, b_stride, b_scale, epilogue, c, c_type, c_stride, workspace,
+                       stream):
+    return library().rlk_fp8_matmul_act(M, N, K, a, a_stride, a_scale, b, b_stride, b_scale,
+                                        None if epilogue is None else ctypes.byref(epilogue), c, c_type, c_stride,
+                                        workspace, stream)
+
+
+def rlk_fp8_grouped_matmul(groups, M, N, K, ends, a, a_stride, a_scale, b, b_stride, b_group_stride, b_scale, epilogue,
+                           c, c_type, c_stride, zero_rest, workspace, stream):
+    return library().rlk_fp8_grouped_matmul(groups, M, N, K, ends, a, a_stride, a_scale, b, b_stride, b_group_stride,
+                                            b_scale, None if epilogue is None else ctypes.byref(epilogue), c, c_type,
+                                            c_stride, zero_rest, workspace, stream)
+
+
+def rlk_fp8_quantize_grouped(groups, rows, cols, ends, x, x_type, x_stride, q, q_stride, scale, qt, qt_stride, scale_t,
+                             stream):
+    return library().rlk_fp8_quantize_grouped(groups, rows, cols, ends, x, x_type, x_stride, q, q_stride, scale, qt,
+                                              qt_stride, scale_t, stream)
+
+
+def rlk_fp8_quantize_batch(count, rows, cols, x, x_type, x_stride, x_batch_stride, q, q_stride, q_batch_stride, scale,
+                           qt, qt_stride, qt_batch_stride, scale_t, stream):
+    return library().rlk_fp8_quantize_batch(count, rows, cols, x, x_type, x_stride, x_batch_stride, q, q_stride,
+                                            q_batch_stride, scale, qt, qt_stride, qt_batch_stride, scale_t, stream)
+
+
+def rlk_fp8_grouped_dweight(groups, rows, M, N, ends, a, a_stride, a_scale, b, b_stride, b_scale, c, c_type, c_stride,
+                            c_group_stride, accumulate, workspace, stream):
+    return library().rlk_fp8_grouped_dweight(groups, rows, M, N, ends, a, a_stride, a_scale, b, b_stride, b_scale, c,
+                                             c_type, c_stride, c_group_stride, accumulate, workspace, stream)
+
+
+def rlk_fp8_act_grad_workspace_size(groups, rows, cols, gated):
+    return library().rlk_fp8_act_grad_workspace_size(groups, rows, cols, gated)
+
+
+def rlk_fp8_act_grad(groups, rows, cols, ends, dy, dy_type, dy_stride, z, z_stride, activation, gated, q, q_stride,
+                     scale, qt, qt_stride, scale_t, dbias, dbias_type, workspace, stream):
+    return library().rlk_fp8_act_grad(groups, rows, cols, ends, dy, dy_type, dy_stride, z, z_stride, activation, gated,
+                                      q, q_stride, scale, qt, qt_stride, scale_t, dbias, dbias_type, workspace, stream)
 
 
 def rlk_logp_workspace_status(workspace, stream):
@@ -902,20 +975,108 @@ def _quantize(x, block_rows, rowwise, transposed, stream):
     return q, scale, qt, scale_t
 
 
+def _type(t):
+    return RLK_F32 if t.dtype is _t().float32 else RLK_BF16
+
+
+def _matrices(t, name, dtypes):
+    """A 3-D CUDA tensor of matrices with contiguous rows: (count, rows, columns, row stride, matrix stride)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D CUDA tensor, not {list(t.shape)} on {t.device}")
+    rows, cols, stride = _matrix(t[0] if t.shape[0] else t.new_empty(t.shape[1:]), name, dtypes)
+    between = t.stride(0)
+    if t.shape[0] > 1 and between < (rows - 1) * stride + cols:
+        raise ValueError(f"{name}'s matrices overlap: its strides are {list(t.stride())}")
+    return t.shape[0], rows, cols, stride, between
+
+
+def _batch_codes(x, count, rows, cols):
+    """E4M3 matrices whose rows start on 16-byte boundaries, and their row stride."""
+    stride = -(-cols // 16) * 16
+    return _t().empty_strided((count, rows, cols), (rows * stride, stride, 1), dtype=_t().float8_e4m3fn,
+                              device=x.device), stride
+
+
+def _quantize_batch(x, block_rows, rowwise, transposed, stream):
+    torch = _t()
+    G, R, C, stride, between = _matrices(x, "x", (torch.bfloat16, torch.float32))
+    if block_rows != 128:
+        raise ValueError("several matrices are quantised with block_rows 128")
+    q = scale = qt = scale_t = None
+    ldq = ldt = 0
+    gr, gc = -(-R // 128), -(-C // 128)
+    with _allocating(stream):
+        if rowwise:
+            q, ldq = _batch_codes(x, G, R, C)
+            scale = torch.empty((G, gc, gr), dtype=torch.float32, device=x.device)
+        if transposed:
+            qt, ldt = _batch_codes(x, G, C, R)
+            scale_t = torch.empty((G, gr, gc), dtype=torch.float32, device=x.device)
+    st = rlk_fp8_quantize_batch(G, R, C, x.data_ptr(), _type(x), stride, between, _ptr(q), ldq, R * ldq, _ptr(scale),
+                                _ptr(qt), ldt, C * ldt, _ptr(scale_t), _raw_stream(x, stream))
+    if st:
+        check(st)
+    _used_here(stream, q, scale, qt, scale_t)
+    return q, scale, qt, scale_t
+
+
 def fp8_quantize(x, block_rows=1, transpose=False, stream=None):
     """(q, scale) of a BF16 or FP32 matrix [R, C]: E4M3 values and one FP32 scale for each 1 x 128 group of a row
     (block_rows 1) or each 128 x 128 block (128), so that x ~ q * scale.
 
     ``scale`` is group-major: [ceil(C / 128), R] or [ceil(C / 128), ceil(R / 128)].  With ``transpose`` the result
     is that of x's transpose [C, R].  q's rows start on 16-byte boundaries (a view where C is not a multiple of 16).
+    Several matrices [G, R, C] (experts' weights, block_rows 128) give q [G, R, C] and scale [G, ...], each its own.
     """
-    q, scale, qt, scale_t = _quantize(x, block_rows, not transpose, transpose, stream)
+    q, scale, qt, scale_t = (_quantize if x.dim() != 3 else _quantize_batch)(x, block_rows, not transpose, transpose, stream)
     return (qt, scale_t) if transpose else (q, scale)
 
 
 def fp8_quantize_both(x, block_rows=1, stream=None):
     """(q, scale, qt, scale_t): fp8_quantize of x and of its transpose from one read of x."""
-    return _quantize(x, block_rows, True, True, stream)
+    return (_quantize if x.dim() != 3 else _quantize_batch)(x, block_rows, True, True, stream)
+
+
+def _ends(ends, like):
+    """The groups that int32 ends [G] describe: (G, pointer)."""
+    if ends.dtype is not _t().int32 or ends.dim() != 1 or not ends.is_contiguous() or not ends.is_cuda:
+        raise TypeError(f"ends must be a contiguous int32 CUDA tensor [G], not {str(ends.dtype)[6:]} "
+                        f"{list(ends.shape)} on {ends.device}")
+    return ends.shape[0], ends.data_ptr()
+
+
+def group_tiles(groups, rows):
+    """Groups of 128 rows that fp8_quantize_grouped leaves room for: what any division of `rows` can ask for."""
+    return rows // 128 + min(groups, rows)
+
+
+def fp8_quantize_grouped(x, ends, rowwise=True, transpose=True, stream=None):
+    """(q, scale, qt, scale_t): fp8_quantize_both of rows that belong to groups, group e ending at row ends[e].
+
+    The transpose's groups of 128 start anew with each group of rows, padded with zeros to whole 128s: qt is
+    [C, 128 * group_tiles(G, R)] and scale_t [group_tiles(G, R), C], of which the first ceil(rows / 128) of each group,
+    one group after the other, are written.  Rows of q and scale behind the last group are not written.  ``rowwise`` or
+    ``transpose`` False leaves the one pair out (None).
+    """
+    torch = _t()
+    R, C, stride = _matrix(x, "x", (torch.bfloat16, torch.float32))
+    G, pe = _ends(ends, x)
+    q = scale = qt = scale_t = None
+    ldq = ldt = 0
+    tiles = group_tiles(G, R)
+    with _allocating(stream):
+        if rowwise:
+            q, ldq = _codes(x, R, C)
+            scale = _new(x, -(-C // 128), R, torch.float32)
+        if transpose:
+            qt, ldt = _codes(x, C, 128 * tiles)
+            scale_t = _new(x, tiles, C, torch.float32)
+    st = rlk_fp8_quantize_grouped(G, R, C, pe, x.data_ptr(), _type(x), stride, _ptr(q), ldq, _ptr(scale), _ptr(qt),
+                                  ldt, _ptr(scale_t), _raw_stream(x, stream))
+    if st:
+        check(st)
+    _used_here(stream, q, scale, qt, scale_t)
+    return q, scale, qt, scale_t
 
 
 _fp8_workspaces = {}
@@ -1003,6 +1164,232 @@ def fp8_matmul(a, a_scale, b, b_scale, b_block_rows=128, out_dtype=None, out=Non
                 workspace.zero_()  # reported once, not with every later call
         check(status)
     return out
+
+
+def _validated(validate, workspace, given, st, stream):
+    """Reports an expired wait of this call or of ones before it on its stream, once where the record is ours."""
+    if not validate:
+        return
+    status = rlk_logp_workspace_status(workspace.data_ptr(), st)
+    if status and not given:
+        with _allocating(stream):
+            workspace.zero_()
+    check(status)
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(str(a) for a in ACTIVATIONS)}, not {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _layer(a, a_scale, b, b_scale, ends, bias, activation, gated, residual, keep, out_dtype, out, workspace, validate,
+           stream):
+    torch = _t()
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    both = (torch.bfloat16, torch.float32)
+    M, K, lda = _matrix(a, "a", codes)
+    if ends is None:
+        rows, Kb, ldb = _matrix(b, "b", codes)
+        lead, group = (), 0
+    else:
+        G, pe = _ends(ends, a)
+        Gb, rows, Kb, ldb, group = _matrices(b, "b", codes)
+        if Gb != G:
+            raise ValueError(f"ends has {G} groups and b {Gb}")
+        lead = (G,)
+    if Kb != K or K < 1:
+        raise ValueError(f"a is [{M}, {K}] and b {list(b.shape)}: their rows must have one length, at least 1")
+    act = _activation(activation)
+    if gated and rows % 128:
+        raise ValueError(f"a gated layer's b holds two halves of a multiple of 64 rows, not {rows} rows")
+    N = rows // 2 if gated else rows
+    groups = -(-K // 128)
+    pa = _scale_operand(a_scale, "a_scale", groups, M)
+    want = lead + (groups, -(-rows // 128))
+    if b_scale.dtype is not torch.float32 or b_scale.shape != want or not b_scale.is_contiguous() or \
+            not b_scale.is_cuda:
+        raise ValueError(f"b_scale must be a contiguous FP32 CUDA tensor {list(want)}, not "
+                         f"{str(b_scale.dtype)[6:]} {list(b_scale.shape)}")
+    e = Fp8Epilogue(activation=act, gated=int(bool(gated)))
+    if bias is not None:
+        if bias.shape != lead + (rows,):
+            raise ValueError(f"bias is {list(bias.shape)}; the layer's is {list(lead + (rows,))}")
+        e.bias, e.bias_type = _vector(bias, "bias", bias.numel(), both), _type(bias)
+    if residual is not None:
+        r, c, e.residual_stride = _matrix(residual, "residual", both)
+        if (r, c) != (M, N):
+            raise ValueError(f"residual is {list(residual.shape)}; the result is [{M}, {N}]")
+        e.residual, e.residual_type = residual.data_ptr(), _type(residual)
+    z = None
+    fresh = out is None
+    if fresh:
+        out_dtype = out_dtype or torch.bfloat16
+        if out_dtype not in both:
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    else:
+        r, c, ldc = _matrix(out, "out", both)
+        if (r, c) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out is {str(out.dtype)[6:]} {list(out.shape)}; the result is [{M}, {N}]")
+    with _allocating(stream):
+        if fresh:
+            out, ldc = _new(a, M, N, out_dtype), N
+        if keep:  # rows on 16-byte boundaries, for the backward's loads
+            e.z_stride = -(-rows // 8) * 8
+            z = _new(a, M, rows, torch.bfloat16, e.z_stride)
+            e.z = z.data_ptr()
+    _used_here(stream, out if fresh else None, z)
+    st = _raw_stream(a, stream)
+    given = workspace is not None
+    if given:
+        _need(workspace, "workspace", RLK_FP8_WORKSPACE, ("uint8",))
+    else:
+        workspace = _fp8_workspace(a, st, stream)
+    lda, ldb = _padded(lda, M, K, 16), _padded(ldb, rows, K, 16)
+    if ends is None:
+        status = rlk_fp8_matmul_act(M, N, K, a.data_ptr(), lda, pa, b.data_ptr(), ldb, b_scale.data_ptr(), e,
+                                    out.data_ptr(), _type(out), ldc, workspace.data_ptr(), st)
+    else:
+        status = rlk_fp8_grouped_matmul(G, M, N, K, pe, a.data_ptr(), lda, pa, b.data_ptr(), ldb, group,
+                                        b_scale.data_ptr(), e, out.data_ptr(), _type(out), ldc, int(fresh),
+                                        workspace.data_ptr(), st)
+    if status:
+        check(status)
+    _validated(validate, workspace, given, st, stream)
+    return (out, z) if keep else out
+
+
+def fp8_matmul_act(a, a_scale, b, b_scale, bias=None, activation=None, gated=False, residual=None, keep=False,
+                   out_dtype=None, out=None, workspace=None, validate=False, stream=None):
+    """act(a @ b^T + bias) + residual [M, N] of E4M3 operands: fp8_matmul (b in 128 x 128 blocks) with a layer's
+    epilogue, all in FP32 and rounded once.
+
+    ``activation`` is None, "relu", "silu", "gelu" or "gelu_tanh".  With ``gated`` b holds N rows of the gate, then N
+    more (N a multiple of 64), and the result is act(gate) * other + residual.  ``bias`` [rows of b] and ``residual``
+    [M, N] (rows may be strided; ``out`` itself is allowed) are BF16 or FP32.  With ``keep`` the result is (out, z), z
+    the pre-activation in BF16 as fp8_act_grad needs it.  ``out_dtype``, ``out``, ``workspace``, ``validate``: as
+    fp8_matmul's.
+    """
+    return _layer(a, a_scale, b, b_scale, None, bias, activation, gated, residual, keep, out_dtype, out, workspace,
+                  validate, stream)
+
+
+def fp8_grouped_matmul(a, a_scale, b, b_scale, ends, bias=None, activation=None, gated=False, keep=False,
+                       out_dtype=None, out=None, workspace=None, validate=False, stream=None):
+    """fp8_matmul_act for rows that belong to groups (a mixture's experts): group e is rows [ends[e - 1], ends[e]) of a.
+
+    ``ends`` is int32 [G] on the GPU (nothing is read back), b [G, rows, K], b_scale [G, ceil(K / 128), ceil(rows / 128)]
+    and ``bias`` [G, rows], as fp8_quantize gives them for [G, rows, K] weights.  Rows behind the last group are zero, or
+    in an ``out`` of the caller's as they were (those of z are undefined).  A group without rows is allowed and costs
+    nothing.
+    """
+    return _layer(a, a_scale, b, b_scale, ends, bias, activation, gated, None, keep, out_dtype, out, workspace,
+                  validate, stream)
+
+
+def fp8_grouped_dweight(at, at_scale, bt, bt_scale, ends, rows, out_dtype=None, out=None, accumulate=False,
+                        workspace=None, validate=False, stream=None):
+    """[G, M, N]: for each group, its columns of ``at`` [M, ...] times those of ``bt`` [N, ...] transposed: the weight
+    gradients dy_e^T x_e, with (at, at_scale) and (bt, bt_scale) the qt and scale_t that fp8_quantize_grouped (or
+    fp8_act_grad) gives for dy and x of ``rows`` rows.
+
+    BF16 or FP32 (``out_dtype``), in ``out`` if given; ``accumulate`` adds to an FP32 ``out``.  Zero (or unchanged) for a
+    group without rows.
+    """
+    torch = _t()
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    both = (torch.bfloat16, torch.float32)
+    G, pe = _ends(ends, at)
+    tiles = group_tiles(G, rows)
+    M, deep, lda = _matrix(at, "at", codes)
+    N, deep_b, ldb = _matrix(bt, "bt", codes)
+    if deep != 128 * tiles or deep_b != deep:
+        raise ValueError(f"at and bt are {list(at.shape)} and {list(bt.shape)}; {G} groups of {rows} rows have "
+                         f"{128 * tiles} columns")
+    pa = _scale_operand(at_scale, "at_scale", tiles, M)
+    pb = _scale_operand(bt_scale, "bt_scale", tiles, N)
+    fresh = out is None
+    if fresh:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out_dtype = out_dtype or torch.bfloat16
+        if out_dtype not in both:
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+        with _allocating(stream):
+            out = torch.empty((G, M, N), dtype=out_dtype, device=at.device)
+        _used_here(stream, out)
+        ldc, between = N, M * N
+    else:
+        Go, Mo, No, ldc, between = _matrices(out, "out", both)
+        if (Go, Mo, No) != (G, M, N) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out is {str(out.dtype)[6:]} {list(out.shape)}; the result is [{G}, {M}, {N}]")
+    if rows == 0:
+        if not accumulate:
+            with _allocating(stream):
+                out.zero_()
+        return out
+    st = _raw_stream(at, stream)
+    given = workspace is not None
+    if given:
+        _need(workspace, "workspace", RLK_FP8_WORKSPACE, ("uint8",))
+    else:
+        workspace = _fp8_workspace(at, st, stream)
+    status = rlk_fp8_grouped_dweight(G, rows, M, N, pe, at.data_ptr(), _padded(lda, M, deep, 16), pa, bt.data_ptr(),
+                                     _padded(ldb, N, deep, 16), pb, out.data_ptr(), _type(out), ldc, between,
+                                     int(accumulate), workspace.data_ptr(), st)
+    if status:
+        check(status)
+    _validated(validate, workspace, given, st, stream)
+    return out
+
+
+def fp8_act_grad(dy, z=None, activation=None, gated=False, ends=None, rowwise=True, transpose=True, bias_dtype=None,
+                 stream=None):
+    """(q, scale, qt, scale_t, dbias): the backward of fp8_matmul_act's epilogue, quantised as the products that follow
+    need it, in one pass.
+
+    From dy [R, N] (BF16 or FP32) and the kept z, in FP32: dz = dy * act'(z), or (gated) the gate's half
+    dy * z_other * act'(z_gate), then the other half dy * act(z_gate).  q, scale, qt, scale_t are fp8_quantize_both of dz,
+    with ``ends`` fp8_quantize_grouped's.  ``bias_dtype`` asks for dbias, the sum of dz over the rows ([G, ...] with
+    ``ends``).  What is not asked for is None.  z may be None without an activation and a gate.
+    """
+    torch = _t()
+    both = (torch.bfloat16, torch.float32)
+    R, N, stride = _matrix(dy, "dy", both)
+    act = _activation(activation)
+    wide = 2 * N if gated else N
+    pz = ldz = 0
+    if act or gated:
+        if z is None:
+            raise ValueError("an activation or a gate needs z")
+        rz, cz, ldz = _matrix(z, "z", (torch.bfloat16,))
+        if (rz, cz) != (R, wide):
+            raise ValueError(f"z is {list(z.shape)} and dy {list(dy.shape)}: z must be [{R}, {wide}]")
+        pz = z.data_ptr()
+    G, pe = (0, None) if ends is None else _ends(ends, dy)
+    q = scale = qt = scale_t = dbias = ws = None
+    ldq = ldt = 0
+    tiles = group_tiles(G, R) if G else -(-R // 128)
+    with _allocating(stream):
+        if rowwise:
+            q, ldq = _codes(dy, R, wide)
+            scale = _new(dy, -(-wide // 128), R, torch.float32)
+        if transpose:
+            qt, ldt = _codes(dy, wide, 128 * tiles if G else R)
+            scale_t = _new(dy, tiles, wide, torch.float32)
+        if bias_dtype is not None:
+            if bias_dtype not in both:
+                raise TypeError("bias_dtype must be torch.bfloat16 or torch.float32")
+            dbias = torch.empty((G, wide) if ends is not None else (wide,), dtype=bias_dtype, device=dy.device)
+            ws = torch.empty(max(1, rlk_fp8_act_grad_workspace_size(G, R, N, int(bool(gated)))), dtype=torch.uint8,
+                             device=dy.device)
+    st = rlk_fp8_act_grad(G, R, N, pe, dy.data_ptr(), _type(dy), stride, pz or None, ldz, act, int(bool(gated)),
+                          _ptr(q), ldq, _ptr(scale), _ptr(qt), ldt, _ptr(scale_t), _ptr(dbias),
+                          RLK_F32 if bias_dtype is torch.float32 else RLK_BF16, _ptr(ws), _raw_stream(dy, stream))
+    if st:
+        check(st)
+    _used_here(stream, q, scale, qt, scale_t, dbias)
+    return q, scale, qt, scale_t, dbias
 
 
 # ------------------------------------------------------------------ cross entropy over a large vocabulary

@@ -15,14 +15,18 @@ differentiable.
 ``LinearCrossEntropy`` (``linear_cross_entropy``) runs ``rlk_linear_ce_fwd``
 and ``rlk_linear_ce_bwd``; ``Fp8Linear`` (``fp8_linear``) quantises with
 ``rlk_fp8_quantize`` and forms its output and both gradients with
-``rlk_fp8_matmul``.
+``rlk_fp8_matmul``; ``Fp8Layer`` (``fp8_linear`` with a bias, an activation, a
+gate or a residual) and ``Fp8GroupedLayer`` (``fp8_grouped_linear``) with
+``rlk_fp8_matmul_act`` and ``rlk_fp8_act_grad``, ``rlk_fp8_grouped_matmul`` and
+``rlk_fp8_grouped_dweight``.
 """
 import torch
 from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
-from . import (MASK_EXPLICIT, MASK_IGNORE_INDEX, REDUCE_MEAN, REDUCE_NONE, REDUCE_SUM, Contract, fp8_matmul,
-               fp8_quantize, fp8_quantize_both, linear_ce_bwd, linear_ce_contract, linear_ce_fwd, logp_bwd,
+from . import (ACTIVATIONS, MASK_EXPLICIT, MASK_IGNORE_INDEX, REDUCE_MEAN, REDUCE_NONE, REDUCE_SUM, Contract,
+               fp8_act_grad, fp8_grouped_dweight, fp8_grouped_matmul, fp8_matmul, fp8_matmul_act, fp8_quantize,
+               fp8_quantize_both, fp8_quantize_grouped, linear_ce_bwd, linear_ce_contract, linear_ce_fwd, logp_bwd,
                logp_fused_lmhead, logp_fused_lmhead_bwd, logp_fused_lmhead_bwd_kept, logp_fused_lmhead_keep, logp_fwd)
 
 _LOGIT_DTYPES = (torch.bfloat16, torch.int16)  # int16: BF16 bits viewed as integers
@@ -211,12 +215,139 @@ class Fp8Linear(torch.autograd.Function):
         return dx, dw
 
 
-def fp8_linear(x, weight):
-    """x [..., K] @ weight [N, K]^T in FP8 with autograd: BF16 out, gradients in the inputs' types (BF16 or FP32).
+def _rows_of(dy):
+    """dy as the quantisations take it: BF16 or FP32, contiguous rows that do not overlap."""
+    dy = dy if dy.dtype in (torch.bfloat16, torch.float32) else dy.to(torch.bfloat16)
+    return dy if dy.stride(-1) == 1 and (dy.shape[0] <= 1 or dy.stride(0) >= dy.shape[1]) else dy.contiguous()
+
+
+class Fp8Layer(torch.autograd.Function):
+    """y = act(x @ weight^T + bias) + residual in FP8.  z, the argument of the activation, is kept in BF16; the backward
+    forms dz, the sum of its rows for the bias, and its codes along the rows and along the tokens in one pass, then the
+    two products of Fp8Linear's."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, activation, gated):
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        plain = not gated and not ACTIVATIONS[activation]
+        xq, xs, xtq, xts = fp8_quantize_both(x) if need_w else (*fp8_quantize(x), None, None)
+        wq, ws, wtq, wts = fp8_quantize_both(weight, block_rows=128) if need_x else \
+            (*fp8_quantize(weight, block_rows=128), None, None)
+        keep = not plain and (need_x or need_w or need_b)
+        y = fp8_matmul_act(xq, xs, wq, ws, bias, activation, gated, residual, keep)
+        y, z = y if keep else (y, None)
+        ctx.save_for_backward(xtq, xts, wtq, wts, z)
+        ctx.types = [None if t is None else t.dtype for t in (x, weight, bias, residual)]
+        ctx.sizes = x.shape, weight.shape
+        ctx.layer = activation, gated
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        xtq, xts, wtq, wts, z = ctx.saved_tensors
+        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        tx, tw, tb, tr = ctx.types
+        dres = dy.to(tr) if need_r else None
+        dx = dw = db = None
+        if dy.shape[0] == 0:
+            x, w = ctx.sizes
+            dx = dy.new_zeros(x, dtype=tx) if need_x else None
+            dw = dy.new_zeros(w, dtype=tw) if need_w else None
+            db = dy.new_zeros(w[:1], dtype=tb) if need_b else None
+        elif need_x or need_w or need_b:
+            q, s, qt, st, db = fp8_act_grad(_rows_of(dy), z, *ctx.layer, rowwise=need_x, transpose=need_w,
+                                            bias_dtype=tb if need_b else None)
+            dx = fp8_matmul(q, s, wtq, wts, out_dtype=tx) if need_x else None
+            dw = fp8_matmul(qt, st, xtq, xts, b_block_rows=1, out_dtype=tw) if need_w else None
+        return dx, dw, db, dres, None, None
+
+
+class Fp8GroupedLayer(torch.autograd.Function):
+    """Fp8Layer for rows that belong to groups, each with a weight and a bias of its own."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, ends, activation, gated):
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        plain = not gated and not ACTIVATIONS[activation]
+        xq, xs, xtq, xts = fp8_quantize_grouped(x, ends) if need_w else (*fp8_quantize(x), None, None)
+        wq, ws, wtq, wts = fp8_quantize_both(weight, block_rows=128) if need_x else \
+            (*fp8_quantize(weight, block_rows=128), None, None)
+        keep = not plain and (need_x or need_w or need_b)
+        y = fp8_grouped_matmul(xq, xs, wq, ws, ends, bias, activation, gated, keep)
+        y, z = y if keep else (y, None)
+        ctx.save_for_backward(xtq, xts, wtq, wts, z, ends)
+        ctx.types = x.dtype, weight.dtype, None if bias is None else bias.dtype
+        ctx.sizes = x.shape, weight.shape
+        ctx.layer = activation, gated
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        xtq, xts, wtq, wts, z, ends = ctx.saved_tensors
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        tx, tw, tb = ctx.types
+        x, w = ctx.sizes
+        dx = dw = db = None
+        if dy.shape[0] == 0:
+            dx = dy.new_zeros(x, dtype=tx) if need_x else None
+            dw = dy.new_zeros(w, dtype=tw) if need_w else None
+            db = dy.new_zeros(w[:2], dtype=tb) if need_b else None
+        else:
+            dy = _rows_of(dy)
+            if z is None and not need_b:
+                q, s, qt, st = fp8_quantize_grouped(dy, ends, need_x, need_w)
+            else:
+                q, s, qt, st, db = fp8_act_grad(dy, z, *ctx.layer, ends=ends, rowwise=need_x, transpose=need_w,
+                                                bias_dtype=tb if need_b else None)
+            dx = fp8_grouped_matmul(q, s, wtq, wts, ends, out_dtype=tx) if need_x else None
+            dw = fp8_grouped_dweight(qt, st, xtq, xts, ends, x[0], out_dtype=tw) if need_w else None
+        return dx, dw, db, None, None, None
+
+
+def fp8_linear(x, weight, bias=None, activation=None, gated=False, residual=None):
+    """act(x [..., K] @ weight [N, K]^T + bias) + residual in FP8 with autograd: BF16 out, gradients in the inputs' types
+    (BF16 or FP32).
 
     Forward and backward quantise with one FP32 scale per 128 elements (or 128 x 128 weights) and sum in FP32; what is
-    saved for the backward are the E4M3 transposes, one byte an element.
+    saved for the backward are the E4M3 transposes, one byte an element, and with an activation or a gate its argument
+    in BF16.  ``activation`` is None, "relu", "silu", "gelu" or "gelu_tanh"; with ``gated`` the weight holds the gate's
+    rows, then as many more (a multiple of 64 each), and the result is act(gate) * other.  ``bias`` has a value for each
+    row of the weight; ``residual`` has the result's shape.
     """
+    if bias is None and residual is None and not gated and activation in (None, "none"):
+        return _linear(x, weight)
+    lead = x.shape[:-1]
+    rows = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    n = weight.shape[0] // 2 if gated else weight.shape[0]
+    if residual is not None:
+        if residual.shape != (*lead, n):
+            raise ValueError(f"residual is {list(residual.shape)}; the result is {[*lead, n]}")
+        residual = residual if x.dim() == 2 else residual.reshape(-1, n)
+        residual = residual if residual.stride(-1) == 1 else residual.contiguous()
+    if _differentiated(*(t for t in (x, weight, bias, residual) if t is not None)):
+        y = Fp8Layer.apply(rows, weight, bias, residual, activation, bool(gated))
+    else:
+        y = fp8_matmul_act(*fp8_quantize(rows), *fp8_quantize(weight, block_rows=128), bias, activation, gated, residual)
+    return y if x.dim() == 2 else y.reshape(*lead, n)
+
+
+def fp8_grouped_linear(x, weight, ends, bias=None, activation=None, gated=False):
+    """fp8_linear for rows that belong to groups (a mixture's experts), with autograd: group e is rows
+    [ends[e - 1], ends[e]) of x [M, K], with weight[e] of weight [G, N, K] and bias[e] of bias [G, N].
+
+    ``ends`` is int32 [G] on the GPU, the running sum of the groups' counts of rows; nothing is read back.  Rows behind
+    the last group (padding) have a zero result and a zero gradient, and reach nothing whatever they hold; a group
+    without rows has zero gradients.
+    """
+    if _differentiated(*(t for t in (x, weight, bias) if t is not None)):
+        return Fp8GroupedLayer.apply(x, weight, bias, ends, activation, bool(gated))
+    return fp8_grouped_matmul(*fp8_quantize(x), *fp8_quantize(weight, block_rows=128), ends, bias, activation, gated)
+
+
+def _linear(x, weight):
+    """fp8_linear without an epilogue."""
     lead = x.shape[:-1]
     rows = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
     if _differentiated(x, weight):

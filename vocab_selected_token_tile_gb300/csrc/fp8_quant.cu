@@ -39,7 +39,10 @@
 #include <stdint.h>
 
 #include <string>
+#include <type_traits>
 
+#include "rlk_act.cuh"
+#include "rlk_groups.cuh"
 #include "rlk_internal.h"
 #include "rlk_ptx.cuh"
 
@@ -58,6 +61,29 @@ struct QuantParams {
     int64_t ldq, ldqt;
     float *scale, *scale_t;
     int32_t vec;  // x rows are 16-byte aligned
+};
+
+// What the tile's 128 rows are: one matrix's; one of several matrices' (the
+// batch: pointers moved to it, else as before); rows of a group, whose 128
+// columns of the transpose are the group's own.
+enum Rows8 : int { kOne, kBatch, kGroups };
+
+struct QuantExtParams : QuantParams {
+    int64_t x_b, q_b, qt_b, s_b, st_b;  // kBatch: elements between matrices
+    const int32_t* ends;                // kGroups
+    int32_t G;
+    // the epilogue's backward: dy [R, C or C / 2] and z [R, C] instead of x
+    const void* dy;
+    const uint16_t* z;                  // NULL: dz = dy
+    int64_t lddy, ldz;
+    int32_t dy_f32, dy_vec, z_vec, act, gated;
+    float* part;                        // NULL, or each tile's sums over its rows [row tile, C]
+};
+
+// Where a tile's rows lie: rows [row0, end) of x and q, columns [t0, t_end) of
+// qt, row rt of scale_t.
+struct RowTile {
+    int64_t row0, end, t0, t_end, rt;
 };
 
 __device__ __forceinline__ void scale_of(float amax, float& s, float& r) {
@@ -83,9 +109,10 @@ struct Block {
 };
 
 template <bool F32>
-__device__ __forceinline__ void load_row(Block<F32>& b, int i, const QuantParams& p, int64_t r, int64_t c0) {
+__device__ __forceinline__ void load_row(Block<F32>& b, int i, const QuantParams& p, int64_t r, int64_t end,
+                                         int64_t c0) {
     constexpr int W = F32 ? 8 : 4;
-    if (r >= p.R || c0 >= p.C) {
+    if (r >= end || c0 >= p.C) {
 #pragma unroll
         for (int j = 0; j < W; ++j) b.w[i][j] = 0u;
         return;
@@ -109,6 +136,58 @@ __device__ __forceinline__ void load_row(Block<F32>& b, int i, const QuantParams
             const uint32_t lo = c0 + 2 * j < p.C ? src[0] : 0u, hi = c0 + 2 * j + 1 < p.C ? src[1] : 0u;
             b.w[i][j] = lo | (hi << 16);
         }
+    }
+}
+
+// 8 consecutive elements of a row in FP32, zero from `left` on.
+__device__ __forceinline__ void load8(float (&v)[8], const void* x, int64_t at, bool f32, bool vec, int64_t left) {
+    if (vec && left >= 8) {
+        if (f32) {
+            const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+            const float4 a = __ldcs(s), b = __ldcs(s + 1);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const uint4 a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[2 * j] = bf16lo_to_f32(w[j]), v[2 * j + 1] = bf16hi_to_f32(w[j]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = j >= left ? 0.f
+               : f32     ? static_cast<const float*>(x)[at + j]
+                         : __uint_as_float((uint32_t) static_cast<const uint16_t*>(x)[at + j] << 16);
+}
+
+// Row i of the thread's block of dz.  Gated: columns [0, C / 2) are the gate's
+// (8 columns are of one half: C / 2 is a multiple of 64).
+template <int ACT>
+__device__ __forceinline__ void load_dz_row(Block<true>& b, int i, const QuantExtParams& p, int64_t r, int64_t end,
+                                            int64_t c0) {
+    const int64_t N = p.gated ? p.C / 2 : p.C, c = c0 >= N ? c0 - N : c0, left = c0 < p.C ? N - c : 0;
+    if (r >= end || left <= 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b.w[i][j] = 0u;
+        return;
+    }
+    float dy[8], z[8];
+    load8(dy, p.dy, r * p.lddy + c, p.dy_f32, p.dy_vec, left);
+    if (ACT != RLK_ACT_NONE || p.gated) load8(z, p.z, r * p.ldz + c, false, p.z_vec, left);
+    if (p.gated && c0 < N) {
+        float up[8];
+        load8(up, p.z, r * p.ldz + N + c, false, p.z_vec, left);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dy[j] = __fmul_rn(dy[j], up[j]);
+    }
+    const bool other = p.gated && c0 >= N;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float d = other ? __fmul_rn(dy[j], act_f32(z[j], ACT))
+                        : ACT == RLK_ACT_NONE ? dy[j]
+                                              : __fmul_rn(dy[j], act_slope_f32(z[j], ACT));
+        b.w[i][j] = __float_as_uint(j < left ? d : 0.f);
     }
 }
 
@@ -137,10 +216,10 @@ struct TileShared {
 };
 
 template <bool F32, bool BLOCKS, bool TRANS>
-__device__ __forceinline__ void quantize_tile(const QuantParams& p, const Block<F32>& b, int64_t ct, int64_t rt,
-                                              TileShared<F32, BLOCKS, TRANS>& sh) {
+__device__ __forceinline__ void quantize_tile(const QuantParams& p, const Block<F32>& b, int64_t ct,
+                                              const RowTile& at, TileShared<F32, BLOCKS, TRANS>& sh) {
     const int t = threadIdx.x, cx = t & 15, ry = t >> 4;
-    const int64_t r0 = rt * kQT + ry * 8, c0 = ct * kQT + cx * 8;
+    const int64_t r0 = at.row0 + ry * 8, c0 = ct * kQT + cx * 8, rt = at.rt;
     constexpr int W = F32 ? 8 : 4;  // words of a row's 8 elements
 
     // the columns' maxima over this thread's 8 rows, word by word
@@ -221,7 +300,7 @@ __device__ __forceinline__ void quantize_tile(const QuantParams& p, const Block<
             }
             float s, r;
             scale_of(m, s, r);
-            if (cx < 8 && r0 + cx < p.R) p.scale[ct * p.R + r0 + cx] = s;
+            if (cx < 8 && r0 + cx < at.end) p.scale[ct * p.R + r0 + cx] = s;
 #pragma unroll
             for (int i = 0; i < 8; ++i) rr[i] = __shfl_sync(0xFFFFFFFFu, r, i, 16);
         }
@@ -275,7 +354,7 @@ __device__ __forceinline__ void quantize_tile(const QuantParams& p, const Block<
         if (p.q) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (r0 + i + h < p.R)
+                if (r0 + i + h < at.end)
                     store_codes(p.q + (r0 + i + h) * p.ldq, c0, p.C, make_uint2(code[h][0], code[h][1]));
         }
     }
@@ -287,8 +366,8 @@ __device__ __forceinline__ void quantize_tile(const QuantParams& p, const Block<
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int col = k * 16 + ry, piece = cx;
-            if (ct * kQT + col < p.C && rt * kQT + piece * 8 < p.R)
-                store_codes(p.qt + (ct * kQT + col) * p.ldqt, rt * kQT + piece * 8, p.R,
+            if (ct * kQT + col < p.C && at.t0 + piece * 8 < at.t_end)
+                store_codes(p.qt + (ct * kQT + col) * p.ldqt, at.t0 + piece * 8, at.t_end,
                             sh.tile_t[col * 16 + (piece ^ (col >> 3))]);
         }
     }
@@ -302,8 +381,123 @@ __global__ void __launch_bounds__(kQThreads, F32 ? 3 : 4) quantize_kernel(const 
     if (rt * kQT >= p.R) return;
     Block<F32> b;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) load_row(b, i, p, rt * kQT + ry * 8 + i, ct * kQT + cx * 8);
-    quantize_tile<F32, BLOCKS, TRANS>(p, b, ct, rt, sh);
+    for (int i = 0; i < 8; ++i) load_row(b, i, p, rt * kQT + ry * 8 + i, p.R, ct * kQT + cx * 8);
+    quantize_tile<F32, BLOCKS, TRANS>(p, b, ct, RowTile{rt * kQT, p.R, rt * kQT, p.R, rt}, sh);
+}
+
+// The row tile of a group that blockIdx.y counts, false behind the last.  Each
+// CTA looks it up for itself (rlk_groups.cuh), 0.5 us beside its own chain of 3.
+__device__ __forceinline__ bool group_tile(const QuantExtParams& p, int64_t rt, GroupTable* tab, RowTile& at) {
+    groups_build<kQThreads>(tab, p.ends, p.G, (int)p.R, kQT, 1, false);
+    __syncthreads();
+    if (rt >= tab->first[p.G]) return false;
+    const int e = group_of(tab, p.G - 1, (int)rt);
+    const int64_t row0 = tab->begin[e] + (rt - tab->first[e]) * kQT;
+    at = RowTile{row0, min(row0 + kQT, (int64_t)tab->begin[e + 1]), rt * kQT, rt * kQT + kQT, rt};
+    return true;
+}
+
+// Rows of groups, and several matrices, from x.
+template <bool F32, bool TRANS, int ROWS>
+__global__ void __launch_bounds__(kQThreads, F32 ? 3 : 4)
+    quantize_ext_kernel(const __grid_constant__ QuantExtParams p0) {
+    constexpr bool kBlocks = ROWS == kBatch;
+    __shared__ TileShared<F32, kBlocks, TRANS> sh;
+    __shared__ typename std::conditional<ROWS == kGroups, GroupTable, int>::type tab;
+    const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
+    const int64_t ct = blockIdx.x, rt = blockIdx.y + (int64_t)blockIdx.z * 65535;
+    QuantParams p = p0;
+    RowTile at;
+    if constexpr (ROWS == kGroups) {
+        if (!group_tile(p0, rt, &tab, at)) return;
+    } else {
+        const int64_t tiles = (p.R + kQT - 1) / kQT, k = rt / tiles, r = rt - k * tiles;
+        if (k >= p0.G) return;
+        p.x = static_cast<const char*>(p.x) + k * p0.x_b * (F32 ? 4 : 2);
+        if (p.q) p.q += k * p0.q_b, p.scale += k * p0.s_b;
+        if (TRANS) p.qt += k * p0.qt_b, p.scale_t += k * p0.st_b;
+        at = RowTile{r * kQT, p.R, r * kQT, p.R, r};
+    }
+    Block<F32> b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load_row(b, i, p, at.row0 + ry * 8 + i, at.end, ct * kQT + cx * 8);
+    quantize_tile<F32, kBlocks, TRANS>(p, b, ct, at, sh);
+}
+
+// The epilogue's backward.
+template <bool TRANS, int ROWS, int ACT>
+__global__ void __launch_bounds__(kQThreads, 3) act_grad_kernel(const __grid_constant__ QuantExtParams p) {
+    __shared__ TileShared<true, false, TRANS> sh;
+    __shared__ typename std::conditional<ROWS == kGroups, GroupTable, int>::type tab;
+    __shared__ float4 sums[16][kQT / 4];
+    const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
+    const int64_t ct = blockIdx.x, rt = blockIdx.y + (int64_t)blockIdx.z * 65535;
+    RowTile at;
+    if constexpr (ROWS == kGroups) {
+        if (!group_tile(p, rt, &tab, at)) return;
+    } else {
+        if (rt * kQT >= p.R) return;
+        at = RowTile{rt * kQT, p.R, rt * kQT, p.R, rt};
+    }
+    Block<true> b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load_dz_row<ACT>(b, i, p, at.row0 + ry * 8 + i, at.end, ct * kQT + cx * 8);
+    if (p.part) {
+        float s[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            s[j] = b.at(0, j);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) s[j] = __fadd_rn(s[j], b.at(i, j));
+        }
+        sums[ry][2 * cx] = make_float4(s[0], s[1], s[2], s[3]);
+        sums[ry][2 * cx + 1] = make_float4(s[4], s[5], s[6], s[7]);
+        __syncthreads();
+        if (threadIdx.x < kQT && ct * kQT + threadIdx.x < p.C) {
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                v = __fadd_rn(v, reinterpret_cast<const float*>(sums[k])[threadIdx.x]);
+            p.part[rt * p.C + ct * kQT + threadIdx.x] = v;
+        }
+    }
+    if (p.q || TRANS) quantize_tile<true, false, TRANS>(p, b, ct, at, sh);
+}
+
+// dbias from the row tiles' sums: a warp of 32 columns, eight runs of a group's
+// tiles at a time, joined in order.
+template <int ROWS>
+__global__ void __launch_bounds__(kQThreads) bias_grad_kernel(const __grid_constant__ QuantExtParams p, void* dbias,
+                                                              const int f32) {
+    __shared__ typename std::conditional<ROWS == kGroups, GroupTable, int>::type tab;
+    __shared__ float join[8][32];
+    const int run = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    if constexpr (ROWS == kGroups) {
+        groups_build<kQThreads>(&tab, p.ends, p.G, (int)p.R, kQT, 1, false);
+        __syncthreads();
+    }
+    for (int e = blockIdx.y; e < (ROWS == kGroups ? p.G : 1); e += gridDim.y) {
+        int64_t t0 = 0, t1 = (p.R + kQT - 1) / kQT;
+        if constexpr (ROWS == kGroups) t0 = tab.first[e], t1 = tab.first[e + 1];
+        const int64_t lo = t0 + (t1 - t0) * run / 8, hi = t0 + (t1 - t0) * (run + 1) / 8;
+        float v = 0.f;
+        if (c < p.C) {
+#pragma unroll 4
+            for (int64_t t = lo; t < hi; ++t) v = __fadd_rn(v, p.part[t * p.C + c]);
+        }
+        join[run][lane] = v;
+        __syncthreads();
+        if (run == 0 && c < p.C) {
+#pragma unroll
+            for (int k = 1; k < 8; ++k) v = __fadd_rn(v, join[k][lane]);
+            if (f32)
+                static_cast<float*>(dbias)[e * p.C + c] = v;
+            else
+                static_cast<uint16_t*>(dbias)[e * p.C + c] = (uint16_t)pack_bf16x2_rn(v, 0.f);
+        }
+        __syncthreads();
+    }
 }
 
 rlk_status quant_cuda(const char* what) {
@@ -326,7 +520,122 @@ rlk_status launch_typed(const QuantParams& p, bool blocks, cudaStream_t st) {
     return trans ? launch_as<F32, false, true>(p, st) : launch_as<F32, false, false>(p, st);
 }
 
+dim3 tile_grid(int64_t C, int64_t row_tiles) {
+    return dim3((unsigned)((C + kQT - 1) / kQT), (unsigned)(row_tiles < 65535 ? row_tiles : 65535),
+                (unsigned)((row_tiles + 65534) / 65535));
+}
+
+template <int ROWS>
+rlk_status launch_ext(const QuantExtParams& p, bool f32, int64_t row_tiles, cudaStream_t st) {
+    const dim3 grid = tile_grid(p.C, row_tiles);
+    if (f32)
+        p.qt ? quantize_ext_kernel<true, true, ROWS><<<grid, kQThreads, 0, st>>>(p)
+             : quantize_ext_kernel<true, false, ROWS><<<grid, kQThreads, 0, st>>>(p);
+    else
+        p.qt ? quantize_ext_kernel<false, true, ROWS><<<grid, kQThreads, 0, st>>>(p)
+             : quantize_ext_kernel<false, false, ROWS><<<grid, kQThreads, 0, st>>>(p);
+    return quant_cuda("fp8 quantize launch");
+}
+
+template <bool TRANS, int ROWS>
+void launch_act(const QuantExtParams& p, dim3 grid, cudaStream_t st) {
+    switch (p.act) {
+        case RLK_ACT_RELU: act_grad_kernel<TRANS, ROWS, RLK_ACT_RELU><<<grid, kQThreads, 0, st>>>(p); break;
+        case RLK_ACT_SILU: act_grad_kernel<TRANS, ROWS, RLK_ACT_SILU><<<grid, kQThreads, 0, st>>>(p); break;
+        case RLK_ACT_GELU: act_grad_kernel<TRANS, ROWS, RLK_ACT_GELU><<<grid, kQThreads, 0, st>>>(p); break;
+        case RLK_ACT_GELU_TANH: act_grad_kernel<TRANS, ROWS, RLK_ACT_GELU_TANH><<<grid, kQThreads, 0, st>>>(p); break;
+        default: act_grad_kernel<TRANS, ROWS, RLK_ACT_NONE><<<grid, kQThreads, 0, st>>>(p);
+    }
+}
+
+template <int ROWS>
+rlk_status launch_act_rows(const QuantExtParams& p, int64_t row_tiles, void* dbias, bool f32, cudaStream_t st) {
+    const dim3 grid = tile_grid(p.C, row_tiles);
+    p.qt ? launch_act<true, ROWS>(p, grid, st) : launch_act<false, ROWS>(p, grid, st);
+    rlk_status s = quant_cuda("fp8 activation gradient launch");
+    if (s != RLK_OK || !dbias) return s;
+    const dim3 sums((unsigned)((p.C + 31) / 32), (unsigned)(p.G < 1 ? 1 : p.G < 32 ? p.G : 32));
+    bias_grad_kernel<ROWS><<<sums, kQThreads, 0, st>>>(p, dbias, f32);
+    return quant_cuda("bias gradient launch");
+}
+
 }  // namespace
+
+// Row tiles that any counts of the groups' rows can ask for.
+int64_t group_row_tiles(int64_t groups, int64_t rows) { return rows / kQT + (groups < rows ? groups : rows); }
+
+rlk_status launch_fp8_quantize_grouped(int64_t G, int64_t rows, int64_t cols, const int32_t* ends, const void* x,
+                                       int32_t x_f32, int64_t ldx, uint8_t* q, int64_t ldq, float* scale, uint8_t* qt,
+                                       int64_t ldqt, float* scale_t, cudaStream_t stream) {
+    QuantExtParams p{};
+    p.x = x;
+    p.R = rows;
+    p.C = cols;
+    p.ldx = ldx;
+    p.q = q;
+    p.qt = qt;
+    p.ldq = ldq;
+    p.ldqt = ldqt;
+    p.scale = scale;
+    p.scale_t = scale_t;
+    p.vec = (reinterpret_cast<uintptr_t>(x) % 16 == 0) && (ldx * (x_f32 ? 4 : 2)) % 16 == 0;
+    p.ends = ends;
+    p.G = (int32_t)G;
+    return launch_ext<kGroups>(p, x_f32, group_row_tiles(G, rows), stream);
+}
+
+rlk_status launch_fp8_quantize_batch(int64_t count, int64_t rows, int64_t cols, const void* x, int32_t x_f32,
+                                     int64_t ldx, int64_t x_b, uint8_t* q, int64_t ldq, int64_t q_b, float* scale,
+                                     uint8_t* qt, int64_t ldqt, int64_t qt_b, float* scale_t, cudaStream_t stream) {
+    QuantExtParams p{};
+    p.x = x;
+    p.R = rows;
+    p.C = cols;
+    p.ldx = ldx;
+    p.q = q;
+    p.qt = qt;
+    p.ldq = ldq;
+    p.ldqt = ldqt;
+    p.scale = scale;
+    p.scale_t = scale_t;
+    p.x_b = x_b;
+    p.q_b = q_b;
+    p.qt_b = qt_b;
+    p.s_b = p.st_b = ((rows + kQT - 1) / kQT) * ((cols + kQT - 1) / kQT);
+    p.vec = (reinterpret_cast<uintptr_t>(x) % 16 == 0) && (ldx * (x_f32 ? 4 : 2)) % 16 == 0 &&
+            (x_b * (x_f32 ? 4 : 2)) % 16 == 0;
+    p.G = (int32_t)count;
+    return launch_ext<kBatch>(p, x_f32, count * ((rows + kQT - 1) / kQT), stream);
+}
+
+rlk_status launch_fp8_act_grad(int64_t G, int64_t rows, int64_t wide, const int32_t* ends, const void* dy,
+                               int32_t dy_f32, int64_t lddy, const void* z, int64_t ldz, int32_t act, int32_t gated,
+                               uint8_t* q, int64_t ldq, float* scale, uint8_t* qt, int64_t ldqt, float* scale_t,
+                               void* dbias, int32_t dbias_f32, float* part, cudaStream_t stream) {
+    QuantExtParams p{};
+    p.R = rows;
+    p.C = wide;
+    p.q = q;
+    p.qt = qt;
+    p.ldq = ldq;
+    p.ldqt = ldqt;
+    p.scale = scale;
+    p.scale_t = scale_t;
+    p.ends = ends;
+    p.G = (int32_t)G;
+    p.dy = dy;
+    p.dy_f32 = dy_f32;
+    p.lddy = lddy;
+    p.dy_vec = (reinterpret_cast<uintptr_t>(dy) % 16 == 0) && (lddy * (dy_f32 ? 4 : 2)) % 16 == 0;
+    p.z = static_cast<const uint16_t*>(z);
+    p.ldz = ldz;
+    p.z_vec = (reinterpret_cast<uintptr_t>(z) % 16 == 0) && (ldz * 2) % 16 == 0;
+    p.act = act;
+    p.gated = gated;
+    p.part = dbias ? part : nullptr;
+    return G > 0 ? launch_act_rows<kGroups>(p, group_row_tiles(G, rows), dbias, dbias_f32, stream)
+                 : launch_act_rows<kOne>(p, (rows + kQT - 1) / kQT, dbias, dbias_f32, stream);
+}
 
 rlk_status launch_fp8_quantize(int64_t rows, int64_t cols, const void* x, int32_t x_f32, int64_t ldx,
                                int32_t block_rows, uint8_t* q, int64_t ldq, float* scale, uint8_t* qt, int64_t ldqt,

@@ -962,6 +962,331 @@ RLK_EXPORT rlk_status rlk_fp8_matmul(int64_t M, int64_t N, int64_t K, const void
 
 namespace rlk {
 namespace {
+constexpr int64_t kMaxRows8 = (int64_t)1 << 30;  // rows of groups: with their padding below 2^31
+
+rlk_status check_type(const char* name, int32_t type) {
+    if (type != RLK_BF16 && type != RLK_F32)
+        return fail(RLK_ERR_INVALID_ARG, std::string(name) + " must be RLK_BF16 or RLK_F32");
+    return RLK_OK;
+}
+
+rlk_status check_act(int32_t activation, int32_t gated, int64_t N) {
+    if (activation < RLK_ACT_NONE || activation > RLK_ACT_GELU_TANH)
+        return fail(RLK_ERR_INVALID_ARG, "activation must be one of rlk_activation");
+    if (gated != 0 && gated != 1) return fail(RLK_ERR_INVALID_ARG, "gated must be 0 or 1");
+    if (gated && N % 64 != 0)
+        return fail(RLK_ERR_UNSUPPORTED, "a gated layer's columns must be a multiple of 64");
+    return RLK_OK;
+}
+
+rlk_status check_stride(const char* name, int64_t stride, int64_t width) {
+    if (stride < width) return fail(RLK_ERR_INVALID_ARG, std::string(name) + "_stride is below its row's length");
+    if (stride > ((int64_t)1 << 38)) return fail(RLK_ERR_UNSUPPORTED, std::string(name) + "_stride above 2^38");
+    return RLK_OK;
+}
+
+// A stride between groups' matrices of E4M3, or between their results (multiple 1).
+rlk_status check_group_stride(const char* name, int64_t groups, int64_t stride, int64_t least, int64_t multiple) {
+    if (groups <= 1) return RLK_OK;
+    if (stride < least) return fail(RLK_ERR_INVALID_ARG, std::string(name) + " is below a matrix's length");
+    if (stride % multiple != 0) return fail(RLK_ERR_MISALIGNED, std::string(name) + " must be a multiple of 16");
+    if (stride > ((int64_t)1 << 38)) return fail(RLK_ERR_UNSUPPORTED, std::string(name) + " above 2^38");
+    return RLK_OK;
+}
+
+rlk_status check_groups(int64_t groups, int64_t rows) {
+    if (groups < 1) return fail(RLK_ERR_INVALID_ARG, "groups must be >= 1");
+    if (groups > 1024) return fail(RLK_ERR_UNSUPPORTED, "more than 1024 groups");
+    if (rows > kMaxRows8) return fail(RLK_ERR_UNSUPPORTED, "above 2^30 rows of groups");
+    return RLK_OK;
+}
+
+int64_t type_size(int32_t type) { return type == RLK_F32 ? 4 : 2; }
+
+// Both products with an epilogue (groups 0: one B).
+rlk_status matmul_act(int64_t groups, int64_t M, int64_t N, int64_t K, const int32_t* ends, const void* a,
+                      int64_t a_stride, const float* a_scale, const void* b, int64_t b_stride, int64_t b_group_stride,
+                      const float* b_scale, const rlk_fp8_epilogue* e, void* c, int32_t c_type, int64_t c_stride,
+                      int32_t zero_rest, void* workspace, cudaStream_t stream) {
+    rlk_status s;
+    if (M < 0 || N < 0) return fail(RLK_ERR_INVALID_ARG, "M and N must be >= 0");
+    if (K < 1) return fail(RLK_ERR_INVALID_ARG, "K must be >= 1");
+    if (groups > 0 && (s = check_groups(groups, M)) != RLK_OK) return s;
+    if (zero_rest != 0 && zero_rest != 1) return fail(RLK_ERR_INVALID_ARG, "zero_rest must be 0 or 1");
+    if ((s = check_type("c_type", c_type)) != RLK_OK) return s;
+    const bool gated = e && e->gated;
+    if (e) {
+        if ((s = check_act(e->activation, e->gated, N)) != RLK_OK) return s;
+        if (e->bias && (s = check_type("bias_type", e->bias_type)) != RLK_OK) return s;
+        if (e->residual && (s = check_type("residual_type", e->residual_type)) != RLK_OK) return s;
+        if (e->residual && groups > 0)
+            return fail(RLK_ERR_UNSUPPORTED, "a residual of groups' rows is not supported");
+    }
+    if (M > kMaxDim8 || N > kMaxDim8 / 2 || K > kMaxDim8)
+        return fail(RLK_ERR_UNSUPPORTED, "M or K above 2^31 - 512, or N above 2^30 - 256");
+    const int64_t wide = gated ? 2 * N : N, count = groups > 0 ? groups : 1, kg = (K + 127) / 128;
+    if ((M / 16 + count + 1) * ((wide + 127) / 128) > ((int64_t)1 << 30))
+        return fail(RLK_ERR_UNSUPPORTED, "above 2^30 tiles of 16 x 128");
+    if (M == 0 || N == 0) return RLK_OK;
+    if (!a || !b || !a_scale || !b_scale || !c || (groups > 0 && !ends))
+        return fail(RLK_ERR_INVALID_ARG, groups > 0 ? "ends, a, a_scale, b, b_scale and c are required"
+                                                    : "a, a_scale, b, b_scale and c are required");
+    if (!workspace) return fail(RLK_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned16(workspace)) return fail(RLK_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    if ((s = check_codes("a", a, a_stride, K)) != RLK_OK) return s;
+    if ((s = check_codes("b", b, b_stride, K)) != RLK_OK) return s;
+    const int64_t b_bytes = extent(wide, b_stride, K, 1);
+    if ((s = check_group_stride("b_group_stride", groups, b_group_stride, b_bytes, 16)) != RLK_OK) return s;
+    if (gated && N * b_stride >= ((int64_t)1 << 40))
+        return fail(RLK_ERR_UNSUPPORTED, "N * b_stride of a gated b above 2^40");
+    if ((s = check_natural("ends", ends, 4)) != RLK_OK) return s;
+    if ((s = check_natural("a_scale", a_scale, 4)) != RLK_OK) return s;
+    if ((s = check_natural("b_scale", b_scale, 4)) != RLK_OK) return s;
+    if ((s = check_natural("c", c, type_size(c_type))) != RLK_OK) return s;
+    if ((s = check_stride("c", c_stride, N)) != RLK_OK) return s;
+    Span bias{nullptr, 0, "bias"}, res{nullptr, 0, "residual"}, z{nullptr, 0, "z"};
+    if (e && e->bias) {
+        if ((s = check_natural("bias", e->bias, type_size(e->bias_type))) != RLK_OK) return s;
+        bias = Span{e->bias, count * wide * type_size(e->bias_type), "bias"};
+    }
+    if (e && e->residual) {
+        if ((s = check_natural("residual", e->residual, type_size(e->residual_type))) != RLK_OK) return s;
+        if ((s = check_stride("residual", e->residual_stride, N)) != RLK_OK) return s;
+        res = Span{e->residual, extent(M, e->residual_stride, N, type_size(e->residual_type)), "residual"};
+    }
+    if (e && e->z) {
+        if ((s = check_natural("z", e->z, 2)) != RLK_OK) return s;
+        if ((s = check_stride("z", e->z_stride, wide)) != RLK_OK) return s;
+        z = Span{e->z, extent(M, e->z_stride, wide, 2), "z"};
+    }
+    const Span out{c, extent(M, c_stride, N, type_size(c_type)), "c"}, ws{workspace, RLK_FP8_WORKSPACE, "workspace"};
+    const Span sa{a, extent(M, a_stride, K, 1), "a"}, sb{b, (count - 1) * b_group_stride + b_bytes, "b"};
+    const Span sas{a_scale, 4 * kg * M, "a_scale"}, sbs{b_scale, 4 * count * kg * ((wide + 127) / 128), "b_scale"};
+    const Span se{ends, 4 * groups, "ends"};
+    if ((s = check_outputs({out, z, ws}, {sa, sb, sas, sbs, se, bias})) != RLK_OK) return s;
+    if ((s = check_outputs({z, ws}, {res})) != RLK_OK) return s;
+    // in place: each element of the residual is read by the thread block that writes its place, before it does
+    const bool in_place = res.ptr == c && e && e->residual_type == c_type && e->residual_stride == c_stride;
+    if (!in_place && (s = check_disjoint(out, {res})) != RLK_OK) return s;
+    if ((s = select_device(a)) != RLK_OK) return s;
+    if ((s = check_device_ptrs({{a_scale, "a_scale"}, {b, "b"}, {b_scale, "b_scale"}, {c, "c"}, {ends, "ends"},
+                                {bias.ptr, "bias"}, {res.ptr, "residual"}, {z.ptr, "z"},
+                                {workspace, "workspace"}})) != RLK_OK)
+        return s;
+    uint32_t* status = static_cast<uint32_t*>(workspace);
+    if (groups > 0)
+        return launch_fp8_grouped_matmul(groups, M, N, K, ends, a, a_stride, a_scale, b, b_stride, b_group_stride,
+                                         b_scale, e, c, c_stride, c_type == RLK_F32, zero_rest, status, stream);
+    return launch_fp8_matmul_act(M, N, K, a, a_stride, a_scale, b, b_stride, b_scale, e, c, c_stride,
+                                 c_type == RLK_F32, status, stream);
+}
+
+// The outputs of a quantisation along rows and along groups of rows: pointers, strides and their spans.
+rlk_status check_quantized(int64_t rows, int64_t cols, int64_t deep, int64_t tiles, void* q, int64_t q_stride,
+                           float* scale, void* qt, int64_t qt_stride, float* scale_t, Span (&out)[4]) {
+    rlk_status s;
+    if ((q != nullptr) != (scale != nullptr) || (qt != nullptr) != (scale_t != nullptr))
+        return fail(RLK_ERR_INVALID_ARG, "q comes with scale and qt with scale_t");
+    if (q && (s = check_codes("q", q, q_stride, cols)) != RLK_OK) return s;
+    if (qt && (s = check_codes("qt", qt, qt_stride, deep)) != RLK_OK) return s;
+    if ((s = check_natural("scale", scale, 4)) != RLK_OK) return s;
+    if ((s = check_natural("scale_t", scale_t, 4)) != RLK_OK) return s;
+    out[0] = Span{q, extent(rows, q_stride, cols, 1), "q"};
+    out[1] = Span{scale, 4 * ((cols + 127) / 128) * rows, "scale"};
+    out[2] = Span{qt, extent(cols, qt_stride, deep, 1), "qt"};
+    out[3] = Span{scale_t, 4 * tiles * cols, "scale_t"};
+    return RLK_OK;
+}
+}  // namespace
+}  // namespace rlk
+
+RLK_EXPORT rlk_status rlk_fp8_matmul_act(int64_t M, int64_t N, int64_t K, const void* a, int64_t a_stride,
+                                         const float* a_scale, const void* b, int64_t b_stride, const float* b_scale,
+                                         const rlk_fp8_epilogue* epilogue, void* c, int32_t c_type, int64_t c_stride,
+                                         void* workspace, rlk_stream_t stream) {
+    return matmul_act(0, M, N, K, nullptr, a, a_stride, a_scale, b, b_stride, 0, b_scale, epilogue, c, c_type,
+                      c_stride, 0, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+RLK_EXPORT rlk_status rlk_fp8_grouped_matmul(int64_t groups, int64_t M, int64_t N, int64_t K, const int32_t* ends,
+                                             const void* a, int64_t a_stride, const float* a_scale, const void* b,
+                                             int64_t b_stride, int64_t b_group_stride, const float* b_scale,
+                                             const rlk_fp8_epilogue* epilogue, void* c, int32_t c_type,
+                                             int64_t c_stride, int32_t zero_rest, void* workspace,
+                                             rlk_stream_t stream) {
+    if (groups < 1) return fail(RLK_ERR_INVALID_ARG, "groups must be >= 1");
+    return matmul_act(groups, M, N, K, ends, a, a_stride, a_scale, b, b_stride, b_group_stride, b_scale, epilogue, c,
+                      c_type, c_stride, zero_rest, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+RLK_EXPORT rlk_status rlk_fp8_quantize_grouped(int64_t groups, int64_t rows, int64_t cols, const int32_t* ends,
+                                               const void* x, int32_t x_type, int64_t x_stride, void* q,
+                                               int64_t q_stride, float* scale, void* qt, int64_t qt_stride,
+                                               float* scale_t, rlk_stream_t stream) {
+    rlk_status s;
+    if (rows < 0 || cols < 0) return fail(RLK_ERR_INVALID_ARG, "rows and cols must be >= 0");
+    if ((s = check_groups(groups, rows)) != RLK_OK) return s;
+    if ((s = check_type("x_type", x_type)) != RLK_OK) return s;
+    if (cols > kMaxDim8) return fail(RLK_ERR_UNSUPPORTED, "cols above 2^31 - 512");
+    if (rows == 0 || cols == 0) return RLK_OK;
+    if (!x || !ends) return fail(RLK_ERR_INVALID_ARG, "x and ends are required");
+    if (!q && !qt) return fail(RLK_ERR_INVALID_ARG, "q or qt is required");
+    if ((s = check_stride("x", x_stride, cols)) != RLK_OK) return s;
+    if ((s = check_natural("x", x, type_size(x_type))) != RLK_OK) return s;
+    if ((s = check_natural("ends", ends, 4)) != RLK_OK) return s;
+    const int64_t tiles = group_row_tiles(groups, rows);
+    Span o[4];
+    if ((s = check_quantized(rows, cols, 128 * tiles, tiles, q, q_stride, scale, qt, qt_stride, scale_t, o)) != RLK_OK)
+        return s;
+    if ((s = check_outputs({o[0], o[1], o[2], o[3]}, {{x, extent(rows, x_stride, cols, type_size(x_type)), "x"},
+                                                      {ends, 4 * groups, "ends"}})) != RLK_OK)
+        return s;
+    if ((s = select_device(x)) != RLK_OK) return s;
+    if ((s = check_device_ptrs({{ends, "ends"}, {q, "q"}, {scale, "scale"}, {qt, "qt"}, {scale_t, "scale_t"}})) !=
+        RLK_OK)
+        return s;
+    return launch_fp8_quantize_grouped(groups, rows, cols, ends, x, x_type == RLK_F32, x_stride,
+                                       static_cast<uint8_t*>(q), q_stride, scale, static_cast<uint8_t*>(qt),
+                                       qt_stride, scale_t, reinterpret_cast<cudaStream_t>(stream));
+}
+
+RLK_EXPORT rlk_status rlk_fp8_quantize_batch(int64_t count, int64_t rows, int64_t cols, const void* x, int32_t x_type,
+                                             int64_t x_stride, int64_t x_batch_stride, void* q, int64_t q_stride,
+                                             int64_t q_batch_stride, float* scale, void* qt, int64_t qt_stride,
+                                             int64_t qt_batch_stride, float* scale_t, rlk_stream_t stream) {
+    rlk_status s;
+    if (count < 0 || rows < 0 || cols < 0) return fail(RLK_ERR_INVALID_ARG, "count, rows and cols must be >= 0");
+    if ((s = check_type("x_type", x_type)) != RLK_OK) return s;
+    const int64_t rg = (rows + 127) / 128, cg = (cols + 127) / 128;
+    if (rows > kMaxDim8 || cols > kMaxDim8 || count > ((int64_t)1 << 20) || (rg > 0 && count > ((int64_t)1 << 30) / rg))
+        return fail(RLK_ERR_UNSUPPORTED, "rows or cols above 2^31 - 512, or above 2^20 matrices or 2^30 blocks of rows");
+    if (count == 0 || rows == 0 || cols == 0) return RLK_OK;
+    if (!x) return fail(RLK_ERR_INVALID_ARG, "x is NULL");
+    if (!q && !qt) return fail(RLK_ERR_INVALID_ARG, "q or qt is required");
+    if ((s = check_stride("x", x_stride, cols)) != RLK_OK) return s;
+    if ((s = check_natural("x", x, type_size(x_type))) != RLK_OK) return s;
+    const int64_t one = extent(rows, x_stride, cols, 1), size = type_size(x_type);
+    if ((s = check_group_stride("x_batch_stride", count, x_batch_stride, one, 1)) != RLK_OK) return s;
+    Span o[4];
+    if ((s = check_quantized(rows, cols, rows, rg, q, q_stride, scale, qt, qt_stride, scale_t, o)) != RLK_OK) return s;
+    if (q && (s = check_group_stride("q_batch_stride", count, q_batch_stride, o[0].bytes, 16)) != RLK_OK) return s;
+    if (qt && (s = check_group_stride("qt_batch_stride", count, qt_batch_stride, o[2].bytes, 16)) != RLK_OK) return s;
+    if (count > 1) o[0].bytes += (count - 1) * q_batch_stride, o[2].bytes += (count - 1) * qt_batch_stride;
+    o[1].bytes = o[3].bytes = 4 * count * rg * cg;
+    const int64_t x_bytes = (one + (count > 1 ? (count - 1) * x_batch_stride : 0)) * size;
+    if ((s = check_outputs({o[0], o[1], o[2], o[3]}, {{x, x_bytes, "x"}})) != RLK_OK) return s;
+    if ((s = select_device(x)) != RLK_OK) return s;
+    if ((s = check_device_ptrs({{q, "q"}, {scale, "scale"}, {qt, "qt"}, {scale_t, "scale_t"}})) != RLK_OK) return s;
+    return launch_fp8_quantize_batch(count, rows, cols, x, x_type == RLK_F32, x_stride, x_batch_stride,
+                                     static_cast<uint8_t*>(q), q_stride, q_batch_stride, scale,
+                                     static_cast<uint8_t*>(qt), qt_stride, qt_batch_stride, scale_t,
+                                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+RLK_EXPORT rlk_status rlk_fp8_grouped_dweight(int64_t groups, int64_t rows, int64_t M, int64_t N, const int32_t* ends,
+                                              const void* a, int64_t a_stride, const float* a_scale, const void* b,
+                                              int64_t b_stride, const float* b_scale, void* c, int32_t c_type,
+                                              int64_t c_stride, int64_t c_group_stride, int32_t accumulate,
+                                              void* workspace, rlk_stream_t stream) {
+    rlk_status s;
+    if (rows < 1 || M < 0 || N < 0) return fail(RLK_ERR_INVALID_ARG, "rows must be >= 1, M and N >= 0");
+    if ((s = check_groups(groups, rows)) != RLK_OK) return s;
+    if ((s = check_type("c_type", c_type)) != RLK_OK) return s;
+    if (accumulate != 0 && accumulate != 1) return fail(RLK_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+    if (accumulate && c_type != RLK_F32) return fail(RLK_ERR_INVALID_ARG, "accumulate needs an RLK_F32 c");
+    if (M > kMaxDim8 || N > kMaxDim8 || groups * ((M + 255) / 256) * ((N + 255) / 256) > ((int64_t)1 << 30))
+        return fail(RLK_ERR_UNSUPPORTED, "M or N above 2^31 - 512, or above 2^30 tiles of 256 x 256");
+    if (M == 0 || N == 0) return RLK_OK;
+    if (!ends || !a || !b || !a_scale || !b_scale || !c)
+        return fail(RLK_ERR_INVALID_ARG, "ends, a, a_scale, b, b_scale and c are required");
+    if (!workspace) return fail(RLK_ERR_INVALID_ARG, "workspace is NULL");
+    if (!aligned16(workspace)) return fail(RLK_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    const int64_t tiles = group_row_tiles(groups, rows), deep = 128 * tiles, size = type_size(c_type);
+    if ((s = check_codes("a", a, a_stride, deep)) != RLK_OK) return s;
+    if ((s = check_codes("b", b, b_stride, deep)) != RLK_OK) return s;
+    if ((s = check_natural("ends", ends, 4)) != RLK_OK) return s;
+    if ((s = check_natural("a_scale", a_scale, 4)) != RLK_OK) return s;
+    if ((s = check_natural("b_scale", b_scale, 4)) != RLK_OK) return s;
+    if ((s = check_natural("c", c, size)) != RLK_OK) return s;
+    if ((s = check_stride("c", c_stride, N)) != RLK_OK) return s;
+    const int64_t one = extent(M, c_stride, N, 1);
+    if ((s = check_group_stride("c_group_stride", groups, c_group_stride, one, 1)) != RLK_OK) return s;
+    const Span out{c, (one + (groups > 1 ? (groups - 1) * c_group_stride : 0)) * size, "c"};
+    if ((s = check_outputs({out, {workspace, RLK_FP8_WORKSPACE, "workspace"}},
+                           {{a, extent(M, a_stride, deep, 1), "a"},
+                            {b, extent(N, b_stride, deep, 1), "b"},
+                            {a_scale, 4 * tiles * M, "a_scale"},
+                            {b_scale, 4 * tiles * N, "b_scale"},
+                            {ends, 4 * groups, "ends"}})) != RLK_OK)
+        return s;
+    if ((s = select_device(a)) != RLK_OK) return s;
+    if ((s = check_device_ptrs({{ends, "ends"}, {a_scale, "a_scale"}, {b, "b"}, {b_scale, "b_scale"}, {c, "c"},
+                                {workspace, "workspace"}})) != RLK_OK)
+        return s;
+    return launch_fp8_grouped_dweight(groups, rows, M, N, ends, a, a_stride, a_scale, b, b_stride, b_scale, c,
+                                      c_stride, c_group_stride, c_type == RLK_F32, accumulate,
+                                      static_cast<uint32_t*>(workspace), reinterpret_cast<cudaStream_t>(stream));
+}
+
+RLK_EXPORT size_t rlk_fp8_act_grad_workspace_size(int64_t groups, int64_t rows, int64_t cols, int32_t gated) {
+    if (groups < 0 || rows < 0 || cols < 0 || rows > kMaxDim8 || cols > kMaxDim8 / 2) return 0;
+    const int64_t tiles = groups > 0 ? group_row_tiles(groups, rows) : (rows + 127) / 128;
+    return (size_t)(4 * tiles * cols * (gated ? 2 : 1));
+}
+
+RLK_EXPORT rlk_status rlk_fp8_act_grad(int64_t groups, int64_t rows, int64_t cols, const int32_t* ends, const void* dy,
+                                       int32_t dy_type, int64_t dy_stride, const void* z, int64_t z_stride,
+                                       int32_t activation, int32_t gated, void* q, int64_t q_stride, float* scale,
+                                       void* qt, int64_t qt_stride, float* scale_t, void* dbias, int32_t dbias_type,
+                                       void* workspace, rlk_stream_t stream) {
+    rlk_status s;
+    if (rows < 1 || cols < 0) return fail(RLK_ERR_INVALID_ARG, "rows must be >= 1 and cols >= 0");
+    if (groups < 0) return fail(RLK_ERR_INVALID_ARG, "groups must be >= 0");
+    if (groups > 0 && (s = check_groups(groups, rows)) != RLK_OK) return s;
+    if ((s = check_type("dy_type", dy_type)) != RLK_OK) return s;
+    if ((s = check_act(activation, gated, cols)) != RLK_OK) return s;
+    if (dbias && (s = check_type("dbias_type", dbias_type)) != RLK_OK) return s;
+    if (rows > kMaxDim8 || cols > kMaxDim8 / 2)
+        return fail(RLK_ERR_UNSUPPORTED, "rows above 2^31 - 512 or cols above 2^30 - 256");
+    if (cols == 0) return RLK_OK;
+    const int64_t wide = gated ? 2 * cols : cols;
+    const bool need_z = activation != RLK_ACT_NONE || gated;
+    if (!dy || (need_z && !z) || (groups > 0 && !ends))
+        return fail(RLK_ERR_INVALID_ARG, "dy, z (with an activation or a gate) and ends (with groups) are required");
+    if (!q && !qt && !dbias) return fail(RLK_ERR_INVALID_ARG, "q, qt or dbias is required");
+    if (dbias && !workspace) return fail(RLK_ERR_INVALID_ARG, "dbias needs a workspace");
+    if (dbias && !aligned16(workspace)) return fail(RLK_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    if ((s = check_stride("dy", dy_stride, cols)) != RLK_OK) return s;
+    if ((s = check_natural("dy", dy, type_size(dy_type))) != RLK_OK) return s;
+    if (need_z && (s = check_stride("z", z_stride, wide)) != RLK_OK) return s;
+    if (need_z && (s = check_natural("z", z, 2)) != RLK_OK) return s;
+    if ((s = check_natural("ends", ends, 4)) != RLK_OK) return s;
+    if (dbias && (s = check_natural("dbias", dbias, type_size(dbias_type))) != RLK_OK) return s;
+    const int64_t tiles = groups > 0 ? group_row_tiles(groups, rows) : (rows + 127) / 128;
+    Span o[4];
+    if ((s = check_quantized(rows, wide, groups > 0 ? 128 * tiles : rows, tiles, q, q_stride, scale, qt, qt_stride,
+                             scale_t, o)) != RLK_OK)
+        return s;
+    const Span db{dbias, (groups > 0 ? groups : 1) * wide * type_size(dbias_type), "dbias"};
+    const Span ws{dbias ? workspace : nullptr, 4 * tiles * wide, "workspace"};
+    if ((s = check_outputs({o[0], o[1], o[2], o[3], db, ws},
+                           {{dy, extent(rows, dy_stride, cols, type_size(dy_type)), "dy"},
+                            {need_z ? z : nullptr, extent(rows, z_stride, wide, 2), "z"},
+                            {groups > 0 ? ends : nullptr, 4 * groups, "ends"}})) != RLK_OK)
+        return s;
+    if ((s = select_device(dy)) != RLK_OK) return s;
+    if ((s = check_device_ptrs({{need_z ? z : nullptr, "z"}, {groups > 0 ? ends : nullptr, "ends"}, {q, "q"},
+                                {scale, "scale"}, {qt, "qt"}, {scale_t, "scale_t"}, {dbias, "dbias"},
+                                {ws.ptr, "workspace"}})) != RLK_OK)
+        return s;
+    return launch_fp8_act_grad(groups, rows, wide, ends, dy, dy_type == RLK_F32, dy_stride, z, z_stride, activation,
+                               gated, static_cast<uint8_t*>(q), q_stride, scale, static_cast<uint8_t*>(qt), qt_stride,
+                               scale_t, dbias, dbias_type == RLK_F32, static_cast<float*>(workspace),
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace rlk {
+namespace {
 rlk_status check_ce(const rlk_linear_ce_contract* c) {
     if (!c) return fail(RLK_ERR_INVALID_ARG, "contract is NULL");
     if (c->T < 0) return fail(RLK_ERR_INVALID_ARG, "T must be >= 0");

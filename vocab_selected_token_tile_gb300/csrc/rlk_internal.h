@@ -162,6 +162,34 @@ rlk_status launch_fp8_matmul(int64_t M, int64_t N, int64_t K, const void* a, int
                              const void* b, int64_t ldb, const float* sb, int32_t b_block_rows, void* c, int64_t ldc,
                              int32_t c_f32, int32_t accumulate, uint32_t* status, cudaStream_t stream);
 
+// The product with a layer's epilogue (fp8_epilogue.cu), and products of rows
+// that belong to groups (fp8_grouped.cu).
+rlk_status launch_fp8_matmul_act(int64_t M, int64_t N, int64_t K, const void* a, int64_t lda, const float* sa,
+                                 const void* b, int64_t ldb, const float* sb, const rlk_fp8_epilogue* e, void* c,
+                                 int64_t ldc, int32_t c_f32, uint32_t* status, cudaStream_t stream);
+rlk_status launch_fp8_grouped_matmul(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t* ends, const void* a,
+                                     int64_t lda, const float* sa, const void* b, int64_t ldb, int64_t group,
+                                     const float* sb, const rlk_fp8_epilogue* e, void* c, int64_t ldc, int32_t c_f32,
+                                     int32_t rest, uint32_t* status, cudaStream_t stream);
+rlk_status launch_fp8_grouped_dweight(int64_t G, int64_t rows, int64_t M, int64_t N, const int32_t* ends,
+                                      const void* a, int64_t lda, const float* sa, const void* b, int64_t ldb,
+                                      const float* sb, void* c, int64_t ldc, int64_t group, int32_t c_f32,
+                                      int32_t accumulate, uint32_t* status, cudaStream_t stream);
+
+// Quantisation of groups of rows, of several matrices, and of the epilogue's
+// backward with the bias's gradient (fp8_quant.cu); part: the row tiles' sums.
+int64_t group_row_tiles(int64_t groups, int64_t rows);
+rlk_status launch_fp8_quantize_grouped(int64_t G, int64_t rows, int64_t cols, const int32_t* ends, const void* x,
+                                       int32_t x_f32, int64_t ldx, uint8_t* q, int64_t ldq, float* scale, uint8_t* qt,
+                                       int64_t ldqt, float* scale_t, cudaStream_t stream);
+rlk_status launch_fp8_quantize_batch(int64_t count, int64_t rows, int64_t cols, const void* x, int32_t x_f32,
+                                     int64_t ldx, int64_t x_b, uint8_t* q, int64_t ldq, int64_t q_b, float* scale,
+                                     uint8_t* qt, int64_t ldqt, int64_t qt_b, float* scale_t, cudaStream_t stream);
+rlk_status launch_fp8_act_grad(int64_t G, int64_t rows, int64_t wide, const int32_t* ends, const void* dy,
+                               int32_t dy_f32, int64_t lddy, const void* z, int64_t ldz, int32_t act, int32_t gated,
+                               uint8_t* q, int64_t ldq, float* scale, uint8_t* qt, int64_t ldqt, float* scale_t,
+                               void* dbias, int32_t dbias_f32, float* part, cudaStream_t stream);
+
 // Launches the bounded-wait self-test kernel (one warp waiting on an mbarrier
 // that nothing arrives at).
 rlk_status launch_selftest_wait(uint64_t limit_ns, uint32_t* status, cudaStream_t stream);
