@@ -49,15 +49,18 @@ rlk_status launch_fp8_grouped_matmul(int64_t G, int64_t M, int64_t N, int64_t K,
     p.sb_g = (int64_t)p.KB * p.nsb;
     p.w.status = status;
     p.w.wait_ns = kDefaultWaitNs;
-    const int halves = p.gated ? 2 : 1;
+    const bool gated = e && e->gated;
+    const int halves = gated ? 2 : 1;
     const int64_t live = G < M ? G : M;  // groups that have rows, at most
     CUtensorMap ta, tb;
     if (const int nt = block_rows_of(M, G)) {
         p.NB = (int32_t)((N * halves + kSRows - 1) / kSRows);
         if (!make_map8(&ta, a, K, M, lda, (uint32_t)nt) ||
-            !make_map_halves(&tb, b, K, N, halves, G, ldb, group, p.gated ? 32 : kSRows))
+            !make_map_halves(&tb, b, K, N, halves, G, ldb, group, gated ? 32 : kSRows))
             return fail(RLK_ERR_CUDA, "cuTensorMapEncodeTiled failed for an operand of the grouped fp8 product");
-        return launch_skinny_nt<false, kRows>(nt, p, ta, tb, (live + M / nt + 1) * p.NB, sms, stream);
+        const int64_t most = (live + M / nt + 1) * p.NB;
+        return gated ? launch_skinny_nt<false, kRowsGated>(nt, p, ta, tb, most, sms, stream)
+                     : launch_skinny_nt<false, kRows>(nt, p, ta, tb, most, sms, stream);
     }
     p.MB = 0;
     p.NB = (int32_t)((N * halves + kGN - 1) / kGN);
@@ -65,8 +68,11 @@ rlk_status launch_fp8_grouped_matmul(int64_t G, int64_t M, int64_t N, int64_t K,
     p.band = band_of((M + 2 * kGM - 1) / (2 * kGM), K);
     if (!make_map8(&ta, a, K, M, lda, kGM) || !make_map_halves(&tb, b, K, N, halves, G, ldb, group, kGN / 2))
         return fail(RLK_ERR_CUDA, "cuTensorMapEncodeTiled failed for an operand of the grouped fp8 product");
-    return launch_clusters<gemm_kernel<false, kRows>>(2 * (int)(tiles < sms / 2 ? tiles : sms / 2), kGThreads,
-                                                      kGSmemOf<false, kRows>, 2, false, stream, ta, tb, p, 0, 0, 1);
+    const int blocks = 2 * (int)(tiles < sms / 2 ? tiles : sms / 2);
+    return gated ? launch_clusters<gemm_kernel<false, kRowsGated>>(blocks, kGThreads, kGSmemOf<false, kRowsGated>, 2,
+                                                                   false, stream, ta, tb, p, 0, 0, 1)
+                 : launch_clusters<gemm_kernel<false, kRows>>(blocks, kGThreads, kGSmemOf<false, kRows>, 2, false,
+                                                              stream, ta, tb, p, 0, 0, 1);
 }
 
 rlk_status launch_fp8_grouped_dweight(int64_t G, int64_t rows, int64_t M, int64_t N, const int32_t* ends,

@@ -161,33 +161,77 @@ __device__ __forceinline__ void load8(float (&v)[8], const void* x, int64_t at, 
                          : __uint_as_float((uint32_t) static_cast<const uint16_t*>(x)[at + j] << 16);
 }
 
-// Row i of the thread's block of dz.  Gated: columns [0, C / 2) are the gate's
-// (8 columns are of one half: C / 2 is a multiple of 64).
-template <int ACT>
+// Two values of dz; `up` the gate's other half (or of no use).
+template <int ACT, bool GATED>
+__device__ __forceinline__ float2 dz_of(float2 dy, float2 z, float2 up, bool other) {
+    if (GATED) return other ? fmul2(dy, act_pair<ACT>(z)) : fmul2(fmul2(dy, up), act_slope_pair<ACT>(z));
+    return ACT == RLK_ACT_NONE ? dy : fmul2(dy, act_slope_pair<ACT>(z));
+}
+
+// Row i of the thread's block of dz, 8 columns from c0 on (of one half: C / 2 is
+// a multiple of 64).  Gated: columns [0, C / 2) are the gate's.
+template <int ACT, bool GATED>
 __device__ __forceinline__ void load_dz_row(Block<true>& b, int i, const QuantExtParams& p, int64_t r, int64_t end,
                                             int64_t c0) {
-    const int64_t N = p.gated ? p.C / 2 : p.C, c = c0 >= N ? c0 - N : c0, left = c0 < p.C ? N - c : 0;
+    const int64_t N = GATED ? p.C / 2 : p.C;
+    const bool other = GATED && c0 >= N;
+    const int64_t c = other ? c0 - N : c0, left = c0 < p.C ? N - c : 0;
     if (r >= end || left <= 0) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) b.w[i][j] = 0u;
         return;
     }
-    float dy[8], z[8];
+    float dy[8], z[8] = {}, up[8] = {};
     load8(dy, p.dy, r * p.lddy + c, p.dy_f32, p.dy_vec, left);
-    if (ACT != RLK_ACT_NONE || p.gated) load8(z, p.z, r * p.ldz + c, false, p.z_vec, left);
-    if (p.gated && c0 < N) {
-        float up[8];
-        load8(up, p.z, r * p.ldz + N + c, false, p.z_vec, left);
+    if (ACT != RLK_ACT_NONE || GATED) load8(z, p.z, r * p.ldz + c, false, p.z_vec, left);
+    if (GATED && !other) load8(up, p.z, r * p.ldz + N + c, false, p.z_vec, left);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dy[j] = __fmul_rn(dy[j], up[j]);
+    for (int j = 0; j < 8; j += 2) {
+        const float2 d = dz_of<ACT, GATED>(make_float2(dy[j], dy[j + 1]), make_float2(z[j], z[j + 1]),
+                                           make_float2(up[j], up[j + 1]), other);
+        b.w[i][j] = j < left ? __float_as_uint(d.x) : 0u;
+        b.w[i][j + 1] = j + 1 < left ? __float_as_uint(d.y) : 0u;
     }
-    const bool other = p.gated && c0 >= N;
+}
+
+// The thread's 8 rows of it: BF16 on the 16-byte grid by four rows' loads at a
+// time (a row at a time the tile was a chain of eight memory latencies: 4096 x
+// 6144 gated 145 us, XX so).
+template <int ACT, bool GATED>
+__device__ __forceinline__ void load_dz(Block<true>& b, const QuantExtParams& p, int64_t r0, int64_t end, int64_t c0) {
+    const int64_t N = GATED ? p.C / 2 : p.C;
+    const bool other = GATED && c0 >= N;
+    const int64_t c = other ? c0 - N : c0;
+    if (p.dy_f32 || !p.dy_vec || (!p.z_vec && (ACT != RLK_ACT_NONE || GATED)) || c + 8 > N) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float d = other ? __fmul_rn(dy[j], act_f32(z[j], ACT))
-                        : ACT == RLK_ACT_NONE ? dy[j]
-                                              : __fmul_rn(dy[j], act_slope_f32(z[j], ACT));
-        b.w[i][j] = __float_as_uint(j < left ? d : 0.f);
+        for (int i = 0; i < 8; ++i) load_dz_row<ACT, GATED>(b, i, p, r0 + i, end, c0);
+        return;
+    }
+    const uint16_t *dy = static_cast<const uint16_t*>(p.dy) + r0 * p.lddy + c, *z = p.z + r0 * p.ldz + c;
+    const int rows = (int)min((int64_t)8, end - r0);
+#pragma unroll
+    for (int h = 0; h < 8; h += 4) {
+        uint4 d[4], a[4], u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            d[i] = a[i] = u[i] = make_uint4(0, 0, 0, 0);
+            if (h + i < rows) {
+                d[i] = __ldcs(reinterpret_cast<const uint4*>(dy + (h + i) * p.lddy));
+                if (ACT != RLK_ACT_NONE || GATED) a[i] = __ldcs(reinterpret_cast<const uint4*>(z + (h + i) * p.ldz));
+                if (GATED && !other) u[i] = __ldcs(reinterpret_cast<const uint4*>(z + (h + i) * p.ldz + N));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t wd[4] = {d[i].x, d[i].y, d[i].z, d[i].w}, wa[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+            const uint32_t wu[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                auto two = [](uint32_t w) { return make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w)); };
+                const float2 v = dz_of<ACT, GATED>(two(wd[k]), two(wa[k]), two(wu[k]), other);
+                b.w[h + i][2 * k] = __float_as_uint(v.x), b.w[h + i][2 * k + 1] = __float_as_uint(v.y);
+            }
+        }
     }
 }
 
@@ -425,8 +469,8 @@ __global__ void __launch_bounds__(kQThreads, F32 ? 3 : 4)
 }
 
 // The epilogue's backward.
-template <bool TRANS, int ROWS, int ACT>
-__global__ void __launch_bounds__(kQThreads, 3) act_grad_kernel(const __grid_constant__ QuantExtParams p) {
+template <bool TRANS, int ROWS, int ACT, bool GATED>
+__global__ void __launch_bounds__(kQThreads, 2) act_grad_kernel(const __grid_constant__ QuantExtParams p) {
     __shared__ TileShared<true, false, TRANS> sh;
     __shared__ typename std::conditional<ROWS == kGroups, GroupTable, int>::type tab;
     __shared__ float4 sums[16][kQT / 4];
@@ -440,8 +484,7 @@ __global__ void __launch_bounds__(kQThreads, 3) act_grad_kernel(const __grid_con
         at = RowTile{rt * kQT, p.R, rt * kQT, p.R, rt};
     }
     Block<true> b;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) load_dz_row<ACT>(b, i, p, at.row0 + ry * 8 + i, at.end, ct * kQT + cx * 8);
+    load_dz<ACT, GATED>(b, p, at.row0 + ry * 8, at.end, ct * kQT + cx * 8);
     if (p.part) {
         float s[8];
 #pragma unroll
@@ -537,21 +580,25 @@ rlk_status launch_ext(const QuantExtParams& p, bool f32, int64_t row_tiles, cuda
     return quant_cuda("fp8 quantize launch");
 }
 
-template <bool TRANS, int ROWS>
+template <bool TRANS, int ROWS, bool GATED>
 void launch_act(const QuantExtParams& p, dim3 grid, cudaStream_t st) {
+    auto go = [&](auto kernel) { kernel<<<grid, kQThreads, 0, st>>>(p); };
     switch (p.act) {
-        case RLK_ACT_RELU: act_grad_kernel<TRANS, ROWS, RLK_ACT_RELU><<<grid, kQThreads, 0, st>>>(p); break;
-        case RLK_ACT_SILU: act_grad_kernel<TRANS, ROWS, RLK_ACT_SILU><<<grid, kQThreads, 0, st>>>(p); break;
-        case RLK_ACT_GELU: act_grad_kernel<TRANS, ROWS, RLK_ACT_GELU><<<grid, kQThreads, 0, st>>>(p); break;
-        case RLK_ACT_GELU_TANH: act_grad_kernel<TRANS, ROWS, RLK_ACT_GELU_TANH><<<grid, kQThreads, 0, st>>>(p); break;
-        default: act_grad_kernel<TRANS, ROWS, RLK_ACT_NONE><<<grid, kQThreads, 0, st>>>(p);
+        case RLK_ACT_RELU: return go(act_grad_kernel<TRANS, ROWS, RLK_ACT_RELU, GATED>);
+        case RLK_ACT_SILU: return go(act_grad_kernel<TRANS, ROWS, RLK_ACT_SILU, GATED>);
+        case RLK_ACT_GELU: return go(act_grad_kernel<TRANS, ROWS, RLK_ACT_GELU, GATED>);
+        case RLK_ACT_GELU_TANH: return go(act_grad_kernel<TRANS, ROWS, RLK_ACT_GELU_TANH, GATED>);
+        default: return go(act_grad_kernel<TRANS, ROWS, RLK_ACT_NONE, GATED>);
     }
 }
 
 template <int ROWS>
 rlk_status launch_act_rows(const QuantExtParams& p, int64_t row_tiles, void* dbias, bool f32, cudaStream_t st) {
     const dim3 grid = tile_grid(p.C, row_tiles);
-    p.qt ? launch_act<true, ROWS>(p, grid, st) : launch_act<false, ROWS>(p, grid, st);
+    if (p.gated)
+        p.qt ? launch_act<true, ROWS, true>(p, grid, st) : launch_act<false, ROWS, true>(p, grid, st);
+    else
+        p.qt ? launch_act<true, ROWS, false>(p, grid, st) : launch_act<false, ROWS, false>(p, grid, st);
     rlk_status s = quant_cuda("fp8 activation gradient launch");
     if (s != RLK_OK || !dbias) return s;
     const dim3 sums((unsigned)((p.C + 31) / 32), (unsigned)(p.G < 1 ? 1 : p.G < 32 ? p.G : 32));

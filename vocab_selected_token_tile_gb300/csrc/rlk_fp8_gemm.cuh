@@ -230,7 +230,10 @@ struct Gemm8Params {
 // activation, residual); of rows that belong to groups, each with a B of its
 // own, and that epilogue; of operands whose K axis belongs to groups, each with
 // a C of its own.
-enum Kind8 : int { kPlain, kEpi, kRows, kDepth };
+enum Kind8 : int { kPlain, kEpi, kEpiGated, kRows, kRowsGated, kDepth };
+__host__ __device__ constexpr bool gated_kind(int k) { return k == kEpiGated || k == kRowsGated; }
+__host__ __device__ constexpr bool rows_kind(int k) { return k == kRows || k == kRowsGated; }
+__host__ __device__ constexpr bool layer_kind(int k) { return k == kEpi || k == kEpiGated || rows_kind(k); }
 
 struct Ext8Params : Gemm8Params {
     // kEpi, kRows: z = A B^T + bias, y = act(z) (gated: B holds N rows of the gate, then N more; y = act(gate) * up),
@@ -238,7 +241,7 @@ struct Ext8Params : Gemm8Params {
     const void *bias, *res;
     uint16_t* z;          // NULL, or where z goes in BF16
     int64_t ldr, ldz;
-    int32_t bias_f32, res_f32, res_vec, z_vec, act, gated;
+    int32_t bias_f32, res_f32, res_vec, z_vec, act;
     // kRows, kDepth
     const int32_t* ends;
     int32_t G, rest;      // rest: the rows behind the groups are set to zero
@@ -422,7 +425,7 @@ template <bool BROWS>
 constexpr size_t kGSmem = 1024 + (size_t)kGStages * (kGA + kGB) + 8 * kGOut +
                           (size_t)kGSlots * kGroups * kGScales<BROWS> * 4 + 1024;
 template <bool BROWS, int KIND>
-constexpr size_t kGSmemOf = kGSmem<BROWS> + (KIND == kRows || KIND == kDepth ? sizeof(GroupTable) : 0);
+constexpr size_t kGSmemOf = kGSmem<BROWS> + (rows_kind(KIND) || KIND == kDepth ? sizeof(GroupTable) : 0);
 struct GemmBars {
     PairBars<kGStages> pair;
     uint64_t sfull[kGSlots], sempty[kGSlots];
@@ -457,7 +460,7 @@ __device__ __forceinline__ Tile8 tile_at(const typename ParamsOf<KIND>::type& p,
                                          int k1) {
     Tile8 x{0, p.M, 0, 0, k0, k1};
     int mb, MB = p.MB;
-    if constexpr (KIND == kRows) {
+    if constexpr (rows_kind(KIND)) {
         x.group = group_of(tab, p.G, t);
         t -= tab->first[x.group];
         x.row0 = tab->begin[x.group], x.end = tab->begin[x.group + 1];
@@ -474,37 +477,77 @@ __device__ __forceinline__ Tile8 tile_at(const typename ParamsOf<KIND>::type& p,
     return x;
 }
 
-// 64 columns of the residual from `col` on, added to the lane's row v, through shared memory as store_chunk's output.
+// 64 columns of the residual from `col` on, added to the lane's row v, through
+// shared memory as store_chunk's output; eight loads under way at a time (one by
+// one a tile's took 19,500 clocks).
 template <bool F32>
 __device__ __forceinline__ void add_residual(const Ext8Params& p, unsigned char* out, int lane, int64_t row0,
                                              int64_t limit, int col, float2* v) {
-    constexpr int kPer = F32 ? 4 : 8;
+    constexpr int kPer = F32 ? 4 : 8, kCols = F32 ? 32 : 64;
+    const int rows = (int)min((int64_t)32, limit - row0);
 #pragma unroll
     for (int half = 0; half < (F32 ? 2 : 1); ++half) {
-        const int j = lane & 7, at = col + half * 32 + j * kPer, left = p.N - at;
-        const int64_t rows = limit - row0;
+        const int at = col + half * 32, cols = min(kCols, p.N - at);
         __syncwarp();
+        if (p.res_vec) {
+            const int j = lane & 7, left = cols - j * kPer;
+            const char* src = static_cast<const char*>(p.res) +
+                              ((row0 + (lane >> 3)) * p.ldr + at + j * kPer) * (16 / kPer);
+            const int64_t four = 4 * p.ldr * (16 / kPer);
+            uint4 x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3);
-            uint32_t w[4] = {};
-            if (r < rows && left > 0) {
-                const int64_t o = (row0 + r) * p.ldr + at;
-                if (p.res_vec && left >= kPer) {
-                    const uint4 x = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(p.res) + o * (16 / kPer)));
-                    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-                } else {
+            for (int i = 0; i < 8; ++i) {
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (i * 4 + (lane >> 3) < rows && left >= kPer) x[i] = __ldcs(reinterpret_cast<const uint4*>(src + i * four));
+            }
+            if (left > 0 && left < kPer) {  // the last columns of an N between pieces
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t w[4] = {};
 #pragma unroll
                     for (int e = 0; e < kPer; ++e)
-                        if (e < left) {
+                        if (i * 4 + (lane >> 3) < rows && e < left) {
                             if (F32)
-                                w[e] = static_cast<const uint32_t*>(p.res)[o + e];
+                                w[e] = reinterpret_cast<const uint32_t*>(src + i * four)[e];
                             else
-                                w[e >> 1] |= (uint32_t) static_cast<const uint16_t*>(p.res)[o + e] << (16 * (e & 1));
+                                w[e >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(src + i * four)[e] << (16 * (e & 1));
                         }
+                    x[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
-            *reinterpret_cast<uint4*>(out + r * 128 + ((j ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = i * 4 + (lane >> 3);
+                *reinterpret_cast<uint4*>(out + r * 128 + ((j ^ (r & 7)) * 16)) = x[i];
+            }
+        } else if (F32) {
+            const uint32_t* src = static_cast<const uint32_t*>(p.res) + row0 * p.ldr + at + lane;
+#pragma unroll
+            for (int b = 0; b < 32; b += 8) {
+                uint32_t x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = b + i < rows && lane < cols ? __ldcs(src + (b + i) * p.ldr) : 0u;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint32_t*>(out + (b + i) * 128 + (((lane >> 2) ^ i) * 16) + (lane & 3) * 4) = x[i];
+            }
+        } else {
+            const uint16_t* src = static_cast<const uint16_t*>(p.res) + row0 * p.ldr + at + 2 * lane;
+#pragma unroll
+            for (int b = 0; b < 32; b += 8) {
+                uint32_t x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = 0u;
+                    if (b + i < rows) {
+                        if (2 * lane < cols) x[i] = src[(b + i) * p.ldr];
+                        if (2 * lane + 1 < cols) x[i] |= (uint32_t)src[(b + i) * p.ldr + 1] << 16;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint32_t*>(out + (b + i) * 128 + (((lane >> 2) ^ i) * 16) + (lane & 3) * 4) = x[i];
+            }
         }
         __syncwarp();
 #pragma unroll
@@ -533,60 +576,51 @@ __device__ __forceinline__ float res_at(const Ext8Params& p, int64_t i) {
                      : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.res)[i] << 16);
 }
 
-template <int N>
-__device__ __forceinline__ void act_pairs(float2 (&v)[N], int lo, int hi, int act) {
-#define RLK_ACT_CASE(A)                                                                          case A:                                                                                          _Pragma("unroll") for (int i = 0; i < N; ++i) if (i >= lo && i < hi) v[i] =                      make_float2(act_f32(v[i].x, A), act_f32(v[i].y, A));                                     break;
-    switch (act) {
-        RLK_ACT_CASE(RLK_ACT_RELU)
-        RLK_ACT_CASE(RLK_ACT_SILU)
-        RLK_ACT_CASE(RLK_ACT_GELU)
-        RLK_ACT_CASE(RLK_ACT_GELU_TANH)
-        default: break;
+// The sums of a warp's columns start from their biases: four columns a lane,
+// read once, then all of them by every lane through shared memory.
+template <bool GATED>
+__device__ __forceinline__ void start_with_bias(const Ext8Params& p, unsigned char* out, int lane, const Tile8& t,
+                                                int part, float2 (&sum)[64]) {
+    if (p.rest && t.group == p.G) return;  // rows behind the groups: zeros
+    const int half = GATED ? lane >> 4 : 0;
+    const int col = t.nb * (GATED ? kGN / 2 : kGN) + part * (GATED ? 64 : 128) + 4 * (GATED ? lane & 15 : lane);
+    const int64_t at = (int64_t)t.group * (GATED ? 2 : 1) * p.N + (half ? p.N : 0) + col;
+    float b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = col + i < p.N ? bias_at(p, at + i) : 0.f;
+    __syncwarp();
+    reinterpret_cast<float4*>(out)[lane] = make_float4(b[0], b[1], b[2], b[3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float4 x = reinterpret_cast<const float4*>(out)[i];
+        sum[2 * i] = make_float2(x.x, x.y), sum[2 * i + 1] = make_float2(x.z, x.w);
     }
-#undef RLK_ACT_CASE
+    __syncwarp();
 }
 
 // The epilogue of a warp's 32 rows x 128 columns of B's rows, a row a lane: the
 // columns are 128 of the result, or (gated) 64 of the gate and the same 64 of
 // the other half, which the loads of B have laid side by side.
-__device__ __forceinline__ void finish_rows(const Ext8Params& p, unsigned char* out, int lane, const Tile8& t, int part,
-                                            int64_t row0, float2 (&sum)[64]) {
+template <bool GATED>
+__device__ __forceinline__ void finish_rows(const Ext8Params& p, unsigned char* out, int lane, const Tile8& t,
+                                            int part, int64_t row0, float2 (&sum)[64]) {
     const bool behind = p.rest && t.group == p.G;  // rows behind the groups: zeros
-    const int col0 = t.nb * (p.gated ? kGN / 2 : kGN) + part * (p.gated ? 64 : 128);
-    const int64_t wide = p.gated ? 2 * (int64_t)p.N : p.N;
+    const int col0 = t.nb * (GATED ? kGN / 2 : kGN) + part * (GATED ? 64 : 128);
+    if (p.z && !behind) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int col = col0 + (p.gated ? 0 : 64 * h), other = p.gated && h ? p.N : 0;
-        if (p.bias && !behind) {
-            __syncwarp();
-            float2 b = make_float2(0.f, 0.f);
-            const int64_t at = t.group * wide + other + col + 2 * lane;
-            if (col + 2 * lane < p.N) b.x = bias_at(p, at);
-            if (col + 2 * lane + 1 < p.N) b.y = bias_at(p, at + 1);
-            reinterpret_cast<float2*>(out)[lane] = b;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float4 x = reinterpret_cast<const float4*>(out)[i];
-                sum[32 * h + 2 * i] = fadd2(sum[32 * h + 2 * i], make_float2(x.x, x.y));
-                sum[32 * h + 2 * i + 1] = fadd2(sum[32 * h + 2 * i + 1], make_float2(x.z, x.w));
-            }
-        }
-        if (p.z && !behind)
-            store_chunk<false, false>(Dest{p.z + other, p.ldz, t.end, p.N, p.z_vec, 0}, out, lane, row0, col,
-                                      sum + 32 * h);
+        for (int h = 0; h < 2; ++h)
+            store_chunk<false, false>(Dest{p.z + (GATED && h ? p.N : 0), p.ldz, t.end, p.N, p.z_vec, 0}, out, lane,
+                                      row0, col0 + (GATED ? 0 : 64 * h), sum + 32 * h);
     }
-    if (p.gated) {
-        act_pairs(sum, 0, 32, p.act);
+    act_pairs<0, GATED ? 32 : 64>(sum, p.act);
+    if (GATED) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) sum[i] = fmul2(sum[i], sum[32 + i]);
-    } else {
-        act_pairs(sum, 0, 64, p.act);
     }
     const Dest d = dest_of(p, t.end);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (h && p.gated) break;
+    for (int h = 0; h < (GATED ? 1 : 2); ++h) {
         const int col = col0 + 64 * h;
         if (p.res) {
             if (p.res_f32)
@@ -613,8 +647,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ typename ParamsOf<KIND>::type p, const int tile0, const int tiles_given,
                 const int split_given) {
-    constexpr bool kGrouped = KIND == kRows || KIND == kDepth;
-    static_assert(!BROWS || KIND == kPlain || KIND == kDepth, "an epilogue's B has scales by the block");
+    constexpr bool kGrouped = rows_kind(KIND) || KIND == kDepth, kLayer = layer_kind(KIND), kGated = gated_kind(KIND);
+    static_assert(!BROWS || !kLayer, "an epilogue's B has scales by the block");
     const int split = kGrouped ? 1 : split_given;
     extern __shared__ unsigned char smem_raw[];
     // The same offset in both CTAs (their dynamic shared memory starts alike): descriptors name one offset.
@@ -639,13 +673,13 @@ __global__ void __launch_bounds__(kGThreads, 1)
             mbar_init(smem_u32(&all->sempty[i]), 8);
         }
     }
-    if constexpr (KIND == kRows) groups_build<kGThreads>(tab, p.ends, p.G, p.M, 2 * kGM, p.NB, p.rest);
+    if constexpr (rows_kind(KIND)) groups_build<kGThreads>(tab, p.ends, p.G, p.M, 2 * kGM, p.NB, p.rest);
     if constexpr (KIND == kDepth) groups_build<kGThreads>(tab, p.ends, p.G, p.deep, kGK, 1, false);
     const uint32_t tmem = pair_begin(bars, warp, 8);
     int* ab = &bars->abort_flag;
     grid_launch_dependents();  // the launch of the last tiles
     int tiles = tiles_given;
-    if constexpr (KIND == kRows) tiles = tab->first[p.G + 1];
+    if constexpr (rows_kind(KIND)) tiles = tab->first[p.G + 1];
     auto tile = [&](int t) { return tile_at<KIND>(p, tab, t, k0, k1); };
 
     if (warp < 4) {
@@ -668,8 +702,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
                         const uint32_t fb = full0 + r.slot * 8;
                         pair_arm(fb, smem_u32(&bars->full[r.slot]), rank, kGB + (mine ? kGA : 0));
                         if (mine) tma_load_2d_pair(smem_u32(sA + r.slot * kGA), &tmA, kb * kGK, a_row, fb);
-                        if constexpr (KIND == kEpi || KIND == kRows)  // half as many rows of each half
-                            tma_load_4d_pair(smem_u32(sB + r.slot * kGB), &tmB, kb * kGK, p.gated ? b_row / 2 : b_row,
+                        if constexpr (kLayer)  // gated: half as many rows of each half
+                            tma_load_4d_pair(smem_u32(sB + r.slot * kGB), &tmB, kb * kGK, kGated ? b_row / 2 : b_row,
                                              0, x.group, fb);
                         else
                             tma_load_2d_pair(smem_u32(sB + r.slot * kGB), &tmB, kb * kGK, b_row, fb);
@@ -719,7 +753,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                     if (!ok) break;
                     uint32_t dst = smem_u32(scales + r.slot * kGroups * kGScales<BROWS>) + lane * 4;
                     const float *a = p.sa + (int64_t)kg * p.M, *b = p.sb + (int64_t)kg * p.nsb;
-                    if constexpr (KIND == kRows) b += x.group * p.sb_g;
+                    if constexpr (rows_kind(KIND)) b += x.group * p.sb_g;
                     for (int kb = kg; kb < min(kg + kGroups, x.k1); ++kb) {
 #pragma unroll
                         for (int i = 0; i < kGM; i += 32)
@@ -728,11 +762,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
 #pragma unroll
                             for (int i = 0; i < kGN; i += 32)
                                 cp_async4(dst + (kGM + i) * 4, b + (col + i < p.N ? col + i : 0), col + i < p.N);
-                        } else if constexpr (KIND == kEpi || KIND == kRows) {
-                            // of each half of the columns, and if gated of both halves of B
-                            if (lane < (p.gated ? 4 : 2)) {
-                                const int blk = p.gated ? ((lane >> 1) * p.N + x.nb * 128 + (lane & 1) * 64) >> 7
-                                                        : x.nb * 2 + lane;
+                        } else if constexpr (kGated) {
+                            // of each half of the columns, of both halves of B
+                            if (lane < 4) {
+                                const int blk = ((lane >> 1) * p.N + x.nb * 128 + (lane & 1) * 64) >> 7;
                                 cp_async4(dst + kGM * 4, b + (blk < p.nsb ? blk : 0), blk < p.nsb);
                             }
                         } else if (lane < 2) {
@@ -748,6 +781,19 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 }
             }
             cp_async_wait_all();
+        } else if (warp == 3) {
+            if constexpr (kLayer) {
+                // -------------------------------------------- the residual's rows of the next tiles, into L2
+                for (int t = first; p.res && split == 1 && t < tiles; t += step) {
+                    const Tile8 x = tile(t);
+                    const int cols = kGated ? kGN / 2 : kGN, col = x.nb * cols;
+                    const int size = p.res_f32 ? 4 : 2, row = x.row0 + rank * kGM;
+                    const int pieces = (min(cols, p.N - col) * size + 127) / 128;
+                    const char* src = static_cast<const char*>(p.res) + ((int64_t)row * p.ldr + col) * size;
+                    for (int i = lane; i < min(kGM, x.end - row) * pieces; i += 32)
+                        prefetch_l2(src + i / pieces * p.ldr * size + i % pieces * 128);
+                }
+            }
         }
         __syncwarp();
     } else {
@@ -763,6 +809,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
             float2 sum[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
+            if constexpr (kLayer)
+                if (p.bias && split == 1) start_with_bias<kGated>(p, out, lane, tile(t), part, sum);
             const float* s = nullptr;
             const Tile8 x = tile(t);
             for (int kb = x.k0; kb < x.k1; ++kb) {
@@ -777,9 +825,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                     for (int i = 0; i < 4; ++i) f[i] = s[quarter * 32 + i * 8 + (lane >> 2)];
                 } else {
                     f[0] = __fmul_rn(s[quarter * 32 + lane], s[kGM + part]);
-                    f[1] = f[0];
-                    if constexpr (KIND == kEpi || KIND == kRows)
-                        if (p.gated) f[1] = __fmul_rn(s[quarter * 32 + lane], s[kGM + 2 + part]);
+                    f[1] = kGated ? __fmul_rn(s[quarter * 32 + lane], s[kGM + 2 + part]) : f[0];
                 }
                 if (!ready) ok = ok && pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w);
                 ok = __all_sync(0xFFFFFFFFu, ok);
@@ -855,8 +901,8 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 break;
             }
             const int64_t row0 = (int64_t)x.row0 + rank * kGM + quarter * 32;
-            if constexpr (KIND == kEpi || KIND == kRows) {
-                if (row0 < x.end) finish_rows(p, out, lane, x, part, row0, sum);
+            if constexpr (kLayer) {
+                if (row0 < x.end) finish_rows<kGated>(p, out, lane, x, part, row0, sum);
             } else {
                 const int col0 = x.nb * kGN + part * 128;
                 Dest d = dest_of(p, p.M);
@@ -895,7 +941,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             }
         };
         int quads = kGN / 4;  // of the result's columns, four each
-        if constexpr (KIND == kEpi) quads = p.gated ? kGN / 8 : kGN / 4;
+        if constexpr (kGated) quads = kGN / 8;
 #pragma unroll 2
         for (int e = threadIdx.x; e < (hi - lo) * quads && !failed; e += kGThreads) {
             const int r = lo + e / quads, c = e % quads * 4;
@@ -903,26 +949,26 @@ __global__ void __launch_bounds__(kGThreads, 1)
             const int col = tl.nb * 4 * quads + c;
             if (row >= p.M || col >= p.N) continue;
             float x[4];
-            if constexpr (KIND == kEpi) {
+            if constexpr (kLayer) {
                 float u[4] = {};
                 // gated: 64 columns of the gate, then the same of the other half, for each half of the tile
-                const int in = p.gated ? (c & 64) * 2 + (c & 63) : c;
+                const int in = kGated ? (c & 64) * 2 + (c & 63) : c;
                 joined(r, in, x);
-                if (p.gated) joined(r, in + 64, u);
+                if (kGated) joined(r, in + 64, u);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (col + i < p.N) {
                         if (p.bias) {
                             x[i] = __fadd_rn(x[i], bias_at(p, col + i));
-                            if (p.gated) u[i] = __fadd_rn(u[i], bias_at(p, (int64_t)p.N + col + i));
+                            if (kGated) u[i] = __fadd_rn(u[i], bias_at(p, (int64_t)p.N + col + i));
                         }
                         if (p.z) {
                             uint16_t* z = p.z + row * p.ldz + col + i;
                             z[0] = (uint16_t)pack_bf16x2_rn(x[i], 0.f);
-                            if (p.gated) z[p.N] = (uint16_t)pack_bf16x2_rn(u[i], 0.f);
+                            if (kGated) z[p.N] = (uint16_t)pack_bf16x2_rn(u[i], 0.f);
                         }
                         x[i] = act_f32(x[i], p.act);
-                        if (p.gated) x[i] = __fmul_rn(x[i], u[i]);
+                        if (kGated) x[i] = __fmul_rn(x[i], u[i]);
                         if (p.res) x[i] = __fadd_rn(x[i], res_at(p, row * p.ldr + col + i));
                     }
             } else {
@@ -969,7 +1015,7 @@ struct Skinny {
 };
 
 template <int NT, int KIND>
-constexpr size_t kSSmemOf = Skinny<NT>::kSmem + (KIND == kRows ? sizeof(GroupTable) : 0);
+constexpr size_t kSSmemOf = Skinny<NT>::kSmem + (rows_kind(KIND) ? sizeof(GroupTable) : 0);
 static_assert(2 * (kSSmemOf<64, kRows> + 1024) <= 233472, "two CTAs an SM");
 
 // A unit: 128 rows of B (gated: 64 of each half, 16 and 16 by turns, so that a
@@ -983,7 +1029,7 @@ struct Unit8 {
 template <int NT, int KIND>
 __device__ __forceinline__ Unit8 unit_at(const typename ParamsOf<KIND>::type& p, const GroupTable* tab, int t, int k0,
                                          int k1) {
-    if constexpr (KIND == kRows) {
+    if constexpr (rows_kind(KIND)) {
         // the blocks of rows that share 128 rows of B come one after the other
         const int e = group_of(tab, p.G, t), begin = tab->begin[e], n = tab->begin[e + 1] - begin;
         const int blocks = (n + NT - 1) / NT, at = t - tab->first[e], j = at % blocks;
@@ -992,10 +1038,11 @@ __device__ __forceinline__ Unit8 unit_at(const typename ParamsOf<KIND>::type& p,
     return Unit8{0, p.M, t, 0, k0, k1};
 }
 
-// One result of few rows: z and its other half u (gated) of `row` and `col`.
+// One result of K split over a cluster: z and its other half u (gated) of `row` and `col`.
+template <bool GATED>
 __device__ __forceinline__ void finish_one(const Ext8Params& p, int64_t row, int col, float z, float u) {
     float y = act_f32(z, p.act);
-    if (p.gated) y = __fmul_rn(y, u);
+    if (GATED) y = __fmul_rn(y, u);
     if (p.res) y = __fadd_rn(y, res_at(p, row * p.ldr + col));
     if (p.c_f32)
         static_cast<float*>(p.c)[row * p.ldc + col] = y;
@@ -1003,12 +1050,82 @@ __device__ __forceinline__ void finish_one(const Ext8Params& p, int64_t row, int
         static_cast<uint16_t*>(p.c)[row * p.ldc + col] = (uint16_t)pack_bf16x2_rn(y, 0.f);
 }
 
+// The epilogue of few rows: a lane has a row of B against up to NT rows of A.
+// Gated: lanes l and l + 16 have a column's gate and its other half, and after
+// one exchange the first finishes the even rows and the second the odd ones.
+// Sixteen rows at a time, which bounds the registers.
+template <int NT, bool GATED>
+__device__ __forceinline__ void finish_lanes(const Ext8Params& p, const Unit8& x, int quarter, int lane,
+                                             const float (&sum)[NT]) {
+    const bool behind = p.rest && x.group == p.G;  // rows behind the groups: zeros
+    const int half = GATED ? lane >> 4 : 0;
+    const int col = GATED ? x.nb * 64 + quarter * 16 + (lane & 15) : x.nb * 128 + quarter * 32 + lane;
+    const bool in = col < p.N;
+    const int64_t zc = col + (half ? (int64_t)p.N : 0);  // its row of the group's B
+    float b = 0.f;
+    if (p.bias && in && !behind) b = bias_at(p, (int64_t)x.group * (GATED ? 2 : 1) * p.N + zc);
+    constexpr int kStep = GATED ? 2 : 1, kPairs = 8 / kStep;  // value i of a lane is row kStep i + half of the sixteen
+#pragma unroll
+    for (int r0 = 0; r0 < NT; r0 += 16) {
+        if (r0 >= x.rows) break;
+        float2 v[8], u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = fadd2(make_float2(sum[r0 + 2 * i], sum[r0 + 2 * i + 1]), make_float2(b, b));
+        if (p.z && in && !behind) {
+            uint16_t* z = p.z + (int64_t)(x.row0 + r0) * p.ldz + zc;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (r0 + i < x.rows) z[i * p.ldz] = (uint16_t)pack_bf16x2_rn(i & 1 ? v[i >> 1].y : v[i >> 1].x, 0.f);
+        }
+        if (GATED) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float g[2], o[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 w = v[2 * i + e];
+                    const float got = __shfl_xor_sync(0xFFFFFFFFu, half ? w.x : w.y, 16);
+                    g[e] = half ? got : w.x, o[e] = half ? w.y : got;
+                }
+                v[i] = make_float2(g[0], g[1]), u[i] = make_float2(o[0], o[1]);
+            }
+        }
+        act_pairs<0, kPairs>(v, p.act);
+        if (GATED) {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) v[i] = fmul2(v[i], u[i]);
+        }
+        const int64_t row = (int64_t)x.row0 + r0 + half;
+        const int left = in ? x.rows - r0 - half : 0;
+        if (p.res) {
+            float r[2 * kPairs];
+#pragma unroll
+            for (int i = 0; i < 2 * kPairs; ++i) r[i] = kStep * i < left ? res_at(p, (row + kStep * i) * p.ldr + col) : 0.f;
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) v[i] = fadd2(v[i], make_float2(r[2 * i], r[2 * i + 1]));
+        }
+        if (p.c_f32) {
+            float* c = static_cast<float*>(p.c) + row * p.ldc + col;
+#pragma unroll
+            for (int i = 0; i < 2 * kPairs; ++i)
+                if (kStep * i < left) c[kStep * i * p.ldc] = i & 1 ? v[i >> 1].y : v[i >> 1].x;
+        } else {
+            uint16_t* c = static_cast<uint16_t*>(p.c) + row * p.ldc + col;
+#pragma unroll
+            for (int i = 0; i < 2 * kPairs; ++i)
+                if (kStep * i < left)
+                    c[kStep * i * p.ldc] = (uint16_t)pack_bf16x2_rn(i & 1 ? v[i >> 1].y : v[i >> 1].x, 0.f);
+        }
+    }
+}
+
 template <int NT, bool BROWS, int KIND>
 __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     skinny_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ typename ParamsOf<KIND>::type p, const int split) {
     using S = Skinny<NT>;
-    constexpr bool kExt = KIND != kPlain;
+    constexpr bool kExt = KIND != kPlain, kGated = gated_kind(KIND);
     static_assert(!BROWS || !kExt, "an epilogue's B has scales by the block");
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem =
@@ -1024,7 +1141,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     const int k0 = (int)((int64_t)p.KB * rank / split), k1 = (int)((int64_t)p.KB * (rank + 1) / split);
 
     if (threadIdx.x == 0) init_bars8(bars, 4);
-    if constexpr (KIND == kRows) groups_build<kSThreads>(tab, p.ends, p.G, p.M, NT, p.NB, p.rest);
+    if constexpr (rows_kind(KIND)) groups_build<kSThreads>(tab, p.ends, p.G, p.M, NT, p.NB, p.rest);
     if (warp == 1) {
         tmem_alloc(smem_u32(&bars->tmem_addr), S::kTmem);
         tmem_relinquish();
@@ -1036,7 +1153,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     int* ab = &bars->abort_flag;
     const int quarter = warp & 3, row_in = quarter * 32 + lane;
     int tiles = p.NB;  // of 128 rows of B; all of A's rows are one block
-    if constexpr (KIND == kRows) tiles = tab->first[p.G + 1];
+    if constexpr (rows_kind(KIND)) tiles = tab->first[p.G + 1];
     auto unit = [&](int t) { return unit_at<NT, KIND>(p, tab, t, k0, k1); };
     float sum[NT];  // epilogue: this thread's row of B against the NT rows of A
 
@@ -1052,7 +1169,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
                     const uint32_t fb = smem_u32(&bars->full[r.slot]);
                     mbar_arrive_expect_tx(fb, S::kW + S::kX);
                     if constexpr (kExt) {
-                        if (p.gated) {
+                        if constexpr (kGated) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 tma_load_4d(smem_u32(sW + r.slot * S::kW + i * (S::kW / 4)), &tmB, kb * kGK,
@@ -1107,7 +1224,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
                 const uint32_t dst = smem_u32(scales + r.slot * S::kScale);
                 const float* a = p.sa + (int64_t)kb * p.M + x.row0;
                 const float* b = p.sb + (int64_t)kb * p.nsb;
-                if constexpr (KIND == kRows) b += x.group * p.sb_g;
+                if constexpr (rows_kind(KIND)) b += x.group * p.sb_g;
                 for (int i = lane; i < NT; i += 32) cp_async4(dst + i * 4, a + (i < x.rows ? i : 0), i < x.rows);
                 if (BROWS) {
 #pragma unroll
@@ -1116,8 +1233,8 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
                         cp_async4(dst + (NT + i) * 4, b + (row < p.N ? row : 0), row < p.N);
                     }
                 } else if constexpr (kExt) {
-                    if (lane < (p.gated ? 2 : 1)) {
-                        const int blk = p.gated ? (lane * p.N + x.nb * (kSRows / 2)) >> 7 : x.nb;
+                    if (lane < (kGated ? 2 : 1)) {
+                        const int blk = kGated ? (lane * p.N + x.nb * (kSRows / 2)) >> 7 : x.nb;
                         cp_async4(dst + (NT + lane) * 4, b + (blk < p.nsb ? blk : 0), blk < p.nsb);
                     }
                 } else if (lane == 0) {
@@ -1136,8 +1253,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
 #pragma unroll
             for (int i = 0; i < NT; ++i) sum[i] = 0.f;
             const Unit8 x = unit(t);
-            int half = 0;  // of B that this lane's row is of
-            if constexpr (kExt) half = p.gated ? lane >> 4 : 0;
+            const int half = kGated ? lane >> 4 : 0;  // of B that this lane's row is of
             for (int kb = x.k0; kb < x.k1; ++kb) {
                 ok = pipe_wait(ab, smem_u32(&bars->sc.full[sc.slot]), sc.phase, p.w);
                 const float* s = scales + sc.slot * S::kScale;
@@ -1170,31 +1286,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
             }
             if (!ok || split > 1) break;  // a split launch has one tile a cluster, added up below
             if constexpr (kExt) {
-                const bool behind = p.rest && x.group == p.G;  // rows behind the groups: zeros
-                const int64_t wide = p.gated ? 2 * (int64_t)p.N : p.N;
-                const int col = p.gated ? x.nb * (kSRows / 2) + quarter * 16 + (lane & 15) : x.nb * kSRows + row_in;
-                const bool in = col < p.N;
-                const int64_t zc = col + (half ? (int64_t)p.N : 0);  // its row of the group's B
-                const float b = p.bias && in && !behind ? bias_at(p, x.group * wide + zc) : 0.f;
-#pragma unroll
-                for (int i = 0; i < NT; i += 2) {
-                    if (i >= x.rows) break;
-                    const int64_t row = (int64_t)x.row0 + i;
-                    const float z0 = __fadd_rn(sum[i], b), z1 = __fadd_rn(sum[i + 1], b);
-                    const bool two = i + 1 < x.rows;
-                    if (p.z && in && !behind) {
-                        p.z[row * p.ldz + zc] = (uint16_t)pack_bf16x2_rn(z0, 0.f);
-                        if (two) p.z[(row + 1) * p.ldz + zc] = (uint16_t)pack_bf16x2_rn(z1, 0.f);
-                    }
-                    if (p.gated) {
-                        // the gate's lane finishes the first row, the other half's lane the second
-                        const float got = __shfl_xor_sync(0xFFFFFFFFu, half ? z0 : z1, 16);
-                        if (in && (!half || two)) finish_one(p, row + half, col, half ? got : z0, half ? z1 : got);
-                    } else if (in) {
-                        finish_one(p, row, col, z0, 0.f);
-                        if (two) finish_one(p, row + 1, col, z1, 0.f);
-                    }
-                }
+                finish_lanes<NT, kGated>(p, x, quarter, lane, sum);
                 continue;
             }
             const int col = t * kSRows + row_in;
@@ -1236,23 +1328,23 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
             if (first < tiles && !failed) {
                 const Unit8 x = unit(first);
                 const bool behind = p.rest && x.group == p.G;
-                const int per = p.gated ? kSRows / 2 : kSRows;
-                const int64_t at_b = x.group * (p.gated ? 2 * (int64_t)p.N : p.N);
+                const int per = kGated ? kSRows / 2 : kSRows;
+                const int64_t at_b = (int64_t)x.group * (kGated ? 2 : 1) * p.N;
                 for (int e = threadIdx.x; e < (hi - lo) * per; e += kSThreads) {
                     const int i = lo + e / per, c = e % per, col = x.nb * per + c;
                     if (i >= x.rows || col >= p.N) continue;
                     const int64_t row = (int64_t)x.row0 + i;
-                    const int in = p.gated ? (c >> 4) * 32 + (c & 15) : c;
-                    float z = joined(i, in), u = p.gated ? joined(i, in + 16) : 0.f;
+                    const int in = kGated ? (c >> 4) * 32 + (c & 15) : c;
+                    float z = joined(i, in), u = kGated ? joined(i, in + 16) : 0.f;
                     if (p.bias && !behind) {
                         z = __fadd_rn(z, bias_at(p, at_b + col));
-                        if (p.gated) u = __fadd_rn(u, bias_at(p, at_b + p.N + col));
+                        if (kGated) u = __fadd_rn(u, bias_at(p, at_b + p.N + col));
                     }
                     if (p.z && !behind) {
                         p.z[row * p.ldz + col] = (uint16_t)pack_bf16x2_rn(z, 0.f);
-                        if (p.gated) p.z[row * p.ldz + p.N + col] = (uint16_t)pack_bf16x2_rn(u, 0.f);
+                        if (kGated) p.z[row * p.ldz + p.N + col] = (uint16_t)pack_bf16x2_rn(u, 0.f);
                     }
-                    finish_one(p, row, col, z, u);
+                    finish_one<kGated>(p, row, col, z, u);
                 }
             }
         }
@@ -1384,7 +1476,7 @@ rlk_status launch_gemm(const typename ParamsOf<KIND>::type& p, const CUtensorMap
     // the sums' joining cost about as much as 12 K groups, so it has to save 16 (4096 x 4096 x 8192, scales by the
     // row, FP32: 172 us in one launch, 157 in two; 2560 x 4096 of BF16: 31 and 32 at K = 2048, 48.8 and 45.3 at 4096).
     constexpr auto kernel = gemm_kernel<BROWS, KIND>;
-    constexpr size_t smem = kGSmem<BROWS>;
+    constexpr size_t smem = kGSmemOf<BROWS, KIND>;
     const int tiles = p.MB * p.NB, pairs = sms / 2, whole = tiles / pairs * pairs, rest = tiles - whole;
     int split = rest > 0 ? kGSplit : 1;
     while (split > 1 && (p.KB < split * 4 || rest > clusters_at_once<kernel>(kGThreads, smem, 2 * split))) split /= 2;
@@ -1441,8 +1533,7 @@ int32_t band_of(int64_t MB, int64_t K) {
 // What a product with an epilogue takes from its call.
 void set_epilogue(Ext8Params& p, const rlk_fp8_epilogue* e, int64_t N) {
     p.act = e ? e->activation : RLK_ACT_NONE;
-    p.gated = e ? e->gated : 0;
-    p.nsb = (int32_t)(((p.gated ? 2 * N : N) + 127) / 128);
+    p.nsb = (int32_t)(((e && e->gated ? 2 * N : N) + 127) / 128);
     if (!e) return;
     p.bias = e->bias;
     p.bias_f32 = e->bias_type == RLK_F32;
