@@ -936,13 +936,18 @@ def _padded(stride, rows, cols, piece):
     return -(-cols // piece) * piece if rows <= 1 else stride
 
 
-def _codes(x, rows, cols):
-    """An E4M3 [rows, cols] tensor whose rows start on 16-byte boundaries, and its row stride.
+def _code_stride(cols):
+    """Bytes from one row of codes to the next: whole 16-byte pieces.
 
     Long rows that need padding at all start on 128-byte lines, which each of their 128-byte groups then fills
     (8000 x 3517: written in 22.6 us against 23.4; as a weight of 37 tokens read in 40.5 us against 41.8).
     """
-    stride = -(-cols // 128) * 128 if cols % 16 and cols >= 2048 else -(-cols // 16) * 16
+    return -(-cols // 128) * 128 if cols % 16 and cols >= 2048 else -(-cols // 16) * 16
+
+
+def _codes(x, rows, cols):
+    """An E4M3 [rows, cols] tensor whose rows start on 16-byte boundaries, and its row stride."""
+    stride = _code_stride(cols)
     return _new(x, rows, cols, _t().float8_e4m3fn, stride), stride
 
 
@@ -1390,6 +1395,181 @@ def fp8_act_grad(dy, z=None, activation=None, gated=False, ends=None, rowwise=Tr
         check(st)
     _used_here(stream, q, scale, qt, scale_t, dbias)
     return q, scale, qt, scale_t, dbias
+
+
+class _Places:
+    """Pieces of one buffer: codes, scales and partial sums that live and die together (an allocation each costs 3 us of
+    host time, ten of them a training step)."""
+
+    def __init__(self):
+        self.size = 0
+
+    def take(self, nbytes):
+        at = self.size
+        self.size = (at + nbytes + 255) & ~255
+        return at
+
+
+class Fp8LayerStep:
+    """The forward and the backward of a layer act(x @ weight^T + bias) + residual, dense or (with ``ends``) of rows that
+    belong to groups, as autograd's functions call them: the operands' quantisation and the products as
+    fp8_quantize_both, fp8_quantize_grouped, fp8_matmul_act, fp8_grouped_matmul, fp8_act_grad, fp8_matmul and
+    fp8_grouped_dweight make them, with what a pass quantises in one buffer.
+
+    forward gives (y, z, saved): z the pre-activation (None where no derivative needs it) and saved the transposes' codes
+    and scales; backward takes them back.
+    """
+
+    def __init__(self, x, weight, bias, residual, ends, activation, gated, need_x, need_w, need_b):
+        torch = _t()
+        both = (torch.bfloat16, torch.float32)
+        self.M, self.K, self.sx = _matrix(x, "x", both)
+        self.G, self.pe = (0, None) if ends is None else _ends(ends, x)
+        if ends is None:
+            self.rows, Kw, self.sw = _matrix(weight, "weight", both)
+            self.between, lead = 0, ()
+        else:
+            Gw, self.rows, Kw, self.sw, self.between = _matrices(weight, "weight", both)
+            lead = (self.G,)
+            if Gw != self.G:
+                raise ValueError(f"ends has {self.G} groups and weight {Gw}")
+        if Kw != self.K or Kw < 1:
+            raise ValueError(f"x is {list(x.shape)} and weight {list(weight.shape)}: their rows must have one length, "
+                             "at least 1")
+        if gated and self.rows % 128:
+            raise ValueError(f"a gated layer's weight holds two halves of a multiple of 64 rows, not {self.rows} rows")
+        self.N = self.rows // 2 if gated else self.rows
+        self.act, self.gated = _activation(activation), int(bool(gated))
+        self.e = Fp8Epilogue(activation=self.act, gated=self.gated)
+        self.tb = None if bias is None else bias.dtype
+        if bias is not None:
+            if bias.shape != lead + (self.rows,):
+                raise ValueError(f"bias is {list(bias.shape)}; the layer's is {list(lead + (self.rows,))}")
+            self.e.bias, self.e.bias_type = _vector(bias, "bias", bias.numel(), both), _type(bias)
+        if residual is not None:
+            r, c, self.e.residual_stride = _matrix(residual, "residual", both)
+            if (r, c) != (self.M, self.N):
+                raise ValueError(f"residual is {list(residual.shape)}; the result is [{self.M}, {self.N}]")
+            self.e.residual, self.e.residual_type = residual.data_ptr(), _type(residual)
+        self.types = x.dtype, weight.dtype
+        self.weight_shape, self.device = weight.shape, x.device
+        self.need_x, self.need_w, self.need_b = need_x, need_w, need_b
+        count = max(1, self.G)
+        self.kg, self.rg = -(-self.K // 128), -(-self.rows // 128)
+        self.tiles = group_tiles(self.G, self.M) if self.G else -(-self.M // 128)
+        self.ldm = 128 * self.tiles if self.G else _code_stride(self.M)  # of codes along the rows of x
+        self.ldk, self.ldr = _code_stride(self.K), _code_stride(self.rows)
+        keep = _Places()
+        self.xt, self.xts = (keep.take(self.K * self.ldm), keep.take(4 * self.tiles * self.K)) if need_w else (0, 0)
+        self.wt, self.wts = (keep.take(count * self.K * self.ldr), keep.take(4 * count * self.rg * self.kg)) if need_x \
+            else (0, 0)
+        self.kept = keep.size
+
+    def _buffer(self, size):
+        return _t().empty((size,), dtype=_t().uint8, device=self.device)
+
+    def forward(self, x, weight):
+        torch = _t()
+        M, K, rows, G, kg, rg, ldk = self.M, self.K, self.rows, self.G, self.kg, self.rg, self.ldk
+        count = max(1, G)
+        own = _Places()
+        xq, xs = own.take(M * ldk), own.take(4 * kg * M)
+        wq, ws = own.take(count * rows * ldk), own.take(4 * count * kg * rg)
+        scratch = self._buffer(own.size)
+        saved = self._buffer(self.kept) if self.kept else None
+        b, k = scratch.data_ptr(), 0 if saved is None else saved.data_ptr()
+        st = _raw_stream(x, None)
+        xt, xts = (k + self.xt, k + self.xts) if self.need_w else (None, None)
+        wt, wts = (k + self.wt, k + self.wts) if self.need_x else (None, None)
+        tx, tw = _type(x), _type(weight)
+        if G and self.need_w:
+            status = rlk_fp8_quantize_grouped(G, M, K, self.pe, x.data_ptr(), tx, self.sx, b + xq, ldk, b + xs, xt,
+                                              self.ldm, xts, st)
+        else:
+            status = rlk_fp8_quantize(M, K, x.data_ptr(), tx, self.sx, 1, b + xq, ldk, b + xs, xt, self.ldm, xts, st)
+        if G:
+            status = status or rlk_fp8_quantize_batch(G, rows, K, weight.data_ptr(), tw, self.sw, self.between, b + wq,
+                                                      ldk, rows * ldk, b + ws, wt, self.ldr, K * self.ldr, wts, st)
+        else:
+            status = status or rlk_fp8_quantize(rows, K, weight.data_ptr(), tw, self.sw, 128, b + wq, ldk, b + ws, wt,
+                                                self.ldr, wts, st)
+        if status:
+            check(status)
+        y, z, e = _new(x, M, self.N, torch.bfloat16), None, self.e
+        if (self.act or self.gated) and (self.need_x or self.need_w or self.need_b):
+            e.z_stride = -(-rows // 8) * 8
+            z = _new(x, M, rows, torch.bfloat16, e.z_stride)
+            e.z = z.data_ptr()
+        w = _fp8_workspace(x, st, None).data_ptr()
+        if G:
+            status = rlk_fp8_grouped_matmul(G, M, self.N, K, self.pe, b + xq, ldk, b + xs, b + wq, ldk, rows * ldk, b + ws,
+                                            e, y.data_ptr(), RLK_BF16, self.N, 1, w, st)
+        else:
+            status = rlk_fp8_matmul_act(M, self.N, K, b + xq, ldk, b + xs, b + wq, ldk, b + ws, e, y.data_ptr(),
+                                        RLK_BF16, self.N, w, st)
+        if status:
+            check(status)
+        return y, z, saved
+
+    def backward(self, dy, z, saved, ends):
+        """(dx, dweight, dbias), None where none is needed."""
+        torch = _t()
+        M, K, rows, G, rg, tiles = self.M, self.K, self.rows, self.G, self.rg, self.tiles
+        need_x, need_w, need_b = self.need_x, self.need_w, self.need_b
+        tx, tw = self.types
+        dx = _new(dy, M, K, tx) if need_x else None
+        dw = torch.empty(self.weight_shape, dtype=tw, device=dy.device) if need_w else None
+        db = torch.empty(self.weight_shape[:-1], dtype=self.tb, device=dy.device) if need_b else None
+        if M == 0 or rows == 0:
+            for t in (dx, dw, db):
+                if t is not None:
+                    t.zero_()
+            return dx, dw, db
+        R, N, sy = _matrix(dy, "dy", (torch.bfloat16, torch.float32))
+        if (R, N) != (M, self.N):
+            raise ValueError(f"dy is {list(dy.shape)}; the result is [{M}, {self.N}]")
+        pe = None if ends is None else ends.data_ptr()
+        own = _Places()
+        q, s = (own.take(M * self.ldr), own.take(4 * rg * M)) if need_x else (0, 0)
+        qt, sq = (own.take(rows * self.ldm), own.take(4 * tiles * rows)) if need_w else (0, 0)
+        part = own.take(4 * tiles * rows) if need_b else 0
+        scratch = self._buffer(own.size)
+        b = scratch.data_ptr()
+        q, s = (b + q, b + s) if need_x else (None, None)
+        qt, sq = (b + qt, b + sq) if need_w else (None, None)
+        st = _raw_stream(dy, None)
+        if z is None and not need_b and G:
+            status = rlk_fp8_quantize_grouped(G, M, rows, pe, dy.data_ptr(), _type(dy), sy, q, self.ldr, s, qt, self.ldm,
+                                              sq, st)
+        elif z is None and not need_b:
+            status = rlk_fp8_quantize(M, rows, dy.data_ptr(), _type(dy), sy, 1, q, self.ldr, s, qt, self.ldm, sq, st)
+        else:
+            status = rlk_fp8_act_grad(G, M, N, pe, dy.data_ptr(), _type(dy), sy, _ptr(z), 0 if z is None else z.stride(0),
+                                      self.act, self.gated, q, self.ldr, s, qt, self.ldm, sq, _ptr(db),
+                                      RLK_F32 if self.tb is torch.float32 else RLK_BF16, b + part if need_b else None, st)
+        if status:
+            check(status)
+        k = 0 if saved is None else saved.data_ptr()
+        w = _fp8_workspace(dy, st, None).data_ptr()
+        if need_x:
+            out, kind = dx.data_ptr(), _type(dx)
+            if G:
+                status = rlk_fp8_grouped_matmul(G, M, K, rows, pe, q, self.ldr, s, k + self.wt, self.ldr, K * self.ldr,
+                                                k + self.wts, None, out, kind, K, 1, w, st)
+            else:
+                status = rlk_fp8_matmul(M, K, rows, q, self.ldr, s, k + self.wt, self.ldr, k + self.wts, 128, out, kind, K,
+                                        0, w, st)
+        if need_w and not status:
+            out, kind = dw.data_ptr(), _type(dw)
+            if G:
+                status = rlk_fp8_grouped_dweight(G, M, rows, K, pe, qt, self.ldm, sq, k + self.xt, self.ldm, k + self.xts,
+                                                 out, kind, K, rows * K, 0, w, st)
+            else:
+                status = rlk_fp8_matmul(rows, K, M, qt, self.ldm, sq, k + self.xt, self.ldm, k + self.xts, 1, out, kind, K,
+                                        0, w, st)
+        if status:
+            check(status)
+        return dx, dw, db
 
 
 # ------------------------------------------------------------------ cross entropy over a large vocabulary

@@ -16,18 +16,18 @@ differentiable.
 and ``rlk_linear_ce_bwd``; ``Fp8Linear`` (``fp8_linear``) quantises with
 ``rlk_fp8_quantize`` and forms its output and both gradients with
 ``rlk_fp8_matmul``; ``Fp8Layer`` (``fp8_linear`` with a bias, an activation, a
-gate or a residual) and ``Fp8GroupedLayer`` (``fp8_grouped_linear``) with
-``rlk_fp8_matmul_act`` and ``rlk_fp8_act_grad``, ``rlk_fp8_grouped_matmul`` and
-``rlk_fp8_grouped_dweight``.
+gate or a residual, and ``fp8_grouped_linear``) runs ``rlk_fp8_matmul_act`` or
+``rlk_fp8_grouped_matmul``, ``rlk_fp8_act_grad`` and the products of the
+gradients.
 """
 import torch
 from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
-from . import (ACTIVATIONS, MASK_EXPLICIT, MASK_IGNORE_INDEX, REDUCE_MEAN, REDUCE_NONE, REDUCE_SUM, Contract,
-               fp8_act_grad, fp8_grouped_dweight, fp8_grouped_matmul, fp8_matmul, fp8_matmul_act, fp8_quantize,
-               fp8_quantize_both, fp8_quantize_grouped, linear_ce_bwd, linear_ce_contract, linear_ce_fwd, logp_bwd,
-               logp_fused_lmhead, logp_fused_lmhead_bwd, logp_fused_lmhead_bwd_kept, logp_fused_lmhead_keep, logp_fwd)
+from . import (MASK_EXPLICIT, MASK_IGNORE_INDEX, REDUCE_MEAN, REDUCE_NONE, REDUCE_SUM, Contract, Fp8LayerStep,
+               fp8_grouped_matmul, fp8_matmul, fp8_matmul_act, fp8_quantize, fp8_quantize_both, linear_ce_bwd,
+               linear_ce_contract, linear_ce_fwd, logp_bwd, logp_fused_lmhead, logp_fused_lmhead_bwd,
+               logp_fused_lmhead_bwd_kept, logp_fused_lmhead_keep, logp_fwd)
 
 _LOGIT_DTYPES = (torch.bfloat16, torch.int16)  # int16: BF16 bits viewed as integers
 
@@ -222,88 +222,29 @@ def _rows_of(dy):
 
 
 class Fp8Layer(torch.autograd.Function):
-    """y = act(x @ weight^T + bias) + residual in FP8.  z, the argument of the activation, is kept in BF16; the backward
-    forms dz, the sum of its rows for the bias, and its codes along the rows and along the tokens in one pass, then the
-    two products of Fp8Linear's."""
+    """y = act(x @ weight^T + bias) + residual in FP8, dense or (with ends) of rows that belong to groups, each with a
+    weight and a bias of its own.  z, the argument of the activation, is kept in BF16; the backward forms dz, the sum of
+    its rows for the bias, and its codes along the rows and along the tokens in one pass, then the two products of
+    Fp8Linear's (Fp8LayerStep makes the calls)."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, residual, activation, gated):
+    def forward(ctx, x, weight, bias, residual, ends, activation, gated):
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
-        plain = not gated and not ACTIVATIONS[activation]
-        xq, xs, xtq, xts = fp8_quantize_both(x) if need_w else (*fp8_quantize(x), None, None)
-        wq, ws, wtq, wts = fp8_quantize_both(weight, block_rows=128) if need_x else \
-            (*fp8_quantize(weight, block_rows=128), None, None)
-        keep = not plain and (need_x or need_w or need_b)
-        y = fp8_matmul_act(xq, xs, wq, ws, bias, activation, gated, residual, keep)
-        y, z = y if keep else (y, None)
-        ctx.save_for_backward(xtq, xts, wtq, wts, z)
-        ctx.types = [None if t is None else t.dtype for t in (x, weight, bias, residual)]
-        ctx.sizes = x.shape, weight.shape
-        ctx.layer = activation, gated
+        step = Fp8LayerStep(x, weight, bias, residual, ends, activation, gated, need_x, need_w, need_b)
+        y, z, saved = step.forward(x, weight)
+        ctx.save_for_backward(z, saved, ends)
+        ctx.step = step
+        ctx.residual = None if residual is None else residual.dtype
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        xtq, xts, wtq, wts, z = ctx.saved_tensors
-        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
-        tx, tw, tb, tr = ctx.types
-        dres = dy.to(tr) if need_r else None
-        dx = dw = db = None
-        if dy.shape[0] == 0:
-            x, w = ctx.sizes
-            dx = dy.new_zeros(x, dtype=tx) if need_x else None
-            dw = dy.new_zeros(w, dtype=tw) if need_w else None
-            db = dy.new_zeros(w[:1], dtype=tb) if need_b else None
-        elif need_x or need_w or need_b:
-            q, s, qt, st, db = fp8_act_grad(_rows_of(dy), z, *ctx.layer, rowwise=need_x, transpose=need_w,
-                                            bias_dtype=tb if need_b else None)
-            dx = fp8_matmul(q, s, wtq, wts, out_dtype=tx) if need_x else None
-            dw = fp8_matmul(qt, st, xtq, xts, b_block_rows=1, out_dtype=tw) if need_w else None
-        return dx, dw, db, dres, None, None
-
-
-class Fp8GroupedLayer(torch.autograd.Function):
-    """Fp8Layer for rows that belong to groups, each with a weight and a bias of its own."""
-
-    @staticmethod
-    def forward(ctx, x, weight, bias, ends, activation, gated):
-        need_x, need_w, need_b = ctx.needs_input_grad[:3]
-        plain = not gated and not ACTIVATIONS[activation]
-        xq, xs, xtq, xts = fp8_quantize_grouped(x, ends) if need_w else (*fp8_quantize(x), None, None)
-        wq, ws, wtq, wts = fp8_quantize_both(weight, block_rows=128) if need_x else \
-            (*fp8_quantize(weight, block_rows=128), None, None)
-        keep = not plain and (need_x or need_w or need_b)
-        y = fp8_grouped_matmul(xq, xs, wq, ws, ends, bias, activation, gated, keep)
-        y, z = y if keep else (y, None)
-        ctx.save_for_backward(xtq, xts, wtq, wts, z, ends)
-        ctx.types = x.dtype, weight.dtype, None if bias is None else bias.dtype
-        ctx.sizes = x.shape, weight.shape
-        ctx.layer = activation, gated
-        return y
-
-    @staticmethod
-    @once_differentiable
-    def backward(ctx, dy):
-        xtq, xts, wtq, wts, z, ends = ctx.saved_tensors
-        need_x, need_w, need_b = ctx.needs_input_grad[:3]
-        tx, tw, tb = ctx.types
-        x, w = ctx.sizes
-        dx = dw = db = None
-        if dy.shape[0] == 0:
-            dx = dy.new_zeros(x, dtype=tx) if need_x else None
-            dw = dy.new_zeros(w, dtype=tw) if need_w else None
-            db = dy.new_zeros(w[:2], dtype=tb) if need_b else None
-        else:
-            dy = _rows_of(dy)
-            if z is None and not need_b:
-                q, s, qt, st = fp8_quantize_grouped(dy, ends, need_x, need_w)
-            else:
-                q, s, qt, st, db = fp8_act_grad(dy, z, *ctx.layer, ends=ends, rowwise=need_x, transpose=need_w,
-                                                bias_dtype=tb if need_b else None)
-            dx = fp8_grouped_matmul(q, s, wtq, wts, ends, out_dtype=tx) if need_x else None
-            dw = fp8_grouped_dweight(qt, st, xtq, xts, ends, x[0], out_dtype=tw) if need_w else None
-        return dx, dw, db, None, None, None
+        dres = dy.to(ctx.residual) if ctx.needs_input_grad[3] else None
+        if not any(ctx.needs_input_grad[:3]):
+            return None, None, None, dres, None, None, None
+        z, saved, ends = ctx.saved_tensors
+        return *ctx.step.backward(_rows_of(dy), z, saved, ends), dres, None, None, None
 
 
 def fp8_linear(x, weight, bias=None, activation=None, gated=False, residual=None):
@@ -327,7 +268,7 @@ def fp8_linear(x, weight, bias=None, activation=None, gated=False, residual=None
         residual = residual if x.dim() == 2 else residual.reshape(-1, n)
         residual = residual if residual.stride(-1) == 1 else residual.contiguous()
     if _differentiated(*(t for t in (x, weight, bias, residual) if t is not None)):
-        y = Fp8Layer.apply(rows, weight, bias, residual, activation, bool(gated))
+        y = Fp8Layer.apply(rows, weight, bias, residual, None, activation, gated)
     else:
         y = fp8_matmul_act(*fp8_quantize(rows), *fp8_quantize(weight, block_rows=128), bias, activation, gated, residual)
     return y if x.dim() == 2 else y.reshape(*lead, n)
@@ -342,7 +283,7 @@ def fp8_grouped_linear(x, weight, ends, bias=None, activation=None, gated=False)
     without rows has zero gradients.
     """
     if _differentiated(*(t for t in (x, weight, bias) if t is not None)):
-        return Fp8GroupedLayer.apply(x, weight, bias, ends, activation, bool(gated))
+        return Fp8Layer.apply(x, weight, bias, None, ends, activation, gated)
     return fp8_grouped_matmul(*fp8_quantize(x), *fp8_quantize(weight, block_rows=128), ends, bias, activation, gated)
 
 
