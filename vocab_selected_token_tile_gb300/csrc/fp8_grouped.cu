@@ -7,21 +7,37 @@
 // load rows of the next group; they only reach rows of the accumulator that
 // are not stored.
 //
-// Which kernel: by the average number of rows a group, all the host knows.  Few
-// rows: the kernel that lays the weight's rows on the lanes, in blocks of 16,
-// 32 or 64 tokens; a group with more rows takes several blocks, which run next
+// Which kernel: by the average number of rows a group, all the host knows.
+// Measured for 64 groups of 4096 x 2048 (us; the weights' bytes take 79), rows
+// spread around the average as a router spreads them:
+//   rows a group                   4     8    12    16    24    32    48    64    96   128   160   192   256
+//   weight's rows on lanes, 16    84    88    93    92   111
+//                           32    84    87    89    89    94   100   125
+//                           64    91    96   100   101   105   108   125   151   204   245
+//   half tiles (128 rows)                          110   111   112   114   114   130   149   178   206   259
+//   tiles (256 rows)                               159   162   162   164   165   165   167   177   189   230
+// (16 groups of 2816 x 2048: 19.0, 20.6, 25.2 us for 4 rows; 22.0 and 21.5 for 16; 24.5, 28.9, 27.2 for 32; 36 and 41
+// for 128, 44 and 42 for 192).  On the lanes a group with more rows than a block takes several blocks, which run next
 // to each other, so that the weight comes from L2 after the first.
 #include "rlk_fp8_gemm.cuh"
 
 namespace rlk {
 namespace {
 
-// Rows of a block of few-row units, 0: tiles of CTA pairs.
-int block_rows_of(int64_t rows, int64_t groups) {
-    if (rows <= 16) return 16;
-    if (rows <= 6 * groups) return 16;
-    if (rows <= 14 * groups) return 32;
-    return rows <= 48 * groups || rows <= 64 ? 64 : 0;
+enum class Shape { kLanes16, kLanes32, kHalfTiles, kTiles };
+
+Shape shape_of(int64_t rows, int64_t groups) {
+    if (rows <= 10 * groups || rows <= 16) return Shape::kLanes16;
+    if (rows <= 36 * groups) return Shape::kLanes32;
+    return rows <= 152 * groups ? Shape::kHalfTiles : Shape::kTiles;
+}
+
+template <int KIND>
+rlk_status launch_group_tiles(const Ext8Params& p, const CUtensorMap& a, const CUtensorMap& b, int64_t tiles, int sms,
+                              cudaStream_t st) {
+    const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
+    return launch_clusters<gemm_kernel<false, KIND>>(2 * pairs, kGThreads, kGSmemOf<false, KIND>, 2, false, st, a, b, p,
+                                                     0, 0, 1);
 }
 
 }  // namespace
@@ -53,7 +69,9 @@ rlk_status launch_fp8_grouped_matmul(int64_t G, int64_t M, int64_t N, int64_t K,
     const int halves = gated ? 2 : 1;
     const int64_t live = G < M ? G : M;  // groups that have rows, at most
     CUtensorMap ta, tb;
-    if (const int nt = block_rows_of(M, G)) {
+    const Shape shape = shape_of(M, G);
+    if (shape == Shape::kLanes16 || shape == Shape::kLanes32) {
+        const int nt = shape == Shape::kLanes16 ? 16 : 32;
         p.NB = (int32_t)((N * halves + kSRows - 1) / kSRows);
         if (!make_map8(&ta, a, K, M, lda, (uint32_t)nt) ||
             !make_map_halves(&tb, b, K, N, halves, G, ldb, group, gated ? 32 : kSRows))
@@ -62,17 +80,18 @@ rlk_status launch_fp8_grouped_matmul(int64_t G, int64_t M, int64_t N, int64_t K,
         return gated ? launch_skinny_nt<false, kRowsGated>(nt, p, ta, tb, most, sms, stream)
                      : launch_skinny_nt<false, kRows>(nt, p, ta, tb, most, sms, stream);
     }
-    p.MB = 0;
+    const int rows = shape == Shape::kHalfTiles ? kGM : 2 * kGM;  // of a tile
     p.NB = (int32_t)((N * halves + kGN - 1) / kGN);
-    const int64_t tiles = (live + M / (2 * kGM) + 1) * p.NB;
-    p.band = band_of((M + 2 * kGM - 1) / (2 * kGM), K);
-    if (!make_map8(&ta, a, K, M, lda, kGM) || !make_map_halves(&tb, b, K, N, halves, G, ldb, group, kGN / 2))
+    p.band = band_of((M + 2 * kGM - 1) / (2 * kGM), K) * (2 * kGM / rows);
+    const int64_t tiles = (live + M / rows + 1) * p.NB;
+    if (!make_map8(&ta, a, K, M, lda, (uint32_t)rows / 2) ||
+        !make_map_halves(&tb, b, K, N, halves, G, ldb, group, kGN / 2))
         return fail(RLK_ERR_CUDA, "cuTensorMapEncodeTiled failed for an operand of the grouped fp8 product");
-    const int blocks = 2 * (int)(tiles < sms / 2 ? tiles : sms / 2);
-    return gated ? launch_clusters<gemm_kernel<false, kRowsGated>>(blocks, kGThreads, kGSmemOf<false, kRowsGated>, 2,
-                                                                   false, stream, ta, tb, p, 0, 0, 1)
-                 : launch_clusters<gemm_kernel<false, kRows>>(blocks, kGThreads, kGSmemOf<false, kRows>, 2, false,
-                                                              stream, ta, tb, p, 0, 0, 1);
+    if (shape == Shape::kHalfTiles)
+        return gated ? launch_group_tiles<kHalvesGated>(p, ta, tb, tiles, sms, stream)
+                     : launch_group_tiles<kHalves>(p, ta, tb, tiles, sms, stream);
+    return gated ? launch_group_tiles<kRowsGated>(p, ta, tb, tiles, sms, stream)
+                 : launch_group_tiles<kRows>(p, ta, tb, tiles, sms, stream);
 }
 
 rlk_status launch_fp8_grouped_dweight(int64_t G, int64_t rows, int64_t M, int64_t N, const int32_t* ends,

@@ -186,25 +186,25 @@ __device__ void init_scales(ScaleBars* b, int epilogue_warps) {
 }
 
 // The barriers of a CTA on its own (skinny_kernel).
-template <int STAGES>
+template <int STAGES, int ACCS>
 struct Bars8 {
     uint64_t full[STAGES];
     uint64_t empty[STAGES];
-    uint64_t tfull[2];
-    uint64_t tempty[2];
+    uint64_t tfull[ACCS];
+    uint64_t tempty[ACCS];
     ScaleBars sc;
     uint64_t drain;
     uint32_t tmem_addr;
     int abort_flag;
 };
 
-template <int STAGES>
-__device__ void init_bars8(Bars8<STAGES>* b, int epilogue_warps) {
+template <int STAGES, int ACCS>
+__device__ void init_bars8(Bars8<STAGES, ACCS>* b, int epilogue_warps) {
     for (int s = 0; s < STAGES; ++s) {
         mbar_init(smem_u32(&b->full[s]), 1);
         mbar_init(smem_u32(&b->empty[s]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < ACCS; ++i) {
         mbar_init(smem_u32(&b->tfull[i]), 1);
         mbar_init(smem_u32(&b->tempty[i]), epilogue_warps);
     }
@@ -230,9 +230,10 @@ struct Gemm8Params {
 // activation, residual); of rows that belong to groups, each with a B of its
 // own, and that epilogue; of operands whose K axis belongs to groups, each with
 // a C of its own.
-enum Kind8 : int { kPlain, kEpi, kEpiGated, kRows, kRowsGated, kDepth };
-__host__ __device__ constexpr bool gated_kind(int k) { return k == kEpiGated || k == kRowsGated; }
-__host__ __device__ constexpr bool rows_kind(int k) { return k == kRows || k == kRowsGated; }
+enum Kind8 : int { kPlain, kEpi, kEpiGated, kRows, kRowsGated, kHalves, kHalvesGated, kDepth };
+__host__ __device__ constexpr bool gated_kind(int k) { return k == kEpiGated || k == kRowsGated || k == kHalvesGated; }
+__host__ __device__ constexpr bool half_kind(int k) { return k == kHalves || k == kHalvesGated; }
+__host__ __device__ constexpr bool rows_kind(int k) { return k == kRows || k == kRowsGated || half_kind(k); }
 __host__ __device__ constexpr bool layer_kind(int k) { return k == kEpi || k == kEpiGated || rows_kind(k); }
 
 struct Ext8Params : Gemm8Params {
@@ -424,14 +425,26 @@ constexpr int kGScales = kGM + (BROWS ? kGN : 4);
 template <bool BROWS>
 constexpr size_t kGSmem = 1024 + (size_t)kGStages * (kGA + kGB) + 8 * kGOut +
                           (size_t)kGSlots * kGroups * kGScales<BROWS> * 4 + 1024;
+
+// A half tile (kHalves): 128 rows of A by 256 of B, of groups of few rows.  The
+// MMA takes M = 128, 64 rows of each CTA; a CTA's 128 lanes hold them twice, the
+// lower 64 the tile's first 128 columns and the upper 64 the others, in 128
+// columns of tensor memory.  So four accumulators are in flight, not two: from
+// one's completion to the next it is the hand-overs that take the time.
+__host__ __device__ constexpr int tile_rows(int k) { return half_kind(k) ? kGM : 2 * kGM; }  // of A, by a pair
+__host__ __device__ constexpr int stages_of(int k) { return half_kind(k) ? 6 : kGStages; }
+__host__ __device__ constexpr int accs_of(int k) { return half_kind(k) ? 4 : 2; }
 template <bool BROWS, int KIND>
-constexpr size_t kGSmemOf = kGSmem<BROWS> + (rows_kind(KIND) || KIND == kDepth ? sizeof(GroupTable) : 0);
+constexpr size_t kGSmemOf = kGSmem<BROWS> - (size_t)kGStages * (kGA + kGB) +
+                            (size_t)stages_of(KIND) * ((half_kind(KIND) ? kGA / 2 : kGA) + kGB) +
+                            (rows_kind(KIND) || KIND == kDepth ? sizeof(GroupTable) : 0);
+template <int STAGES, int ACCS>
 struct GemmBars {
-    PairBars<kGStages> pair;
+    PairBars<STAGES, ACCS> pair;
     uint64_t sfull[kGSlots], sempty[kGSlots];
 };
-static_assert(sizeof(GemmBars) <= 1024, "barriers fit their kilobyte");
-static_assert(kGSmemOf<true, kDepth> <= 232448, "shared memory of a CTA");
+static_assert(sizeof(GemmBars<6, 4>) <= 1024, "barriers fit their kilobyte");
+static_assert(kGSmemOf<true, kDepth> <= 232448 && kGSmemOf<false, kHalves> <= 232448, "shared memory of a CTA");
 
 constexpr int kGSplit = 4;  // pairs that share a tile at most: a cluster of eight CTAs
 constexpr int kTailSaves = 16;  // K groups that a launch of the last tiles has to save a pair
@@ -464,7 +477,7 @@ __device__ __forceinline__ Tile8 tile_at(const typename ParamsOf<KIND>::type& p,
         x.group = group_of(tab, p.G, t);
         t -= tab->first[x.group];
         x.row0 = tab->begin[x.group], x.end = tab->begin[x.group + 1];
-        MB = (x.end - x.row0 + 2 * kGM - 1) / (2 * kGM);
+        MB = (x.end - x.row0 + tile_rows(KIND) - 1) / tile_rows(KIND);
         if (x.group == p.G) x.k1 = k0;  // rows behind the groups: an empty sum
     }
     if constexpr (KIND == kDepth) {
@@ -473,7 +486,7 @@ __device__ __forceinline__ Tile8 tile_at(const typename ParamsOf<KIND>::type& p,
         x.k0 = tab->first[x.group], x.k1 = tab->first[x.group + 1];
     }
     tile_of(p, MB, t, mb, x.nb);
-    x.row0 += 2 * mb * kGM;
+    x.row0 += mb * tile_rows(KIND);
     return x;
 }
 
@@ -580,61 +593,63 @@ __device__ __forceinline__ float res_at(const Ext8Params& p, int64_t i) {
 // read once, then all of them by every lane through shared memory.  (Reading
 // them before the tile before was finished gained nothing, and registers of the
 // gated product's loop suffered: 331 -> 348 us at 8192 x 12288 x 4096.)
-template <bool GATED>
+// PAIRS: of columns a warp has, 64 or (of a half tile) 32; gated, half of them
+// the gate's.  col: the first of the result's; zcol: of B's rows, so of z's.
+template <bool GATED, int PAIRS>
 __device__ __forceinline__ void start_with_bias(const Ext8Params& p, unsigned char* out, int lane, const Tile8& t,
-                                                int part, float2 (&sum)[64]) {
+                                                int col, float2 (&sum)[PAIRS]) {
     if (p.rest && t.group == p.G) return;  // rows behind the groups: zeros
-    const int half = GATED ? lane >> 4 : 0;
-    const int col = t.nb * (GATED ? kGN / 2 : kGN) + part * (GATED ? 64 : 128) + 4 * (GATED ? lane & 15 : lane);
-    const int64_t at = (int64_t)t.group * (GATED ? 2 : 1) * p.N + (half ? p.N : 0) + col;
-    float b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = col + i < p.N ? bias_at(p, at + i) : 0.f;
-    __syncwarp();
-    reinterpret_cast<float4*>(out)[lane] = make_float4(b[0], b[1], b[2], b[3]);
+    constexpr int kEach = PAIRS / 16, kOf = GATED ? 16 : 32;  // columns a lane, lanes of a half
+    const int half = lane / kOf, c = col + kEach * (lane % kOf);
+    const int64_t at = (int64_t)t.group * (GATED ? 2 : 1) * p.N + (half ? p.N : 0) + c;
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < kEach; ++i)
+        reinterpret_cast<float*>(out)[kEach * lane + i] = c + i < p.N ? bias_at(p, at + i) : 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < PAIRS / 2; ++i) {
         const float4 x = reinterpret_cast<const float4*>(out)[i];
         sum[2 * i] = make_float2(x.x, x.y), sum[2 * i + 1] = make_float2(x.z, x.w);
     }
     __syncwarp();
 }
 
-// The epilogue of a warp's 32 rows x 128 columns of B's rows, a row a lane: the
-// columns are 128 of the result, or (gated) 64 of the gate and the same 64 of
-// the other half, which the loads of B have laid side by side.
-template <bool GATED>
-__device__ __forceinline__ void finish_rows(const Ext8Params& p, unsigned char* out, int lane, const Tile8& t,
-                                            int part, int64_t row0, float2 (&sum)[64]) {
+// The epilogue of a warp's 32 rows and their PAIRS pairs of columns, a row a
+// lane; gated: the first half of them is the gate's and the second the other
+// half's same columns, which the loads of B have laid side by side.
+template <bool GATED, int PAIRS>
+__device__ __forceinline__ void finish_rows(const Ext8Params& p, unsigned char* out, int lane, const Tile8& t, int col0,
+                                            int64_t row0, float2 (&sum)[PAIRS]) {
     const bool behind = p.rest && t.group == p.G;  // rows behind the groups: zeros
-    const int col0 = t.nb * (GATED ? kGN / 2 : kGN) + part * (GATED ? 64 : 128);
+    constexpr int kOwn = GATED ? PAIRS / 2 : PAIRS, kAt = kOwn < 32 ? kOwn : 32;  // pairs of a half, and at a time
+    const int N = kOwn < 32 ? min(p.N, col0 + 2 * kOwn) : p.N;  // a chunk of BF16 is 64 columns
     if (p.z && !behind) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            store_chunk<false, false>(Dest{p.z + (GATED && h ? p.N : 0), p.ldz, t.end, p.N, p.z_vec, 0}, out, lane,
-                                      row0, col0 + (GATED ? 0 : 64 * h), sum + 32 * h);
+        for (int h = 0; h < PAIRS / kAt; ++h)
+            store_chunk<false, false>(Dest{p.z + (GATED && h ? p.N : 0), p.ldz, t.end, N, p.z_vec, 0}, out, lane, row0,
+                                      col0 + (GATED ? 0 : 2 * kAt * h), sum + kAt * h);
     }
-    act_pairs<0, GATED ? 32 : 64>(sum, p.act);
+    act_pairs<0, kOwn>(sum, p.act);
     if (GATED) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) sum[i] = fmul2(sum[i], sum[32 + i]);
+        for (int i = 0; i < kOwn; ++i) sum[i] = fmul2(sum[i], sum[kOwn + i]);
     }
-    const Dest d = dest_of(p, t.end);
+    const Dest d{p.c, p.ldc, t.end, N, p.vec, 0};
 #pragma unroll
-    for (int h = 0; h < (GATED ? 1 : 2); ++h) {
-        const int col = col0 + 64 * h;
+    for (int h = 0; h < kOwn / kAt; ++h) {
+        const int col = col0 + 2 * kAt * h;
         if (p.res) {
             if (p.res_f32)
-                add_residual<true>(p, out, lane, row0, t.end, col, sum + 32 * h);
+                add_residual<true>(p, out, lane, row0, t.end, col, sum + kAt * h);
             else
-                add_residual<false>(p, out, lane, row0, t.end, col, sum + 32 * h);
+                add_residual<false>(p, out, lane, row0, t.end, col, sum + kAt * h);
         }
         if (p.c_f32) {
-            store_chunk<true, false>(d, out, lane, row0, col, sum + 32 * h);
-            store_chunk<true, false>(d, out, lane, row0, col + 32, sum + 32 * h + 16);
+            store_chunk<true, false>(d, out, lane, row0, col, sum + kAt * h);
+            if (kAt == 32) store_chunk<true, false>(d, out, lane, row0, col + 32, sum + kAt * h + 16);
         } else {
-            store_chunk<false, false>(d, out, lane, row0, col, sum + 32 * h);
+            store_chunk<false, false>(d, out, lane, row0, col, sum + kAt * h);
         }
     }
 }
@@ -650,6 +665,10 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 const __grid_constant__ typename ParamsOf<KIND>::type p, const int tile0, const int tiles_given,
                 const int split_given) {
     constexpr bool kGrouped = rows_kind(KIND) || KIND == kDepth, kLayer = layer_kind(KIND), kGated = gated_kind(KIND);
+    constexpr bool kHalf = half_kind(KIND);
+    constexpr int kStages = stages_of(KIND), kAccs = accs_of(KIND), kAcc = 512 / kAccs;  // columns of an accumulator
+    constexpr int kOwn = tile_rows(KIND) / 2, kPairs = kHalf ? 32 : 64;  // a CTA's rows of A, a thread's pairs of sums
+    constexpr uint32_t kA = kOwn * kGK;
     static_assert(!BROWS || !kLayer, "an epilogue's B has scales by the block");
     const int split = kGrouped ? 1 : split_given;
     extern __shared__ unsigned char smem_raw[];
@@ -657,11 +676,11 @@ __global__ void __launch_bounds__(kGThreads, 1)
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* sA = smem;
-    unsigned char* sB = smem + kGStages * kGA;
-    unsigned char* sOut = sB + kGStages * kGB;
+    unsigned char* sB = smem + kStages * kA;
+    unsigned char* sOut = sB + kStages * kGB;
     float* scales = reinterpret_cast<float*>(sOut + 8 * kGOut);
-    auto* all = reinterpret_cast<GemmBars*>(scales + kGSlots * kGroups * kGScales<BROWS>);
-    PairBars<kGStages>* bars = &all->pair;
+    auto* all = reinterpret_cast<GemmBars<kStages, kAccs>*>(scales + kGSlots * kGroups * kGScales<BROWS>);
+    PairBars<kStages, kAccs>* bars = &all->pair;
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int place = (int)cluster_ctarank(), rank = place & 1, leader = place & ~1;
     const uint16_t both = (uint16_t)(3 << leader);
@@ -675,7 +694,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             mbar_init(smem_u32(&all->sempty[i]), 8);
         }
     }
-    if constexpr (rows_kind(KIND)) groups_build<kGThreads>(tab, p.ends, p.G, p.M, 2 * kGM, p.NB, p.rest);
+    if constexpr (rows_kind(KIND)) groups_build<kGThreads>(tab, p.ends, p.G, p.M, tile_rows(KIND), p.NB, p.rest);
     if constexpr (KIND == kDepth) groups_build<kGThreads>(tab, p.ends, p.G, p.deep, kGK, 1, false);
     const uint32_t tmem = pair_begin(bars, warp, 8);
     int* ab = &bars->abort_flag;
@@ -695,15 +714,15 @@ __global__ void __launch_bounds__(kGThreads, 1)
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
                 const Tile8 x = tile(t);
-                const int a_row = x.row0 + rank * kGM, b_row = x.nb * kGN + rank * (kGN / 2);
+                const int a_row = x.row0 + rank * kOwn, b_row = x.nb * kGN + rank * (kGN / 2);
                 // a CTA without a row of its own loads none: its rows of the accumulator are not used
                 const bool mine = a_row < x.end;
                 for (int kb = x.k0; kb < x.k1; ++kb) {
                     if (!(ok = pipe_wait_warp(ab, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, p.w))) break;
                     if (one) {
                         const uint32_t fb = full0 + r.slot * 8;
-                        pair_arm(fb, smem_u32(&bars->full[r.slot]), rank, kGB + (mine ? kGA : 0));
-                        if (mine) tma_load_2d_pair(smem_u32(sA + r.slot * kGA), &tmA, kb * kGK, a_row, fb);
+                        pair_arm(fb, smem_u32(&bars->full[r.slot]), rank, kGB + (mine ? kA : 0));
+                        if (mine) tma_load_2d_pair(smem_u32(sA + r.slot * kA), &tmA, kb * kGK, a_row, fb);
                         if constexpr (kLayer)  // gated: half as many rows of each half
                             tma_load_4d_pair(smem_u32(sB + r.slot * kGB), &tmB, kb * kGK, kGated ? b_row / 2 : b_row,
                                              0, x.group, fb);
@@ -711,7 +730,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                             tma_load_2d_pair(smem_u32(sB + r.slot * kGB), &tmB, kb * kGK, b_row, fb);
                     }
                     ++issued;
-                    r.next(kGStages);
+                    r.next(kStages);
                 }
             }
             pair_end_copies(bars, r, one, issued, ok, p.w);
@@ -719,7 +738,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             // ------------------------------------------------ MMA issuer of the pair
             const bool one = elect_one();
             const uint64_t da = smem_desc_sw128(smem_u32(sA)), db = smem_desc_sw128(smem_u32(sB));
-            const uint32_t idesc = idesc_e4m3_f32(2 * kGM, kGN);
+            const uint32_t idesc = idesc_e4m3_f32(tile_rows(KIND), kGN);
             Ring r, acc;
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
@@ -732,14 +751,14 @@ __global__ void __launch_bounds__(kGThreads, 1)
                     if (one) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_e4m3_pair(tmem + (uint32_t)(acc.slot * kGN), da + ((r.slot * kGA + kk * 32) >> 4),
+                            umma_e4m3_pair(tmem + (uint32_t)(acc.slot * kAcc), da + ((r.slot * kA + kk * 32) >> 4),
                                            db + ((r.slot * kGB + kk * 32) >> 4), idesc, kk != 0);
                         umma_commit_pair(smem_u32(&bars->tfull[acc.slot]), both);
                         umma_commit_pair(smem_u32(&bars->empty[r.slot]), both);
                     }
                     __syncwarp();
-                    r.next(kGStages);
-                    acc.next(2);
+                    r.next(kStages);
+                    acc.next(kAccs);
                 }
             }
             pair_end_mmas(bars, acc, one, ok, p.w, both);
@@ -749,7 +768,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step) {
                 const Tile8 x = tile(t);
-                const int row = x.row0 + rank * kGM + lane, col = x.nb * kGN + lane;
+                const int row = x.row0 + rank * kOwn + lane, col = x.nb * kGN + lane;
                 for (int kg = x.k0; kg < x.k1; kg += kGroups) {
                     ok = pipe_wait_warp(ab, smem_u32(&all->sempty[r.slot]), r.phase ^ 1u, p.w);
                     if (!ok) break;
@@ -758,9 +777,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
                         // operands out)
                         if (p.res && kg == x.k0 && split == 1) {
                             const int cols = kGated ? kGN / 2 : kGN, at = x.nb * cols, size = p.res_f32 ? 4 : 2;
-                            const int top = x.row0 + rank * kGM, pieces = (min(cols, p.N - at) * size + 127) / 128;
+                            const int top = x.row0 + rank * kOwn, pieces = (min(cols, p.N - at) * size + 127) / 128;
                             const char* src = static_cast<const char*>(p.res) + ((int64_t)top * p.ldr + at) * size;
-                            for (int i = lane; i < min(kGM, x.end - top) * pieces; i += 32)
+                            for (int i = lane; i < min(kOwn, x.end - top) * pieces; i += 32)
                                 prefetch_l2(src + i / pieces * p.ldr * size + i % pieces * 128);
                         }
                     }
@@ -769,7 +788,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                     if constexpr (rows_kind(KIND)) b += x.group * p.sb_g;
                     for (int kb = kg; kb < min(kg + kGroups, x.k1); ++kb) {
 #pragma unroll
-                        for (int i = 0; i < kGM; i += 32)
+                        for (int i = 0; i < kOwn; i += 32)
                             cp_async4(dst + i * 4, a + (row + i < p.M ? row + i : 0), row + i < p.M);
                         if (BROWS) {
 #pragma unroll
@@ -801,16 +820,21 @@ __global__ void __launch_bounds__(kGThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int quarter = warp & 3, part = (warp - 4) >> 2;  // 32 rows, and 128 of the tile's columns
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        // this warp's 32 of the CTA's rows, its 128 of the tile's columns, and (half) which 64 of those
+        const int rows32 = kHalf ? quarter & 1 : quarter, side = kHalf ? quarter >> 1 : part;
         unsigned char* out = sOut + (warp - 4) * kGOut;
         const uint32_t done = mapa_shared(smem_u32(&bars->tempty[0]), (uint32_t)leader);
         Ring acc, sc;
         bool ok = first < tiles, ready = false;
+        auto first_column = [&](const Tile8& x) {  // of the result, of this warp's
+            return x.nb * (kGated ? kGN / 2 : kGN) + side * (kGated ? 64 : 128) + (kHalf ? part * (kGated ? 32 : 64) : 0);
+        };
         for (int t = first; ok && t < tiles; t += step) {
-            float2 sum[64];
+            float2 sum[kPairs];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) sum[i] = make_float2(0.f, 0.f);
+            for (int i = 0; i < kPairs; ++i) sum[i] = make_float2(0.f, 0.f);
             if constexpr (kLayer)
-                if (p.bias && split == 1) start_with_bias<kGated>(p, out, lane, tile(t), part, sum);
+                if (p.bias && split == 1) start_with_bias<kGated, kPairs>(p, out, lane, tile(t), first_column(tile(t)), sum);
             const float* s = nullptr;
             const Tile8 x = tile(t);
             for (int kb = x.k0; kb < x.k1; ++kb) {
@@ -824,29 +848,31 @@ __global__ void __launch_bounds__(kGThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) f[i] = s[quarter * 32 + i * 8 + (lane >> 2)];
                 } else {
-                    f[0] = __fmul_rn(s[quarter * 32 + lane], s[kGM + part]);
-                    f[1] = kGated ? __fmul_rn(s[quarter * 32 + lane], s[kGM + 2 + part]) : f[0];
+                    f[0] = __fmul_rn(s[rows32 * 32 + lane], s[kGM + side]);
+                    f[1] = kGated ? __fmul_rn(s[rows32 * 32 + lane], s[kGM + 2 + side]) : f[0];
                 }
                 if (!ready) ok = ok && pipe_wait(ab, smem_u32(&bars->tfull[acc.slot]), acc.phase, p.w);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 // 32 columns at a time, the next 32 under way while these are summed
-                const uint32_t t0 = tmem + lane_base + (uint32_t)(acc.slot * kGN + part * 128);
+                // half: 64 of the lanes' 128 columns, or (gated) 32 of the gate's 64 and the same of the other half's
+                constexpr int kChunks = kPairs / 16, kApart = kHalf && kGated ? 64 : 32;
+                const uint32_t t0 = tmem + lane_base + (uint32_t)(acc.slot * kAcc + part * (kHalf ? kGated ? 32 : 64 : 128));
                 uint32_t v[2][32];
                 BROWS ? tmem_ld_frag_issue(t0, v[0]) : tmem_ld32_issue(t0, v[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < kChunks; ++c) {
                     tmem_wait32(v[c & 1]);
-                    if (c < 3) {
-                        BROWS ? tmem_ld_frag_issue(t0 + (c + 1) * 32, v[(c + 1) & 1])
-                              : tmem_ld32_issue(t0 + (c + 1) * 32, v[(c + 1) & 1]);
+                    if (c < kChunks - 1) {
+                        BROWS ? tmem_ld_frag_issue(t0 + (c + 1) * kApart, v[(c + 1) & 1])
+                              : tmem_ld32_issue(t0 + (c + 1) * kApart, v[(c + 1) & 1]);
                     } else {
                         // the accumulator is free again; ask for the next one before this one's last sums
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_remote(done + acc.slot * 8);
-                        acc.next(2);
+                        acc.next(kAccs);
                         ready = mbar_test_wait(smem_u32(&bars->tfull[acc.slot]), acc.phase);  // must not suspend
                     }
                     if (BROWS) {
@@ -868,7 +894,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                         for (int i = 0; i < 16; ++i)
                             sum[c * 16 + i] = ffma2(make_float2(__uint_as_float(v[c & 1][2 * i]),
                                                                 __uint_as_float(v[c & 1][2 * i + 1])),
-                                                    make_float2(f[c >> 1], f[c >> 1]), sum[c * 16 + i]);
+                                                    make_float2(f[2 * c / kChunks], f[2 * c / kChunks]), sum[c * 16 + i]);
                     }
                 }
                 s += kGScales<BROWS>;
@@ -879,7 +905,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 }
             }
             if (!ok) break;
-            if (split > 1) {
+            if constexpr (!kHalf) if (split > 1) {
                 // every load has been consumed, so the ring's memory takes the partial sums [128][256], a row's
                 // pitch 260 for the banks
                 float* red = reinterpret_cast<float*>(sA) + (quarter * 32) * kRedPitch + part * 128;
@@ -900,9 +926,9 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 }
                 break;
             }
-            const int64_t row0 = (int64_t)x.row0 + rank * kGM + quarter * 32;
+            const int64_t row0 = (int64_t)x.row0 + rank * kOwn + rows32 * 32;
             if constexpr (kLayer) {
-                if (row0 < x.end) finish_rows<kGated>(p, out, lane, x, part, row0, sum);
+                if (row0 < x.end) finish_rows<kGated, kPairs>(p, out, lane, x, first_column(x), row0, sum);
             } else {
                 const int col0 = x.nb * kGN + part * 128;
                 Dest d = dest_of(p, p.M);
@@ -920,7 +946,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             }
         }
     }
-    if (split > 1) {
+    if constexpr (!kHalf) if (split > 1) {
         // This CTA adds up its share of the rows, the pairs' sums in order.
         cluster_sync_all();
         const bool failed = *reinterpret_cast<volatile int*>(ab) != 0;
@@ -1056,7 +1082,7 @@ __device__ __forceinline__ void finish_one(const Ext8Params& p, int64_t row, int
 // Sixteen rows at a time, which bounds the registers.
 template <int NT, bool GATED>
 __device__ __forceinline__ void finish_lanes(const Ext8Params& p, const Unit8& x, int quarter, int lane,
-                                             const float (&sum)[NT]) {
+                                             const float2 (&sum)[NT / 2]) {
     const bool behind = p.rest && x.group == p.G;  // rows behind the groups: zeros
     const int half = GATED ? lane >> 4 : 0;
     const int col = GATED ? x.nb * 64 + quarter * 16 + (lane & 15) : x.nb * 128 + quarter * 32 + lane;
@@ -1071,7 +1097,7 @@ __device__ __forceinline__ void finish_lanes(const Ext8Params& p, const Unit8& x
         float2 v[8], u[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] = fadd2(make_float2(sum[r0 + 2 * i], sum[r0 + 2 * i + 1]), make_float2(b, b));
+            v[i] = fadd2(sum[r0 / 2 + i], make_float2(b, b));
         if (p.z && in && !behind) {
             uint16_t* z = p.z + (int64_t)(x.row0 + r0) * p.ldz + zc;
 #pragma unroll
@@ -1127,13 +1153,17 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     using S = Skinny<NT>;
     constexpr bool kExt = KIND != kPlain, kGated = gated_kind(KIND);
     static_assert(!BROWS || !kExt, "an epilogue's B has scales by the block");
+    // A layer's accumulators are four: with fewer CTAs than the device holds, the hand-overs of two are what a CTA waits
+    // for (37 x 4096 to 2 x 12288 gated: 28.4 us with two, XX with four).
+    constexpr int kAccs = kExt ? 4 : 2;
+    constexpr uint32_t kTmem = kExt ? (uint32_t)kAccs * NT : S::kTmem;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem =
         reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char* sW = smem;
     unsigned char* sX = smem + S::kStages * S::kW;
     float* scales = reinterpret_cast<float*>(sX + S::kStages * S::kX);
-    auto* bars = reinterpret_cast<Bars8<S::kStages>*>(scales + kScaleStages * S::kScale);
+    auto* bars = reinterpret_cast<Bars8<S::kStages, kAccs>*>(scales + kScaleStages * S::kScale);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto* tab = reinterpret_cast<GroupTable*>(reinterpret_cast<unsigned char*>(bars) + 1024);
     const int rank = split > 1 ? (int)cluster_ctarank() : 0;
@@ -1143,7 +1173,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     if (threadIdx.x == 0) init_bars8(bars, 4);
     if constexpr (rows_kind(KIND)) groups_build<kSThreads>(tab, p.ends, p.G, p.M, NT, p.NB, p.rest);
     if (warp == 1) {
-        tmem_alloc(smem_u32(&bars->tmem_addr), S::kTmem);
+        tmem_alloc(smem_u32(&bars->tmem_addr), kTmem);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -1156,6 +1186,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     if constexpr (rows_kind(KIND)) tiles = tab->first[p.G + 1];
     auto unit = [&](int t) { return unit_at<NT, KIND>(p, tab, t, k0, k1); };
     float sum[NT];  // epilogue: this thread's row of B against the NT rows of A
+    float2 pairs[kExt ? NT / 2 : 1];
 
     if (warp == 0) {
         if (lane == 0) {
@@ -1207,7 +1238,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
                     umma_commit(smem_u32(&bars->empty[r.slot]));
                     umma_commit(smem_u32(&bars->tfull[acc.slot]));
                     r.next(S::kStages);
-                    acc.next(2);
+                    acc.next(kAccs);
                 }
             }
             umma_commit(smem_u32(&bars->drain));
@@ -1252,6 +1283,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
         for (int t = first; ok && t < tiles; t += step) {
 #pragma unroll
             for (int i = 0; i < NT; ++i) sum[i] = 0.f;
+            for (float2& x : pairs) x = make_float2(0.f, 0.f);
             const Unit8 x = unit(t);
             const int half = kGated ? lane >> 4 : 0;  // of B that this lane's row is of
             for (int kb = x.k0; kb < x.k1; ++kb) {
@@ -1274,19 +1306,32 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&bars->tempty[acc.slot]));
                     }
+                    if constexpr (kExt) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sum[c * 16 + i] = __fmaf_rn(__uint_as_float(v[c & 1][i]), __fmul_rn(s[c * 16 + i], sb),
-                                                    sum[c * 16 + i]);
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(s + c * 16 + i);
+                            const float2 lo = fmul2(make_float2(f.x, f.y), make_float2(sb, sb));
+                            const float2 hi = fmul2(make_float2(f.z, f.w), make_float2(sb, sb));
+                            const uint32_t* w = &v[c & 1][i];
+                            float2* d = pairs + (c * 16 + i) / 2;
+                            d[0] = ffma2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), lo, d[0]);
+                            d[1] = ffma2(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), hi, d[1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            sum[c * 16 + i] = __fmaf_rn(__uint_as_float(v[c & 1][i]), __fmul_rn(s[c * 16 + i], sb),
+                                                        sum[c * 16 + i]);
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->sc.empty[sc.slot]));
-                acc.next(2);
+                acc.next(kAccs);
                 sc.next(kScaleStages);
             }
             if (!ok || split > 1) break;  // a split launch has one tile a cluster, added up below
             if constexpr (kExt) {
-                finish_lanes<NT, kGated>(p, x, quarter, lane, sum);
+                finish_lanes<NT, kGated>(p, x, quarter, lane, pairs);
                 continue;
             }
             const int col = t * kSRows + row_in;
@@ -1312,7 +1357,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
         __syncthreads();
         if (warp >= 4) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) red[i * kSRows + row_in] = sum[i];
+            for (int i = 0; i < NT; ++i) red[i * kSRows + row_in] = !kExt ? sum[i] : i & 1 ? pairs[i / 2].y : pairs[i / 2].x;
         }
         cluster_sync_all();
         const bool failed = *reinterpret_cast<volatile int*>(ab) != 0;
@@ -1366,7 +1411,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, S::kTmem);
+        tmem_dealloc(tmem, kTmem);
     }
 }
 
@@ -1507,11 +1552,10 @@ rlk_status launch_skinny(const typename ParamsOf<KIND>::type& p, const CUtensorM
 template <bool BROWS, int KIND>
 rlk_status launch_skinny_nt(int nt, const typename ParamsOf<KIND>::type& p, const CUtensorMap& a,
                             const CUtensorMap& b, int64_t most, int sms, cudaStream_t st) {
-    switch (nt) {
-        case 16: return launch_skinny<16, BROWS, KIND>(p, a, b, most, sms, st);
-        case 32: return launch_skinny<32, BROWS, KIND>(p, a, b, most, sms, st);
-        default: return launch_skinny<64, BROWS, KIND>(p, a, b, most, sms, st);
-    }
+    if (nt == 16) return launch_skinny<16, BROWS, KIND>(p, a, b, most, sms, st);
+    if constexpr (!rows_kind(KIND))  // of groups, more rows a group take half tiles
+        if (nt == 64) return launch_skinny<64, BROWS, KIND>(p, a, b, most, sms, st);
+    return launch_skinny<32, BROWS, KIND>(p, a, b, most, sms, st);
 }
 
 // The device's SMs, for a launch; 0 and a reason if they cannot be had.

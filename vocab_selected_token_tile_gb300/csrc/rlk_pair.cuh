@@ -58,12 +58,13 @@ __device__ __forceinline__ bool pipe_wait_warp(int* abort_flag, uint32_t bar, ui
     return __all_sync(0xFFFFFFFFu, pipe_wait(abort_flag, bar, parity, w));
 }
 
-template <int STAGES>
+// ACCS: accumulators in flight.
+template <int STAGES, int ACCS = 2>
 struct PairBars {
     uint64_t full[STAGES];   // the even CTA's count both producers' arrivals and copies
     uint64_t empty[STAGES];
-    uint64_t tfull[2];
-    uint64_t tempty[2];      // the even CTA's count both CTAs' epilogue warps
+    uint64_t tfull[ACCS];
+    uint64_t tempty[ACCS];   // the even CTA's count both CTAs' epilogue warps
     uint64_t drain;
     uint64_t issued;         // stages that this CTA's producer has issued
     uint32_t tmem_addr;
@@ -71,13 +72,13 @@ struct PairBars {
     uint32_t drained;        // the issuer has committed on `drain`
 };
 
-template <int STAGES>
-__device__ void pair_init(PairBars<STAGES>* b, int epilogue_warps) {
+template <int STAGES, int ACCS>
+__device__ void pair_init(PairBars<STAGES, ACCS>* b, int epilogue_warps) {
     for (int s = 0; s < STAGES; ++s) {
         mbar_init(smem_u32(&b->full[s]), 2);
         mbar_init(smem_u32(&b->empty[s]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < ACCS; ++i) {
         mbar_init(smem_u32(&b->tfull[i]), 1);
         mbar_init(smem_u32(&b->tempty[i]), 2 * epilogue_warps);
     }
@@ -90,8 +91,8 @@ __device__ void pair_init(PairBars<STAGES>* b, int epilogue_warps) {
 
 // Start and end of a pair's kernel, by all threads of all CTAs of the cluster:
 // all 512 columns of tensor memory are the pair's in between.
-template <int STAGES>
-__device__ __forceinline__ uint32_t pair_begin(PairBars<STAGES>* bars, int warp, int epilogue_warps) {
+template <int STAGES, int ACCS>
+__device__ __forceinline__ uint32_t pair_begin(PairBars<STAGES, ACCS>* bars, int warp, int epilogue_warps) {
     if (threadIdx.x == 0) pair_init(bars, epilogue_warps);
     if (warp == 1) {
         tmem_alloc_pair(smem_u32(&bars->tmem_addr), 512);
@@ -115,8 +116,8 @@ __device__ __forceinline__ void pair_arm(uint32_t fb, uint32_t local, int rank, 
 
 // The end of a producer (its whole warp; r: its position, one: the thread that
 // issued `issued` stages, ok: no wait has expired).
-template <int STAGES>
-__device__ __forceinline__ void pair_end_copies(PairBars<STAGES>* bars, Ring r, bool one, uint64_t issued,
+template <int STAGES, int ACCS>
+__device__ __forceinline__ void pair_end_copies(PairBars<STAGES, ACCS>* bars, Ring r, bool one, uint64_t issued,
                                                 bool ok, const PipeWait& w) {
     for (int j = 0; ok && j < STAGES; ++j) {
         ok = pipe_wait_warp(&bars->abort_flag, smem_u32(&bars->empty[r.slot]), r.phase ^ 1u, w);
@@ -127,12 +128,12 @@ __device__ __forceinline__ void pair_end_copies(PairBars<STAGES>* bars, Ring r, 
 
 // The end of the issuer: every MMA issued so far has completed.  acc: its
 // position; one: the thread that issued them.
-template <int STAGES>
-__device__ __forceinline__ void pair_end_mmas(PairBars<STAGES>* bars, Ring acc, bool one, bool ok, const PipeWait& w,
+template <int STAGES, int ACCS>
+__device__ __forceinline__ void pair_end_mmas(PairBars<STAGES, ACCS>* bars, Ring acc, bool one, bool ok, const PipeWait& w,
                                               uint16_t mask = 3) {
-    for (int i = 0; ok && i < 2; ++i) {
+    for (int i = 0; ok && i < ACCS; ++i) {
         ok = pipe_wait_warp(&bars->abort_flag, smem_u32(&bars->tempty[acc.slot]), acc.phase ^ 1u, w);
-        acc.next(2);
+        acc.next(ACCS);
     }
     if (ok) return;
     if (one) {
@@ -145,8 +146,8 @@ __device__ __forceinline__ void pair_end_mmas(PairBars<STAGES>* bars, Ring acc, 
 
 // All CTAs have met and a wait of one of them has expired: the copies and the
 // commits still under way arrive before any CTA leaves.
-template <int STAGES>
-__device__ __noinline__ void pair_give_up(PairBars<STAGES>* bars, uint32_t* status) {
+template <int STAGES, int ACCS>
+__device__ __noinline__ void pair_give_up(PairBars<STAGES, ACCS>* bars, uint32_t* status) {
     const PipeWait w{status, 0};
     const int warp = warp_index();
     const uint32_t place = cluster_ctarank(), rank = place & 1u, even = place & ~1u;
@@ -163,8 +164,8 @@ __device__ __noinline__ void pair_give_up(PairBars<STAGES>* bars, uint32_t* stat
     cluster_sync_all();
 }
 
-template <int STAGES>
-__device__ __forceinline__ void pair_end(PairBars<STAGES>* bars, uint32_t tmem, int warp, const PipeWait& w) {
+template <int STAGES, int ACCS>
+__device__ __forceinline__ void pair_end(PairBars<STAGES, ACCS>* bars, uint32_t tmem, int warp, const PipeWait& w) {
     volatile int* flag = &bars->abort_flag;
     tc_fence_before();
     if (*flag) {  // the thread that set it is among those that see it here
