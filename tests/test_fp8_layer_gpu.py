@@ -105,12 +105,10 @@ def test_what_is_left_out(built, M, residual, bias):
         check_layer(M, 333, 260, "relu", False, bias, residual, out)
 
 
-def test_without_an_epilogue_it_is_the_product(built):
+def test_without_an_epilogue(built):
     for M, N, K in ((5, 300, 700), (64, 4096, 1024), (400, 1300, 2000), (2100, 2500, 300)):
-        qa, sa, qb, sb = operands(M, N, K, 3)
-        for dtype in (torch.bfloat16, torch.float32):
-            assert torch.equal(rlk.fp8_matmul_act(qa, sa, qb, sb, out_dtype=dtype),
-                               rlk.fp8_matmul(qa, sa, qb, sb, out_dtype=dtype))
+        for out in ("bf16", "f32"):
+            check_layer(M, N, K, out=out)
 
 
 def test_special_arguments_of_the_activations(built):

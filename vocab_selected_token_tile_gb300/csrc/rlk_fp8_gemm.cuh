@@ -448,6 +448,9 @@ static_assert(kGSmemOf<true, kDepth> <= 232448 && kGSmemOf<false, kHalves> <= 23
 
 constexpr int kGSplit = 4;  // pairs that share a tile at most: a cluster of eight CTAs
 constexpr int kTailSaves = 16;  // K groups that a launch of the last tiles has to save a pair
+// and with an epilogue, whose code the launch fetches anew: 4096 x 4096 x 4096 66.9 us in one launch, 72.2 in two (24
+// groups saved), 4096 x 6144 x 8192 176 and 167 (48)
+constexpr int kLayerTailSaves = 32;
 constexpr int kRedPitch = kGN + 4;
 static_assert((size_t)kGM * kRedPitch * 4 <= (size_t)kGStages * (kGA + kGB), "the partial sums fit the ring");
 
@@ -1525,7 +1528,7 @@ rlk_status launch_gemm(const typename ParamsOf<KIND>::type& p, const CUtensorMap
     const int tiles = p.MB * p.NB, pairs = sms / 2, whole = tiles / pairs * pairs, rest = tiles - whole;
     int split = rest > 0 ? kGSplit : 1;
     while (split > 1 && (p.KB < split * 4 || rest > clusters_at_once<kernel>(kGThreads, smem, 2 * split))) split /= 2;
-    if (whole > 0 && p.KB * (split - 1) < kTailSaves * split) split = 1;
+    if (whole > 0 && p.KB * (split - 1) < (layer_kind(KIND) ? kLayerTailSaves : kTailSaves) * split) split = 1;
     if (split == 1)
         return launch_clusters<kernel>(2 * (tiles < pairs ? tiles : pairs), kGThreads, smem, 2, false, st, a, b, p, 0,
                                        tiles, 1);
@@ -1543,7 +1546,14 @@ rlk_status launch_skinny(const typename ParamsOf<KIND>::type& p, const CUtensorM
                          int64_t most, int sms, cudaStream_t st) {
     const int tiles = (int)most, room = Skinny<NT>::kPerSm * sms;
     int split = 1;
-    while (split < 8 && (int64_t)tiles * split * 2 <= room && split * 4 <= p.KB) split *= 2;
+    if constexpr (KIND == kEpi || KIND == kEpiGated) {
+        // as many CTAs a tile as run at once, of three too (37 x 4096 to 12288, 96 tiles: 22.4 us over two, 20.1 over
+        // three; 1 x 4096: 15.3 and 14.9).  A second round of clusters costs more than it saves: 16 x 4096 gated to
+        // 2 x 12288, 192 tiles, 21.3 us unsplit, 27.6 over three.
+        for (int s = 2; s <= 8 && s * 2 <= p.KB && (int64_t)tiles * s <= room; ++s) split = s;
+    } else {
+        while (split < 8 && (int64_t)tiles * split * 2 <= room && split * 4 <= p.KB) split *= 2;
+    }
     return launch_clusters<skinny_kernel<NT, BROWS, KIND>>(split > 1 ? tiles * split : tiles < room ? tiles : room,
                            kSThreads, kSSmemOf<NT, KIND>, split, false, st, a, b, p, split);
 }
