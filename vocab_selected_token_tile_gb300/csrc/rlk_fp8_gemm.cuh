@@ -495,7 +495,9 @@ __device__ __forceinline__ Tile8 tile_at(const typename ParamsOf<KIND>::type& p,
 
 // 64 columns of the residual from `col` on, added to the lane's row v, through
 // shared memory as store_chunk's output; eight loads under way at a time (one by
-// one a tile's took 19,500 clocks).
+// one a tile's took 19,500 clocks), sixteen of FP32 rows off the 16-byte grid
+// (1000 x 5003 x 2000: 50.6 us by eight, 44.0; thirty-two gain nothing and cost
+// the loop registers).
 template <bool F32>
 __device__ __forceinline__ void add_residual(const Ext8Params& p, unsigned char* out, int lane, int64_t row0,
                                              int64_t limit, int col, float2* v) {
@@ -539,13 +541,13 @@ __device__ __forceinline__ void add_residual(const Ext8Params& p, unsigned char*
         } else if (F32) {
             const uint32_t* src = static_cast<const uint32_t*>(p.res) + row0 * p.ldr + at + lane;
 #pragma unroll
-            for (int b = 0; b < 32; b += 8) {
-                uint32_t x[8];
+            for (int b = 0; b < 32; b += 16) {
+                uint32_t x[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = b + i < rows && lane < cols ? __ldcs(src + (b + i) * p.ldr) : 0u;
+                for (int i = 0; i < 16; ++i) x[i] = b + i < rows && lane < cols ? __ldcs(src + (b + i) * p.ldr) : 0u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint32_t*>(out + (b + i) * 128 + (((lane >> 2) ^ i) * 16) + (lane & 3) * 4) = x[i];
+                for (int i = 0; i < 16; ++i)
+                    *reinterpret_cast<uint32_t*>(out + (b + i) * 128 + (((lane >> 2) ^ (i & 7)) * 16) + (lane & 3) * 4) = x[i];
             }
         } else {
             const uint16_t* src = static_cast<const uint16_t*>(p.res) + row0 * p.ldr + at + 2 * lane;
