@@ -112,9 +112,10 @@ def test_without_an_epilogue(built):
 
 
 def test_special_arguments_of_the_activations(built):
-    # one-hot rows of A pick z out of B's columns and the bias: +-large, zero, infinities, NaN
-    z = np.array([0.0, -0.0, 1e-30, -1e-30, 5.0, -5.0, 60.0, -60.0, 1e4, -1e4, 3e38, -3e38, np.inf, np.nan], np.float32)
-    n = len(z)
+    # zeros in B leave the bias: a NaN or an infinity beside numbers reaches its own column only
+    z = np.array([0.0, -0.0, 1e-30, -1e-30, 5.0, -5.0, 60.0, -60.0, 1e4, np.nan, -1e4, 3e38, -3e38, np.inf, np.nan, -np.inf],
+                 np.float32)
+    n, big = len(z), (0.0, -1e4, -3e38, -np.inf)
     for M in (2, 130):
         qa, sa, qb, sb = operands(M, n, 128, 1)
         qb = torch.zeros_like(qb.view(torch.uint8)).view(torch.float8_e4m3fn)
@@ -123,10 +124,34 @@ def test_special_arguments_of_the_activations(built):
                                          out_dtype=torch.float32))
             with np.errstate(all="ignore"):
                 want = layer.act(z.astype(np.float64), act)
-            assert np.isnan(got[:, n - 1]).all()
-            for j in range(n - 1):
-                err = 0.0 if np.isinf(want[j]) else layer.act_error(np.float64(z[j:j + 1]), act)[0] + 2.0 ** -20 * abs(want[j])
-                assert np.all(got[:, j] == want[j]) if np.isinf(want[j]) else np.all(np.abs(got[:, j] - want[j]) <= err), (act, z[j])
+            if act != "none":
+                want[np.isin(z, big)] = 0.0  # the limits
+            assert (np.isnan(got) == np.isnan(z)).all()
+            for j in range(n):
+                if np.isinf(want[j]):
+                    assert (got[:, j] == want[j]).all(), (act, z[j])
+                elif not np.isnan(want[j]):
+                    err = layer.act_error(np.float64(z[j:j + 1]) if abs(z[j]) < 1e5 else np.zeros(1), act)[0]
+                    assert np.all(np.abs(got[:, j] - want[j]) <= err + 2.0 ** -20 * abs(want[j])), (act, z[j])
+
+
+def test_gradients_of_special_arguments(built):
+    z = np.tile(np.array([0.0, -0.0, 3.0, -3.0, 30.0, -30.0, np.inf, -np.inf, 3e38, -3e38, np.nan], np.float32), 2)
+    dy = np.ones((130, len(z)), np.float32)
+    t = torch.from_numpy(np.tile(z, (130, 1))).cuda().to(torch.bfloat16)
+    for act in layer.ACTS[1:]:
+        q, s, _, _, db = rlk.fp8_act_grad(torch.from_numpy(dy).cuda(), t, act, bias_dtype=torch.float32)
+        got = f64(db) / 130
+        want = np.where(z > 0, 1.0, 0.0)
+        few = np.abs(z) < 10
+        want[few] = layer.slope(z[few].astype(np.float64), act)
+        assert (np.isnan(got) == np.isnan(z)).all()
+        ok = ~np.isnan(z)
+        assert np.all(np.abs(got - want)[ok] <= 2.0 ** -17)
+    # relu passes an infinite gradient on where z > 0 and nowhere else
+    dy[:, 3] = np.inf
+    db = f64(rlk.fp8_act_grad(torch.from_numpy(dy).cuda(), t, "relu", bias_dtype=torch.float32)[4])
+    assert db[3] == 0 and np.isfinite(db[~np.isnan(z)]).all()
 
 
 @pytest.mark.parametrize("M", [9, 300])
@@ -223,7 +248,8 @@ SPLITS = {
     "one": ([37], 0), "all in the last": ([0, 0, 0, 90], 0), "all in the first": ([200, 0, 0], 3),
     "even": ([64, 64, 64, 64], 0), "ragged": ([1, 0, 130, 7, 0, 256, 33, 129], 21), "none at all": ([0, 0, 0], 50),
     "single rows": ([1] * 40, 0), "few of many": ([0] * 60 + [2, 0, 1] + [0] * 65, 5), "large": ([700, 3, 515, 0, 300], 0),
-    "1024 groups": ([1, 0, 2, 0] * 256, 1),
+    "1024 groups": ([1, 0, 2, 0] * 256, 1), "some tens": ([20, 35, 0, 12, 66, 1, 40], 9), "hundreds": ([300, 129, 513], 70),
+    "a hundred each": ([128, 100, 129, 64, 65, 1], 130),
 }
 
 

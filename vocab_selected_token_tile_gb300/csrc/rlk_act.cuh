@@ -1,15 +1,23 @@
-// The activations of a feed-forward block, and their derivatives, in FP32.
+// The activations of a feed-forward block, and their derivatives, in FP32, two
+// values at a time (packed arithmetic):
 //
 //   silu       x s(x)                s(u) = 1 / (1 + e^-u)
 //   gelu       x Phi(x)              Phi the normal distribution
 //   gelu_tanh  x (1 + tanh(v)) / 2 = x s(2 v),  v = sqrt(2 / pi) (x + 0.044715 x^3)
 //
-// e^x is the special-function unit's (2 ulp) and so is 1 / x (1 ulp): 2^-21 of
-// the result, where BF16 keeps 2^-9.  Phi is 1 - erfc(|x| / sqrt 2) / 2 (or
-// the second term for x < 0) with the five-term approximation of erfc by
-// Hastings (Abramowitz and Stegun 7.1.26): t (a1 + t (a2 + ...)) e^-y^2 with
-// t = 1 / (1 + p y), within 1.5e-7 of erfc, so 7.5e-8 of Phi, about one FP32
-// rounding of 1.
+// e^x and 1 / x are the special-function unit's (2 ulp and 1 ulp), so a value is
+// within 2^-20 of itself where BF16 keeps 2^-9; gelu is within 7.5e-8 |x|: Phi is
+// 1 - erfc(|x| / sqrt 2) / 2 (or the second term for x < 0) with the five-term
+// approximation of erfc by Hastings (Abramowitz and Stegun 7.1.26),
+// t (a1 + t (a2 + ...)) e^-y^2, t = 1 / (1 + p y), within 1.5e-7.
+//
+// The warps of a product's epilogue have nothing to hide this behind, so two
+// values share one reciprocal, 1 / d0 = d1 (1 / (d0 d1)).  Hence x is held above
+// -40 (silu), -7 (gelu_tanh) and -12 (gelu), where act is below 2e-16, 3e-15 and
+// 3e-32 in magnitude, lest d0 d1 overflow; and a NaN is kept out of the
+// reciprocal and meets its own result only, in the product by x.  8192 x 12288 x
+// 4096: gelu adds 55 us to the product and silu 27; one value at a time they
+// added 70 and 36.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -24,56 +32,23 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluTwo = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kGeluCube = 0.044715f;
 
-__device__ __forceinline__ float sigmoid_f32(float u) { return rcp_approx(1.f + ex2_approx(-kLog2e * u)); }
-
-// Phi(x), and e^(-x^2 / 2) with it.
-__device__ __forceinline__ float normal_cdf(float x, float& bell) {
-    const float y = fabsf(x) * 0.70710678f, t = rcp_approx(__fmaf_rn(0.3275911f, y, 1.f));
-    bell = ex2_approx(x * x * (-0.5f * kLog2e));
-    float p = __fmaf_rn(1.061405429f, t, -1.453152027f);
-    p = __fmaf_rn(p, t, 1.421413741f);
-    p = __fmaf_rn(p, t, -0.284496736f);
-    p = __fmaf_rn(p, t, 0.254829592f);
-    const float half = 0.5f * p * t * bell;  // erfc / 2
-    return x < 0.f ? half : 1.f - half;
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 above(float2 x, float least) {
+    return make_float2(fmax_nan(x.x, least), fmax_nan(x.y, least));
 }
-
-// act(x); NaN stays NaN.
-__device__ __forceinline__ float act_f32(float x, int act) {
-    switch (act) {
-        case RLK_ACT_RELU: return x < 0.f ? 0.f : x;
-        case RLK_ACT_SILU: return x * sigmoid_f32(x);
-        case RLK_ACT_GELU: {
-            float bell;
-            return x * normal_cdf(x, bell);
-        }
-        case RLK_ACT_GELU_TANH: return x * sigmoid_f32(kGeluTwo * x * __fmaf_rn(kGeluCube, x * x, 1.f));
-        default: return x;
-    }
-}
-
-// The same of two values at a time (packed arithmetic), for the products'
-// epilogues, whose warps have nothing to hide it behind: one reciprocal serves
-// both, r = 1 / (d0 d1), and so x is held above -40 (silu), -7 (gelu_tanh) and
-// -12 (gelu), where act is below 2e-16, 3e-15 and 3e-32 in magnitude, lest d0
-// d1 overflow.  8192 x 12288 x 4096: gelu 70 us over none one by one, XX in pairs.
 __device__ __forceinline__ float2 rcp_pair(float2 d) {
     const float r = rcp_approx(d.x * d.y);
     return fmul2(make_float2(d.y, d.x), make_float2(r, r));
 }
-__device__ __forceinline__ float2 above(float2 x, float least) {
-    return make_float2(fmax_nan(x.x, least), fmax_nan(x.y, least));
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-// 2^t and 1 / (1 + 2^t), t at most 58 where it is a number (the minimum takes that
-// for a NaN, which would reach its neighbour through the reciprocal; the factor
-// that the caller multiplies by keeps it).
+
+// e = 2^t and 1 / (1 + 2^t), t at most 58 where it is a number (the minimum takes
+// that for a NaN).
 __device__ __forceinline__ float2 sigmoid_pair(float2 t, float2& e) {
     e = make_float2(ex2_approx(fminf(t.x, 58.f)), ex2_approx(fminf(t.y, 58.f)));
     return rcp_pair(fadd2(e, both(1.f)));
 }
 
-// Phi(x) as normal_cdf's, of numbers (a NaN gives some number), and e^(-x^2 / 2).
+// Phi(x) of numbers (a NaN gives some number), and e^(-x^2 / 2).
 __device__ __forceinline__ float2 normal_cdf_pair(float2 x, float2& bell) {
     const float2 c = make_float2(fminf(fabsf(x.x), 12.f), fminf(fabsf(x.y), 12.f));
     const float2 t = rcp_pair(ffma2(c, both(0.3275911f * 0.70710678f), both(1.f)));
@@ -88,6 +63,7 @@ __device__ __forceinline__ float2 normal_cdf_pair(float2 x, float2& bell) {
     return fadd2(both(0.5f), make_float2(copysignf(h.x, x.x), copysignf(h.y, x.y)));
 }
 
+// act of two values.
 template <int ACT>
 __device__ __forceinline__ float2 act_pair(float2 v) {
     if (ACT == RLK_ACT_RELU) return make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);
@@ -110,29 +86,36 @@ __device__ __forceinline__ float2 act_pair(float2 v) {
     return v;
 }
 
-// act of N pairs, [LO, HI) of v.
+#define RLK_ACT_SWITCH(ACT, CALL)                         \
+    switch (ACT) {                                        \
+        case RLK_ACT_RELU: CALL(RLK_ACT_RELU) break;      \
+        case RLK_ACT_SILU: CALL(RLK_ACT_SILU) break;      \
+        case RLK_ACT_GELU: CALL(RLK_ACT_GELU) break;      \
+        case RLK_ACT_GELU_TANH: CALL(RLK_ACT_GELU_TANH) break; \
+        default: break;                                   \
+    }
+
+// act of the pairs [LO, HI) of v.
 template <int LO, int HI, int N>
 __device__ __forceinline__ void act_pairs(float2 (&v)[N], int act) {
-#define RLK_ACT_CASE(A)                                                              \
-    case A:                                                                          \
-        _Pragma("unroll") for (int i = LO; i < HI; ++i) v[i] = act_pair<A>(v[i]);    \
-        break;
-    switch (act) {
-        RLK_ACT_CASE(RLK_ACT_RELU)
-        RLK_ACT_CASE(RLK_ACT_SILU)
-        RLK_ACT_CASE(RLK_ACT_GELU)
-        RLK_ACT_CASE(RLK_ACT_GELU_TANH)
-        default: break;
-    }
-#undef RLK_ACT_CASE
+#define RLK_ACT_ALL(A) _Pragma("unroll") for (int i = LO; i < HI; ++i) v[i] = act_pair<A>(v[i]);
+    RLK_ACT_SWITCH(act, RLK_ACT_ALL)
+#undef RLK_ACT_ALL
+}
+
+// act of one value, the same as of a pair of it.
+__device__ __forceinline__ float act_one(float x, int act) {
+    float2 v = both(x);
+#define RLK_ACT_ONE(A) v = act_pair<A>(v);
+    RLK_ACT_SWITCH(act, RLK_ACT_ONE)
+#undef RLK_ACT_ONE
+    return v.x;
 }
 
 // act'(x) of two values.  Beyond the clamps it is 0 or 1 to FP32, and within them
 // no infinity meets a zero; a NaN stays one, and its neighbour does not.
 template <int ACT>
 __device__ __forceinline__ float2 act_slope_pair(float2 v) {
-    if (ACT == RLK_ACT_RELU)
-        return make_float2(v.x > 0.f ? 1.f : v.x <= 0.f ? 0.f : v.x, v.y > 0.f ? 1.f : v.y <= 0.f ? 0.f : v.y);
     constexpr float edge = ACT == RLK_ACT_SILU ? 40.f : ACT == RLK_ACT_GELU_TANH ? 7.f : 12.f;
     const float2 low = above(v, -edge);
     const float2 x = make_float2(fmin_nan(low.x, edge), fmin_nan(low.y, edge));
@@ -153,6 +136,14 @@ __device__ __forceinline__ float2 act_slope_pair(float2 v) {
         return ffma2(fmul2(x, both(0.3989422804f)), bell, p);
     }
     return both(1.f);
+}
+
+// g act'(x).  relu passes g on or does not: an infinite g meets no zero.
+template <int ACT>
+__device__ __forceinline__ float2 act_back_pair(float2 g, float2 x) {
+    if (ACT == RLK_ACT_RELU)
+        return make_float2(x.x > 0.f ? g.x : x.x <= 0.f ? 0.f : x.x, x.y > 0.f ? g.y : x.y <= 0.f ? 0.f : x.y);
+    return ACT == RLK_ACT_NONE ? g : fmul2(g, act_slope_pair<ACT>(x));
 }
 
 }  // namespace rlk
