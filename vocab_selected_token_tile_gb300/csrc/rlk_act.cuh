@@ -9,15 +9,14 @@
 // within 2^-20 of itself where BF16 keeps 2^-9; gelu is within 7.5e-8 |x|: Phi is
 // 1 - erfc(|x| / sqrt 2) / 2 (or the second term for x < 0) with the five-term
 // approximation of erfc by Hastings (Abramowitz and Stegun 7.1.26),
-// t (a1 + t (a2 + ...)) e^-y^2, t = 1 / (1 + p y), within 1.5e-7.
+// t (a1 + t (a2 + ...)) e^-y^2, t = 1 / (1 + p y), within 1.5e-7 of it.
 //
 // The warps of a product's epilogue have nothing to hide this behind, so two
 // values share one reciprocal, 1 / d0 = d1 (1 / (d0 d1)).  Hence x is held above
-// -40 (silu), -7 (gelu_tanh) and -12 (gelu), where act is below 2e-16, 3e-15 and
-// 3e-32 in magnitude, lest d0 d1 overflow; and a NaN is kept out of the
-// reciprocal and meets its own result only, in the product by x.  8192 x 12288 x
-// 4096: gelu adds 55 us to the product and silu 27; one value at a time they
-// added 70 and 36.
+// -40 (silu) and -7 (gelu_tanh), where act is below 2e-16 and 3e-15 in magnitude,
+// lest d0 d1 overflow; and a NaN is kept out of the reciprocal and meets its own
+// result only, in the last operation.  8192 x 12288 x 4096: gelu adds 47 us to the
+// product and silu 28; one value at a time they added 70 and 36.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -48,19 +47,18 @@ __device__ __forceinline__ float2 sigmoid_pair(float2 t, float2& e) {
     return rcp_pair(fadd2(e, both(1.f)));
 }
 
-// Phi(x) of numbers (a NaN gives some number), and e^(-x^2 / 2).
-__device__ __forceinline__ float2 normal_cdf_pair(float2 x, float2& bell) {
-    const float2 c = make_float2(fminf(fabsf(x.x), 12.f), fminf(fabsf(x.y), 12.f));
+// -erfc(c / sqrt 2) / 2 for c = min(|x|, 12), which is 0 to FP32 from there on (a
+// NaN takes 12), and e^(-c^2 / 2).
+__device__ __forceinline__ float2 minus_tail_pair(float2 x, float2& c, float2& bell) {
+    c = make_float2(fminf(fabsf(x.x), 12.f), fminf(fabsf(x.y), 12.f));
     const float2 t = rcp_pair(ffma2(c, both(0.3275911f * 0.70710678f), both(1.f)));
     const float2 e = fmul2(fmul2(c, c), both(-0.5f * kLog2e));
     bell = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-    // minus erfc / 2 of |x|; Phi is 1/2 + sign(x) (1/2 - erfc / 2)
     float2 p = ffma2(both(-0.5f * 1.061405429f), t, both(0.5f * 1.453152027f));
     p = ffma2(p, t, both(-0.5f * 1.421413741f));
     p = ffma2(p, t, both(0.5f * 0.284496736f));
     p = ffma2(p, t, both(-0.5f * 0.254829592f));
-    const float2 h = ffma2(fmul2(p, t), bell, both(0.5f));
-    return fadd2(both(0.5f), make_float2(copysignf(h.x, x.x), copysignf(h.y, x.y)));
+    return fmul2(fmul2(p, t), bell);
 }
 
 // act of two values.
@@ -78,10 +76,10 @@ __device__ __forceinline__ float2 act_pair(float2 v) {
         float2 e;
         return fmul2(x, sigmoid_pair(fmul2(x, w), e));
     }
-    if (ACT == RLK_ACT_GELU) {
-        const float2 x = above(v, -12.f);
-        float2 bell;
-        return fmul2(x, normal_cdf_pair(x, bell));
+    if (ACT == RLK_ACT_GELU) {  // x Phi(x) = max(x, 0) - |x| erfc(|x| / sqrt 2) / 2 for either sign
+        float2 c, bell;
+        const float2 tail = minus_tail_pair(v, c, bell);
+        return ffma2(c, tail, above(v, 0.f));
     }
     return v;
 }
@@ -131,8 +129,9 @@ __device__ __forceinline__ float2 act_slope_pair(float2 v) {
         return fmul2(s, ffma2(fmul2(x, up), fmul2(e, s), both(1.f)));
     }
     if (ACT == RLK_ACT_GELU) {
-        float2 bell;
-        const float2 p = normal_cdf_pair(x, bell);
+        float2 c, bell;
+        const float2 h = fadd2(minus_tail_pair(x, c, bell), both(0.5f));  // Phi(|x|) - 1/2
+        const float2 p = fadd2(make_float2(copysignf(h.x, x.x), copysignf(h.y, x.y)), both(0.5f));
         return ffma2(fmul2(x, both(0.3989422804f)), bell, p);
     }
     return both(1.f);
