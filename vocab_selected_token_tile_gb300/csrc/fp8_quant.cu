@@ -35,6 +35,14 @@
 // TB/s), rows 17.3 (5.9 TB/s); FP32, 151936 x 4096 in blocks: 443 us (7.0 TB/s:
 // HBM).  Rows off the 16-byte grid are read by the element (8000 x 3517: BF16
 // 27.3 us, FP32 33.8; 8000 x 3520: 16.1 and 22.5).
+//
+// Several matrices (a batch: experts' weights) are the same tiles with the
+// pointers moved: 32 of 2816 x 2048, BF16, both directions 116 us (738 MB, 6.4
+// TB/s).  Rows that belong to groups: a tile is up to 128 rows of one group, so
+// that the transpose's groups of 128 are the group's own; each CTA looks its tile
+// up by itself, which takes 18% of its time: 16384 rows of 32 groups x 2048, both
+// directions 34 us, without groups 28.6 (looking up once for two or four tiles of
+// columns was no faster).
 #include "rlk_fp8_quant.cuh"
 
 namespace rlk {

@@ -41,6 +41,26 @@
 // splits K, and adds its partial sums through distributed shared memory in
 // rank order: no workspace, no second launch, the same bits every time.
 //
+// Both are also built for a feed-forward layer (kEpi and on): z = A B^T + bias,
+// y = act(z) or act(gate) * up, c = y + residual, in FP32 and rounded where they
+// are stored.  A gated layer's B is loaded so that a thread has a column's gate
+// and its other half: 64 rows of each by turns for a tile of a pair (one 4-D box a
+// CTA), 16 for few rows.  The epilogue warps have nothing to hide this work
+// behind, so it adds to a tile's time: 8192 x 12288 x 4096, 317 us bare, 329
+// through this path, 357 with silu, 380 with gelu, 327 gated with silu (half as
+// many results), 350 with a bias alone, 370 with z kept, 400 with a BF16 residual;
+// a pass over the result would take 60 (a read and a write of 201 MB) or 90.
+//
+// And for rows that belong to groups, each with a B of its own (kRows, kHalves),
+// and operands whose K axis belongs to groups (kDepth), where a CTA finds its
+// tiles from the groups' ends (rlk_groups.cuh).
+//
+// Registers decide a lot here: a layer's loop keeps 128 sums and 64 loaded values
+// a thread of the 224.  A barrier for biases that another warp had fetched (so
+// one more wait in the epilogue) took the bare path from 333 to 370 us, and
+// finishing the tile in loops over shared memory, with little code, took it to
+// 420; what is there now came out of such trials.
+//
 // Every wait is bounded; on expiry the CTA records the time-out in the status
 // word, stops issuing, waits (bounded) for the copies and MMAs under way (a
 // pair for those of both of its CTAs), frees its tensor memory and returns.
@@ -430,7 +450,8 @@ constexpr size_t kGSmem = 1024 + (size_t)kGStages * (kGA + kGB) + 8 * kGOut +
 // MMA takes M = 128, 64 rows of each CTA; a CTA's 128 lanes hold them twice, the
 // lower 64 the tile's first 128 columns and the upper 64 the others, in 128
 // columns of tensor memory.  So four accumulators are in flight, not two: from
-// one's completion to the next it is the hand-overs that take the time.
+// one's completion to the next it is the hand-overs that take the time, 530
+// clocks a group against 870 for a whole tile (with two, 850).
 __host__ __device__ constexpr int tile_rows(int k) { return half_kind(k) ? kGM : 2 * kGM; }  // of A, by a pair
 __host__ __device__ constexpr int stages_of(int k) { return half_kind(k) ? 6 : kGStages; }
 __host__ __device__ constexpr int accs_of(int k) { return half_kind(k) ? 4 : 2; }

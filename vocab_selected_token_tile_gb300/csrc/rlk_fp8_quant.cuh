@@ -289,7 +289,7 @@ __device__ __forceinline__ void quantize_tile(const QuantParams& p, const Block<
 }
 
 // The row tile of a group that blockIdx.y counts, false behind the last.  Each
-// CTA looks it up for itself (rlk_groups.cuh), 0.5 us beside its own chain of 3.
+// CTA looks it up for itself (rlk_groups.cuh).
 __device__ __forceinline__ bool group_tile(const QuantExtParams& p, int64_t rt, GroupTable* tab, RowTile& at) {
     groups_build<kQThreads>(tab, p.ends, p.G, (int)p.R, kQT, 1, false);
     __syncthreads();

@@ -4,8 +4,9 @@
 // row 0.  The counts are on the device, so each CTA works out by itself which
 // group a unit of work falls into: one pass over `ends` by all threads (a
 // running maximum, then a running sum of the groups' units), two tables in
-// shared memory, and a binary search a unit.  A launch of its own for the
-// tables would cost more than the 1-2 us that this does (1024 groups at most).
+// shared memory, and a binary search a unit.  It takes a microsecond or two; a
+// launch of its own for the tables would cost as much, and a buffer (1024 groups
+// at most: two tables of 4 KB).
 //
 // Whatever `ends` holds, no group reaches past [0, rows) and no two groups
 // meet: it is taken as its running maximum, held within [0, rows].
