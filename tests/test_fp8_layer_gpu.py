@@ -187,6 +187,33 @@ def test_residual_in_place(built, M, N, K):
         assert torch.equal(res, want)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,rows,K", [(2304, 2304, 5632), (2500, 2176, 6000)])
+def test_last_tiles_in_a_launch_of_their_own(built, M, rows, K, gated):
+    # a round of the pairs and a few tiles more, which are split along K
+    N = rows // 2 if gated else rows
+    qa, sa, qb, sb = operands(M, rows, K, 14)
+    bias, res = tensor(rand((1, rows), 15, 0.5)[0], "f32"), tensor(rand((M, N), 16), "f32")
+    y, z = rlk.fp8_matmul_act(qa, sa, qb, sb, bias=bias, activation="gelu_tanh", gated=gated, residual=res, keep=True,
+                              out_dtype=torch.float32, validate=True)
+
+    def stands_for(q, s, r):
+        s = s.double().t().repeat_interleave(r, dim=0)[:q.shape[0]]
+        return q.double() * s.repeat_interleave(128, dim=1)[:, :K]
+
+    a, b = stands_for(qa, sa, 1), stands_for(qb, sb, 128)
+    want = a @ b.t() + bias.double()
+    err = ref.bound(K, (a.abs() @ b.abs().t()).cpu().numpy())
+    within(z, f64(want), err + 2.0 ** -24 * np.abs(f64(want)))
+    n = want.shape[1] // 2 if gated else want.shape[1]
+    act = torch.nn.functional.gelu(want[:, :n], approximate="tanh")
+    out = f64(act * want[:, n:] if gated else act) + f64(res)
+    lim = 1.13 * err[:, :n] + layer.act_error(f64(want[:, :n]), "gelu_tanh")
+    if gated:
+        lim = lim * (np.abs(f64(want[:, n:])) + err[:, n:]) + np.abs(f64(act)) * err[:, n:]
+    within(y, out, lim + 3 * 2.0 ** -24 * (np.abs(out) + np.abs(f64(res))))
+
+
 # ------------------------------------------------------------------ the epilogue's backward
 
 # The derivatives are sums of a few products, each with 2^-21 for e^x and 1 / x and an exponent rounded to 2^-23 of
@@ -609,6 +636,28 @@ def test_captured_steps(built):
         got = [t.clone() for t in held]
         for a, b in zip(got, step()):
             assert torch.equal(a, b)
+
+
+def test_two_captured_graphs_at_once(built):
+    """Graphs that share the stream's status word, replayed on two streams."""
+    counts, M, ends, _ = split_of("large")
+    ga, gsa, gb, gsb = operands(M, 256, 384, 112, (len(counts),))
+    qa, sa, qb, sb = operands(300, 640, 512, 113)
+    want = rlk.fp8_grouped_matmul(ga, gsa, gb, gsb, ends), rlk.fp8_matmul_act(qa, sa, qb, sb, activation="silu", gated=True)
+    calls = (lambda: rlk.fp8_grouped_matmul(ga, gsa, gb, gsb, ends),
+             lambda: rlk.fp8_matmul_act(qa, sa, qb, sb, activation="silu", gated=True))
+    graphs, held = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for g, call in zip(graphs, calls):
+        with torch.cuda.graph(g):
+            held.append(call())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(held[0], want[0]) and torch.equal(held[1], want[1])
 
 
 def test_same_bits_again(built):

@@ -57,9 +57,14 @@ def test_group_tensors(built, error, change):
         rlk.fp8_grouped_matmul(**{**grouped(), **{k: v() for k, v in change.items()}})
 
 
-def test_too_many_groups(built):
-    with pytest.raises(rlk.RlkError):
-        rlk.fp8_quantize_grouped(cuda(10, 16), cuda(1025, dtype=torch.int32))
+@pytest.mark.parametrize("n", [0, 1025])
+def test_numbers_of_groups(built, n):
+    ends, x, w = cuda(n, dtype=torch.int32), cuda(10, 64), cuda(n, 32, 64)
+    for call in (lambda: rlk.fp8_quantize_grouped(x, ends), lambda: rlk.fp8_act_grad(x, x, "relu", ends=ends),
+                 lambda: autograd.fp8_grouped_linear(x, w, ends),
+                 lambda: autograd.fp8_grouped_linear(x, w.requires_grad_(), ends, activation="relu")):
+        with pytest.raises(ValueError):
+            call()
 
 
 def test_other_calls_tensors(built):

@@ -1047,6 +1047,8 @@ def _ends(ends, like):
     if ends.dtype is not _t().int32 or ends.dim() != 1 or not ends.is_contiguous() or not ends.is_cuda:
         raise TypeError(f"ends must be a contiguous int32 CUDA tensor [G], not {str(ends.dtype)[6:]} "
                         f"{list(ends.shape)} on {ends.device}")
+    if not 1 <= ends.shape[0] <= 1024:
+        raise ValueError(f"ends has {ends.shape[0]} groups; 1 to 1024 are taken")
     return ends.shape[0], ends.data_ptr()
 
 
