@@ -46,10 +46,11 @@
 // are stored.  A gated layer's B is loaded so that a thread has a column's gate
 // and its other half: 64 rows of each by turns for a tile of a pair (one 4-D box a
 // CTA), 16 for few rows.  The epilogue warps have nothing to hide this work
-// behind, so it adds to a tile's time: 8192 x 12288 x 4096, 317 us bare, 329
-// through this path, 357 with silu, 380 with gelu, 327 gated with silu (half as
-// many results), 350 with a bias alone, 370 with z kept, 400 with a BF16 residual;
-// a pass over the result would take 60 (a read and a write of 201 MB) or 90.
+// behind, so it adds to a tile's time: 8192 x 12288 x 4096, 317 us bare, 330
+// through this path, 358 with silu, 375 with gelu, 326 gated with silu (half as
+// many results), 340-348 with a bias alone, 365 with z kept, 400 with a BF16
+// residual; a pass over the result would take 60 (a read and a write of 201 MB) or
+// 90.
 //
 // And for rows that belong to groups, each with a B of its own (kRows, kHalves),
 // and operands whose K axis belongs to groups (kDepth), where a CTA finds its
@@ -262,7 +263,7 @@ struct Ext8Params : Gemm8Params {
     const void *bias, *res;
     uint16_t* z;          // NULL, or where z goes in BF16
     int64_t ldr, ldz;
-    int32_t bias_f32, res_f32, res_vec, z_vec, act;
+    int32_t bias_f32, bias_vec, res_f32, res_vec, z_vec, act;
     // kRows, kDepth
     const int32_t* ends;
     int32_t G, rest;      // rest: the rows behind the groups are set to zero
@@ -615,10 +616,12 @@ __device__ __forceinline__ float res_at(const Ext8Params& p, int64_t i) {
                      : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.res)[i] << 16);
 }
 
-// The sums of a warp's columns start from their biases: four columns a lane,
-// read once, then all of them by every lane through shared memory.  (Reading
-// them before the tile before was finished gained nothing, and registers of the
-// gated product's loop suffered: 331 -> 348 us at 8192 x 12288 x 4096.)
+// The sums of a warp's columns start from their biases, which every lane reads
+// (one address a warp), or where they lie off the 16-byte grid or end inside the
+// tile through shared memory: 8192 x 12288 x 4096, 330 us without, FP32 340 read
+// and 350 through shared memory, BF16 348 either way.  (Fetching them before the
+// tile before was finished gained nothing, and registers of the gated product's
+// loop suffered: 331 -> 348 us.)
 // PAIRS: of columns a warp has, 64 or (of a half tile) 32; gated, half of them
 // the gate's.  col: the first of the result's; zcol: of B's rows, so of z's.
 template <bool GATED, int PAIRS>
@@ -627,7 +630,34 @@ __device__ __forceinline__ void start_with_bias(const Ext8Params& p, unsigned ch
     if (p.rest && t.group == p.G) return;  // rows behind the groups: zeros
     constexpr int kEach = PAIRS / 16, kOf = GATED ? 16 : 32;  // columns a lane, lanes of a half
     const int half = lane / kOf, c = col + kEach * (lane % kOf);
-    const int64_t at = (int64_t)t.group * (GATED ? 2 : 1) * p.N + (half ? p.N : 0) + c;
+    const int64_t group = (int64_t)t.group * (GATED ? 2 : 1) * p.N, at = group + (half ? p.N : 0) + c;
+    if (p.bias_vec && col + (GATED ? PAIRS : 2 * PAIRS) <= p.N) {
+        // every lane reads all of them, one address a warp
+#pragma unroll
+        for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+            constexpr int kOwn = GATED ? PAIRS / 2 : PAIRS;
+            const int64_t from = group + (h ? p.N : 0) + col;
+            if (p.bias_f32) {
+                const float4* b = reinterpret_cast<const float4*>(static_cast<const float*>(p.bias) + from);
+#pragma unroll
+                for (int i = 0; i < kOwn / 2; ++i) {
+                    const float4 x = __ldg(b + i);
+                    sum[kOwn * h + 2 * i] = make_float2(x.x, x.y), sum[kOwn * h + 2 * i + 1] = make_float2(x.z, x.w);
+                }
+            } else {
+                const uint4* b = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + from);
+#pragma unroll
+                for (int i = 0; i < kOwn / 4; ++i) {
+                    const uint4 x = __ldg(b + i);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sum[kOwn * h + 4 * i + e] = make_float2(bf16lo_to_f32(w[e]), bf16hi_to_f32(w[e]));
+                }
+            }
+        }
+        return;
+    }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
@@ -1614,6 +1644,7 @@ void set_epilogue(Ext8Params& p, const rlk_fp8_epilogue* e, int64_t N) {
     if (!e) return;
     p.bias = e->bias;
     p.bias_f32 = e->bias_type == RLK_F32;
+    p.bias_vec = reinterpret_cast<uintptr_t>(p.bias) % 16 == 0 && (N * (p.bias_f32 ? 4 : 2)) % 16 == 0;
     p.res = e->residual;
     p.res_f32 = e->residual_type == RLK_F32;
     p.ldr = e->residual_stride;
