@@ -1,5 +1,5 @@
 // Quantisation to E4M3 with one FP32 scale for each group of 128 (sm_103a):
-// the operands of the FP8 product in fp8_gemm.cu.
+// the operands of the FP8 products (rlk_fp8_gemm.cuh).
 //
 // A group is 128 consecutive elements of a row (block_rows 1), or a block of
 // 128 rows x 128 columns (block_rows 128); the last group of a row and the

@@ -1,4 +1,4 @@
-// What the tensor-core kernels share (lmhead.cu, linear_ce.cu, fp8_gemm.cu):
+// What the tensor-core kernels share (lmhead.cu, linear_ce.cu, rlk_fp8_gemm.cuh):
 // the tile sizes of the BF16 ones, the bounded waits of their pipelines, and
 // the tensor maps of BF16 operands.
 #pragma once

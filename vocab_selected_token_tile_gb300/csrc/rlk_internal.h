@@ -177,7 +177,7 @@ rlk_status launch_fp8_grouped_dweight(int64_t G, int64_t rows, int64_t M, int64_
                                       int32_t accumulate, uint32_t* status, cudaStream_t stream);
 
 // Quantisation of groups of rows, of several matrices, and of the epilogue's
-// backward with the bias's gradient (fp8_quant.cu); part: the row tiles' sums.
+// backward with the bias's gradient (fp8_act_grad.cu); part: the row tiles' sums.
 int64_t group_row_tiles(int64_t groups, int64_t rows);
 rlk_status launch_fp8_quantize_grouped(int64_t G, int64_t rows, int64_t cols, const int32_t* ends, const void* x,
                                        int32_t x_f32, int64_t ldx, uint8_t* q, int64_t ldq, float* scale, uint8_t* qt,

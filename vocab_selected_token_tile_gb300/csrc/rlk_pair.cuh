@@ -1,4 +1,4 @@
-// What the kernels of CTA pairs share (fp8_gemm.cu, linear_ce.cu): ring
+// What the kernels of CTA pairs share (rlk_fp8_gemm.cuh, linear_ce.cu): ring
 // positions and the barriers of a pair's pipeline from its start to its end.
 //
 // Two CTAs work one 256 x 256 tile: each loads its 128 rows of A and half of
