@@ -668,3 +668,35 @@ def test_same_bits_again(built):
     runs = [torch.autograd.grad(autograd.fp8_grouped_linear(x, w, ends, b, "gelu", True), (x, w, b), dy) for _ in range(3)]
     for r in runs[1:]:
         assert all(torch.equal(a, c) for a, c in zip(r, runs[0]))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_a_rows_result_is_its_own(built, act, gated):
+    """Other rows of the call, of the next group and behind the groups leave a row's bits as they are."""
+    N, K = 192, 130
+    for M in (3, 8, 23, 50, 64, 100, 300):
+        qb, sb = operands(1, 2 * N if gated else N, K, 130)[2:]
+        x = tensor(rand((M, K), 131 + M))
+        other = tensor(rand((M, K), 132 + M, 3.0))
+        mine = torch.arange(M, device="cuda") % 3 == 0  # no row beside it, nor two away, is
+        other[mine] = x[mine]
+        a, b = (rlk.fp8_matmul_act(*rlk.fp8_quantize(v), qb, sb, activation=act, gated=gated, out_dtype=torch.float32)
+                for v in (x, other))
+        assert torch.equal(a[mine], b[mine]), M
+        assert not torch.equal(a, b)
+    G = 6
+    qb, sb = operands(1, 2 * N if gated else N, K, 133, (G,))[2:]
+    for counts in ([1, 0, 2, 1, 3, 1], [5, 1, 1, 20, 7, 1], [30, 1, 0, 33, 20, 3], [50, 1, 70, 40, 1, 60], [200, 1, 300, 0, 129, 1]):
+        used = sum(counts)
+        M = used + 7
+        ends = torch.tensor(counts, device="cuda").cumsum(0).to(torch.int32)
+        x = tensor(rand((M, K), 134 + M))
+        other = tensor(rand((M, K), 135 + M, 3.0))
+        mine = torch.arange(M, device="cuda") % 3 == 0
+        mine[used - 1], mine[used:] = True, False
+        other[mine] = x[mine]
+        a, b = (rlk.fp8_grouped_matmul(*rlk.fp8_quantize(v), qb, sb, ends, activation=act, gated=gated,
+                                       out_dtype=torch.float32) for v in (x, other))
+        assert torch.equal(a[mine], b[mine]), counts
+        assert not torch.equal(a, b)

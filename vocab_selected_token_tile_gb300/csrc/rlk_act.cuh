@@ -15,8 +15,12 @@
 // values share one reciprocal, 1 / d0 = d1 (1 / (d0 d1)).  Hence x is held above
 // -40 (silu) and -7 (gelu_tanh), where act is below 2e-16 and 3e-15 in magnitude,
 // lest d0 d1 overflow; and a NaN is kept out of the reciprocal and meets its own
-// result only, in the last operation.  8192 x 12288 x 4096: gelu adds 45 us to the
-// product and silu 28; one value at a time they added 70 and 36.
+// result only, in the last operation.  The last bit of a value is then its
+// neighbour's too, which may be a column beside it but not another row, of another
+// token or of none: where the two are of different rows (OWN, the epilogue of few
+// rows, which waits for memory: no slower) each has its own reciprocal.
+// 8192 x 12288 x 4096: gelu adds 45 us to the product and silu 28; one value at a
+// time they added 70 and 36.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -35,23 +39,27 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 above(float2 x, float least) {
     return make_float2(fmax_nan(x.x, least), fmax_nan(x.y, least));
 }
+template <bool OWN>
 __device__ __forceinline__ float2 rcp_pair(float2 d) {
+    if (OWN) return make_float2(rcp_approx(d.x), rcp_approx(d.y));
     const float r = rcp_approx(d.x * d.y);
     return fmul2(make_float2(d.y, d.x), make_float2(r, r));
 }
 
 // e = 2^t and 1 / (1 + 2^t), t at most 58 where it is a number (the minimum takes
 // that for a NaN).
+template <bool OWN>
 __device__ __forceinline__ float2 sigmoid_pair(float2 t, float2& e) {
     e = make_float2(ex2_approx(fminf(t.x, 58.f)), ex2_approx(fminf(t.y, 58.f)));
-    return rcp_pair(fadd2(e, both(1.f)));
+    return rcp_pair<OWN>(fadd2(e, both(1.f)));
 }
 
 // -erfc(c / sqrt 2) / 2 for c = min(|x|, 12), which is 0 to FP32 from there on (a
 // NaN takes 12), and e^(-c^2 / 2).
+template <bool OWN>
 __device__ __forceinline__ float2 minus_tail_pair(float2 x, float2& c, float2& bell) {
     c = make_float2(fminf(fabsf(x.x), 12.f), fminf(fabsf(x.y), 12.f));
-    const float2 t = rcp_pair(ffma2(c, both(0.3275911f * 0.70710678f), both(1.f)));
+    const float2 t = rcp_pair<OWN>(ffma2(c, both(0.3275911f * 0.70710678f), both(1.f)));
     const float2 e = fmul2(fmul2(c, c), both(-0.5f * kLog2e));
     bell = make_float2(ex2_approx(e.x), ex2_approx(e.y));
     float2 p = ffma2(both(-0.5f * 1.061405429f), t, both(0.5f * 1.453152027f));
@@ -62,23 +70,23 @@ __device__ __forceinline__ float2 minus_tail_pair(float2 x, float2& c, float2& b
 }
 
 // act of two values.
-template <int ACT>
+template <int ACT, bool OWN = false>
 __device__ __forceinline__ float2 act_pair(float2 v) {
     if (ACT == RLK_ACT_RELU) return make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);
     if (ACT == RLK_ACT_SILU) {
         const float2 x = above(v, -40.f);
         float2 e;
-        return fmul2(x, sigmoid_pair(fmul2(x, both(-kLog2e)), e));
+        return fmul2(x, sigmoid_pair<OWN>(fmul2(x, both(-kLog2e)), e));
     }
     if (ACT == RLK_ACT_GELU_TANH) {
         const float2 x = above(v, -7.f);
         const float2 w = ffma2(fmul2(x, x), both(-kLog2e * kGeluTwo * kGeluCube), both(-kLog2e * kGeluTwo));
         float2 e;
-        return fmul2(x, sigmoid_pair(fmul2(x, w), e));
+        return fmul2(x, sigmoid_pair<OWN>(fmul2(x, w), e));
     }
     if (ACT == RLK_ACT_GELU) {  // x Phi(x) = max(x, 0) - |x| erfc(|x| / sqrt 2) / 2 for either sign
         float2 c, bell;
-        const float2 tail = minus_tail_pair(v, c, bell);
+        const float2 tail = minus_tail_pair<OWN>(v, c, bell);
         return ffma2(c, tail, above(v, 0.f));
     }
     return v;
@@ -94,9 +102,9 @@ __device__ __forceinline__ float2 act_pair(float2 v) {
     }
 
 // act of the pairs [LO, HI) of v.
-template <int LO, int HI, int N>
+template <int LO, int HI, bool OWN = false, int N>
 __device__ __forceinline__ void act_pairs(float2 (&v)[N], int act) {
-#define RLK_ACT_ALL(A) _Pragma("unroll") for (int i = LO; i < HI; ++i) v[i] = act_pair<A>(v[i]);
+#define RLK_ACT_ALL(A) _Pragma("unroll") for (int i = LO; i < HI; ++i) v[i] = act_pair<A, OWN>(v[i]);
     RLK_ACT_SWITCH(act, RLK_ACT_ALL)
 #undef RLK_ACT_ALL
 }
@@ -123,14 +131,14 @@ __device__ __forceinline__ float2 act_slope_pair(float2 v) {
         const float2 w = ACT == RLK_ACT_SILU ? both(-kLog2e)
                                              : ffma2(x2, both(-kLog2e * kGeluTwo * kGeluCube), both(-kLog2e * kGeluTwo));
         float2 e;
-        const float2 s = sigmoid_pair(fmul2(x, w), e);
+        const float2 s = sigmoid_pair<false>(fmul2(x, w), e);
         const float2 up = ACT == RLK_ACT_SILU ? both(1.f) : ffma2(x2, both(3.f * kGeluTwo * kGeluCube), both(kGeluTwo));
         // 1 - s is 2^t s, which keeps its digits where s is near 1 and x u' large
         return fmul2(s, ffma2(fmul2(x, up), fmul2(e, s), both(1.f)));
     }
     if (ACT == RLK_ACT_GELU) {
         float2 c, bell;
-        const float2 h = fadd2(minus_tail_pair(x, c, bell), both(0.5f));  // Phi(|x|) - 1/2
+        const float2 h = fadd2(minus_tail_pair<false>(x, c, bell), both(0.5f));  // Phi(|x|) - 1/2
         const float2 p = fadd2(make_float2(copysignf(h.x, x.x), copysignf(h.y, x.y)), both(0.5f));
         return ffma2(fmul2(x, both(0.3989422804f)), bell, p);
     }

@@ -1173,7 +1173,7 @@ __device__ __forceinline__ void finish_lanes(const Ext8Params& p, const Unit8& x
                 v[i] = make_float2(g[0], g[1]), u[i] = make_float2(o[0], o[1]);
             }
         }
-        act_pairs<0, kPairs>(v, p.act);
+        act_pairs<0, kPairs, true>(v, p.act);  // of different rows
         if (GATED) {
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) v[i] = fmul2(v[i], u[i]);
