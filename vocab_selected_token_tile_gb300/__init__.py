@@ -986,13 +986,22 @@ def _type(t):
 
 def _matrices(t, name, dtypes):
     """A 3-D CUDA tensor of matrices with contiguous rows: (count, rows, columns, row stride, matrix stride)."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be a 3-D CUDA tensor, not {list(t.shape)} on {t.device}")
-    rows, cols, stride = _matrix(t[0] if t.shape[0] else t.new_empty(t.shape[1:]), name, dtypes)
-    between = t.stride(0)
-    if t.shape[0] > 1 and between < (rows - 1) * stride + cols:
+    shape = t.shape
+    if len(shape) != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 3-D CUDA tensor, not {list(shape)} on {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d)[6:] for d in dtypes)}, not {str(t.dtype)[6:]}")
+    count, rows, cols = shape
+    between, stride, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name}'s rows must be contiguous: its strides are {list(t.stride())}")
+    if rows <= 1:
+        stride = max(cols, stride)
+    elif stride < cols:
+        raise ValueError(f"{name}'s rows overlap: its strides are {list(t.stride())}")
+    if count > 1 and between < (rows - 1) * stride + cols:
         raise ValueError(f"{name}'s matrices overlap: its strides are {list(t.stride())}")
-    return t.shape[0], rows, cols, stride, between
+    return count, rows, cols, stride, between
 
 
 def _batch_codes(x, count, rows, cols):
