@@ -73,6 +73,7 @@
 
 #include <mutex>
 #include <string>
+#include <type_traits>
 
 #include "rlk_act.cuh"
 #include "rlk_gemm.cuh"
@@ -302,17 +303,31 @@ __device__ __forceinline__ void store_piece(uint16_t* c, uint4 w, int cols) {
         if (e < cols) c[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
 }
 
+// f(0) ... f(COUNT - 1), each number a type, for places in an array that the
+// compiler is to check.
+template <int COUNT, int AT = 0, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    if constexpr (AT < COUNT) {
+        f(std::integral_constant<int, AT>{});
+        each<COUNT, AT + 1>(f);
+    }
+}
+
 // A warp's 32 rows x 128 bytes of C (32 FP32 or 64 BF16 columns) through shared
 // memory, so that a row's 128 bytes leave in one piece: 16 bytes a lane
 // straight from the registers, 32 rows an instruction, took 10,700 clocks a 128
 // x 256 tile, a third of the product's time at K = 4096.  16-byte piece j of
 // row r is kept at j ^ turn(r), which spreads both directions over the banks.
-// v: the lane's row (pairs of columns), or with FRAG, of each 32 columns, 4 rows
-// (t / 4 and 8, 16, 24 after) x 4 pairs (2 (t mod 4) and 8, 16, 24 after).
-template <bool F32, bool FRAG>
+// The pairs [FIRST, FIRST + PAIRS) of v: the lane's row (pairs of columns), or with FRAG, of each 32 columns, 4 rows
+// (t / 4 and 8, 16, 24 after) x 4 pairs (2 (t mod 4) and 8, 16, 24 after).  PAIRS below 16 (FP32) or 32 (BF16): only
+// the first columns, 16 bytes of them at least.
+template <bool F32, bool FRAG, int FIRST, int PAIRS = F32 ? 16 : 32, int N>
 __device__ __forceinline__ void store_chunk(const Dest& p, unsigned char* out, int lane, int64_t row0, int col0,
-                                            const float2* v) {
+                                            const float2 (&v)[N]) {
     constexpr int kPer = F32 ? 4 : 8;  // elements of 16 bytes
+    constexpr int kPieces = 2 * PAIRS / kPer;
+    static_assert(FIRST >= 0 && FIRST + PAIRS <= N, "a chunk's pairs are the array's");
+    static_assert(2 * PAIRS % kPer == 0 && kPieces <= 8 && (!FRAG || kPieces == 8), "a chunk is whole 16-byte pieces");
     auto turn = [](int r) { return F32 && FRAG ? 2 * (r & 3) : r & 7; };
     __syncwarp();
     if (FRAG) {
@@ -322,7 +337,7 @@ __device__ __forceinline__ void store_chunk(const Dest& p, unsigned char* out, i
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 x = v[q * 16 + i * 4 + j];
+                    const float2 x = v[FIRST + q * 16 + i * 4 + j];
                     const int r = i * 8 + (lane >> 2);
                     if (F32)
                         *reinterpret_cast<float2*>(out + r * 128 + (((2 * j + ((lane & 3) >> 1)) ^ turn(r)) * 16) +
@@ -333,20 +348,20 @@ __device__ __forceinline__ void store_chunk(const Dest& p, unsigned char* out, i
                 }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kPieces; ++j) {
             uint4 w;
-            if (F32)
-                w = make_uint4(__float_as_uint(v[2 * j].x), __float_as_uint(v[2 * j].y),
-                               __float_as_uint(v[2 * j + 1].x), __float_as_uint(v[2 * j + 1].y));
+            const int at = FIRST + (F32 ? 2 : 4) * j;
+            if constexpr (F32)
+                w = make_uint4(__float_as_uint(v[at].x), __float_as_uint(v[at].y), __float_as_uint(v[at + 1].x),
+                               __float_as_uint(v[at + 1].y));
             else
-                w = make_uint4(pack_bf16x2_rn(v[4 * j].x, v[4 * j].y), pack_bf16x2_rn(v[4 * j + 1].x, v[4 * j + 1].y),
-                               pack_bf16x2_rn(v[4 * j + 2].x, v[4 * j + 2].y),
-                               pack_bf16x2_rn(v[4 * j + 3].x, v[4 * j + 3].y));
+                w = make_uint4(pack_bf16x2_rn(v[at].x, v[at].y), pack_bf16x2_rn(v[at + 1].x, v[at + 1].y),
+                               pack_bf16x2_rn(v[at + 2].x, v[at + 2].y), pack_bf16x2_rn(v[at + 3].x, v[at + 3].y));
             *reinterpret_cast<uint4*>(out + lane * 128 + ((j ^ turn(lane)) * 16)) = w;
         }
     }
     __syncwarp();
-    const int rows = (int)min((int64_t)32, p.limit - row0), cols = min(8 * kPer, p.N - col0);
+    const int rows = (int)min((int64_t)32, p.limit - row0), cols = min(2 * PAIRS, p.N - col0);
     if (cols <= 0) return;
     if (p.vec) {
         const int j = lane & 7, left = cols - j * kPer;
@@ -515,14 +530,15 @@ __device__ __forceinline__ Tile8 tile_at(const typename ParamsOf<KIND>::type& p,
     return x;
 }
 
-// 64 columns of the residual from `col` on, added to the lane's row v, through
+// 64 columns of the residual from `col` on, added to the pairs [FIRST, FIRST + 32) of the lane's row v, through
 // shared memory as store_chunk's output; eight loads under way at a time (one by
 // one a tile's took 19,500 clocks), sixteen of FP32 rows off the 16-byte grid
 // (1000 x 5003 x 2000: 50.6 us by eight, 44.0; thirty-two gain nothing and cost
 // the loop registers).
-template <bool F32>
+template <bool F32, int FIRST, int N>
 __device__ __forceinline__ void add_residual(const Ext8Params& p, unsigned char* out, int lane, int64_t row0,
-                                             int64_t limit, int col, float2* v) {
+                                             int64_t limit, int col, float2 (&v)[N]) {
+    static_assert(FIRST >= 0 && FIRST + 32 <= N, "a chunk's pairs are the array's");
     constexpr int kPer = F32 ? 4 : 8, kCols = F32 ? 32 : 64;
     const int rows = (int)min((int64_t)32, limit - row0);
 #pragma unroll
@@ -594,14 +610,15 @@ __device__ __forceinline__ void add_residual(const Ext8Params& p, unsigned char*
         for (int k = 0; k < 8; ++k) {
             const uint4 x = *reinterpret_cast<const uint4*>(out + lane * 128 + ((k ^ (lane & 7)) * 16));
             if (F32) {
-                float2* d = v + half * 16 + 2 * k;
-                d[0] = fadd2(d[0], make_float2(__uint_as_float(x.x), __uint_as_float(x.y)));
-                d[1] = fadd2(d[1], make_float2(__uint_as_float(x.z), __uint_as_float(x.w)));
+                const int at = FIRST + half * 16 + 2 * k;
+                v[at] = fadd2(v[at], make_float2(__uint_as_float(x.x), __uint_as_float(x.y)));
+                v[at + 1] = fadd2(v[at + 1], make_float2(__uint_as_float(x.z), __uint_as_float(x.w)));
             } else {
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    v[4 * k + e] = fadd2(v[4 * k + e], make_float2(bf16lo_to_f32(w[e]), bf16hi_to_f32(w[e])));
+                    v[FIRST + 4 * k + e] =
+                        fadd2(v[FIRST + 4 * k + e], make_float2(bf16lo_to_f32(w[e]), bf16hi_to_f32(w[e])));
             }
         }
     }
@@ -679,35 +696,35 @@ __device__ __forceinline__ void finish_rows(const Ext8Params& p, unsigned char* 
                                             int64_t row0, float2 (&sum)[PAIRS]) {
     const bool behind = p.rest && t.group == p.G;  // rows behind the groups: zeros
     constexpr int kOwn = GATED ? PAIRS / 2 : PAIRS, kAt = kOwn < 32 ? kOwn : 32;  // pairs of a half, and at a time
-    const int N = kOwn < 32 ? min(p.N, col0 + 2 * kOwn) : p.N;  // a chunk of BF16 is 64 columns
-    if (p.z && !behind) {
-#pragma unroll
-        for (int h = 0; h < PAIRS / kAt; ++h)
-            store_chunk<false, false>(Dest{p.z + (GATED && h ? p.N : 0), p.ldz, t.end, N, p.z_vec, 0}, out, lane, row0,
-                                      col0 + (GATED ? 0 : 2 * kAt * h), sum + kAt * h);
-    }
+    if (p.z && !behind)
+        each<PAIRS / kAt>([&](auto h) {
+            store_chunk<false, false, kAt * h.value, kAt>(
+                Dest{p.z + (GATED && h.value ? p.N : 0), p.ldz, t.end, p.N, p.z_vec, 0}, out, lane, row0,
+                col0 + (GATED ? 0 : 2 * kAt * h.value), sum);
+        });
     act_pairs<0, kOwn>(sum, p.act);
     if (GATED) {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) sum[i] = fmul2(sum[i], sum[kOwn + i]);
     }
-    const Dest d{p.c, p.ldc, t.end, N, p.vec, 0};
-#pragma unroll
-    for (int h = 0; h < kOwn / kAt; ++h) {
-        const int col = col0 + 2 * kAt * h;
-        if (p.res) {
-            if (p.res_f32)
-                add_residual<true>(p, out, lane, row0, t.end, col, sum + kAt * h);
-            else
-                add_residual<false>(p, out, lane, row0, t.end, col, sum + kAt * h);
-        }
+    const Dest d{p.c, p.ldc, t.end, p.N, p.vec, 0};
+    each<kOwn / kAt>([&](auto h) {
+        constexpr int kFirst = kAt * decltype(h)::value;
+        const int col = col0 + 2 * kFirst;
+        if constexpr (kAt == 32)  // rows of groups, which halves are, have no residual
+            if (p.res) {
+                if (p.res_f32)
+                    add_residual<true, kFirst>(p, out, lane, row0, t.end, col, sum);
+                else
+                    add_residual<false, kFirst>(p, out, lane, row0, t.end, col, sum);
+            }
         if (p.c_f32) {
-            store_chunk<true, false>(d, out, lane, row0, col, sum + kAt * h);
-            if (kAt == 32) store_chunk<true, false>(d, out, lane, row0, col + 32, sum + kAt * h + 16);
+            store_chunk<true, false, kFirst>(d, out, lane, row0, col, sum);
+            if constexpr (kAt == 32) store_chunk<true, false, kFirst + 16>(d, out, lane, row0, col + 32, sum);
         } else {
-            store_chunk<false, false>(d, out, lane, row0, col, sum + kAt * h);
+            store_chunk<false, false, kFirst, kAt>(d, out, lane, row0, col, sum);
         }
-    }
+    });
 }
 
 // Tiles tile0 .. tiles - 1.  split: pairs of a cluster that share a tile, each
@@ -990,15 +1007,14 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 Dest d = dest_of(p, p.M);
                 if constexpr (KIND == kDepth)
                     d.c = static_cast<char*>(d.c) + x.group * p.c_g * (p.c_f32 ? 4 : 2);
-                if (p.c_f32) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        store_chunk<true, BROWS>(d, out, lane, row0, col0 + q * 32, sum + q * 16);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        store_chunk<false, BROWS>(d, out, lane, row0, col0 + q * 64, sum + q * 32);
-                }
+                if (p.c_f32)
+                    each<kPairs / 16>([&](auto q) {
+                        store_chunk<true, BROWS, 16 * q.value>(d, out, lane, row0, col0 + 32 * q.value, sum);
+                    });
+                else
+                    each<kPairs / 32>([&](auto q) {
+                        store_chunk<false, BROWS, 32 * q.value>(d, out, lane, row0, col0 + 64 * q.value, sum);
+                    });
             }
         }
     }
