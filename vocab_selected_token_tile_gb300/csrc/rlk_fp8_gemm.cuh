@@ -37,8 +37,8 @@
 // weight once and wastes no more than 15 columns.  Bound: HBM, N K bytes (37 x
 // 151936 x 4096: 100 us, 6.3 TB/s; 1 x 4096 x 4096: 7.2 us).  Two
 // CTAs per SM keep loads in flight across each other's start and end.  Where N
-// / 128 tiles are fewer than the SMs can hold, a cluster of 2, 4 or 8 CTAs
-// splits K, and adds its partial sums through distributed shared memory in
+// / 128 tiles are fewer than the SMs can hold, a cluster of 2, 4 or 8 CTAs (of a
+// layer without groups any number up to 8) splits K, and adds its partial sums through distributed shared memory in
 // rank order: no workspace, no second launch, the same bits every time.
 //
 // Both are also built for a feed-forward layer (kEpi and on): z = A B^T + bias,
@@ -641,10 +641,11 @@ __device__ __forceinline__ float res_at(const Ext8Params& p, int64_t i) {
 // loop suffered: 331 -> 348 us.)
 // PAIRS: of columns a warp has, 64 or (of a half tile) 32; gated, half of them
 // the gate's.  col: the first of the result's; zcol: of B's rows, so of z's.
-template <bool GATED, int PAIRS>
+template <int KIND, int PAIRS>
 __device__ __forceinline__ void start_with_bias(const Ext8Params& p, unsigned char* out, int lane, const Tile8& t,
                                                 int col, float2 (&sum)[PAIRS]) {
-    if (p.rest && t.group == p.G) return;  // rows behind the groups: zeros
+    constexpr bool GATED = gated_kind(KIND);
+    if (rows_kind(KIND) && p.rest && t.group == p.G) return;  // rows behind the groups: zeros
     constexpr int kEach = PAIRS / 16, kOf = GATED ? 16 : 32;  // columns a lane, lanes of a half
     const int half = lane / kOf, c = col + kEach * (lane % kOf);
     const int64_t group = (int64_t)t.group * (GATED ? 2 : 1) * p.N, at = group + (half ? p.N : 0) + c;
@@ -691,10 +692,11 @@ __device__ __forceinline__ void start_with_bias(const Ext8Params& p, unsigned ch
 // The epilogue of a warp's 32 rows and their PAIRS pairs of columns, a row a
 // lane; gated: the first half of them is the gate's and the second the other
 // half's same columns, which the loads of B have laid side by side.
-template <bool GATED, int PAIRS>
+template <int KIND, int PAIRS>
 __device__ __forceinline__ void finish_rows(const Ext8Params& p, unsigned char* out, int lane, const Tile8& t, int col0,
                                             int64_t row0, float2 (&sum)[PAIRS]) {
-    const bool behind = p.rest && t.group == p.G;  // rows behind the groups: zeros
+    constexpr bool GATED = gated_kind(KIND);
+    const bool behind = rows_kind(KIND) && p.rest && t.group == p.G;  // rows behind the groups: zeros
     constexpr int kOwn = GATED ? PAIRS / 2 : PAIRS, kAt = kOwn < 32 ? kOwn : 32;  // pairs of a half, and at a time
     if (p.z && !behind)
         each<PAIRS / kAt>([&](auto h) {
@@ -711,7 +713,7 @@ __device__ __forceinline__ void finish_rows(const Ext8Params& p, unsigned char* 
     each<kOwn / kAt>([&](auto h) {
         constexpr int kFirst = kAt * decltype(h)::value;
         const int col = col0 + 2 * kFirst;
-        if constexpr (kAt == 32)  // rows of groups, which halves are, have no residual
+        if constexpr (!rows_kind(KIND))  // rows of groups have no residual
             if (p.res) {
                 if (p.res_f32)
                     add_residual<true, kFirst>(p, out, lane, row0, t.end, col, sum);
@@ -845,7 +847,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
                 for (int kg = x.k0; kg < x.k1; kg += kGroups) {
                     ok = pipe_wait_warp(ab, smem_u32(&all->sempty[r.slot]), r.phase ^ 1u, p.w);
                     if (!ok) break;
-                    if constexpr (kLayer) {
+                    if constexpr (kLayer && !rows_kind(KIND)) {
                         // the tile's residual comes into L2 meanwhile (by the tile: all tiles' at once drove the
                         // operands out)
                         if (p.res && kg == x.k0 && split == 1) {
@@ -907,7 +909,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) sum[i] = make_float2(0.f, 0.f);
             if constexpr (kLayer)
-                if (p.bias && split == 1) start_with_bias<kGated, kPairs>(p, out, lane, tile(t), first_column(tile(t)), sum);
+                if (p.bias && split == 1) start_with_bias<KIND, kPairs>(p, out, lane, tile(t), first_column(tile(t)), sum);
             const float* s = nullptr;
             const Tile8 x = tile(t);
             for (int kb = x.k0; kb < x.k1; ++kb) {
@@ -1001,7 +1003,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             }
             const int64_t row0 = (int64_t)x.row0 + rank * kOwn + rows32 * 32;
             if constexpr (kLayer) {
-                if (row0 < x.end) finish_rows<kGated, kPairs>(p, out, lane, x, first_column(x), row0, sum);
+                if (row0 < x.end) finish_rows<KIND, kPairs>(p, out, lane, x, first_column(x), row0, sum);
             } else {
                 const int col0 = x.nb * kGN + part * 128;
                 Dest d = dest_of(p, p.M);
@@ -1114,7 +1116,8 @@ struct Skinny {
 
 template <int NT, int KIND>
 constexpr size_t kSSmemOf = Skinny<NT>::kSmem + (rows_kind(KIND) ? sizeof(GroupTable) : 0);
-static_assert(2 * (kSSmemOf<64, kRows> + 1024) <= 233472, "two CTAs an SM");
+// the largest that are launched: 64 rows of one product, 32 of groups
+static_assert(2 * (kSSmemOf<64, kEpi> + 1024) <= 233472 && 2 * (kSSmemOf<32, kRows> + 1024) <= 233472, "two CTAs an SM");
 
 // A unit: 128 rows of B (gated: 64 of each half, 16 and 16 by turns, so that a
 // warp's lanes l and l + 16 hold a column's gate and its other half) against
@@ -1137,11 +1140,11 @@ __device__ __forceinline__ Unit8 unit_at(const typename ParamsOf<KIND>::type& p,
 }
 
 // One result of K split over a cluster: z and its other half u (gated) of `row` and `col`.
-template <bool GATED>
+template <int KIND>
 __device__ __forceinline__ void finish_one(const Ext8Params& p, int64_t row, int col, float z, float u) {
     float y = act_one(z, p.act);
-    if (GATED) y = __fmul_rn(y, u);
-    if (p.res) y = __fadd_rn(y, res_at(p, row * p.ldr + col));
+    if (gated_kind(KIND)) y = __fmul_rn(y, u);
+    if (!rows_kind(KIND) && p.res) y = __fadd_rn(y, res_at(p, row * p.ldr + col));
     if (p.c_f32)
         static_cast<float*>(p.c)[row * p.ldc + col] = y;
     else
@@ -1152,10 +1155,11 @@ __device__ __forceinline__ void finish_one(const Ext8Params& p, int64_t row, int
 // Gated: lanes l and l + 16 have a column's gate and its other half, and after
 // one exchange the first finishes the even rows and the second the odd ones.
 // Sixteen rows at a time, which bounds the registers.
-template <int NT, bool GATED>
+template <int NT, int KIND>
 __device__ __forceinline__ void finish_lanes(const Ext8Params& p, const Unit8& x, int quarter, int lane,
                                              const float2 (&sum)[NT / 2]) {
-    const bool behind = p.rest && x.group == p.G;  // rows behind the groups: zeros
+    constexpr bool GATED = gated_kind(KIND);
+    const bool behind = rows_kind(KIND) && p.rest && x.group == p.G;  // rows behind the groups: zeros
     const int half = GATED ? lane >> 4 : 0;
     const int col = GATED ? x.nb * 64 + quarter * 16 + (lane & 15) : x.nb * 128 + quarter * 32 + lane;
     const bool in = col < p.N;
@@ -1196,13 +1200,15 @@ __device__ __forceinline__ void finish_lanes(const Ext8Params& p, const Unit8& x
         }
         const int64_t row = (int64_t)x.row0 + r0 + half;
         const int left = in ? x.rows - r0 - half : 0;
-        if (p.res) {
-            float r[2 * kPairs];
+        if constexpr (!rows_kind(KIND))  // rows of groups have no residual
+            if (p.res) {
+                float r[2 * kPairs];
 #pragma unroll
-            for (int i = 0; i < 2 * kPairs; ++i) r[i] = kStep * i < left ? res_at(p, (row + kStep * i) * p.ldr + col) : 0.f;
+                for (int i = 0; i < 2 * kPairs; ++i)
+                    r[i] = kStep * i < left ? res_at(p, (row + kStep * i) * p.ldr + col) : 0.f;
 #pragma unroll
-            for (int i = 0; i < kPairs; ++i) v[i] = fadd2(v[i], make_float2(r[2 * i], r[2 * i + 1]));
-        }
+                for (int i = 0; i < kPairs; ++i) v[i] = fadd2(v[i], make_float2(r[2 * i], r[2 * i + 1]));
+            }
         if (p.c_f32) {
             float* c = static_cast<float*>(p.c) + row * p.ldc + col;
 #pragma unroll
@@ -1403,7 +1409,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
             }
             if (!ok || split > 1) break;  // a split launch has one tile a cluster, added up below
             if constexpr (kExt) {
-                finish_lanes<NT, kGated>(p, x, quarter, lane, pairs);
+                finish_lanes<NT, KIND>(p, x, quarter, lane, pairs);
                 continue;
             }
             const int col = t * kSRows + row_in;
@@ -1444,7 +1450,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
         if constexpr (kExt) {
             if (first < tiles && !failed) {
                 const Unit8 x = unit(first);
-                const bool behind = p.rest && x.group == p.G;
+                const bool behind = rows_kind(KIND) && p.rest && x.group == p.G;
                 const int per = kGated ? kSRows / 2 : kSRows;
                 const int64_t at_b = (int64_t)x.group * (kGated ? 2 : 1) * p.N;
                 for (int e = threadIdx.x; e < (hi - lo) * per; e += kSThreads) {
@@ -1461,7 +1467,7 @@ __global__ void __launch_bounds__(kSThreads, Skinny<NT>::kPerSm)
                         p.z[row * p.ldz + col] = (uint16_t)pack_bf16x2_rn(z, 0.f);
                         if (kGated) p.z[row * p.ldz + p.N + col] = (uint16_t)pack_bf16x2_rn(u, 0.f);
                     }
-                    finish_one<kGated>(p, row, col, z, u);
+                    finish_one<KIND>(p, row, col, z, u);
                 }
             }
         }
