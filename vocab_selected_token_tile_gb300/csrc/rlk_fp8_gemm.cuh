@@ -689,6 +689,26 @@ __device__ __forceinline__ void start_with_bias(const Ext8Params& p, unsigned ch
     __syncwarp();
 }
 
+// The pairs [FIRST, FIRST + PAIRS) of a warp's results, which start at column `col` of c: the residual, and to memory.
+template <int KIND, int FIRST, int PAIRS, int N>
+__device__ __forceinline__ void finish_run(const Ext8Params& p, unsigned char* out, int lane, const Tile8& t, int col,
+                                           int64_t row0, float2 (&sum)[N]) {
+    const Dest d{p.c, p.ldc, t.end, p.N, p.vec, 0};
+    if constexpr (!rows_kind(KIND))  // rows of groups have no residual
+        if (p.res) {
+            if (p.res_f32)
+                add_residual<true, FIRST>(p, out, lane, row0, t.end, col, sum);
+            else
+                add_residual<false, FIRST>(p, out, lane, row0, t.end, col, sum);
+        }
+    if (p.c_f32) {
+        store_chunk<true, false, FIRST>(d, out, lane, row0, col, sum);
+        if constexpr (PAIRS == 32) store_chunk<true, false, FIRST + 16>(d, out, lane, row0, col + 32, sum);
+    } else {
+        store_chunk<false, false, FIRST, PAIRS>(d, out, lane, row0, col, sum);
+    }
+}
+
 // The epilogue of a warp's 32 rows and their PAIRS pairs of columns, a row a
 // lane; gated: the first half of them is the gate's and the second the other
 // half's same columns, which the loads of B have laid side by side.
@@ -698,35 +718,22 @@ __device__ __forceinline__ void finish_rows(const Ext8Params& p, unsigned char* 
     constexpr bool GATED = gated_kind(KIND);
     const bool behind = rows_kind(KIND) && p.rest && t.group == p.G;  // rows behind the groups: zeros
     constexpr int kOwn = GATED ? PAIRS / 2 : PAIRS, kAt = kOwn < 32 ? kOwn : 32;  // pairs of a half, and at a time
-    if (p.z && !behind)
-        each<PAIRS / kAt>([&](auto h) {
-            store_chunk<false, false, kAt * h.value, kAt>(
-                Dest{p.z + (GATED && h.value ? p.N : 0), p.ldz, t.end, p.N, p.z_vec, 0}, out, lane, row0,
-                col0 + (GATED ? 0 : 2 * kAt * h.value), sum);
-        });
+    static_assert(PAIRS == kAt || PAIRS == 2 * kAt, "one run or two");
+    if (p.z && !behind) {
+        const Dest d{p.z, p.ldz, t.end, p.N, p.z_vec, 0};
+        store_chunk<false, false, 0, kAt>(d, out, lane, row0, col0, sum);
+        if constexpr (GATED)
+            store_chunk<false, false, kAt, kAt>(Dest{p.z + p.N, p.ldz, t.end, p.N, p.z_vec, 0}, out, lane, row0, col0, sum);
+        else if constexpr (PAIRS > kAt)
+            store_chunk<false, false, kAt, kAt>(d, out, lane, row0, col0 + 2 * kAt, sum);
+    }
     act_pairs<0, kOwn>(sum, p.act);
     if (GATED) {
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) sum[i] = fmul2(sum[i], sum[kOwn + i]);
     }
-    const Dest d{p.c, p.ldc, t.end, p.N, p.vec, 0};
-    each<kOwn / kAt>([&](auto h) {
-        constexpr int kFirst = kAt * decltype(h)::value;
-        const int col = col0 + 2 * kFirst;
-        if constexpr (!rows_kind(KIND))  // rows of groups have no residual
-            if (p.res) {
-                if (p.res_f32)
-                    add_residual<true, kFirst>(p, out, lane, row0, t.end, col, sum);
-                else
-                    add_residual<false, kFirst>(p, out, lane, row0, t.end, col, sum);
-            }
-        if (p.c_f32) {
-            store_chunk<true, false, kFirst>(d, out, lane, row0, col, sum);
-            if constexpr (kAt == 32) store_chunk<true, false, kFirst + 16>(d, out, lane, row0, col + 32, sum);
-        } else {
-            store_chunk<false, false, kFirst, kAt>(d, out, lane, row0, col, sum);
-        }
-    });
+    finish_run<KIND, 0, kAt>(p, out, lane, t, col0, row0, sum);
+    if constexpr (kOwn > kAt) finish_run<KIND, kAt, kAt>(p, out, lane, t, col0 + 2 * kAt, row0, sum);
 }
 
 // Tiles tile0 .. tiles - 1.  split: pairs of a cluster that share a tile, each
