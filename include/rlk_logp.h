@@ -707,6 +707,7 @@ rlk_status rlk_fp8_grouped_dweight(int64_t groups, int64_t rows, int64_t M, int6
  *   dbias = the sum of dz over the rows (of each group);
  * and the codes of dz [rows, cols (2 cols gated)] along its rows and of its
  * transpose, from one pass; dz itself is not stored.
+ *   rows     >= 1: without any there is nothing but a zero dbias, the caller's.
  *   groups   0: the rows are one matrix, and q, scale, qt, scale_t as
  *            rlk_fp8_quantize's with block_rows 1; 1 to 1024: as
  *            rlk_fp8_quantize_grouped's, with ends.

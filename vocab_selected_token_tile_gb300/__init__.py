@@ -1367,7 +1367,8 @@ def fp8_act_grad(dy, z=None, activation=None, gated=False, ends=None, rowwise=Tr
     From dy [R, N] (BF16 or FP32) and the kept z, in FP32: dz = dy * act'(z), or (gated) the gate's half
     dy * z_other * act'(z_gate), then the other half dy * act(z_gate).  q, scale, qt, scale_t are fp8_quantize_both of dz,
     with ``ends`` fp8_quantize_grouped's.  ``bias_dtype`` asks for dbias, the sum of dz over the rows ([G, ...] with
-    ``ends``).  What is not asked for is None.  z may be None without an activation and a gate.
+    ``ends``).  What is not asked for is None.  z may be None without an activation and a gate.  No rows (R = 0) give
+    empty codes and a zero dbias.
     """
     torch = _t()
     both = (torch.bfloat16, torch.float32)
@@ -1399,6 +1400,11 @@ def fp8_act_grad(dy, z=None, activation=None, gated=False, ends=None, rowwise=Tr
             dbias = torch.empty((G, wide) if ends is not None else (wide,), dtype=bias_dtype, device=dy.device)
             ws = torch.empty(max(1, rlk_fp8_act_grad_workspace_size(G, R, N, int(bool(gated)))), dtype=torch.uint8,
                              device=dy.device)
+            if R == 0:
+                dbias.zero_()
+    if R == 0:  # a batch without rows, which the C call refuses
+        _used_here(stream, q, scale, qt, scale_t, dbias)
+        return q, scale, qt, scale_t, dbias
     st = rlk_fp8_act_grad(G, R, N, pe, dy.data_ptr(), _type(dy), stride, pz or None, ldz, act, int(bool(gated)),
                           _ptr(q), ldq, _ptr(scale), _ptr(qt), ldt, _ptr(scale_t), _ptr(dbias),
                           RLK_F32 if bias_dtype is torch.float32 else RLK_BF16, _ptr(ws), _raw_stream(dy, stream))
