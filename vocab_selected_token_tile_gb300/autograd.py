@@ -215,10 +215,14 @@ class Fp8Linear(torch.autograd.Function):
         return dx, dw
 
 
+def _dense_rows(t):
+    """t with contiguous rows that do not overlap: a copy of what is transposed, or expanded from fewer rows."""
+    return t if t.stride(-1) == 1 and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1]) else t.contiguous()
+
+
 def _rows_of(dy):
     """dy as the quantisations take it: BF16 or FP32, contiguous rows that do not overlap."""
-    dy = dy if dy.dtype in (torch.bfloat16, torch.float32) else dy.to(torch.bfloat16)
-    return dy if dy.stride(-1) == 1 and (dy.shape[0] <= 1 or dy.stride(0) >= dy.shape[1]) else dy.contiguous()
+    return _dense_rows(dy if dy.dtype in (torch.bfloat16, torch.float32) else dy.to(torch.bfloat16))
 
 
 class Fp8Layer(torch.autograd.Function):
@@ -265,8 +269,7 @@ def fp8_linear(x, weight, bias=None, activation=None, gated=False, residual=None
     if residual is not None:
         if residual.shape != (*lead, n):
             raise ValueError(f"residual is {list(residual.shape)}; the result is {[*lead, n]}")
-        residual = residual if x.dim() == 2 else residual.reshape(-1, n)
-        residual = residual if residual.stride(-1) == 1 else residual.contiguous()
+        residual = _dense_rows(residual if x.dim() == 2 else residual.reshape(rows.shape[0], n))
     if _differentiated(*(t for t in (x, weight, bias, residual) if t is not None)):
         y = Fp8Layer.apply(rows, weight, bias, residual, None, activation, gated)
     else:
