@@ -1437,9 +1437,12 @@ class Fp8LayerStep:
     and scales; backward takes them back.
     """
 
-    def __init__(self, x, weight, bias, residual, ends, activation, gated, need_x, need_w, need_b):
+    def __init__(self, x, weight, bias, residual, ends, activation, gated, need_x, need_w, need_b, out_dtype=None):
         torch = _t()
         both = (torch.bfloat16, torch.float32)
+        self.out = out_dtype or torch.bfloat16
+        if self.out not in both:
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
         self.M, self.K, self.sx = _matrix(x, "x", both)
         self.G, self.pe = (0, None) if ends is None else _ends(ends, x)
         if ends is None:
@@ -1512,7 +1515,7 @@ class Fp8LayerStep:
                                                 self.ldr, wts, st)
         if status:
             check(status)
-        y, z, e = _new(x, M, self.N, torch.bfloat16), None, self.e
+        y, z, e = _new(x, M, self.N, self.out), None, self.e
         if (self.act or self.gated) and (self.need_x or self.need_w or self.need_b):
             e.z_stride = -(-rows // 8) * 8
             z = _new(x, M, rows, torch.bfloat16, e.z_stride)
@@ -1520,10 +1523,10 @@ class Fp8LayerStep:
         w = _fp8_workspace(x, st, None).data_ptr()
         if G:
             status = rlk_fp8_grouped_matmul(G, M, self.N, K, self.pe, b + xq, ldk, b + xs, b + wq, ldk, rows * ldk, b + ws,
-                                            e, y.data_ptr(), RLK_BF16, self.N, 1, w, st)
+                                            e, y.data_ptr(), _type(y), self.N, 1, w, st)
         else:
             status = rlk_fp8_matmul_act(M, self.N, K, b + xq, ldk, b + xs, b + wq, ldk, b + ws, e, y.data_ptr(),
-                                        RLK_BF16, self.N, w, st)
+                                        _type(y), self.N, w, st)
         if status:
             check(status)
         return y, z, saved

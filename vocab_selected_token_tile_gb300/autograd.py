@@ -186,12 +186,12 @@ class Fp8Linear(torch.autograd.Function):
     along its rows for dx = dy @ weight, and dy and x along the tokens for dweight = dy^T @ x."""
 
     @staticmethod
-    def forward(ctx, x, weight):
-        need_x, need_w = ctx.needs_input_grad
+    def forward(ctx, x, weight, to):
+        need_x, need_w = ctx.needs_input_grad[:2]
         xq, xs, xtq, xts = fp8_quantize_both(x) if need_w else (*fp8_quantize(x), None, None)
         wq, ws, wtq, wts = fp8_quantize_both(weight, block_rows=128) if need_x else \
             (*fp8_quantize(weight, block_rows=128), None, None)
-        y = fp8_matmul(xq, xs, wq, ws)
+        y = fp8_matmul(xq, xs, wq, ws, **to)
         ctx.save_for_backward(xtq, xts, wtq, wts)
         ctx.types = x.dtype, weight.dtype
         return y
@@ -200,7 +200,7 @@ class Fp8Linear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         xtq, xts, wtq, wts = ctx.saved_tensors
-        need_x, need_w = ctx.needs_input_grad
+        need_x, need_w = ctx.needs_input_grad[:2]
         dy = dy if dy.dtype in (torch.bfloat16, torch.float32) else dy.to(torch.bfloat16)
         dy = dy if dy.stride(-1) == 1 and (dy.shape[0] <= 1 or dy.stride(0) >= dy.shape[1]) else dy.contiguous()
         q = s = qt = st = None
@@ -212,7 +212,7 @@ class Fp8Linear(torch.autograd.Function):
             qt, st = fp8_quantize(dy, transpose=True)
         dx = fp8_matmul(q, s, wtq, wts, out_dtype=ctx.types[0]) if need_x else None
         dw = fp8_matmul(qt, st, xtq, xts, b_block_rows=1, out_dtype=ctx.types[1]) if need_w else None
-        return dx, dw
+        return dx, dw, None
 
 
 def _dense_rows(t):
@@ -232,9 +232,9 @@ class Fp8Layer(torch.autograd.Function):
     Fp8Linear's (Fp8LayerStep makes the calls)."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, residual, ends, activation, gated):
+    def forward(ctx, x, weight, bias, residual, ends, activation, gated, out_dtype):
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
-        step = Fp8LayerStep(x, weight, bias, residual, ends, activation, gated, need_x, need_w, need_b)
+        step = Fp8LayerStep(x, weight, bias, residual, ends, activation, gated, need_x, need_w, need_b, out_dtype)
         y, z, saved = step.forward(x, weight)
         ctx.save_for_backward(z, saved, ends)
         ctx.step = step
@@ -246,23 +246,26 @@ class Fp8Layer(torch.autograd.Function):
     def backward(ctx, dy):
         dres = dy.to(ctx.residual) if ctx.needs_input_grad[3] else None
         if not any(ctx.needs_input_grad[:3]):
-            return None, None, None, dres, None, None, None
+            return None, None, None, dres, None, None, None, None
         z, saved, ends = ctx.saved_tensors
-        return *ctx.step.backward(_rows_of(dy), z, saved, ends), dres, None, None, None
+        return *ctx.step.backward(_rows_of(dy), z, saved, ends), dres, None, None, None, None
 
 
-def fp8_linear(x, weight, bias=None, activation=None, gated=False, residual=None):
-    """act(x [..., K] @ weight [N, K]^T + bias) + residual in FP8 with autograd: BF16 out, gradients in the inputs' types
-    (BF16 or FP32).
+def fp8_linear(x, weight, bias=None, activation=None, gated=False, residual=None, out_dtype=None):
+    """act(x [..., K] @ weight [N, K]^T + bias) + residual in FP8 with autograd: BF16 out, or FP32 with ``out_dtype``
+    torch.float32, rounded once; gradients in the inputs' types (BF16 or FP32).
 
     Forward and backward quantise with one FP32 scale per 128 elements (or 128 x 128 weights) and sum in FP32; what is
     saved for the backward are the E4M3 transposes, one byte an element, and with an activation or a gate its argument
     in BF16.  ``activation`` is None, "relu", "silu", "gelu" or "gelu_tanh"; with ``gated`` the weight holds the gate's
     rows, then as many more (a multiple of 64 each), and the result is act(gate) * other.  ``bias`` has a value for each
-    row of the weight; ``residual`` has the result's shape.
+    row of the weight; ``residual`` has the result's shape (an FP32 stream keeps its digits in an FP32 result only).
+
+    The weight is quantised at every call: a server, whose weights stay, does that once (fp8_quantize with block_rows
+    128) and calls fp8_matmul_act.
     """
     if bias is None and residual is None and not gated and activation in (None, "none"):
-        return _linear(x, weight)
+        return _linear(x, weight, out_dtype)
     lead = x.shape[:-1]
     rows = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
     n = weight.shape[0] // 2 if gated else weight.shape[0]
@@ -271,31 +274,34 @@ def fp8_linear(x, weight, bias=None, activation=None, gated=False, residual=None
             raise ValueError(f"residual is {list(residual.shape)}; the result is {[*lead, n]}")
         residual = _dense_rows(residual if x.dim() == 2 else residual.reshape(rows.shape[0], n))
     if _differentiated(*(t for t in (x, weight, bias, residual) if t is not None)):
-        y = Fp8Layer.apply(rows, weight, bias, residual, None, activation, gated)
+        y = Fp8Layer.apply(rows, weight, bias, residual, None, activation, gated, out_dtype)
     else:
-        y = fp8_matmul_act(*fp8_quantize(rows), *fp8_quantize(weight, block_rows=128), bias, activation, gated, residual)
+        y = fp8_matmul_act(*fp8_quantize(rows), *fp8_quantize(weight, block_rows=128), bias, activation, gated, residual,
+                           False, out_dtype)
     return y if x.dim() == 2 else y.reshape(*lead, n)
 
 
-def fp8_grouped_linear(x, weight, ends, bias=None, activation=None, gated=False):
+def fp8_grouped_linear(x, weight, ends, bias=None, activation=None, gated=False, out_dtype=None):
     """fp8_linear for rows that belong to groups (a mixture's experts), with autograd: group e is rows
     [ends[e - 1], ends[e]) of x [M, K], with weight[e] of weight [G, N, K] and bias[e] of bias [G, N].
 
     ``ends`` is int32 [G] on the GPU, the running sum of the groups' counts of rows; nothing is read back.  Rows behind
     the last group (padding) have a zero result and a zero gradient, and reach nothing whatever they hold; a group
-    without rows has zero gradients.
+    without rows has zero gradients.  All weights are quantised at every call; fp8_grouped_matmul takes kept codes.
     """
     if _differentiated(*(t for t in (x, weight, bias) if t is not None)):
-        return Fp8Layer.apply(x, weight, bias, None, ends, activation, gated)
-    return fp8_grouped_matmul(*fp8_quantize(x), *fp8_quantize(weight, block_rows=128), ends, bias, activation, gated)
+        return Fp8Layer.apply(x, weight, bias, None, ends, activation, gated, out_dtype)
+    return fp8_grouped_matmul(*fp8_quantize(x), *fp8_quantize(weight, block_rows=128), ends, bias, activation, gated,
+                              False, out_dtype)
 
 
-def _linear(x, weight):
+def _linear(x, weight, out_dtype):
     """fp8_linear without an epilogue."""
     lead = x.shape[:-1]
     rows = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    to = {} if out_dtype is None else {"out_dtype": out_dtype}
     if _differentiated(x, weight):
-        y = Fp8Linear.apply(rows, weight)
+        y = Fp8Linear.apply(rows, weight, to)
     else:
-        y = fp8_matmul(*fp8_quantize(rows), *fp8_quantize(weight, block_rows=128))
+        y = fp8_matmul(*fp8_quantize(rows), *fp8_quantize(weight, block_rows=128), **to)
     return y if x.dim() == 2 else y.reshape(*lead, weight.shape[0])
