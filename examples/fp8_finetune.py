@@ -1,7 +1,7 @@
 """A fine-tuning step and a rollout with 8-bit projections: the FP8 operators and the cross entropy as they are used.
 
-A small residual network whose projections run in FP8 (``fp8_linear``: forward, input gradient and weight gradient)
-below a BF16 vocabulary head whose loss is ``linear_cross_entropy`` (with a little label smoothing and z-loss, no
+A small residual network whose projections run in FP8 (``fp8_linear``: forward, input gradient and weight gradient; the
+activation and the addition to the FP32 residual stream are in the products' epilogues) below a BF16 vocabulary head whose loss is ``linear_cross_entropy`` (with a little label smoothing and z-loss, no
 logits kept) is trained on a synthetic task: the next token is a fixed permutation of the present one.  Then the head
 is quantised once, in 128 x 128 blocks, and the trained network's tokens are scored twice, as a rollout with an 8-bit
 head and a BF16 trainer would: FP8 logits of single tokens through ``logp_fwd``, and the fused BF16 head.  The
@@ -35,8 +35,8 @@ class Network(torch.nn.Module):
     def forward(self, tokens):
         x = self.embed[tokens]
         for up, down in zip(self.up, self.down):
-            h = torch.nn.functional.gelu(fp8_linear(self.norm(x), up))
-            x = x + fp8_linear(h, down).float()
+            h = fp8_linear(self.norm(x), up, activation="gelu")
+            x = fp8_linear(h, down, residual=x, out_dtype=torch.float32)
         return self.norm(x)
 
     @staticmethod
