@@ -116,3 +116,91 @@ def test_other_result_types_are_refused(built, trained):
                  lambda: autograd.fp8_grouped_linear(x, w[None], ends, out_dtype=torch.float16)):
         with pytest.raises(TypeError):
             call()
+
+
+# ------------------------------------------------------------------ the bits of the calls that the functions stand for
+
+def by_calls(x, w, bias, residual, ends, act, gated, out, dy):
+    """(y, dx, dw, dbias) of a layer from the public calls, each with buffers of its own."""
+    K = x.shape[1]
+    wq, ws, wtq, wts = rlk.fp8_quantize_both(w, block_rows=128)
+    z = None
+    keep = act is not None or gated
+    kind = F32 if bias is None else bias.dtype
+    if ends is None:
+        xq, xs, xtq, xts = rlk.fp8_quantize_both(x)
+        y = rlk.fp8_matmul_act(xq, xs, wq, ws, bias, act, gated, residual, keep, out)
+    else:
+        xq, xs, xtq, xts = rlk.fp8_quantize_grouped(x, ends)
+        y = rlk.fp8_grouped_matmul(xq, xs, wq, ws, ends, bias, act, gated, keep, out)
+    if keep:
+        y, z = y
+    q, s, qt, st, db = rlk.fp8_act_grad(dy, z, act, gated, ends, bias_dtype=kind)
+    if ends is None:
+        dx = rlk.fp8_matmul(q, s, wtq, wts, out_dtype=x.dtype)
+        dw = rlk.fp8_matmul(qt, st, xtq, xts, b_block_rows=1, out_dtype=w.dtype)
+    else:
+        dx = rlk.fp8_grouped_matmul(q, s, wtq, wts, ends, out_dtype=x.dtype)
+        dw = rlk.fp8_grouped_dweight(qt, st, xtq, xts, ends, x.shape[0], out_dtype=w.dtype)
+    return y, dx, dw, db
+
+
+SIZES = [(1, 128, 40), (9, 128, 16), (130, 256, 300), (257, 384, 2056), (300, 2176, 130), (1000, 640, 514)]
+LAYERS = [(None, False, True, None), (None, False, False, BF16), ("gelu", False, False, F32), ("silu", True, True, None),
+          ("relu", False, True, BF16), ("gelu_tanh", True, False, None), (None, True, True, F32)]
+
+
+@pytest.mark.parametrize("M,rows,K", SIZES)
+@pytest.mark.parametrize("act,gated,bias,residual", LAYERS)
+@pytest.mark.parametrize("types", [(BF16, F32, BF16), (F32, BF16, F32)])
+def test_a_step_is_its_calls(built, M, rows, K, act, gated, bias, residual, types):
+    tx, tw, out = types
+    n = rows // 2 if gated else rows
+    x, w = rand(M, K, seed=51, dtype=tx), rand(rows, K, seed=52, sigma=0.08, dtype=tw)
+    b = rand(rows, seed=53, dtype=tw) if bias else None
+    r = rand(M, n, seed=54, dtype=residual) if residual else None
+    dy = rand(M, n, seed=55, sigma=1e-3, dtype=out)
+    want = by_calls(x, w, b, r, None, act, gated, out, dy)
+    leaves = [t.clone().requires_grad_() for t in (x, w, b) if t is not None]
+    y = autograd.fp8_linear(*leaves[:2], leaves[2] if bias else None, act, gated, r, out)
+    got = (y.detach(), *torch.autograd.grad(y, leaves, dy))
+    for g, t in zip(got, want):
+        assert g.dtype == t.dtype and torch.equal(g, t)
+
+
+COUNTS = [[1], [0, 3, 0, 5], [128, 0, 129, 1], [40, 60, 100, 56], [300, 1, 200], [1, 0, 2] * 30]
+
+
+@pytest.mark.parametrize("counts", COUNTS, ids=str)
+@pytest.mark.parametrize("rows,K", [(128, 40), (384, 300), (256, 2056)])
+@pytest.mark.parametrize("act,gated,bias", [(None, False, True), (None, False, False), ("gelu", False, False),
+                                            ("silu", True, True), ("relu", True, False)])
+@pytest.mark.parametrize("types", [(BF16, F32, BF16), (F32, BF16, F32)])
+def test_a_step_by_groups_is_its_calls(built, counts, rows, K, act, gated, bias, types):
+    tx, tw, out = types
+    G, used = len(counts), sum(counts)
+    M, n = used + 5, rows // 2 if gated else rows
+    ends = torch.tensor(counts, device="cuda").cumsum(0).to(torch.int32)
+    x, w = rand(M, K, seed=61, dtype=tx), rand(G, rows, K, seed=62, sigma=0.08, dtype=tw)
+    b = rand(G, rows, seed=63, dtype=tw) if bias else None
+    dy = rand(M, n, seed=64, sigma=1e-3, dtype=out)
+    want = by_calls(x, w, b, None, ends, act, gated, out, dy)
+    leaves = [t.clone().requires_grad_() for t in (x, w, b) if t is not None]
+    y = autograd.fp8_grouped_linear(*leaves[:2], ends, leaves[2] if bias else None, act, gated, out)
+    got = (y.detach(), *torch.autograd.grad(y, leaves, dy))
+    for g, t in zip(got, want):
+        assert g.dtype == t.dtype and torch.equal(g, t)
+
+
+def test_only_what_is_asked_for_has_the_same_bits(built):
+    """Frozen inputs take other calls (no transposes, no codes along the rows): the same bits."""
+    ends = torch.tensor([50, 50, 190], dtype=torch.int32, device="cuda")
+    x, w, b, dy = rand(200, 300, seed=71), rand(3, 256, 300, seed=72, sigma=0.08), rand(3, 256, seed=73), rand(200, 256, seed=74)
+    for g in (None, ends):
+        ww, bb = (w, b) if g is not None else (w[0], b[0])
+        for act in (None, "silu"):
+            want = by_calls(x, ww, bb, None, g, act, False, BF16, dy)
+            for which in range(3):
+                args = [t.clone().requires_grad_(k == which) for k, t in enumerate((x, ww, bb))]
+                y = autograd.fp8_linear(*args, act) if g is None else autograd.fp8_grouped_linear(args[0], args[1], g, args[2], act)
+                assert torch.equal(torch.autograd.grad(y, args[which], dy)[0], want[1 + which]) and torch.equal(y.detach(), want[0])
