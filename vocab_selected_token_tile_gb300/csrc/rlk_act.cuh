@@ -5,11 +5,17 @@
 //   gelu       x Phi(x)              Phi the normal distribution
 //   gelu_tanh  x (1 + tanh(v)) / 2 = x s(2 v),  v = sqrt(2 / pi) (x + 0.044715 x^3)
 //
-// e^x and 1 / x are the special-function unit's (2 ulp and 1 ulp), so a value is
-// within 2^-20 of itself where BF16 keeps 2^-9; gelu is within 7.5e-8 |x|: Phi is
-// 1 - erfc(|x| / sqrt 2) / 2 (or the second term for x < 0) with the five-term
-// approximation of erfc by Hastings (Abramowitz and Stegun 7.1.26),
-// t (a1 + t (a2 + ...)) e^-y^2, t = 1 / (1 + p y), within 1.5e-7 of it.
+// e^x and 1 / x are the special-function unit's (2 ulp and 1 ulp).  An exponent
+// of up to 58 rounded to FP32 moves its power more than that: silu is within
+// 2^-18 of itself and gelu_tanh within 2^-17 where BF16 keeps 2^-9; below the
+// clamps that follow they are within 2e-16 and 3e-15, but no longer of themselves.
+// gelu is within 3e-7 |x|, and for x < 0 within 2^-14 of itself down to -12: Phi is
+// 1 - Q(|x|), or Q for x < 0, Q = t (a1 + t (a2 + ... + t a6)) e^(-x^2 / 2),
+// t = 1 / (1 + p |x|), whose seven numbers were fitted by linear programming to the
+// least of the larger of |error| / 1e-7 and |error| / (2^-14 Q) on [0, 12]: 8e-8 and
+// 4.1e-5 Q.  (Five terms, Hastings' in Abramowitz and Stegun 7.1.26, are as close but
+// off by 0.16% of the value at -5 and 1% at -8, where BF16 rounds by 0.2% at most; the sixth
+// costs 2 us of 398 at 8192 x 12288 x 4096.)
 //
 // The warps of a product's epilogue have nothing to hide this behind, so two
 // values share one reciprocal, 1 / d0 = d1 (1 / (d0 d1)).  Hence x is held above
@@ -54,18 +60,19 @@ __device__ __forceinline__ float2 sigmoid_pair(float2 t, float2& e) {
     return rcp_pair<OWN>(fadd2(e, both(1.f)));
 }
 
-// -erfc(c / sqrt 2) / 2 for c = min(|x|, 12), which is 0 to FP32 from there on (a
-// NaN takes 12), and e^(-c^2 / 2).
+// -Q(c) for c = min(|x|, 12), beyond which it is below 2e-33 (a NaN takes 12), and
+// e^(-c^2 / 2).
 template <bool OWN>
 __device__ __forceinline__ float2 minus_tail_pair(float2 x, float2& c, float2& bell) {
     c = make_float2(fminf(fabsf(x.x), 12.f), fminf(fabsf(x.y), 12.f));
-    const float2 t = rcp_pair<OWN>(ffma2(c, both(0.3275911f * 0.70710678f), both(1.f)));
+    const float2 t = rcp_pair<OWN>(ffma2(c, both(0.29249999f), both(1.f)));
     const float2 e = fmul2(fmul2(c, c), both(-0.5f * kLog2e));
     bell = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-    float2 p = ffma2(both(-0.5f * 1.061405429f), t, both(0.5f * 1.453152027f));
-    p = ffma2(p, t, both(-0.5f * 1.421413741f));
-    p = ffma2(p, t, both(0.5f * 0.284496736f));
-    p = ffma2(p, t, both(-0.5f * 0.254829592f));
+    float2 p = ffma2(both(0.086254731f), t, both(-0.26742002f));
+    p = ffma2(p, t, both(0.072400913f));
+    p = ffma2(p, t, both(-0.16905613f));
+    p = ffma2(p, t, both(-0.10457607f));
+    p = ffma2(p, t, both(-0.11760336f));
     return fmul2(fmul2(p, t), bell);
 }
 
@@ -84,7 +91,7 @@ __device__ __forceinline__ float2 act_pair(float2 v) {
         float2 e;
         return fmul2(x, sigmoid_pair<OWN>(fmul2(x, w), e));
     }
-    if (ACT == RLK_ACT_GELU) {  // x Phi(x) = max(x, 0) - |x| erfc(|x| / sqrt 2) / 2 for either sign
+    if (ACT == RLK_ACT_GELU) {  // x Phi(x) = max(x, 0) - |x| Q(|x|) for either sign
         float2 c, bell;
         const float2 tail = minus_tail_pair<OWN>(v, c, bell);
         return ffma2(c, tail, above(v, 0.f));
