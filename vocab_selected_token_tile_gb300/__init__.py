@@ -1277,8 +1277,8 @@ def _layer(a, a_scale, b, b_scale, ends, bias, activation, gated, residual, keep
 
 def fp8_matmul_act(a, a_scale, b, b_scale, bias=None, activation=None, gated=False, residual=None, keep=False,
                    out_dtype=None, out=None, workspace=None, validate=False, stream=None):
-    """act(a @ b^T + bias) + residual [M, N] of E4M3 operands: fp8_matmul (b in 128 x 128 blocks) with a layer's
-    epilogue, all in FP32 and rounded once.
+    """act(a @ b^T + bias) + residual [M, N] of E4M3 operands: fp8_matmul (b in 128 x 128 blocks, K at least 1) with a
+    layer's epilogue, all in FP32 and rounded once.
 
     ``activation`` is None, "relu", "silu", "gelu" or "gelu_tanh".  With ``gated`` b holds N rows of the gate, then N
     more (N a multiple of 64), and the result is act(gate) * other + residual.  ``bias`` [rows of b] and ``residual``

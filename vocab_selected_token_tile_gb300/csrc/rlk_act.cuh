@@ -25,7 +25,7 @@
 // neighbour's too, which may be a column beside it but not another row, of another
 // token or of none: where the two are of different rows (OWN, the epilogue of few
 // rows, which waits for memory: no slower) each has its own reciprocal.
-// 8192 x 12288 x 4096: gelu adds 45 us to the product and silu 28; one value at a
+// 8192 x 12288 x 4096: gelu adds 49 us to the product and silu 26; one value at a
 // time they added 70 and 36.
 #pragma once
 

@@ -46,11 +46,11 @@
 // are stored.  A gated layer's B is loaded so that a thread has a column's gate
 // and its other half: 64 rows of each by turns for a tile of a pair (one 4-D box a
 // CTA), 16 for few rows.  The epilogue warps have nothing to hide this work
-// behind, so it adds to a tile's time: 8192 x 12288 x 4096, 317 us bare, 330
-// through this path, 358 with silu, 375 with gelu, 326 gated with silu (half as
-// many results), 340-348 with a bias alone, 365 with z kept, 400 with a BF16
-// residual; a pass over the result would take 60 (a read and a write of 201 MB) or
-// 90.
+// behind, so it adds to a tile's time: 8192 x 12288 x 4096, 320 us bare, 331
+// through this path, 357 with silu, 380 with gelu, 326 gated with silu (half as
+// many results), 340 with an FP32 bias alone and 348 with a BF16 one, 366 with z
+// kept, 390 with a BF16 residual and 451 with an FP32 one; a pass over the result
+// would take 60 (a read and a write of 201 MB) or 90.
 //
 // And for rows that belong to groups, each with a B of its own (kRows, kHalves),
 // and operands whose K axis belongs to groups (kDepth), where a CTA finds its
