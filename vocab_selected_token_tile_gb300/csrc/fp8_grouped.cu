@@ -16,12 +16,11 @@
 //                           64    91    96   100   101   105   108   125   151   204   245
 //   half tiles (128 rows)                          110   111   112   114   114   130   149   178   206   259
 //   tiles (256 rows)                               159   162   162   164   165   165   167   177   189   230
-// The average is of the call's rows, those behind the groups among them, and a router may be far from it: 1024 rows of 128
-// groups of 2048 x 2048 (blocks of 16 rows on the lanes) take 96 us in eights, 108 with half of them in one group, 39
-// with all of them in one, whose weight then comes from L2 for all but the first block.
 // (16 groups of 2816 x 2048: 19.0, 20.6, 25.2 us for 4 rows; 22.0 and 21.5 for 16; 24.5, 28.9, 27.2 for 32; 36 and 41
 // for 128, 44 and 42 for 192).  On the lanes a group with more rows than a block takes several blocks, which run next
-// to each other, so that the weight comes from L2 after the first.
+// to each other, so that the weight comes from L2 after the first.  So a router that is far from its average costs
+// little: 1024 rows of 128 groups of 2048 x 2048 (blocks of 16 rows) take 96 us in eights, 108 with half of them in one
+// group, 39 with all of them in one.  (The average is of the call's rows, those behind the groups among them.)
 #include "rlk_fp8_gemm.cuh"
 
 namespace rlk {
