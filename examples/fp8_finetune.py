@@ -1,11 +1,12 @@
 """A fine-tuning step and a rollout with 8-bit projections: the FP8 operators and the cross entropy as they are used.
 
 A small residual network whose projections run in FP8 (``fp8_linear``: forward, input gradient and weight gradient; the
-activation and the addition to the FP32 residual stream are in the products' epilogues) below a BF16 vocabulary head whose loss is ``linear_cross_entropy`` (with a little label smoothing and z-loss, no
-logits kept) is trained on a synthetic task: the next token is a fixed permutation of the present one.  Then the head
-is quantised once, in 128 x 128 blocks, and the trained network's tokens are scored twice, as a rollout with an 8-bit
-head and a BF16 trainer would: FP8 logits of single tokens through ``logp_fwd``, and the fused BF16 head.  The
-difference of the two log-probabilities is the drift that an importance ratio between them sees.
+activation and the addition to the FP32 residual stream are in the products' epilogues) below a BF16 vocabulary head
+whose loss is ``linear_cross_entropy`` (with a little label smoothing and z-loss, no logits kept) is trained on a
+synthetic task: the next token is a fixed permutation of the present one.  Then the head is quantised once, in 128 x 128
+blocks, and the trained network's tokens are scored twice, as a rollout with an 8-bit head and a BF16 trainer would: FP8
+logits of single tokens through ``logp_fwd``, and the fused BF16 head.  The difference of the two log-probabilities is
+the drift that an importance ratio between them sees.
 
     python examples/fp8_finetune.py [--steps 60]
 """
